@@ -58,6 +58,7 @@ extern "C" {
 /* ---- device error word bits (fa_get_device_error) ------------------------- */
 #define FA_DEVERR_WAIT_TIMEOUT 0x1  /* a pipeline wait gave up (bounded wait)     */
 #define FA_DEVERR_BAD_SEQLENS 0x2   /* cu_seqlens disagreed with N or the tensors */
+#define FA_DEVERR_BAD_PAGE 0x4      /* a page table entry is no page of the cache  */
 
 /*
  * Row softmax, numerically stable ([L22] §二 "数值稳定 Softmax": shift by the
@@ -427,6 +428,82 @@ FA_API int fa_splitkv_num_splits(int B, int H, int Nq, int Nk, int d);
 FA_API int fa_attention_fwd_splitkv_noalloc(const void *Q, const void *K, const void *V, void *O,
                                             float *lse, int B, int H, int Nq, int Nk, int d,
                                             float scale, int causal, int num_splits);
+
+/* ---- 4-bit paged key/value cache ---------------------------------------------
+ *
+ * The pages know split-KV for a decode step ([OF] risk 6) and blockwise
+ * quantisation of the operands ([FG] §4.6); a cache that holds K and V in 4
+ * bits is the library's own combination of the two.
+ *
+ * A sequence's tokens lie in pages of page_size tokens: token t of sequence b
+ * is token t % page_size of page page_table[b * max_pages + t / page_size].
+ *   cache:      DEVICE uint8 [num_pages, Hkv, fa_kv4_page_bytes(page_size, d,
+ *               group)], 16-byte aligned.
+ *   page_size:  a multiple of 16.  d: 64 or 128.  group: 32, 64 or 128, <= d.
+ *   page_table: DEVICE int32 [B, max_pages].  Entries behind a sequence's last
+ *               page are not read.
+ *   seqlens:    DEVICE int32 [B], the tokens of each sequence in the cache; a
+ *               writing call counts those that it writes.
+ *
+ * Values.  Along d, each group of `group` values x holds
+ *     min   = the least x (one of the bf16 inputs, so exact),
+ *     scale = bf16((max / 2 - min / 2) * f32(2 / 15)), 0 if below 2^-126,
+ *     code  = rint((x / 2 - min / 2) * (1 / (scale / 2)))      in 0 .. 15,
+ * the code computed in fp32, each operation rounded once, ties to even; the
+ * value held is min + scale * code.  A group with a NaN or an infinity holds
+ * NaN throughout; other groups of the row are not touched by it.
+ *
+ * Layout.  A head's page is page_size / 16 cells of 16 tokens, 16 d + 128 d /
+ * group bytes each: K codes [16][d / 2], V codes [16][d / 2], K parameters
+ * [16][d / group] (scale, min) bf16 pairs, V parameters likewise.  Within a K
+ * row the 32-bit word of values 8 w .. 8 w + 7 (lowest nibble first), w = 4 j +
+ * c with c < 4, stands at word c (d / 32) + j.  Within a V row the 16-bit half
+ * of values 4 h .. 4 h + 3, h = 8 q + g with g < 8, stands at half g (d / 32) +
+ * q; then the 32-byte sector s of the cell's V codes stands at sector
+ * (s & ~3) | ((s + (s >> 2)) & 3).
+ *
+ * Errors raised by the device (fa_get_device_error): FA_DEVERR_BAD_SEQLENS for
+ * a sequence whose counts are negative, above N or Nk, or do not fit (seqlens
+ * below the new tokens, or above max_pages * page_size), FA_DEVERR_BAD_PAGE for
+ * a page outside [0, num_pages).  Such a sequence, or such a page's tokens, is
+ * left out: nothing is read or written out of bounds.
+ */
+
+/* Bytes of one head's page, or a negative FA_ERR_* code. */
+FA_API int64_t fa_kv4_page_bytes(int page_size, int d, int group);
+
+/*
+ * Quantises new K and V rows into the cache: of each sequence its last n_b
+ * tokens, at positions seqlens[b] - n_b .. seqlens[b] - 1.
+ *   K, V: bf16 rows of Hkv * d contiguous values, k_stride and v_stride
+ *   elements apart (multiples of 8, at least Hkv * d: K and V may be parts of
+ *   the rows of a fused projection); 16-byte aligned.
+ *   dense  (cu_seqlens == NULL): n_b = N, row b * N + i; total = B * N.
+ *   packed: row cu_seqlens[b] + i, n_b = cu_seqlens[b + 1] - cu_seqlens[b] <= N;
+ *   total rows are there, those behind cu_seqlens[B] are not used.
+ * The positions written must be distinct places of the cache: no page that two
+ * sequences share may get new tokens at the same offset from both (which of
+ * the two a byte then comes from is not defined).  One kernel on the library
+ * stream.
+ * Errors: FA_ERR_BAD_SIZE, FA_ERR_UNSUPPORTED (d, group, page_size),
+ * FA_ERR_NULL_POINTER, FA_ERR_MISALIGNED (pointers, strides),
+ * FA_ERR_TOO_LARGE, FA_ERR_NO_DEVICE, FA_ERR_CUDA.
+ */
+FA_API int fa_kv4_append(const void *K, const void *V, int64_t k_stride, int64_t v_stride,
+                         void *cache, int num_pages, int page_size, const int32_t *page_table,
+                         int max_pages, const int32_t *seqlens, const int32_t *cu_seqlens, int B,
+                         int N, int64_t total, int Hkv, int d, int group);
+
+/*
+ * Reads tokens back: the arguments of fa_kv4_append, with K and V written.  The
+ * row of a token receives min + scale * code, rounded once to bf16.  Rows
+ * behind the last sequence, and those of a sequence or page that is left out,
+ * are left as they were.  n_b = seqlens[b] reads whole sequences.
+ */
+FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, const void *cache,
+                       int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                       const int32_t *seqlens, const int32_t *cu_seqlens, int B, int N,
+                       int64_t total, int Hkv, int d, int group);
 
 /*
  * Exact attention forward in fp32 throughout (fp32 Q, K, V, O, lse), on the

@@ -15,10 +15,12 @@ Raw C-ABI names (same names, same argument order, ints and pointers only):
 ``fa_attention_fwd_fp8``, ``fa_attention_fwd_fp8_varlen``,
 ``fa_attention_fp8_workspace_bytes``, ``fa_attention_fwd_host``,
 ``fa_attention_host_workspace_bytes``,
+``fa_kv4_page_bytes``, ``fa_kv4_append``, ``fa_kv4_read``,
 ``fa_set_stream``, ``fa_get_stream``, ``fa_get_device_error``, ``fa_strerror``,
 ``fa_version``, ``fa_debug_expire_next_wait``.
 Tensor-level helpers: :func:`softmax_rows`, :func:`attention_fwd`,
-:func:`attention_fwd_splitkv`, :func:`attention_bwd`, :func:`attention_fwd_fp8`.
+:func:`attention_fwd_splitkv`, :func:`attention_bwd`, :func:`attention_fwd_fp8`,
+:func:`kv4_cache`, :func:`kv4_append`, :func:`kv4_read`.
 """
 from __future__ import annotations
 
@@ -39,6 +41,7 @@ FA_ERR_TOO_LARGE = -6
 FA_ERR_NO_DEVICE = -7
 FA_DEVERR_WAIT_TIMEOUT = 0x1
 FA_DEVERR_BAD_SEQLENS = 0x2
+FA_DEVERR_BAD_PAGE = 0x4
 FA_ERR_SCRATCH_LIMIT = -8
 FA_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024   # static scratch of the _noalloc entry point
 
@@ -103,6 +106,11 @@ def lib():
                                                      i32, i32, i64, i32, f32, i32, vp, vp, i64]
         L.fa_attention_bwd_atomic_varlen_workspace_bytes.argtypes = [i32, i32, i32, i64, i32]
         L.fa_attention_bwd_atomic_varlen_workspace_bytes.restype = i64
+        L.fa_kv4_page_bytes.argtypes = [i32, i32, i32]
+        L.fa_kv4_page_bytes.restype = i64
+        L.fa_kv4_append.argtypes = [vp, vp, i64, i64, vp, i32, i32, vp, i32, vp, vp, i32, i32,
+                                    i64, i32, i32, i32]
+        L.fa_kv4_read.argtypes = L.fa_kv4_append.argtypes
         L.fa_set_stream.argtypes = [vp]
         L.fa_get_stream.argtypes = []
         L.fa_get_stream.restype = vp
@@ -118,7 +126,7 @@ def lib():
                      "fa_attention_bwd_atomic_varlen",
                      "fa_attention_fwd_splitkv_varlen",
                      "fa_attention_fwd_fp8", "fa_attention_fwd_fp8_varlen",
-                     "fa_attention_fwd_host",
+                     "fa_attention_fwd_host", "fa_kv4_append", "fa_kv4_read",
                      "fa_set_stream", "fa_get_device_error", "fa_version",
                      "fa_debug_expire_next_wait"):
             getattr(L, name).restype = ctypes.c_int
@@ -241,6 +249,22 @@ def fa_attention_bwd_atomic_varlen(q, k, v, o, do, lse, dq, dk, dv, d_buf, B, H,
 
 def fa_attention_bwd_atomic_varlen_workspace_bytes(B, H, N, total, d) -> int:
     return lib().fa_attention_bwd_atomic_varlen_workspace_bytes(B, H, N, total, d)
+
+
+def fa_kv4_page_bytes(page_size, d, group) -> int:
+    return lib().fa_kv4_page_bytes(page_size, d, group)
+
+
+def fa_kv4_append(k, v, k_stride, v_stride, cache, num_pages, page_size, page_table, max_pages,
+                  seqlens, cu_seqlens, B, N, total, Hkv, d, group) -> int:
+    return lib().fa_kv4_append(k, v, k_stride, v_stride, cache, num_pages, page_size, page_table,
+                               max_pages, seqlens, cu_seqlens, B, N, total, Hkv, d, group)
+
+
+def fa_kv4_read(k, v, k_stride, v_stride, cache, num_pages, page_size, page_table, max_pages,
+                seqlens, cu_seqlens, B, N, total, Hkv, d, group) -> int:
+    return lib().fa_kv4_read(k, v, k_stride, v_stride, cache, num_pages, page_size, page_table,
+                             max_pages, seqlens, cu_seqlens, B, N, total, Hkv, d, group)
 
 
 def fa_set_stream(stream_ptr) -> int:
@@ -587,7 +611,133 @@ def attention_bwd(q, k, v, o, do, lse, causal: bool = False, scale: float | None
     return dq, dk, dv
 
 
+# ---- 4-bit paged key/value cache ------------------------------------------------
+
+def _on(device):
+    """The tensors' device made current, for as long as the call takes."""
+    import torch
+    return torch.cuda.device(device)
+
+
+def kv4_cache(num_pages: int, kv_heads: int, page_size: int, d: int, group: int = 64,
+              device="cuda"):
+    """An empty 4-bit cache: a uint8 tensor [num_pages, kv_heads, page bytes].
+
+    Its contents are undefined until :func:`kv4_append` writes them.
+    """
+    import torch
+    nbytes = fa_kv4_page_bytes(page_size, d, group)
+    _check(int(min(nbytes, 0)), "fa_kv4_page_bytes")
+    return torch.empty((num_pages, kv_heads, nbytes), dtype=torch.uint8, device=device)
+
+
+def _kv4_args(cache, page_table, seqlens, cu_seqlens, d, group):
+    """The checked cache arguments: (num_pages, Hkv, page_size, B, max_pages)."""
+    import torch
+    if not (cache.is_cuda and cache.dtype == torch.uint8 and cache.dim() == 3
+            and cache.is_contiguous()):
+        raise ValueError("cache must be a contiguous uint8 CUDA tensor [pages, kv_heads, bytes]")
+    if d not in (64, 128) or group not in (32, 64, 128) or group > d:
+        raise FaError(FA_ERR_UNSUPPORTED, "kv4: d, group")
+    pages, hkv, nbytes = cache.shape
+    page_size, rest = divmod(nbytes, d + 8 * (d // group))
+    if rest or page_size == 0 or page_size % 16:
+        raise ValueError(f"cache has pages of {nbytes} bytes a head: not a whole number of cells "
+                         f"for d = {d}, group = {group}")
+    B = seqlens.numel()
+    for name, t, shape in (("page_table", page_table, None), ("seqlens", seqlens, (B,)),
+                           ("cu_seqlens", cu_seqlens, (B + 1,))):
+        if t is None:
+            continue
+        if not (t.dtype == torch.int32 and t.device == cache.device and t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 tensor on the cache's device")
+        if (t.dim() != 2 or t.shape[0] != B) if shape is None else tuple(t.shape) != shape:
+            raise ValueError(f"{name} has the wrong shape for {B} sequences")
+    return pages, hkv, page_size, B, page_table.shape[1]
+
+
+def _kv4_rows(call, where, k, v, cache, page_table, seqlens, cu_seqlens, max_new, group):
+    import torch
+    if not (k.dtype == v.dtype == torch.bfloat16 and k.shape == v.shape
+            and k.device == v.device == cache.device):
+        raise ValueError("k and v must be bf16 tensors of one shape on the cache's device")
+    if k.dim() != (4 if cu_seqlens is None else 3):
+        raise ValueError("k and v must be [B, N, kv_heads, d], or [total, kv_heads, d] with "
+                         "cu_seqlens")
+    hk, d = k.shape[-2:]
+    pages, hkv, page_size, B, max_pages = _kv4_args(cache, page_table, seqlens, cu_seqlens, d,
+                                                    group)
+    if hk != hkv:
+        raise ValueError(f"k and v have {hk} heads, the cache {hkv}")
+    strides = []
+    for t in (k, v):
+        st = t.stride()
+        if t.numel() and (st[-1] != 1 or (hkv > 1 and st[-2] != d)):
+            raise ValueError("a token's heads must be contiguous in k and v")
+        if cu_seqlens is None and t.shape[0] > 1 and t.shape[1] > 1 and \
+                st[0] != t.shape[1] * st[1]:
+            raise ValueError("k's and v's rows must be evenly spaced")
+        # a row's distance to the next; of a single row any will do
+        n = st[0] if t.dim() == 3 or t.shape[1] == 1 else st[1]
+        strides.append(n if t.numel() > hkv * d else hkv * d)
+    if cu_seqlens is None:
+        if k.shape[0] != B:
+            raise ValueError(f"k and v hold {k.shape[0]} sequences, seqlens {B}")
+        N = k.shape[1]
+        total = B * N
+    else:
+        total = k.shape[0]
+        N = total if max_new is None else int(max_new)
+    with _on(cache.device):
+        _use_current_stream(cache.device)
+        rc = call(_ptr(k), _ptr(v), *strides, _ptr(cache), pages, page_size, _ptr(page_table),
+                  max_pages, _ptr(seqlens), _ptr(cu_seqlens), B, N, total, hkv, d, group)
+    _check(rc, where)
+
+
+def kv4_append(k, v, cache, page_table, seqlens, cu_seqlens=None, max_new: int | None = None,
+               group: int = 64):
+    """Quantise new K and V rows into a 4-bit paged cache.
+
+    k, v: bf16 [B, N, kv_heads, d], or packed [total, kv_heads, d] with
+    ``cu_seqlens`` (int32 [B+1]) and ``max_new`` (the longest run of new tokens;
+    default: total).  A token's heads are contiguous, tokens may be any
+    multiple of 8 elements apart (slices of a fused projection).  ``cache``
+    from :func:`kv4_cache`; ``page_table`` int32 [B, max_pages]; ``seqlens``
+    int32 [B]: tokens in the cache AFTER the call; the new ones are each
+    sequence's last.
+    """
+    _kv4_rows(fa_kv4_append, "fa_kv4_append", k, v, cache, page_table, seqlens, cu_seqlens,
+              max_new, group)
+
+
+def kv4_read(cache, page_table, seqlens, total: int | None = None, d: int = 128, cu_seqlens=None,
+             max_new: int | None = None, group: int = 64, n: int = 1, k=None, v=None):
+    """The last tokens of each sequence from a 4-bit paged cache, as bf16 (k, v).
+
+    With ``cu_seqlens`` (int32 [B+1]) the last cu_seqlens[b+1] - cu_seqlens[b]
+    tokens of sequence b, packed into [total, kv_heads, d]; otherwise the last
+    ``n`` of each, [B, n, kv_heads, d].  ``k`` and ``v``: write into these (rows
+    that belong to no sequence are left as they are).
+    """
+    import torch
+    if k is None or v is None:
+        if cu_seqlens is None:
+            shape = (seqlens.numel(), n, cache.shape[1], d)
+        elif total is None:
+            raise ValueError("total (rows of k and v) is needed with cu_seqlens")
+        else:
+            shape = (total, cache.shape[1], d)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+    _kv4_rows(fa_kv4_read, "fa_kv4_read", k, v, cache, page_table, seqlens, cu_seqlens, max_new,
+              group)
+    return k, v
+
+
 __all__ = [
+    "kv4_cache", "kv4_append", "kv4_read", "fa_kv4_page_bytes", "fa_kv4_append", "fa_kv4_read",
+    "FA_DEVERR_BAD_PAGE",
     "build", "lib", "strerror", "FaError", "softmax_rows", "attention_fwd",
     "attention_fwd_splitkv", "attention_fwd_splitkv_varlen", "fa_attention_fwd_splitkv",
     "fa_attention_fwd_splitkv_varlen",

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "../../include/fa.h"
+#include "kv4.cuh"
 #include "launch.h"
 
 namespace fa {
@@ -759,6 +760,103 @@ int fa_attention_fwd_host(const void *Q, const void *K, const void *V, void *O, 
     if (!ok(cudaEventRecord(pp->done, pp->s_out)) || !ok(cudaStreamWaitEvent(s_main, pp->done, 0)))
         return join_and_fail(FA_ERR_CUDA);
     return FA_OK;
+}
+
+}  // extern "C"
+
+namespace fa {
+namespace {
+// The cache's own arguments, shared by the kv4 entry points.
+int check_kv4_format(int num_pages, int page_size, int max_pages, int Hkv, int d, int group)
+{
+    if (num_pages < 0 || page_size < 0 || max_pages < 0 || Hkv < 0)
+        return FA_ERR_BAD_SIZE;
+    if ((d != 64 && d != 128) || (group != 32 && group != 64 && group != 128) || group > d ||
+        page_size == 0 || page_size % kv4::kCellTokens != 0)
+        return FA_ERR_UNSUPPORTED;
+    if (int64_t(max_pages) * page_size > (int64_t(1) << 31) - 512 || Hkv > 65535)
+        return FA_ERR_TOO_LARGE;
+    return FA_OK;
+}
+
+// fa_kv4_append (write) and fa_kv4_read.
+int kv4_rows(const void *K, const void *V, int64_t k_stride, int64_t v_stride, const void *cache,
+             int num_pages, int page_size, const int32_t *page_table, int max_pages,
+             const int32_t *seqlens, const int32_t *cu_seqlens, int B, int N, int64_t total,
+             int Hkv, int d, int group, bool write)
+{
+    if (B < 0 || N < 0 || total < 0)
+        return FA_ERR_BAD_SIZE;
+    const int rc = check_kv4_format(num_pages, page_size, max_pages, Hkv, d, group);
+    if (rc != FA_OK)
+        return rc;
+    if (cu_seqlens == nullptr && total != int64_t(B) * N)
+        return FA_ERR_BAD_SIZE;
+    if (B == 0 || N == 0 || total == 0 || Hkv == 0)
+        return FA_OK;
+    if (!K || !V || !cache || !page_table || !seqlens)
+        return FA_ERR_NULL_POINTER;
+    if (k_stride < int64_t(Hkv) * d || v_stride < int64_t(Hkv) * d)
+        return FA_ERR_BAD_SIZE;
+    if (!aligned(K, 16) || !aligned(V, 16) || !aligned(cache, 16) || !aligned(page_table, 4) ||
+        !aligned(seqlens, 4) || (cu_seqlens && !aligned(cu_seqlens, 4)) || k_stride % 8 != 0 ||
+        v_stride % 8 != 0)
+        return FA_ERR_MISALIGNED;
+    if (total > (int64_t(1) << 31) - 512 || k_stride > (int64_t(1) << 31) ||
+        v_stride > (int64_t(1) << 31))
+        return FA_ERR_TOO_LARGE;
+    DeviceInfo *dev = current_device();
+    if (dev == nullptr)
+        return FA_ERR_NO_DEVICE;
+    Kv4CacheArgs a;
+    a.K = const_cast<void *>(K);           // read-only for the appending kernel
+    a.V = const_cast<void *>(V);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.cache = const_cast<void *>(cache);   // read-only for the reading kernel
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.page_table = page_table;
+    a.max_pages = max_pages;
+    a.seqlens = seqlens;
+    a.cu_seqlens = cu_seqlens;
+    a.B = B;
+    a.N = N;
+    a.total = total;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.group = group;
+    a.err_word = dev->err_word;
+    return write ? launch_kv4_append(a, t_stream) : launch_kv4_read(a, t_stream);
+}
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+int64_t fa_kv4_page_bytes(int page_size, int d, int group)
+{
+    const int rc = fa::check_kv4_format(0, page_size, 1, 0, d, group);
+    return rc != FA_OK ? rc
+                       : int64_t(page_size) / fa::kv4::kCellTokens * fa::kv4::cell_bytes(d, group);
+}
+
+int fa_kv4_append(const void *K, const void *V, int64_t k_stride, int64_t v_stride, void *cache,
+                  int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                  const int32_t *seqlens, const int32_t *cu_seqlens, int B, int N, int64_t total,
+                  int Hkv, int d, int group)
+{
+    return fa::kv4_rows(K, V, k_stride, v_stride, cache, num_pages, page_size, page_table,
+                        max_pages, seqlens, cu_seqlens, B, N, total, Hkv, d, group, true);
+}
+
+int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, const void *cache,
+                int num_pages, int page_size, const int32_t *page_table, int max_pages,
+                const int32_t *seqlens, const int32_t *cu_seqlens, int B, int N, int64_t total,
+                int Hkv, int d, int group)
+{
+    return fa::kv4_rows(K, V, k_stride, v_stride, cache, num_pages, page_size, page_table,
+                        max_pages, seqlens, cu_seqlens, B, N, total, Hkv, d, group, false);
 }
 
 int fa_attention_fwd_f32(const float *Q, const float *K, const float *V, float *O, float *lse,

@@ -158,4 +158,22 @@ struct Fp8QuantArgs {
 };
 int launch_fp8_quantize(const Fp8QuantArgs &a, cudaStream_t stream);
 
+// Writing to and reading from the 4-bit paged cache (layouts as in fa.h).
+struct Kv4CacheArgs {
+    void *K, *V;               // read by the appending kernel, written by the reading one
+    int64_t k_stride, v_stride;
+    void *cache;               // the other way round
+    int num_pages, page_size;
+    const int32_t *page_table;
+    int max_pages;
+    const int32_t *seqlens;
+    const int32_t *cu_seqlens; // or nullptr: N rows each
+    int B, N;
+    int64_t total;
+    int Hkv, d, group;
+    int *err_word;
+};
+int launch_kv4_append(const Kv4CacheArgs &a, cudaStream_t stream);
+int launch_kv4_read(const Kv4CacheArgs &a, cudaStream_t stream);
+
 }  // namespace fa
