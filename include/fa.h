@@ -506,6 +506,46 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
                        int64_t total, int Hkv, int d, int group);
 
 /*
+ * Exact attention of bf16 queries on the cache's values (min + scale * code,
+ * unrounded): S = scale * Q K^T (+ mask), P = softmax(S), O = P V, lse as in
+ * fa_attention_fwd, fp32 accumulation.  A decode step has Nq = 1 (or a few
+ * drafted tokens); chunks of a prompt any Nq.  Query head h reads kv head
+ * h / (H / Hkv); H is a multiple of Hkv.
+ *   dense  (cu_seqlens_q == NULL): Q rows and O [B, Nq, H, d], lse [B, H, Nq];
+ *          total_q = B * Nq.
+ *   packed: Q rows and O [total_q, H, d], lse [H, total_q]; cu_seqlens_q DEVICE
+ *          int32 [B + 1], Nq the most queries of a sequence (an upper bound is
+ *          fine).  Rows behind the last sequence are left as they were.
+ *   Q: rows of H * d contiguous bf16, q_stride elements apart (a multiple of
+ *   8, at least H * d).  O: contiguous bf16.
+ *   seqlens: each sequence's keys, 0 .. Nk (Nk: an upper bound, <= max_pages *
+ *   page_size).
+ *   causal != 0: query i of n sees keys j <= i + seqlens[b] - n (bottom-right,
+ *   as in fa_attention_fwd_splitkv); otherwise all seqlens[b] keys.  A query
+ *   that sees no key gets O = 0 and lse = -inf.  What the cache holds behind a
+ *   sequence's end, or at keys that a query does not see, does not reach its
+ *   result, NaN or not.
+ *   workspace: DEVICE scratch owned by the caller, 256-byte aligned, at least
+ *   fa_attention_kv4_workspace_bytes(Nq, H, Hkv, d) bytes; contents on entry
+ *   are ignored.  Calls that may run at the same time need one each.
+ * B <= 1024.  Results do not depend on timing: the same call gives the same
+ * bits.  Two kernels on the library stream, no synchronisation.
+ * Errors: FA_ERR_BAD_SIZE (also a workspace that is too small, Nk above the
+ * table, H no multiple of Hkv), FA_ERR_UNSUPPORTED (d, group, page_size),
+ * FA_ERR_NULL_POINTER, FA_ERR_MISALIGNED, FA_ERR_TOO_LARGE, FA_ERR_NO_DEVICE,
+ * FA_ERR_CUDA.
+ */
+FA_API int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num_pages,
+                            int page_size, const int32_t *page_table, int max_pages,
+                            const int32_t *seqlens, const int32_t *cu_seqlens_q, void *O,
+                            float *lse, int B, int Nq, int64_t total_q, int Nk, int H, int Hkv,
+                            int d, int group, float scale, int causal, void *workspace,
+                            int64_t workspace_bytes);
+
+/* Workspace bytes fa_attention_kv4 needs, or a negative FA_ERR_* code. */
+FA_API int64_t fa_attention_kv4_workspace_bytes(int Nq, int H, int Hkv, int d);
+
+/*
  * Exact attention forward in fp32 throughout (fp32 Q, K, V, O, lse), on the
  * CUDA cores, for inputs that need fp32 accuracy.  Same definition, layouts,
  * masks and cu_seqlens convention as fa_attention_fwd (the packed form reads

@@ -16,11 +16,12 @@ Raw C-ABI names (same names, same argument order, ints and pointers only):
 ``fa_attention_fp8_workspace_bytes``, ``fa_attention_fwd_host``,
 ``fa_attention_host_workspace_bytes``,
 ``fa_kv4_page_bytes``, ``fa_kv4_append``, ``fa_kv4_read``,
+``fa_attention_kv4``, ``fa_attention_kv4_workspace_bytes``,
 ``fa_set_stream``, ``fa_get_stream``, ``fa_get_device_error``, ``fa_strerror``,
 ``fa_version``, ``fa_debug_expire_next_wait``.
 Tensor-level helpers: :func:`softmax_rows`, :func:`attention_fwd`,
 :func:`attention_fwd_splitkv`, :func:`attention_bwd`, :func:`attention_fwd_fp8`,
-:func:`kv4_cache`, :func:`kv4_append`, :func:`kv4_read`.
+:func:`kv4_cache`, :func:`kv4_append`, :func:`kv4_read`, :func:`attention_kv4`.
 """
 from __future__ import annotations
 
@@ -111,6 +112,10 @@ def lib():
         L.fa_kv4_append.argtypes = [vp, vp, i64, i64, vp, i32, i32, vp, i32, vp, vp, i32, i32,
                                     i64, i32, i32, i32]
         L.fa_kv4_read.argtypes = L.fa_kv4_append.argtypes
+        L.fa_attention_kv4.argtypes = [vp, i64, vp, i32, i32, vp, i32, vp, vp, vp, vp, i32, i32,
+                                       i64, i32, i32, i32, i32, i32, f32, i32, vp, i64]
+        L.fa_attention_kv4_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.fa_attention_kv4_workspace_bytes.restype = i64
         L.fa_set_stream.argtypes = [vp]
         L.fa_get_stream.argtypes = []
         L.fa_get_stream.restype = vp
@@ -127,7 +132,7 @@ def lib():
                      "fa_attention_fwd_splitkv_varlen",
                      "fa_attention_fwd_fp8", "fa_attention_fwd_fp8_varlen",
                      "fa_attention_fwd_host", "fa_kv4_append", "fa_kv4_read",
-                     "fa_set_stream", "fa_get_device_error", "fa_version",
+                     "fa_attention_kv4", "fa_set_stream", "fa_get_device_error", "fa_version",
                      "fa_debug_expire_next_wait"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -265,6 +270,18 @@ def fa_kv4_read(k, v, k_stride, v_stride, cache, num_pages, page_size, page_tabl
                 seqlens, cu_seqlens, B, N, total, Hkv, d, group) -> int:
     return lib().fa_kv4_read(k, v, k_stride, v_stride, cache, num_pages, page_size, page_table,
                              max_pages, seqlens, cu_seqlens, B, N, total, Hkv, d, group)
+
+
+def fa_attention_kv4(q, q_stride, cache, num_pages, page_size, page_table, max_pages, seqlens,
+                     cu_seqlens_q, o, lse, B, Nq, total_q, Nk, H, Hkv, d, group, scale, causal,
+                     workspace, workspace_bytes) -> int:
+    return lib().fa_attention_kv4(q, q_stride, cache, num_pages, page_size, page_table, max_pages,
+                                  seqlens, cu_seqlens_q, o, lse, B, Nq, total_q, Nk, H, Hkv, d,
+                                  group, scale, causal, workspace, workspace_bytes)
+
+
+def fa_attention_kv4_workspace_bytes(Nq, H, Hkv, d) -> int:
+    return lib().fa_attention_kv4_workspace_bytes(Nq, H, Hkv, d)
 
 
 def fa_set_stream(stream_ptr) -> int:
@@ -656,6 +673,24 @@ def _kv4_args(cache, page_table, seqlens, cu_seqlens, d, group):
     return pages, hkv, page_size, B, page_table.shape[1]
 
 
+def _row_stride(t, heads, d, name):
+    """Elements between the token rows of t ([B, N, heads, d] or [total, heads, d])."""
+    st = t.stride()
+    if t.numel() <= heads * d:             # one row: any distance will do
+        if t.numel() and not t.is_contiguous():
+            raise ValueError(f"a token's heads must be contiguous in {name}")
+        return heads * d
+    if st[-1] != 1 or (heads > 1 and st[-2] != d):
+        raise ValueError(f"a token's heads must be contiguous in {name}")
+    if t.dim() == 3:
+        return st[0]
+    if t.shape[1] == 1:
+        return st[0]
+    if t.shape[0] > 1 and st[0] != t.shape[1] * st[1]:
+        raise ValueError(f"{name}'s rows must be evenly spaced")
+    return st[1]
+
+
 def _kv4_rows(call, where, k, v, cache, page_table, seqlens, cu_seqlens, max_new, group):
     import torch
     if not (k.dtype == v.dtype == torch.bfloat16 and k.shape == v.shape
@@ -669,17 +704,7 @@ def _kv4_rows(call, where, k, v, cache, page_table, seqlens, cu_seqlens, max_new
                                                     group)
     if hk != hkv:
         raise ValueError(f"k and v have {hk} heads, the cache {hkv}")
-    strides = []
-    for t in (k, v):
-        st = t.stride()
-        if t.numel() and (st[-1] != 1 or (hkv > 1 and st[-2] != d)):
-            raise ValueError("a token's heads must be contiguous in k and v")
-        if cu_seqlens is None and t.shape[0] > 1 and t.shape[1] > 1 and \
-                st[0] != t.shape[1] * st[1]:
-            raise ValueError("k's and v's rows must be evenly spaced")
-        # a row's distance to the next; of a single row any will do
-        n = st[0] if t.dim() == 3 or t.shape[1] == 1 else st[1]
-        strides.append(n if t.numel() > hkv * d else hkv * d)
+    strides = _row_stride(k, hkv, d, "k"), _row_stride(v, hkv, d, "v")
     if cu_seqlens is None:
         if k.shape[0] != B:
             raise ValueError(f"k and v hold {k.shape[0]} sequences, seqlens {B}")
@@ -735,8 +760,73 @@ def kv4_read(cache, page_table, seqlens, total: int | None = None, d: int = 128,
     return k, v
 
 
+def attention_kv4(q, cache, page_table, seqlens, max_seqlen: int | None = None, group: int = 64,
+                  causal: bool = True, scale: float | None = None, cu_seqlens=None,
+                  max_q: int | None = None, out=None, lse=None, workspace=None):
+    """Attention of bf16 queries on a 4-bit paged cache.
+
+    q: [B, Nq, H, d] -> (O [B, Nq, H, d], lse [B, H, Nq] fp32), or packed
+    [total, H, d] with ``cu_seqlens`` (int32 [B+1]) and ``max_q`` (the most
+    queries of a sequence; default: total) -> (O [total, H, d], lse [H,
+    total]).  H is a multiple of the cache's kv heads; query rows may be any
+    multiple of 8 elements apart.  ``seqlens`` int32 [B]: keys of each sequence,
+    at most ``max_seqlen`` (default: what the page table can hold).  causal:
+    query i of n sees keys j <= i + seqlens[b] - n.  The workspace is allocated
+    here (torch) unless given (uint8, fa_attention_kv4_workspace_bytes).
+    """
+    import torch
+    if q.dtype != torch.bfloat16 or q.device != cache.device:
+        raise ValueError("q must be a bf16 tensor on the cache's device")
+    if q.dim() != (4 if cu_seqlens is None else 3):
+        raise ValueError("q must be [B, Nq, H, d], or [total, H, d] with cu_seqlens")
+    H, d = q.shape[-2:]
+    pages, hkv, page_size, B, max_pages = _kv4_args(cache, page_table, seqlens, cu_seqlens, d,
+                                                    group)
+    if hkv == 0 or H % hkv:
+        raise ValueError(f"{H} query heads on {hkv} kv heads")
+    q_stride = _row_stride(q, H, d, "q")
+    if cu_seqlens is None:
+        if q.shape[0] != B:
+            raise ValueError(f"q holds {q.shape[0]} sequences, seqlens {B}")
+        Nq = q.shape[1]
+        total = B * Nq
+        lse_shape = (B, H, Nq)
+    else:
+        total = q.shape[0]
+        Nq = total if max_q is None else int(max_q)
+        lse_shape = (H, total)
+    Nk = max_pages * page_size if max_seqlen is None else int(max_seqlen)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif not (out.shape == q.shape and out.dtype == q.dtype and out.device == q.device
+              and out.is_contiguous()):
+        raise ValueError("out must be a contiguous tensor like q")
+    if lse is None:
+        lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+    elif not (tuple(lse.shape) == lse_shape and lse.dtype == torch.float32
+              and lse.device == q.device and lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 tensor {list(lse_shape)}")
+    nbytes = fa_attention_kv4_workspace_bytes(Nq, H, hkv, d)
+    _check(int(min(nbytes, 0)), "fa_attention_kv4_workspace_bytes")
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    elif not (workspace.dtype == torch.uint8 and workspace.device == q.device
+              and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    with _on(q.device):
+        _use_current_stream(q.device)
+        rc = fa_attention_kv4(_ptr(q), q_stride, _ptr(cache), pages, page_size, _ptr(page_table),
+                              max_pages, _ptr(seqlens), _ptr(cu_seqlens), _ptr(out), _ptr(lse), B,
+                              Nq, total, Nk, H, hkv, d, group, float(scale), int(bool(causal)),
+                              _ptr(workspace), workspace.numel())
+    _check(rc, "fa_attention_kv4")
+    return out, lse
+
+
 __all__ = [
-    "kv4_cache", "kv4_append", "kv4_read", "fa_kv4_page_bytes", "fa_kv4_append", "fa_kv4_read",
+    "attention_kv4", "fa_attention_kv4", "fa_attention_kv4_workspace_bytes", "kv4_cache", "kv4_append", "kv4_read", "fa_kv4_page_bytes", "fa_kv4_append", "fa_kv4_read",
     "FA_DEVERR_BAD_PAGE",
     "build", "lib", "strerror", "FaError", "softmax_rows", "attention_fwd",
     "attention_fwd_splitkv", "attention_fwd_splitkv_varlen", "fa_attention_fwd_splitkv",

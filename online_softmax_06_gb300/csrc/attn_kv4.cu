@@ -1,0 +1,651 @@
+// attn_kv4.cu -- attention over the 4-bit paged cache (kv4.cuh, include/fa.h).
+//
+// With k_j = mK_j + sK_j u_j and v_j = mV_j + sV_j w_j (u, w the codes 0..15, s
+// and m per token and group of the head dimension):
+//     S_ij = scale * sum_g ( sK_jg * sum_{k in g} q_ik u_jk + mK_jg * Qbar_ig ),
+//     Qbar_ig = sum_{k in g} q_ik,
+//     O_ik = sum_j (P_ij sV_jg) w_jk + sum_j P_ij mV_jg        (k in group g),
+// so the codes go into the matrix products as they are and the scales act on
+// the small results: nothing is dequantised.
+//
+// A code as an fp16 number costs one logical operation for two values: the
+// nibble u at the low end of a half-word IS the subnormal u * 2^-24, and the
+// nibble above it 16 u * 2^-24 (fp16 is linear up to 2^11 units of 2^-24).  The
+// matrix instructions take subnormals exactly; 2^24 and the 16 go into Q and
+// the epilogue.  Q is scaled per row by a power of two into fp16's range, so
+// its 8 bits are exact down to 2^-26 of the row's largest value.  P s is
+// rounded to fp16 (2^-11), against 2^-8 for bf16.
+//
+// Layout: keys are the rows (M = 16 tokens), query rows (query, head of the
+// group) the columns (N = 8) of mma.m16n8k16, S^T = K Q^T and O^T = V^T P^T, so
+// that a decode step with up to 8 heads a kv head wastes nothing.  tcgen05 has
+// M = 64 at least and takes its operands from shared or tensor memory: the
+// codes would be expanded fourfold into shared memory first, which costs more
+// than the products.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/fa.h"
+#include "kv4.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kBlock = kWarps * kv4::kCellTokens;   // tokens of a block: a cell each warp
+constexpr float kNoRef = -1e30f;   // reference of a row that has seen no key: exp2(-inf - kNoRef) = 0
+// A row's reference is max(S + log2 w), w the weight of a key's V parameters, so
+// that P s <= 1 in fp16 whatever the scales are; it may lag by a factor of 16.
+// w >= 2^-92 keeps P <= 2^96 and the sum of 2^31 of them finite.
+constexpr float kLag = 16.f;
+constexpr float kLeastWeight = 0x1p-92f;
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+                 "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+// A work item is (sequence, kv head, tile of R query rows); its keys are cut
+// into blocks of kBlock tokens.  All items' blocks, sequence by sequence, form
+// one line that is cut into equal ranges, one a CTA: ragged batches and single
+// long sequences fill the GPU alike, and nothing of it needs the host.
+struct Desc {          // of an item that begins in this CTA's range and does not end there
+    int parts;         // CTAs that hold a part (0: no such item)
+    int b, kvh, tile;
+};
+
+// Workspace: Desc[kMaxCtas], then (reference, sum) [2 kMaxCtas][R], then
+// the unnormalised O [2 kMaxCtas][R][d] fp32.  A CTA's slot 0 holds the part of
+// an item that began before its range, slot 1 that of one that goes on after.
+struct Parts {
+    Desc *desc;
+    float2 *ml;
+    float *O;
+};
+
+template <int R>
+__host__ __device__ inline Parts parts_of(void *ws)
+{
+    Parts p;
+    p.desc = static_cast<Desc *>(ws);
+    p.ml = reinterpret_cast<float2 *>(p.desc + kKv4MaxCtas);
+    p.O = reinterpret_cast<float *>(p.ml + 2 * kKv4MaxCtas * R);
+    return p;
+}
+
+// Blocks of a sequence: its items have one at least, so that a row without a
+// key is written too.
+__device__ __forceinline__ int blocks_of(int L) { return L <= 0 ? 1 : (L + kBlock - 1) / kBlock; }
+
+// Sequence b's first query row and query count, or a count of 0 (with the
+// error recorded) where its lengths are not allowed.
+__device__ __forceinline__ int2 queries_of(const Kv4AttnArgs &a, int b)
+{
+    if (a.cu_seqlens_q == nullptr)
+        return make_int2(b * a.Nq, a.Nq);
+    const int c0 = a.cu_seqlens_q[b], n = a.cu_seqlens_q[b + 1] - c0;
+    return make_int2(c0, n);
+}
+
+template <int D, int G, int NT>
+__global__ void __launch_bounds__(kThreads) attn_kv4_kernel(const Kv4AttnArgs a)
+{
+    constexpr int R = 8 * NT;              // query rows of a tile
+    constexpr int NG = D / G;              // groups of the head dimension
+    constexpr int NJ = D / 32;             // words a lane holds of a K row
+    constexpr int kCell = kv4::cell_bytes(D, G);
+    constexpr int kRow = D + 4;            // padded fp32 row of the merge buffer
+    extern __shared__ uint8_t smem[];
+    uint32_t *s_pre = reinterpret_cast<uint32_t *>(smem);           // [B + 1] blocks before b
+    float *s_ref = reinterpret_cast<float *>(s_pre + kKv4MaxSeqs + 4);  // [kWarps][R]
+    float *s_sum = s_ref + kWarps * R;                              // [kWarps][R]
+    float *s_O = s_sum + kWarps * R;                                // [kWarps][8][kRow]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int grp = a.H / a.Hkv;
+
+    // ---- the line of blocks ------------------------------------------------
+    const int per = (a.B + kThreads - 1) / kThreads;
+    uint32_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b >= a.B)
+            break;
+        const int2 q = queries_of(a, b);
+        const int L = a.seqlens[b];
+        uint32_t n = 0;
+        if (q.y < 0 || q.y > a.Nq || q.x < 0 || int64_t(q.x) + q.y > a.total_q || L < 0 ||
+            L > a.Nk)
+            record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
+        else
+            n = uint32_t((q.y * grp + R - 1) / R) * a.Hkv * blocks_of(L);
+        s_pre[b + 1] = n;
+        mine += n;
+    }
+    // exclusive scan over the threads, then over each thread's sequences
+    uint32_t incl = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += t;
+    }
+    uint32_t *s_w = reinterpret_cast<uint32_t *>(s_ref);
+    if (lane == 31)
+        s_w[warp] = incl;
+    __syncthreads();
+    uint32_t base = incl - mine;
+    for (int w = 0; w < warp; ++w)
+        base += s_w[w];
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b >= a.B)
+            break;
+        base += s_pre[b + 1];
+        s_pre[b + 1] = base;
+    }
+    if (tid == 0)
+        s_pre[0] = 0;
+    __syncthreads();
+    const uint64_t T = s_pre[a.B];
+    const uint32_t n_ctas = uint32_t(T < gridDim.x ? T : gridDim.x);
+    const Parts parts = parts_of<R>(a.workspace);
+    if (blockIdx.x >= n_ctas) {
+        if (tid == 0)
+            parts.desc[blockIdx.x].parts = 0;
+        return;
+    }
+    const uint32_t begin = uint32_t(T * blockIdx.x / n_ctas);
+    const uint32_t end = uint32_t(T * (blockIdx.x + 1) / n_ctas);
+    Desc desc{0, 0, 0, 0};
+
+    for (uint32_t cur = begin; cur < end;) {
+        // ---- the item at `cur` ---------------------------------------------
+        int lo = 0, hi = a.B;              // s_pre[lo] <= cur < s_pre[lo + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_pre[mid] <= cur)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const int b = lo;
+        const int2 qb = queries_of(a, b);
+        const int L = a.seqlens[b], nb = blocks_of(L);
+        const int tiles = (qb.y * grp + R - 1) / R;
+        const uint32_t item = (cur - s_pre[b]) / nb, blk0 = (cur - s_pre[b]) % nb;
+        const int kvh = item / tiles, tile = item % tiles;
+        const uint32_t item0 = cur - blk0;                      // the item's first block
+        const uint32_t stop = min(end, item0 + nb);
+        const int blk1 = int(stop - item0);
+        const int rows = min(R, qb.y * grp - tile * R);         // rows of this tile
+
+        // ---- Q: fragments, group sums, factors -----------------------------
+        uint32_t qf[NT][2 * NJ][2];
+        float mul[NT][2], qbar[NT][NG][2];     // of rows 2 c, 2 c + 1 of n-tile nt
+        int lim[NT][2];                        // keys that these rows see
+        int lim_least = L;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + g;
+            uint4 w[NJ];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                w[j] = make_uint4(0, 0, 0, 0);
+            if (r < rows) {
+                const int i = (tile * R + r) / grp, h = kvh * grp + (tile * R + r) % grp;
+                const auto *src = static_cast<const __nv_bfloat16 *>(a.Q) +
+                                  int64_t(qb.x + i) * a.q_stride + int64_t(h) * D + 8 * c;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    w[j] = __ldg(reinterpret_cast<const uint4 *>(src + 32 * j));
+            }
+            float big = 0.f, sum[NG];
+#pragma unroll
+            for (int x = 0; x < NG; ++x)
+                sum[x] = 0.f;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    big = fmaxf(big, fmaxf(fabsf(bf16_lo(v[e])), fabsf(bf16_hi(v[e]))));
+                    sum[32 * j / G] += bf16_lo(v[e]) + bf16_hi(v[e]);
+                }
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // a power of two that brings the row's largest value into [2^12, 2^13)
+            const int ex = big > 0.f ? max(-100, min(100, 139 - int(__float_as_uint(big) >> 23)))
+                                     : 0;
+            const float up = __uint_as_float(uint32_t(127 + ex) << 23);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const float x0 = bf16_lo(w[j].x) * up, x1 = bf16_hi(w[j].x) * up,
+                            x2 = bf16_lo(w[j].y) * up, x3 = bf16_hi(w[j].y) * up,
+                            x4 = bf16_lo(w[j].z) * up, x5 = bf16_hi(w[j].z) * up,
+                            x6 = bf16_lo(w[j].w) * up, x7 = bf16_hi(w[j].w) * up;
+                // nibbles i and i + 4 of a word are a half-word apart; the upper
+                // nibble of a byte counts 16 times
+                qf[nt][2 * j][0] = pack_f16(x0, x4);
+                qf[nt][2 * j][1] = pack_f16(x1 * 0.0625f, x5 * 0.0625f);
+                qf[nt][2 * j + 1][0] = pack_f16(x2, x6);
+                qf[nt][2 * j + 1][1] = pack_f16(x3 * 0.0625f, x7 * 0.0625f);
+            }
+            const float sc = a.scale * kLog2e;
+            const float m = sc * __uint_as_float(uint32_t(127 + 24 - ex) << 23);
+#pragma unroll
+            for (int x = 0; x < NG; ++x) {
+                sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
+                sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
+                sum[x] *= sc;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mul[nt][e] = __shfl_sync(0xffffffffu, m, (2 * c + e) * 4);
+#pragma unroll
+                for (int x = 0; x < NG; ++x)
+                    qbar[nt][x][e] = __shfl_sync(0xffffffffu, sum[x], (2 * c + e) * 4);
+                const int i = (tile * R + nt * 8 + 2 * c + e) / grp;
+                lim[nt][e] = a.causal ? min(L, L - qb.y + i + 1) : L;
+            }
+        }
+        if (a.causal)
+            lim_least = L - qb.y + tile * R / grp + 1;
+
+        // ---- the keys ----------------------------------------------------------
+        float O[NT][D / 16][4], ref[NT][2], sum[NT][2], pm[NT][NG][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x)
+                O[nt][x][0] = O[nt][x][1] = O[nt][x][2] = O[nt][x][3] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                ref[nt][e] = kNoRef;
+                sum[nt][e] = 0.f;
+#pragma unroll
+                for (int x = 0; x < NG; ++x)
+                    pm[nt][x][e] = 0.f;
+            }
+        }
+        const int cells = a.page_size / kv4::kCellTokens;
+        const int last = a.causal ? min(L, L - qb.y + (tile * R + rows - 1) / grp + 1) : L;
+        for (int blk = int(blk0); blk < blk1; ++blk) {
+            const int tok = blk * kBlock + warp * kv4::kCellTokens;
+            if (tok >= last)
+                break;
+            const int page = a.page_table[int64_t(b) * a.max_pages + tok / a.page_size];
+            if (page < 0 || page >= a.num_pages) {
+                record_device_error(a.err_word, FA_DEVERR_BAD_PAGE);
+                continue;
+            }
+            const uint8_t *cell =
+                static_cast<const uint8_t *>(a.cache) +
+                ((int64_t(page) * a.Hkv + kvh) * cells + tok % a.page_size / kv4::kCellTokens) *
+                    kCell;
+
+            // S^T = K Q^T: lane (g, c) holds tokens g, g + 8
+            uint32_t k0[NJ], k1[NJ];
+            if constexpr (NJ == 4) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(cell + g * 64 + c * 16);
+                const uint4 y = *reinterpret_cast<const uint4 *>(cell + (g + 8) * 64 + c * 16);
+                k0[0] = x.x, k0[1] = x.y, k0[2] = x.z, k0[3] = x.w;
+                k1[0] = y.x, k1[1] = y.y, k1[2] = y.z, k1[3] = y.w;
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2 *>(cell + g * 32 + c * 8);
+                const uint2 y = *reinterpret_cast<const uint2 *>(cell + (g + 8) * 32 + c * 8);
+                k0[0] = x.x, k0[1] = x.y;
+                k1[0] = y.x, k1[1] = y.y;
+            }
+            // parameters of tokens g and g + 8; of a token behind the sequence's
+            // end they may be anything and count as 0
+            float sK[NG][2], mK[NG][2], sV[NG][2], mV[NG][2], w[2];
+            const auto *kp = reinterpret_cast<const uint32_t *>(cell + kv4::k_par_off(D));
+            const auto *vp = reinterpret_cast<const uint32_t *>(cell + kv4::v_par_off(D, G));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const bool in = tok + g + 8 * t < L;
+                float s_big = 0.f, m_big = 0.f;
+#pragma unroll
+                for (int x = 0; x < NG; ++x) {
+                    const uint32_t pk = in ? kp[(g + 8 * t) * NG + x] : 0;
+                    const uint32_t pv = in ? vp[(g + 8 * t) * NG + x] : 0;
+                    sK[x][t] = bf16_lo(pk);
+                    mK[x][t] = bf16_hi(pk);
+                    sV[x][t] = bf16_lo(pv);
+                    mV[x][t] = bf16_hi(pv);
+                    s_big = fmaxf(s_big, sV[x][t]);
+                    m_big = fmaxf(m_big, fabsf(mV[x][t]));
+                }
+                // |m| counts too (a constant group has s = 0), so that P m stays
+                // finite in fp32
+                w[t] = fmaxf(fmaxf(s_big, m_big * 0x1p-12f), kLeastWeight);
+            }
+            const bool masked = tok + kv4::kCellTokens > lim_least;
+            uint32_t pf[NT][NG][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float acc[NG][4];
+#pragma unroll
+                for (int x = 0; x < NG; ++x)
+                    acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
+                    mma(acc[32 * j / G], k0[j] & kLo, k1[j] & kLo, k0[j] & kHi, k1[j] & kHi,
+                        qf[nt][2 * j][0], qf[nt][2 * j][1]);
+                    const uint32_t y0 = k0[j] >> 8, y1 = k1[j] >> 8;
+                    mma(acc[32 * j / G], y0 & kLo, y1 & kLo, y0 & kHi, y1 & kHi,
+                        qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+                }
+                float S[2][2], P[2][2];        // [token g, g + 8][row 2 c, 2 c + 1]
+                bool seen[2][2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = 0.f, y = 0.f;
+#pragma unroll
+                        for (int gr = 0; gr < NG; ++gr) {
+                            x = fmaf(sK[gr][t], acc[gr][2 * t + e], x);
+                            y = fmaf(mK[gr][t], qbar[nt][gr][e], y);
+                        }
+                        S[t][e] = fmaf(x, mul[nt][e], y);
+                        seen[t][e] = !masked || tok + g + 8 * t < lim[nt][e];
+                        if (!seen[t][e])
+                            S[t][e] = -INFINITY;
+                    }
+                float over = 0.f;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        P[t][e] = ptx::ex2(S[t][e] - ref[nt][e]);
+                        over = fmaxf(over, P[t][e] * w[t]);
+                    }
+                if (__any_sync(0xffffffffu, over > kLag)) {
+                    // a row outgrew its reference: every row's becomes the
+                    // largest S + log2 w seen
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float m = fmaxf(S[0][e] + __log2f(w[0]), S[1][e] + __log2f(w[1]));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                        m = fmaxf(m, ref[nt][e]);
+                        const float f = ptx::ex2(ref[nt][e] - m);
+                        ref[nt][e] = m;
+                        sum[nt][e] *= f;
+#pragma unroll
+                        for (int x = 0; x < NG; ++x)
+                            pm[nt][x][e] *= f;
+#pragma unroll
+                        for (int x = 0; x < D / 16; ++x) {
+                            O[nt][x][e] *= f;
+                            O[nt][x][2 + e] *= f;
+                        }
+                        P[0][e] = ptx::ex2(S[0][e] - m);
+                        P[1][e] = ptx::ex2(S[1][e] - m);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    sum[nt][e] += P[0][e] + P[1][e];
+#pragma unroll
+                for (int x = 0; x < NG; ++x)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        float y[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            // a key that the row does not see adds nothing,
+                            // whatever its parameters are
+                            y[e] = seen[t][e] ? P[t][e] * sV[x][t] : 0.f;
+                            pm[nt][x][e] += seen[t][e] ? P[t][e] * mV[x][t] : 0.f;
+                        }
+                        pf[nt][x][t] = transpose8x8(pack_f16(y[0], y[1]));
+                    }
+            }
+
+            // O^T += V^T P^T: lane (g, c) holds its halves of tokens 2 c, 2 c + 1,
+            // 2 c + 8, 2 c + 9; a half-word pair of two tokens is one A register
+            const uint8_t *vc = cell + kv4::v_off(D);
+            uint32_t v[4][D / 64];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int t = 2 * c + (x & 1) + 8 * (x >> 1);
+                const uint8_t *src = vc + kv4::v_swizzle(t * (D / 2) + g * (D / 16));
+                if constexpr (D == 128) {
+                    const uint2 y = *reinterpret_cast<const uint2 *>(src);
+                    v[x][0] = y.x;
+                    v[x][1] = y.y;
+                } else {
+                    v[x][0] = *reinterpret_cast<const uint32_t *>(src);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+                constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
+                const uint32_t sel = (q & 1) ? 0x7632 : 0x5410;
+                const uint32_t x = __byte_perm(v[0][q / 2], v[1][q / 2], sel);
+                const uint32_t y = __byte_perm(v[2][q / 2], v[3][q / 2], sel);
+                const uint32_t x8 = x >> 8, y8 = y >> 8;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma(O[nt][2 * q], x & kLo, x & kHi, y & kLo, y & kHi, pf[nt][32 * q / G][0],
+                        pf[nt][32 * q / G][1]);
+                    mma(O[nt][2 * q + 1], x8 & kLo, x8 & kHi, y8 & kLo, y8 & kHi,
+                        pf[nt][32 * q / G][0], pf[nt][32 * q / G][1]);
+                }
+            }
+        }
+
+        // ---- the warps' parts joined, and written ----------------------------
+        const bool whole = blk0 == 0 && stop == item0 + nb;
+        const int slot = 2 * int(blockIdx.x) + (blk0 == 0 ? 1 : 0);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float s = sum[nt][e];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1)
+                    s += __shfl_xor_sync(0xffffffffu, s, o);
+#pragma unroll
+                for (int x = 0; x < NG; ++x)
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1)
+                        pm[nt][x][e] += __shfl_xor_sync(0xffffffffu, pm[nt][x][e], o);
+                if (g == 0) {
+                    s_ref[warp * R + nt * 8 + 2 * c + e] = ref[nt][e];
+                    s_sum[warp * R + nt * 8 + 2 * c + e] = s;
+                }
+            }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = nt * 8 + 2 * c + e;
+                float m = s_ref[r];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w)
+                    m = fmaxf(m, s_ref[w * R + r]);
+                const float f = ptx::ex2(ref[nt][e] - m);
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    const float p = pm[nt][32 * q / G][e];
+                    const float4 y = make_float4(
+                        fmaf(O[nt][2 * q][e], 0x1p24f, p) * f,
+                        fmaf(O[nt][2 * q][2 + e], 0x1p20f, p) * f,
+                        fmaf(O[nt][2 * q + 1][e], 0x1p24f, p) * f,
+                        fmaf(O[nt][2 * q + 1][2 + e], 0x1p20f, p) * f);
+                    *reinterpret_cast<float4 *>(s_O + (warp * 8 + 2 * c + e) * kRow + 32 * q +
+                                                4 * g) = y;
+                }
+            }
+            __syncthreads();
+            // 8 rows x D values over the threads, four consecutive values each
+            for (int it = tid; it < 8 * (D / 4); it += kThreads) {
+                const int rr = it / (D / 4), d4 = it % (D / 4) * 4, r = nt * 8 + rr;
+                float4 y = *reinterpret_cast<const float4 *>(s_O + rr * kRow + d4);
+                float m = s_ref[r];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) {
+                    const float4 z =
+                        *reinterpret_cast<const float4 *>(s_O + (w * 8 + rr) * kRow + d4);
+                    y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+                    m = fmaxf(m, s_ref[w * R + r]);
+                }
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    s = fmaf(s_sum[w * R + r], ptx::ex2(s_ref[w * R + r] - m), s);
+                if (r >= rows)
+                    continue;
+                if (whole) {
+                    const int i = (tile * R + r) / grp, h = kvh * grp + (tile * R + r) % grp;
+                    const float inv = s > 0.f || s != s ? 1.f / s : 0.f;
+                    const uint2 o = make_uint2(ptx::pack_bf16x2(y.x * inv, y.y * inv),
+                                               ptx::pack_bf16x2(y.z * inv, y.w * inv));
+                    auto *dst = static_cast<__nv_bfloat16 *>(a.O) +
+                                (int64_t(qb.x + i) * a.H + h) * D + d4;
+                    *reinterpret_cast<uint2 *>(dst) = o;
+                    if (d4 == 0)
+                        a.lse[a.cu_seqlens_q ? int64_t(h) * a.total_q + qb.x + i
+                                             : (int64_t(b) * a.H + h) * a.Nq + i] =
+                            s > 0.f || s != s ? (m + log2f(s)) * kLn2 : -INFINITY;
+                } else {
+                    *reinterpret_cast<float4 *>(parts.O + (int64_t(slot) * R + r) * D + d4) = y;
+                    if (d4 == 0)
+                        parts.ml[slot * R + r] = make_float2(m, s);
+                }
+            }
+            __syncthreads();
+        }
+        if (blk0 == 0 && !whole) {
+            // CTAs that hold a part: up to the one whose range has the last block
+            const uint64_t x = uint64_t(item0) + nb;            // ceil(x n / T) - 1
+            const int last_cta = int((x * n_ctas + T - 1) / T) - 1;
+            desc = Desc{last_cta - int(blockIdx.x) + 1, b, kvh, tile};
+        }
+        cur = stop;
+    }
+    if (tid == 0)
+        parts.desc[blockIdx.x] = desc;
+}
+
+// Joins the parts of the items that span CTAs: block (x, y) takes row y of the
+// item that begins in CTA x's range.  Parts are added in the order of the CTAs.
+template <int D, int R>
+__global__ void __launch_bounds__(D) attn_kv4_join_kernel(const Kv4AttnArgs a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Parts parts = parts_of<R>(a.workspace);
+    const Desc desc = parts.desc[blockIdx.x];
+    if (desc.parts == 0)
+        return;
+    const int2 qb = queries_of(a, desc.b);
+    const int grp = a.H / a.Hkv, r = blockIdx.y, at = desc.tile * R + r;
+    if (at >= qb.y * grp)
+        return;
+    const int x = threadIdx.x;
+    float m = kNoRef;
+    for (int p = 0; p < desc.parts; ++p) {
+        const int slot = 2 * (blockIdx.x + p) + (p == 0);
+        m = fmaxf(m, parts.ml[slot * R + r].x);
+    }
+    float s = 0.f, y = 0.f;
+    for (int p = 0; p < desc.parts; ++p) {
+        const int slot = 2 * (blockIdx.x + p) + (p == 0);
+        const float2 ml = parts.ml[slot * R + r];
+        const float f = ptx::ex2(ml.x - m);
+        s = fmaf(ml.y, f, s);
+        y = fmaf(parts.O[(int64_t(slot) * R + r) * D + x], f, y);
+    }
+    const int i = at / grp, h = desc.kvh * grp + at % grp;
+    const bool any = s > 0.f || s != s;
+    static_cast<__nv_bfloat16 *>(a.O)[(int64_t(qb.x + i) * a.H + h) * D + x] =
+        __float2bfloat16_rn(any ? y / s : 0.f);
+    if (x == 0)
+        a.lse[a.cu_seqlens_q ? int64_t(h) * a.total_q + qb.x + i
+                             : (int64_t(desc.b) * a.H + h) * a.Nq + i] =
+            any ? (m + log2f(s)) * kLn2 : -INFINITY;
+}
+
+template <int D, int G, int NT>
+int launch(const Kv4AttnArgs &a, cudaStream_t stream)
+{
+    constexpr int R = 8 * NT;
+    constexpr int smem = (kKv4MaxSeqs + 4) * 4 + 2 * kWarps * R * 4 + kWarps * 8 * (D + 4) * 4;
+    static PerDeviceOnce once;
+    if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(attn_kv4_kernel<D, G, NT>), smem))
+        return FA_ERR_CUDA;
+    // one CTA of the widest tile fits an SM (registers), two of the others
+    const int ctas = NT == 4 ? kKv4MaxCtas / 2 : kKv4MaxCtas;
+    attn_kv4_kernel<D, G, NT><<<ctas, kThreads, smem, stream>>>(a);
+    if (cudaGetLastError() != cudaSuccess)
+        return FA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, R);
+    cfg.blockDim = dim3(D);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_kv4_join_kernel<D, R>, a);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D, int G>
+int launch_rows(const Kv4AttnArgs &a, cudaStream_t stream)
+{
+    switch (kv4_attention_rows(a.Nq, a.H, a.Hkv)) {
+    case 8: return launch<D, G, 1>(a, stream);
+    case 16: return launch<D, G, 2>(a, stream);
+    default: return launch<D, G, 4>(a, stream);
+    }
+}
+
+}  // namespace
+
+int launch_attention_kv4(const Kv4AttnArgs &a, cudaStream_t stream)
+{
+    if (a.d == 64)
+        return a.group == 32 ? launch_rows<64, 32>(a, stream) : launch_rows<64, 64>(a, stream);
+    return a.group == 32   ? launch_rows<128, 32>(a, stream)
+           : a.group == 64 ? launch_rows<128, 64>(a, stream)
+                           : launch_rows<128, 128>(a, stream);
+}
+
+}  // namespace fa

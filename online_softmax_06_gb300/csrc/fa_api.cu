@@ -859,6 +859,80 @@ int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, const void
                         max_pages, seqlens, cu_seqlens, B, N, total, Hkv, d, group, false);
 }
 
+int64_t fa_attention_kv4_workspace_bytes(int Nq, int H, int Hkv, int d)
+{
+    if (Nq < 0 || H < 0 || Hkv < 0 || (H > 0 && (Hkv == 0 || H % Hkv != 0)))
+        return FA_ERR_BAD_SIZE;
+    if (d != 64 && d != 128)
+        return FA_ERR_UNSUPPORTED;
+    return H == 0 ? 0 : fa::kv4_attention_workspace_bytes(Nq, H, Hkv, d);
+}
+
+int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num_pages,
+                     int page_size, const int32_t *page_table, int max_pages,
+                     const int32_t *seqlens, const int32_t *cu_seqlens_q, void *O, float *lse,
+                     int B, int Nq, int64_t total_q, int Nk, int H, int Hkv, int d, int group,
+                     float scale, int causal, void *workspace, int64_t workspace_bytes)
+{
+    if (B < 0 || Nq < 0 || total_q < 0 || Nk < 0 || H < 0 || workspace_bytes < 0)
+        return FA_ERR_BAD_SIZE;
+    const int rc = fa::check_kv4_format(num_pages, page_size, max_pages, Hkv, d, group);
+    if (rc != FA_OK)
+        return rc;
+    if ((H > 0 && (Hkv == 0 || H % Hkv != 0)) || Nk > int64_t(max_pages) * page_size ||
+        (cu_seqlens_q == nullptr && total_q != int64_t(B) * Nq))
+        return FA_ERR_BAD_SIZE;
+    if (B == 0 || Nq == 0 || total_q == 0 || H == 0)
+        return FA_OK;
+    // with Nk = 0 nothing of the cache is read
+    if (!Q || !seqlens || !O || !lse || !workspace || (Nk > 0 && (!cache || !page_table)))
+        return FA_ERR_NULL_POINTER;
+    if (q_stride < int64_t(H) * d ||
+        workspace_bytes < fa::kv4_attention_workspace_bytes(Nq, H, Hkv, d))
+        return FA_ERR_BAD_SIZE;
+    if (!fa::aligned(Q, 16) || !fa::aligned(O, 16) || !fa::aligned(cache, 16) ||
+        !fa::aligned(lse, 4) || !fa::aligned(page_table, 4) || !fa::aligned(seqlens, 4) ||
+        !fa::aligned(cu_seqlens_q, 4) || !fa::aligned(workspace, 256) || q_stride % 8 != 0)
+        return FA_ERR_MISALIGNED;
+    // the blocks of 128 keys of all (sequence, kv head, row tile) items are
+    // counted in 32 bits
+    const int rows = fa::kv4_attention_rows(Nq, H, Hkv);
+    const int64_t tiles = (int64_t(Nq) * (H / Hkv) + rows - 1) / rows;
+    const int64_t blocks = Nk / 128 + 1;
+    if (B > fa::kKv4MaxSeqs || total_q > (int64_t(1) << 31) - 512 || q_stride > (int64_t(1) << 31) ||
+        H > 65535 || int64_t(Nq) * (H / Hkv) > (int64_t(1) << 31) - 512 ||
+        double(tiles) * double(blocks) * B * Hkv > double((int64_t(1) << 31) - 512))
+        return FA_ERR_TOO_LARGE;
+    fa::DeviceInfo *dev = fa::current_device();
+    if (dev == nullptr)
+        return FA_ERR_NO_DEVICE;
+    fa::Kv4AttnArgs a;
+    a.Q = Q;
+    a.q_stride = q_stride;
+    a.cache = cache;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.page_table = page_table;
+    a.max_pages = max_pages;
+    a.seqlens = seqlens;
+    a.cu_seqlens_q = cu_seqlens_q;
+    a.O = O;
+    a.lse = lse;
+    a.B = B;
+    a.Nq = Nq;
+    a.Nk = Nk;
+    a.total_q = total_q;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.group = group;
+    a.scale = scale;
+    a.causal = causal ? 1 : 0;
+    a.workspace = workspace;
+    a.err_word = dev->err_word;
+    return fa::launch_attention_kv4(a, fa::t_stream);
+}
+
 int fa_attention_fwd_f32(const float *Q, const float *K, const float *V, float *O, float *lse,
                          int B, int H, int N, int d, float scale, int causal,
                          const int32_t *cu_seqlens)

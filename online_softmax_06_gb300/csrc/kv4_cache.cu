@@ -4,7 +4,7 @@
 // Writing: per group of `group` values m = min, s = bf16((max/2 - min/2) *
 // f32(2/15)), code = rint((x/2 - m/2) * (1 / (s/2))).  m is one of the bf16
 // inputs, so storing it in bf16 loses nothing; s loses half a step of bf16
-// (2^-9), 0.03 of a code at the far end of the range.  Halving first keeps
+// (2^-8), 0.06 of a code at the far end of the range.  Halving first keeps
 // max - min finite for every pair of finite inputs.  Reading: m + s * code,
 // rounded once to bf16.
 //

@@ -176,4 +176,40 @@ struct Kv4CacheArgs {
 int launch_kv4_append(const Kv4CacheArgs &a, cudaStream_t stream);
 int launch_kv4_read(const Kv4CacheArgs &a, cudaStream_t stream);
 
+// Attention over the 4-bit paged cache.
+struct Kv4AttnArgs {
+    const void *Q;
+    int64_t q_stride;          // elements between query rows
+    const void *cache;
+    int num_pages, page_size;
+    const int32_t *page_table;
+    int max_pages;
+    const int32_t *seqlens;
+    const int32_t *cu_seqlens_q;  // or nullptr: Nq queries each
+    void *O;
+    float *lse;
+    int B, Nq, Nk;             // Nq, Nk: the most queries and keys of a sequence
+    int64_t total_q;
+    int H, Hkv, d, group;
+    float scale;
+    int causal;
+    void *workspace;
+    int *err_word;
+};
+constexpr int kKv4MaxSeqs = 1024;  // each CTA lays the sequences' work out in shared memory
+constexpr int kKv4MaxCtas = 304;   // two on each of 152 SMs
+// Query rows (queries x heads of a kv head) that a CTA takes at once.
+inline int kv4_attention_rows(int Nq, int H, int Hkv)
+{
+    const int64_t rows = int64_t(Nq) * (H / Hkv);
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
+// Descriptors (16 bytes a CTA), then for two parts a CTA the (reference, sum)
+// and the fp32 O of each row.
+inline int64_t kv4_attention_workspace_bytes(int Nq, int H, int Hkv, int d)
+{
+    return kKv4MaxCtas * 16 + int64_t(2) * kKv4MaxCtas * kv4_attention_rows(Nq, H, Hkv) * (8 + 4 * d);
+}
+int launch_attention_kv4(const Kv4AttnArgs &a, cudaStream_t stream);
+
 }  // namespace fa

@@ -1,0 +1,444 @@
+"""Attention over the 4-bit paged cache against the float64 oracle.
+
+Tolerances, from the arithmetic (half a step is finfo.eps / 2 of the value: u16 =
+2^-11 for fp16 with its 10 fraction bits, ub = 2^-8 for bf16 with its 7):
+  * a score is a sum of d products of exact factors; the tensor core rounds it
+    once per 16 of them and the groups' sums add a few fp32 roundings more,
+    12 steps of 2^-23 at most of the sum of magnitudes:
+        eS = scale * max_j sum_k |q_k| (15 s_jk + |m_jk|) * 2^-19;
+  * |lse - ref| <= 2 eS + 2^-20 (exp2's error) + 2^-22 |lse|;
+  * P s is rounded to fp16 and multiplies codes up to 15; below 2^-14 of a
+    row's largest P s the step is fixed, which L <= 2^13 keys can add up to the
+    same again; errors of S act on P twice (weight and sum); O is rounded:
+        |O - ref| <= 2 u16 * 15 max_j s_j + 4 eS max |v| + ub |ref|.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import device_error_clear, require_gpu
+from kv4_common import Pool, bf16_rows, fa, gpu_bf16, gpu_i32, kv4
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def dev():
+    d = require_gpu()
+    fa.fa_get_device_error()
+    return d
+
+
+def params(pool, b):
+    """(largest 15 s + |m| of K, largest s of V, largest |value| of V) over the sequence."""
+    K, V = pool.rows(b)
+    g = pool.group
+    span = lambda x: (x.reshape(*x.shape[:2], -1, g).max(-1) -  # noqa: E731
+                      x.reshape(*x.shape[:2], -1, g).min(-1))
+    if not len(K):
+        return np.zeros((0, pool.Hkv, pool.d)), 0.0, 0.0
+    # a group's largest code is 15 (or its scale 0): 15 s is the span
+    k_abs = np.repeat(span(K), g, -1) + np.abs(K)
+    return (k_abs, float(np.nanmax(span(V), initial=0)) / 15,
+            float(np.nanmax(np.abs(V), initial=0)))
+
+
+def check(pool, q_rows, O, lse, scale, causal, rows=None):
+    """O [total, H, d], lse [H, total] against the oracle, sequence by sequence."""
+    at = 0
+    for b, q in enumerate(q_rows):
+        n, H, d = q.shape
+        K, V = pool.rows(b)
+        Or, lr = kv4.attention(q, K, V, scale, causal)
+        o, l = O[at:at + n].double().cpu().numpy(), lse[:, at:at + n].double().cpu().numpy()
+        at += n
+        k_abs, s_v, v_max = params(pool, b)
+        eS = 0.0
+        if len(K) and n:
+            for h in range(H):
+                eS = max(eS, scale * float(np.nanmax(np.abs(q[:, h]) @ k_abs[:, h // (H // pool.Hkv)].T))
+                         * 2.0 ** -19)
+        assert np.array_equal(np.isneginf(l), np.isneginf(lr)), b
+        assert np.array_equal(np.isnan(l), np.isnan(lr)), b
+        fin = np.isfinite(lr)
+        err_l = np.abs(l[fin] - lr[fin])
+        assert (err_l <= 2 * eS + 2.0 ** -20 + 2.0 ** -22 * np.abs(lr[fin])).all(), (b, err_l.max(), eS)
+        assert np.array_equal(np.isnan(o), np.isnan(Or)), b
+        ok = ~np.isnan(Or)
+        err = np.abs(o[ok] - Or[ok])
+        tol = 2.0 ** -10 * 15 * s_v + 4 * eS * v_max + 2.0 ** -8 * np.abs(Or[ok])
+        assert (err <= tol).all(), (b, (err - tol).max(), err.max())
+
+
+def make(lens, Nq, H, Hkv, d, group, page, seed, k_off=1.0, q_std=1.5, v_std=1.0, **kw):
+    """(pool, q rows of each sequence); Nq: one count, or one for each sequence."""
+    rng = np.random.default_rng(seed)
+    nq = [Nq] * len(lens) if np.isscalar(Nq) else Nq
+    pool = Pool(lens, Hkv, d, group, page, seed=seed + 1, **kw)
+    off = rng.standard_normal((Hkv, d)) * k_off
+    k = [bf16_rows(rng, n, Hkv, d, offset=off) for n in lens]
+    v = [bf16_rows(rng, n, Hkv, d, std=v_std) for n in lens]
+    pool.fill(k, v)
+    return pool, [bf16_rows(rng, n, H, d, std=q_std) for n in nq]
+
+
+def run(pool, q_rows, causal, packed, scale=None, pad=0, lens=None, **kw):
+    """(O [total, H, d], lse [H, total]) through the helper, dense or packed."""
+    cache = torch.from_numpy(pool.bytes).cuda()
+    table, sl = gpu_i32(pool.table), gpu_i32(pool.lengths if lens is None else lens)
+    kw = dict(group=pool.group, causal=causal, scale=scale, **kw)
+    if packed:
+        n = [len(q) for q in q_rows]
+        x = np.concatenate(q_rows + [np.ones((pad, *q_rows[0].shape[1:]))])
+        o, l = fa.attention_kv4(gpu_bf16(x), cache, table, sl,
+                                cu_seqlens=gpu_i32(np.concatenate([[0], np.cumsum(n)])),
+                                max_q=max(n), **kw)
+        return o, l
+    o, l = fa.attention_kv4(gpu_bf16(np.stack(q_rows)), cache, table, sl, **kw)
+    B, Nq, H, d = o.shape
+    return o.reshape(-1, H, d), l.transpose(0, 1).reshape(H, -1)
+
+
+CASES = [
+    # lens, Nq, H, Hkv, d, group, page, causal, packed
+    ([1], 1, 1, 1, 128, 128, 16, True, False),
+    ([15, 16, 17, 0, 130], 1, 8, 2, 128, 64, 16, True, False),
+    ([127, 128, 129, 1000], 1, 4, 4, 128, 32, 48, True, False),
+    ([300, 77], 1, 16, 1, 64, 64, 32, False, False),
+    ([257, 31, 2], 1, 24, 2, 64, 32, 16, True, False),           # 12 heads a kv head: two tiles of 8
+    ([4000], 1, 8, 1, 128, 64, 64, True, False),                 # split over many CTAs
+    ([2100, 5, 900], 4, 8, 2, 128, 128, 128, True, False),       # 16 rows
+    ([150, 3, 0, 64], 5, 14, 2, 128, 64, 16, True, False),       # 35 rows: two tiles; rows without a key
+    ([150, 3, 0, 64], 5, 14, 2, 64, 64, 16, False, False),
+    ([600, 70, 129], [100, 1, 129], 8, 2, 128, 32, 32, True, True),
+    ([600, 70, 0], [33, 0, 2], 2, 2, 64, 32, 64, True, True),
+    ([40, 300], [64, 7], 3, 1, 128, 128, 256, False, True),      # more queries than keys
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=[str(i) for i in range(len(CASES))])
+def test_against_the_oracle(case):
+    lens, Nq, H, Hkv, d, group, page, causal, packed = case
+    pool, q = make(lens, Nq, H, Hkv, d, group, page, seed=100)
+    scale = 1 / math.sqrt(d)
+    O, lse = run(pool, q, causal, packed)
+    check(pool, q, O, lse, scale, causal)
+    device_error_clear()
+
+
+@pytest.mark.parametrize("B", [300, 1024])
+def test_many_sequences(B):
+    rng = np.random.default_rng(110)
+    lens = [int(x) for x in rng.integers(0, 40, B)]
+    pool, q = make(lens, 1, 2, 1, 64, 64, 16, seed=111)
+    O, lse = run(pool, q, True, False)
+    check(pool, q, O, lse, 1 / 8, True)
+    device_error_clear()
+
+
+def test_scores_that_grow_with_the_position():
+    """Every key outscores all earlier ones by far: the reference moves on every tile."""
+    d, L = 128, 700
+    rng = np.random.default_rng(120)
+    pool = Pool([L], 1, d, 32, 64, seed=121)
+    k = bf16_rows(rng, L, 1, d, std=0.05) + np.linspace(0, 8, L)[:, None, None]
+    pool.fill([kv4.bf16(k)], [bf16_rows(rng, L, 1, d)])
+    q = [np.abs(bf16_rows(rng, 1, 8, d, std=1.0))]
+    for sign in (1, -1):
+        O, lse = run(pool, [sign * q[0]], True, False, scale=0.5)
+        check(pool, [sign * q[0]], O, lse, 0.5, True)
+
+
+def test_values_of_far_apart_scales():
+    """P s goes into fp16 relative to the row's largest P s, not to its largest P."""
+    d, L = 128, 400
+    rng = np.random.default_rng(130)
+    for lo, hi in ((1e-6, 1.0), (1e-30, 1e-30), (1e30, 1e30), (1.0, 1e-5)):
+        pool = Pool([L], 1, d, 64, 16, seed=131)
+        v = bf16_rows(rng, L, 1, d)
+        v[:200] *= lo
+        v[200:] *= hi
+        k = bf16_rows(rng, L, 1, d, std=0.3)
+        k[200:] -= 2.0                       # the second half scores far below the first
+        pool.fill([kv4.bf16(k)], [kv4.bf16(v)])
+        q = [np.abs(bf16_rows(rng, 1, 4, d))]
+        O, lse = run(pool, q, True, False, scale=0.15)
+        K, V = pool.rows(0)
+        Or, lr = kv4.attention(q[0], K, V, 0.15, True)
+        o = O.double().cpu().numpy()
+        # the bound of the module's head, but with each key's own weight: the sum
+        # over the keys of P 15 s, and a fixed step of 2^-24 of the largest P s
+        s = 0.15 * q[0][0] @ K[:, 0].T
+        p = np.exp(s - s.max(1, keepdims=True))
+        p /= p.sum(1, keepdims=True)
+        sv = (V[:, 0].reshape(L, 2, 64).max(-1) - V[:, 0].reshape(L, 2, 64).min(-1)).max(-1) / 15
+        eS = 0.15 * (np.abs(q[0][0]) @ (np.abs(K[:, 0]) + 15).T).max() * 2.0 ** -19
+        tol = (p * sv).sum(1) * (15 * 2.0 ** -11 + 4 * eS) + L * 15 * 2.0 ** -24 * (p * sv).max(1)
+        assert (np.abs(o[0] - Or[0]) <= tol[:, None] + 2.0 ** -8 * np.abs(Or[0])).all(), (lo, hi)
+    device_error_clear()
+
+
+def test_constant_values_and_keys():
+    """Groups of one value have scale 0: the minimum alone carries them."""
+    d, L = 64, 90
+    pool = Pool([L], 2, d, 32, 16, seed=140)
+    v = np.zeros((L, 2, d))
+    v[:, 0, :32], v[:, 0, 32:], v[:, 1] = 3.0, -0.5, 1e4
+    k = np.full((L, 2, d), 0.25)
+    pool.fill([k], [v])
+    rng = np.random.default_rng(141)
+    q = [bf16_rows(rng, 1, 4, d)]
+    O, lse = run(pool, q, True, False)
+    want = np.repeat(v[0][None], 1, 0)
+    o = O.double().cpu().numpy()
+    # equal scores: P is 1 / L up to the sums' roundings, L * 2^-24 relative
+    assert (np.abs(o[0, :2] - want[0, 0]) <= (2.0 ** -8 + L * 2.0 ** -23) * np.abs(want[0, 0])).all()
+    assert (np.abs(o[0, 2:] - want[0, 1]) <= (2.0 ** -8 + L * 2.0 ** -23) * np.abs(want[0, 1])).all()
+
+
+def test_nan_at_keys_that_a_query_does_not_see():
+    d, L, Nq = 128, 200, 4
+    pool, q = make([L], Nq, 8, 2, d, 64, 16, seed=150)
+    rng = np.random.default_rng(151)
+    bad = bf16_rows(rng, 2, 2, d)
+    bad[:, 0, 5] = np.nan
+    bad[:, 1, 70] = np.inf
+    kv4.write(pool.bytes, pool.table[0], np.array([L - 2, L - 1]), bad, bad, 16, 64)
+    O, lse = run(pool, q, True, False)
+    o = O.double().cpu().numpy()
+    assert np.isfinite(o[:2]).all() and np.isfinite(lse[:, :2].cpu().numpy()).all()
+    clean, _ = make([L], Nq, 8, 2, d, 64, 16, seed=150)
+    # queries 0 and 1 see keys up to L - 3: as if the last two were not there
+    O1, l1 = run(clean, q, True, False)
+    assert torch.equal(O[:2], O1[:2]) and torch.equal(lse[:, :2], l1[:, :2])
+    assert np.isnan(o[2:]).all() and torch.isnan(lse[:, 2:]).all()
+
+
+def test_nan_values_stay_in_their_group():
+    """A NaN in V reaches its own group of the head dimension alone; lse not at all."""
+    d, L = 128, 60
+    pool, q = make([L], 1, 4, 1, d, 32, 16, seed=155)
+    rng = np.random.default_rng(156)
+    k, v = bf16_rows(rng, 1, 1, d), bf16_rows(rng, 1, 1, d)
+    v[0, 0, 40] = np.nan
+    kv4.write(pool.bytes, pool.table[0], np.array([30]), k, v, 16, 32)
+    O, lse = run(pool, q, True, False)
+    o = O.cpu().float().numpy()
+    assert np.isnan(o[..., 32:64]).all()
+    assert np.isfinite(o[..., :32]).all() and np.isfinite(o[..., 64:]).all()
+    assert np.isfinite(lse.cpu().numpy()).all()
+
+
+def test_zero_and_huge_queries():
+    d = 64
+    pool, q = make([77], 1, 3, 1, d, 64, 16, seed=160)
+    q[0][0, 0] = 0.0                                # uniform weights
+    q[0][0, 1] *= 2.0 ** 60                         # one key takes all
+    q[0][0, 2] *= 2.0 ** -120
+    O, lse = run(pool, q, True, False)
+    K, V = pool.rows(0)
+    Or, lr = kv4.attention(q[0], K, V, 1 / 8, True)
+    o, l = O.double().cpu().numpy(), lse.double().cpu().numpy()
+    tol = 2.0 ** -8 * np.abs(Or) + 2.0 ** -7        # s < 0.5: 2 u16 15 s, the head's bound
+    assert (np.abs(o - Or) <= tol).all()
+    assert np.abs(l[[0, 2]] - lr[[0, 2]]).max() < 2.0 ** -17
+    assert abs(l[1, 0] / lr[1, 0] - 1) < 2.0 ** -19
+
+
+def test_fused_query_rows_and_given_buffers():
+    pool, q = make([100, 40], 3, 4, 2, 128, 64, 32, seed=170)
+    O, lse = run(pool, q, True, False)
+    fused = torch.zeros(2, 3, 8, 128, dtype=torch.bfloat16, device="cuda")
+    fused[:, :, :4] = gpu_bf16(np.stack(q))
+    fused[:, :, 4:] = float("nan")
+    cache, table, sl = torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table), gpu_i32([100, 40])
+    out = torch.empty(2, 3, 4, 128, dtype=torch.bfloat16, device="cuda")
+    l = torch.empty(2, 4, 3, device="cuda")
+    ws = torch.full((fa.fa_attention_kv4_workspace_bytes(3, 4, 2, 128),), 0xff, dtype=torch.uint8,
+                    device="cuda")
+    o2, l2 = fa.attention_kv4(fused[:, :, :4], cache, table, sl, out=out, lse=l, workspace=ws,
+                              max_seqlen=100)
+    assert o2 is out and l2 is l
+    assert torch.equal(out.reshape(-1, 4, 128), O)
+    assert torch.equal(l.transpose(0, 1).reshape(4, -1), lse)
+
+
+def test_rows_behind_the_last_sequence_stay():
+    pool, q = make([50, 20], [3, 2], 4, 2, 64, 64, 16, seed=180)
+    x = np.concatenate(q + [np.ones((4, 4, 64))])
+    out = torch.full((9, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    l = torch.full((4, 9), 9.0, device="cuda")
+    fa.attention_kv4(gpu_bf16(x), torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table),
+                     gpu_i32([50, 20]), cu_seqlens=gpu_i32([0, 3, 5]), max_q=3, out=out, lse=l)
+    check(pool, q, out[:5], l[:, :5], 1 / 8, True)
+    assert (out[5:] == 9).all() and (l[:, 5:] == 9).all()
+
+
+def test_bad_lengths_and_pages():
+    pool, q = make([50, 60, 70], 1, 4, 2, 64, 64, 16, seed=190)
+    # lengths above the bound, and below 0: those sequences are left out
+    out = torch.full((3, 1, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    cache, table = torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table)
+    for bad in (61, -1):
+        out.fill_(9.0)
+        o, l = fa.attention_kv4(gpu_bf16(np.stack(q)), cache, table, gpu_i32([50, 60, bad]), out=out,
+                                max_seqlen=60)
+        assert fa.fa_get_device_error() == fa.FA_DEVERR_BAD_SEQLENS
+        sub = Pool.__new__(Pool)
+        sub.__dict__.update(pool.__dict__, lengths=[50, 60])
+        check(sub, q[:2], o.reshape(3, 4, 64)[:2], l.transpose(0, 1).reshape(4, -1)[:, :2], 1 / 8, True)
+        assert (o[2] == 9).all()
+    # a page outside the cache: its tokens are left out, the others stay right
+    t2 = pool.table.copy()
+    t2[1, 1], t2[2, 0] = pool.num_pages, -5
+    o, l = fa.attention_kv4(gpu_bf16(np.stack(q)), cache, gpu_i32(t2), gpu_i32([50, 60, 70]))
+    assert fa.fa_get_device_error() == fa.FA_DEVERR_BAD_PAGE
+    assert torch.isfinite(o).all()
+    sub.__dict__.update(pool.__dict__, lengths=[50])
+    check(sub, q[:1], o.reshape(3, 4, 64)[:1], l.transpose(0, 1).reshape(4, -1)[:, :1], 1 / 8, True)
+    # packed: more queries than max_q, a run that leaves the rows
+    x = gpu_bf16(np.concatenate(q))
+    for cu in ([0, 2, 3, 3], [0, 1, 2, 9]):
+        fa.attention_kv4(x, cache, table, gpu_i32([50, 60, 70]), cu_seqlens=gpu_i32(cu), max_q=1)
+        assert fa.fa_get_device_error() == fa.FA_DEVERR_BAD_SEQLENS
+
+
+def test_cache_beyond_32_bits():
+    """Pages whose bytes lie beyond 4 GiB of the cache."""
+    pool, q = make([150], 1, 8, 8, 128, 64, 64, seed=200)
+    per = pool.bytes[0].size
+    pages = (1 << 32) // per + 20
+    cache = torch.empty((pages, *pool.bytes.shape[1:]), dtype=torch.uint8, device="cuda")
+    shift = pages - pool.num_pages
+    cache[shift:] = torch.from_numpy(pool.bytes).cuda()
+    table = np.where(pool.table >= 0, pool.table + shift, -1)
+    sl = gpu_i32([150])
+    o, l = fa.attention_kv4(gpu_bf16(np.stack(q)), cache, gpu_i32(table), sl)
+    check(pool, q, o[0], l[0], 1 / math.sqrt(128), True)
+    k, v = fa.kv4_read(cache, gpu_i32(table), sl, d=128, n=150)
+    assert np.array_equal(k[0].double().cpu().numpy(), kv4.bf16(pool.rows(0)[0]))
+    low = cache[:shift].clone() if shift < 64 else None
+    assert low is None
+    fa.kv4_append(-k, -v, cache, gpu_i32(table), sl)
+    k2, _ = fa.kv4_read(cache, gpu_i32(table), sl, d=128, n=150)
+    assert torch.equal(torch.sign(k2.float().mean()), torch.sign(-k.float().mean()))
+    device_error_clear()
+
+
+def test_decode_steps_follow_the_prompt():
+    """As a program uses them together: a prompt is written, then tokens one at a
+    time, each step's queries attending to what the cache holds."""
+    rng = np.random.default_rng(210)
+    H, Hkv, d, group, page = 8, 2, 128, 64, 16
+    prompt, steps = [40, 0, 17], 9
+    B = len(prompt)
+    pool = Pool([n + steps for n in prompt], Hkv, d, group, page, seed=211)
+    cache, table = torch.from_numpy(pool.bytes.copy()).cuda(), gpu_i32(pool.table)
+    k = [bf16_rows(rng, n, Hkv, d) for n in prompt]
+    v = [bf16_rows(rng, n, Hkv, d) for n in prompt]
+    pool.fill(k, v)
+    cu = gpu_i32(np.concatenate([[0], np.cumsum(prompt)]))
+    fa.kv4_append(gpu_bf16(np.concatenate(k)), gpu_bf16(np.concatenate(v)), cache, table,
+                  gpu_i32(prompt), cu_seqlens=cu, group=group)
+    for t in range(steps):
+        lens = [n + t + 1 for n in prompt]
+        kn, vn = bf16_rows(rng, B, Hkv, d), bf16_rows(rng, B, Hkv, d)
+        q = bf16_rows(rng, B, H, d)
+        sl = gpu_i32(lens)
+        fa.kv4_append(gpu_bf16(kn[:, None]), gpu_bf16(vn[:, None]), cache, table, sl, group=group)
+        O, lse = fa.attention_kv4(gpu_bf16(q[:, None]), cache, table, sl, group=group)
+        for b in range(B):
+            kv4.write(pool.bytes, pool.table[b], np.array([lens[b] - 1]), kn[b:b + 1], vn[b:b + 1],
+                      page, group)
+        now = Pool.__new__(Pool)
+        now.__dict__.update(pool.__dict__, lengths=lens)
+        check(now, [q[b:b + 1] for b in range(B)], O[:, 0], lse[:, :, 0].T.contiguous(),
+              1 / math.sqrt(d), True)
+    device_error_clear()
+
+
+def test_agrees_with_split_kv_on_what_is_read_back():
+    """The cache read back as bf16 and attended to by the framework's own split-KV
+    forward: the values differ by their rounding to bf16 alone."""
+    lens, H, d = [500, 130], 4, 128
+    pool, q = make(lens, 6, H, H, d, 64, 32, seed=220, k_off=0.0, q_std=1.0)
+    cache, table, sl = torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table), gpu_i32(lens)
+    cu_k, cu_q = gpu_i32([0, 500, 630]), gpu_i32([0, 6, 12])
+    k, v = fa.kv4_read(cache, table, sl, total=630, d=d, cu_seqlens=cu_k)
+    x = gpu_bf16(np.concatenate(q))
+    O1, l1 = fa.attention_fwd_splitkv_varlen(x, k, v, cu_q, cu_k, 6, 500, causal=True)
+    O2, l2 = fa.attention_kv4(x, cache, table, sl, cu_seqlens=cu_q, max_q=6)
+    # K rounded to bf16 moves a score by sum |q k| 2^-8 / sqrt(d) at most and O by
+    # twice that times |v|; V, P and O rounded to bf16 by 2^-8 of |v| each
+    qk = max(float((np.abs(q[b]).transpose(1, 0, 2) @ np.abs(pool.rows(b)[0]).transpose(1, 2, 0)).max())
+             for b in range(2)) / math.sqrt(d) * 2.0 ** -8
+    vm = max(float(np.abs(pool.rows(b)[1]).max()) for b in range(2))
+    assert (l1 - l2).abs().max() <= qk + 1e-3
+    assert (O1.float() - O2.float()).abs().max() <= 2 * qk * vm + 2.0 ** -6 * vm
+
+
+def test_same_bits_every_time_and_in_a_graph_on_a_stream():
+    pool, q = make([3000, 10, 700], 1, 8, 2, 128, 64, 64, seed=230)
+    O, lse = run(pool, q, True, False)
+    for _ in range(3):
+        O1, l1 = run(pool, q, True, False)
+        assert torch.equal(O, O1) and torch.equal(lse, l1)
+    cache, table, sl = torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table), gpu_i32([3000, 10, 700])
+    x = gpu_bf16(np.stack(q))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o, l = fa.attention_kv4(x, cache, table, sl)
+    s.synchronize()
+    assert torch.equal(o.reshape(O.shape), O)
+    # two graphs, each with its own workspace, replayed on two streams at once
+    graphs = []
+    for _ in range(2):
+        xx, ss = x.clone(), sl.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            og, lg = fa.attention_kv4(xx, cache, table, ss, max_seqlen=3000)
+        graphs.append((g, xx, ss, og, lg))
+    graphs[1][1].neg_()
+    graphs[1][2].copy_(gpu_i32([2000, 0, 701 - 1]))
+    torch.cuda.synchronize()
+    t = torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(s):
+            graphs[0][0].replay()
+        with torch.cuda.stream(t):
+            graphs[1][0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(graphs[0][3].reshape(O.shape), O)
+    # the replayed call went by the new lengths and queries
+    sub = Pool.__new__(Pool)
+    sub.__dict__.update(pool.__dict__, lengths=[2000, 0, 700])
+    og, lg = graphs[1][3], graphs[1][4]
+    check(sub, [-x for x in q], og.reshape(O.shape), lg.transpose(0, 1).reshape(8, -1), 1 / math.sqrt(128),
+          True)
+    device_error_clear()
+
+
+def test_helper_refusals():
+    cache = fa.kv4_cache(4, 2, 16, 128)
+    table, sl = gpu_i32([[0, 1]]), gpu_i32([20])
+    q = torch.zeros(1, 1, 4, 128, dtype=torch.bfloat16, device="cuda")
+    ok = dict(q=q, cache=cache, page_table=table, seqlens=sl)
+    fa.attention_kv4(**ok)
+    bad = [dict(q=q.float()), dict(q=q[0]), dict(q=q[:, :, :3]), dict(q=q.cpu()),
+           dict(q=torch.zeros(2, 1, 4, 128, dtype=torch.bfloat16, device="cuda")),
+           dict(max_seqlen=33), dict(group=128), dict(group=48), dict(seqlens=sl.float()),
+           dict(cu_seqlens=gpu_i32([0, 1])), dict(out=q.float()), dict(lse=torch.zeros(1, device="cuda")),
+           dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           dict(page_table=gpu_i32([[0], [1]]))]
+    for change in bad:
+        with pytest.raises((ValueError, fa.FaError)):
+            fa.attention_kv4(**{**ok, **change})
+    B = 1025
+    with pytest.raises(fa.FaError):
+        fa.attention_kv4(torch.zeros(B, 1, 4, 128, dtype=torch.bfloat16, device="cuda"), cache,
+                         torch.zeros(B, 2, dtype=torch.int32, device="cuda"),
+                         torch.zeros(B, dtype=torch.int32, device="cuda"))
+    device_error_clear()

@@ -52,7 +52,7 @@ def test_quantise_against_a_search(group):
     val = kv4.values(code, scale, lo)
     g = x.reshape(7, 2, -1, group)
     # the least value is held exactly; every other within half a step of its
-    # value (and the top one within the scale's own rounding, 15 * 2^-9 steps)
+    # value (and the top one within the scale's own rounding, 15 * 2^-8 steps)
     assert np.array_equal(val.reshape(g.shape).min(-1), g.min(-1))
     step = scale[..., None]
     assert (np.abs(val.reshape(g.shape) - g) <= step * (0.5 + 2.0 ** -20)).all()
@@ -174,3 +174,39 @@ def test_helper_refusals_without_gpu():
         fa.kv4_append(k, k, cache, table, lens)            # no CUDA tensors
     with pytest.raises(ValueError):
         fa.kv4_append(k.float(), k.float(), cache, table, lens)
+
+
+def test_attention_refusals_without_gpu():
+    wb = fa.fa_attention_kv4_workspace_bytes
+    assert wb(-1, 8, 2, 128) == fa.FA_ERR_BAD_SIZE
+    assert wb(1, 9, 2, 128) == fa.FA_ERR_BAD_SIZE
+    assert wb(1, 8, 0, 128) == fa.FA_ERR_BAD_SIZE
+    assert wb(1, 8, 2, 96) == fa.FA_ERR_UNSUPPORTED
+    # 304 descriptors, then two parts a CTA of 8, 16 or 32 rows
+    for Nq, rows in ((1, 8), (2, 8), (3, 16), (4, 16), (5, 32), (500, 32)):
+        assert wb(Nq, 8, 2, 128) == 304 * 16 + 608 * rows * (8 + 512)
+
+    def go(q=256, qs=1024, cache=256, pages=4, ps=16, table=256, mp=2, lens=256, cu=None, o=256,
+           lse=256, B=1, Nq=1, total=1, Nk=20, H=8, Hkv=2, d=128, group=64, ws=256, wsb=1 << 30):
+        return fa.fa_attention_kv4(q, qs, cache, pages, ps, table, mp, lens, cu, o, lse, B, Nq,
+                                   total, Nk, H, Hkv, d, group, 1.0, 1, ws, wsb)
+    assert go(B=-1) == fa.FA_ERR_BAD_SIZE
+    assert go(Nk=33) == fa.FA_ERR_BAD_SIZE                 # more keys than the table holds
+    assert go(H=7) == fa.FA_ERR_BAD_SIZE
+    assert go(Hkv=0) == fa.FA_ERR_BAD_SIZE
+    assert go(total=2) == fa.FA_ERR_BAD_SIZE
+    assert go(qs=1016) == fa.FA_ERR_BAD_SIZE
+    assert go(wsb=1000) == fa.FA_ERR_BAD_SIZE
+    assert go(qs=1028) == fa.FA_ERR_MISALIGNED
+    assert go(ws=16) == fa.FA_ERR_MISALIGNED
+    assert go(o=8) == fa.FA_ERR_MISALIGNED
+    assert go(d=96) == fa.FA_ERR_UNSUPPORTED
+    assert go(group=16) == fa.FA_ERR_UNSUPPORTED
+    assert go(q=None) == fa.FA_ERR_NULL_POINTER
+    assert go(cache=None) == fa.FA_ERR_NULL_POINTER
+    assert go(ws=None) == fa.FA_ERR_NULL_POINTER
+    assert go(B=1025, total=1025) == fa.FA_ERR_TOO_LARGE
+    assert go(B=1024, total=1024 << 14, Nq=1 << 14, mp=1 << 20, Nk=1 << 24) == fa.FA_ERR_TOO_LARGE
+    assert go(B=0, total=0) == fa.FA_OK
+    assert go(Nq=0, total=0) == fa.FA_OK
+    assert go(H=0, Hkv=0) == fa.FA_OK
