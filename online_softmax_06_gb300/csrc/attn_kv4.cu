@@ -74,6 +74,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
+// Cells on their way or in use: each warp keeps a ring of its own, one bulk copy
+// a cell, no barrier between warps.  Two CTAs an SM with 4 cells of 2304 bytes a
+// warp have up to 147 KB in flight, against the 36 KB that cover HBM's latency at
+// full rate.
+constexpr int kStages = 4;
+
 // A work item is (sequence, kv head, tile of R query rows); its keys are cut
 // into blocks of kBlock tokens.  All items' blocks, sequence by sequence, form
 // one line that is cut into equal ranges, one a CTA: ragged batches and single
@@ -117,20 +123,50 @@ __device__ __forceinline__ int2 queries_of(const Kv4AttnArgs &a, int b)
 }
 
 template <int D, int G, int NT>
-__global__ void __launch_bounds__(kThreads) attn_kv4_kernel(const Kv4AttnArgs a)
+struct Shared {
+    static constexpr int R = 8 * NT;
+    static constexpr int ring = 0;                                   // [kWarps][kStages] cells
+    static constexpr int full = ring + kWarps * kStages * kv4::cell_bytes(D, G);
+    static constexpr int pre = full + kWarps * kStages * 8;
+    static constexpr int ref = pre + (kKv4MaxSeqs + 4) * 4;
+    static constexpr int sum = ref + kWarps * R * 4;
+    static constexpr int O = sum + kWarps * R * 4;
+    static constexpr int bytes = O + kWarps / 2 * 8 * (D + 4) * 4;
+};
+
+// The keys that the query rows of a tile see lie below this.
+__device__ __forceinline__ int key_end(const Kv4AttnArgs &a, int L, int nq, int last_query)
+{
+    return a.causal ? min(L, L - nq + last_query + 1) : L;
+}
+
+template <int D, int G, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(const Kv4AttnArgs a)
 {
     constexpr int R = 8 * NT;              // query rows of a tile
     constexpr int NG = D / G;              // groups of the head dimension
     constexpr int NJ = D / 32;             // words a lane holds of a K row
     constexpr int kCell = kv4::cell_bytes(D, G);
     constexpr int kRow = D + 4;            // padded fp32 row of the merge buffer
-    extern __shared__ uint8_t smem[];
-    uint32_t *s_pre = reinterpret_cast<uint32_t *>(smem);           // [B + 1] blocks before b
-    float *s_ref = reinterpret_cast<float *>(s_pre + kKv4MaxSeqs + 4);  // [kWarps][R]
-    float *s_sum = s_ref + kWarps * R;                              // [kWarps][R]
-    float *s_O = s_sum + kWarps * R;                                // [kWarps][8][kRow]
+    using Smem = Shared<D, G, NT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + Smem::full);   // [kWarps][kStages]
+    uint32_t *s_pre = reinterpret_cast<uint32_t *>(smem + Smem::pre);     // [B + 1] blocks before b
+    float *s_ref = reinterpret_cast<float *>(smem + Smem::ref);           // [kWarps][R]
+    float *s_sum = reinterpret_cast<float *>(smem + Smem::sum);           // [kWarps][R]
+    float *s_O = reinterpret_cast<float *>(smem + Smem::O);               // [kWarps / 2][8][kRow]
+    __shared__ int s_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const int grp = a.H / a.Hkv;
+    const int grp = a.H / a.Hkv, cells = a.page_size / kv4::kCellTokens;
+    uint64_t *full = s_full + warp * kStages;
+    uint8_t *ring = smem + Smem::ring + warp * kStages * kCell;
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i)
+            ptx::mbar_init(full + i, 1);
+        ptx::fence_barrier_init();
+    }
+    if (tid == 0)
+        s_abort = 0;
 
     // ---- the line of blocks ------------------------------------------------
     const int per = (a.B + kThreads - 1) / kThreads;
@@ -185,6 +221,63 @@ __global__ void __launch_bounds__(kThreads) attn_kv4_kernel(const Kv4AttnArgs a)
     const uint32_t begin = uint32_t(T * blockIdx.x / n_ctas);
     const uint32_t end = uint32_t(T * (blockIdx.x + 1) / n_ctas);
     Desc desc{0, 0, 0, 0};
+
+    // ---- copies ---------------------------------------------------------------
+    // Lane i finds where this warp's cell of every 32nd block begins, so that the
+    // search and the page table's latency are paid once for 32 cells; it then
+    // issues that cell's copy itself.  `have`: which of the batch's cells are read.
+    const uint32_t n_cells = end - begin;
+    const uint8_t *src = nullptr;
+    uint32_t have = 0, have_before = 0;
+    auto find = [&](uint32_t k0) {
+        src = nullptr;
+        const uint32_t x = begin + k0 + lane;
+        if (x < end) {
+            int lo = 0, hi = a.B;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_pre[mid] <= x)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            const int2 qb = queries_of(a, lo);
+            const int L = a.seqlens[lo], nb = blocks_of(L);
+            const int tiles = (qb.y * grp + R - 1) / R;
+            const uint32_t item = (x - s_pre[lo]) / nb;
+            const int kvh = item / tiles, tile = item % tiles;
+            const int tok = int((x - s_pre[lo]) % nb) * kBlock + warp * kv4::kCellTokens;
+            if (tok < key_end(a, L, qb.y, (min(qb.y * grp, (tile + 1) * R) - 1) / grp)) {
+                const int page = a.page_table[int64_t(lo) * a.max_pages + tok / a.page_size];
+                if (page >= 0 && page < a.num_pages)
+                    src = static_cast<const uint8_t *>(a.cache) +
+                          ((int64_t(page) * a.Hkv + kvh) * cells +
+                           tok % a.page_size / kv4::kCellTokens) * kCell;
+                else
+                    record_device_error(a.err_word, FA_DEVERR_BAD_PAGE);
+            }
+        }
+        have_before = have;
+        have = __ballot_sync(0xffffffffu, src != nullptr);
+    };
+    auto issue = [&](uint32_t k) {         // all lanes of the warp
+        if (k >= n_cells)
+            return;
+        if ((k & 31) == 0)
+            find(k);
+        if (lane == int(k & 31)) {
+            uint64_t *bar = full + k % kStages;
+            if (src != nullptr) {
+                ptx::mbar_arrive_expect_tx(bar, kCell);
+                ptx::bulk_load(ring + k % kStages * kCell, src, kCell, bar);
+            } else {
+                ptx::mbar_arrive(bar);
+            }
+        }
+    };
+    for (uint32_t k = 0; k < kStages; ++k)
+        issue(k);
+    uint32_t done = 0;                     // cells read
 
     for (uint32_t cur = begin; cur < end;) {
         // ---- the item at `cur` ---------------------------------------------
@@ -296,21 +389,20 @@ __global__ void __launch_bounds__(kThreads) attn_kv4_kernel(const Kv4AttnArgs a)
                     pm[nt][x][e] = 0.f;
             }
         }
-        const int cells = a.page_size / kv4::kCellTokens;
-        const int last = a.causal ? min(L, L - qb.y + (tile * R + rows - 1) / grp + 1) : L;
         for (int blk = int(blk0); blk < blk1; ++blk) {
-            const int tok = blk * kBlock + warp * kv4::kCellTokens;
-            if (tok >= last)
-                break;
-            const int page = a.page_table[int64_t(b) * a.max_pages + tok / a.page_size];
-            if (page < 0 || page >= a.num_pages) {
-                record_device_error(a.err_word, FA_DEVERR_BAD_PAGE);
+            const uint32_t k = item0 + blk - begin;
+            if (!ptx::mbar_wait_warp(full + k % kStages, k / kStages & 1, &s_abort, a.err_word))
+                break;                     // the error is recorded, nothing is written
+            // the batch that cell k + kStages - 1 is in may be the next one already
+            const uint32_t ahead = min(k + kStages, n_cells) - 1;
+            const uint32_t bits = ahead / 32 == k / 32 ? have : have_before;
+            done = k + 1;
+            if (!(bits >> (k & 31) & 1)) {
+                issue(k + kStages);
                 continue;
             }
-            const uint8_t *cell =
-                static_cast<const uint8_t *>(a.cache) +
-                ((int64_t(page) * a.Hkv + kvh) * cells + tok % a.page_size / kv4::kCellTokens) *
-                    kCell;
+            const int tok = blk * kBlock + warp * kv4::kCellTokens;
+            const uint8_t *cell = ring + k % kStages * kCell;
 
             // S^T = K Q^T: lane (g, c) holds tokens g, g + 8
             uint32_t k0[NJ], k1[NJ];
@@ -466,6 +558,8 @@ __global__ void __launch_bounds__(kThreads) attn_kv4_kernel(const Kv4AttnArgs a)
                         pf[nt][32 * q / G][0], pf[nt][32 * q / G][1]);
                 }
             }
+            __syncwarp();                  // every lane has read the cell
+            issue(k + kStages);
         }
 
         // ---- the warps' parts joined, and written ----------------------------
@@ -492,44 +586,57 @@ __global__ void __launch_bounds__(kThreads) attn_kv4_kernel(const Kv4AttnArgs a)
         __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+            // the upper warps' rows through shared memory into the lower warps'
+            // registers, then the lower warps' rows for all to sum
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = nt * 8 + 2 * c + e;
-                float m = s_ref[r];
+            for (int half = 0; half < 2; ++half) {
+                if (warp / (kWarps / 2) == 1 - half) {
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w)
-                    m = fmaxf(m, s_ref[w * R + r]);
-                const float f = ptx::ex2(ref[nt][e] - m);
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = nt * 8 + 2 * c + e;
+                        float m = s_ref[r];
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    const float p = pm[nt][32 * q / G][e];
-                    const float4 y = make_float4(
-                        fmaf(O[nt][2 * q][e], 0x1p24f, p) * f,
-                        fmaf(O[nt][2 * q][2 + e], 0x1p20f, p) * f,
-                        fmaf(O[nt][2 * q + 1][e], 0x1p24f, p) * f,
-                        fmaf(O[nt][2 * q + 1][2 + e], 0x1p20f, p) * f);
-                    *reinterpret_cast<float4 *>(s_O + (warp * 8 + 2 * c + e) * kRow + 32 * q +
-                                                4 * g) = y;
+                        for (int w = 1; w < kWarps; ++w)
+                            m = fmaxf(m, s_ref[w * R + r]);
+                        const float f = ptx::ex2(ref[nt][e] - m);
+                        float *row = s_O + (warp % (kWarps / 2) * 8 + 2 * c + e) * kRow + 4 * g;
+#pragma unroll
+                        for (int q = 0; q < D / 32; ++q) {
+                            const float p = pm[nt][32 * q / G][e];
+                            float4 y = make_float4(fmaf(O[nt][2 * q][e], 0x1p24f, p) * f,
+                                                   fmaf(O[nt][2 * q][2 + e], 0x1p20f, p) * f,
+                                                   fmaf(O[nt][2 * q + 1][e], 0x1p24f, p) * f,
+                                                   fmaf(O[nt][2 * q + 1][2 + e], 0x1p20f, p) * f);
+                            float4 *at = reinterpret_cast<float4 *>(row + 32 * q);
+                            if (half == 1) {
+                                const float4 z = *at;
+                                y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+                            }
+                            *at = y;
+                        }
+                    }
                 }
+                __syncthreads();
             }
-            __syncthreads();
             // 8 rows x D values over the threads, four consecutive values each
             for (int it = tid; it < 8 * (D / 4); it += kThreads) {
                 const int rr = it / (D / 4), d4 = it % (D / 4) * 4, r = nt * 8 + rr;
                 float4 y = *reinterpret_cast<const float4 *>(s_O + rr * kRow + d4);
                 float m = s_ref[r];
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) {
+                for (int w = 1; w < kWarps / 2; ++w) {
                     const float4 z =
                         *reinterpret_cast<const float4 *>(s_O + (w * 8 + rr) * kRow + d4);
                     y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
-                    m = fmaxf(m, s_ref[w * R + r]);
                 }
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w)
+                    m = fmaxf(m, s_ref[w * R + r]);
                 float s = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
                     s = fmaf(s_sum[w * R + r], ptx::ex2(s_ref[w * R + r] - m), s);
-                if (r >= rows)
+                if (r >= rows || s_abort)
                     continue;
                 if (whole) {
                     const int i = (tile * R + r) / grp, h = kvh * grp + (tile * R + r) % grp;
@@ -558,6 +665,14 @@ __global__ void __launch_bounds__(kThreads) attn_kv4_kernel(const Kv4AttnArgs a)
             desc = Desc{last_cta - int(blockIdx.x) + 1, b, kvh, tile};
         }
         cur = stop;
+    }
+    if (s_abort) {
+        // a wait ran out: copies still on their way must land before the CTA ends
+        desc.parts = 0;
+        volatile int go_on = 0;
+        for (uint32_t k = done; k < min(done + kStages, n_cells); ++k)
+            ptx::mbar_wait_limited(full + k % kStages, k / kStages & 1, &go_on, a.err_word,
+                                   kWaitTimeoutNs);
     }
     if (tid == 0)
         parts.desc[blockIdx.x] = desc;
@@ -605,7 +720,7 @@ template <int D, int G, int NT>
 int launch(const Kv4AttnArgs &a, cudaStream_t stream)
 {
     constexpr int R = 8 * NT;
-    constexpr int smem = (kKv4MaxSeqs + 4) * 4 + 2 * kWarps * R * 4 + kWarps * 8 * (D + 4) * 4;
+    constexpr int smem = Shared<D, G, NT>::bytes;
     static PerDeviceOnce once;
     if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(attn_kv4_kernel<D, G, NT>), smem))
         return FA_ERR_CUDA;
