@@ -28,6 +28,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/fa.h"
 #include "kv4.cuh"
@@ -69,6 +70,27 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
+{
+    if constexpr (N == 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if constexpr (N == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x, w[1] = x.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
@@ -229,9 +251,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
     const uint32_t n_cells = end - begin;
     const uint8_t *src = nullptr;
     uint32_t have = 0, have_before = 0;
+    bool bad_pages = false;
     auto find = [&](uint32_t k0) {
         src = nullptr;
         const uint32_t x = begin + k0 + lane;
+        bool bad = false;
         if (x < end) {
             int lo = 0, hi = a.B;
             while (hi - lo > 1) {
@@ -254,9 +278,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                           ((int64_t(page) * a.Hkv + kvh) * cells +
                            tok % a.page_size / kv4::kCellTokens) * kCell;
                 else
-                    record_device_error(a.err_word, FA_DEVERR_BAD_PAGE);
+                    bad = true;
             }
         }
+        if (bad)
+            record_device_error(a.err_word, FA_DEVERR_BAD_PAGE);
+        bad_pages |= __any_sync(0xffffffffu, bad) != 0;
         have_before = have;
         have = __ballot_sync(0xffffffffu, src != nullptr);
     };
@@ -278,6 +305,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
     for (uint32_t k = 0; k < kStages; ++k)
         issue(k);
     uint32_t done = 0;                     // cells read
+    // whether cell k was left out; the batch that cell k + kStages - 1 is in, the
+    // last one issued, may be the next one already
+    auto skipped = [&](uint32_t k) {
+        const uint32_t ahead = min(k + kStages, n_cells) - 1;
+        return !((ahead / 32 == k / 32 ? have : have_before) >> (k & 31) & 1);
+    };
+    int v_at[4];                           // this lane's halves of its four tokens
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        v_at[x] = kv4::v_swizzle((2 * c + (x & 1) + 8 * (x >> 1)) * (D / 2) + g * (D / 16));
 
     for (uint32_t cur = begin; cur < end;) {
         // ---- the item at `cur` ---------------------------------------------
@@ -389,59 +426,41 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                     pm[nt][x][e] = 0.f;
             }
         }
-        for (int blk = int(blk0); blk < blk1; ++blk) {
-            const uint32_t k = item0 + blk - begin;
-            if (!ptx::mbar_wait_warp(full + k % kStages, k / kStages & 1, &s_abort, a.err_word))
-                break;                     // the error is recorded, nothing is written
-            // the batch that cell k + kStages - 1 is in may be the next one already
-            const uint32_t ahead = min(k + kStages, n_cells) - 1;
-            const uint32_t bits = ahead / 32 == k / 32 ? have : have_before;
-            done = k + 1;
-            if (!(bits >> (k & 31) & 1)) {
-                issue(k + kStages);
-                continue;
-            }
-            const int tok = blk * kBlock + warp * kv4::kCellTokens;
-            const uint8_t *cell = ring + k % kStages * kCell;
-
+        // One cell's keys.  kMasked: some query row of the tile does not see all
+        // of them, or the sequence ends inside the cell.
+        auto cell_step = [&](const uint8_t *cell, int tok, auto masked_tag) {
+            constexpr bool kMasked = decltype(masked_tag)::value;
+            constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
             // S^T = K Q^T: lane (g, c) holds tokens g, g + 8
             uint32_t k0[NJ], k1[NJ];
-            if constexpr (NJ == 4) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(cell + g * 64 + c * 16);
-                const uint4 y = *reinterpret_cast<const uint4 *>(cell + (g + 8) * 64 + c * 16);
-                k0[0] = x.x, k0[1] = x.y, k0[2] = x.z, k0[3] = x.w;
-                k1[0] = y.x, k1[1] = y.y, k1[2] = y.z, k1[3] = y.w;
-            } else {
-                const uint2 x = *reinterpret_cast<const uint2 *>(cell + g * 32 + c * 8);
-                const uint2 y = *reinterpret_cast<const uint2 *>(cell + (g + 8) * 32 + c * 8);
-                k0[0] = x.x, k0[1] = x.y;
-                k1[0] = y.x, k1[1] = y.y;
-            }
-            // parameters of tokens g and g + 8; of a token behind the sequence's
-            // end they may be anything and count as 0
-            float sK[NG][2], mK[NG][2], sV[NG][2], mV[NG][2], w[2];
-            const auto *kp = reinterpret_cast<const uint32_t *>(cell + kv4::k_par_off(D));
-            const auto *vp = reinterpret_cast<const uint32_t *>(cell + kv4::v_par_off(D, G));
+            load_words<NJ>(k0, cell + lane * (4 * NJ));
+            load_words<NJ>(k1, cell + 8 * (D / 2) + lane * (4 * NJ));
+            // (scale, min) pairs of tokens g and g + 8
+            uint32_t pk[2][NG], pv[2][NG];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const bool in = tok + g + 8 * t < L;
-                float s_big = 0.f, m_big = 0.f;
+                load_words<NG>(pk[t], cell + kv4::k_par_off(D) + (g + 8 * t) * (4 * NG));
+                load_words<NG>(pv[t], cell + kv4::v_par_off(D, G) + (g + 8 * t) * (4 * NG));
+                // behind the sequence's end they may be anything, and count as 0
+                if (kMasked && tok + g + 8 * t >= L) {
 #pragma unroll
-                for (int x = 0; x < NG; ++x) {
-                    const uint32_t pk = in ? kp[(g + 8 * t) * NG + x] : 0;
-                    const uint32_t pv = in ? vp[(g + 8 * t) * NG + x] : 0;
-                    sK[x][t] = bf16_lo(pk);
-                    mK[x][t] = bf16_hi(pk);
-                    sV[x][t] = bf16_lo(pv);
-                    mV[x][t] = bf16_hi(pv);
-                    s_big = fmaxf(s_big, sV[x][t]);
-                    m_big = fmaxf(m_big, fabsf(mV[x][t]));
+                    for (int x = 0; x < NG; ++x)
+                        pk[t][x] = pv[t][x] = 0;
+                }
+            }
+            float w[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                float s_big = bf16_lo(pv[t][0]), m_big = fabsf(bf16_hi(pv[t][0]));
+#pragma unroll
+                for (int x = 1; x < NG; ++x) {
+                    s_big = fmaxf(s_big, bf16_lo(pv[t][x]));
+                    m_big = fmaxf(m_big, fabsf(bf16_hi(pv[t][x])));
                 }
                 // |m| counts too (a constant group has s = 0), so that P m stays
                 // finite in fp32
-                w[t] = fmaxf(fmaxf(s_big, m_big * 0x1p-12f), kLeastWeight);
+                w[t] = max3(s_big, m_big * 0x1p-12f, kLeastWeight);
             }
-            const bool masked = tok + kv4::kCellTokens > lim_least;
             uint32_t pf[NT][NG][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -451,44 +470,53 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                     acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
-                    constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
                     mma(acc[32 * j / G], k0[j] & kLo, k1[j] & kLo, k0[j] & kHi, k1[j] & kHi,
                         qf[nt][2 * j][0], qf[nt][2 * j][1]);
                     const uint32_t y0 = k0[j] >> 8, y1 = k1[j] >> 8;
                     mma(acc[32 * j / G], y0 & kLo, y1 & kLo, y0 & kHi, y1 & kHi,
                         qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
                 }
-                float S[2][2], P[2][2];        // [token g, g + 8][row 2 c, 2 c + 1]
+                // S - reference, [token g, g + 8][row 2 c, 2 c + 1]
+                float S[2][2], P[2][2];
                 bool seen[2][2];
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = 0.f, y = 0.f;
+                        float x = bf16_lo(pk[t][0]) * acc[0][2 * t + e], y = -ref[nt][e];
 #pragma unroll
-                        for (int gr = 0; gr < NG; ++gr) {
-                            x = fmaf(sK[gr][t], acc[gr][2 * t + e], x);
-                            y = fmaf(mK[gr][t], qbar[nt][gr][e], y);
-                        }
+                        for (int gr = 1; gr < NG; ++gr)
+                            x = fmaf(bf16_lo(pk[t][gr]), acc[gr][2 * t + e], x);
+#pragma unroll
+                        for (int gr = 0; gr < NG; ++gr)
+                            y = fmaf(bf16_hi(pk[t][gr]), qbar[nt][gr][e], y);
                         S[t][e] = fmaf(x, mul[nt][e], y);
-                        seen[t][e] = !masked || tok + g + 8 * t < lim[nt][e];
+                        seen[t][e] = !kMasked || tok + g + 8 * t < lim[nt][e];
                         if (!seen[t][e])
                             S[t][e] = -INFINITY;
+                        P[t][e] = ptx::ex2(S[t][e]);
                     }
-                float over = 0.f;
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        P[t][e] = ptx::ex2(S[t][e] - ref[nt][e]);
-                        over = fmaxf(over, P[t][e] * w[t]);
-                    }
+                const float over = fmaxf(max3(P[0][0] * w[0], P[0][1] * w[0], P[1][0] * w[1]),
+                                         P[1][1] * w[1]);
                 if (__any_sync(0xffffffffu, over > kLag)) {
                     // a row outgrew its reference: every row's becomes the
-                    // largest S + log2 w seen
+                    // largest S + log2 w seen (S formed anew: from kNoRef, the
+                    // difference has lost its digits)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = fmaxf(S[0][e] + __log2f(w[0]), S[1][e] + __log2f(w[1]));
+                        float S0[2];
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            float x = bf16_lo(pk[t][0]) * acc[0][2 * t + e], y = 0.f;
+#pragma unroll
+                            for (int gr = 1; gr < NG; ++gr)
+                                x = fmaf(bf16_lo(pk[t][gr]), acc[gr][2 * t + e], x);
+#pragma unroll
+                            for (int gr = 0; gr < NG; ++gr)
+                                y = fmaf(bf16_hi(pk[t][gr]), qbar[nt][gr][e], y);
+                            S0[t] = seen[t][e] ? fmaf(x, mul[nt][e], y) : -INFINITY;
+                        }
+                        float m = fmaxf(S0[0] + __log2f(w[0]), S0[1] + __log2f(w[1]));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -504,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                             O[nt][x][e] *= f;
                             O[nt][x][2 + e] *= f;
                         }
-                        P[0][e] = ptx::ex2(S[0][e] - m);
-                        P[1][e] = ptx::ex2(S[1][e] - m);
+                        P[0][e] = ptx::ex2(S0[0] - m);
+                        P[1][e] = ptx::ex2(S0[1] - m);
                     }
                 }
 #pragma unroll
@@ -520,8 +548,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                         for (int e = 0; e < 2; ++e) {
                             // a key that the row does not see adds nothing,
                             // whatever its parameters are
-                            y[e] = seen[t][e] ? P[t][e] * sV[x][t] : 0.f;
-                            pm[nt][x][e] += seen[t][e] ? P[t][e] * mV[x][t] : 0.f;
+                            y[e] = P[t][e] * bf16_lo(pv[t][x]);
+                            const float z = fmaf(P[t][e], bf16_hi(pv[t][x]), pm[nt][x][e]);
+                            if (kMasked && !seen[t][e])
+                                y[e] = 0.f;
+                            else
+                                pm[nt][x][e] = z;
                         }
                         pf[nt][x][t] = transpose8x8(pack_f16(y[0], y[1]));
                     }
@@ -529,23 +561,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
 
             // O^T += V^T P^T: lane (g, c) holds its halves of tokens 2 c, 2 c + 1,
             // 2 c + 8, 2 c + 9; a half-word pair of two tokens is one A register
-            const uint8_t *vc = cell + kv4::v_off(D);
             uint32_t v[4][D / 64];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int t = 2 * c + (x & 1) + 8 * (x >> 1);
-                const uint8_t *src = vc + kv4::v_swizzle(t * (D / 2) + g * (D / 16));
-                if constexpr (D == 128) {
-                    const uint2 y = *reinterpret_cast<const uint2 *>(src);
-                    v[x][0] = y.x;
-                    v[x][1] = y.y;
-                } else {
-                    v[x][0] = *reinterpret_cast<const uint32_t *>(src);
-                }
-            }
+            for (int x = 0; x < 4; ++x)
+                load_words<D / 64>(v[x], cell + kv4::v_off(D) + v_at[x]);
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
-                constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
                 const uint32_t sel = (q & 1) ? 0x7632 : 0x5410;
                 const uint32_t x = __byte_perm(v[0][q / 2], v[1][q / 2], sel);
                 const uint32_t y = __byte_perm(v[2][q / 2], v[3][q / 2], sel);
@@ -557,6 +578,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                     mma(O[nt][2 * q + 1], x8 & kLo, x8 & kHi, y8 & kLo, y8 & kHi,
                         pf[nt][32 * q / G][0], pf[nt][32 * q / G][1]);
                 }
+            }
+        };
+
+        const int tok_end = key_end(a, L, qb.y, (tile * R + rows - 1) / grp);
+        int tok = int(blk0) * kBlock + warp * kv4::kCellTokens;
+        for (uint32_t k = cur - begin; k < stop - begin; ++k, tok += kBlock) {
+            const uint8_t *cell = ring + k % kStages * kCell;
+            if (!ptx::mbar_wait_warp(full + k % kStages, k / kStages & 1, &s_abort, a.err_word))
+                break;                     // the error is recorded, nothing is written
+            done = k + 1;
+            if (tok < tok_end && !(bad_pages && skipped(k))) {
+                if (tok + kv4::kCellTokens <= lim_least)
+                    cell_step(cell, tok, std::false_type{});
+                else
+                    cell_step(cell, tok, std::true_type{});
             }
             __syncwarp();                  // every lane has read the cell
             issue(k + kStages);
