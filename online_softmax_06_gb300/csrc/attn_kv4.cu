@@ -50,13 +50,22 @@ constexpr float kNoRef = -1e30f;   // reference of a row that has seen no key: e
 constexpr float kLag = 16.f;
 constexpr float kLeastWeight = 0x1p-92f;
 
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
                  "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The same on a zero accumulator.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+                 "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
@@ -79,18 +88,37 @@ __device__ __forceinline__ float max3(float x, float y, float z)
     return r;
 }
 
-template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
+// N words of shared memory at address `at` + OFF.  Volatile: the ring's contents
+// change, and the queries' fragments are read again each time rather than held.
+template <int OFF, int N>
+__device__ __forceinline__ void load_shared(uint32_t (&w)[N], uint32_t at)
 {
-    if constexpr (N == 4) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(p);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-    } else if constexpr (N == 2) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(p);
-        w[0] = x.x, w[1] = x.y;
-    } else {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
-    }
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at), "n"(OFF));
+    else if constexpr (N == 2)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];"
+                     : "=r"(w[0]), "=r"(w[1])
+                     : "r"(at), "n"(OFF));
+    else
+        asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(w[0]) : "r"(at), "n"(OFF));
+}
+
+// Lane `mine` of the warp: arrives at the cell's barrier and starts its copy; with
+// no source it only arrives.
+template <int BYTES>
+__device__ __forceinline__ void copy_cell(uint32_t bar, uint32_t to, const uint8_t *src, bool mine)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 n;\n\t"
+                 "setp.ne.u32 p, %3, 0;\n\t"
+                 "setp.ne.and.u64 q, %2, 0, p;\n\t"
+                 "selp.b32 n, %4, 0, q;\n\t"
+                 "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], n;\n\t"
+                 "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2], "
+                 "%4, [%0];\n\t}"
+                 ::"r"(bar), "r"(to), "l"(src), "r"(uint32_t(mine)), "n"(BYTES)
+                 : "memory");
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
@@ -144,22 +172,131 @@ __device__ __forceinline__ int2 queries_of(const Kv4AttnArgs &a, int b)
     return make_int2(c0, n);
 }
 
+// A tile's queries in shared memory.
+template <int D, int G, int NT>
+struct alignas(16) QueryTile {
+    uint4 frag[NT][D / 32][32];    // B fragments of two k-steps, lane by lane
+    float bar[D / G][8 * NT];      // scale log2e * (sum of the row's values in the group)
+    float mul[8 * NT];             // scale log2e * 2^24 / (the row's power of two)
+    int end[8 * NT];               // the keys that the row sees lie below this
+};
+
 template <int D, int G, int NT>
 struct Shared {
     static constexpr int R = 8 * NT;
     static constexpr int ring = 0;                                   // [kWarps][kStages] cells
-    static constexpr int full = ring + kWarps * kStages * kv4::cell_bytes(D, G);
-    static constexpr int pre = full + kWarps * kStages * 8;
-    static constexpr int ref = pre + (kKv4MaxSeqs + 4) * 4;
-    static constexpr int sum = ref + kWarps * R * 4;
-    static constexpr int O = sum + kWarps * R * 4;
-    static constexpr int bytes = O + kWarps / 2 * 8 * (D + 4) * 4;
+    static constexpr int q = ring + kWarps * kStages * kv4::cell_bytes(D, G);  // [2] QueryTile
+    static constexpr int O = q + 2 * int(sizeof(QueryTile<D, G, NT>));  // [kWarps / 2][8][D + 4]
+    static constexpr int full = O + kWarps / 2 * 8 * (D + 4) * 4;    // [kWarps][kStages] barriers
+    static constexpr int pre = full + kWarps * kStages * 8;          // [B + 1] blocks before b
+    static constexpr int len = pre + (kKv4MaxSeqs + 4) * 4;          // [B] keys
+    static constexpr int ref = len + kKv4MaxSeqs * 4;                // [kWarps][R]
+    static constexpr int sum = ref + kWarps * R * 4;                 // [kWarps][R]
+    static constexpr int bytes = sum + kWarps * R * 4;
 };
 
-// The keys that the query rows of a tile see lie below this.
-__device__ __forceinline__ int key_end(const Kv4AttnArgs &a, int L, int nq, int last_query)
+// Where block x of the line is.
+struct Item {
+    int b, q0, nq, L;      // sequence, its first query row, queries, keys
+    int kvh, tile;
+    uint32_t first;        // the item's first block
+    int nb;                // its blocks
+};
+
+__device__ __forceinline__ Item item_at(const Kv4AttnArgs &a, const uint32_t *s_pre,
+                                        const int *s_len, int grp, int R, uint32_t x)
 {
-    return a.causal ? min(L, L - nq + last_query + 1) : L;
+    int lo = 0, hi = a.B;                  // s_pre[lo] <= x < s_pre[lo + 1]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_pre[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    Item it;
+    const int2 q = queries_of(a, lo);
+    it.b = lo;
+    it.q0 = q.x;
+    it.nq = q.y;
+    it.L = s_len[lo];
+    it.nb = blocks_of(it.L);
+    const uint32_t tiles = uint32_t(q.y * grp + R - 1) / R, at = x - s_pre[lo];
+    const uint32_t i = at / uint32_t(it.nb);
+    it.kvh = int(i / tiles);
+    it.tile = int(i % tiles);
+    it.first = s_pre[lo] + i * it.nb;
+    return it;
+}
+
+// The keys that query i of the item's sequence sees lie below this.
+__device__ __forceinline__ int key_end(const Kv4AttnArgs &a, const Item &it, int i)
+{
+    return a.causal ? min(it.L, it.L - it.nq + i + 1) : it.L;
+}
+
+// The 8 query rows of n-tile nt as B fragments, by one warp.
+template <int D, int G, int NT>
+__device__ __forceinline__ void load_queries(const Kv4AttnArgs &a, const Item &it, int grp, int nt,
+                                             QueryTile<D, G, NT> &to)
+{
+    constexpr int R = 8 * NT, NJ = D / 32, NG = D / G;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, r = nt * 8 + g;
+    const int at = it.tile * R + r, i = at / grp;
+    uint4 w[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+        w[j] = make_uint4(0, 0, 0, 0);
+    if (at < it.nq * grp) {
+        const auto *src = static_cast<const __nv_bfloat16 *>(a.Q) +
+                          int64_t(it.q0 + i) * a.q_stride +
+                          int64_t(it.kvh * grp + at % grp) * D + 8 * c;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            w[j] = __ldg(reinterpret_cast<const uint4 *>(src + 32 * j));
+    }
+    float big = 0.f, sum[NG];
+#pragma unroll
+    for (int x = 0; x < NG; ++x)
+        sum[x] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            big = max3(big, fabsf(bf16_lo(v[e])), fabsf(bf16_hi(v[e])));
+            sum[32 * j / G] += bf16_lo(v[e]) + bf16_hi(v[e]);
+        }
+    }
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    // a power of two that brings the row's largest value into [2^12, 2^13)
+    const int ex = big > 0.f ? max(-100, min(100, 139 - int(__float_as_uint(big) >> 23))) : 0;
+    const float up = __uint_as_float(uint32_t(127 + ex) << 23);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const float x0 = bf16_lo(w[j].x) * up, x1 = bf16_hi(w[j].x) * up,
+                    x2 = bf16_lo(w[j].y) * up, x3 = bf16_hi(w[j].y) * up,
+                    x4 = bf16_lo(w[j].z) * up, x5 = bf16_hi(w[j].z) * up,
+                    x6 = bf16_lo(w[j].w) * up, x7 = bf16_hi(w[j].w) * up;
+        // nibbles i and i + 4 of a word are a half-word apart; the upper nibble
+        // of a byte counts 16 times
+        to.frag[nt][j][lane] =
+            make_uint4(pack_f16(x0, x4), pack_f16(x1 * 0.0625f, x5 * 0.0625f), pack_f16(x2, x6),
+                       pack_f16(x3 * 0.0625f, x7 * 0.0625f));
+    }
+    const float sc = a.scale * kLog2e;
+#pragma unroll
+    for (int x = 0; x < NG; ++x) {
+        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
+        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
+        if (c == 0)
+            to.bar[x][r] = sum[x] * sc;
+    }
+    if (c == 0) {
+        to.mul[r] = sc * __uint_as_float(uint32_t(127 + 24 - ex) << 23);
+        to.end[r] = key_end(a, it, i);
+    }
 }
 
 template <int D, int G, int NT>
@@ -172,15 +309,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
     constexpr int kRow = D + 4;            // padded fp32 row of the merge buffer
     using Smem = Shared<D, G, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + Smem::full);   // [kWarps][kStages]
-    uint32_t *s_pre = reinterpret_cast<uint32_t *>(smem + Smem::pre);     // [B + 1] blocks before b
-    float *s_ref = reinterpret_cast<float *>(smem + Smem::ref);           // [kWarps][R]
-    float *s_sum = reinterpret_cast<float *>(smem + Smem::sum);           // [kWarps][R]
-    float *s_O = reinterpret_cast<float *>(smem + Smem::O);               // [kWarps / 2][8][kRow]
+    auto *s_q = reinterpret_cast<QueryTile<D, G, NT> *>(smem + Smem::q);
+    float *s_O = reinterpret_cast<float *>(smem + Smem::O);
+    uint32_t *s_pre = reinterpret_cast<uint32_t *>(smem + Smem::pre);
+    int *s_len = reinterpret_cast<int *>(smem + Smem::len);
+    float *s_ref = reinterpret_cast<float *>(smem + Smem::ref);
+    float *s_sum = reinterpret_cast<float *>(smem + Smem::sum);
     __shared__ int s_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const int grp = a.H / a.Hkv, cells = a.page_size / kv4::kCellTokens;
-    uint64_t *full = s_full + warp * kStages;
+    const int grp = a.H / a.Hkv;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Smem::full) + warp * kStages;
     uint8_t *ring = smem + Smem::ring + warp * kStages * kCell;
     if (lane == 0) {
         for (int i = 0; i < kStages; ++i)
@@ -205,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
             record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
         else
             n = uint32_t((q.y * grp + R - 1) / R) * a.Hkv * blocks_of(L);
+        s_len[b] = L;
         s_pre[b + 1] = n;
         mine += n;
     }
@@ -257,25 +396,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
         const uint32_t x = begin + k0 + lane;
         bool bad = false;
         if (x < end) {
-            int lo = 0, hi = a.B;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (s_pre[mid] <= x)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            const int2 qb = queries_of(a, lo);
-            const int L = a.seqlens[lo], nb = blocks_of(L);
-            const int tiles = (qb.y * grp + R - 1) / R;
-            const uint32_t item = (x - s_pre[lo]) / nb;
-            const int kvh = item / tiles, tile = item % tiles;
-            const int tok = int((x - s_pre[lo]) % nb) * kBlock + warp * kv4::kCellTokens;
-            if (tok < key_end(a, L, qb.y, (min(qb.y * grp, (tile + 1) * R) - 1) / grp)) {
-                const int page = a.page_table[int64_t(lo) * a.max_pages + tok / a.page_size];
+            const Item it = item_at(a, s_pre, s_len, grp, R, x);
+            const int tok = int(x - it.first) * kBlock + warp * kv4::kCellTokens;
+            if (tok < key_end(a, it, (min(it.nq * grp, (it.tile + 1) * R) - 1) / grp)) {
+                const int page = a.page_table[int64_t(it.b) * a.max_pages + tok / a.page_size];
                 if (page >= 0 && page < a.num_pages)
                     src = static_cast<const uint8_t *>(a.cache) +
-                          ((int64_t(page) * a.Hkv + kvh) * cells +
+                          ((int64_t(page) * a.Hkv + it.kvh) * (a.page_size / kv4::kCellTokens) +
                            tok % a.page_size / kv4::kCellTokens) * kCell;
                 else
                     bad = true;
@@ -287,20 +414,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
         have_before = have;
         have = __ballot_sync(0xffffffffu, src != nullptr);
     };
+    const uint32_t ring_at = ptx::smem_u32(ring), full_at = ptx::smem_u32(full);
     auto issue = [&](uint32_t k) {         // all lanes of the warp
-        if (k >= n_cells)
-            return;
-        if ((k & 31) == 0)
+        if ((k & 31) == 0 && k < n_cells)
             find(k);
-        if (lane == int(k & 31)) {
-            uint64_t *bar = full + k % kStages;
-            if (src != nullptr) {
-                ptx::mbar_arrive_expect_tx(bar, kCell);
-                ptx::bulk_load(ring + k % kStages * kCell, src, kCell, bar);
-            } else {
-                ptx::mbar_arrive(bar);
-            }
-        }
+        if (k < n_cells)
+            copy_cell<kCell>(full_at + (k % kStages) * 8, ring_at + (k % kStages) * kCell, src,
+                             lane == int(k & 31));
     };
     for (uint32_t k = 0; k < kStages; ++k)
         issue(k);
@@ -311,104 +431,37 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
         const uint32_t ahead = min(k + kStages, n_cells) - 1;
         return !((ahead / 32 == k / 32 ? have : have_before) >> (k & 31) & 1);
     };
-    int v_at[4];                           // this lane's halves of its four tokens
+
+    // this lane's places in a cell
+    const uint32_t at_K = ring_at + lane * (4 * NJ);
+    const uint32_t at_par = ring_at + kv4::k_par_off(D) + g * (4 * NG);
+    uint32_t at_V[4];                      // of tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9
 #pragma unroll
     for (int x = 0; x < 4; ++x)
-        v_at[x] = kv4::v_swizzle((2 * c + (x & 1) + 8 * (x >> 1)) * (D / 2) + g * (D / 16));
+        at_V[x] = ring_at + kv4::v_off(D) +
+                  kv4::v_swizzle((2 * c + (x & 1) + 8 * (x >> 1)) * (D / 2) + g * (D / 16));
 
+    Item it = item_at(a, s_pre, s_len, grp, R, begin);
+    if (warp < NT)
+        load_queries<D, G, NT>(a, it, grp, warp, s_q[0]);
+    __syncthreads();
+    int buf = 0;
     for (uint32_t cur = begin; cur < end;) {
-        // ---- the item at `cur` ---------------------------------------------
-        int lo = 0, hi = a.B;              // s_pre[lo] <= cur < s_pre[lo + 1]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_pre[mid] <= cur)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        const int b = lo;
-        const int2 qb = queries_of(a, b);
-        const int L = a.seqlens[b], nb = blocks_of(L);
-        const int tiles = (qb.y * grp + R - 1) / R;
-        const uint32_t item = (cur - s_pre[b]) / nb, blk0 = (cur - s_pre[b]) % nb;
-        const int kvh = item / tiles, tile = item % tiles;
-        const uint32_t item0 = cur - blk0;                      // the item's first block
-        const uint32_t stop = min(end, item0 + nb);
-        const int blk1 = int(stop - item0);
-        const int rows = min(R, qb.y * grp - tile * R);         // rows of this tile
-
-        // ---- Q: fragments, group sums, factors -----------------------------
-        uint32_t qf[NT][2 * NJ][2];
+        const uint32_t stop = min(end, it.first + it.nb);
+        const int rows = min(R, it.nq * grp - it.tile * R);         // rows of this tile
+        const QueryTile<D, G, NT> &qt = s_q[buf];
+        const uint32_t at_Q = ptx::smem_u32(&qt.frag[0][0][lane]);
         float mul[NT][2], qbar[NT][NG][2];     // of rows 2 c, 2 c + 1 of n-tile nt
-        int lim[NT][2];                        // keys that these rows see
-        int lim_least = L;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = nt * 8 + g;
-            uint4 w[NJ];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                w[j] = make_uint4(0, 0, 0, 0);
-            if (r < rows) {
-                const int i = (tile * R + r) / grp, h = kvh * grp + (tile * R + r) % grp;
-                const auto *src = static_cast<const __nv_bfloat16 *>(a.Q) +
-                                  int64_t(qb.x + i) * a.q_stride + int64_t(h) * D + 8 * c;
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    w[j] = __ldg(reinterpret_cast<const uint4 *>(src + 32 * j));
-            }
-            float big = 0.f, sum[NG];
-#pragma unroll
-            for (int x = 0; x < NG; ++x)
-                sum[x] = 0.f;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    big = fmaxf(big, fmaxf(fabsf(bf16_lo(v[e])), fabsf(bf16_hi(v[e]))));
-                    sum[32 * j / G] += bf16_lo(v[e]) + bf16_hi(v[e]);
-                }
-            }
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // a power of two that brings the row's largest value into [2^12, 2^13)
-            const int ex = big > 0.f ? max(-100, min(100, 139 - int(__float_as_uint(big) >> 23)))
-                                     : 0;
-            const float up = __uint_as_float(uint32_t(127 + ex) << 23);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const float x0 = bf16_lo(w[j].x) * up, x1 = bf16_hi(w[j].x) * up,
-                            x2 = bf16_lo(w[j].y) * up, x3 = bf16_hi(w[j].y) * up,
-                            x4 = bf16_lo(w[j].z) * up, x5 = bf16_hi(w[j].z) * up,
-                            x6 = bf16_lo(w[j].w) * up, x7 = bf16_hi(w[j].w) * up;
-                // nibbles i and i + 4 of a word are a half-word apart; the upper
-                // nibble of a byte counts 16 times
-                qf[nt][2 * j][0] = pack_f16(x0, x4);
-                qf[nt][2 * j][1] = pack_f16(x1 * 0.0625f, x5 * 0.0625f);
-                qf[nt][2 * j + 1][0] = pack_f16(x2, x6);
-                qf[nt][2 * j + 1][1] = pack_f16(x3 * 0.0625f, x7 * 0.0625f);
-            }
-            const float sc = a.scale * kLog2e;
-            const float m = sc * __uint_as_float(uint32_t(127 + 24 - ex) << 23);
-#pragma unroll
-            for (int x = 0; x < NG; ++x) {
-                sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
-                sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
-                sum[x] *= sc;
-            }
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mul[nt][e] = __shfl_sync(0xffffffffu, m, (2 * c + e) * 4);
+                const int r = nt * 8 + 2 * c + e;
+                mul[nt][e] = qt.mul[r];
 #pragma unroll
                 for (int x = 0; x < NG; ++x)
-                    qbar[nt][x][e] = __shfl_sync(0xffffffffu, sum[x], (2 * c + e) * 4);
-                const int i = (tile * R + nt * 8 + 2 * c + e) / grp;
-                lim[nt][e] = a.causal ? min(L, L - qb.y + i + 1) : L;
+                    qbar[nt][x][e] = qt.bar[x][r];
             }
-        }
-        if (a.causal)
-            lim_least = L - qb.y + tile * R / grp + 1;
 
         // ---- the keys ----------------------------------------------------------
         float O[NT][D / 16][4], ref[NT][2], sum[NT][2], pm[NT][NG][2];
@@ -428,24 +481,44 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
         }
         // One cell's keys.  kMasked: some query row of the tile does not see all
         // of them, or the sequence ends inside the cell.
-        auto cell_step = [&](const uint8_t *cell, int tok, auto masked_tag) {
+        auto cell_step = [&](uint32_t slot, int tok, auto masked_tag) {
             constexpr bool kMasked = decltype(masked_tag)::value;
             constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
             // S^T = K Q^T: lane (g, c) holds tokens g, g + 8
             uint32_t k0[NJ], k1[NJ];
-            load_words<NJ>(k0, cell + lane * (4 * NJ));
-            load_words<NJ>(k1, cell + 8 * (D / 2) + lane * (4 * NJ));
+            load_shared<0>(k0, at_K + slot);
+            load_shared<8 * (D / 2)>(k1, at_K + slot);
             // (scale, min) pairs of tokens g and g + 8
             uint32_t pk[2][NG], pv[2][NG];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                load_words<NG>(pk[t], cell + kv4::k_par_off(D) + (g + 8 * t) * (4 * NG));
-                load_words<NG>(pv[t], cell + kv4::v_par_off(D, G) + (g + 8 * t) * (4 * NG));
+            constexpr int kV = 64 * NG, kUp = 32 * NG;
+            load_shared<0>(pk[0], at_par + slot);
+            load_shared<kUp>(pk[1], at_par + slot);
+            load_shared<kV>(pv[0], at_par + slot);
+            load_shared<kV + kUp>(pv[1], at_par + slot);
+            if constexpr (kMasked) {
                 // behind the sequence's end they may be anything, and count as 0
-                if (kMasked && tok + g + 8 * t >= L) {
 #pragma unroll
-                    for (int x = 0; x < NG; ++x)
-                        pk[t][x] = pv[t][x] = 0;
+                for (int t = 0; t < 2; ++t)
+                    if (tok + g + 8 * t >= it.L)
+#pragma unroll
+                        for (int x = 0; x < NG; ++x)
+                            pk[t][x] = pv[t][x] = 0;
+            }
+            float acc[NT][NG][4];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const uint32_t y0 = k0[j] >> 8, y1 = k1[j] >> 8;
+                const uint32_t a0[4] = {k0[j] & kLo, k1[j] & kLo, k0[j] & kHi, k1[j] & kHi};
+                const uint32_t a1[4] = {y0 & kLo, y1 & kLo, y0 & kHi, y1 & kHi};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    uint32_t q[4];
+                    load_shared<0>(q, at_Q + (nt * NJ + j) * 512);
+                    if (32 * j % G == 0)
+                        mma_first(acc[nt][32 * j / G], a0, q[0], q[1]);
+                    else
+                        mma(acc[nt][32 * j / G], a0, q[0], q[1]);
+                    mma(acc[nt][32 * j / G], a1, q[2], q[3]);
                 }
             }
             float w[2];
@@ -464,59 +537,37 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
             uint32_t pf[NT][NG][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float acc[NG][4];
-#pragma unroll
-                for (int x = 0; x < NG; ++x)
-                    acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    mma(acc[32 * j / G], k0[j] & kLo, k1[j] & kLo, k0[j] & kHi, k1[j] & kHi,
-                        qf[nt][2 * j][0], qf[nt][2 * j][1]);
-                    const uint32_t y0 = k0[j] >> 8, y1 = k1[j] >> 8;
-                    mma(acc[32 * j / G], y0 & kLo, y1 & kLo, y0 & kHi, y1 & kHi,
-                        qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
-                }
-                // S - reference, [token g, g + 8][row 2 c, 2 c + 1]
-                float S[2][2], P[2][2];
+                // S - `from`, [token g, g + 8][row 2 c, 2 c + 1]
                 bool seen[2][2];
+                auto score = [&](int t, int e, float from) {
+                    float x = bf16_lo(pk[t][0]) * acc[nt][0][2 * t + e], y = -from;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                    for (int gr = 1; gr < NG; ++gr)
+                        x = fmaf(bf16_lo(pk[t][gr]), acc[nt][gr][2 * t + e], x);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = bf16_lo(pk[t][0]) * acc[0][2 * t + e], y = -ref[nt][e];
+                    for (int gr = 0; gr < NG; ++gr)
+                        y = fmaf(bf16_hi(pk[t][gr]), qbar[nt][gr][e], y);
+                    return seen[t][e] ? fmaf(x, mul[nt][e], y) : -INFINITY;
+                };
+                float P[2][2];
 #pragma unroll
-                        for (int gr = 1; gr < NG; ++gr)
-                            x = fmaf(bf16_lo(pk[t][gr]), acc[gr][2 * t + e], x);
+                for (int e = 0; e < 2; ++e) {
+                    const int last = kMasked ? qt.end[nt * 8 + 2 * c + e] : 0;
 #pragma unroll
-                        for (int gr = 0; gr < NG; ++gr)
-                            y = fmaf(bf16_hi(pk[t][gr]), qbar[nt][gr][e], y);
-                        S[t][e] = fmaf(x, mul[nt][e], y);
-                        seen[t][e] = !kMasked || tok + g + 8 * t < lim[nt][e];
-                        if (!seen[t][e])
-                            S[t][e] = -INFINITY;
-                        P[t][e] = ptx::ex2(S[t][e]);
+                    for (int t = 0; t < 2; ++t) {
+                        seen[t][e] = !kMasked || tok + g + 8 * t < last;
+                        P[t][e] = ptx::ex2(score(t, e, ref[nt][e]));
                     }
+                }
                 const float over = fmaxf(max3(P[0][0] * w[0], P[0][1] * w[0], P[1][0] * w[1]),
                                          P[1][1] * w[1]);
                 if (__any_sync(0xffffffffu, over > kLag)) {
-                    // a row outgrew its reference: every row's becomes the
-                    // largest S + log2 w seen (S formed anew: from kNoRef, the
-                    // difference has lost its digits)
+                    // a row outgrew its reference: every row's becomes the largest
+                    // S + log2 w seen
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float S0[2];
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            float x = bf16_lo(pk[t][0]) * acc[0][2 * t + e], y = 0.f;
-#pragma unroll
-                            for (int gr = 1; gr < NG; ++gr)
-                                x = fmaf(bf16_lo(pk[t][gr]), acc[gr][2 * t + e], x);
-#pragma unroll
-                            for (int gr = 0; gr < NG; ++gr)
-                                y = fmaf(bf16_hi(pk[t][gr]), qbar[nt][gr][e], y);
-                            S0[t] = seen[t][e] ? fmaf(x, mul[nt][e], y) : -INFINITY;
-                        }
-                        float m = fmaxf(S0[0] + __log2f(w[0]), S0[1] + __log2f(w[1]));
+                        const float S0 = score(0, e, 0.f), S1 = score(1, e, 0.f);
+                        float m = fmaxf(S0 + __log2f(w[0]), S1 + __log2f(w[1]));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -532,8 +583,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                             O[nt][x][e] *= f;
                             O[nt][x][2 + e] *= f;
                         }
-                        P[0][e] = ptx::ex2(S0[0] - m);
-                        P[1][e] = ptx::ex2(S0[1] - m);
+                        P[0][e] = ptx::ex2(S0 - m);
+                        P[1][e] = ptx::ex2(S1 - m);
                     }
                 }
 #pragma unroll
@@ -564,43 +615,45 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
             uint32_t v[4][D / 64];
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                load_words<D / 64>(v[x], cell + kv4::v_off(D) + v_at[x]);
+                load_shared<0>(v[x], at_V[x] + slot);
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
                 const uint32_t sel = (q & 1) ? 0x7632 : 0x5410;
                 const uint32_t x = __byte_perm(v[0][q / 2], v[1][q / 2], sel);
                 const uint32_t y = __byte_perm(v[2][q / 2], v[3][q / 2], sel);
                 const uint32_t x8 = x >> 8, y8 = y >> 8;
+                const uint32_t a0[4] = {x & kLo, x & kHi, y & kLo, y & kHi};
+                const uint32_t a1[4] = {x8 & kLo, x8 & kHi, y8 & kLo, y8 & kHi};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma(O[nt][2 * q], x & kLo, x & kHi, y & kLo, y & kHi, pf[nt][32 * q / G][0],
-                        pf[nt][32 * q / G][1]);
-                    mma(O[nt][2 * q + 1], x8 & kLo, x8 & kHi, y8 & kLo, y8 & kHi,
-                        pf[nt][32 * q / G][0], pf[nt][32 * q / G][1]);
+                    mma(O[nt][2 * q], a0, pf[nt][32 * q / G][0], pf[nt][32 * q / G][1]);
+                    mma(O[nt][2 * q + 1], a1, pf[nt][32 * q / G][0], pf[nt][32 * q / G][1]);
                 }
             }
         };
 
-        const int tok_end = key_end(a, L, qb.y, (tile * R + rows - 1) / grp);
-        int tok = int(blk0) * kBlock + warp * kv4::kCellTokens;
+        // keys that some row of the tile sees, and that all rows see
+        const int tok_end = key_end(a, it, (it.tile * R + rows - 1) / grp);
+        const int all_end = key_end(a, it, it.tile * R / grp);
+        int tok = int(cur - it.first) * kBlock + warp * kv4::kCellTokens;
         for (uint32_t k = cur - begin; k < stop - begin; ++k, tok += kBlock) {
-            const uint8_t *cell = ring + k % kStages * kCell;
             if (!ptx::mbar_wait_warp(full + k % kStages, k / kStages & 1, &s_abort, a.err_word))
                 break;                     // the error is recorded, nothing is written
             done = k + 1;
             if (tok < tok_end && !(bad_pages && skipped(k))) {
-                if (tok + kv4::kCellTokens <= lim_least)
-                    cell_step(cell, tok, std::false_type{});
+                const uint32_t slot = k % kStages * kCell;
+                if (tok + kv4::kCellTokens <= all_end)
+                    cell_step(slot, tok, std::false_type{});
                 else
-                    cell_step(cell, tok, std::true_type{});
+                    cell_step(slot, tok, std::true_type{});
             }
             __syncwarp();                  // every lane has read the cell
             issue(k + kStages);
         }
 
         // ---- the warps' parts joined, and written ----------------------------
-        const bool whole = blk0 == 0 && stop == item0 + nb;
-        const int slot = 2 * int(blockIdx.x) + (blk0 == 0 ? 1 : 0);
+        const bool whole = cur == it.first && stop == it.first + it.nb;
+        const int slot = 2 * int(blockIdx.x) + (cur == it.first ? 1 : 0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -620,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                 }
             }
         __syncthreads();
+        const Item next = stop < end ? item_at(a, s_pre, s_len, grp, R, stop) : it;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             // the upper warps' rows through shared memory into the lower warps'
@@ -651,12 +705,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                             *at = y;
                         }
                     }
+                } else if (half == 0 && nt == 0 && warp < NT && stop < end) {
+                    // meanwhile the next item's queries
+                    load_queries<D, G, NT>(a, next, grp, warp, s_q[buf ^ 1]);
                 }
                 __syncthreads();
             }
             // 8 rows x D values over the threads, four consecutive values each
-            for (int it = tid; it < 8 * (D / 4); it += kThreads) {
-                const int rr = it / (D / 4), d4 = it % (D / 4) * 4, r = nt * 8 + rr;
+            for (int x = tid; x < 8 * (D / 4); x += kThreads) {
+                const int rr = x / (D / 4), d4 = x % (D / 4) * 4, r = nt * 8 + rr;
                 float4 y = *reinterpret_cast<const float4 *>(s_O + rr * kRow + d4);
                 float m = s_ref[r];
 #pragma unroll
@@ -675,17 +732,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                 if (r >= rows || s_abort)
                     continue;
                 if (whole) {
-                    const int i = (tile * R + r) / grp, h = kvh * grp + (tile * R + r) % grp;
-                    const float inv = s > 0.f || s != s ? 1.f / s : 0.f;
+                    const int at = it.tile * R + r, i = at / grp, h = it.kvh * grp + at % grp;
+                    const bool any = s > 0.f || s != s;
+                    const float inv = any ? 1.f / s : 0.f;
                     const uint2 o = make_uint2(ptx::pack_bf16x2(y.x * inv, y.y * inv),
                                                ptx::pack_bf16x2(y.z * inv, y.w * inv));
                     auto *dst = static_cast<__nv_bfloat16 *>(a.O) +
-                                (int64_t(qb.x + i) * a.H + h) * D + d4;
+                                (int64_t(it.q0 + i) * a.H + h) * D + d4;
                     *reinterpret_cast<uint2 *>(dst) = o;
                     if (d4 == 0)
-                        a.lse[a.cu_seqlens_q ? int64_t(h) * a.total_q + qb.x + i
-                                             : (int64_t(b) * a.H + h) * a.Nq + i] =
-                            s > 0.f || s != s ? (m + log2f(s)) * kLn2 : -INFINITY;
+                        a.lse[a.cu_seqlens_q ? int64_t(h) * a.total_q + it.q0 + i
+                                             : (int64_t(it.b) * a.H + h) * a.Nq + i] =
+                            any ? (m + log2f(s)) * kLn2 : -INFINITY;
                 } else {
                     *reinterpret_cast<float4 *>(parts.O + (int64_t(slot) * R + r) * D + d4) = y;
                     if (d4 == 0)
@@ -694,13 +752,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
             }
             __syncthreads();
         }
-        if (blk0 == 0 && !whole) {
+        if (cur == it.first && !whole) {
             // CTAs that hold a part: up to the one whose range has the last block
-            const uint64_t x = uint64_t(item0) + nb;            // ceil(x n / T) - 1
+            const uint64_t x = uint64_t(it.first) + it.nb;      // ceil(x n / T) - 1
             const int last_cta = int((x * n_ctas + T - 1) / T) - 1;
-            desc = Desc{last_cta - int(blockIdx.x) + 1, b, kvh, tile};
+            desc = Desc{last_cta - int(blockIdx.x) + 1, it.b, it.kvh, it.tile};
         }
         cur = stop;
+        it = next;
+        buf ^= 1;
     }
     if (s_abort) {
         // a wait ran out: copies still on their way must land before the CTA ends
