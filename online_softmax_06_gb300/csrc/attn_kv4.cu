@@ -40,9 +40,10 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBlock = kWarps * kv4::kCellTokens;   // tokens of a block: a cell each warp
+constexpr int kPair = 2 * kv4::kCellTokens;         // tokens that a warp copies and takes at once
+constexpr int kBlock = kWarps * kPair;              // tokens of a block: two cells each warp
 constexpr float kNoRef = -1e30f;   // reference of a row that has seen no key: exp2(-inf - kNoRef) = 0
 // A row's reference is max(S + log2 w), w the weight of a key's V parameters, so
 // that P s <= 1 in fp16 whatever the scales are; it may lag by a factor of 16.
@@ -88,6 +89,13 @@ __device__ __forceinline__ float max3(float x, float y, float z)
     return r;
 }
 
+// The same value in every lane, as the compiler cannot know: what follows from it
+// (addresses, loop control) then runs on the uniform datapath.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Keeps a lane's address in its register instead of computing it anew at each use.
+__device__ __forceinline__ void keep(uint32_t &x) { asm volatile("" : "+r"(x)); }
+
 // N words of shared memory at address `at` + OFF.  Volatile: the ring's contents
 // change, and the queries' fragments are read again each time rather than held.
 template <int OFF, int N>
@@ -105,30 +113,36 @@ __device__ __forceinline__ void load_shared(uint32_t (&w)[N], uint32_t at)
         asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(w[0]) : "r"(at), "n"(OFF));
 }
 
-// Lane `mine` of the warp: arrives at the cell's barrier and starts its copy; with
-// no source it only arrives.
-template <int BYTES>
-__device__ __forceinline__ void copy_cell(uint32_t bar, uint32_t to, const uint8_t *src, bool mine)
+// Of NC cells the words at address `at` + OFF and, for token g + 8, UP on.
+template <int NC, int CELL, int OFF, int UP, int N>
+__device__ __forceinline__ void load_tokens(uint32_t (&w)[NC][2][N], uint32_t at)
 {
-    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 n;\n\t"
-                 "setp.ne.u32 p, %3, 0;\n\t"
-                 "setp.ne.and.u64 q, %2, 0, p;\n\t"
-                 "selp.b32 n, %4, 0, q;\n\t"
-                 "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], n;\n\t"
-                 "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2], "
-                 "%4, [%0];\n\t}"
-                 ::"r"(bar), "r"(to), "l"(src), "r"(uint32_t(mine)), "n"(BYTES)
-                 : "memory");
+    load_shared<OFF>(w[0][0], at);
+    load_shared<OFF + UP>(w[0][1], at);
+    if constexpr (NC == 2) {
+        load_shared<CELL + OFF>(w[1][0], at);
+        load_shared<CELL + OFF + UP>(w[1][1], at);
+    }
+}
+
+// The words of token number i of a lane's four.
+template <int NC, int CELL, int OFF, int N>
+__device__ __forceinline__ void load_values(uint32_t (&v)[NC][4][N], int i, uint32_t at)
+{
+    load_shared<OFF>(v[0][i], at);
+    if constexpr (NC == 2)
+        load_shared<CELL + OFF>(v[1][i], at);
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// Cells on their way or in use: each warp keeps a ring of its own, one bulk copy
-// a cell, no barrier between warps.  Two CTAs an SM with 4 cells of 2304 bytes a
-// warp have up to 147 KB in flight, against the 36 KB that cover HBM's latency at
-// full rate.
-constexpr int kStages = 4;
+// Pairs of cells on their way or in use: each warp has a ring of its own and
+// fills a place again as soon as it has read it; no barrier between warps.  16
+// warps an SM with one pair of 4608 bytes each on its way are 74 KB in flight,
+// against the 36 KB that cover HBM's latency at full rate.
+constexpr int kStages = 2;
+constexpr int kJoinWarps = 8;
 
 // A work item is (sequence, kv head, tile of R query rows); its keys are cut
 // into blocks of kBlock tokens.  All items' blocks, sequence by sequence, form
@@ -139,8 +153,8 @@ struct Desc {          // of an item that begins in this CTA's range and does no
     int b, kvh, tile;
 };
 
-// Workspace: Desc[kMaxCtas], then (reference, sum) [2 kMaxCtas][R], then
-// the unnormalised O [2 kMaxCtas][R][d] fp32.  A CTA's slot 0 holds the part of
+// Workspace: Desc[ctas], then (reference, sum) [2 ctas][R], then the
+// unnormalised O [2 ctas][R][d] fp32.  A CTA's slot 0 holds the part of
 // an item that began before its range, slot 1 that of one that goes on after.
 struct Parts {
     Desc *desc;
@@ -153,8 +167,8 @@ __host__ __device__ inline Parts parts_of(void *ws)
 {
     Parts p;
     p.desc = static_cast<Desc *>(ws);
-    p.ml = reinterpret_cast<float2 *>(p.desc + kKv4MaxCtas);
-    p.O = reinterpret_cast<float *>(p.ml + 2 * kKv4MaxCtas * R);
+    p.ml = reinterpret_cast<float2 *>(p.desc + kv4_attention_ctas(R));
+    p.O = reinterpret_cast<float *>(p.ml + 2 * kv4_attention_ctas(R) * R);
     return p;
 }
 
@@ -184,13 +198,12 @@ struct alignas(16) QueryTile {
 template <int D, int G, int NT>
 struct Shared {
     static constexpr int R = 8 * NT;
-    static constexpr int ring = 0;                                   // [kWarps][kStages] cells
-    static constexpr int q = ring + kWarps * kStages * kv4::cell_bytes(D, G);  // [2] QueryTile
-    static constexpr int O = q + 2 * int(sizeof(QueryTile<D, G, NT>));  // [kWarps / 2][8][D + 4]
+    static constexpr int ring = 0;                                   // [kWarps][kStages] pairs
+    static constexpr int q = ring + kWarps * kStages * 2 * kv4::cell_bytes(D, G);  // QueryTile
+    static constexpr int O = q + int(sizeof(QueryTile<D, G, NT>));   // [kWarps / 2][8][D + 4]
     static constexpr int full = O + kWarps / 2 * 8 * (D + 4) * 4;    // [kWarps][kStages] barriers
     static constexpr int pre = full + kWarps * kStages * 8;          // [B + 1] blocks before b
-    static constexpr int len = pre + (kKv4MaxSeqs + 4) * 4;          // [B] keys
-    static constexpr int ref = len + kKv4MaxSeqs * 4;                // [kWarps][R]
+    static constexpr int ref = pre + (kKv4MaxSeqs + 4) * 4;          // [kWarps][R]
     static constexpr int sum = ref + kWarps * R * 4;                 // [kWarps][R]
     static constexpr int bytes = sum + kWarps * R * 4;
 };
@@ -203,8 +216,8 @@ struct Item {
     int nb;                // its blocks
 };
 
-__device__ __forceinline__ Item item_at(const Kv4AttnArgs &a, const uint32_t *s_pre,
-                                        const int *s_len, int grp, int R, uint32_t x)
+__device__ __forceinline__ Item item_at(const Kv4AttnArgs &a, const uint32_t *s_pre, int grp, int R,
+                                        uint32_t x)
 {
     int lo = 0, hi = a.B;                  // s_pre[lo] <= x < s_pre[lo + 1]
     while (hi - lo > 1) {
@@ -219,13 +232,26 @@ __device__ __forceinline__ Item item_at(const Kv4AttnArgs &a, const uint32_t *s_
     it.b = lo;
     it.q0 = q.x;
     it.nq = q.y;
-    it.L = s_len[lo];
+    it.L = a.seqlens[lo];
     it.nb = blocks_of(it.L);
     const uint32_t tiles = uint32_t(q.y * grp + R - 1) / R, at = x - s_pre[lo];
     const uint32_t i = at / uint32_t(it.nb);
     it.kvh = int(i / tiles);
     it.tile = int(i % tiles);
     it.first = s_pre[lo] + i * it.nb;
+    return it;
+}
+
+__device__ __forceinline__ Item uniform(Item it)
+{
+    it.b = uniform(it.b);
+    it.q0 = uniform(it.q0);
+    it.nq = uniform(it.nq);
+    it.L = uniform(it.L);
+    it.kvh = uniform(it.kvh);
+    it.tile = uniform(it.tile);
+    it.first = uint32_t(uniform(int(it.first)));
+    it.nb = uniform(it.nb);
     return it;
 }
 
@@ -299,34 +325,70 @@ __device__ __forceinline__ void load_queries(const Kv4AttnArgs &a, const Item &i
     }
 }
 
+// One copy: `bytes` from `src`; 0: none; -n: n bytes of a page that there is not.
+struct Copy {
+    const uint8_t *src;
+    int bytes;
+};
+
+// What lane `half` of two has to copy of the pair of cells from token `tok0` of
+// block x on: the cells of a page of a multiple of 32 tokens are one piece of
+// memory, which the first lane copies; otherwise each lane copies a cell.
+__device__ __noinline__ Copy find_copy(const Kv4AttnArgs &a, const uint32_t *s_pre, int grp, int R,
+                                       int cell_bytes, uint32_t x, int tok0, int half)
+{
+    Copy c{nullptr, 0};
+    const Item it = item_at(a, s_pre, grp, R, x);
+    const bool one = a.page_size % kPair == 0;
+    const int tok = int(x - it.first) * kBlock + tok0 + half * kv4::kCellTokens;
+    const int stop = key_end(a, it, (min(it.nq * grp, (it.tile + 1) * R) - 1) / grp);
+    if (tok >= stop || (one && half == 1))
+        return c;
+    c.bytes = one && tok + kv4::kCellTokens < stop ? 2 * cell_bytes : cell_bytes;
+    const int col = tok / a.page_size;
+    const int page = a.page_table[int64_t(it.b) * a.max_pages + col];
+    if (page < 0 || page >= a.num_pages) {
+        record_device_error(a.err_word, FA_DEVERR_BAD_PAGE);
+        c.bytes = -c.bytes;
+        return c;
+    }
+    c.src = static_cast<const uint8_t *>(a.cache) +
+            ((int64_t(page) * a.Hkv + it.kvh) * (a.page_size / kv4::kCellTokens) +
+             (tok - col * a.page_size) / kv4::kCellTokens) * cell_bytes;
+    return c;
+}
+
 template <int D, int G, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(const Kv4AttnArgs a)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(const Kv4AttnArgs a)
 {
     constexpr int R = 8 * NT;              // query rows of a tile
     constexpr int NG = D / G;              // groups of the head dimension
     constexpr int NJ = D / 32;             // words a lane holds of a K row
     constexpr int kCell = kv4::cell_bytes(D, G);
     constexpr int kRow = D + 4;            // padded fp32 row of the merge buffer
+    constexpr int kVBases = D == 128 ? 2 : 4;   // d = 128: 8 tokens are 512 bytes on
     using Smem = Shared<D, G, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
-    auto *s_q = reinterpret_cast<QueryTile<D, G, NT> *>(smem + Smem::q);
+    auto &s_q = *reinterpret_cast<QueryTile<D, G, NT> *>(smem + Smem::q);
     float *s_O = reinterpret_cast<float *>(smem + Smem::O);
     uint32_t *s_pre = reinterpret_cast<uint32_t *>(smem + Smem::pre);
-    int *s_len = reinterpret_cast<int *>(smem + Smem::len);
     float *s_ref = reinterpret_cast<float *>(smem + Smem::ref);
     float *s_sum = reinterpret_cast<float *>(smem + Smem::sum);
     __shared__ int s_abort;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, g = lane >> 2,
+              c = lane & 3;
     const int grp = a.H / a.Hkv;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Smem::full) + warp * kStages;
-    uint8_t *ring = smem + Smem::ring + warp * kStages * kCell;
+    uint8_t *ring = smem + Smem::ring + warp * (kStages * 2 * kCell);
     if (lane == 0) {
         for (int i = 0; i < kStages; ++i)
-            ptx::mbar_init(full + i, 1);
+            ptx::mbar_init(full + i, 2);   // a pair's two lanes
         ptx::fence_barrier_init();
     }
     if (tid == 0)
         s_abort = 0;
+    // the join's launch may overlap this kernel: it waits for its end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the line of blocks ------------------------------------------------
     const int per = (a.B + kThreads - 1) / kThreads;
@@ -343,7 +405,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
             record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
         else
             n = uint32_t((q.y * grp + R - 1) / R) * a.Hkv * blocks_of(L);
-        s_len[b] = L;
         s_pre[b + 1] = n;
         mine += n;
     }
@@ -371,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
     if (tid == 0)
         s_pre[0] = 0;
     __syncthreads();
-    const uint64_t T = s_pre[a.B];
+    const uint64_t T = uint32_t(uniform(int(s_pre[a.B])));
     const uint32_t n_ctas = uint32_t(T < gridDim.x ? T : gridDim.x);
     const Parts parts = parts_of<R>(a.workspace);
     if (blockIdx.x >= n_ctas) {
@@ -383,84 +444,73 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
     const uint32_t end = uint32_t(T * (blockIdx.x + 1) / n_ctas);
     Desc desc{0, 0, 0, 0};
 
-    // ---- copies ---------------------------------------------------------------
-    // Lane i finds where this warp's cell of every 32nd block begins, so that the
-    // search and the page table's latency are paid once for 32 cells; it then
-    // issues that cell's copy itself.  `have`: which of the batch's cells are read.
-    const uint32_t n_cells = end - begin;
-    const uint8_t *src = nullptr;
-    uint32_t have = 0, have_before = 0;
-    bool bad_pages = false;
-    auto find = [&](uint32_t k0) {
-        src = nullptr;
-        const uint32_t x = begin + k0 + lane;
-        bool bad = false;
-        if (x < end) {
-            const Item it = item_at(a, s_pre, s_len, grp, R, x);
-            const int tok = int(x - it.first) * kBlock + warp * kv4::kCellTokens;
-            if (tok < key_end(a, it, (min(it.nq * grp, (it.tile + 1) * R) - 1) / grp)) {
-                const int page = a.page_table[int64_t(it.b) * a.max_pages + tok / a.page_size];
-                if (page >= 0 && page < a.num_pages)
-                    src = static_cast<const uint8_t *>(a.cache) +
-                          ((int64_t(page) * a.Hkv + it.kvh) * (a.page_size / kv4::kCellTokens) +
-                           tok % a.page_size / kv4::kCellTokens) * kCell;
-                else
-                    bad = true;
-            }
+    // ---- copies ------------------------------------------------------------------
+    // Each warp copies its own pairs.  32 lanes find the sources of 16 pairs at
+    // once, so that the search and the page table's latency are paid once for
+    // them, and issue them when their turn comes.
+    const uint32_t n_blocks = end - begin;
+    Copy copy{nullptr, 0};
+    auto fill = [&](uint32_t k) {
+        if (k >= n_blocks)
+            return;
+        if (k % 16 == 0) {
+            const uint32_t x = begin + k + lane / 2;
+            copy = x < end ? find_copy(a, s_pre, grp, R, kCell, x, warp * kPair, lane & 1)
+                           : Copy{nullptr, 0};
         }
-        if (bad)
-            record_device_error(a.err_word, FA_DEVERR_BAD_PAGE);
-        bad_pages |= __any_sync(0xffffffffu, bad) != 0;
-        have_before = have;
-        have = __ballot_sync(0xffffffffu, src != nullptr);
-    };
-    const uint32_t ring_at = ptx::smem_u32(ring), full_at = ptx::smem_u32(full);
-    auto issue = [&](uint32_t k) {         // all lanes of the warp
-        if ((k & 31) == 0 && k < n_cells)
-            find(k);
-        if (k < n_cells)
-            copy_cell<kCell>(full_at + (k % kStages) * 8, ring_at + (k % kStages) * kCell, src,
-                             lane == int(k & 31));
+        if (lane / 2 == int(k % 16)) {
+            uint8_t *to = ring + k % kStages * (2 * kCell) + (lane & 1) * kCell;
+            uint64_t *bar = full + k % kStages;
+            if (copy.bytes < 0) {
+                // the tokens of a page outside the cache count as zeros
+                for (int i = 0; i < -copy.bytes; i += 16)
+                    *reinterpret_cast<uint4 *>(to + i) = make_uint4(0, 0, 0, 0);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            ptx::mbar_arrive_expect_tx(bar, uint32_t(max(copy.bytes, 0)));
+            if (copy.bytes > 0)
+                ptx::bulk_load(to, copy.src, uint32_t(copy.bytes), bar);
+        }
     };
     for (uint32_t k = 0; k < kStages; ++k)
-        issue(k);
-    uint32_t done = 0;                     // cells read
-    // whether cell k was left out; the batch that cell k + kStages - 1 is in, the
-    // last one issued, may be the next one already
-    auto skipped = [&](uint32_t k) {
-        const uint32_t ahead = min(k + kStages, n_cells) - 1;
-        return !((ahead / 32 == k / 32 ? have : have_before) >> (k & 31) & 1);
-    };
+        fill(k);
+    const uint32_t ring_at = ptx::smem_u32(ring);
+    bool stuck = false;                    // a wait ran out, at block `done`
+    uint32_t done = n_blocks;
 
     // this lane's places in a cell
-    const uint32_t at_K = ring_at + lane * (4 * NJ);
-    const uint32_t at_par = ring_at + kv4::k_par_off(D) + g * (4 * NG);
+    uint32_t at_K = ring_at + lane * (4 * NJ);
+    uint32_t at_par = ring_at + kv4::k_par_off(D) + g * (4 * NG);
     uint32_t at_V[4];                      // of tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < 4; ++x) {
         at_V[x] = ring_at + kv4::v_off(D) +
                   kv4::v_swizzle((2 * c + (x & 1) + 8 * (x >> 1)) * (D / 2) + g * (D / 16));
+        if (x < kVBases)
+            keep(at_V[x]);
+    }
+    uint32_t at_Q = ptx::smem_u32(&s_q.frag[0][0][lane]);
+    keep(at_K);
+    keep(at_par);
+    keep(at_Q);
 
-    Item it = item_at(a, s_pre, s_len, grp, R, begin);
+    Item it = uniform(item_at(a, s_pre, grp, R, begin));
     if (warp < NT)
-        load_queries<D, G, NT>(a, it, grp, warp, s_q[0]);
+        load_queries<D, G, NT>(a, it, grp, warp, s_q);
     __syncthreads();
-    int buf = 0;
     for (uint32_t cur = begin; cur < end;) {
         const uint32_t stop = min(end, it.first + it.nb);
         const int rows = min(R, it.nq * grp - it.tile * R);         // rows of this tile
-        const QueryTile<D, G, NT> &qt = s_q[buf];
-        const uint32_t at_Q = ptx::smem_u32(&qt.frag[0][0][lane]);
         float mul[NT][2], qbar[NT][NG][2];     // of rows 2 c, 2 c + 1 of n-tile nt
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = nt * 8 + 2 * c + e;
-                mul[nt][e] = qt.mul[r];
+                mul[nt][e] = s_q.mul[r];
 #pragma unroll
                 for (int x = 0; x < NG; ++x)
-                    qbar[nt][x][e] = qt.bar[x][r];
+                    qbar[nt][x][e] = s_q.bar[x][r];
             }
 
         // ---- the keys ----------------------------------------------------------
@@ -479,176 +529,224 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                     pm[nt][x][e] = 0.f;
             }
         }
-        // One cell's keys.  kMasked: some query row of the tile does not see all
-        // of them, or the sequence ends inside the cell.
-        auto cell_step = [&](uint32_t slot, int tok, auto masked_tag) {
+        // NC cells' keys, from token `tok` on.  kMasked: some query row of the tile
+        // does not see all of them, or the sequence ends among them.
+        const int tok_end = key_end(a, it, (it.tile * R + rows - 1) / grp);
+        auto step = [&](uint32_t slot, int tok, auto masked_tag, auto cells_tag) {
             constexpr bool kMasked = decltype(masked_tag)::value;
+            constexpr int NC = decltype(cells_tag)::value;
             constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
-            // S^T = K Q^T: lane (g, c) holds tokens g, g + 8
-            uint32_t k0[NJ], k1[NJ];
-            load_shared<0>(k0, at_K + slot);
-            load_shared<8 * (D / 2)>(k1, at_K + slot);
-            // (scale, min) pairs of tokens g and g + 8
-            uint32_t pk[2][NG], pv[2][NG];
-            constexpr int kV = 64 * NG, kUp = 32 * NG;
-            load_shared<0>(pk[0], at_par + slot);
-            load_shared<kUp>(pk[1], at_par + slot);
-            load_shared<kV>(pv[0], at_par + slot);
-            load_shared<kV + kUp>(pv[1], at_par + slot);
-            if constexpr (kMasked) {
-                // behind the sequence's end they may be anything, and count as 0
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (tok + g + 8 * t >= it.L)
-#pragma unroll
-                        for (int x = 0; x < NG; ++x)
-                            pk[t][x] = pv[t][x] = 0;
-            }
-            float acc[NT][NG][4];
+            // S^T = K Q^T: lane (g, c) holds tokens g, g + 8 of each cell
+            uint32_t kw[NC][2][NJ];
+            load_tokens<NC, kCell, 0, 8 * (D / 2)>(kw, at_K + slot);
+            float acc[NC][NT][NG][4];
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const uint32_t y0 = k0[j] >> 8, y1 = k1[j] >> 8;
-                const uint32_t a0[4] = {k0[j] & kLo, k1[j] & kLo, k0[j] & kHi, k1[j] & kHi};
-                const uint32_t a1[4] = {y0 & kLo, y1 & kLo, y0 & kHi, y1 & kHi};
+                uint32_t a0[NC][4], a1[NC][4];
+#pragma unroll
+                for (int x = 0; x < NC; ++x) {
+                    const uint32_t w0 = kw[x][0][j], w1 = kw[x][1][j];
+                    const uint32_t y0 = w0 >> 8, y1 = w1 >> 8;
+                    a0[x][0] = w0 & kLo, a0[x][1] = w1 & kLo, a0[x][2] = w0 & kHi,
+                    a0[x][3] = w1 & kHi;
+                    a1[x][0] = y0 & kLo, a1[x][1] = y1 & kLo, a1[x][2] = y0 & kHi,
+                    a1[x][3] = y1 & kHi;
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     uint32_t q[4];
                     load_shared<0>(q, at_Q + (nt * NJ + j) * 512);
-                    if (32 * j % G == 0)
-                        mma_first(acc[nt][32 * j / G], a0, q[0], q[1]);
-                    else
-                        mma(acc[nt][32 * j / G], a0, q[0], q[1]);
-                    mma(acc[nt][32 * j / G], a1, q[2], q[3]);
+#pragma unroll
+                    for (int x = 0; x < NC; ++x) {
+                        float (&to)[4] = acc[x][nt][32 * j / G];
+                        if (32 * j % G == 0)
+                            mma_first(to, a0[x], q[0], q[1]);
+                        else
+                            mma(to, a0[x], q[0], q[1]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < NC; ++x)
+                        mma(acc[x][nt][32 * j / G], a1[x], q[2], q[3]);
                 }
             }
-            float w[2];
+            // (scale, min) pairs of tokens g and g + 8
+            uint32_t pk[NC][2][NG], pv[NC][2][NG];
+            load_tokens<NC, kCell, 0, 32 * NG>(pk, at_par + slot);
+            load_tokens<NC, kCell, 64 * NG, 32 * NG>(pv, at_par + slot);
+            if constexpr (kMasked) {
+                // behind the last key they may be anything, and count as 0
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float s_big = bf16_lo(pv[t][0]), m_big = fabsf(bf16_hi(pv[t][0]));
+                for (int x = 0; x < NC; ++x)
 #pragma unroll
-                for (int x = 1; x < NG; ++x) {
-                    s_big = fmaxf(s_big, bf16_lo(pv[t][x]));
-                    m_big = fmaxf(m_big, fabsf(bf16_hi(pv[t][x])));
-                }
-                // |m| counts too (a constant group has s = 0), so that P m stays
-                // finite in fp32
-                w[t] = max3(s_big, m_big * 0x1p-12f, kLeastWeight);
+                    for (int t = 0; t < 2; ++t)
+                        if (tok + 16 * x + g + 8 * t >= tok_end)
+#pragma unroll
+                            for (int y = 0; y < NG; ++y)
+                                pk[x][t][y] = pv[x][t][y] = 0;
             }
-            uint32_t pf[NT][NG][2];
+            float w[NC][2];
+#pragma unroll
+            for (int x = 0; x < NC; ++x)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    float s_big = bf16_lo(pv[x][t][0]), m_big = fabsf(bf16_hi(pv[x][t][0]));
+#pragma unroll
+                    for (int y = 1; y < NG; ++y) {
+                        s_big = fmaxf(s_big, bf16_lo(pv[x][t][y]));
+                        m_big = fmaxf(m_big, fabsf(bf16_hi(pv[x][t][y])));
+                    }
+                    // |m| counts too (a constant group has s = 0), so that P m stays
+                    // finite in fp32
+                    w[x][t] = max3(s_big, m_big * 0x1p-12f, kLeastWeight);
+                }
+            uint32_t pf[NC][NT][NG][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                bool seen[NC][2][2];
                 // S - `from`, [token g, g + 8][row 2 c, 2 c + 1]
-                bool seen[2][2];
-                auto score = [&](int t, int e, float from) {
-                    float x = bf16_lo(pk[t][0]) * acc[nt][0][2 * t + e], y = -from;
+                auto score = [&](int x, int t, int e, float from) {
+                    float s = bf16_lo(pk[x][t][0]) * acc[x][nt][0][2 * t + e], y = -from;
 #pragma unroll
                     for (int gr = 1; gr < NG; ++gr)
-                        x = fmaf(bf16_lo(pk[t][gr]), acc[nt][gr][2 * t + e], x);
+                        s = fmaf(bf16_lo(pk[x][t][gr]), acc[x][nt][gr][2 * t + e], s);
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr)
-                        y = fmaf(bf16_hi(pk[t][gr]), qbar[nt][gr][e], y);
-                    return seen[t][e] ? fmaf(x, mul[nt][e], y) : -INFINITY;
+                        y = fmaf(bf16_hi(pk[x][t][gr]), qbar[nt][gr][e], y);
+                    return seen[x][t][e] ? fmaf(s, mul[nt][e], y) : -INFINITY;
                 };
-                float P[2][2];
+                float P[NC][2][2], over = 0.f;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int last = kMasked ? qt.end[nt * 8 + 2 * c + e] : 0;
+                for (int x = 0; x < NC; ++x)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        seen[t][e] = !kMasked || tok + g + 8 * t < last;
-                        P[t][e] = ptx::ex2(score(t, e, ref[nt][e]));
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            seen[x][t][e] = !kMasked || tok + 16 * x + g + 8 * t <
+                                                            s_q.end[nt * 8 + 2 * c + e];
+                            P[x][t][e] = ptx::ex2(score(x, t, e, ref[nt][e]));
+                        }
+                        over = max3(over, P[x][t][0] * w[x][t], P[x][t][1] * w[x][t]);
                     }
-                }
-                const float over = fmaxf(max3(P[0][0] * w[0], P[0][1] * w[0], P[1][0] * w[1]),
-                                         P[1][1] * w[1]);
                 if (__any_sync(0xffffffffu, over > kLag)) {
                     // a row outgrew its reference: every row's becomes the largest
                     // S + log2 w seen
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float S0 = score(0, e, 0.f), S1 = score(1, e, 0.f);
-                        float m = fmaxf(S0 + __log2f(w[0]), S1 + __log2f(w[1]));
+                        float S[NC][2], m = ref[nt][e];
+#pragma unroll
+                        for (int x = 0; x < NC; ++x)
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                S[x][t] = score(x, t, e, 0.f);
+                                m = fmaxf(m, S[x][t] + __log2f(w[x][t]));
+                            }
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        m = fmaxf(m, ref[nt][e]);
                         const float f = ptx::ex2(ref[nt][e] - m);
                         ref[nt][e] = m;
                         sum[nt][e] *= f;
 #pragma unroll
-                        for (int x = 0; x < NG; ++x)
-                            pm[nt][x][e] *= f;
+                        for (int y = 0; y < NG; ++y)
+                            pm[nt][y][e] *= f;
 #pragma unroll
-                        for (int x = 0; x < D / 16; ++x) {
-                            O[nt][x][e] *= f;
-                            O[nt][x][2 + e] *= f;
+                        for (int y = 0; y < D / 16; ++y) {
+                            O[nt][y][e] *= f;
+                            O[nt][y][2 + e] *= f;
                         }
-                        P[0][e] = ptx::ex2(S0 - m);
-                        P[1][e] = ptx::ex2(S1 - m);
+#pragma unroll
+                        for (int x = 0; x < NC; ++x)
+#pragma unroll
+                            for (int t = 0; t < 2; ++t)
+                                P[x][t][e] = ptx::ex2(S[x][t] - m);
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    sum[nt][e] += P[0][e] + P[1][e];
+                for (int x = 0; x < NC; ++x) {
 #pragma unroll
-                for (int x = 0; x < NG; ++x)
+                    for (int e = 0; e < 2; ++e)
+                        sum[nt][e] += P[x][0][e] + P[x][1][e];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        float y[2];
+                    for (int y = 0; y < NG; ++y)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            // a key that the row does not see adds nothing,
-                            // whatever its parameters are
-                            y[e] = P[t][e] * bf16_lo(pv[t][x]);
-                            const float z = fmaf(P[t][e], bf16_hi(pv[t][x]), pm[nt][x][e]);
-                            if (kMasked && !seen[t][e])
-                                y[e] = 0.f;
-                            else
-                                pm[nt][x][e] = z;
+                        for (int t = 0; t < 2; ++t) {
+                            float ps[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                // a key that the row does not see adds nothing,
+                                // whatever its parameters are
+                                ps[e] = P[x][t][e] * bf16_lo(pv[x][t][y]);
+                                const float z =
+                                    fmaf(P[x][t][e], bf16_hi(pv[x][t][y]), pm[nt][y][e]);
+                                if (kMasked && !seen[x][t][e])
+                                    ps[e] = 0.f;
+                                else
+                                    pm[nt][y][e] = z;
+                            }
+                            pf[x][nt][y][t] = transpose8x8(pack_f16(ps[0], ps[1]));
                         }
-                        pf[nt][x][t] = transpose8x8(pack_f16(y[0], y[1]));
-                    }
+                }
             }
 
             // O^T += V^T P^T: lane (g, c) holds its halves of tokens 2 c, 2 c + 1,
             // 2 c + 8, 2 c + 9; a half-word pair of two tokens is one A register
-            uint32_t v[4][D / 64];
+            uint32_t v[NC][4][D / 64];
+            constexpr int kUp = kVBases == 2 ? 8 * (D / 2) : 0;
+            load_values<NC, kCell, 0>(v, 0, at_V[0] + slot);
+            load_values<NC, kCell, 0>(v, 1, at_V[1] + slot);
+            load_values<NC, kCell, kUp>(v, 2, at_V[2 % kVBases] + slot);
+            load_values<NC, kCell, kUp>(v, 3, at_V[3 % kVBases] + slot);
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                load_shared<0>(v[x], at_V[x] + slot);
+            for (int x = 0; x < NC; ++x)
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-                const uint32_t sel = (q & 1) ? 0x7632 : 0x5410;
-                const uint32_t x = __byte_perm(v[0][q / 2], v[1][q / 2], sel);
-                const uint32_t y = __byte_perm(v[2][q / 2], v[3][q / 2], sel);
-                const uint32_t x8 = x >> 8, y8 = y >> 8;
-                const uint32_t a0[4] = {x & kLo, x & kHi, y & kLo, y & kHi};
-                const uint32_t a1[4] = {x8 & kLo, x8 & kHi, y8 & kLo, y8 & kHi};
+                for (int q = 0; q < D / 32; ++q) {
+                    const uint32_t sel = (q & 1) ? 0x7632 : 0x5410;
+                    const uint32_t u = __byte_perm(v[x][0][q / 2], v[x][1][q / 2], sel);
+                    const uint32_t y = __byte_perm(v[x][2][q / 2], v[x][3][q / 2], sel);
+                    const uint32_t u8 = u >> 8, y8 = y >> 8;
+                    const uint32_t a0[4] = {u & kLo, u & kHi, y & kLo, y & kHi};
+                    const uint32_t a1[4] = {u8 & kLo, u8 & kHi, y8 & kLo, y8 & kHi};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma(O[nt][2 * q], a0, pf[nt][32 * q / G][0], pf[nt][32 * q / G][1]);
-                    mma(O[nt][2 * q + 1], a1, pf[nt][32 * q / G][0], pf[nt][32 * q / G][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint32_t (&b)[2] = pf[x][nt][32 * q / G];
+                        mma(O[nt][2 * q], a0, b[0], b[1]);
+                        mma(O[nt][2 * q + 1], a1, b[0], b[1]);
+                    }
                 }
+        };
+        auto pair_step = [&](uint32_t slot, int tok, auto masked_tag) {
+            if constexpr (NT < 4) {
+                step(slot, tok, masked_tag, std::integral_constant<int, 2>{});
+            } else {
+                // the registers do not hold two cells of the widest tile
+                step(slot, tok, masked_tag, std::integral_constant<int, 1>{});
+                step(slot + kCell, tok + kv4::kCellTokens, masked_tag,
+                     std::integral_constant<int, 1>{});
             }
         };
 
-        // keys that some row of the tile sees, and that all rows see
-        const int tok_end = key_end(a, it, (it.tile * R + rows - 1) / grp);
-        const int all_end = key_end(a, it, it.tile * R / grp);
-        int tok = int(cur - it.first) * kBlock + warp * kv4::kCellTokens;
-        for (uint32_t k = cur - begin; k < stop - begin; ++k, tok += kBlock) {
-            if (!ptx::mbar_wait_warp(full + k % kStages, k / kStages & 1, &s_abort, a.err_word))
-                break;                     // the error is recorded, nothing is written
-            done = k + 1;
-            if (tok < tok_end && !(bad_pages && skipped(k))) {
-                const uint32_t slot = k % kStages * kCell;
-                if (tok + kv4::kCellTokens <= all_end)
-                    cell_step(slot, tok, std::false_type{});
-                else
-                    cell_step(slot, tok, std::true_type{});
-            }
-            __syncwarp();                  // every lane has read the cell
-            issue(k + kStages);
+        const int all_end = key_end(a, it, it.tile * R / grp);   // all rows see the keys below
+        int tok = int(cur - it.first) * kBlock + warp * kPair;
+        uint32_t k = cur - begin;
+        const uint32_t k_stop = stop - begin;
+        const int n_full = max(0, (all_end - kPair - tok + kBlock) / kBlock);
+        const uint32_t k_full = min(k_stop, k + uint32_t(n_full));
+        auto landed = [&] {                // else the error is recorded, nothing written
+            stuck = stuck || !ptx::mbar_wait_warp(full + k % kStages, k / kStages & 1, &s_abort,
+                                                  a.err_word);
+            done = stuck ? min(done, k) : done;
+            return !stuck;
+        };
+        for (; k < k_full && landed(); ++k, tok += kBlock) {
+            pair_step(k % kStages * (2 * kCell), tok, std::false_type{});
+            __syncwarp();                  // every lane has read the cells
+            fill(k + kStages);
+        }
+        for (; k < k_stop && landed(); ++k, tok += kBlock) {
+            if (tok < tok_end)
+                pair_step(k % kStages * (2 * kCell), tok, std::true_type{});
+            __syncwarp();
+            fill(k + kStages);
         }
 
         // ---- the warps' parts joined, and written ----------------------------
@@ -673,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                 }
             }
         __syncthreads();
-        const Item next = stop < end ? item_at(a, s_pre, s_len, grp, R, stop) : it;
+        const Item next = stop < end ? uniform(item_at(a, s_pre, grp, R, stop)) : it;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             // the upper warps' rows through shared memory into the lower warps'
@@ -707,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
                     }
                 } else if (half == 0 && nt == 0 && warp < NT && stop < end) {
                     // meanwhile the next item's queries
-                    load_queries<D, G, NT>(a, next, grp, warp, s_q[buf ^ 1]);
+                    load_queries<D, G, NT>(a, next, grp, warp, s_q);
                 }
                 __syncthreads();
             }
@@ -760,13 +858,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
         }
         cur = stop;
         it = next;
-        buf ^= 1;
     }
     if (s_abort) {
-        // a wait ran out: copies still on their way must land before the CTA ends
+        // a wait ran out: the copies under way must land before the CTA ends
         desc.parts = 0;
         volatile int go_on = 0;
-        for (uint32_t k = done; k < min(done + kStages, n_cells); ++k)
+        for (uint32_t k = done; k < min(done + kStages, n_blocks); ++k)
             ptx::mbar_wait_limited(full + k % kStages, k / kStages & 1, &go_on, a.err_word,
                                    kWaitTimeoutNs);
     }
@@ -774,39 +871,75 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kv4_kernel(con
         parts.desc[blockIdx.x] = desc;
 }
 
-// Joins the parts of the items that span CTAs: block (x, y) takes row y of the
-// item that begins in CTA x's range.  Parts are added in the order of the CTAs.
+// Joins the parts of the items that span CTAs: block x the item that begins in
+// CTA x's range and does not end there, a warp a row.  Lane l holds the weight of
+// one part of 32; the parts are added in the order of the CTAs, eight loads of O
+// under way at a time.
 template <int D, int R>
-__global__ void __launch_bounds__(D) attn_kv4_join_kernel(const Kv4AttnArgs a)
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_kv4_join_kernel(const Kv4AttnArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kPer = D / 32;
     const Parts parts = parts_of<R>(a.workspace);
     const Desc desc = parts.desc[blockIdx.x];
     if (desc.parts == 0)
         return;
     const int2 qb = queries_of(a, desc.b);
-    const int grp = a.H / a.Hkv, r = blockIdx.y, at = desc.tile * R + r;
+    const int grp = a.H / a.Hkv, lane = threadIdx.x & 31;
+    const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), at = desc.tile * R + r;
     if (at >= qb.y * grp)
         return;
-    const int x = threadIdx.x;
+    // the first part lies in its CTA's slot 1, the others in their CTAs' slot 0
+    auto place = [&](int p) { return (int64_t(2) * (blockIdx.x + p) + (p == 0)) * R + r; };
     float m = kNoRef;
-    for (int p = 0; p < desc.parts; ++p) {
-        const int slot = 2 * (blockIdx.x + p) + (p == 0);
-        m = fmaxf(m, parts.ml[slot * R + r].x);
-    }
-    float s = 0.f, y = 0.f;
-    for (int p = 0; p < desc.parts; ++p) {
-        const int slot = 2 * (blockIdx.x + p) + (p == 0);
-        const float2 ml = parts.ml[slot * R + r];
-        const float f = ptx::ex2(ml.x - m);
+    for (int p = lane; p < desc.parts; p += 32)
+        m = fmaxf(m, parts.ml[place(p)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float s = 0.f, y[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+        y[e] = 0.f;
+    for (int p0 = 0; p0 < desc.parts; p0 += 32) {
+        const int n = min(32, desc.parts - p0);
+        const float2 ml = lane < n ? parts.ml[place(p0 + lane)] : make_float2(m, 0.f);
+        const float f = lane < n ? ptx::ex2(ml.x - m) : 0.f;
         s = fmaf(ml.y, f, s);
-        y = fmaf(parts.O[(int64_t(slot) * R + r) * D + x], f, y);
+        for (int u0 = 0; u0 < n; u0 += 8) {
+            float v[8][kPer];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float *src =
+                    parts.O + place(p0 + min(u0 + u, n - 1)) * D + lane * kPer;
+#pragma unroll
+                for (int e = 0; e < kPer; e += 2) {
+                    const float2 z = *reinterpret_cast<const float2 *>(src + e);
+                    v[u][e] = z.x;
+                    v[u][e + 1] = z.y;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float g = __shfl_sync(0xffffffffu, f, (u0 + u) & 31);   // 0 behind the last
+                if (u0 + u < n)
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e)
+                        y[e] = fmaf(v[u][e], g, y[e]);
+            }
+        }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
     const int i = at / grp, h = desc.kvh * grp + at % grp;
     const bool any = s > 0.f || s != s;
-    static_cast<__nv_bfloat16 *>(a.O)[(int64_t(qb.x + i) * a.H + h) * D + x] =
-        __float2bfloat16_rn(any ? y / s : 0.f);
-    if (x == 0)
+    const float inv = any ? 1.f / s : 0.f;
+    auto *dst = static_cast<__nv_bfloat16 *>(a.O) + (int64_t(qb.x + i) * a.H + h) * D + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2)
+        *reinterpret_cast<uint32_t *>(dst + e) = ptx::pack_bf16x2(y[e] * inv, y[e + 1] * inv);
+    if (lane == 0)
         a.lse[a.cu_seqlens_q ? int64_t(h) * a.total_q + qb.x + i
                              : (int64_t(desc.b) * a.H + h) * a.Nq + i] =
             any ? (m + log2f(s)) * kLn2 : -INFINITY;
@@ -820,14 +953,13 @@ int launch(const Kv4AttnArgs &a, cudaStream_t stream)
     static PerDeviceOnce once;
     if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(attn_kv4_kernel<D, G, NT>), smem))
         return FA_ERR_CUDA;
-    // one CTA of the widest tile fits an SM (registers), two of the others
-    const int ctas = NT == 4 ? kKv4MaxCtas / 2 : kKv4MaxCtas;
+    constexpr int ctas = kv4_attention_ctas(R);
     attn_kv4_kernel<D, G, NT><<<ctas, kThreads, smem, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess)
         return FA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, R);
-    cfg.blockDim = dim3(D);
+    cfg.gridDim = dim3(ctas, R / kJoinWarps);
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

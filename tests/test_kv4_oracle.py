@@ -182,9 +182,9 @@ def test_attention_refusals_without_gpu():
     assert wb(1, 9, 2, 128) == fa.FA_ERR_BAD_SIZE
     assert wb(1, 8, 0, 128) == fa.FA_ERR_BAD_SIZE
     assert wb(1, 8, 2, 96) == fa.FA_ERR_UNSUPPORTED
-    # 304 descriptors, then two parts a CTA of 8, 16 or 32 rows
+    # a descriptor and two parts a CTA, of 8 rows (608 CTAs), 16 or 32 (304)
     for Nq, rows in ((1, 8), (2, 8), (3, 16), (4, 16), (5, 32), (500, 32)):
-        assert wb(Nq, 8, 2, 128) == 304 * 16 + 608 * rows * (8 + 512)
+        assert wb(Nq, 8, 2, 128) == (608 if rows == 8 else 304) * (16 + 2 * rows * (8 + 512))
 
     def go(q=256, qs=1024, cache=256, pages=4, ps=16, table=256, mp=2, lens=256, cu=None, o=256,
            lse=256, B=1, Nq=1, total=1, Nk=20, H=8, Hkv=2, d=128, group=64, ws=256, wsb=1 << 30):
