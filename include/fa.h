@@ -529,7 +529,8 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  *   fa_attention_kv4_workspace_bytes(Nq, H, Hkv, d) bytes; contents on entry
  *   are ignored.  Calls that may run at the same time need one each.
  * B <= 1024.  Results do not depend on timing: the same call gives the same
- * bits.  Two kernels on the library stream, no synchronisation.
+ * bits.  One or two kernels on the library stream, no
+ * synchronisation.
  * Errors: FA_ERR_BAD_SIZE (also a workspace that is too small, Nk above the
  * table, H no multiple of Hkv), FA_ERR_UNSUPPORTED (d, group, page_size),
  * FA_ERR_NULL_POINTER, FA_ERR_MISALIGNED, FA_ERR_TOO_LARGE, FA_ERR_NO_DEVICE,

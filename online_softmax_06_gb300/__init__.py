@@ -630,10 +630,25 @@ def attention_bwd(q, k, v, o, do, lse, causal: bool = False, scale: float | None
 
 # ---- 4-bit paged key/value cache ------------------------------------------------
 
-def _on(device):
-    """The tensors' device made current, for as long as the call takes."""
-    import torch
-    return torch.cuda.device(device)
+class _On:
+    """Makes a device current, and its current stream the library's, for one call."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, index: int):
+        import torch
+        self.guard = None
+        if torch.cuda.current_device() != index:
+            self.guard = torch.cuda.device(index)
+            self.guard.__enter__()
+        lib().fa_set_stream(torch._C._cuda_getCurrentRawStream(index))
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def kv4_cache(num_pages: int, kv_heads: int, page_size: int, d: int, group: int = 64,
@@ -713,8 +728,7 @@ def _kv4_rows(call, where, k, v, cache, page_table, seqlens, cu_seqlens, max_new
     else:
         total = k.shape[0]
         N = total if max_new is None else int(max_new)
-    with _on(cache.device):
-        _use_current_stream(cache.device)
+    with _On(cache.get_device()):
         rc = call(_ptr(k), _ptr(v), *strides, _ptr(cache), pages, page_size, _ptr(page_table),
                   max_pages, _ptr(seqlens), _ptr(cu_seqlens), B, N, total, hkv, d, group)
     _check(rc, where)
@@ -815,8 +829,7 @@ def attention_kv4(q, cache, page_table, seqlens, max_seqlen: int | None = None, 
     elif not (workspace.dtype == torch.uint8 and workspace.device == q.device
               and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-    with _on(q.device):
-        _use_current_stream(q.device)
+    with _On(q.get_device()):
         rc = fa_attention_kv4(_ptr(q), q_stride, _ptr(cache), pages, page_size, _ptr(page_table),
                               max_pages, _ptr(seqlens), _ptr(cu_seqlens), _ptr(out), _ptr(lse), B,
                               Nq, total, Nk, H, hkv, d, group, float(scale), int(bool(causal)),

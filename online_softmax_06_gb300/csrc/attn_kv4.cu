@@ -261,6 +261,16 @@ __device__ __forceinline__ int key_end(const Kv4AttnArgs &a, const Item &it, int
     return a.causal ? min(it.L, it.L - it.nq + i + 1) : it.L;
 }
 
+// The first item that begins at block x or after it.
+__device__ __forceinline__ uint32_t item_from(const Kv4AttnArgs &a, const uint32_t *s_pre, int grp,
+                                              int R, uint32_t x, uint32_t T)
+{
+    if (x >= T)
+        return T;
+    const Item it = uniform(item_at(a, s_pre, grp, R, x));
+    return it.first == x ? x : it.first + it.nb;
+}
+
 // The 8 query rows of n-tile nt as B fragments, by one warp.
 template <int D, int G, int NT>
 __device__ __forceinline__ void load_queries(const Kv4AttnArgs &a, const Item &it, int grp, int nt,
@@ -436,12 +446,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
     const uint32_t n_ctas = uint32_t(T < gridDim.x ? T : gridDim.x);
     const Parts parts = parts_of<R>(a.workspace);
     if (blockIdx.x >= n_ctas) {
-        if (tid == 0)
+        if (tid == 0 && !a.whole_items)
             parts.desc[blockIdx.x].parts = 0;
         return;
     }
-    const uint32_t begin = uint32_t(T * blockIdx.x / n_ctas);
-    const uint32_t end = uint32_t(T * (blockIdx.x + 1) / n_ctas);
+    uint32_t begin = uint32_t(T * blockIdx.x / n_ctas);
+    uint32_t end = uint32_t(T * (blockIdx.x + 1) / n_ctas);
+    if (a.whole_items) {                   // the items that begin in the range
+        begin = item_from(a, s_pre, grp, R, begin, uint32_t(T));
+        end = item_from(a, s_pre, grp, R, end, uint32_t(T));
+        if (begin >= end)
+            return;
+    }
     Desc desc{0, 0, 0, 0};
 
     // ---- copies ------------------------------------------------------------------
@@ -867,51 +883,62 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
             ptx::mbar_wait_limited(full + k % kStages, k / kStages & 1, &go_on, a.err_word,
                                    kWaitTimeoutNs);
     }
-    if (tid == 0)
+    if (tid == 0 && !a.whole_items)
         parts.desc[blockIdx.x] = desc;
 }
 
-// Joins the parts of the items that span CTAs: block x the item that begins in
-// CTA x's range and does not end there, a warp a row.  Lane l holds the weight of
-// one part of 32; the parts are added in the order of the CTAs, eight loads of O
-// under way at a time.
-template <int D, int R>
+// Joins the parts of the items that span CTAs: blocks (x, *) the item that begins
+// in CTA x's range and does not end there, kPart warps a row.  The warps of a row
+// take every kPart-th part, eight loads of O under way at a time, and their sums
+// are added in the order of the warps.  Few items have many parts each and take
+// 8 warps a row (1 x 130001 keys, 76 parts: 28 us with one, 7 with eight); many
+// items have a few and take one (64 x 8 items: 6 us, with eight 10).
+template <int D, int R, int kPart>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_kv4_join_kernel(const Kv4AttnArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int kPer = D / 32;
+    constexpr int kRows = kJoinWarps / kPart;      // of a block
+    __shared__ float s_y[kJoinWarps][D], s_m[kJoinWarps], s_s[kJoinWarps];
     const Parts parts = parts_of<R>(a.workspace);
     const Desc desc = parts.desc[blockIdx.x];
     if (desc.parts == 0)
         return;
     const int2 qb = queries_of(a, desc.b);
-    const int grp = a.H / a.Hkv, lane = threadIdx.x & 31;
-    const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), at = desc.tile * R + r;
-    if (at >= qb.y * grp)
+    const int grp = a.H / a.Hkv, all = qb.y * grp, row0 = desc.tile * R + blockIdx.y * kRows;
+    if (row0 >= all)
         return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y * kRows + warp / kPart;
     // the first part lies in its CTA's slot 1, the others in their CTAs' slot 0
     auto place = [&](int p) { return (int64_t(2) * (blockIdx.x + p) + (p == 0)) * R + r; };
-    float m = kNoRef;
-    for (int p = lane; p < desc.parts; p += 32)
-        m = fmaxf(m, parts.ml[place(p)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float s = 0.f, y[kPer];
+    // lane l: reference and sum of the warp's l-th part of 32
+    float m = kNoRef, s = 0.f, y[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e)
         y[e] = 0.f;
-    for (int p0 = 0; p0 < desc.parts; p0 += 32) {
-        const int n = min(32, desc.parts - p0);
-        const float2 ml = lane < n ? parts.ml[place(p0 + lane)] : make_float2(m, 0.f);
-        const float f = lane < n ? ptx::ex2(ml.x - m) : 0.f;
-        s = fmaf(ml.y, f, s);
+    const int n_parts = desc.tile * R + r < all ? desc.parts : 0;
+    for (int p0 = warp % kPart; p0 < n_parts; p0 += 32 * kPart) {
+        const int n = min(32, (n_parts - p0 + kPart - 1) / kPart);
+        float2 ml = make_float2(kNoRef, 0.f);
+        if (lane < n)
+            ml = parts.ml[place(p0 + lane * kPart)];
+        float top = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top, m);
+        const float old = ptx::ex2(m - top), f = lane < n ? ptx::ex2(ml.x - top) : 0.f;
+        m = top;
+        s = fmaf(ml.y, f, s * old);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            y[e] *= old;
         for (int u0 = 0; u0 < n; u0 += 8) {
             float v[8][kPer];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 const float *src =
-                    parts.O + place(p0 + min(u0 + u, n - 1)) * D + lane * kPer;
+                    parts.O + place(p0 + min(u0 + u, n - 1) * kPart) * D + lane * kPer;
 #pragma unroll
                 for (int e = 0; e < kPer; e += 2) {
                     const float2 z = *reinterpret_cast<const float2 *>(src + e);
@@ -921,28 +948,50 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_kv4_join_kernel(const Kv
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const float g = __shfl_sync(0xffffffffu, f, (u0 + u) & 31);   // 0 behind the last
+                const float w = __shfl_sync(0xffffffffu, f, (u0 + u) & 31);
                 if (u0 + u < n)
 #pragma unroll
                     for (int e = 0; e < kPer; ++e)
-                        y[e] = fmaf(v[u][e], g, y[e]);
+                        y[e] = fmaf(v[u][e], w, y[e]);
             }
         }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         s += __shfl_xor_sync(0xffffffffu, s, o);
-    const int i = at / grp, h = desc.kvh * grp + at % grp;
-    const bool any = s > 0.f || s != s;
-    const float inv = any ? 1.f / s : 0.f;
-    auto *dst = static_cast<__nv_bfloat16 *>(a.O) + (int64_t(qb.x + i) * a.H + h) * D + lane * kPer;
 #pragma unroll
-    for (int e = 0; e < kPer; e += 2)
-        *reinterpret_cast<uint32_t *>(dst + e) = ptx::pack_bf16x2(y[e] * inv, y[e + 1] * inv);
-    if (lane == 0)
-        a.lse[a.cu_seqlens_q ? int64_t(h) * a.total_q + qb.x + i
-                             : (int64_t(desc.b) * a.H + h) * a.Nq + i] =
-            any ? (m + log2f(s)) * kLn2 : -INFINITY;
+    for (int e = 0; e < kPer; ++e)
+        s_y[warp][lane * kPer + e] = y[e];
+    if (lane == 0) {
+        s_m[warp] = m;
+        s_s[warp] = s;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < kRows * D; e += kJoinWarps * 32) {
+        const int w0 = e / D * kPart, x = e % D, at = row0 + e / D;
+        if (at >= all)
+            break;
+        m = s_m[w0];
+#pragma unroll
+        for (int w = 1; w < kPart; ++w)
+            m = fmaxf(m, s_m[w0 + w]);
+        s = 0.f;
+        float o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kPart; ++w) {
+            const float f = ptx::ex2(s_m[w0 + w] - m);
+            s = fmaf(s_s[w0 + w], f, s);
+            o = fmaf(s_y[w0 + w][x], f, o);
+        }
+        const int i = at / grp, h = desc.kvh * grp + at % grp;
+        const bool any = s > 0.f || s != s;
+        static_cast<__nv_bfloat16 *>(a.O)[(int64_t(qb.x + i) * a.H + h) * D + x] =
+            __float2bfloat16_rn(any ? o / s : 0.f);
+        if (x == 0)
+            a.lse[a.cu_seqlens_q ? int64_t(h) * a.total_q + qb.x + i
+                                 : (int64_t(desc.b) * a.H + h) * a.Nq + i] =
+                any ? (m + log2f(s)) * kLn2 : -INFINITY;
+    }
 }
 
 template <int D, int G, int NT>
@@ -958,7 +1007,13 @@ int launch(const Kv4AttnArgs &a, cudaStream_t stream)
     if (cudaGetLastError() != cudaSuccess)
         return FA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, R / kJoinWarps);
+    if (a.whole_items)
+        return FA_OK;                      // no parts
+    const int64_t all_rows = int64_t(a.Nq) * (a.H / a.Hkv), items = int64_t(a.B) * a.Hkv *
+                                                                  ((all_rows + R - 1) / R);
+    const int rows = int(all_rows < R ? all_rows : R);
+    const bool few = 16 * items <= ctas;
+    cfg.gridDim = dim3(ctas, few ? rows : (rows + kJoinWarps - 1) / kJoinWarps);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -966,7 +1021,8 @@ int launch(const Kv4AttnArgs &a, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_kv4_join_kernel<D, R>, a);
+    const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, attn_kv4_join_kernel<D, R, kJoinWarps>, a)
+                              : cudaLaunchKernelEx(&cfg, attn_kv4_join_kernel<D, R, 1>, a);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

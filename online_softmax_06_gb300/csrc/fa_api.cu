@@ -929,6 +929,7 @@ int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num
     a.scale = scale;
     a.causal = causal ? 1 : 0;
     a.workspace = workspace;
+    a.whole_items = Nk <= fa::kKv4Short;
     a.err_word = dev->err_word;
     return fa::launch_attention_kv4(a, fa::t_stream);
 }

@@ -193,9 +193,11 @@ struct Kv4AttnArgs {
     int H, Hkv, d, group;
     float scale;
     int causal;
-    void *workspace;
+    void *workspace;           // not used with whole_items
+    int whole_items;           // Nk <= kKv4Short
     int *err_word;
 };
+constexpr int kKv4Short = 1024;    // keys up to which a CTA takes a sequence's head whole
 constexpr int kKv4MaxSeqs = 1024;  // each CTA lays the sequences' work out in shared memory
 // Query rows (queries x heads of a kv head) that a CTA takes at once.
 inline int kv4_attention_rows(int Nq, int H, int Hkv)
