@@ -526,8 +526,8 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  *   sequence's end, or at keys that a query does not see, does not reach its
  *   result, NaN or not.
  *   workspace: DEVICE scratch owned by the caller, 256-byte aligned, at least
- *   fa_attention_kv4_workspace_bytes(Nq, H, Hkv, d) bytes; contents on entry
- *   are ignored.  Calls that may run at the same time need one each.
+ *   fa_attention_kv4_workspace_bytes(Nq, Nk, H, Hkv, d) bytes; contents on
+ *   entry are ignored.  Calls that may run at the same time need one each.
  * B <= 1024.  Results do not depend on timing: the same call gives the same
  * bits.  One or two kernels on the library stream, no
  * synchronisation.
@@ -543,8 +543,9 @@ FA_API int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, 
                             int d, int group, float scale, int causal, void *workspace,
                             int64_t workspace_bytes);
 
-/* Workspace bytes fa_attention_kv4 needs, or a negative FA_ERR_* code. */
-FA_API int64_t fa_attention_kv4_workspace_bytes(int Nq, int H, int Hkv, int d);
+/* Workspace bytes fa_attention_kv4 needs (0 with Nk <= 1024: the workspace may be
+ * NULL then), or a negative FA_ERR_* code. */
+FA_API int64_t fa_attention_kv4_workspace_bytes(int Nq, int Nk, int H, int Hkv, int d);
 
 /*
  * Exact attention forward in fp32 throughout (fp32 Q, K, V, O, lse), on the

@@ -114,7 +114,7 @@ def lib():
         L.fa_kv4_read.argtypes = L.fa_kv4_append.argtypes
         L.fa_attention_kv4.argtypes = [vp, i64, vp, i32, i32, vp, i32, vp, vp, vp, vp, i32, i32,
                                        i64, i32, i32, i32, i32, i32, f32, i32, vp, i64]
-        L.fa_attention_kv4_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.fa_attention_kv4_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
         L.fa_attention_kv4_workspace_bytes.restype = i64
         L.fa_set_stream.argtypes = [vp]
         L.fa_get_stream.argtypes = []
@@ -280,8 +280,8 @@ def fa_attention_kv4(q, q_stride, cache, num_pages, page_size, page_table, max_p
                                   group, scale, causal, workspace, workspace_bytes)
 
 
-def fa_attention_kv4_workspace_bytes(Nq, H, Hkv, d) -> int:
-    return lib().fa_attention_kv4_workspace_bytes(Nq, H, Hkv, d)
+def fa_attention_kv4_workspace_bytes(Nq, Nk, H, Hkv, d) -> int:
+    return lib().fa_attention_kv4_workspace_bytes(Nq, Nk, H, Hkv, d)
 
 
 def fa_set_stream(stream_ptr) -> int:
@@ -635,8 +635,7 @@ class _On:
 
     __slots__ = ("guard",)
 
-    def __init__(self, index: int):
-        import torch
+    def __init__(self, torch, index: int):
         self.guard = None
         if torch.cuda.current_device() != index:
             self.guard = torch.cuda.device(index)
@@ -651,6 +650,74 @@ class _On:
             self.guard.__exit__(*exc)
 
 
+# What the shapes and strides of a call's tensors say, checked once for each set of
+# them: a decode step is short enough for the checks to show.
+_kv4_plans: dict = {}
+
+
+def _kv4_plan(key, make, *args):
+    plan = _kv4_plans.get(key)
+    if plan is None:
+        plan = make(*args)
+        if len(_kv4_plans) >= 1024:
+            _kv4_plans.clear()
+        _kv4_plans[key] = plan
+    return plan
+
+
+def _kv4_check(torch, rows, cache, page_table, seqlens, cu_seqlens):
+    """The tensors' types, devices and contiguity; returns the device's index."""
+    index = cache.get_device()
+    if index < 0 or cache.dtype is not torch.uint8 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 CUDA tensor [pages, kv_heads, bytes]")
+    for t in rows:
+        if t.dtype is not torch.bfloat16 or t.get_device() != index:
+            raise ValueError("q, k and v must be bf16 tensors on the cache's device")
+    for t in (page_table, seqlens) if cu_seqlens is None else (page_table, seqlens, cu_seqlens):
+        if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous():
+            raise ValueError("page_table, seqlens and cu_seqlens must be contiguous int32 tensors "
+                             "on the cache's device")
+    return index
+
+
+def _kv4_format(cache, page_table, seqlens, cu, d, group):
+    """(num_pages, Hkv, page_size, B, max_pages) from the shapes."""
+    if d not in (64, 128) or group not in (32, 64, 128) or group > d:
+        raise FaError(FA_ERR_UNSUPPORTED, "kv4: d, group")
+    if len(cache) != 3:
+        raise ValueError("cache must be [pages, kv_heads, bytes]")
+    pages, hkv, nbytes = cache
+    page_size, rest = divmod(nbytes, d + 8 * (d // group))
+    if rest or page_size == 0 or page_size % 16:
+        raise ValueError(f"cache has pages of {nbytes} bytes a head: not a whole number of cells "
+                         f"for d = {d}, group = {group}")
+    if len(seqlens) != 1 or len(page_table) != 2 or page_table[0] != seqlens[0]:
+        raise ValueError("seqlens must be [B], page_table [B, max_pages]")
+    B = seqlens[0]
+    if cu is not None and tuple(cu) != (B + 1,):
+        raise ValueError(f"cu_seqlens must be [{B + 1}] for {B} sequences")
+    return pages, hkv, page_size, B, page_table[1]
+
+
+def _row_stride(shape, stride, name):
+    """Elements between the token rows of a tensor [B, N, heads, d] or [total, heads, d]."""
+    heads, d = shape[-2:]
+    n = 1
+    for s in shape[:-2]:
+        n *= s
+    if n * heads * d == 0:
+        return heads * d
+    if (d > 1 and stride[-1] != 1) or (heads > 1 and stride[-2] != d):
+        raise ValueError(f"a token's heads must be contiguous in {name}")
+    if n == 1:                             # one row: any distance will do
+        return heads * d
+    if len(shape) == 3 or shape[1] == 1:
+        return stride[0]
+    if shape[0] > 1 and stride[0] != shape[1] * stride[1]:
+        raise ValueError(f"{name}'s rows must be evenly spaced")
+    return stride[1]
+
+
 def kv4_cache(num_pages: int, kv_heads: int, page_size: int, d: int, group: int = 64,
               device="cuda"):
     """An empty 4-bit cache: a uint8 tensor [num_pages, kv_heads, page bytes].
@@ -663,75 +730,39 @@ def kv4_cache(num_pages: int, kv_heads: int, page_size: int, d: int, group: int 
     return torch.empty((num_pages, kv_heads, nbytes), dtype=torch.uint8, device=device)
 
 
-def _kv4_args(cache, page_table, seqlens, cu_seqlens, d, group):
-    """The checked cache arguments: (num_pages, Hkv, page_size, B, max_pages)."""
-    import torch
-    if not (cache.is_cuda and cache.dtype == torch.uint8 and cache.dim() == 3
-            and cache.is_contiguous()):
-        raise ValueError("cache must be a contiguous uint8 CUDA tensor [pages, kv_heads, bytes]")
-    if d not in (64, 128) or group not in (32, 64, 128) or group > d:
-        raise FaError(FA_ERR_UNSUPPORTED, "kv4: d, group")
-    pages, hkv, nbytes = cache.shape
-    page_size, rest = divmod(nbytes, d + 8 * (d // group))
-    if rest or page_size == 0 or page_size % 16:
-        raise ValueError(f"cache has pages of {nbytes} bytes a head: not a whole number of cells "
-                         f"for d = {d}, group = {group}")
-    B = seqlens.numel()
-    for name, t, shape in (("page_table", page_table, None), ("seqlens", seqlens, (B,)),
-                           ("cu_seqlens", cu_seqlens, (B + 1,))):
-        if t is None:
-            continue
-        if not (t.dtype == torch.int32 and t.device == cache.device and t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous int32 tensor on the cache's device")
-        if (t.dim() != 2 or t.shape[0] != B) if shape is None else tuple(t.shape) != shape:
-            raise ValueError(f"{name} has the wrong shape for {B} sequences")
-    return pages, hkv, page_size, B, page_table.shape[1]
-
-
-def _row_stride(t, heads, d, name):
-    """Elements between the token rows of t ([B, N, heads, d] or [total, heads, d])."""
-    st = t.stride()
-    if t.numel() <= heads * d:             # one row: any distance will do
-        if t.numel() and not t.is_contiguous():
-            raise ValueError(f"a token's heads must be contiguous in {name}")
-        return heads * d
-    if st[-1] != 1 or (heads > 1 and st[-2] != d):
-        raise ValueError(f"a token's heads must be contiguous in {name}")
-    if t.dim() == 3:
-        return st[0]
-    if t.shape[1] == 1:
-        return st[0]
-    if t.shape[0] > 1 and st[0] != t.shape[1] * st[1]:
-        raise ValueError(f"{name}'s rows must be evenly spaced")
-    return st[1]
+def _plan_rows(k, ks, v, vs, cache, page_table, seqlens, cu, max_new, group):
+    if k != v:
+        raise ValueError("k and v must have one shape")
+    if len(k) != (4 if cu is None else 3):
+        raise ValueError("k and v must be [B, N, kv_heads, d], or [total, kv_heads, d] with "
+                         "cu_seqlens")
+    pages, hkv, page_size, B, max_pages = _kv4_format(cache, page_table, seqlens, cu, k[-1], group)
+    if k[-2] != hkv:
+        raise ValueError(f"k and v have {k[-2]} heads, the cache {hkv}")
+    if cu is None:
+        if k[0] != B:
+            raise ValueError(f"k and v hold {k[0]} sequences, seqlens {B}")
+        N, total = k[1], B * k[1]
+    else:
+        total = k[0]
+        N = total if max_new is None else int(max_new)
+    return (_row_stride(k, ks, "k"), _row_stride(v, vs, "v"), pages, page_size, max_pages, B, N,
+            total, hkv, k[-1])
 
 
 def _kv4_rows(call, where, k, v, cache, page_table, seqlens, cu_seqlens, max_new, group):
     import torch
-    if not (k.dtype == v.dtype == torch.bfloat16 and k.shape == v.shape
-            and k.device == v.device == cache.device):
-        raise ValueError("k and v must be bf16 tensors of one shape on the cache's device")
-    if k.dim() != (4 if cu_seqlens is None else 3):
-        raise ValueError("k and v must be [B, N, kv_heads, d], or [total, kv_heads, d] with "
-                         "cu_seqlens")
-    hk, d = k.shape[-2:]
-    pages, hkv, page_size, B, max_pages = _kv4_args(cache, page_table, seqlens, cu_seqlens, d,
-                                                    group)
-    if hk != hkv:
-        raise ValueError(f"k and v have {hk} heads, the cache {hkv}")
-    strides = _row_stride(k, hkv, d, "k"), _row_stride(v, hkv, d, "v")
-    if cu_seqlens is None:
-        if k.shape[0] != B:
-            raise ValueError(f"k and v hold {k.shape[0]} sequences, seqlens {B}")
-        N = k.shape[1]
-        total = B * N
-    else:
-        total = k.shape[0]
-        N = total if max_new is None else int(max_new)
-    with _On(cache.get_device()):
-        rc = call(_ptr(k), _ptr(v), *strides, _ptr(cache), pages, page_size, _ptr(page_table),
-                  max_pages, _ptr(seqlens), _ptr(cu_seqlens), B, N, total, hkv, d, group)
-    _check(rc, where)
+    index = _kv4_check(torch, (k, v), cache, page_table, seqlens, cu_seqlens)
+    cu = None if cu_seqlens is None else cu_seqlens.shape
+    key = (k.shape, k.stride(), v.shape, v.stride(), cache.shape, page_table.shape, seqlens.shape,
+           cu, max_new, group)
+    ks, vs, pages, page_size, max_pages, B, N, total, hkv, d = _kv4_plan(key, _plan_rows, *key)
+    with _On(torch, index):
+        rc = call(k.data_ptr(), v.data_ptr(), ks, vs, cache.data_ptr(), pages, page_size,
+                  page_table.data_ptr(), max_pages, seqlens.data_ptr(),
+                  None if cu is None else cu_seqlens.data_ptr(), B, N, total, hkv, d, group)
+    if rc != FA_OK:
+        raise FaError(rc, where)
 
 
 def kv4_append(k, v, cache, page_table, seqlens, cu_seqlens=None, max_new: int | None = None,
@@ -774,6 +805,29 @@ def kv4_read(cache, page_table, seqlens, total: int | None = None, d: int = 128,
     return k, v
 
 
+def _plan_attention(q, qs, cache, page_table, seqlens, cu, max_q, max_seqlen, group):
+    if len(q) != (4 if cu is None else 3):
+        raise ValueError("q must be [B, Nq, H, d], or [total, H, d] with cu_seqlens")
+    H, d = q[-2:]
+    pages, hkv, page_size, B, max_pages = _kv4_format(cache, page_table, seqlens, cu, d, group)
+    if hkv == 0 or H % hkv:
+        raise ValueError(f"{H} query heads on {hkv} kv heads")
+    if cu is None:
+        if q[0] != B:
+            raise ValueError(f"q holds {q[0]} sequences, seqlens {B}")
+        Nq, total = q[1], B * q[1]
+        lse_shape = (B, H, Nq)
+    else:
+        total = q[0]
+        Nq = total if max_q is None else int(max_q)
+        lse_shape = (H, total)
+    Nk = max_pages * page_size if max_seqlen is None else int(max_seqlen)
+    nbytes = fa_attention_kv4_workspace_bytes(Nq, Nk, H, hkv, d)
+    _check(int(min(nbytes, 0)), "fa_attention_kv4_workspace_bytes")
+    return (_row_stride(q, qs, "q"), pages, page_size, max_pages, B, Nq, total, Nk, H, hkv, d,
+            lse_shape, nbytes)
+
+
 def attention_kv4(q, cache, page_table, seqlens, max_seqlen: int | None = None, group: int = 64,
                   causal: bool = True, scale: float | None = None, cu_seqlens=None,
                   max_q: int | None = None, out=None, lse=None, workspace=None):
@@ -789,52 +843,38 @@ def attention_kv4(q, cache, page_table, seqlens, max_seqlen: int | None = None, 
     here (torch) unless given (uint8, fa_attention_kv4_workspace_bytes).
     """
     import torch
-    if q.dtype != torch.bfloat16 or q.device != cache.device:
-        raise ValueError("q must be a bf16 tensor on the cache's device")
-    if q.dim() != (4 if cu_seqlens is None else 3):
-        raise ValueError("q must be [B, Nq, H, d], or [total, H, d] with cu_seqlens")
-    H, d = q.shape[-2:]
-    pages, hkv, page_size, B, max_pages = _kv4_args(cache, page_table, seqlens, cu_seqlens, d,
-                                                    group)
-    if hkv == 0 or H % hkv:
-        raise ValueError(f"{H} query heads on {hkv} kv heads")
-    q_stride = _row_stride(q, H, d, "q")
-    if cu_seqlens is None:
-        if q.shape[0] != B:
-            raise ValueError(f"q holds {q.shape[0]} sequences, seqlens {B}")
-        Nq = q.shape[1]
-        total = B * Nq
-        lse_shape = (B, H, Nq)
-    else:
-        total = q.shape[0]
-        Nq = total if max_q is None else int(max_q)
-        lse_shape = (H, total)
-    Nk = max_pages * page_size if max_seqlen is None else int(max_seqlen)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    index = _kv4_check(torch, (q,), cache, page_table, seqlens, cu_seqlens)
+    cu = None if cu_seqlens is None else cu_seqlens.shape
+    key = (q.shape, q.stride(), cache.shape, page_table.shape, seqlens.shape, cu, max_q,
+           max_seqlen, group)
+    (q_stride, pages, page_size, max_pages, B, Nq, total, Nk, H, hkv, d, lse_shape,
+     nbytes) = _kv4_plan(key, _plan_attention, *key)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif not (out.shape == q.shape and out.dtype == q.dtype and out.device == q.device
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    elif not (out.shape == q.shape and out.dtype is torch.bfloat16 and out.get_device() == index
               and out.is_contiguous()):
         raise ValueError("out must be a contiguous tensor like q")
     if lse is None:
         lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
-    elif not (tuple(lse.shape) == lse_shape and lse.dtype == torch.float32
-              and lse.device == q.device and lse.is_contiguous()):
+    elif not (tuple(lse.shape) == lse_shape and lse.dtype is torch.float32
+              and lse.get_device() == index and lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous float32 tensor {list(lse_shape)}")
-    nbytes = fa_attention_kv4_workspace_bytes(Nq, H, hkv, d)
-    _check(int(min(nbytes, 0)), "fa_attention_kv4_workspace_bytes")
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    elif not (workspace.dtype == torch.uint8 and workspace.device == q.device
+        if nbytes > 0:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    elif not (workspace.dtype is torch.uint8 and workspace.get_device() == index
               and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-    with _On(q.get_device()):
-        rc = fa_attention_kv4(_ptr(q), q_stride, _ptr(cache), pages, page_size, _ptr(page_table),
-                              max_pages, _ptr(seqlens), _ptr(cu_seqlens), _ptr(out), _ptr(lse), B,
-                              Nq, total, Nk, H, hkv, d, group, float(scale), int(bool(causal)),
-                              _ptr(workspace), workspace.numel())
-    _check(rc, "fa_attention_kv4")
+    ws, n_ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    with _On(torch, index):
+        rc = fa_attention_kv4(q.data_ptr(), q_stride, cache.data_ptr(), pages, page_size,
+                              page_table.data_ptr(), max_pages, seqlens.data_ptr(),
+                              None if cu is None else cu_seqlens.data_ptr(), out.data_ptr(),
+                              lse.data_ptr(), B, Nq, total, Nk, H, hkv, d, group,
+                              1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0,
+                              ws, n_ws)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_attention_kv4")
     return out, lse
 
 

@@ -545,12 +545,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
                     pm[nt][x][e] = 0.f;
             }
         }
-        // NC cells' keys, from token `tok` on.  kMasked: some query row of the tile
+        // The keys of a pair of cells, from token `tok` on.  kMasked: some query row of the tile
         // does not see all of them, or the sequence ends among them.
         const int tok_end = key_end(a, it, (it.tile * R + rows - 1) / grp);
-        auto step = [&](uint32_t slot, int tok, auto masked_tag, auto cells_tag) {
+        auto step = [&](uint32_t slot, int tok, auto masked_tag) {
             constexpr bool kMasked = decltype(masked_tag)::value;
-            constexpr int NC = decltype(cells_tag)::value;
+            constexpr int NC = 2;
             constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
             // S^T = K Q^T: lane (g, c) holds tokens g, g + 8 of each cell
             uint32_t kw[NC][2][NJ];
@@ -730,17 +730,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
                     }
                 }
         };
-        auto pair_step = [&](uint32_t slot, int tok, auto masked_tag) {
-            if constexpr (NT < 4) {
-                step(slot, tok, masked_tag, std::integral_constant<int, 2>{});
-            } else {
-                // the registers do not hold two cells of the widest tile
-                step(slot, tok, masked_tag, std::integral_constant<int, 1>{});
-                step(slot + kCell, tok + kv4::kCellTokens, masked_tag,
-                     std::integral_constant<int, 1>{});
-            }
-        };
-
         const int all_end = key_end(a, it, it.tile * R / grp);   // all rows see the keys below
         int tok = int(cur - it.first) * kBlock + warp * kPair;
         uint32_t k = cur - begin;
@@ -754,13 +743,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
             return !stuck;
         };
         for (; k < k_full && landed(); ++k, tok += kBlock) {
-            pair_step(k % kStages * (2 * kCell), tok, std::false_type{});
+            step(k % kStages * (2 * kCell), tok, std::false_type{});
             __syncwarp();                  // every lane has read the cells
             fill(k + kStages);
         }
         for (; k < k_stop && landed(); ++k, tok += kBlock) {
             if (tok < tok_end)
-                pair_step(k % kStages * (2 * kCell), tok, std::true_type{});
+                step(k % kStages * (2 * kCell), tok, std::true_type{});
             __syncwarp();
             fill(k + kStages);
         }
@@ -1029,11 +1018,11 @@ int launch(const Kv4AttnArgs &a, cudaStream_t stream)
 template <int D, int G>
 int launch_rows(const Kv4AttnArgs &a, cudaStream_t stream)
 {
-    switch (kv4_attention_rows(a.Nq, a.H, a.Hkv)) {
-    case 8: return launch<D, G, 1>(a, stream);
-    case 16: return launch<D, G, 2>(a, stream);
-    default: return launch<D, G, 4>(a, stream);
-    }
+    // Rows beyond 16 go on as further tiles, whose keys come from L2 the second
+    // time: 32 rows a tile spill their registers (16 sequences x 4 queries x 8
+    // heads a kv head: 102 us, against 77 with two tiles of 16).
+    return kv4_attention_rows(a.Nq, a.H, a.Hkv) == 8 ? launch<D, G, 1>(a, stream)
+                                                     : launch<D, G, 2>(a, stream);
 }
 
 }  // namespace

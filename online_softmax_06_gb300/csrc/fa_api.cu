@@ -859,13 +859,13 @@ int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, const void
                         max_pages, seqlens, cu_seqlens, B, N, total, Hkv, d, group, false);
 }
 
-int64_t fa_attention_kv4_workspace_bytes(int Nq, int H, int Hkv, int d)
+int64_t fa_attention_kv4_workspace_bytes(int Nq, int Nk, int H, int Hkv, int d)
 {
-    if (Nq < 0 || H < 0 || Hkv < 0 || (H > 0 && (Hkv == 0 || H % Hkv != 0)))
+    if (Nq < 0 || Nk < 0 || H < 0 || Hkv < 0 || (H > 0 && (Hkv == 0 || H % Hkv != 0)))
         return FA_ERR_BAD_SIZE;
     if (d != 64 && d != 128)
         return FA_ERR_UNSUPPORTED;
-    return H == 0 ? 0 : fa::kv4_attention_workspace_bytes(Nq, H, Hkv, d);
+    return H == 0 ? 0 : fa::kv4_attention_workspace_bytes(Nq, Nk, H, Hkv, d);
 }
 
 int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num_pages,
@@ -885,10 +885,11 @@ int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num
     if (B == 0 || Nq == 0 || total_q == 0 || H == 0)
         return FA_OK;
     // with Nk = 0 nothing of the cache is read
-    if (!Q || !seqlens || !O || !lse || !workspace || (Nk > 0 && (!cache || !page_table)))
+    const int64_t needs = fa::kv4_attention_workspace_bytes(Nq, Nk, H, Hkv, d);
+    if (!Q || !seqlens || !O || !lse || (needs > 0 && !workspace) ||
+        (Nk > 0 && (!cache || !page_table)))
         return FA_ERR_NULL_POINTER;
-    if (q_stride < int64_t(H) * d ||
-        workspace_bytes < fa::kv4_attention_workspace_bytes(Nq, H, Hkv, d))
+    if (q_stride < int64_t(H) * d || workspace_bytes < needs)
         return FA_ERR_BAD_SIZE;
     if (!fa::aligned(Q, 16) || !fa::aligned(O, 16) || !fa::aligned(cache, 16) ||
         !fa::aligned(lse, 4) || !fa::aligned(page_table, 4) || !fa::aligned(seqlens, 4) ||

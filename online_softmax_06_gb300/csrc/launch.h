@@ -202,15 +202,16 @@ constexpr int kKv4MaxSeqs = 1024;  // each CTA lays the sequences' work out in s
 // Query rows (queries x heads of a kv head) that a CTA takes at once.
 inline int kv4_attention_rows(int Nq, int H, int Hkv)
 {
-    const int64_t rows = int64_t(Nq) * (H / Hkv);
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    return int64_t(Nq) * (H / Hkv) <= 8 ? 8 : 16;
 }
 // CTAs: four on each of 152 SMs, two with the wider tiles' registers.
 __host__ __device__ constexpr int kv4_attention_ctas(int rows) { return rows <= 8 ? 608 : 304; }
 // Descriptors (16 bytes a CTA), then for two parts a CTA the (reference, sum)
 // and the fp32 O of each row.
-inline int64_t kv4_attention_workspace_bytes(int Nq, int H, int Hkv, int d)
+inline int64_t kv4_attention_workspace_bytes(int Nq, int Nk, int H, int Hkv, int d)
 {
+    if (Nk <= kKv4Short)
+        return 0;
     const int rows = kv4_attention_rows(Nq, H, Hkv);
     return int64_t(kv4_attention_ctas(rows)) * (16 + 2 * rows * (8 + 4 * d));
 }

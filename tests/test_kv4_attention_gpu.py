@@ -256,13 +256,20 @@ def test_fused_query_rows_and_given_buffers():
     cache, table, sl = torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table), gpu_i32([100, 40])
     out = torch.empty(2, 3, 4, 128, dtype=torch.bfloat16, device="cuda")
     l = torch.empty(2, 4, 3, device="cuda")
-    ws = torch.full((fa.fa_attention_kv4_workspace_bytes(3, 4, 2, 128),), 0xff, dtype=torch.uint8,
-                    device="cuda")
-    o2, l2 = fa.attention_kv4(fused[:, :, :4], cache, table, sl, out=out, lse=l, workspace=ws,
-                              max_seqlen=100)
+    o2, l2 = fa.attention_kv4(fused[:, :, :4], cache, table, sl, out=out, lse=l, max_seqlen=100)
     assert o2 is out and l2 is l
     assert torch.equal(out.reshape(-1, 4, 128), O)
     assert torch.equal(l.transpose(0, 1).reshape(4, -1), lse)
+    # a workspace full of anything
+    pool, q = make([3000, 40], 3, 4, 2, 128, 64, 32, seed=171)
+    O, lse = run(pool, q, True, False)
+    check(pool, q, O, lse, 1 / math.sqrt(128), True)
+    ws = torch.full((fa.fa_attention_kv4_workspace_bytes(3, 3000, 4, 2, 128),), 0xff,
+                    dtype=torch.uint8, device="cuda")
+    o2, l2 = fa.attention_kv4(gpu_bf16(np.stack(q)), torch.from_numpy(pool.bytes).cuda(),
+                              gpu_i32(pool.table), gpu_i32([3000, 40]), workspace=ws,
+                              max_seqlen=3000)
+    assert torch.equal(o2.reshape(O.shape), O)
 
 
 def test_rows_behind_the_last_sequence_stay():
@@ -431,11 +438,14 @@ def test_helper_refusals():
            dict(q=torch.zeros(2, 1, 4, 128, dtype=torch.bfloat16, device="cuda")),
            dict(max_seqlen=33), dict(group=128), dict(group=48), dict(seqlens=sl.float()),
            dict(cu_seqlens=gpu_i32([0, 1])), dict(out=q.float()), dict(lse=torch.zeros(1, device="cuda")),
-           dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
            dict(page_table=gpu_i32([[0], [1]]))]
     for change in bad:
         with pytest.raises((ValueError, fa.FaError)):
             fa.attention_kv4(**{**ok, **change})
+    wide = torch.zeros(1, 80, dtype=torch.int32, device="cuda")
+    with pytest.raises(fa.FaError):        # too small a workspace
+        fa.attention_kv4(**{**ok, "page_table": wide},
+                         workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     B = 1025
     with pytest.raises(fa.FaError):
         fa.attention_kv4(torch.zeros(B, 1, 4, 128, dtype=torch.bfloat16, device="cuda"), cache,

@@ -178,20 +178,23 @@ def test_helper_refusals_without_gpu():
 
 def test_attention_refusals_without_gpu():
     wb = fa.fa_attention_kv4_workspace_bytes
-    assert wb(-1, 8, 2, 128) == fa.FA_ERR_BAD_SIZE
-    assert wb(1, 9, 2, 128) == fa.FA_ERR_BAD_SIZE
-    assert wb(1, 8, 0, 128) == fa.FA_ERR_BAD_SIZE
-    assert wb(1, 8, 2, 96) == fa.FA_ERR_UNSUPPORTED
-    # a descriptor and two parts a CTA, of 8 rows (608 CTAs), 16 or 32 (304)
-    for Nq, rows in ((1, 8), (2, 8), (3, 16), (4, 16), (5, 32), (500, 32)):
-        assert wb(Nq, 8, 2, 128) == (608 if rows == 8 else 304) * (16 + 2 * rows * (8 + 512))
+    assert wb(-1, 5000, 8, 2, 128) == fa.FA_ERR_BAD_SIZE
+    assert wb(1, 5000, 9, 2, 128) == fa.FA_ERR_BAD_SIZE
+    assert wb(1, 5000, 8, 0, 128) == fa.FA_ERR_BAD_SIZE
+    assert wb(1, 5000, 8, 2, 96) == fa.FA_ERR_UNSUPPORTED
+    # a descriptor and two parts a CTA, of 8 rows (608 CTAs) or 16 (304)
+    for Nq, rows in ((1, 8), (2, 8), (3, 16), (4, 16), (5, 16), (500, 16)):
+        assert wb(Nq, 1025, 8, 2, 128) == (608 if rows == 8 else 304) * (16 + 2 * rows * (8 + 512))
 
-    def go(q=256, qs=1024, cache=256, pages=4, ps=16, table=256, mp=2, lens=256, cu=None, o=256,
-           lse=256, B=1, Nq=1, total=1, Nk=20, H=8, Hkv=2, d=128, group=64, ws=256, wsb=1 << 30):
+    assert wb(1, 1024, 8, 2, 128) == 0                     # whole heads: no parts
+    assert wb(1, -1, 8, 2, 128) == fa.FA_ERR_BAD_SIZE
+
+    def go(q=256, qs=1024, cache=256, pages=4, ps=16, table=256, mp=80, lens=256, cu=None, o=256,
+           lse=256, B=1, Nq=1, total=1, Nk=1100, H=8, Hkv=2, d=128, group=64, ws=256, wsb=1 << 30):
         return fa.fa_attention_kv4(q, qs, cache, pages, ps, table, mp, lens, cu, o, lse, B, Nq,
                                    total, Nk, H, Hkv, d, group, 1.0, 1, ws, wsb)
     assert go(B=-1) == fa.FA_ERR_BAD_SIZE
-    assert go(Nk=33) == fa.FA_ERR_BAD_SIZE                 # more keys than the table holds
+    assert go(Nk=1281) == fa.FA_ERR_BAD_SIZE                 # more keys than the table holds
     assert go(H=7) == fa.FA_ERR_BAD_SIZE
     assert go(Hkv=0) == fa.FA_ERR_BAD_SIZE
     assert go(total=2) == fa.FA_ERR_BAD_SIZE
