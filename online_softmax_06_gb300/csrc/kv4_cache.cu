@@ -9,11 +9,12 @@
 // rounded once to bf16.
 //
 // Both are bound by HBM: 4 d bytes of K and V and d + 8 d / group bytes of the
-// cache per token and head.  A lane takes 8 values (16 bytes of K or V, one
-// 4-byte word of codes), so d / 8 lanes hold a row of a head and the group's
-// extremes come from log2(group / 8) shuffles; a warp's loads and stores cover
-// whole 128-byte lines of K and V and whole rows of codes.  V's 16-bit halves
-// are exchanged by two shuffles so that codes leave (arrive) in whole words.
+// cache per token and head.  A thread takes 16 values: the two words c of value
+// blocks 2 jj and 2 jj + 1 of 32 (kv4.cuh), which stand side by side in a K row
+// and whose halves pair up in a V row, so that no codes change lanes.  d / 16
+// threads hold a row of a head, the group's extremes come from 2 or 3 shuffles of
+// (min x, min -x), and a row's scale is found for 16 values at a time: with 8 a
+// thread the quantising took more issue slots than the copy leaves.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -93,175 +94,253 @@ __device__ __forceinline__ uint32_t min_nan2(uint32_t x, uint32_t y)
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// Codes of 8 values (one word) and the group's (scale, min) pair; the group's
-// lanes are the G / 8 consecutive ones around this lane.
-template <int G>
-__device__ __forceinline__ uint32_t quantise(const uint4 &x, uint32_t &pair)
+__device__ __forceinline__ uint32_t max_nan2(uint32_t x, uint32_t y)
 {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    // (min x, min -x) in the two halves of one word: one shuffle a step
-    uint32_t lo2 = min_nan2(min_nan2(w[0], w[1]), min_nan2(w[2], w[3]));
-    uint32_t hi2 = min_nan2(min_nan2(w[0] ^ 0x80008000u, w[1] ^ 0x80008000u),
-                            min_nan2(w[2] ^ 0x80008000u, w[3] ^ 0x80008000u));
-    uint32_t ext = min_nan2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
-#pragma unroll
-    for (int o = 1; o < G / 8; o <<= 1)
-        ext = min_nan2(ext, __shfl_xor_sync(0xffffffffu, ext, o));
-    const float m = bf16_lo(ext), mx = -bf16_hi(ext);
-    const float half_m = 0.5f * m;
-    const float s32 = __fmul_rn(__fsub_rn(0.5f * mx, half_m), 2.0f / 15.0f);
-    const __nv_bfloat16 sb = __float2bfloat16_rn(s32);
-    float s = __bfloat162float(sb);
-    s = s < 1.17549435e-38f ? 0.f : s;           // below 2^-126: all codes 0
-    const float r = s > 0.f ? __fdiv_rn(1.f, 0.5f * s) : 0.f;
-    const bool bad = !(fabsf(m) < INFINITY && fabsf(mx) < INFINITY);
-    pair = bad ? 0x7fc07fc0u
-               : (__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xffff0000u);
-    // (x - m) / s is in [0, 15.06], so rint needs no clamp; adding 1.5 * 2^23
-    // rounds to nearest even and leaves the code in the low bits
-    uint32_t code = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float t0 = fmaf(bf16_lo(w[i]), 0.5f, -half_m);   // = rn(x/2 - m/2)
-        const float t1 = fmaf(bf16_hi(w[i]), 0.5f, -half_m);
-        const uint32_t c0 = __float_as_uint(__fadd_rn(__fmul_rn(t0, r), 12582912.f));
-        const uint32_t c1 = __float_as_uint(__fadd_rn(__fmul_rn(t1, r), 12582912.f));
-        code |= (c0 & 15u) << (8 * i) | (c1 & 15u) << (8 * i + 4);
-    }
-    return bad ? 0u : code;
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
 }
 
-// grid: blocks of `rows_per_block` rows.  A block's threads are laid over
-// (row, K or V, head, 8 values); `per_row` = 2 Hkv d / 8 items a row.
+// (min x, min -x) of 8 values, in the two halves of a word.
+__device__ __forceinline__ uint32_t extremes(const uint4 &x)
+{
+    const uint32_t lo = min_nan2(min_nan2(x.x, x.y), min_nan2(x.z, x.w));
+    const uint32_t hi = max_nan2(max_nan2(x.x, x.y), max_nan2(x.z, x.w)) ^ 0x80008000u;
+    return min_nan2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+}
+
+// A group's (scale, min) pair as stored, min / 2 and 1 / (scale / 2).
+struct Scale {
+    uint32_t pair;
+    float half_min, inv;
+    bool bad;
+};
+
+__device__ __forceinline__ Scale scale_of(uint32_t ext)
+{
+    Scale r;
+    const float m = bf16_lo(ext), mx = -bf16_hi(ext);
+    r.half_min = 0.5f * m;
+    const float s32 = __fmul_rn(__fsub_rn(0.5f * mx, r.half_min), 2.0f / 15.0f);
+    float s = __bfloat162float(__float2bfloat16_rn(s32));
+    s = s < 1.17549435e-38f ? 0.f : s;           // below 2^-126: all codes 0
+    r.inv = s > 0.f ? __frcp_rn(0.5f * s) : 0.f;
+    r.bad = !(fabsf(m) < INFINITY && fabsf(mx) < INFINITY);
+    r.pair = r.bad ? 0x7fc07fc0u : (__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xffff0000u);
+    return r;
+}
+
+// The codes of 8 values, lowest nibble first.  (x - m) / s is in [0, 15.06], so
+// rint needs no clamp; adding 1.5 * 2^23 rounds to nearest even and leaves the
+// code in the low bits of a word 0x4b400000 + code, whose sum over the nibbles
+// exceeds the codes by 0x3f400000 (mod 2^32).
+__device__ __forceinline__ uint32_t codes_of(const uint4 &x, const Scale &s)
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t sum = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+        const float t1 = fmaf(bf16_hi(w[i]), 0.5f, -s.half_min);   // = rn(x / 2 - m / 2)
+        const float t0 = fmaf(bf16_lo(w[i]), 0.5f, -s.half_min);
+        sum = sum * 16 + __float_as_uint(__fadd_rn(__fmul_rn(t1, s.inv), 12582912.f));
+        sum = sum * 16 + __float_as_uint(__fadd_rn(__fmul_rn(t0, s.inv), 12582912.f));
+    }
+    return s.bad ? 0u : sum - 0x3f400000u;
+}
+
+// What a thread does in every row: its head, its 16 values, their places.
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads)
+struct Part {
+    static constexpr int kCell = kv4::cell_bytes(D, G), kLanes = D / 16, kN = D / 32;
+    int h, jj, c;
+    bool is_v;
+    int64_t head;              // byte offset of the head's page from head 0's
+
+    __device__ __forceinline__ Part(const Kv4CacheArgs &a, int p)
+    {
+        const int l = p % kLanes, h2 = p / kLanes;
+        is_v = h2 >= a.Hkv;
+        h = is_v ? h2 - a.Hkv : h2;
+        jj = l / 4;
+        c = l % 4;
+        head = int64_t(h) * (a.page_size / kv4::kCellTokens) * kCell;
+    }
+    // element of the row at which word w = 4 (2 jj + x) + c begins
+    __device__ __forceinline__ int element(int x) const { return h * D + (4 * (2 * jj + x) + c) * 8; }
+    // byte of the cell at which the thread's K words, or its first V word, stand
+    __device__ __forceinline__ int code_at(int t) const
+    {
+        return is_v ? kv4::v_off(D) + kv4::v_swizzle(t * (D / 2) + c * (kN * 4) + jj * 4)
+                    : t * (D / 2) + (c * kN + 2 * jj) * 4;
+    }
+    // the second V word: halves of g = 2 c + 1
+    static constexpr int kSecond = kN * 2;
+    __device__ __forceinline__ int pair_at(int t) const
+    {
+        return (is_v ? kv4::v_par_off(D, G) : kv4::k_par_off(D)) +
+               (t * (D / G) + (G == 32 ? 2 * jj : G == 64 ? jj : 0)) * 4;
+    }
+};
+
+constexpr int kUnroll = 2;     // rows a thread has under way
+
+// Grid: x over the rows, rows_per_block each; y over a row's threads (2 Hkv d / 16)
+// beyond kThreads.
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 4)
     kv4_append_kernel(const Kv4CacheArgs a, int rows_per_block)
 {
-    constexpr int kCell = kv4::cell_bytes(D, G), kLanes = D / 8, kN = D / 32;
     extern __shared__ RowAt at[];
     const int64_t row0 = int64_t(blockIdx.x) * rows_per_block;
     const int rows = int(min(int64_t(rows_per_block), a.total - row0));
     for (int i = threadIdx.x; i < rows; i += kThreads)
-        at[i] = locate(a, row0 + i, kCell);
+        at[i] = locate(a, row0 + i, Part<D, G>::kCell);
     __syncthreads();
-    const int per_row = 2 * a.Hkv * kLanes, items = rows * per_row;
-    const int head_stride = a.page_size / kv4::kCellTokens * kCell;
-    // every lane of a warp takes part in the shuffles, the last ones idle
-    for (int it = threadIdx.x; (it & ~31) < items; it += kThreads) {
-        const bool in = it < items;
-        const int row = in ? it / per_row : 0, p = in ? it - row * per_row : 0;
-        const int l = p % kLanes, h2 = p / kLanes;
-        const bool is_v = h2 >= a.Hkv;
-        const int h = is_v ? h2 - a.Hkv : h2;
-        const RowAt w = at[row];
-        const bool put = in && w.cell >= 0;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (put) {
-            const auto *src = static_cast<const __nv_bfloat16 *>(is_v ? a.V : a.K) +
-                              (row0 + row) * (is_v ? a.v_stride : a.k_stride) + h * D + l * 8;
-            x = __ldg(reinterpret_cast<const uint4 *>(src));
+    const int all = 2 * a.Hkv * (D / 16), p0 = blockIdx.y * kThreads;
+    const int width = min(all - p0, kThreads), side = kThreads / width;   // rows side by side
+    const bool in = int(threadIdx.x) < width * side;
+    const Part<D, G> part(a, p0 + threadIdx.x % width);
+    const int64_t stride = part.is_v ? a.v_stride : a.k_stride;
+    const auto *src = static_cast<const __nv_bfloat16 *>(part.is_v ? a.V : a.K) + row0 * stride;
+    uint8_t *cache = static_cast<uint8_t *>(a.cache) + part.head;
+    for (int r0 = 0; r0 < rows; r0 += side * kUnroll) {
+        uint4 x[kUnroll][2];
+        RowAt w[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int row = r0 + u * side + int(threadIdx.x) / width;
+            w[u] = in && row < rows ? at[row] : RowAt{-1, 0};
+            x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+            if (w[u].cell >= 0) {
+                x[u][0] = __ldg(reinterpret_cast<const uint4 *>(src + row * stride + part.element(0)));
+                x[u][1] = __ldg(reinterpret_cast<const uint4 *>(src + row * stride + part.element(1)));
+            }
         }
-        uint32_t pair;
-        uint32_t code = quantise<G>(x, pair);
-        // V: this lane's stored word l holds halves q * 8 + g and (q + 1) * 8 + g
-        const int g = 2 * l / kN, q = 2 * l % kN;
-        const uint32_t c0 = __shfl_sync(0xffffffffu, code, q * 4 + g / 2, kLanes);
-        const uint32_t c1 = __shfl_sync(0xffffffffu, code, (q + 1) * 4 + g / 2, kLanes);
-        if (!put)
-            continue;
-        uint8_t *cell = static_cast<uint8_t *>(a.cache) + w.cell + int64_t(h) * head_stride;
-        int off, par;
-        if (is_v) {
-            code = __byte_perm(c0, c1, (g & 1) ? 0x7632 : 0x5410);
-            off = kv4::v_off(D) + kv4::v_swizzle(w.t * (D / 2) + l * 4);
-            par = kv4::v_par_off(D, G);
-        } else {
-            off = w.t * (D / 2) + ((l % 4) * kN + l / 4) * 4;
-            par = kv4::k_par_off(D);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            // the lanes of a group: c = 0 .. 3, and jj with 128 values
+            uint32_t e0 = extremes(x[u][0]), e1 = extremes(x[u][1]);
+            if (G > 32)
+                e0 = min_nan2(e0, e1);
+#pragma unroll
+            for (int o = 1; o < (G == 128 ? 8 : 4); o <<= 1) {
+                e0 = min_nan2(e0, __shfl_xor_sync(0xffffffffu, e0, o));
+                if (G == 32)
+                    e1 = min_nan2(e1, __shfl_xor_sync(0xffffffffu, e1, o));
+            }
+            const Scale s0 = scale_of(e0), s1 = G == 32 ? scale_of(e1) : s0;
+            const uint32_t c0 = codes_of(x[u][0], s0), c1 = codes_of(x[u][1], s1);
+            if (w[u].cell < 0)
+                continue;
+            uint8_t *cell = cache + w[u].cell;
+            uint8_t *to = cell + part.code_at(w[u].t);
+            if (part.is_v) {
+                *reinterpret_cast<uint32_t *>(to) = __byte_perm(c0, c1, 0x5410);
+                *reinterpret_cast<uint32_t *>(to + part.kSecond) = __byte_perm(c0, c1, 0x7632);
+            } else {
+                *reinterpret_cast<uint2 *>(to) = make_uint2(c0, c1);
+            }
+            if (part.c == 0 && (G != 128 || part.jj == 0)) {
+                uint8_t *p = cell + part.pair_at(w[u].t);
+                if (G == 32)
+                    *reinterpret_cast<uint2 *>(p) = make_uint2(s0.pair, s1.pair);
+                else
+                    *reinterpret_cast<uint32_t *>(p) = s0.pair;
+            }
         }
-        *reinterpret_cast<uint32_t *>(cell + off) = code;
-        if (l % (G / 8) == 0)
-            *reinterpret_cast<uint32_t *>(cell + par + (w.t * (D / G) + l / (G / 8)) * 4) = pair;
     }
+}
+
+// min + scale * code of 8 codes: nibbles i and i + 4 as the bf16 pair 128 + code,
+// exact, less 128; then one rounding.
+__device__ __forceinline__ uint4 values_of(uint32_t code, uint32_t pair)
+{
+    const uint32_t s2 = __byte_perm(pair, pair, 0x1010), m2 = __byte_perm(pair, pair, 0x3232);
+    const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162 *>(&s2);
+    const __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162 *>(&m2);
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t u = ((code >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+        const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u),
+                                         __float2bfloat162_rn(128.f));
+        const __nv_bfloat162 y = __hfma2(s, c, m);
+        v[i] = *reinterpret_cast<const uint32_t *>(&y);
+    }
+    return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                      __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
 }
 
 // The same lay-out, the other way.
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     kv4_read_kernel(const Kv4CacheArgs a, int rows_per_block)
 {
-    constexpr int kCell = kv4::cell_bytes(D, G), kLanes = D / 8, kN = D / 32;
     extern __shared__ RowAt at[];
     const int64_t row0 = int64_t(blockIdx.x) * rows_per_block;
     const int rows = int(min(int64_t(rows_per_block), a.total - row0));
     for (int i = threadIdx.x; i < rows; i += kThreads)
-        at[i] = locate(a, row0 + i, kCell);
+        at[i] = locate(a, row0 + i, Part<D, G>::kCell);
     __syncthreads();
-    const int per_row = 2 * a.Hkv * kLanes, items = rows * per_row;
-    const int head_stride = a.page_size / kv4::kCellTokens * kCell;
-    for (int it = threadIdx.x; (it & ~31) < items; it += kThreads) {
-        const bool in = it < items;
-        const int row = in ? it / per_row : 0, p = in ? it - row * per_row : 0;
-        const int l = p % kLanes, h2 = p / kLanes;
-        const bool is_v = h2 >= a.Hkv;
-        const int h = is_v ? h2 - a.Hkv : h2;
-        const RowAt w = at[row];
-        const bool put = in && w.cell >= 0;
-        uint32_t code = 0, pair = 0;
-        if (put) {
-            const uint8_t *cell =
-                static_cast<const uint8_t *>(a.cache) + w.cell + int64_t(h) * head_stride;
-            const int off = is_v ? kv4::v_off(D) + kv4::v_swizzle(w.t * (D / 2) + l * 4)
-                                 : w.t * (D / 2) + ((l % 4) * kN + l / 4) * 4;
-            const int par = is_v ? kv4::v_par_off(D, G) : kv4::k_par_off(D);
-            code = *reinterpret_cast<const uint32_t *>(cell + off);
-            pair = *reinterpret_cast<const uint32_t *>(cell + par +
-                                                       (w.t * (D / G) + l / (G / 8)) * 4);
-        }
-        // V: logical word l = halves 2 l and 2 l + 1, from two stored words
-        const int w0 = (l % 4) * kN + ((l / 4) >> 1);
-        const uint32_t c0 = __shfl_sync(0xffffffffu, code, w0, kLanes);
-        const uint32_t c1 = __shfl_sync(0xffffffffu, code, w0 + kN / 2, kLanes);
-        if (!put)
-            continue;
-        if (is_v)
-            code = __byte_perm(c0, c1, ((l / 4) & 1) ? 0x7632 : 0x5410);
-        const __nv_bfloat162 s = __bfloat162bfloat162(
-            __ushort_as_bfloat16(static_cast<unsigned short>(pair & 0xffffu)));
-        const __nv_bfloat162 m =
-            __bfloat162bfloat162(__ushort_as_bfloat16(static_cast<unsigned short>(pair >> 16)));
-        // nibbles i and i + 4 as the bf16 pair 128 + code, exact; then one
-        // rounding in m + s * code
-        uint32_t v[4];
+    const int all = 2 * a.Hkv * (D / 16), p0 = blockIdx.y * kThreads;
+    const int width = min(all - p0, kThreads), side = kThreads / width;
+    if (int(threadIdx.x) >= width * side)
+        return;
+    const Part<D, G> part(a, p0 + threadIdx.x % width);
+    const int64_t stride = part.is_v ? a.v_stride : a.k_stride;
+    auto *dst = static_cast<__nv_bfloat16 *>(part.is_v ? a.V : a.K) + row0 * stride;
+    const uint8_t *cache = static_cast<const uint8_t *>(a.cache) + part.head;
+    for (int r0 = threadIdx.x / width; r0 < rows; r0 += side * kUnroll) {
+        uint32_t c0[kUnroll], c1[kUnroll], p[kUnroll][2];
+        bool put[kUnroll];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t u = ((code >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-            const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u),
-                                             __float2bfloat162_rn(128.f));
-            const __nv_bfloat162 y = __hfma2(s, c, m);
-            v[i] = *reinterpret_cast<const uint32_t *>(&y);
+        for (int u = 0; u < kUnroll; ++u) {
+            const int row = r0 + u * side;
+            const RowAt w = row < rows ? at[row] : RowAt{-1, 0};
+            put[u] = w.cell >= 0;
+            if (!put[u])
+                continue;
+            const uint8_t *cell = cache + w.cell, *from = cell + part.code_at(w.t);
+            if (part.is_v) {
+                c0[u] = *reinterpret_cast<const uint32_t *>(from);
+                c1[u] = *reinterpret_cast<const uint32_t *>(from + part.kSecond);
+            } else {
+                const uint2 z = *reinterpret_cast<const uint2 *>(from);
+                c0[u] = z.x;
+                c1[u] = z.y;
+            }
+            p[u][0] = *reinterpret_cast<const uint32_t *>(cell + part.pair_at(w.t));
+            p[u][1] = G == 32 ? *reinterpret_cast<const uint32_t *>(cell + part.pair_at(w.t) + 4)
+                              : p[u][0];
         }
-        const uint4 out = make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
-                                     __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
-        auto *dst = static_cast<__nv_bfloat16 *>(is_v ? a.V : a.K) +
-                    (row0 + row) * (is_v ? a.v_stride : a.k_stride) + h * D + l * 8;
-        *reinterpret_cast<uint4 *>(dst) = out;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (!put[u])
+                continue;
+            const uint32_t a0 = part.is_v ? __byte_perm(c0[u], c1[u], 0x5410) : c0[u];
+            const uint32_t a1 = part.is_v ? __byte_perm(c0[u], c1[u], 0x7632) : c1[u];
+            auto *row = dst + (r0 + u * side) * stride;
+            *reinterpret_cast<uint4 *>(row + part.element(0)) = values_of(a0, p[u][0]);
+            *reinterpret_cast<uint4 *>(row + part.element(1)) = values_of(a1, p[u][1]);
+        }
     }
 }
 
 template <typename F>
 int launch_rows(F kernel, const Kv4CacheArgs &a, cudaStream_t stream)
 {
-    // one row a block while that fills the SMs (a decode step's few rows),
-    // else enough rows for about 8 items a thread
-    const int per_row = 2 * a.Hkv * (a.d / 8);
-    int rows = (8 * kThreads + per_row - 1) / per_row;
+    // one row a block while that fills the SMs (a decode step's few rows), else
+    // four rounds of kUnroll rows a thread
+    const int all = 2 * a.Hkv * (a.d / 16);
+    const int side = all < kThreads ? kThreads / all : 1;
+    int rows = 4 * kUnroll * side;
     while (rows > 1 && (a.total + rows - 1) / rows < 2 * 152)
         rows /= 2;
     const int64_t blocks = (a.total + rows - 1) / rows;
     if (blocks > 0x7fffffffLL)
         return FA_ERR_TOO_LARGE;
-    kernel<<<unsigned(blocks), kThreads, rows * sizeof(RowAt), stream>>>(a, rows);
+    const dim3 grid(unsigned(blocks), unsigned((all + kThreads - 1) / kThreads));
+    kernel<<<grid, kThreads, rows * sizeof(RowAt), stream>>>(a, rows);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
