@@ -506,8 +506,7 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
                        int64_t total, int Hkv, int d, int group);
 
 /*
- * Exact attention of bf16 queries on the cache's values (min + scale * code,
- * unrounded): S = scale * Q K^T (+ mask), P = softmax(S), O = P V, lse as in
+ * Exact attention of bf16 queries on the cache's values (min + scale * code): S = scale * Q K^T (+ mask), P = softmax(S), O = P V, lse as in
  * fa_attention_fwd, fp32 accumulation.  A decode step has Nq = 1 (or a few
  * drafted tokens); chunks of a prompt any Nq.  Query head h reads kv head
  * h / (H / Hkv); H is a multiple of Hkv.
@@ -526,8 +525,14 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  *   sequence's end, or at keys that a query does not see, does not reach its
  *   result, NaN or not.
  *   workspace: DEVICE scratch owned by the caller, 256-byte aligned, at least
- *   fa_attention_kv4_workspace_bytes(Nq, Nk, H, Hkv, d) bytes; contents on
- *   entry are ignored.  Calls that may run at the same time need one each.
+ *   fa_attention_kv4_workspace_bytes(...) bytes; contents on entry are
+ *   ignored.  Calls that may run at the same time need one each.
+ * Few query rows a kv head (Nq * H / Hkv; decode steps, drafted tokens): the
+ * codes go into the products as they are and nothing is rounded but P, to fp16.
+ * Many (128 and more on average, enough of them to fill the GPU; chunks of
+ * prompts): the values are first written out as fp16 (2^-11 relative, with a
+ * power of two a tile of 128 tokens), and a NaN of V reaches all of a row that
+ * sees it.
  * B <= 1024.  Results do not depend on timing: the same call gives the same
  * bits.  One or two kernels on the library stream, no
  * synchronisation.
@@ -543,9 +548,11 @@ FA_API int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, 
                             int d, int group, float scale, int causal, void *workspace,
                             int64_t workspace_bytes);
 
-/* Workspace bytes fa_attention_kv4 needs (0 with Nk <= 1024: the workspace may be
- * NULL then), or a negative FA_ERR_* code. */
-FA_API int64_t fa_attention_kv4_workspace_bytes(int Nq, int Nk, int H, int Hkv, int d);
+/* Workspace bytes fa_attention_kv4 needs (where 0, the workspace may be NULL), or
+ * a negative FA_ERR_* code.  A few MB, but for chunks of prompts: fp16 copies of Q
+ * and of the cache's values. */
+FA_API int64_t fa_attention_kv4_workspace_bytes(int B, int Nq, int64_t total_q, int Nk, int H,
+                                                int Hkv, int d);
 
 /*
  * Exact attention forward in fp32 throughout (fp32 Q, K, V, O, lse), on the

@@ -114,7 +114,7 @@ def lib():
         L.fa_kv4_read.argtypes = L.fa_kv4_append.argtypes
         L.fa_attention_kv4.argtypes = [vp, i64, vp, i32, i32, vp, i32, vp, vp, vp, vp, i32, i32,
                                        i64, i32, i32, i32, i32, i32, f32, i32, vp, i64]
-        L.fa_attention_kv4_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.fa_attention_kv4_workspace_bytes.argtypes = [i32, i32, i64, i32, i32, i32, i32]
         L.fa_attention_kv4_workspace_bytes.restype = i64
         L.fa_set_stream.argtypes = [vp]
         L.fa_get_stream.argtypes = []
@@ -280,8 +280,8 @@ def fa_attention_kv4(q, q_stride, cache, num_pages, page_size, page_table, max_p
                                   group, scale, causal, workspace, workspace_bytes)
 
 
-def fa_attention_kv4_workspace_bytes(Nq, Nk, H, Hkv, d) -> int:
-    return lib().fa_attention_kv4_workspace_bytes(Nq, Nk, H, Hkv, d)
+def fa_attention_kv4_workspace_bytes(B, Nq, total_q, Nk, H, Hkv, d) -> int:
+    return lib().fa_attention_kv4_workspace_bytes(B, Nq, total_q, Nk, H, Hkv, d)
 
 
 def fa_set_stream(stream_ptr) -> int:
@@ -630,24 +630,17 @@ def attention_bwd(q, k, v, o, do, lse, causal: bool = False, scale: float | None
 
 # ---- 4-bit paged key/value cache ------------------------------------------------
 
-class _On:
-    """Makes a device current, and its current stream the library's, for one call."""
-
-    __slots__ = ("guard",)
-
-    def __init__(self, torch, index: int):
-        self.guard = None
-        if torch.cuda.current_device() != index:
-            self.guard = torch.cuda.device(index)
-            self.guard.__enter__()
-        lib().fa_set_stream(torch._C._cuda_getCurrentRawStream(index))
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _kv4_call(torch, index, where, *args):
+    """Calls an entry point on the current stream of device `index`, made current."""
+    L = _lib or lib()
+    L.fa_set_stream(torch._C._cuda_getCurrentRawStream(index))
+    if torch.cuda.current_device() == index:
+        rc = getattr(L, where)(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = getattr(L, where)(*args)
+    if rc != FA_OK:
+        raise FaError(rc, where)
 
 
 # What the shapes and strides of a call's tensors say, checked once for each set of
@@ -750,19 +743,16 @@ def _plan_rows(k, ks, v, vs, cache, page_table, seqlens, cu, max_new, group):
             total, hkv, k[-1])
 
 
-def _kv4_rows(call, where, k, v, cache, page_table, seqlens, cu_seqlens, max_new, group):
+def _kv4_rows(where, k, v, cache, page_table, seqlens, cu_seqlens, max_new, group):
     import torch
     index = _kv4_check(torch, (k, v), cache, page_table, seqlens, cu_seqlens)
     cu = None if cu_seqlens is None else cu_seqlens.shape
     key = (k.shape, k.stride(), v.shape, v.stride(), cache.shape, page_table.shape, seqlens.shape,
            cu, max_new, group)
     ks, vs, pages, page_size, max_pages, B, N, total, hkv, d = _kv4_plan(key, _plan_rows, *key)
-    with _On(torch, index):
-        rc = call(k.data_ptr(), v.data_ptr(), ks, vs, cache.data_ptr(), pages, page_size,
-                  page_table.data_ptr(), max_pages, seqlens.data_ptr(),
-                  None if cu is None else cu_seqlens.data_ptr(), B, N, total, hkv, d, group)
-    if rc != FA_OK:
-        raise FaError(rc, where)
+    _kv4_call(torch, index, where, k.data_ptr(), v.data_ptr(), ks, vs, cache.data_ptr(), pages,
+              page_size, page_table.data_ptr(), max_pages, seqlens.data_ptr(),
+              None if cu is None else cu_seqlens.data_ptr(), B, N, total, hkv, d, group)
 
 
 def kv4_append(k, v, cache, page_table, seqlens, cu_seqlens=None, max_new: int | None = None,
@@ -777,8 +767,7 @@ def kv4_append(k, v, cache, page_table, seqlens, cu_seqlens=None, max_new: int |
     int32 [B]: tokens in the cache AFTER the call; the new ones are each
     sequence's last.
     """
-    _kv4_rows(fa_kv4_append, "fa_kv4_append", k, v, cache, page_table, seqlens, cu_seqlens,
-              max_new, group)
+    _kv4_rows("fa_kv4_append", k, v, cache, page_table, seqlens, cu_seqlens, max_new, group)
 
 
 def kv4_read(cache, page_table, seqlens, total: int | None = None, d: int = 128, cu_seqlens=None,
@@ -800,8 +789,7 @@ def kv4_read(cache, page_table, seqlens, total: int | None = None, d: int = 128,
             shape = (total, cache.shape[1], d)
         k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
         v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
-    _kv4_rows(fa_kv4_read, "fa_kv4_read", k, v, cache, page_table, seqlens, cu_seqlens, max_new,
-              group)
+    _kv4_rows("fa_kv4_read", k, v, cache, page_table, seqlens, cu_seqlens, max_new, group)
     return k, v
 
 
@@ -822,7 +810,7 @@ def _plan_attention(q, qs, cache, page_table, seqlens, cu, max_q, max_seqlen, gr
         Nq = total if max_q is None else int(max_q)
         lse_shape = (H, total)
     Nk = max_pages * page_size if max_seqlen is None else int(max_seqlen)
-    nbytes = fa_attention_kv4_workspace_bytes(Nq, Nk, H, hkv, d)
+    nbytes = fa_attention_kv4_workspace_bytes(B, Nq, total, Nk, H, hkv, d)
     _check(int(min(nbytes, 0)), "fa_attention_kv4_workspace_bytes")
     return (_row_stride(q, qs, "q"), pages, page_size, max_pages, B, Nq, total, Nk, H, hkv, d,
             lse_shape, nbytes)
@@ -866,15 +854,11 @@ def attention_kv4(q, cache, page_table, seqlens, max_seqlen: int | None = None, 
               and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
     ws, n_ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    with _On(torch, index):
-        rc = fa_attention_kv4(q.data_ptr(), q_stride, cache.data_ptr(), pages, page_size,
-                              page_table.data_ptr(), max_pages, seqlens.data_ptr(),
-                              None if cu is None else cu_seqlens.data_ptr(), out.data_ptr(),
-                              lse.data_ptr(), B, Nq, total, Nk, H, hkv, d, group,
-                              1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0,
-                              ws, n_ws)
-    if rc != FA_OK:
-        raise FaError(rc, "fa_attention_kv4")
+    _kv4_call(torch, index, "fa_attention_kv4", q.data_ptr(), q_stride, cache.data_ptr(), pages,
+              page_size, page_table.data_ptr(), max_pages, seqlens.data_ptr(),
+              None if cu is None else cu_seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Nq,
+              total, Nk, H, hkv, d, group, 1.0 / math.sqrt(d) if scale is None else scale,
+              1 if causal else 0, ws, n_ws)
     return out, lse
 
 

@@ -148,14 +148,24 @@ constexpr int kJoinWarps = 8;
 // into blocks of kBlock tokens.  All items' blocks, sequence by sequence, form
 // one line that is cut into equal ranges, one a CTA: ragged batches and single
 // long sequences fill the GPU alike, and nothing of it needs the host.
-struct Desc {          // of an item that begins in this CTA's range and does not end there
-    int parts;         // CTAs that hold a part (0: no such item)
-    int b, kvh, tile;
+//
+// An item costs a CTA some time beside its blocks' (queries, the four warps'
+// join): the line is cut as if each item had kItemCost blocks more.  Without it
+// the CTAs whose range holds the short sequences of a batch ended last (32
+// sequences of 1 to 8191 keys, 16 kv heads, d = 64: 74 us, against 46 with 4096
+// each).
+constexpr uint32_t kItemCost = 3;
+
+struct Desc {          // of a CTA
+    uint32_t begin;    // first block of its range
+    uint32_t item_end; // end of the item that begins in it and goes on after it; 0: none
+    int b, kvh, tile;  // that item
+    int unused[3];
 };
 
 // Workspace: Desc[ctas], then (reference, sum) [2 ctas][R], then the
-// unnormalised O [2 ctas][R][d] fp32.  A CTA's slot 0 holds the part of
-// an item that began before its range, slot 1 that of one that goes on after.
+// unnormalised O [2 ctas][R][d] fp32.  A CTA's slot 0 holds the part of an item
+// that began before its range, slot 1 that of one that goes on after.
 struct Parts {
     Desc *desc;
     float2 *ml;
@@ -255,10 +265,53 @@ __device__ __forceinline__ Item uniform(Item it)
     return it;
 }
 
+// The item after `it`.
+__device__ __forceinline__ Item next_item(const Kv4AttnArgs &a, const uint32_t *s_pre, int grp,
+                                          int R, Item it)
+{
+    it.first += it.nb;
+    if (++it.tile * R < it.nq * grp)
+        return it;
+    it.tile = 0;
+    if (++it.kvh < a.Hkv)
+        return it;
+    it.kvh = 0;
+    do                                     // sequences without blocks are passed over
+        ++it.b;
+    while (it.b + 1 < a.B && s_pre[it.b + 1] == s_pre[it.b]);
+    if (it.b < a.B) {
+        const int2 q = queries_of(a, it.b);
+        it.q0 = q.x;
+        it.nq = q.y;
+        it.L = a.seqlens[it.b];
+        it.nb = blocks_of(it.L);
+    }
+    return uniform(it);
+}
+
 // The keys that query i of the item's sequence sees lie below this.
 __device__ __forceinline__ int key_end(const Kv4AttnArgs &a, const Item &it, int i)
 {
     return a.causal ? min(it.L, it.L - it.nq + i + 1) : it.L;
+}
+
+// The block at place x of the line of costs: an item's kItemCost come first.
+__device__ __forceinline__ uint32_t block_of(const Kv4AttnArgs &a, const uint32_t *s_pre,
+                                             const uint32_t *s_cost, uint32_t x)
+{
+    if (x >= s_cost[a.B])
+        return uint32_t(uniform(int(s_pre[a.B])));
+    int lo = 0, hi = a.B;                  // s_cost[lo] <= x < s_cost[lo + 1]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_cost[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const uint32_t nb = blocks_of(a.seqlens[lo]), at = x - s_cost[lo], i = at / (nb + kItemCost);
+    const uint32_t o = at - i * (nb + kItemCost);
+    return uint32_t(uniform(int(s_pre[lo] + i * nb + (o > kItemCost ? o - kItemCost : 0))));
 }
 
 // The first item that begins at block x or after it.
@@ -271,15 +324,14 @@ __device__ __forceinline__ uint32_t item_from(const Kv4AttnArgs &a, const uint32
     return it.first == x ? x : it.first + it.nb;
 }
 
-// The 8 query rows of n-tile nt as B fragments, by one warp.
-template <int D, int G, int NT>
-__device__ __forceinline__ void load_queries(const Kv4AttnArgs &a, const Item &it, int grp, int nt,
-                                             QueryTile<D, G, NT> &to)
+// A lane's share of the 8 query rows of n-tile nt: row g, values 32 j + 8 c ...
+template <int D, int NT>
+__device__ __forceinline__ void fetch_queries(const Kv4AttnArgs &a, const Item &it, int grp, int nt,
+                                              uint4 (&w)[D / 32])
 {
-    constexpr int R = 8 * NT, NJ = D / 32, NG = D / G;
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, r = nt * 8 + g;
-    const int at = it.tile * R + r, i = at / grp;
-    uint4 w[NJ];
+    constexpr int R = 8 * NT, NJ = D / 32;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int at = it.tile * R + nt * 8 + g, i = at / grp;
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
         w[j] = make_uint4(0, 0, 0, 0);
@@ -291,6 +343,16 @@ __device__ __forceinline__ void load_queries(const Kv4AttnArgs &a, const Item &i
         for (int j = 0; j < NJ; ++j)
             w[j] = __ldg(reinterpret_cast<const uint4 *>(src + 32 * j));
     }
+}
+
+// They as B fragments, by the warp.
+template <int D, int G, int NT>
+__device__ __forceinline__ void place_queries(const Kv4AttnArgs &a, const Item &it, int grp, int nt,
+                                              const uint4 (&w)[D / 32], QueryTile<D, G, NT> &to)
+{
+    constexpr int R = 8 * NT, NJ = D / 32, NG = D / G;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, r = nt * 8 + g;
+    const int i = (it.tile * R + r) / grp;
     float big = 0.f, sum[NG];
 #pragma unroll
     for (int x = 0; x < NG; ++x)
@@ -377,6 +439,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
     constexpr int kCell = kv4::cell_bytes(D, G);
     constexpr int kRow = D + 4;            // padded fp32 row of the merge buffer
     constexpr int kVBases = D == 128 ? 2 : 4;   // d = 128: 8 tokens are 512 bytes on
+    // Cells taken at once.  Two overlap better where the registers hold them (16
+    // sequences x 4 queries, group 64: 66 us, one by one 68); where they do not,
+    // one at a time spills less (256 x 1k: 88 -> 84 us with group 64, 111 -> 105
+    // with 32).
+    constexpr int kCells = NG == 4 || (NT == 1 && NG == 2) ? 1 : 2;
     using Smem = Shared<D, G, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     auto &s_q = *reinterpret_cast<QueryTile<D, G, NT> *>(smem + Smem::q);
@@ -402,63 +469,76 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
 
     // ---- the line of blocks ------------------------------------------------
     const int per = (a.B + kThreads - 1) / kThreads;
-    uint32_t mine = 0;
+    uint32_t *s_cost = reinterpret_cast<uint32_t *>(smem + Smem::ring);   // [B + 1], until the first copy
+    uint32_t mine = 0, mine_cost = 0;
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b >= a.B)
             break;
         const int2 q = queries_of(a, b);
         const int L = a.seqlens[b];
-        uint32_t n = 0;
+        uint32_t items = 0;
         if (q.y < 0 || q.y > a.Nq || q.x < 0 || int64_t(q.x) + q.y > a.total_q || L < 0 ||
             L > a.Nk)
             record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
         else
-            n = uint32_t((q.y * grp + R - 1) / R) * a.Hkv * blocks_of(L);
-        s_pre[b + 1] = n;
-        mine += n;
+            items = uint32_t((q.y * grp + R - 1) / R) * a.Hkv;
+        s_pre[b + 1] = items * blocks_of(L);
+        s_cost[b + 1] = items * (blocks_of(L) + kItemCost);
+        mine += s_pre[b + 1];
+        mine_cost += s_cost[b + 1];
     }
-    // exclusive scan over the threads, then over each thread's sequences
-    uint32_t incl = mine;
+    // exclusive scans over the threads, then over each thread's sequences
+    uint32_t incl = mine, incl_cost = mine_cost;
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o)
+        const uint32_t t_cost = __shfl_up_sync(0xffffffffu, incl_cost, o);
+        if (lane >= o) {
             incl += t;
+            incl_cost += t_cost;
+        }
     }
-    uint32_t *s_w = reinterpret_cast<uint32_t *>(s_ref);
+    uint2 *s_w = reinterpret_cast<uint2 *>(s_ref);
     if (lane == 31)
-        s_w[warp] = incl;
+        s_w[warp] = make_uint2(incl, incl_cost);
     __syncthreads();
-    uint32_t base = incl - mine;
-    for (int w = 0; w < warp; ++w)
-        base += s_w[w];
+    uint32_t base = incl - mine, base_cost = incl_cost - mine_cost;
+    for (int w = 0; w < warp; ++w) {
+        base += s_w[w].x;
+        base_cost += s_w[w].y;
+    }
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b >= a.B)
             break;
         base += s_pre[b + 1];
+        base_cost += s_cost[b + 1];
         s_pre[b + 1] = base;
+        s_cost[b + 1] = base_cost;
     }
     if (tid == 0)
-        s_pre[0] = 0;
+        s_pre[0] = s_cost[0] = 0;
     __syncthreads();
-    const uint64_t T = uint32_t(uniform(int(s_pre[a.B])));
-    const uint32_t n_ctas = uint32_t(T < gridDim.x ? T : gridDim.x);
+    const uint32_t T = uint32_t(uniform(int(s_pre[a.B])));
+    const uint32_t n_ctas = min(T, gridDim.x);
     const Parts parts = parts_of<R>(a.workspace);
-    if (blockIdx.x >= n_ctas) {
+    uint32_t begin = T, end = T;
+    if (blockIdx.x < n_ctas) {
+        const uint64_t all = uint32_t(uniform(int(s_cost[a.B])));
+        begin = block_of(a, s_pre, s_cost, uint32_t(all * blockIdx.x / n_ctas));
+        end = block_of(a, s_pre, s_cost, uint32_t(all * (blockIdx.x + 1) / n_ctas));
+        if (a.whole_items) {               // the items that begin in the range
+            begin = item_from(a, s_pre, grp, R, begin, T);
+            end = item_from(a, s_pre, grp, R, end, T);
+        }
+    }
+    Desc desc{begin, 0, 0, 0, 0, {}};
+    if (begin >= end) {
         if (tid == 0 && !a.whole_items)
-            parts.desc[blockIdx.x].parts = 0;
+            parts.desc[blockIdx.x] = desc;
         return;
     }
-    uint32_t begin = uint32_t(T * blockIdx.x / n_ctas);
-    uint32_t end = uint32_t(T * (blockIdx.x + 1) / n_ctas);
-    if (a.whole_items) {                   // the items that begin in the range
-        begin = item_from(a, s_pre, grp, R, begin, uint32_t(T));
-        end = item_from(a, s_pre, grp, R, end, uint32_t(T));
-        if (begin >= end)
-            return;
-    }
-    Desc desc{0, 0, 0, 0};
+    __syncthreads();                       // s_cost gives way to the copies
 
     // ---- copies ------------------------------------------------------------------
     // Each warp copies its own pairs.  32 lanes find the sources of 16 pairs at
@@ -511,8 +591,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
     keep(at_Q);
 
     Item it = uniform(item_at(a, s_pre, grp, R, begin));
-    if (warp < NT)
-        load_queries<D, G, NT>(a, it, grp, warp, s_q);
+    if (warp < NT) {
+        uint4 qw[NJ];
+        fetch_queries<D, NT>(a, it, grp, warp, qw);
+        place_queries<D, G, NT>(a, it, grp, warp, qw, s_q);
+    }
     __syncthreads();
     for (uint32_t cur = begin; cur < end;) {
         const uint32_t stop = min(end, it.first + it.nb);
@@ -545,12 +628,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
                     pm[nt][x][e] = 0.f;
             }
         }
-        // The keys of a pair of cells, from token `tok` on.  kMasked: some query row of the tile
+        // The keys of kCells cells, from token `tok` on.  kMasked: some query row of the tile
         // does not see all of them, or the sequence ends among them.
         const int tok_end = key_end(a, it, (it.tile * R + rows - 1) / grp);
         auto step = [&](uint32_t slot, int tok, auto masked_tag) {
             constexpr bool kMasked = decltype(masked_tag)::value;
-            constexpr int NC = 2;
+            constexpr int NC = kCells;
             constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
             // S^T = K Q^T: lane (g, c) holds tokens g, g + 8 of each cell
             uint32_t kw[NC][2][NJ];
@@ -730,6 +813,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
                     }
                 }
         };
+        auto both = [&](uint32_t slot, int tok, auto masked_tag) {
+#pragma unroll 1
+            for (int x = 0; x < 2; x += kCells)
+                step(slot + x * kCell, tok + x * kv4::kCellTokens, masked_tag);
+        };
         const int all_end = key_end(a, it, it.tile * R / grp);   // all rows see the keys below
         int tok = int(cur - it.first) * kBlock + warp * kPair;
         uint32_t k = cur - begin;
@@ -743,18 +831,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
             return !stuck;
         };
         for (; k < k_full && landed(); ++k, tok += kBlock) {
-            step(k % kStages * (2 * kCell), tok, std::false_type{});
+            both(k % kStages * (2 * kCell), tok, std::false_type{});
             __syncwarp();                  // every lane has read the cells
             fill(k + kStages);
         }
         for (; k < k_stop && landed(); ++k, tok += kBlock) {
             if (tok < tok_end)
-                step(k % kStages * (2 * kCell), tok, std::true_type{});
+                both(k % kStages * (2 * kCell), tok, std::true_type{});
             __syncwarp();
             fill(k + kStages);
         }
 
         // ---- the warps' parts joined, and written ----------------------------
+        // the next item's queries are on their way meanwhile
+        const Item next = stop < end ? next_item(a, s_pre, grp, R, it) : it;
+        uint4 qw[NJ];
+        if (warp < NT && stop < end)
+            fetch_queries<D, NT>(a, next, grp, warp, qw);
+        else
+            for (int j = 0; j < NJ; ++j)
+                qw[j] = make_uint4(0, 0, 0, 0);
         const bool whole = cur == it.first && stop == it.first + it.nb;
         const int slot = 2 * int(blockIdx.x) + (cur == it.first ? 1 : 0);
 #pragma unroll
@@ -776,7 +872,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
                 }
             }
         __syncthreads();
-        const Item next = stop < end ? uniform(item_at(a, s_pre, grp, R, stop)) : it;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             // the upper warps' rows through shared memory into the lower warps'
@@ -809,8 +904,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
                         }
                     }
                 } else if (half == 0 && nt == 0 && warp < NT && stop < end) {
-                    // meanwhile the next item's queries
-                    load_queries<D, G, NT>(a, next, grp, warp, s_q);
+                    place_queries<D, G, NT>(a, next, grp, warp, qw, s_q);
                 }
                 __syncthreads();
             }
@@ -856,17 +950,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
             __syncthreads();
         }
         if (cur == it.first && !whole) {
-            // CTAs that hold a part: up to the one whose range has the last block
-            const uint64_t x = uint64_t(it.first) + it.nb;      // ceil(x n / T) - 1
-            const int last_cta = int((x * n_ctas + T - 1) / T) - 1;
-            desc = Desc{last_cta - int(blockIdx.x) + 1, it.b, it.kvh, it.tile};
+            desc.item_end = it.first + it.nb;
+            desc.b = it.b;
+            desc.kvh = it.kvh;
+            desc.tile = it.tile;
         }
         cur = stop;
         it = next;
     }
     if (s_abort) {
         // a wait ran out: the copies under way must land before the CTA ends
-        desc.parts = 0;
+        desc.item_end = 0;
         volatile int go_on = 0;
         for (uint32_t k = done; k < min(done + kStages, n_blocks); ++k)
             ptx::mbar_wait_limited(full + k % kStages, k / kStages & 1, &go_on, a.err_word,
@@ -891,7 +985,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_kv4_join_kernel(const Kv
     __shared__ float s_y[kJoinWarps][D], s_m[kJoinWarps], s_s[kJoinWarps];
     const Parts parts = parts_of<R>(a.workspace);
     const Desc desc = parts.desc[blockIdx.x];
-    if (desc.parts == 0)
+    if (desc.item_end == 0)
         return;
     const int2 qb = queries_of(a, desc.b);
     const int grp = a.H / a.Hkv, all = qb.y * grp, row0 = desc.tile * R + blockIdx.y * kRows;
@@ -905,7 +999,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_kv4_join_kernel(const Kv
 #pragma unroll
     for (int e = 0; e < kPer; ++e)
         y[e] = 0.f;
-    const int n_parts = desc.tile * R + r < all ? desc.parts : 0;
+    // the CTAs from this one on whose range begins before the item's end
+    int n_parts = 0;
+    for (uint32_t in = ~0u; in == ~0u; n_parts += __popc(in)) {
+        const uint32_t x = blockIdx.x + n_parts + lane;
+        in = __ballot_sync(0xffffffffu, x < gridDim.x && parts.desc[x].begin < desc.item_end);
+    }
+    if (desc.tile * R + r >= all)
+        n_parts = 0;
     for (int p0 = warp % kPart; p0 < n_parts; p0 += 32 * kPart) {
         const int n = min(32, (n_parts - p0 + kPart - 1) / kPart);
         float2 ml = make_float2(kNoRef, 0.f);

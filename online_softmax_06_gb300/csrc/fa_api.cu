@@ -859,13 +859,16 @@ int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, const void
                         max_pages, seqlens, cu_seqlens, B, N, total, Hkv, d, group, false);
 }
 
-int64_t fa_attention_kv4_workspace_bytes(int Nq, int Nk, int H, int Hkv, int d)
+int64_t fa_attention_kv4_workspace_bytes(int B, int Nq, int64_t total_q, int Nk, int H, int Hkv,
+                                         int d)
 {
-    if (Nq < 0 || Nk < 0 || H < 0 || Hkv < 0 || (H > 0 && (Hkv == 0 || H % Hkv != 0)))
+    if (B < 0 || Nq < 0 || total_q < 0 || Nk < 0 || H < 0 || Hkv < 0 ||
+        (H > 0 && (Hkv == 0 || H % Hkv != 0)))
         return FA_ERR_BAD_SIZE;
     if (d != 64 && d != 128)
         return FA_ERR_UNSUPPORTED;
-    return H == 0 ? 0 : fa::kv4_attention_workspace_bytes(Nq, Nk, H, Hkv, d);
+    return B == 0 || H == 0
+               ? 0 : fa::kv4_attention_workspace_bytes(B, Nq, total_q, Nk, H, Hkv, d);
 }
 
 int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num_pages,
@@ -885,7 +888,7 @@ int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num
     if (B == 0 || Nq == 0 || total_q == 0 || H == 0)
         return FA_OK;
     // with Nk = 0 nothing of the cache is read
-    const int64_t needs = fa::kv4_attention_workspace_bytes(Nq, Nk, H, Hkv, d);
+    const int64_t needs = fa::kv4_attention_workspace_bytes(B, Nq, total_q, Nk, H, Hkv, d);
     if (!Q || !seqlens || !O || !lse || (needs > 0 && !workspace) ||
         (Nk > 0 && (!cache || !page_table)))
         return FA_ERR_NULL_POINTER;
@@ -899,7 +902,7 @@ int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num
     // counted in 32 bits
     const int rows = fa::kv4_attention_rows(Nq, H, Hkv);
     const int64_t tiles = (int64_t(Nq) * (H / Hkv) + rows - 1) / rows;
-    const int64_t blocks = Nk / 128 + 1;
+    const int64_t blocks = Nk / 128 + 3;   // and two for the item itself
     if (B > fa::kKv4MaxSeqs || total_q > (int64_t(1) << 31) - 512 || q_stride > (int64_t(1) << 31) ||
         H > 65535 || int64_t(Nq) * (H / Hkv) > (int64_t(1) << 31) - 512 ||
         double(tiles) * double(blocks) * B * Hkv > double((int64_t(1) << 31) - 512))
@@ -932,7 +935,8 @@ int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num
     a.workspace = workspace;
     a.whole_items = Nk <= fa::kKv4Short;
     a.err_word = dev->err_word;
-    return fa::launch_attention_kv4(a, fa::t_stream);
+    return fa::kv4_many(B, total_q, Nk, H, Hkv, d) ? fa::launch_attention_kv4_many(a, fa::t_stream)
+                                                   : fa::launch_attention_kv4(a, fa::t_stream);
 }
 
 int fa_attention_fwd_f32(const float *Q, const float *K, const float *V, float *O, float *lse,

@@ -29,6 +29,7 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBlocksPerSm = 5;
 
 // What a block needs to know of one of its rows.
 struct RowAt {
@@ -187,7 +188,7 @@ constexpr int kUnroll = 2;     // rows a thread has under way
 // Grid: x over the rows, rows_per_block each; y over a row's threads (2 Hkv d / 16)
 // beyond kThreads.
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     kv4_append_kernel(const Kv4CacheArgs a, int rows_per_block)
 {
     extern __shared__ RowAt at[];
@@ -273,7 +274,7 @@ __device__ __forceinline__ uint4 values_of(uint32_t code, uint32_t pair)
 
 // The same lay-out, the other way.
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     kv4_read_kernel(const Kv4CacheArgs a, int rows_per_block)
 {
     extern __shared__ RowAt at[];
@@ -329,18 +330,21 @@ __global__ void __launch_bounds__(kThreads, 4)
 template <typename F>
 int launch_rows(F kernel, const Kv4CacheArgs &a, cudaStream_t stream)
 {
-    // one row a block while that fills the SMs (a decode step's few rows), else
-    // four rounds of kUnroll rows a thread
+    // One row a block while that fills the SMs (a decode step's few rows).  Beyond,
+    // whole waves of the blocks that are resident at once, of 8 rounds or fewer
+    // each: finding its rows' pages costs a block a microsecond or two.
     const int all = 2 * a.Hkv * (a.d / 16);
-    const int side = all < kThreads ? kThreads / all : 1;
-    int rows = 4 * kUnroll * side;
-    while (rows > 1 && (a.total + rows - 1) / rows < 2 * 152)
-        rows /= 2;
+    const int side = all < kThreads ? kThreads / all : 1, round = kUnroll * side;
+    const int64_t resident = 152 * kBlocksPerSm;
+    const int64_t waves = (a.total + 8 * round * resident - 1) / (8 * round * resident);
+    int64_t rows = (a.total + waves * resident - 1) / (waves * resident);
+    if (rows > side)
+        rows = (rows + round - 1) / round * round;
     const int64_t blocks = (a.total + rows - 1) / rows;
     if (blocks > 0x7fffffffLL)
         return FA_ERR_TOO_LARGE;
     const dim3 grid(unsigned(blocks), unsigned((all + kThreads - 1) / kThreads));
-    kernel<<<grid, kThreads, rows * sizeof(RowAt), stream>>>(a, rows);
+    kernel<<<grid, kThreads, rows * sizeof(RowAt), stream>>>(a, int(rows));
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

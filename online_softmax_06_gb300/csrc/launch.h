@@ -4,6 +4,7 @@
 
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <mutex>
 
@@ -206,15 +207,58 @@ inline int kv4_attention_rows(int Nq, int H, int Hkv)
 }
 // CTAs: four on each of 152 SMs, two with the wider tiles' registers.
 __host__ __device__ constexpr int kv4_attention_ctas(int rows) { return rows <= 8 ? 608 : 304; }
-// Descriptors (16 bytes a CTA), then for two parts a CTA the (reference, sum)
-// and the fp32 O of each row.
-inline int64_t kv4_attention_workspace_bytes(int Nq, int Nk, int H, int Hkv, int d)
+
+// The form for many query rows (attn_kv4_many.cu): fp16 copies of Q ([Hkv, total_q,
+// H / Hkv, d]) and of the cache ([B, Hkv, 128 n_tiles, d] each), and their factors.
+struct Kv4ManyBuffers {
+    __half *Q, *K, *V;
+    float *q_mul, *k_mul, *v_exp;  // a row of Q, a tile of K, a tile of V
+    int n_tiles;                   // tiles of 128 keys of the longest sequence
+};
+struct Kv4ManyLayout {
+    int64_t q, k, v, q_mul, k_mul, v_exp, bytes;
+    int n_tiles;
+};
+inline Kv4ManyLayout kv4_many_layout(int B, int64_t total_q, int Nk, int H, int Hkv, int d)
 {
+    auto up = [](int64_t x) { return (x + 255) & ~int64_t(255); };
+    Kv4ManyLayout L;
+    L.n_tiles = (Nk + 127) / 128;
+    const int64_t tiles = int64_t(B) * Hkv * L.n_tiles;
+    L.q = 0;
+    L.k = up(total_q * H * d * 2);
+    L.v = L.k + up(tiles * 128 * d * 2);
+    L.q_mul = L.v + up(tiles * 128 * d * 2);
+    L.k_mul = L.q_mul + up(total_q * H * 4);
+    L.v_exp = L.k_mul + up(tiles * 4);
+    L.bytes = L.v_exp + up(tiles * 4);
+    return L;
+}
+// Whether a call takes that form: it writes the whole cache out once, which pays
+// where a sequence has 128 rows a kv head or more on average, and its CTAs take 256
+// rows each, of which there have to be enough for half of the SMs.
+inline bool kv4_many(int B, int64_t total_q, int Nk, int H, int Hkv, int d)
+{
+    const int64_t rows = total_q * (H / Hkv);          // of a kv head, all sequences
+    return rows >= int64_t(128) * B && rows / 256 * Hkv >= 76 && Nk >= 128 && B < 65535 &&
+           rows * Hkv < (int64_t(1) << 31) - 512 &&
+           double(B) * Hkv * (Nk + 127.0) < double((int64_t(1) << 31) - 512) &&
+           kv4_many_layout(B, total_q, Nk, H, Hkv, d).bytes <= int64_t(8) << 30;
+}
+
+// Workspace: that form's copies; otherwise descriptors (32 bytes a CTA), then for
+// two parts a CTA the (reference, sum) and the fp32 O of each row.
+inline int64_t kv4_attention_workspace_bytes(int B, int Nq, int64_t total_q, int Nk, int H, int Hkv,
+                                             int d)
+{
+    if (kv4_many(B, total_q, Nk, H, Hkv, d))
+        return kv4_many_layout(B, total_q, Nk, H, Hkv, d).bytes;
     if (Nk <= kKv4Short)
         return 0;
     const int rows = kv4_attention_rows(Nq, H, Hkv);
-    return int64_t(kv4_attention_ctas(rows)) * (16 + 2 * rows * (8 + 4 * d));
+    return int64_t(kv4_attention_ctas(rows)) * (32 + 2 * rows * (8 + 4 * d));
 }
+int launch_attention_kv4_many(const Kv4AttnArgs &a, cudaStream_t stream);
 int launch_attention_kv4(const Kv4AttnArgs &a, cudaStream_t stream);
 
 }  // namespace fa

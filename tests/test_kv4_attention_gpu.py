@@ -10,7 +10,10 @@ Tolerances, from the arithmetic (half a step is finfo.eps / 2 of the value: u16 
   * P s is rounded to fp16 and multiplies codes up to 15; below 2^-14 of a
     row's largest P s the step is fixed, which L <= 2^13 keys can add up to the
     same again; errors of S act on P twice (weight and sum); O is rounded:
-        |O - ref| <= 2 u16 * 15 max_j s_j + 4 eS max |v| + ub |ref|.
+        |O - ref| <= 2 u16 * 15 max_j s_j + 4 eS max |v| + ub |ref|;
+  * with many query rows K, V and P are rounded to fp16, K and V once each with
+    their tile's power of two: eS grows by scale * max_j sum_k |q_k k_jk| u16, and
+    |O - ref| by 2 u16 max |v| in the place of the first term (V's rounding and P's).
 """
 import math
 
@@ -45,7 +48,7 @@ def params(pool, b):
             float(np.nanmax(np.abs(V), initial=0)))
 
 
-def check(pool, q_rows, O, lse, scale, causal, rows=None):
+def check(pool, q_rows, O, lse, scale, causal, many=False):
     """O [total, H, d], lse [H, total] against the oracle, sequence by sequence."""
     at = 0
     for b, q in enumerate(q_rows):
@@ -58,8 +61,12 @@ def check(pool, q_rows, O, lse, scale, causal, rows=None):
         eS = 0.0
         if len(K) and n:
             for h in range(H):
-                eS = max(eS, scale * float(np.nanmax(np.abs(q[:, h]) @ k_abs[:, h // (H // pool.Hkv)].T))
-                         * 2.0 ** -19)
+                eS0 = abs(scale) * float(np.nanmax(np.abs(q[:, h]) @ k_abs[:, h // (H // pool.Hkv)].T)) \
+                    * 2.0 ** -19
+                eS = max(eS, eS0)
+                if many:
+                    eS = max(eS, abs(scale) * float(np.nanmax(
+                        np.abs(q[:, h]) @ np.abs(K[:, h // (H // pool.Hkv)]).T)) * 2.0 ** -11 + eS0)
         assert np.array_equal(np.isneginf(l), np.isneginf(lr)), b
         assert np.array_equal(np.isnan(l), np.isnan(lr)), b
         fin = np.isfinite(lr)
@@ -68,7 +75,8 @@ def check(pool, q_rows, O, lse, scale, causal, rows=None):
         assert np.array_equal(np.isnan(o), np.isnan(Or)), b
         ok = ~np.isnan(Or)
         err = np.abs(o[ok] - Or[ok])
-        tol = 2.0 ** -10 * 15 * s_v + 4 * eS * v_max + 2.0 ** -8 * np.abs(Or[ok])
+        tol = 4 * eS * v_max + 2.0 ** -8 * np.abs(Or[ok]) + \
+            (2.0 ** -10 * v_max if many else 2.0 ** -10 * 15 * s_v)
         assert (err <= tol).all(), (b, (err - tol).max(), err.max())
 
 
@@ -264,7 +272,7 @@ def test_fused_query_rows_and_given_buffers():
     pool, q = make([3000, 40], 3, 4, 2, 128, 64, 32, seed=171)
     O, lse = run(pool, q, True, False)
     check(pool, q, O, lse, 1 / math.sqrt(128), True)
-    ws = torch.full((fa.fa_attention_kv4_workspace_bytes(3, 3000, 4, 2, 128),), 0xff,
+    ws = torch.full((fa.fa_attention_kv4_workspace_bytes(2, 3, 6, 3000, 4, 2, 128),), 0xff,
                     dtype=torch.uint8, device="cuda")
     o2, l2 = fa.attention_kv4(gpu_bf16(np.stack(q)), torch.from_numpy(pool.bytes).cuda(),
                               gpu_i32(pool.table), gpu_i32([3000, 40]), workspace=ws,
@@ -451,4 +459,151 @@ def test_helper_refusals():
         fa.attention_kv4(torch.zeros(B, 1, 4, 128, dtype=torch.bfloat16, device="cuda"), cache,
                          torch.zeros(B, 2, dtype=torch.int32, device="cuda"),
                          torch.zeros(B, dtype=torch.int32, device="cuda"))
+    device_error_clear()
+
+
+# ---- many query rows: the cache's values through fp16 and the tcgen05 kernel --------
+
+def takes_many(pool, q_rows, bound):
+    B, total = len(q_rows), sum(len(q) for q in q_rows)
+    H, d = q_rows[0].shape[1:]
+    L = fa.fa_attention_kv4_workspace_bytes(B, max(len(q) for q in q_rows), total, bound, H, pool.Hkv, d)
+    return L > total * H * d * 2 + 4 * B * pool.Hkv * bound * d
+
+
+MANY = [
+    # lens, queries, H, Hkv, d, group, page, causal, packed
+    ([700, 513, 64], [700, 600, 64], 16, 16, 64, 64, 48, True, True),
+    ([900, 300], [500, 160], 32, 8, 128, 32, 64, True, True),
+    ([260, 700], [700, 160], 24, 8, 128, 128, 16, True, True),   # more queries than keys
+    ([260, 700], [700, 160], 24, 8, 128, 64, 128, False, True),
+    ([129, 640], 640, 16, 16, 64, 32, 32, True, False),
+    ([0, 1, 1300], [300, 300, 700], 16, 16, 128, 64, 16, True, True),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=[str(i) for i in range(len(MANY))])
+def test_many_rows_against_the_oracle(case):
+    lens, Nq, H, Hkv, d, group, page, causal, packed = case
+    pool, q = make(lens, Nq, H, Hkv, d, group, page, seed=300)
+    assert takes_many(pool, q, pool.table.shape[1] * page)
+    O, lse = run(pool, q, causal, packed)
+    check(pool, q, O, lse, 1 / math.sqrt(d), causal, many=True)
+    O1, l1 = run(pool, q, causal, packed)
+    assert torch.equal(O, O1) and torch.equal(lse, l1)
+    device_error_clear()
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0])
+def test_many_rows_other_scales(scale):
+    pool, q = make([400, 200], [400, 240], 32, 8, 64, 64, 32, seed=310)
+    O, lse = run(pool, q, True, True, scale=scale)
+    check(pool, q, O, lse, scale, True, many=True)
+    small, q1 = make([90], 2, 4, 2, 64, 64, 32, seed=311)         # and the few rows' form
+    O, lse = run(small, q1, True, False, scale=scale)
+    check(small, q1, O, lse, scale, True)
+    device_error_clear()
+
+
+def test_many_rows_scales_of_the_inputs():
+    """Rows of Q, and tiles of K and V, of magnitudes far from 1 and from one another."""
+    d, L, n = 128, 400, 160
+    rng = np.random.default_rng(320)
+    pool = Pool([L], 16, d, 64, 16, seed=321)
+    k, v = bf16_rows(rng, L, 16, d), bf16_rows(rng, L, 16, d)
+    k[:128] *= 2.0 ** -30
+    k[128:256] *= 2.0 ** 20
+    v[:128] *= 2.0 ** 40
+    v[256:] *= 2.0 ** -20
+    q = bf16_rows(rng, n * 9, 16, d)
+    q[::3] *= 2.0 ** -25
+    q[1::3] *= 2.0 ** -40
+    q[2::3] *= 2.0 ** -60
+    pool.fill([k], [v])
+    O, lse = run(pool, [q], False, True, scale=0.1)
+    assert takes_many(pool, [q], pool.table.shape[1] * 16)
+    check(pool, [q], O, lse, 0.1, False, many=True)
+
+
+def test_many_rows_nan_behind_the_mask():
+    d, L, n = 64, 300, 160
+    pool, q = make([L, 200], [n * 6, n * 4], 8, 8, d, 64, 16, seed=330)
+    q = [x[:, :8] for x in q]
+    clean, _ = make([L, 200], [n * 6, n * 4], 8, 8, d, 64, 16, seed=330)
+    rng = np.random.default_rng(331)
+    bad = bf16_rows(rng, 2, 8, d)
+    bad[:, :, 5] = np.nan
+    kv4.write(pool.bytes, pool.table[0], np.array([L - 2, L - 1]), bf16_rows(rng, 2, 8, d), bad, 16, 64)
+    x = [np.repeat(a, 2, 1) for a in q]                             # 16 heads on 8
+    assert takes_many(pool, x, pool.table.shape[1] * 16)
+    O, lse = run(pool, x, True, True)
+    O1, l1 = run(clean, x, True, True)
+    n0 = len(x[0])
+    # sequence 0's queries but the last two, and all of sequence 1, do not see them
+    keep = torch.ones(O.shape[0], dtype=torch.bool)
+    keep[n0 - 2:n0] = False
+    assert torch.equal(O[keep], O1[keep]) and torch.equal(lse[:, keep], l1[:, keep])
+    assert torch.isnan(O[n0 - 2:n0]).all()
+    device_error_clear()
+
+
+def test_many_rows_bad_lengths_and_pages_and_the_rest_stays():
+    pool, q = make([300, 200, 256], [300, 200, 256], 32, 8, 64, 64, 16, seed=340)
+    x = np.concatenate(q + [np.ones((5, 32, 64))])
+    cache, table = torch.from_numpy(pool.bytes).cuda(), pool.table.copy()
+    cu = [0, 300, 500, 756]
+    out = torch.full((761, 32, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((32, 761), 9.0, device="cuda")
+
+    def call(lens, tab, cu=cu):
+        out.fill_(9.0)
+        lse.fill_(9.0)
+        fa.attention_kv4(gpu_bf16(x), cache, gpu_i32(tab), gpu_i32(lens), cu_seqlens=gpu_i32(cu),
+                         max_q=300, max_seqlen=300, out=out, lse=lse)
+        return fa.fa_get_device_error()
+
+    def first(n):
+        sub = Pool.__new__(Pool)
+        sub.__dict__.update(pool.__dict__, lengths=pool.lengths[:n])
+        m = cu[n]
+        check(sub, q[:n], out[:m], lse[:, :m], 1 / 8, True, many=True)
+
+    assert call([300, 200, 256], table) == 0
+    first(3)
+    assert (out[756:] == 9).all() and (lse[:, 756:] == 9).all()
+    for bad in (301, -1):
+        assert call([300, 200, bad], table) == fa.FA_DEVERR_BAD_SEQLENS
+        first(2)
+        assert (out[500:] == 9).all() and (lse[:, 500:] == 9).all()
+    table[2, 3] = pool.num_pages
+    assert call([300, 200, 256], table) == fa.FA_DEVERR_BAD_PAGE
+    first(2)
+    assert torch.isfinite(out[500:756]).all()
+    assert call([300, 200, 256], pool.table, [0, 301, 500, 756]) == fa.FA_DEVERR_BAD_SEQLENS
+
+
+def test_many_rows_in_a_graph_on_a_stream():
+    pool, q = make([300, 640], [300, 1000], 16, 16, 64, 64, 16, seed=350)
+    assert takes_many(pool, q, 640)
+    O, lse = run(pool, q, True, True)
+    cache, table, sl = torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table), gpu_i32([300, 640])
+    x, cu = gpu_bf16(np.concatenate(q)), gpu_i32([0, 300, 1300])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        fa.attention_kv4(x, cache, table, sl, cu_seqlens=cu, max_q=1000)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        og, lg = fa.attention_kv4(x, cache, table, sl, cu_seqlens=cu, max_q=1000)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(og, O) and torch.equal(lg, lse)
+    x.neg_()
+    sl.copy_(gpu_i32([123, 640]))
+    g.replay()
+    torch.cuda.synchronize()
+    sub = Pool.__new__(Pool)
+    sub.__dict__.update(pool.__dict__, lengths=[123, 640])
+    check(sub, [-y for y in q], og, lg, 1 / 8, True, many=True)
     device_error_clear()

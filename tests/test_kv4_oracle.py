@@ -178,16 +178,22 @@ def test_helper_refusals_without_gpu():
 
 def test_attention_refusals_without_gpu():
     wb = fa.fa_attention_kv4_workspace_bytes
-    assert wb(-1, 5000, 8, 2, 128) == fa.FA_ERR_BAD_SIZE
-    assert wb(1, 5000, 9, 2, 128) == fa.FA_ERR_BAD_SIZE
-    assert wb(1, 5000, 8, 0, 128) == fa.FA_ERR_BAD_SIZE
-    assert wb(1, 5000, 8, 2, 96) == fa.FA_ERR_UNSUPPORTED
+    assert wb(1, -1, 1, 5000, 8, 2, 128) == fa.FA_ERR_BAD_SIZE
+    assert wb(1, 1, 1, 5000, 9, 2, 128) == fa.FA_ERR_BAD_SIZE
+    assert wb(1, 1, 1, 5000, 8, 0, 128) == fa.FA_ERR_BAD_SIZE
+    assert wb(1, 1, 1, 5000, 8, 2, 96) == fa.FA_ERR_UNSUPPORTED
     # a descriptor and two parts a CTA, of 8 rows (608 CTAs) or 16 (304)
     for Nq, rows in ((1, 8), (2, 8), (3, 16), (4, 16), (5, 16), (500, 16)):
-        assert wb(Nq, 1025, 8, 2, 128) == (608 if rows == 8 else 304) * (16 + 2 * rows * (8 + 512))
+        assert wb(1, Nq, Nq, 1025, 8, 2, 128) == (608 if rows == 8 else 304) * (32 + 2 * rows * (8 + 512))
 
-    assert wb(1, 1024, 8, 2, 128) == 0                     # whole heads: no parts
-    assert wb(1, -1, 8, 2, 128) == fa.FA_ERR_BAD_SIZE
+    assert wb(1, 1, 1, 1024, 8, 2, 128) == 0                     # whole heads: no parts
+    assert wb(1, 1, 1, -1, 8, 2, 128) == fa.FA_ERR_BAD_SIZE
+
+    # many rows: fp16 Q [total, H, d], K and V [B, Hkv, tiles of 128, d], the factors
+    up = lambda x: -(-x // 256) * 256  # noqa: E731
+    assert wb(3, 900, 2000, 1000, 32, 8, 128) == (
+        up(2000 * 32 * 256) + 2 * 3 * 8 * 1024 * 256 + up(2000 * 32 * 4) + 2 * up(3 * 8 * 8 * 4))
+    assert wb(64, 1, 64, 1000, 32, 8, 128) == 0
 
     def go(q=256, qs=1024, cache=256, pages=4, ps=16, table=256, mp=80, lens=256, cu=None, o=256,
            lse=256, B=1, Nq=1, total=1, Nk=1100, H=8, Hkv=2, d=128, group=64, ws=256, wsb=1 << 30):
