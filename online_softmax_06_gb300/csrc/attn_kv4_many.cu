@@ -102,21 +102,24 @@ __device__ __forceinline__ uint4 values_of(uint32_t code, __half2 s, __half2 m)
                       __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
 }
 
-// Grid (tiles of the longest sequence, Hkv, B + 1): block (j, h, b) writes the K and
-// V tile of keys 128 j .. of head h of sequence b, zeros behind its end; the blocks
-// with z = B the queries.
+// Grid (tiles of the longest sequence, Hkv, B + some): block (j, h, b) writes the K
+// and V tile of keys 128 j .. of head h of sequence b, zeros behind its end; the
+// blocks with z >= B the queries.
 template <int D, int G>
 __global__ void __launch_bounds__(kExpandThreads, 4)
     kv4_expand_kernel(const Kv4AttnArgs a, const Kv4ManyBuffers w)
 {
     constexpr int kCell = kv4::cell_bytes(D, G), NG = D / G, kN = D / 32, kLanes = D / 16;
     const int tid = threadIdx.x, lane = tid & 31, grp = a.H / a.Hkv;
-    if (blockIdx.z == unsigned(a.B)) {
+    if (blockIdx.z >= unsigned(a.B)) {
         // queries: a warp a row of a head
         constexpr int kPer = D / 32;
-        const int64_t all = a.total_q * a.H, step = int64_t(gridDim.x) * gridDim.y * (kExpandThreads / 32);
-        for (int64_t x = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (kExpandThreads / 32) + tid / 32;
-             x < all; x += step) {
+        constexpr int kRows = kExpandThreads / 32;
+        const int64_t all = a.total_q * a.H;
+        const int64_t step = int64_t(gridDim.x) * gridDim.y * (gridDim.z - a.B) * kRows;
+        const int64_t block = (int64_t(blockIdx.z - a.B) * gridDim.y + blockIdx.y) * gridDim.x +
+                              blockIdx.x;
+        for (int64_t x = block * kRows + tid / 32; x < all; x += step) {
             const int64_t tok = x / a.H;
             const int head = int(x - tok * a.H);
             const auto *src = static_cast<const __nv_bfloat16 *>(a.Q) + tok * a.q_stride +
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(kExpandThreads, 4)
     const int n = min(BN, seq.L - tok0);
     __shared__ const uint8_t *s_cell[BN / kv4::kCellTokens];
     __shared__ float s_big[2][kExpandThreads / 32];
-    __shared__ uint8_t s_nan[BN];
+    __shared__ uint8_t s_nan[BN];      // tokens whose V is not finite
     if (tid < BN)
         s_nan[tid] = 0;
     if (tid < BN / kv4::kCellTokens) {
@@ -169,27 +172,57 @@ __global__ void __launch_bounds__(kExpandThreads, 4)
         s_cell[tid] = cell;
     }
     __syncthreads();
-    // the largest magnitude that the tile's parameters allow
+    // Everything that the thread converts is loaded first (the layout of
+    // kv4_cache.cu: 16 values a thread, K then V), so that the largest magnitude
+    // that the tile's parameters allow comes from registers.
+    constexpr int kRounds = BN * kLanes / kExpandThreads;          // of K, and as many of V
+    constexpr int kPairs = G == 32 ? 2 : 1;
+    uint32_t code[2][kRounds][2], pair[2][kRounds][kPairs];
     float big[2] = {0.f, 0.f};
-    for (int x = tid; x < n * NG; x += kExpandThreads) {
-        const int t = x / NG;
-        const uint8_t *cell = s_cell[t / 16];
-        if (cell == nullptr)
-            continue;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t p = *reinterpret_cast<const uint32_t *>(
-                cell + (kv ? kv4::v_par_off(D, G) : kv4::k_par_off(D)) +
-                (t % 16 * NG + x % NG) * 4);
-            const float m = bf16_hi(p), top = fmaf(15.f, bf16_lo(p), m);
-            if (fabsf(m) < INFINITY && fabsf(top) < INFINITY)
-                big[kv] = ptx::max3(big[kv], fabsf(m), fabsf(top));
-            else if (kv)
-                s_nan[t] = 1;
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int x = 0; x < kRounds; ++x) {
+            const int l = tid % kLanes, t = tid / kLanes + x * (kExpandThreads / kLanes);
+            const int jj = l / 4, c = l % 4;
+            const uint8_t *cell = t < n ? s_cell[t / 16] : nullptr;
+            code[kv][x][0] = code[kv][x][1] = 0;
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i)
+                pair[kv][x][i] = 0;
+            if (cell == nullptr)
+                continue;
+            if (kv) {
+                const uint8_t *from =
+                    cell + kv4::v_off(D) + kv4::v_swizzle(t % 16 * (D / 2) + c * (kN * 4) + jj * 4);
+                code[kv][x][0] = *reinterpret_cast<const uint32_t *>(from);
+                code[kv][x][1] = *reinterpret_cast<const uint32_t *>(from + kN * 2);
+            } else {
+                const uint2 z = *reinterpret_cast<const uint2 *>(cell + t % 16 * (D / 2) +
+                                                                 (c * kN + 2 * jj) * 4);
+                code[kv][x][0] = z.x;
+                code[kv][x][1] = z.y;
+            }
+            const auto *par = reinterpret_cast<const uint32_t *>(
+                                  cell + (kv ? kv4::v_par_off(D, G) : kv4::k_par_off(D))) +
+                              t % 16 * NG + (G == 32 ? 2 * jj : G == 64 ? jj : 0);
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i)
+                pair[kv][x][i] = par[i];
         }
-    }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+        for (int x = 0; x < kRounds; ++x)
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                const uint32_t p = pair[kv][x][i];
+                const float m = bf16_hi(p), top = fmaf(15.f, bf16_lo(p), m);
+                if (fabsf(m) < INFINITY && fabsf(top) < INFINITY)
+                    big[kv] = ptx::max3(big[kv], fabsf(m), fabsf(top));
+                else if (kv)
+                    s_nan[tid / kLanes + x * (kExpandThreads / kLanes)] = 1;
+            }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             big[kv] = fmaxf(big[kv], __shfl_xor_sync(0xffffffffu, big[kv], o));
@@ -197,57 +230,44 @@ __global__ void __launch_bounds__(kExpandThreads, 4)
             s_big[kv][tid / 32] = big[kv];
     }
     __syncthreads();
-    int e[2];
+    const int64_t bh = int64_t(b) * a.Hkv + h;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-        float x = s_big[kv][0];
+        float top = s_big[kv][0];
 #pragma unroll
         for (int i = 1; i < kExpandThreads / 32; ++i)
-            x = fmaxf(x, s_big[kv][i]);
-        e[kv] = exponent_of(x);
-    }
-    const int64_t bh = int64_t(b) * a.Hkv + h;
-    if (tid == 0) {
-        w.k_mul[bh * w.n_tiles + blockIdx.x] = pow2(e[0]);
-        w.v_exp[bh * w.n_tiles + blockIdx.x] = float(e[1]);
-    }
-    // the layout of kv4_cache.cu: 16 values a thread
-    const float up[2] = {pow2(-e[0]), pow2(-e[1])};
-    for (int x = tid; x < BN * kLanes * 2; x += kExpandThreads) {
-        const int l = x % kLanes, t = x / kLanes % BN, jj = l / 4, c = l % 4;
-        const bool is_v = x >= BN * kLanes;
-        const uint8_t *cell = s_cell[t / 16];
-        uint4 y0 = make_uint4(0, 0, 0, 0), y1 = y0;
-        if (t < n && cell != nullptr) {
-            uint32_t c0, c1;
-            if (is_v) {
-                const uint8_t *from =
-                    cell + kv4::v_off(D) + kv4::v_swizzle(t % 16 * (D / 2) + c * (kN * 4) + jj * 4);
-                const uint32_t z0 = *reinterpret_cast<const uint32_t *>(from);
-                const uint32_t z1 = *reinterpret_cast<const uint32_t *>(from + kN * 2);
-                c0 = __byte_perm(z0, z1, 0x5410);
-                c1 = __byte_perm(z0, z1, 0x7632);
-            } else {
-                const uint2 z = *reinterpret_cast<const uint2 *>(cell + t % 16 * (D / 2) +
-                                                                 (c * kN + 2 * jj) * 4);
-                c0 = z.x;
-                c1 = z.y;
-            }
-            const auto *par = reinterpret_cast<const uint32_t *>(
-                                  cell + (is_v ? kv4::v_par_off(D, G) : kv4::k_par_off(D))) +
-                              t % 16 * NG + (G == 32 ? 2 * jj : G == 64 ? jj : 0);
-            const uint32_t p0 = par[0], p1 = G == 32 ? par[1] : p0;
-            const float u = up[is_v];
-            y0 = values_of(c0, __float2half2_rn(bf16_lo(p0) * u), __float2half2_rn(bf16_hi(p0) * u));
-            y1 = values_of(c1, __float2half2_rn(bf16_lo(p1) * u), __float2half2_rn(bf16_hi(p1) * u));
-            if (s_nan[t]) {
-                const uint32_t fill = is_v ? 0u : 0x7e007e00u;
-                y0 = y1 = make_uint4(fill, fill, fill, fill);
-            }
+            top = fmaxf(top, s_big[kv][i]);
+        const int e = exponent_of(top);
+        if (tid == 0) {
+            float2 &f = w.tile[bh * w.n_tiles + blockIdx.x];
+            if (kv)
+                f.y = float(e);
+            else
+                f.x = pow2(e);
         }
-        __half *dst = (is_v ? w.V : w.K) + (bh * w.n_tiles * BN + tok0 + t) * D + (8 * jj + c) * 8;
-        *reinterpret_cast<uint4 *>(dst) = y0;
-        *reinterpret_cast<uint4 *>(dst + 32) = y1;
+        const float up = pow2(-e);
+#pragma unroll
+        for (int x = 0; x < kRounds; ++x) {
+            const int l = tid % kLanes, t = tid / kLanes + x * (kExpandThreads / kLanes);
+            uint4 y[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t z = code[kv][x][i], other = code[kv][x][i ^ 1];
+                // V: the halves of two stored words
+                const uint32_t u = !kv ? z : i == 0 ? __byte_perm(z, other, 0x5410)
+                                                    : __byte_perm(other, z, 0x7632);
+                const uint32_t p = pair[kv][x][kPairs == 2 ? i : 0];
+                y[i] = values_of(u, __float2half2_rn(bf16_lo(p) * up), __float2half2_rn(bf16_hi(p) * up));
+            }
+            if (s_nan[t]) {
+                const uint32_t fill = kv ? 0u : 0x7e007e00u;
+                y[0] = y[1] = make_uint4(fill, fill, fill, fill);
+            }
+            __half *dst = (kv ? w.V : w.K) + (bh * w.n_tiles * BN + tok0 + t) * D +
+                          (8 * (l / 4) + l % 4) * 8;
+            *reinterpret_cast<uint4 *>(dst) = y[0];
+            *reinterpret_cast<uint4 *>(dst + 32) = y[1];
+        }
     }
 }
 
@@ -315,10 +335,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + (C::kBarBytes / 8));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    // ---- work item: (sequence, kv head, pair of Q tiles), last pairs first --------
+    // ---- work item: (sequence, kv head, pair of Q tiles, range of p.w.chunk key
+    //      tiles), last pairs first ----------------------------------------------------
     const Kv4AttnArgs &a = p.a;
     const int bh_count = a.B * a.Hkv, grp = a.H / a.Hkv;
-    const int pair = p.n_pairs - 1 - int(blockIdx.x) / bh_count, bh = int(blockIdx.x) % bh_count;
+    const int split = int(blockIdx.x) % p.w.splits, rest = int(blockIdx.x) / p.w.splits;
+    const int pair = p.n_pairs - 1 - rest / bh_count, bh = rest % bh_count;
     const int b = bh / a.Hkv, h = bh % a.Hkv;
     Seq seq;
     if (!seq_of(a, b, false, seq))
@@ -337,7 +359,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int last = last_key(min(rows, (qt + 1) * BM) - 1);
         return last < 0 ? 0 : min(n_kv, last / BN + 1);
     };
-    const int n0 = tiles_seen(qt0), n1 = tiles_seen(qt0 + 1);
+    const int all0 = tiles_seen(qt0), all1 = tiles_seen(qt0 + 1);
+    const int all = all0 > all1 ? all0 : all1, j0 = split * p.w.chunk;
+    if (split > 0 && j0 >= all)
+        return;
+    const bool parts = all > p.w.chunk;        // the item has further ranges
+    const int n0 = max(0, min(all0 - j0, p.w.chunk)), n1 = max(0, min(all1 - j0, p.w.chunk));
     const int n_max = n0 > n1 ? n0 : n1;
 
     auto store_lse = [&](int x, float lse) {
@@ -386,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 last_phase[s] = -1;
             bool q_issued[2] = {false, false};
             const int q_row = int((int64_t(h) * a.total_q + seq.q0) * grp);
-            const int k_row = bh * p.w.n_tiles * BN;
+            const int k_row = (bh * p.w.n_tiles + j0) * BN;
             auto load_q = [&](int t) {
                 q_issued[t] = true;
                 ptx::mbar_arrive_expect_tx(&q_full[t], C::kTileBytes);
@@ -556,16 +583,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool row_ok = x < rows;
         const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_bits + col_s(t), tO = tmem + lane_bits + col_o<D>(t);
-        const float *k_mul = p.w.k_mul + int64_t(bh) * p.w.n_tiles;
-        const float *v_exp = p.w.v_exp + int64_t(bh) * p.w.n_tiles;
+        const int tile0 = bh * p.w.n_tiles + j0;
         const float sl = row_ok
             ? p.w.q_mul[(int64_t(h) * a.total_q + seq.q0) * grp + x] : 0.f;
-        const int last = last_key(x), last_first = last_key(qt * BM);
+        // relative to the range's first key
+        const int last = last_key(x) - j0 * BN, last_first = last_key(qt * BM) - j0 * BN;
         float m = -INFINITY, l = 0.f;
 
         for (int j = 0; j < n_t; ++j) {
             // (a factor of 0 would make NaN of the mask's -inf)
-            const float slj = fmaxf(sl * k_mul[j], 1.2e-38f), f = v_exp[j];
+            const float2 factor = p.w.tile[tile0 + j];
+            const float slj = fmaxf(sl * factor.x, 1.2e-38f), f = factor.y;
             if (!ptx::mbar_wait(&s_full[t], uint32_t(j) & 1u, abort_flag, a.err_word)) {
                 aborted = true;
                 break;
@@ -638,8 +666,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 
         // ---- epilogue: O = O~ / l (bf16), lse = (m + log2 l) ln 2 --------------------
+        const int64_t part = int64_t(split) * a.total_q * a.H +
+                             (int64_t(h) * a.total_q + seq.q0) * grp + x;
         if (n_t == 0) {
-            if (row_ok) {
+            if (row_ok && parts) {
+                p.w.ml[part] = make_float2(-INFINITY, 0.f);
+            } else if (row_ok) {
                 uint4 *dst = reinterpret_cast<uint4 *>(out_row(x));
 #pragma unroll
                 for (int q = 0; q < D / 8; ++q)
@@ -657,6 +689,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tmem_wait_ld();
                 if (!row_ok)
                     continue;
+                if (parts) {
+                    float4 *dst = reinterpret_cast<float4 *>(p.w.O_part + part * D + c * 32);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        dst[q] = make_float4(__uint_as_float(o[4 * q + 0]),
+                                             __uint_as_float(o[4 * q + 1]),
+                                             __uint_as_float(o[4 * q + 2]),
+                                             __uint_as_float(o[4 * q + 3]));
+                    continue;
+                }
                 uint4 *dst = reinterpret_cast<uint4 *>(out_row(x) + c * 32);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -672,7 +714,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     dst[q] = y;
                 }
             }
-            if (row_ok)
+            if (row_ok && parts)
+                p.w.ml[part] = make_float2(m, l);
+            else if (row_ok)
                 store_lse(x, any ? (m + log2f(l)) * kLn2 : -INFINITY);
         }
     }
@@ -683,6 +727,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after_sync();
     if (warp == kWarpMma)
         ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the ranges of the items that have several, in their order: block (x, y)
+// takes every eighth eight rows of item x, a warp a row.
+template <int D>
+__global__ void __launch_bounds__(kExpandThreads) kv4_many_join_kernel(const ManyParams p)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Kv4AttnArgs &a = p.a;
+    const int grp = a.H / a.Hkv, bh = int(blockIdx.x) % (a.B * a.Hkv), b = bh / a.Hkv, h = bh % a.Hkv;
+    Seq seq;
+    if (!seq_of(a, b, false, seq))
+        return;
+    const int rows = seq.nq * grp, x0 = int(blockIdx.x) / (a.B * a.Hkv) * 2 * BM;
+    const int x1 = min(rows, x0 + 2 * BM), lane = threadIdx.x & 31;
+    if (x0 >= x1)
+        return;
+    const int last = a.causal ? min(seq.L, seq.L - seq.nq + (x1 - 1) / grp + 1) : seq.L;
+    const int n = (((last + BN - 1) / BN) + p.w.chunk - 1) / p.w.chunk;
+    if (last <= 0 || n <= 1)
+        return;
+    constexpr int kPer = D / 32;
+    for (int x = x0 + int(blockIdx.y * kExpandThreads + threadIdx.x) / 32; x < x1;
+         x += int(gridDim.y) * (kExpandThreads / 32)) {
+        const int64_t row = (int64_t(h) * a.total_q + seq.q0) * grp + x, step = a.total_q * a.H;
+        float m = -INFINITY, l = 0.f, y[kPer];
+        for (int s = 0; s < n; ++s)
+            m = fmaxf(m, p.w.ml[s * step + row].x);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            y[e] = 0.f;
+        for (int s = 0; s < n; ++s) {
+            const float2 ml = p.w.ml[s * step + row];
+            if (ml.x == -INFINITY)             // nothing seen, nothing written
+                continue;
+            const float f = ptx::ex2(ml.x - m);
+            l = fmaf(ml.y, f, l);
+            const float *src = p.w.O_part + (s * step + row) * D + lane * kPer;
+#pragma unroll
+            for (int e = 0; e < kPer; e += 2) {
+                const float2 z = *reinterpret_cast<const float2 *>(src + e);
+                y[e] = fmaf(z.x, f, y[e]);
+                y[e + 1] = fmaf(z.y, f, y[e + 1]);
+            }
+        }
+        const bool any = l > 0.f || l != l;
+        const float inv = any ? 1.f / l : 0.f;
+        const int i = x / grp, head = h * grp + x % grp;
+        auto *dst = static_cast<__nv_bfloat16 *>(a.O) + (int64_t(seq.q0 + i) * a.H + head) * D +
+                    lane * kPer;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2)
+            *reinterpret_cast<uint32_t *>(dst + e) = ptx::pack_bf16x2(y[e] * inv, y[e + 1] * inv);
+        if (lane == 0)
+            a.lse[a.cu_seqlens_q ? int64_t(head) * a.total_q + seq.q0 + i
+                                 : (int64_t(b) * a.H + head) * a.Nq + i] =
+                any ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
 }
 
 template <int D, int G>
@@ -696,19 +798,26 @@ int launch(const Kv4AttnArgs &a, cudaStream_t stream)
     p.w.K = reinterpret_cast<__half *>(ws + at.k);
     p.w.V = reinterpret_cast<__half *>(ws + at.v);
     p.w.q_mul = reinterpret_cast<float *>(ws + at.q_mul);
-    p.w.k_mul = reinterpret_cast<float *>(ws + at.k_mul);
-    p.w.v_exp = reinterpret_cast<float *>(ws + at.v_exp);
+    p.w.tile = reinterpret_cast<float2 *>(ws + at.tile);
+    p.w.O_part = reinterpret_cast<float *>(ws + at.O_part);
+    p.w.ml = reinterpret_cast<float2 *>(ws + at.ml);
     p.w.n_tiles = at.n_tiles;
+    p.w.splits = at.splits;
+    p.w.chunk = at.chunk;
     const int64_t k_rows = int64_t(a.B) * a.Hkv * at.n_tiles * BN;
     if (!make_tmap_bf16(&p.tm_q, p.w.Q, a.total_q * a.H, 1, D) ||
         !make_tmap_bf16(&p.tm_k, p.w.K, k_rows, 1, D) || !make_tmap_bf16(&p.tm_v, p.w.V, k_rows, 1, D))
         return FA_ERR_CUDA;
     const int64_t rows = int64_t(a.Nq) * (a.H / a.Hkv);
     p.n_pairs = int((rows + 2 * BM - 1) / (2 * BM));
-    const int64_t blocks = int64_t(p.n_pairs) * a.B * a.Hkv;
+    const int64_t items = int64_t(p.n_pairs) * a.B * a.Hkv, blocks = items * at.splits;
     if (blocks > 0x7fffffffLL)
         return FA_ERR_TOO_LARGE;
-    kv4_expand_kernel<D, G><<<dim3(at.n_tiles, a.Hkv, a.B + 1), kExpandThreads, 0, stream>>>(a, p.w);
+    // about four rows of Q a warp
+    const int64_t per_layer = int64_t(at.n_tiles) * a.Hkv * (kExpandThreads / 32) * 4;
+    const int64_t layers = (a.total_q * a.H + per_layer - 1) / per_layer;
+    const dim3 grid(at.n_tiles, a.Hkv, unsigned(a.B + (layers < 1024 ? layers : 1024)));
+    kv4_expand_kernel<D, G><<<grid, kExpandThreads, 0, stream>>>(a, p.w);
     if (cudaGetLastError() != cudaSuccess)
         return FA_ERR_CUDA;
     auto kern = attn_kv4_many_kernel<D>;
@@ -725,7 +834,13 @@ int launch(const Kv4AttnArgs &a, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e == cudaSuccess && at.splits > 1) {
+        cfg.gridDim = dim3(unsigned(items), 8);
+        cfg.blockDim = dim3(kExpandThreads);
+        cfg.dynamicSmemBytes = 0;
+        e = cudaLaunchKernelEx(&cfg, kv4_many_join_kernel<D>, p);
+    }
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

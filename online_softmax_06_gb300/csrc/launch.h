@@ -212,38 +212,63 @@ __host__ __device__ constexpr int kv4_attention_ctas(int rows) { return rows <= 
 // H / Hkv, d]) and of the cache ([B, Hkv, 128 n_tiles, d] each), and their factors.
 struct Kv4ManyBuffers {
     __half *Q, *K, *V;
-    float *q_mul, *k_mul, *v_exp;  // a row of Q, a tile of K, a tile of V
+    float *q_mul;                  // a row of Q's factor
+    float2 *tile;                  // a tile's: K's, and the exponent of V's
+    float *O_part;                 // with splits > 1: [splits, rows of Q, d], unnormalised
+    float2 *ml;                    // and [splits, rows of Q]: (reference, sum)
     int n_tiles;                   // tiles of 128 keys of the longest sequence
+    int splits, chunk;             // ranges of `chunk` tiles that its keys are cut into
 };
 struct Kv4ManyLayout {
-    int64_t q, k, v, q_mul, k_mul, v_exp, bytes;
-    int n_tiles;
+    int64_t q, k, v, q_mul, tile, O_part, ml, bytes;
+    int n_tiles, splits, chunk;
 };
+// CTAs of 256 rows of a kv head, as far as the host can tell.
+inline int64_t kv4_many_items(int B, int64_t total_q, int H, int Hkv)
+{
+    const int64_t pairs = (total_q * (H / Hkv) + 255) / 256;
+    return (pairs > B ? pairs : B) * Hkv;
+}
 inline Kv4ManyLayout kv4_many_layout(int B, int64_t total_q, int Nk, int H, int Hkv, int d)
 {
     auto up = [](int64_t x) { return (x + 255) & ~int64_t(255); };
     Kv4ManyLayout L;
     L.n_tiles = (Nk + 127) / 128;
+    // The CTAs (256 rows of a kv head each) should come to two and a half waves of
+    // 152, so that long sequences and the last wave do not leave SMs idle; a range
+    // has 16 tiles at least, which pays for its part.
+    const int64_t items = kv4_many_items(B, total_q, H, Hkv);
+    int64_t splits = items > 0 ? (380 + items - 1) / items : 1;
+    splits = splits < L.n_tiles / 16 ? splits : L.n_tiles / 16;
+    splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+    L.chunk = L.n_tiles > 0 ? int((L.n_tiles + splits - 1) / splits) : 1;
+    L.splits = L.n_tiles > 0 ? (L.n_tiles + L.chunk - 1) / L.chunk : 1;
     const int64_t tiles = int64_t(B) * Hkv * L.n_tiles;
     L.q = 0;
     L.k = up(total_q * H * d * 2);
     L.v = L.k + up(tiles * 128 * d * 2);
     L.q_mul = L.v + up(tiles * 128 * d * 2);
-    L.k_mul = L.q_mul + up(total_q * H * 4);
-    L.v_exp = L.k_mul + up(tiles * 4);
-    L.bytes = L.v_exp + up(tiles * 4);
+    L.tile = L.q_mul + up(total_q * H * 4);
+    L.O_part = L.tile + up(tiles * 8);
+    L.ml = L.O_part + (L.splits > 1 ? up(L.splits * total_q * H * d * 4) : 0);
+    L.bytes = L.ml + (L.splits > 1 ? up(L.splits * total_q * H * 8) : 0);
     return L;
 }
-// Whether a call takes that form: it writes the whole cache out once, which pays
-// where a sequence has 128 rows a kv head or more on average, and its CTAs take 256
-// rows each, of which there have to be enough for half of the SMs.
+// Whether a call takes that form.  It writes the whole cache out once, which pays
+// where a sequence has 128 rows a kv head or more on average (4 x 16k keys, 8 kv
+// heads: 128 rows 127 us against 161; 64 x 4k with 64 rows 427 against 330), its
+// kernels where there is some work (4 x 256 queries on 256 keys, 16 heads, 2 GFLOP:
+// 19 us against 34), and some tens of its CTAs where each has few tiles.
 inline bool kv4_many(int B, int64_t total_q, int Nk, int H, int Hkv, int d)
 {
     const int64_t rows = total_q * (H / Hkv);          // of a kv head, all sequences
-    return rows >= int64_t(128) * B && rows / 256 * Hkv >= 76 && Nk >= 128 && B < 65535 &&
-           rows * Hkv < (int64_t(1) << 31) - 512 &&
-           double(B) * Hkv * (Nk + 127.0) < double((int64_t(1) << 31) - 512) &&
-           kv4_many_layout(B, total_q, Nk, H, Hkv, d).bytes <= int64_t(8) << 30;
+    if (rows < int64_t(128) * B || Nk < 128 || B > kKv4MaxSeqs ||
+        rows * Hkv > (int64_t(1) << 31) - 512 ||
+        double(B) * Hkv * (Nk + 127.0) > double((int64_t(1) << 31) - 512) ||
+        4.0 * rows * Hkv * Nk * d < 1e9)
+        return false;
+    const Kv4ManyLayout L = kv4_many_layout(B, total_q, Nk, H, Hkv, d);
+    return kv4_many_items(B, total_q, H, Hkv) * L.splits >= 24 && L.bytes <= int64_t(8) << 30;
 }
 
 // Workspace: that form's copies; otherwise descriptors (32 bytes a CTA), then for

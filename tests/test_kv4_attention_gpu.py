@@ -479,6 +479,8 @@ MANY = [
     ([260, 700], [700, 160], 24, 8, 128, 64, 128, False, True),
     ([129, 640], 640, 16, 16, 64, 32, 32, True, False),
     ([0, 1, 1300], [300, 300, 700], 16, 16, 128, 64, 16, True, True),
+    ([4500, 130, 2300], [700, 200, 400], 16, 16, 64, 64, 64, True, True),   # several ranges of keys
+    ([2200, 2049], [2500, 100], 8, 8, 128, 128, 128, True, True),           # and rows that see none
 ]
 
 

@@ -192,7 +192,7 @@ def test_attention_refusals_without_gpu():
     # many rows: fp16 Q [total, H, d], K and V [B, Hkv, tiles of 128, d], the factors
     up = lambda x: -(-x // 256) * 256  # noqa: E731
     assert wb(3, 900, 2000, 1000, 32, 8, 128) == (
-        up(2000 * 32 * 256) + 2 * 3 * 8 * 1024 * 256 + up(2000 * 32 * 4) + 2 * up(3 * 8 * 8 * 4))
+        up(2000 * 32 * 256) + 2 * 3 * 8 * 1024 * 256 + up(2000 * 32 * 4) + up(3 * 8 * 8 * 8))
     assert wb(64, 1, 64, 1000, 32, 8, 128) == 0
 
     def go(q=256, qs=1024, cache=256, pages=4, ps=16, table=256, mp=80, lens=256, cu=None, o=256,
