@@ -534,7 +534,7 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  * power of two a tile of 128 tokens), and a NaN of V reaches all of a row that
  * sees it.
  * B <= 1024.  Results do not depend on timing: the same call gives the same
- * bits.  One or two kernels on the library stream, no
+ * bits.  One to three kernels on the library stream, no
  * synchronisation.
  * Errors: FA_ERR_BAD_SIZE (also a workspace that is too small, Nk above the
  * table, H no multiple of Hkv), FA_ERR_UNSUPPORTED (d, group, page_size),

@@ -21,7 +21,15 @@
 // that a decode step with up to 8 heads a kv head wastes nothing.  tcgen05 has
 // M = 64 at least and takes its operands from shared or tensor memory: the
 // codes would be expanded fourfold into shared memory first, which costs more
-// than the products.
+// than the products (attn_kv4_many.cu does it where there are rows enough).
+//
+// What bounds it: a cell of 16 tokens (2304 bytes with d = 128, group 64) costs a
+// warp some 270 instructions, of which half are logical operations at two a cycle
+// and SM, 88 of them the expansion; HBM leaves 100 cycles a cell.  Without the
+// copies 32 x 8184 keys (8 kv heads) take 53 us, a plain read of their cache 51,
+// both together 67: 4.5 TB/s, 0.66 of the measured copy rate; 64 sequences of 2k to
+// 16k keys 117 us, 5.1 TB/s.  One MMA of 16 x 8 x 16 takes two cycles of an SM (605
+// TFLOP/s), a quarter of the time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -138,9 +146,10 @@ __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x 
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
 // Pairs of cells on their way or in use: each warp has a ring of its own and
-// fills a place again as soon as it has read it; no barrier between warps.  16
-// warps an SM with one pair of 4608 bytes each on its way are 74 KB in flight,
-// against the 36 KB that cover HBM's latency at full rate.
+// fills a place again as soon as it has read it; no barrier between warps.  12
+// warps an SM with one pair of 4608 bytes each on its way are 55 KB in flight,
+// against the 36 KB that cover HBM's latency at full rate; three pairs a ring
+// measured the same (64 x 8k keys: 119 us, with two 117).
 constexpr int kStages = 2;
 constexpr int kJoinWarps = 8;
 
@@ -431,7 +440,7 @@ __device__ __noinline__ Copy find_copy(const Kv4AttnArgs &a, const uint32_t *s_p
 }
 
 template <int D, int G, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(const Kv4AttnArgs a)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(const Kv4AttnArgs a)
 {
     constexpr int R = 8 * NT;              // query rows of a tile
     constexpr int NG = D / G;              // groups of the head dimension
@@ -439,11 +448,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
     constexpr int kCell = kv4::cell_bytes(D, G);
     constexpr int kRow = D + 4;            // padded fp32 row of the merge buffer
     constexpr int kVBases = D == 128 ? 2 : 4;   // d = 128: 8 tokens are 512 bytes on
-    // Cells taken at once.  Two overlap better where the registers hold them (16
-    // sequences x 4 queries, group 64: 66 us, one by one 68); where they do not,
-    // one at a time spills less (256 x 1k: 88 -> 84 us with group 64, 111 -> 105
-    // with 32).
-    constexpr int kCells = NG == 4 || (NT == 1 && NG == 2) ? 1 : 2;
+    // Cells taken at once: two overlap, but with four groups a head their
+    // parameters do not fit the registers.
+    constexpr int kCells = NG == 4 ? 1 : 2;
     using Smem = Shared<D, G, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     auto &s_q = *reinterpret_cast<QueryTile<D, G, NT> *>(smem + Smem::q);
@@ -628,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
                     pm[nt][x][e] = 0.f;
             }
         }
-        // The keys of kCells cells, from token `tok` on.  kMasked: some query row of the tile
-        // does not see all of them, or the sequence ends among them.
+        // The keys of kCells cells, from token `tok` on.  kMasked: some query row of
+        // the tile does not see all of them, or the sequence ends among them.
         const int tok_end = key_end(a, it, (it.tile * R + rows - 1) / grp);
         auto step = [&](uint32_t slot, int tok, auto masked_tag) {
             constexpr bool kMasked = decltype(masked_tag)::value;
@@ -974,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) attn_kv4_kernel(con
 // in CTA x's range and does not end there, kPart warps a row.  The warps of a row
 // take every kPart-th part, eight loads of O under way at a time, and their sums
 // are added in the order of the warps.  Few items have many parts each and take
-// 8 warps a row (1 x 130001 keys, 76 parts: 28 us with one, 7 with eight); many
+// 8 warps a row (1 x 130001 keys in 76 parts: 28 us with one, 7 with eight); many
 // items have a few and take one (64 x 8 items: 6 us, with eight 10).
 template <int D, int R, int kPart>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_kv4_join_kernel(const Kv4AttnArgs a)

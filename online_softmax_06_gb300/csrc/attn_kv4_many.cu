@@ -5,8 +5,10 @@
 // with hundreds of rows a kv head the products are what costs.  Here the cache's
 // values are written out once, as fp16, and a kernel of the shape of attn_bf16.cu
 // (two 128-row Q tiles a CTA, K and V tiles of 128 keys through a TMA ring, S, P
-// and O in tensor memory) reads them: 4 sequences x 512 queries on 2k to 16k keys
-// take 854 us with the one and are given with this one in the design notes.
+// and O in tensor memory) reads them: 4 sequences x 256 to 512 queries on 2k to 16k
+// keys, 32 heads on 8, take 843 us with the one and 214 with the other, 44 of them
+// for the copy (5.2 TB/s) and 15 for the join; with 1024 queries each on 16k keys
+// the whole runs at 1.36 PFLOP/s, 0.72 of the measured cuBLAS rate.
 //
 // fp16 has 11 bits where min + scale * code needs up to 16: each value is rounded
 // once, by 2^-11 of itself at most, after the power of two that brings the largest
@@ -335,12 +337,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + (C::kBarBytes / 8));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    // ---- work item: (sequence, kv head, pair of Q tiles, range of p.w.chunk key
-    //      tiles), last pairs first ----------------------------------------------------
+    // ---- work item: (sequence, kv head, range of p.w.chunk key tiles, pair of Q
+    //      tiles), the pairs side by side: they read the same K and V tiles (with the
+    //      pairs apart, 4 x 512 queries on 16k keys took 240 us, so 214) --------------
     const Kv4AttnArgs &a = p.a;
     const int bh_count = a.B * a.Hkv, grp = a.H / a.Hkv;
-    const int split = int(blockIdx.x) % p.w.splits, rest = int(blockIdx.x) / p.w.splits;
-    const int pair = p.n_pairs - 1 - rest / bh_count, bh = rest % bh_count;
+    const int rest = int(blockIdx.x) / p.n_pairs, px = int(blockIdx.x) % p.n_pairs;
+    const int pair = p.n_pairs - 1 - px;   // the heaviest of a causal run first
+    const int split = rest % p.w.splits, bh = rest / p.w.splits;
     const int b = bh / a.Hkv, h = bh % a.Hkv;
     Seq seq;
     if (!seq_of(a, b, false, seq))

@@ -902,7 +902,7 @@ int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num
     // counted in 32 bits
     const int rows = fa::kv4_attention_rows(Nq, H, Hkv);
     const int64_t tiles = (int64_t(Nq) * (H / Hkv) + rows - 1) / rows;
-    const int64_t blocks = Nk / 128 + 3;   // and two for the item itself
+    const int64_t blocks = Nk / 128 + 4;   // one begun, three for the item itself
     if (B > fa::kKv4MaxSeqs || total_q > (int64_t(1) << 31) - 512 || q_stride > (int64_t(1) << 31) ||
         H > 65535 || int64_t(Nq) * (H / Hkv) > (int64_t(1) << 31) - 512 ||
         double(tiles) * double(blocks) * B * Hkv > double((int64_t(1) << 31) - 512))

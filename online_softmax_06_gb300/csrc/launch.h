@@ -205,8 +205,10 @@ inline int kv4_attention_rows(int Nq, int H, int Hkv)
 {
     return int64_t(Nq) * (H / Hkv) <= 8 ? 8 : 16;
 }
-// CTAs: four on each of 152 SMs, two with the wider tiles' registers.
-__host__ __device__ constexpr int kv4_attention_ctas(int rows) { return rows <= 8 ? 608 : 304; }
+// CTAs: three on each of 152 SMs, two with the wider tiles' registers.  (Four, of 128
+// registers a thread, take one cell at a time and spill: 64 x 8k keys 123 us against
+// 117, 256 x 1k with groups of 32 102 against 94.)
+__host__ __device__ constexpr int kv4_attention_ctas(int rows) { return rows <= 8 ? 456 : 304; }
 
 // The form for many query rows (attn_kv4_many.cu): fp16 copies of Q ([Hkv, total_q,
 // H / Hkv, d]) and of the cache ([B, Hkv, 128 n_tiles, d] each), and their factors.
