@@ -506,7 +506,8 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
                        int64_t total, int Hkv, int d, int group);
 
 /*
- * Exact attention of bf16 queries on the cache's values (min + scale * code): S = scale * Q K^T (+ mask), P = softmax(S), O = P V, lse as in
+ * Exact attention of bf16 queries on the cache's values (min + scale * code):
+ * S = scale * Q K^T (+ mask), P = softmax(S), O = P V, lse as in
  * fa_attention_fwd, fp32 accumulation.  A decode step has Nq = 1 (or a few
  * drafted tokens); chunks of a prompt any Nq.  Query head h reads kv head
  * h / (H / Hkv); H is a multiple of Hkv.
@@ -531,11 +532,10 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  * codes go into the products as they are and nothing is rounded but P, to fp16.
  * Many (128 and more on average, enough of them to fill the GPU; chunks of
  * prompts): the values are first written out as fp16 (2^-11 relative, with a
- * power of two a tile of 128 tokens), and a NaN of V reaches all of a row that
- * sees it.
+ * power of two a tile of 128 tokens of a head: values below 2^-28 of the tile's
+ * largest have fewer bits), and a NaN of V reaches all of a row that sees it.
  * B <= 1024.  Results do not depend on timing: the same call gives the same
- * bits.  One to three kernels on the library stream, no
- * synchronisation.
+ * bits.  One to three kernels on the library stream, no synchronisation.
  * Errors: FA_ERR_BAD_SIZE (also a workspace that is too small, Nk above the
  * table, H no multiple of Hkv), FA_ERR_UNSUPPORTED (d, group, page_size),
  * FA_ERR_NULL_POINTER, FA_ERR_MISALIGNED, FA_ERR_TOO_LARGE, FA_ERR_NO_DEVICE,

@@ -829,6 +829,8 @@ def attention_kv4(q, cache, page_table, seqlens, max_seqlen: int | None = None, 
     at most ``max_seqlen`` (default: what the page table can hold).  causal:
     query i of n sees keys j <= i + seqlens[b] - n.  The workspace is allocated
     here (torch) unless given (uint8, fa_attention_kv4_workspace_bytes).
+    ``max_q`` and ``max_seqlen`` lay out the work: close bounds run faster, and
+    with chunks of prompts take less workspace.
     """
     import torch
     index = _kv4_check(torch, (q,), cache, page_table, seqlens, cu_seqlens)
@@ -863,7 +865,8 @@ def attention_kv4(q, cache, page_table, seqlens, max_seqlen: int | None = None, 
 
 
 __all__ = [
-    "attention_kv4", "fa_attention_kv4", "fa_attention_kv4_workspace_bytes", "kv4_cache", "kv4_append", "kv4_read", "fa_kv4_page_bytes", "fa_kv4_append", "fa_kv4_read",
+    "attention_kv4", "kv4_cache", "kv4_append", "kv4_read", "fa_attention_kv4",
+    "fa_attention_kv4_workspace_bytes", "fa_kv4_page_bytes", "fa_kv4_append", "fa_kv4_read",
     "FA_DEVERR_BAD_PAGE",
     "build", "lib", "strerror", "FaError", "softmax_rows", "attention_fwd",
     "attention_fwd_splitkv", "attention_fwd_splitkv_varlen", "fa_attention_fwd_splitkv",

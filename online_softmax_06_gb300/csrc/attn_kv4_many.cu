@@ -6,9 +6,9 @@
 // values are written out once, as fp16, and a kernel of the shape of attn_bf16.cu
 // (two 128-row Q tiles a CTA, K and V tiles of 128 keys through a TMA ring, S, P
 // and O in tensor memory) reads them: 4 sequences x 256 to 512 queries on 2k to 16k
-// keys, 32 heads on 8, take 843 us with the one and 214 with the other, 44 of them
+// keys, 32 heads on 8, take 843 us with the one and 216 with the other, 44 of them
 // for the copy (5.2 TB/s) and 15 for the join; with 1024 queries each on 16k keys
-// the whole runs at 1.36 PFLOP/s, 0.72 of the measured cuBLAS rate.
+// the whole runs at 1.35 PFLOP/s, 0.72 of the measured cuBLAS rate.
 //
 // fp16 has 11 bits where min + scale * code needs up to 16: each value is rounded
 // once, by 2^-11 of itself at most, after the power of two that brings the largest
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---- work item: (sequence, kv head, range of p.w.chunk key tiles, pair of Q
     //      tiles), the pairs side by side: they read the same K and V tiles (with the
-    //      pairs apart, 4 x 512 queries on 16k keys took 240 us, so 214) --------------
+    //      pairs apart, 4 x 512 queries on 16k keys took 240 us, so 216) --------------
     const Kv4AttnArgs &a = p.a;
     const int bh_count = a.B * a.Hkv, grp = a.H / a.Hkv;
     const int rest = int(blockIdx.x) / p.n_pairs, px = int(blockIdx.x) % p.n_pairs;
@@ -595,10 +595,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m = -INFINITY, l = 0.f;
 
         for (int j = 0; j < n_t; ++j) {
-            // (a factor of 0 would make NaN of the mask's -inf)
+            // (a factor of 0 would make NaN of the mask's -inf, one of inf of a score of 0)
             const float2 factor = p.w.tile[tile0 + j];
-            const float slj = fmaxf(sl * factor.x, 1.2e-38f), f = factor.y;
-            if (!ptx::mbar_wait(&s_full[t], uint32_t(j) & 1u, abort_flag, a.err_word)) {
+            const float slj = fminf(fmaxf(sl * factor.x, 1.2e-38f), 3e38f);
+            float f = factor.y;
+            // |raw scores| are below 2^28 d: scores beyond 2^18 are possible
+            const bool large = slj > 0x1p-10f / D;
+            const bool any_large = __any_sync(0xffffffffu, large);
+            // (the warp gives up as one: votes and aligned loads follow)
+            if (!ptx::mbar_wait_warp(&s_full[t], uint32_t(j) & 1u, abort_flag, a.err_word)) {
                 aborted = true;
                 break;
             }
@@ -608,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 4; ++c)
                 ptx::tmem_ld32(tS + c * 32, sr[c]);
             ptx::tmem_wait_ld();
-            if (j * BN + BN - 1 > last_first) {
+            if (any_large || j * BN + BN - 1 > last_first) {
                 const int lim = last - j * BN;
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -616,6 +621,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 32; ++e)
                         if (c * 32 + e > lim)
                             sr[c][e] = __float_as_uint(-INFINITY);
+                if (any_large) {
+                    // The rounding of the reference would show in P, and from 2^40 on make
+                    // infinities: such a row's scores go by their distance to the largest.
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            top = fmaxf(top, __uint_as_float(sr[c][e]));
+                    top = large && fabsf(top) < INFINITY ? top : 0.f;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            sr[c][e] = __float_as_uint(__uint_as_float(sr[c][e]) - top);
+                    f = fmaf(top, slj, f);
+                }
             }
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -665,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tmem_wait_st();
             ptx::tc_fence_before_sync();
             ptx::mbar_arrive(&p_full[t]);
-            l = l * corr + (rowsum2.x + rowsum2.y) * ptx::ex2(-f);
+            l = l * corr + (rowsum2.x + rowsum2.y) * ptx::ex2(-factor.y);
             m = m_new;
         }
 
@@ -764,7 +786,7 @@ __global__ void __launch_bounds__(kExpandThreads) kv4_many_join_kernel(const Man
             y[e] = 0.f;
         for (int s = 0; s < n; ++s) {
             const float2 ml = p.w.ml[s * step + row];
-            if (ml.x == -INFINITY)             // nothing seen, nothing written
+            if (ml.y == 0.f)                   // nothing seen, or nothing written
                 continue;
             const float f = ptx::ex2(ml.x - m);
             l = fmaf(ml.y, f, l);

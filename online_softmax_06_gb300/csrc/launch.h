@@ -263,10 +263,10 @@ inline Kv4ManyLayout kv4_many_layout(int B, int64_t total_q, int Nk, int H, int 
 // 19 us against 34), and some tens of its CTAs where each has few tiles.
 inline bool kv4_many(int B, int64_t total_q, int Nk, int H, int Hkv, int d)
 {
-    const int64_t rows = total_q * (H / Hkv);          // of a kv head, all sequences
-    if (rows < int64_t(128) * B || Nk < 128 || B > kKv4MaxSeqs ||
-        rows * Hkv > (int64_t(1) << 31) - 512 ||
-        double(B) * Hkv * (Nk + 127.0) > double((int64_t(1) << 31) - 512) ||
+    const int64_t limit = (int64_t(1) << 31) - 512;
+    const int64_t rows = total_q > limit ? 0 : total_q * (H / Hkv);   // of a kv head, all sequences
+    if (rows < int64_t(128) * B || Nk < 128 || B > kKv4MaxSeqs || double(rows) * Hkv > limit ||
+        double(B) * Hkv * (Nk + 127.0) > limit ||
         4.0 * rows * Hkv * Nk * d < 1e9)
         return false;
     const Kv4ManyLayout L = kv4_many_layout(B, total_q, Nk, H, Hkv, d);

@@ -609,3 +609,84 @@ def test_many_rows_in_a_graph_on_a_stream():
     sub.__dict__.update(pool.__dict__, lengths=[123, 640])
     check(sub, [-y for y in q], og, lg, 1 / 8, True, many=True)
     device_error_clear()
+
+
+FORMS = [  # the few rows' form and the many rows', keys in several ranges
+    ([5000, 40], 2, 8, 2, 128, 64, 32),
+    ([4500, 130, 2300], [700, 200, 400], 16, 16, 64, 64, 64),
+]
+
+
+@pytest.mark.parametrize("form", FORMS, ids=["few", "many"])
+def test_nan_query_rows_stay_alone(form):
+    lens, Nq, H, Hkv, d, group, page = form
+    pool, q = make(lens, Nq, H, Hkv, d, group, page, seed=360)
+    O, lse = run(pool, q, True, True)
+    q[0][1, 3, 7] = np.nan
+    q[0][-1, 0] = np.inf
+    O1, l1 = run(pool, q, True, True)
+    for i, h in ((1, 3), (len(q[0]) - 1, 0)):
+        assert torch.isnan(O1[i, h]).all() and torch.isnan(l1[h, i])
+        O1[i, h], l1[h, i] = O[i, h], lse[h, i]
+    assert torch.equal(O, O1) and torch.equal(lse, l1)
+    device_error_clear()
+
+
+@pytest.mark.parametrize("form", FORMS, ids=["few", "many"])
+def test_sequences_that_share_pages(form):
+    _, Nq, H, Hkv, d, group, page = form
+    nq = Nq if np.isscalar(Nq) else Nq[:2]
+    pool, q = make([2310, 2300], nq, H, Hkv, d, group, page, seed=370)
+    pool.table[1] = pool.table[0]
+    O, lse = run(pool, q, True, True)
+    check(pool, q, O, lse, 1 / math.sqrt(d), True, many=not np.isscalar(Nq))
+    device_error_clear()
+
+
+def test_calls_at_once_on_two_streams():
+    sets = []
+    for i, (lens, Nq, H, Hkv, d, group, page) in enumerate(FORMS):
+        pool, q = make(lens, Nq, H, Hkv, d, group, page, seed=380 + i)
+        n = [len(x) for x in q]
+        sets.append(dict(q=gpu_bf16(np.concatenate(q)), cache=torch.from_numpy(pool.bytes).cuda(),
+                         page_table=gpu_i32(pool.table), seqlens=gpu_i32(lens), group=group,
+                         cu_seqlens=gpu_i32(np.concatenate([[0], np.cumsum(n)])), max_q=max(n)))
+    want = [fa.attention_kv4(**s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i % 2, fa.attention_kv4(**sets[i % 2])))
+    torch.cuda.synchronize()
+    for i, (O, lse) in got:
+        assert torch.equal(O, want[i][0]) and torch.equal(lse, want[i][1])
+    device_error_clear()
+
+
+def test_no_keys_and_no_pages():
+    cache = fa.kv4_cache(0, 2, 16, 64)
+    q = torch.ones(3, 2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    O, lse = fa.attention_kv4(q, cache, torch.empty(3, 0, dtype=torch.int32, device="cuda"),
+                              gpu_i32([0, 0, 0]))
+    assert (O == 0).all() and torch.isneginf(lse).all()
+    k = torch.empty(3, 0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    fa.kv4_append(k, k, cache, torch.empty(3, 0, dtype=torch.int32, device="cuda"), gpu_i32([0, 0, 0]))
+    device_error_clear()
+
+
+def test_many_rows_factors_that_overflow_together():
+    """Q's and K's largest values in different places: their factors' product is not finite."""
+    pool, q = make([400, 200], [400, 240], 32, 8, 128, 64, 32, seed=390)
+    rng = np.random.default_rng(391)
+    k, v = bf16_rows(rng, 400, 8, 128), bf16_rows(rng, 400, 8, 128)
+    k[..., 64:] = 0
+    k[..., 100] = 2.0 ** 70
+    q[0][7, :, 1] = 2.0 ** 100
+    q[0][7, :, 64:] = 0
+    pool.fill([k], [v])
+    assert takes_many(pool, q, pool.table.shape[1] * 32)
+    O, lse = run(pool, q, False, True)
+    assert torch.isfinite(O).all() and torch.isfinite(lse).all()
+    device_error_clear()
