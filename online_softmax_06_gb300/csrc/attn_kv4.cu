@@ -25,11 +25,15 @@
 //
 // What bounds it: a cell of 16 tokens (2304 bytes with d = 128, group 64) costs a
 // warp some 270 instructions, of which half are logical operations at two a cycle
-// and SM, 88 of them the expansion; HBM leaves 100 cycles a cell.  Without the
-// copies 32 x 8184 keys (8 kv heads) take 53 us, a plain read of their cache 51,
-// both together 67: 4.5 TB/s, 0.66 of the measured copy rate; 64 sequences of 2k to
-// 16k keys 117 us, 5.1 TB/s.  One MMA of 16 x 8 x 16 takes two cycles of an SM (605
-// TFLOP/s), a quarter of the time.
+// and SM, 88 of them the expansion; HBM leaves 100 cycles a cell.  64 sequences of
+// 300 to 16000 keys (32 heads on 8) take 109 us: 7 until all the first cells are
+// there, 93 of keys at 6.4 TB/s, 5 in which the crews end, 4 of the join: 5.5 TB/s,
+// 0.81 of the measured copy rate.  One MMA of 16 x 8 x 16 takes two cycles of an SM
+// (605 TFLOP/s), a quarter of the time.
+//
+// One CTA an SM, of crews of four warps that share nothing but the layout of the
+// work.  As CTAs of their own, three an SM, the crews were served in the order in
+// which they came and ended 25 us apart (84, 95 and 110 us; so 99, 100 and 101).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -48,7 +52,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;            // of a crew
 constexpr int kThreads = kWarps * 32;
 constexpr int kPair = 2 * kv4::kCellTokens;         // tokens that a warp copies and takes at once
 constexpr int kBlock = kWarps * kPair;              // tokens of a block: two cells each warp
@@ -149,31 +153,31 @@ __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x 
 // fills a place again as soon as it has read it; no barrier between warps.  12
 // warps an SM with one pair of 4608 bytes each on its way are 55 KB in flight,
 // against the 36 KB that cover HBM's latency at full rate; three pairs a ring
-// measured the same (64 x 8k keys: 119 us, with two 117).
+// measured the same (64 x 8k keys 119 us, with two 118).
 constexpr int kStages = 2;
 constexpr int kJoinWarps = 8;
 
 // A work item is (sequence, kv head, tile of R query rows); its keys are cut
 // into blocks of kBlock tokens.  All items' blocks, sequence by sequence, form
-// one line that is cut into equal ranges, one a CTA: ragged batches and single
+// one line that is cut into equal ranges, one a crew: ragged batches and single
 // long sequences fill the GPU alike, and nothing of it needs the host.
 //
-// An item costs a CTA some time beside its blocks' (queries, the four warps'
+// An item costs a crew some time beside its blocks' (queries, the four warps'
 // join): the line is cut as if each item had kItemCost blocks more.  Without it
-// the CTAs whose range holds the short sequences of a batch ended last (32
+// the crews whose range holds the short sequences of a batch ended last (32
 // sequences of 1 to 8191 keys, 16 kv heads, d = 64: 74 us, against 46 with 4096
 // each).
 constexpr uint32_t kItemCost = 3;
 
-struct Desc {          // of a CTA
+struct Desc {          // of a range
     uint32_t begin;    // first block of its range
     uint32_t item_end; // end of the item that begins in it and goes on after it; 0: none
     int b, kvh, tile;  // that item
     int unused[3];
 };
 
-// Workspace: Desc[ctas], then (reference, sum) [2 ctas][R], then the
-// unnormalised O [2 ctas][R][d] fp32.  A CTA's slot 0 holds the part of an item
+// Workspace: Desc[ranges], then (reference, sum) [2 ranges][R], then the
+// unnormalised O [2 ranges][R][d] fp32.  A range's slot 0 holds the part of an item
 // that began before its range, slot 1 that of one that goes on after.
 struct Parts {
     Desc *desc;
@@ -186,8 +190,8 @@ __host__ __device__ inline Parts parts_of(void *ws)
 {
     Parts p;
     p.desc = static_cast<Desc *>(ws);
-    p.ml = reinterpret_cast<float2 *>(p.desc + kv4_attention_ctas(R));
-    p.O = reinterpret_cast<float *>(p.ml + 2 * kv4_attention_ctas(R) * R);
+    p.ml = reinterpret_cast<float2 *>(p.desc + kv4_attention_ranges(R));
+    p.O = reinterpret_cast<float *>(p.ml + 2 * kv4_attention_ranges(R) * R);
     return p;
 }
 
@@ -214,6 +218,7 @@ struct alignas(16) QueryTile {
     int end[8 * NT];               // the keys that the row sees lie below this
 };
 
+// A crew's shared memory, and at its end what the CTA's crews have in common.
 template <int D, int G, int NT>
 struct Shared {
     static constexpr int R = 8 * NT;
@@ -221,10 +226,16 @@ struct Shared {
     static constexpr int q = ring + kWarps * kStages * 2 * kv4::cell_bytes(D, G);  // QueryTile
     static constexpr int O = q + int(sizeof(QueryTile<D, G, NT>));   // [kWarps / 2][8][D + 4]
     static constexpr int full = O + kWarps / 2 * 8 * (D + 4) * 4;    // [kWarps][kStages] barriers
-    static constexpr int pre = full + kWarps * kStages * 8;          // [B + 1] blocks before b
-    static constexpr int ref = pre + (kKv4MaxSeqs + 4) * 4;          // [kWarps][R]
+    static constexpr int ref = full + kWarps * kStages * 8;          // [kWarps][R]
     static constexpr int sum = ref + kWarps * R * 4;                 // [kWarps][R]
-    static constexpr int bytes = sum + kWarps * R * 4;
+    static constexpr int abort = sum + kWarps * R * 4;               // a wait ran out
+    static constexpr int bytes = (abort + 4 + 127) / 128 * 128;
+
+    static constexpr int crews = kv4_attention_crews(R);
+    static constexpr int pre = 0;                                    // [B + 1] blocks before b
+    static constexpr int scan = pre + (kKv4MaxSeqs + 4) * 4;         // a uint2 of each warp
+    static constexpr int own = (scan + crews * kWarps * 8 + 127) / 128 * 128;
+    static constexpr int all = own + crews * bytes;
 };
 
 // Where block x of the line is.
@@ -309,7 +320,7 @@ __device__ __forceinline__ uint32_t block_of(const Kv4AttnArgs &a, const uint32_
                                              const uint32_t *s_cost, uint32_t x)
 {
     if (x >= s_cost[a.B])
-        return uint32_t(uniform(int(s_pre[a.B])));
+        return s_pre[a.B];
     int lo = 0, hi = a.B;                  // s_cost[lo] <= x < s_cost[lo + 1]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -320,7 +331,7 @@ __device__ __forceinline__ uint32_t block_of(const Kv4AttnArgs &a, const uint32_
     }
     const uint32_t nb = blocks_of(a.seqlens[lo]), at = x - s_cost[lo], i = at / (nb + kItemCost);
     const uint32_t o = at - i * (nb + kItemCost);
-    return uint32_t(uniform(int(s_pre[lo] + i * nb + (o > kItemCost ? o - kItemCost : 0))));
+    return s_pre[lo] + i * nb + (o > kItemCost ? o - kItemCost : 0);
 }
 
 // The first item that begins at block x or after it.
@@ -329,7 +340,7 @@ __device__ __forceinline__ uint32_t item_from(const Kv4AttnArgs &a, const uint32
 {
     if (x >= T)
         return T;
-    const Item it = uniform(item_at(a, s_pre, grp, R, x));
+    const Item it = item_at(a, s_pre, grp, R, x);
     return it.first == x ? x : it.first + it.nb;
 }
 
@@ -440,7 +451,8 @@ __device__ __noinline__ Copy find_copy(const Kv4AttnArgs &a, const uint32_t *s_p
 }
 
 template <int D, int G, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(const Kv4AttnArgs a)
+__global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT), 1)
+    attn_kv4_kernel(const Kv4AttnArgs a)
 {
     constexpr int R = 8 * NT;              // query rows of a tile
     constexpr int NG = D / G;              // groups of the head dimension
@@ -452,15 +464,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(con
     // parameters do not fit the registers.
     constexpr int kCells = NG == 4 ? 1 : 2;
     using Smem = Shared<D, G, NT>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem_cta[];
+    const int crew = uniform(int(threadIdx.x) / kThreads);
+    const int id = crew * kv4_attention_sms + int(blockIdx.x);       // of the crew's range
+    uint8_t *smem = smem_cta + Smem::own + crew * Smem::bytes;
     auto &s_q = *reinterpret_cast<QueryTile<D, G, NT> *>(smem + Smem::q);
     float *s_O = reinterpret_cast<float *>(smem + Smem::O);
-    uint32_t *s_pre = reinterpret_cast<uint32_t *>(smem + Smem::pre);
+    uint32_t *s_pre = reinterpret_cast<uint32_t *>(smem_cta + Smem::pre);
     float *s_ref = reinterpret_cast<float *>(smem + Smem::ref);
     float *s_sum = reinterpret_cast<float *>(smem + Smem::sum);
-    __shared__ int s_abort;
-    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, g = lane >> 2,
+    volatile int &s_abort = *reinterpret_cast<volatile int *>(smem + Smem::abort);
+    const int tid = threadIdx.x % kThreads, warp = uniform(tid >> 5), lane = tid & 31, g = lane >> 2,
               c = lane & 3;
+    auto sync_crew = [&] { asm volatile("bar.sync %0, 128;" ::"r"(crew + 1) : "memory"); };
     const int grp = a.H / a.Hkv;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Smem::full) + warp * kStages;
     uint8_t *ring = smem + Smem::ring + warp * (kStages * 2 * kCell);
@@ -475,11 +491,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(con
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the line of blocks ------------------------------------------------
-    const int per = (a.B + kThreads - 1) / kThreads;
-    uint32_t *s_cost = reinterpret_cast<uint32_t *>(smem + Smem::ring);   // [B + 1], until the first copy
+    constexpr int kAll = kThreads * Smem::crews;
+    const int per = (a.B + kAll - 1) / kAll;
+    // [B + 1], in the first crew's ring until the first copy
+    uint32_t *s_cost = reinterpret_cast<uint32_t *>(smem_cta + Smem::own + Smem::ring);
     uint32_t mine = 0, mine_cost = 0;
     for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
+        const int b = threadIdx.x * per + i;
         if (b >= a.B)
             break;
         const int2 q = queries_of(a, b);
@@ -505,17 +523,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(con
             incl_cost += t_cost;
         }
     }
-    uint2 *s_w = reinterpret_cast<uint2 *>(s_ref);
+    uint2 *s_w = reinterpret_cast<uint2 *>(smem_cta + Smem::scan);
     if (lane == 31)
-        s_w[warp] = make_uint2(incl, incl_cost);
+        s_w[crew * kWarps + warp] = make_uint2(incl, incl_cost);
     __syncthreads();
     uint32_t base = incl - mine, base_cost = incl_cost - mine_cost;
-    for (int w = 0; w < warp; ++w) {
+    for (int w = 0; w < crew * kWarps + warp; ++w) {
         base += s_w[w].x;
         base_cost += s_w[w].y;
     }
     for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
+        const int b = threadIdx.x * per + i;
         if (b >= a.B)
             break;
         base += s_pre[b + 1];
@@ -523,34 +541,39 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(con
         s_pre[b + 1] = base;
         s_cost[b + 1] = base_cost;
     }
-    if (tid == 0)
+    if (threadIdx.x == 0)
         s_pre[0] = s_cost[0] = 0;
     __syncthreads();
     const uint32_t T = uint32_t(uniform(int(s_pre[a.B])));
-    const uint32_t n_ctas = min(T, gridDim.x);
+    const uint32_t n_ranges = min(T, uint32_t(kv4_attention_ranges(R)));
     const Parts parts = parts_of<R>(a.workspace);
     uint32_t begin = T, end = T;
-    if (blockIdx.x < n_ctas) {
+    if (id < n_ranges) {
         const uint64_t all = uint32_t(uniform(int(s_cost[a.B])));
-        begin = block_of(a, s_pre, s_cost, uint32_t(all * blockIdx.x / n_ctas));
-        end = block_of(a, s_pre, s_cost, uint32_t(all * (blockIdx.x + 1) / n_ctas));
-        if (a.whole_items) {               // the items that begin in the range
-            begin = item_from(a, s_pre, grp, R, begin, T);
-            end = item_from(a, s_pre, grp, R, end, T);
-        }
+        // both ends at once, by the odd and the even lanes
+        uint32_t x = block_of(a, s_pre, s_cost, uint32_t(all * uint32_t(id + (lane & 1)) / n_ranges));
+        if (a.whole_items)                 // the items that begin in the range
+            x = item_from(a, s_pre, grp, R, x, T);
+        begin = __shfl_sync(0xffffffffu, x, 0);
+        end = __shfl_sync(0xffffffffu, x, 1);
     }
     Desc desc{begin, 0, 0, 0, 0, {}};
+    __syncthreads();                       // s_cost gives way to the copies
     if (begin >= end) {
         if (tid == 0 && !a.whole_items)
-            parts.desc[blockIdx.x] = desc;
+            parts.desc[id] = desc;
         return;
     }
-    __syncthreads();                       // s_cost gives way to the copies
 
     // ---- copies ------------------------------------------------------------------
     // Each warp copies its own pairs.  32 lanes find the sources of 16 pairs at
     // once, so that the search and the page table's latency are paid once for
     // them, and issue them when their turn comes.
+    // The first item's queries are requested before.
+    Item it = uniform(item_at(a, s_pre, grp, R, begin));
+    uint4 first_q[NJ];
+    if (warp < NT)
+        fetch_queries<D, NT>(a, it, grp, warp, first_q);
     const uint32_t n_blocks = end - begin;
     Copy copy{nullptr, 0};
     auto fill = [&](uint32_t k) {
@@ -597,13 +620,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(con
     keep(at_par);
     keep(at_Q);
 
-    Item it = uniform(item_at(a, s_pre, grp, R, begin));
-    if (warp < NT) {
-        uint4 qw[NJ];
-        fetch_queries<D, NT>(a, it, grp, warp, qw);
-        place_queries<D, G, NT>(a, it, grp, warp, qw, s_q);
-    }
-    __syncthreads();
+    if (warp < NT)
+        place_queries<D, G, NT>(a, it, grp, warp, first_q, s_q);
+    sync_crew();
     for (uint32_t cur = begin; cur < end;) {
         const uint32_t stop = min(end, it.first + it.nb);
         const int rows = min(R, it.nq * grp - it.tile * R);         // rows of this tile
@@ -859,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(con
             for (int j = 0; j < NJ; ++j)
                 qw[j] = make_uint4(0, 0, 0, 0);
         const bool whole = cur == it.first && stop == it.first + it.nb;
-        const int slot = 2 * int(blockIdx.x) + (cur == it.first ? 1 : 0);
+        const int slot = 2 * id + (cur == it.first ? 1 : 0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -878,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(con
                     s_sum[warp * R + nt * 8 + 2 * c + e] = s;
                 }
             }
-        __syncthreads();
+        sync_crew();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             // the upper warps' rows through shared memory into the lower warps'
@@ -913,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(con
                 } else if (half == 0 && nt == 0 && warp < NT && stop < end) {
                     place_queries<D, G, NT>(a, next, grp, warp, qw, s_q);
                 }
-                __syncthreads();
+                sync_crew();
             }
             // 8 rows x D values over the threads, four consecutive values each
             for (int x = tid; x < 8 * (D / 4); x += kThreads) {
@@ -954,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(con
                         parts.ml[slot * R + r] = make_float2(m, s);
                 }
             }
-            __syncthreads();
+            sync_crew();
         }
         if (cur == it.first && !whole) {
             desc.item_end = it.first + it.nb;
@@ -966,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(con
         it = next;
     }
     if (s_abort) {
-        // a wait ran out: the copies under way must land before the CTA ends
+        // a wait ran out: the copies under way must land before the crew ends
         desc.item_end = 0;
         volatile int go_on = 0;
         for (uint32_t k = done; k < min(done + kStages, n_blocks); ++k)
@@ -974,11 +993,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kv4_kernel(con
                                    kWaitTimeoutNs);
     }
     if (tid == 0 && !a.whole_items)
-        parts.desc[blockIdx.x] = desc;
+        parts.desc[id] = desc;
 }
 
-// Joins the parts of the items that span CTAs: blocks (x, *) the item that begins
-// in CTA x's range and does not end there, kPart warps a row.  The warps of a row
+// Joins the parts of the items that span ranges: blocks (x, *) the item that begins
+// in range x and does not end there, kPart warps a row.  The warps of a row
 // take every kPart-th part, eight loads of O under way at a time, and their sums
 // are added in the order of the warps.  Few items have many parts each and take
 // 8 warps a row (1 x 130001 keys in 76 parts: 28 us with one, 7 with eight); many
@@ -999,14 +1018,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_kv4_join_kernel(const Kv
     if (row0 >= all)
         return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y * kRows + warp / kPart;
-    // the first part lies in its CTA's slot 1, the others in their CTAs' slot 0
+    // the first part lies in its range's slot 1, the others in their ranges' slot 0
     auto place = [&](int p) { return (int64_t(2) * (blockIdx.x + p) + (p == 0)) * R + r; };
     // lane l: reference and sum of the warp's l-th part of 32
     float m = kNoRef, s = 0.f, y[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e)
         y[e] = 0.f;
-    // the CTAs from this one on whose range begins before the item's end
+    // the ranges from this one on that begin before the item's end
     int n_parts = 0;
     for (uint32_t in = ~0u; in == ~0u; n_parts += __popc(in)) {
         const uint32_t x = blockIdx.x + n_parts + lane;
@@ -1095,12 +1114,13 @@ template <int D, int G, int NT>
 int launch(const Kv4AttnArgs &a, cudaStream_t stream)
 {
     constexpr int R = 8 * NT;
-    constexpr int smem = Shared<D, G, NT>::bytes;
+    constexpr int smem = Shared<D, G, NT>::all;
     static PerDeviceOnce once;
     if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(attn_kv4_kernel<D, G, NT>), smem))
         return FA_ERR_CUDA;
-    constexpr int ctas = kv4_attention_ctas(R);
-    attn_kv4_kernel<D, G, NT><<<ctas, kThreads, smem, stream>>>(a);
+    constexpr int ranges = kv4_attention_ranges(R);
+    attn_kv4_kernel<D, G, NT>
+        <<<kv4_attention_sms, kThreads * kv4_attention_crews(R), smem, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess)
         return FA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -1109,8 +1129,8 @@ int launch(const Kv4AttnArgs &a, cudaStream_t stream)
     const int64_t all_rows = int64_t(a.Nq) * (a.H / a.Hkv), items = int64_t(a.B) * a.Hkv *
                                                                   ((all_rows + R - 1) / R);
     const int rows = int(all_rows < R ? all_rows : R);
-    const bool few = 16 * items <= ctas;
-    cfg.gridDim = dim3(ctas, few ? rows : (rows + kJoinWarps - 1) / kJoinWarps);
+    const bool few = 16 * items <= ranges;
+    cfg.gridDim = dim3(ranges, few ? rows : (rows + kJoinWarps - 1) / kJoinWarps);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

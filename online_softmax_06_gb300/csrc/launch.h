@@ -198,17 +198,23 @@ struct Kv4AttnArgs {
     int whole_items;           // Nk <= kKv4Short
     int *err_word;
 };
-constexpr int kKv4Short = 1024;    // keys up to which a CTA takes a sequence's head whole
+constexpr int kKv4Short = 1024;    // keys up to which a crew takes a sequence's head whole
 constexpr int kKv4MaxSeqs = 1024;  // each CTA lays the sequences' work out in shared memory
-// Query rows (queries x heads of a kv head) that a CTA takes at once.
+// Query rows (queries x heads of a kv head) that a crew takes at once.
 inline int kv4_attention_rows(int Nq, int H, int Hkv)
 {
     return int64_t(Nq) * (H / Hkv) <= 8 ? 8 : 16;
 }
-// CTAs: three on each of 152 SMs, two with the wider tiles' registers.  (Four, of 128
-// registers a thread, take one cell at a time and spill: 64 x 8k keys 123 us against
-// 117, 256 x 1k with groups of 32 102 against 94.)
-__host__ __device__ constexpr int kv4_attention_ctas(int rows) { return rows <= 8 ? 456 : 304; }
+// A CTA an SM, of three crews of four warps, two with the wider tiles' registers; each
+// crew takes a range of the keys.  (Four crews, of 128 registers a thread, take one
+// cell at a time and spill: 64 x 8k keys 122 us against 117, 256 x 1k with groups of
+// 32 103 against 94.)
+constexpr int kv4_attention_sms = 152;
+__host__ __device__ constexpr int kv4_attention_crews(int rows) { return rows <= 8 ? 3 : 2; }
+__host__ __device__ constexpr int kv4_attention_ranges(int rows)
+{
+    return kv4_attention_sms * kv4_attention_crews(rows);
+}
 
 // The form for many query rows (attn_kv4_many.cu): fp16 copies of Q ([Hkv, total_q,
 // H / Hkv, d]) and of the cache ([B, Hkv, 128 n_tiles, d] each), and their factors.
@@ -273,8 +279,8 @@ inline bool kv4_many(int B, int64_t total_q, int Nk, int H, int Hkv, int d)
     return kv4_many_items(B, total_q, H, Hkv) * L.splits >= 24 && L.bytes <= int64_t(8) << 30;
 }
 
-// Workspace: that form's copies; otherwise descriptors (32 bytes a CTA), then for
-// two parts a CTA the (reference, sum) and the fp32 O of each row.
+// Workspace: that form's copies; otherwise descriptors (32 bytes a range), then for
+// two parts a range the (reference, sum) and the fp32 O of each row.
 inline int64_t kv4_attention_workspace_bytes(int B, int Nq, int64_t total_q, int Nk, int H, int Hkv,
                                              int d)
 {
@@ -283,7 +289,7 @@ inline int64_t kv4_attention_workspace_bytes(int B, int Nq, int64_t total_q, int
     if (Nk <= kKv4Short)
         return 0;
     const int rows = kv4_attention_rows(Nq, H, Hkv);
-    return int64_t(kv4_attention_ctas(rows)) * (32 + 2 * rows * (8 + 4 * d));
+    return int64_t(kv4_attention_ranges(rows)) * (32 + 2 * rows * (8 + 4 * d));
 }
 int launch_attention_kv4_many(const Kv4AttnArgs &a, cudaStream_t stream);
 int launch_attention_kv4(const Kv4AttnArgs &a, cudaStream_t stream);

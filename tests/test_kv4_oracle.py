@@ -182,7 +182,7 @@ def test_attention_refusals_without_gpu():
     assert wb(1, 1, 1, 5000, 9, 2, 128) == fa.FA_ERR_BAD_SIZE
     assert wb(1, 1, 1, 5000, 8, 0, 128) == fa.FA_ERR_BAD_SIZE
     assert wb(1, 1, 1, 5000, 8, 2, 96) == fa.FA_ERR_UNSUPPORTED
-    # a descriptor and two parts a CTA, of 8 rows (456 CTAs) or 16 (304)
+    # a descriptor and two parts a range, of 8 rows (456 ranges) or 16 (304)
     for Nq, rows in ((1, 8), (2, 8), (3, 16), (4, 16), (5, 16), (500, 16)):
         assert wb(1, Nq, Nq, 1025, 8, 2, 128) == (456 if rows == 8 else 304) * (32 + 2 * rows * (8 + 512))
 
