@@ -185,13 +185,13 @@ struct Parts {
     float *O;
 };
 
-template <int R>
+template <int D, int R>
 __host__ __device__ inline Parts parts_of(void *ws)
 {
     Parts p;
     p.desc = static_cast<Desc *>(ws);
-    p.ml = reinterpret_cast<float2 *>(p.desc + kv4_attention_ranges(R));
-    p.O = reinterpret_cast<float *>(p.ml + 2 * kv4_attention_ranges(R) * R);
+    p.ml = reinterpret_cast<float2 *>(p.desc + kv4_attention_ranges(R, D));
+    p.O = reinterpret_cast<float *>(p.ml + 2 * kv4_attention_ranges(R, D) * R);
     return p;
 }
 
@@ -231,7 +231,7 @@ struct Shared {
     static constexpr int abort = sum + kWarps * R * 4;               // a wait ran out
     static constexpr int bytes = (abort + 4 + 127) / 128 * 128;
 
-    static constexpr int crews = kv4_attention_crews(R);
+    static constexpr int crews = kv4_attention_crews(R, D);
     static constexpr int pre = 0;                                    // [B + 1] blocks before b
     static constexpr int scan = pre + (kKv4MaxSeqs + 4) * 4;         // a uint2 of each warp
     static constexpr int own = (scan + crews * kWarps * 8 + 127) / 128 * 128;
@@ -451,7 +451,7 @@ __device__ __noinline__ Copy find_copy(const Kv4AttnArgs &a, const uint32_t *s_p
 }
 
 template <int D, int G, int NT>
-__global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT), 1)
+__global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
     attn_kv4_kernel(const Kv4AttnArgs a)
 {
     constexpr int R = 8 * NT;              // query rows of a tile
@@ -545,8 +545,8 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT), 1)
         s_pre[0] = s_cost[0] = 0;
     __syncthreads();
     const uint32_t T = uint32_t(uniform(int(s_pre[a.B])));
-    const uint32_t n_ranges = min(T, uint32_t(kv4_attention_ranges(R)));
-    const Parts parts = parts_of<R>(a.workspace);
+    const uint32_t n_ranges = min(T, uint32_t(kv4_attention_ranges(R, D)));
+    const Parts parts = parts_of<D, R>(a.workspace);
     uint32_t begin = T, end = T;
     if (id < n_ranges) {
         const uint64_t all = uint32_t(uniform(int(s_cost[a.B])));
@@ -1009,7 +1009,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_kv4_join_kernel(const Kv
     constexpr int kPer = D / 32;
     constexpr int kRows = kJoinWarps / kPart;      // of a block
     __shared__ float s_y[kJoinWarps][D], s_m[kJoinWarps], s_s[kJoinWarps];
-    const Parts parts = parts_of<R>(a.workspace);
+    const Parts parts = parts_of<D, R>(a.workspace);
     const Desc desc = parts.desc[blockIdx.x];
     if (desc.item_end == 0)
         return;
@@ -1118,9 +1118,9 @@ int launch(const Kv4AttnArgs &a, cudaStream_t stream)
     static PerDeviceOnce once;
     if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(attn_kv4_kernel<D, G, NT>), smem))
         return FA_ERR_CUDA;
-    constexpr int ranges = kv4_attention_ranges(R);
+    constexpr int ranges = kv4_attention_ranges(R, D);
     attn_kv4_kernel<D, G, NT>
-        <<<kv4_attention_sms, kThreads * kv4_attention_crews(R), smem, stream>>>(a);
+        <<<kv4_attention_sms, kThreads * kv4_attention_crews(R, D), smem, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess)
         return FA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};

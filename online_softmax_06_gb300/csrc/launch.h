@@ -205,15 +205,20 @@ inline int kv4_attention_rows(int Nq, int H, int Hkv)
 {
     return int64_t(Nq) * (H / Hkv) <= 8 ? 8 : 16;
 }
-// A CTA an SM, of three crews of four warps, two with the wider tiles' registers; each
-// crew takes a range of the keys.  (Four crews, of 128 registers a thread, take one
-// cell at a time and spill: 64 x 8k keys 122 us against 117, 256 x 1k with groups of
-// 32 103 against 94.)
+// A CTA an SM, of as many crews of four warps as the registers allow; each crew takes a
+// range of the keys.  More crews of fewer registers take one cell at a time or spill:
+// with d = 128 four crews of 8 rows took 111 us on 64 x 8k keys, three 109, and on 256 x
+// 1k with groups of 32 96, so 88; three of 16 rows 67.5 on 16 x 4 queries, two 65.7.  With
+// d = 64 (accumulators half as large) four instead of three took 49.6 us, not 51.5,
+// on 32 x 4k, and three of 16 rows instead of two 43.7, not 47.2, on 16 x 4 queries.
 constexpr int kv4_attention_sms = 152;
-__host__ __device__ constexpr int kv4_attention_crews(int rows) { return rows <= 8 ? 3 : 2; }
-__host__ __device__ constexpr int kv4_attention_ranges(int rows)
+__host__ __device__ constexpr int kv4_attention_crews(int rows, int d)
 {
-    return kv4_attention_sms * kv4_attention_crews(rows);
+    return (rows <= 8 ? 3 : 2) + (d == 64);
+}
+__host__ __device__ constexpr int kv4_attention_ranges(int rows, int d)
+{
+    return kv4_attention_sms * kv4_attention_crews(rows, d);
 }
 
 // The form for many query rows (attn_kv4_many.cu): fp16 copies of Q ([Hkv, total_q,
@@ -289,7 +294,7 @@ inline int64_t kv4_attention_workspace_bytes(int B, int Nq, int64_t total_q, int
     if (Nk <= kKv4Short)
         return 0;
     const int rows = kv4_attention_rows(Nq, H, Hkv);
-    return int64_t(kv4_attention_ranges(rows)) * (32 + 2 * rows * (8 + 4 * d));
+    return int64_t(kv4_attention_ranges(rows, d)) * (32 + 2 * rows * (8 + 4 * d));
 }
 int launch_attention_kv4_many(const Kv4AttnArgs &a, cudaStream_t stream);
 int launch_attention_kv4(const Kv4AttnArgs &a, cudaStream_t stream);
