@@ -26,9 +26,9 @@
 // What bounds it: a cell of 16 tokens (2304 bytes with d = 128, group 64) costs a
 // warp some 270 instructions, of which half are logical operations at two a cycle
 // and SM, 88 of them the expansion; HBM leaves 100 cycles a cell.  64 sequences of
-// 300 to 16000 keys (32 heads on 8) take 109 us: 7 until all the first cells are
-// there, 93 of keys at 6.4 TB/s, 5 in which the crews end, 4 of the join: 5.5 TB/s,
-// 0.81 of the measured copy rate.  One MMA of 16 x 8 x 16 takes two cycles of an SM
+// 300 to 16000 keys (32 heads on 8) take 106 us: 7 until all the first cells are
+// there, 93 of keys at 6.4 TB/s, 5 in which the crews end, 4 of the join: 5.65 TB/s,
+// 0.83 of the measured copy rate.  One MMA of 16 x 8 x 16 takes two cycles of an SM
 // (605 TFLOP/s), a quarter of the time.
 //
 // One CTA an SM, of crews of four warps that share nothing but the layout of the
@@ -487,7 +487,9 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
     }
     if (tid == 0)
         s_abort = 0;
-    // the join's launch may overlap this kernel: it waits for its end
+    // the kernels before have ended; the join's launch may overlap this kernel, whose
+    // end it waits for
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the line of blocks ------------------------------------------------
@@ -1119,28 +1121,20 @@ int launch(const Kv4AttnArgs &a, cudaStream_t stream)
     if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(attn_kv4_kernel<D, G, NT>), smem))
         return FA_ERR_CUDA;
     constexpr int ranges = kv4_attention_ranges(R, D);
-    attn_kv4_kernel<D, G, NT>
-        <<<kv4_attention_sms, kThreads * kv4_attention_crews(R, D), smem, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess)
+    if (launch_early(attn_kv4_kernel<D, G, NT>, dim3(kv4_attention_sms),
+                     kThreads * kv4_attention_crews(R, D), smem, stream, a) != cudaSuccess)
         return FA_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
     if (a.whole_items)
         return FA_OK;                      // no parts
     const int64_t all_rows = int64_t(a.Nq) * (a.H / a.Hkv), items = int64_t(a.B) * a.Hkv *
                                                                   ((all_rows + R - 1) / R);
     const int rows = int(all_rows < R ? all_rows : R);
     const bool few = 16 * items <= ranges;
-    cfg.gridDim = dim3(ranges, few ? rows : (rows + kJoinWarps - 1) / kJoinWarps);
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, attn_kv4_join_kernel<D, R, kJoinWarps>, a)
-                              : cudaLaunchKernelEx(&cfg, attn_kv4_join_kernel<D, R, 1>, a);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    const dim3 grid(ranges, few ? rows : (rows + kJoinWarps - 1) / kJoinWarps);
+    const cudaError_t e =
+        few ? launch_early(attn_kv4_join_kernel<D, R, kJoinWarps>, grid, kJoinWarps * 32, 0, stream, a)
+            : launch_early(attn_kv4_join_kernel<D, R, 1>, grid, kJoinWarps * 32, 0, stream, a);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D, int G>

@@ -111,6 +111,7 @@ template <int D, int G>
 __global__ void __launch_bounds__(kExpandThreads, 4)
     kv4_expand_kernel(const Kv4AttnArgs a, const Kv4ManyBuffers w)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int kCell = kv4::cell_bytes(D, G), NG = D / G, kN = D / 32, kLanes = D / 16;
     const int tid = threadIdx.x, lane = tid & 31, grp = a.H / a.Hkv;
     if (blockIdx.z >= unsigned(a.B)) {
@@ -859,31 +860,18 @@ int launch(const Kv4AttnArgs &a, cudaStream_t stream)
     const int64_t per_layer = int64_t(at.n_tiles) * a.Hkv * (kExpandThreads / 32) * 4;
     const int64_t layers = (a.total_q * a.H + per_layer - 1) / per_layer;
     const dim3 grid(at.n_tiles, a.Hkv, unsigned(a.B + (layers < 1024 ? layers : 1024)));
-    kv4_expand_kernel<D, G><<<grid, kExpandThreads, 0, stream>>>(a, p.w);
-    if (cudaGetLastError() != cudaSuccess)
+    if (launch_early(kv4_expand_kernel<D, G>, grid, kExpandThreads, 0, stream, a, p.w) != cudaSuccess)
         return FA_ERR_CUDA;
     auto kern = attn_kv4_many_kernel<D>;
     static PerDeviceOnce once;
     if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(kern), int(Cfg<D>::kSmemBytes)))
         return FA_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(blocks));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg<D>::kSmemBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
-    if (e == cudaSuccess && at.splits > 1) {
-        cfg.gridDim = dim3(unsigned(items), 8);
-        cfg.blockDim = dim3(kExpandThreads);
-        cfg.dynamicSmemBytes = 0;
-        e = cudaLaunchKernelEx(&cfg, kv4_many_join_kernel<D>, p);
-    }
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    cudaError_t e = launch_early(kern, dim3(unsigned(blocks)), kThreads, int(Cfg<D>::kSmemBytes),
+                                 stream, p);
+    if (e == cudaSuccess && at.splits > 1)
+        e = launch_early(kv4_many_join_kernel<D>, dim3(unsigned(items), 8), kExpandThreads, 0, stream,
+                         p);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace

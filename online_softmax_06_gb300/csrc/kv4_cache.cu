@@ -191,6 +191,7 @@ template <int D, int G>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     kv4_append_kernel(const Kv4CacheArgs a, int rows_per_block)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     extern __shared__ RowAt at[];
     const int64_t row0 = int64_t(blockIdx.x) * rows_per_block;
     const int rows = int(min(int64_t(rows_per_block), a.total - row0));
@@ -277,6 +278,7 @@ template <int D, int G>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     kv4_read_kernel(const Kv4CacheArgs a, int rows_per_block)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     extern __shared__ RowAt at[];
     const int64_t row0 = int64_t(blockIdx.x) * rows_per_block;
     const int rows = int(min(int64_t(rows_per_block), a.total - row0));
@@ -344,8 +346,8 @@ int launch_rows(F kernel, const Kv4CacheArgs &a, cudaStream_t stream)
     if (blocks > 0x7fffffffLL)
         return FA_ERR_TOO_LARGE;
     const dim3 grid(unsigned(blocks), unsigned((all + kThreads - 1) / kThreads));
-    kernel<<<grid, kThreads, rows * sizeof(RowAt), stream>>>(a, int(rows));
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    return launch_early(kernel, grid, kThreads, int(rows * sizeof(RowAt)), stream, a, int(rows)) ==
+                   cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace

@@ -159,6 +159,27 @@ struct Fp8QuantArgs {
 };
 int launch_fp8_quantize(const Fp8QuantArgs &a, cudaStream_t stream);
 
+// Launches a kernel that waits for those before it (griddepcontrol.wait) ahead of its
+// first access to memory: its start overlaps their end (1 x 200 keys, call after call:
+// 6.2 us, with plain launches 8.2).
+template <typename K, typename... Args>
+cudaError_t launch_early(K kernel, dim3 grid, int threads, int smem, cudaStream_t stream,
+                         const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...), last = cudaGetLastError();
+    return e == cudaSuccess ? last : e;
+}
+
 // Writing to and reading from the 4-bit paged cache (layouts as in fa.h).
 struct Kv4CacheArgs {
     void *K, *V;               // read by the appending kernel, written by the reading one
