@@ -26,10 +26,10 @@
 // What bounds it: a cell of 16 tokens (2304 bytes with d = 128, group 64) costs a
 // warp some 270 instructions, of which half are logical operations at two a cycle
 // and SM, 88 of them the expansion; HBM leaves 100 cycles a cell.  64 sequences of
-// 300 to 16000 keys (32 heads on 8) take 106 us: 7 until all the first cells are
-// there, 93 of keys at 6.4 TB/s, 5 in which the crews end, 4 of the join: 5.65 TB/s,
-// 0.83 of the measured copy rate.  One MMA of 16 x 8 x 16 takes two cycles of an SM
-// (605 TFLOP/s), a quarter of the time.
+// 300 to 16000 keys (32 heads on 8) take 106 us, 5.65 TB/s, 0.83 of the measured copy
+// rate.  By a clock in the kernels (and 3 us more): 7 until all the first cells are
+// there, 93 of keys at 6.4 TB/s, 5 in which the crews end, 4 of the join.  One MMA of
+// 16 x 8 x 16 takes two cycles of an SM (605 TFLOP/s), a quarter of the time.
 //
 // One CTA an SM, of crews of four warps that share nothing but the layout of the
 // work.  As CTAs of their own, three an SM, the crews were served in the order in
@@ -361,7 +361,7 @@ __device__ __forceinline__ void fetch_queries(const Kv4AttnArgs &a, const Item &
                           int64_t(it.kvh * grp + at % grp) * D + 8 * c;
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
-            w[j] = __ldg(reinterpret_cast<const uint4 *>(src + 32 * j));
+            w[j] = *reinterpret_cast<const uint4 *>(src + 32 * j);
     }
 }
 

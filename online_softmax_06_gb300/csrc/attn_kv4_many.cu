@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kExpandThreads, 4)
             float q[kPer], big = 0.f;
 #pragma unroll
             for (int e = 0; e < kPer; e += 2) {
-                const uint32_t z = __ldg(reinterpret_cast<const uint32_t *>(src + e));
+                const uint32_t z = *reinterpret_cast<const uint32_t *>(src + e);
                 q[e] = bf16_lo(z);
                 q[e + 1] = bf16_hi(z);
                 big = ptx::max3(big, fabsf(q[e]), fabsf(q[e + 1]));

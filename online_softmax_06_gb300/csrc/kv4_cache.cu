@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             w[u] = in && row < rows ? at[row] : RowAt{-1, 0};
             x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
             if (w[u].cell >= 0) {
-                x[u][0] = __ldg(reinterpret_cast<const uint4 *>(src + row * stride + part.element(0)));
-                x[u][1] = __ldg(reinterpret_cast<const uint4 *>(src + row * stride + part.element(1)));
+                x[u][0] = *reinterpret_cast<const uint4 *>(src + row * stride + part.element(0));
+                x[u][1] = *reinterpret_cast<const uint4 *>(src + row * stride + part.element(1));
             }
         }
 #pragma unroll

@@ -161,7 +161,8 @@ int launch_fp8_quantize(const Fp8QuantArgs &a, cudaStream_t stream);
 
 // Launches a kernel that waits for those before it (griddepcontrol.wait) ahead of its
 // first access to memory: its start overlaps their end (1 x 200 keys, call after call:
-// 6.2 us, with plain launches 8.2).
+// 6.2 us, with plain launches 8.2).  What it reads may be written after it has started,
+// so not through the read-only path (__ldg).
 template <typename K, typename... Args>
 cudaError_t launch_early(K kernel, dim3 grid, int threads, int smem, cudaStream_t stream,
                          const Args &...args)

@@ -690,3 +690,41 @@ def test_many_rows_factors_that_overflow_together():
     O, lse = run(pool, q, False, True)
     assert torch.isfinite(O).all() and torch.isfinite(lse).all()
     device_error_clear()
+
+
+@pytest.mark.parametrize("form", FORMS, ids=["few", "many"])
+def test_inputs_written_by_the_kernels_just_before(form):
+    """Kernels start while those before them end: queries, new rows, lengths and the table's
+    pages come from the launches directly ahead, again and again in the same places."""
+    lens, Nq, H, Hkv, d, group, page = form
+    pool, q = make(lens, Nq, H, Hkv, d, group, page, seed=400)
+    cache, table = torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table)
+    n = [len(x) for x in q]
+    cu, x = gpu_i32(np.concatenate([[0], np.cumsum(n)])), gpu_bf16(np.concatenate(q))
+    steps = 12
+    g = torch.Generator(device="cuda").manual_seed(7)
+    new = [torch.randn(2, len(lens), 1, Hkv, d, device="cuda", generator=g).bfloat16()
+           for _ in range(steps)]
+    length = [gpu_i32([L - i for L in lens]) for i in range(steps)]
+    place, sl = torch.empty_like(x), torch.empty_like(length[0])
+    rows = torch.empty_like(new[0])
+
+    def step(i, wait):
+        for a, b in ((sl, length[i]), (rows, new[i]), (place, x * (1 + i % 3))):
+            a.copy_(b)
+            wait()
+        fa.kv4_append(rows[0], rows[1], cache, table, sl, group=group)
+        wait()
+        out = fa.attention_kv4(place, cache, table, sl, cu_seqlens=cu, max_q=max(n),
+                               max_seqlen=max(lens), group=group)
+        wait()
+        return out
+
+    fresh = cache.clone()
+    want = [step(i, torch.cuda.synchronize) for i in range(steps)]
+    cache.copy_(fresh)                     # the steps write into it
+    got = [step(i, lambda: None) for i in range(steps)]
+    torch.cuda.synchronize()
+    for (O, lse), (O1, l1) in zip(want, got):
+        assert torch.equal(O, O1) and torch.equal(lse, l1)
+    device_error_clear()
