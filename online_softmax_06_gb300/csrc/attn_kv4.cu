@@ -24,12 +24,12 @@
 // than the products (attn_kv4_many.cu does it where there are rows enough).
 //
 // What bounds it: a cell of 16 tokens (2304 bytes with d = 128, group 64) costs a
-// warp some 270 instructions, of which half are logical operations at two a cycle
-// and SM, 88 of them the expansion; HBM leaves 100 cycles a cell.  64 sequences of
-// 300 to 16000 keys (32 heads on 8) take 106 us, 5.65 TB/s, 0.83 of the measured copy
-// rate.  By a clock in the kernels (and 3 us more): 7 until all the first cells are
-// there, 93 of keys at 6.4 TB/s, 5 in which the crews end, 4 of the join.  One MMA of
-// 16 x 8 x 16 takes two cycles of an SM (605 TFLOP/s), a quarter of the time.
+// warp some 240 instructions with 4 rows, 270 with 8, of which half are logical
+// operations at two a cycle and SM, 88 of them the expansion; HBM leaves 100 cycles a
+// cell.  64 sequences of 300 to 16000 keys (32 heads on 8) take 102 us, 5.9 TB/s, 0.87
+// of the measured copy rate: the start (lengths, page table, first cells: three memory
+// latencies) takes 7 of them, the crews' ends 5, the join 4.  One MMA of 16 x 8 x 16
+// takes two cycles of an SM (605 TFLOP/s), a quarter of the time.
 //
 // One CTA an SM, of crews of four warps that share nothing but the layout of the
 // work.  As CTAs of their own, three an SM, the crews were served in the order in
@@ -221,7 +221,7 @@ struct alignas(16) QueryTile {
 // A crew's shared memory, and at its end what the CTA's crews have in common.
 template <int D, int G, int NT>
 struct Shared {
-    static constexpr int R = 8 * NT;
+    static constexpr int R = 8 * NT;                                 // columns
     static constexpr int ring = 0;                                   // [kWarps][kStages] pairs
     static constexpr int q = ring + kWarps * kStages * 2 * kv4::cell_bytes(D, G);  // QueryTile
     static constexpr int O = q + int(sizeof(QueryTile<D, G, NT>));   // [kWarps / 2][8][D + 4]
@@ -344,18 +344,23 @@ __device__ __forceinline__ uint32_t item_from(const Kv4AttnArgs &a, const uint32
     return it.first == x ? x : it.first + it.nb;
 }
 
-// A lane's share of the 8 query rows of n-tile nt: row g, values 32 j + 8 c ...
-template <int D, int NT>
+// The tile row at column col of the products.  With E = 1 (4 rows and fewer) a lane's
+// second column stays empty, and what it would cost is left out.
+template <int E>
+__host__ __device__ constexpr int row_of(int col) { return E == 1 ? col / 2 : col; }
+
+// A lane's share of the 8 columns of n-tile nt: column g, values 32 j + 8 c ...
+template <int D, int NT, int E>
 __device__ __forceinline__ void fetch_queries(const Kv4AttnArgs &a, const Item &it, int grp, int nt,
                                               uint4 (&w)[D / 32])
 {
-    constexpr int R = 8 * NT, NJ = D / 32;
+    constexpr int R = 4 * NT * E, NJ = D / 32;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int at = it.tile * R + nt * 8 + g, i = at / grp;
+    const int at = it.tile * R + row_of<E>(nt * 8 + g), i = at / grp;
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
         w[j] = make_uint4(0, 0, 0, 0);
-    if (at < it.nq * grp) {
+    if (at < it.nq * grp && (E == 2 || g % 2 == 0)) {
         const auto *src = static_cast<const __nv_bfloat16 *>(a.Q) +
                           int64_t(it.q0 + i) * a.q_stride +
                           int64_t(it.kvh * grp + at % grp) * D + 8 * c;
@@ -366,13 +371,13 @@ __device__ __forceinline__ void fetch_queries(const Kv4AttnArgs &a, const Item &
 }
 
 // They as B fragments, by the warp.
-template <int D, int G, int NT>
+template <int D, int G, int NT, int E>
 __device__ __forceinline__ void place_queries(const Kv4AttnArgs &a, const Item &it, int grp, int nt,
                                               const uint4 (&w)[D / 32], QueryTile<D, G, NT> &to)
 {
-    constexpr int R = 8 * NT, NJ = D / 32, NG = D / G;
+    constexpr int R = 4 * NT * E, NJ = D / 32, NG = D / G;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, r = nt * 8 + g;
-    const int i = (it.tile * R + r) / grp;
+    const int i = (it.tile * R + row_of<E>(r)) / grp;
     float big = 0.f, sum[NG];
 #pragma unroll
     for (int x = 0; x < NG; ++x)
@@ -450,11 +455,12 @@ __device__ __noinline__ Copy find_copy(const Kv4AttnArgs &a, const uint32_t *s_p
     return c;
 }
 
-template <int D, int G, int NT>
+template <int D, int G, int NT, int E>
 __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
     attn_kv4_kernel(const Kv4AttnArgs a)
 {
-    constexpr int R = 8 * NT;              // query rows of a tile
+    constexpr int R = 4 * NT * E;          // query rows of a tile
+    constexpr int kCols = 8 * NT;          // columns of the products
     constexpr int NG = D / G;              // groups of the head dimension
     constexpr int NJ = D / 32;             // words a lane holds of a K row
     constexpr int kCell = kv4::cell_bytes(D, G);
@@ -575,7 +581,7 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
     Item it = uniform(item_at(a, s_pre, grp, R, begin));
     uint4 first_q[NJ];
     if (warp < NT)
-        fetch_queries<D, NT>(a, it, grp, warp, first_q);
+        fetch_queries<D, NT, E>(a, it, grp, warp, first_q);
     const uint32_t n_blocks = end - begin;
     Copy copy{nullptr, 0};
     auto fill = [&](uint32_t k) {
@@ -623,16 +629,16 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
     keep(at_Q);
 
     if (warp < NT)
-        place_queries<D, G, NT>(a, it, grp, warp, first_q, s_q);
+        place_queries<D, G, NT, E>(a, it, grp, warp, first_q, s_q);
     sync_crew();
     for (uint32_t cur = begin; cur < end;) {
         const uint32_t stop = min(end, it.first + it.nb);
         const int rows = min(R, it.nq * grp - it.tile * R);         // rows of this tile
-        float mul[NT][2], qbar[NT][NG][2];     // of rows 2 c, 2 c + 1 of n-tile nt
+        float mul[NT][E], qbar[NT][NG][E];     // of columns 2 c, 2 c + 1 of n-tile nt
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < E; ++e) {
                 const int r = nt * 8 + 2 * c + e;
                 mul[nt][e] = s_q.mul[r];
 #pragma unroll
@@ -641,14 +647,14 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
             }
 
         // ---- the keys ----------------------------------------------------------
-        float O[NT][D / 16][4], ref[NT][2], sum[NT][2], pm[NT][NG][2];
+        float O[NT][D / 16][4], ref[NT][E], sum[NT][E], pm[NT][NG][E];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int x = 0; x < D / 16; ++x)
                 O[nt][x][0] = O[nt][x][1] = O[nt][x][2] = O[nt][x][3] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < E; ++e) {
                 ref[nt][e] = kNoRef;
                 sum[nt][e] = 0.f;
 #pragma unroll
@@ -729,8 +735,8 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
             uint32_t pf[NC][NT][NG][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                bool seen[NC][2][2];
-                // S - `from`, [token g, g + 8][row 2 c, 2 c + 1]
+                bool seen[NC][2][E];
+                // S - `from`, [token g, g + 8][column 2 c, 2 c + 1]
                 auto score = [&](int x, int t, int e, float from) {
                     float s = bf16_lo(pk[x][t][0]) * acc[x][nt][0][2 * t + e], y = -from;
 #pragma unroll
@@ -741,24 +747,24 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
                         y = fmaf(bf16_hi(pk[x][t][gr]), qbar[nt][gr][e], y);
                     return seen[x][t][e] ? fmaf(s, mul[nt][e], y) : -INFINITY;
                 };
-                float P[NC][2][2], over = 0.f;
+                float P[NC][2][E], over = 0.f;
 #pragma unroll
                 for (int x = 0; x < NC; ++x)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
+                        for (int e = 0; e < E; ++e) {
                             seen[x][t][e] = !kMasked || tok + 16 * x + g + 8 * t <
                                                             s_q.end[nt * 8 + 2 * c + e];
                             P[x][t][e] = ptx::ex2(score(x, t, e, ref[nt][e]));
                         }
-                        over = max3(over, P[x][t][0] * w[x][t], P[x][t][1] * w[x][t]);
+                        over = max3(over, P[x][t][0] * w[x][t], P[x][t][E - 1] * w[x][t]);
                     }
                 if (__any_sync(0xffffffffu, over > kLag)) {
                     // a row outgrew its reference: every row's becomes the largest
                     // S + log2 w seen
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < E; ++e) {
                         float S[NC][2], m = ref[nt][e];
 #pragma unroll
                         for (int x = 0; x < NC; ++x)
@@ -791,15 +797,15 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
 #pragma unroll
                 for (int x = 0; x < NC; ++x) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                    for (int e = 0; e < E; ++e)
                         sum[nt][e] += P[x][0][e] + P[x][1][e];
 #pragma unroll
                     for (int y = 0; y < NG; ++y)
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
-                            float ps[2];
+                            float ps[2] = {0.f, 0.f};
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
+                            for (int e = 0; e < E; ++e) {
                                 // a key that the row does not see adds nothing,
                                 // whatever its parameters are
                                 ps[e] = P[x][t][e] * bf16_lo(pv[x][t][y]);
@@ -875,7 +881,7 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
         const Item next = stop < end ? next_item(a, s_pre, grp, R, it) : it;
         uint4 qw[NJ];
         if (warp < NT && stop < end)
-            fetch_queries<D, NT>(a, next, grp, warp, qw);
+            fetch_queries<D, NT, E>(a, next, grp, warp, qw);
         else
             for (int j = 0; j < NJ; ++j)
                 qw[j] = make_uint4(0, 0, 0, 0);
@@ -884,7 +890,7 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < E; ++e) {
                 float s = sum[nt][e];
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1)
@@ -895,8 +901,8 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
                     for (int o = 4; o < 32; o <<= 1)
                         pm[nt][x][e] += __shfl_xor_sync(0xffffffffu, pm[nt][x][e], o);
                 if (g == 0) {
-                    s_ref[warp * R + nt * 8 + 2 * c + e] = ref[nt][e];
-                    s_sum[warp * R + nt * 8 + 2 * c + e] = s;
+                    s_ref[warp * kCols + nt * 8 + 2 * c + e] = ref[nt][e];
+                    s_sum[warp * kCols + nt * 8 + 2 * c + e] = s;
                 }
             }
         sync_crew();
@@ -908,12 +914,12 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
             for (int half = 0; half < 2; ++half) {
                 if (warp / (kWarps / 2) == 1 - half) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = nt * 8 + 2 * c + e;
-                        float m = s_ref[r];
+                    for (int e = 0; e < E; ++e) {
+                        const int col = nt * 8 + 2 * c + e;
+                        float m = s_ref[col];
 #pragma unroll
                         for (int w = 1; w < kWarps; ++w)
-                            m = fmaxf(m, s_ref[w * R + r]);
+                            m = fmaxf(m, s_ref[w * kCols + col]);
                         const float f = ptx::ex2(ref[nt][e] - m);
                         float *row = s_O + (warp % (kWarps / 2) * 8 + 2 * c + e) * kRow + 4 * g;
 #pragma unroll
@@ -932,15 +938,16 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
                         }
                     }
                 } else if (half == 0 && nt == 0 && warp < NT && stop < end) {
-                    place_queries<D, G, NT>(a, next, grp, warp, qw, s_q);
+                    place_queries<D, G, NT, E>(a, next, grp, warp, qw, s_q);
                 }
                 sync_crew();
             }
-            // 8 rows x D values over the threads, four consecutive values each
-            for (int x = tid; x < 8 * (D / 4); x += kThreads) {
-                const int rr = x / (D / 4), d4 = x % (D / 4) * 4, r = nt * 8 + rr;
+            // the rows' D values over the threads, four consecutive values each
+            for (int x = tid; x < 4 * E * (D / 4); x += kThreads) {
+                const int rr = x / (D / 4) * (2 / E), d4 = x % (D / 4) * 4;
+                const int col = nt * 8 + rr, r = row_of<E>(col);
                 float4 y = *reinterpret_cast<const float4 *>(s_O + rr * kRow + d4);
-                float m = s_ref[r];
+                float m = s_ref[col];
 #pragma unroll
                 for (int w = 1; w < kWarps / 2; ++w) {
                     const float4 z =
@@ -949,11 +956,11 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
                 }
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w)
-                    m = fmaxf(m, s_ref[w * R + r]);
+                    m = fmaxf(m, s_ref[w * kCols + col]);
                 float s = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
-                    s = fmaf(s_sum[w * R + r], ptx::ex2(s_ref[w * R + r] - m), s);
+                    s = fmaf(s_sum[w * kCols + col], ptx::ex2(s_ref[w * kCols + col] - m), s);
                 if (r >= rows || s_abort)
                     continue;
                 if (whole) {
@@ -1112,16 +1119,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_kv4_join_kernel(const Kv
     }
 }
 
-template <int D, int G, int NT>
+template <int D, int G, int NT, int E>
 int launch(const Kv4AttnArgs &a, cudaStream_t stream)
 {
-    constexpr int R = 8 * NT;
+    constexpr int R = 4 * NT * E;
     constexpr int smem = Shared<D, G, NT>::all;
     static PerDeviceOnce once;
-    if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(attn_kv4_kernel<D, G, NT>), smem))
+    if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(attn_kv4_kernel<D, G, NT, E>), smem))
         return FA_ERR_CUDA;
     constexpr int ranges = kv4_attention_ranges(R, D);
-    if (launch_early(attn_kv4_kernel<D, G, NT>, dim3(kv4_attention_sms),
+    if (launch_early(attn_kv4_kernel<D, G, NT, E>, dim3(kv4_attention_sms),
                      kThreads * kv4_attention_crews(R, D), smem, stream, a) != cudaSuccess)
         return FA_ERR_CUDA;
     if (a.whole_items)
@@ -1143,8 +1150,11 @@ int launch_rows(const Kv4AttnArgs &a, cudaStream_t stream)
     // Rows beyond 16 go on as further tiles, whose keys come from L2 the second
     // time: 32 rows a tile spill their registers (16 sequences x 4 queries x 8
     // heads a kv head: 102 us, against 77 with two tiles of 16).
-    return kv4_attention_rows(a.Nq, a.H, a.Hkv) == 8 ? launch<D, G, 1>(a, stream)
-                                                     : launch<D, G, 2>(a, stream);
+    switch (kv4_attention_rows(a.Nq, a.H, a.Hkv)) {
+    case 4: return launch<D, G, 1, 1>(a, stream);
+    case 8: return launch<D, G, 1, 2>(a, stream);
+    default: return launch<D, G, 2, 2>(a, stream);
+    }
 }
 
 }  // namespace

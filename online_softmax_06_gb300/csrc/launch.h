@@ -222,10 +222,13 @@ struct Kv4AttnArgs {
 };
 constexpr int kKv4Short = 1024;    // keys up to which a crew takes a sequence's head whole
 constexpr int kKv4MaxSeqs = 1024;  // each CTA lays the sequences' work out in shared memory
-// Query rows (queries x heads of a kv head) that a crew takes at once.
+// Query rows (queries x heads of a kv head) that a crew takes at once.  4 fill every second of
+// 8 columns, and the others' share of the softmax is left out (64 x 8k keys, 4 rows, 103
+// us, as 8 rows 109; 256 x 1k 80 and 88).
 inline int kv4_attention_rows(int Nq, int H, int Hkv)
 {
-    return int64_t(Nq) * (H / Hkv) <= 8 ? 8 : 16;
+    const int64_t rows = int64_t(Nq) * (H / Hkv);
+    return rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
 }
 // A CTA an SM, of as many crews of four warps as the registers allow; each crew takes a
 // range of the keys.  More crews of fewer registers take one cell at a time or spill:

@@ -123,6 +123,10 @@ CASES = [
     ([600, 70, 129], [100, 1, 129], 8, 2, 128, 32, 32, True, True),
     ([600, 70, 0], [33, 0, 2], 2, 2, 64, 32, 64, True, True),
     ([40, 300], [64, 7], 3, 1, 128, 128, 256, False, True),      # more queries than keys
+    ([130, 4100, 9], 1, 3, 1, 128, 64, 32, True, False),         # 3 rows
+    ([2100, 1, 33], 2, 4, 2, 128, 32, 64, True, False),          # 2 queries x 2 heads
+    ([1500, 2, 260], 3, 2, 2, 64, 32, 16, True, False),          # 3 queries; rows without a key
+    ([3000, 700], [4, 1], 1, 1, 128, 128, 128, False, True),
 ]
 
 

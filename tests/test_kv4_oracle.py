@@ -182,9 +182,9 @@ def test_attention_refusals_without_gpu():
     assert wb(1, 1, 1, 5000, 9, 2, 128) == fa.FA_ERR_BAD_SIZE
     assert wb(1, 1, 1, 5000, 8, 0, 128) == fa.FA_ERR_BAD_SIZE
     assert wb(1, 1, 1, 5000, 8, 2, 96) == fa.FA_ERR_UNSUPPORTED
-    # a descriptor and two parts a range, of 8 rows (456 ranges) or 16 (304)
-    for Nq, rows in ((1, 8), (2, 8), (3, 16), (4, 16), (5, 16), (500, 16)):
-        assert wb(1, Nq, Nq, 1025, 8, 2, 128) == (456 if rows == 8 else 304) * (32 + 2 * rows * (8 + 512))
+    # a descriptor and two parts a range, of 4 or 8 rows (456 ranges) or 16 (304)
+    for Nq, rows in ((1, 4), (2, 8), (3, 16), (4, 16), (5, 16), (500, 16)):
+        assert wb(1, Nq, Nq, 1025, 8, 2, 128) == (304 if rows == 16 else 456) * (32 + 2 * rows * (8 + 512))
 
     assert wb(1, 1, 1, 1024, 8, 2, 128) == 0                     # whole heads: no parts
     assert wb(1, 1, 1, -1, 8, 2, 128) == fa.FA_ERR_BAD_SIZE
