@@ -153,7 +153,7 @@ __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x 
 // fills a place again as soon as it has read it; no barrier between warps.  12
 // warps an SM with one pair of 4608 bytes each on its way are 55 KB in flight,
 // against the 36 KB that cover HBM's latency at full rate; three pairs a ring
-// measured the same (64 x 8k keys 119 us, with two 118).
+// measured the same (64 x 8k keys 104 us with either).
 constexpr int kStages = 2;
 constexpr int kJoinWarps = 8;
 
