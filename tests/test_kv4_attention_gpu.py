@@ -732,3 +732,65 @@ def test_inputs_written_by_the_kernels_just_before(form):
     for (O, lse), (O1, l1) in zip(want, got):
         assert torch.equal(O, O1) and torch.equal(lse, l1)
     device_error_clear()
+
+
+@pytest.mark.parametrize("form", FORMS, ids=["few", "many"])
+def test_captured_behind_several_streams(form):
+    """In a graph: behind kernels of two streams, a copy, a fill, and at its very start."""
+    lens, Nq, H, Hkv, d, group, page = form
+    pool, q = make(lens, Nq, H, Hkv, d, group, page, seed=410)
+    O, lse = run(pool, q, True, True)
+    cache, table = torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table)
+    n = [len(x) for x in q]
+    cu, x, sl = gpu_i32(np.concatenate([[0], np.cumsum(n)])), gpu_bf16(np.concatenate(q)), gpu_i32(lens)
+    place, lengths, junk = torch.zeros_like(x), torch.zeros_like(sl), torch.empty(1000, device="cuda")
+    kw = dict(cu_seqlens=cu, max_q=max(n), group=group)
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        first = fa.attention_kv4(x, cache, table, sl, **kw)          # the graph's first nodes
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.mul(x, 1, out=place)                               # a kernel
+            junk.zero_()
+        lengths.copy_(sl)                                            # a copy
+        main.wait_stream(side)
+        second = fa.attention_kv4(place, cache, table, lengths, **kw)
+        lengths.zero_()                                              # a fill
+        third = fa.attention_kv4(place, cache, table, lengths, **kw)
+    for _ in range(3):
+        place.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    for o, l in (first, second):
+        assert torch.equal(o, O) and torch.equal(l, lse)
+    assert (third[0] == 0).all() and torch.isneginf(third[1]).all()
+    device_error_clear()
+
+
+@pytest.mark.parametrize("lens", [[600, 1000, 33], [9000, 40]], ids=["whole", "ranges"])
+def test_steps_straight_after_one_another(lens):
+    """Writing into the pages that the attention launched just before still reads."""
+    steps, B, Hkv, d = 24, len(lens), 4, 128
+    pool, q = make(lens, 1, 16, Hkv, d, 64, 16, seed=420)
+    cache, table = torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table)
+    x, sl = gpu_bf16(np.stack(q)), gpu_i32(lens)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    new = [torch.randn(2, B, 30, Hkv, d, device="cuda", generator=g).bfloat16()
+           for _ in range(steps)]
+
+    def run_all(wait):
+        out = []
+        for k, v in new:                   # the last 30 tokens again and again
+            fa.kv4_append(k, v, cache, table, sl)
+            wait()
+            out.append(fa.attention_kv4(x, cache, table, sl, max_seqlen=max(lens)))
+            wait()
+        torch.cuda.synchronize()
+        return out
+
+    for (O, lse), (O1, l1) in zip(run_all(torch.cuda.synchronize), run_all(lambda: None)):
+        assert torch.equal(O, O1) and torch.equal(lse, l1)
+    device_error_clear()
