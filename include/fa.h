@@ -530,7 +530,7 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  *   ignored.  Calls that may run at the same time need one each.
  * Few query rows a kv head (Nq * H / Hkv; decode steps, drafted tokens): the
  * codes go into the products as they are and nothing is rounded but P, to fp16.
- * Many (128 and more on average, enough of them to fill the GPU; chunks of
+ * Many (about 100 and more on average, enough to fill the GPU; chunks of
  * prompts): the values are first written out as fp16 (2^-11 relative, with a
  * power of two a tile of 128 tokens of a head: values below 2^-28 of the tile's
  * largest have fewer bits), and a NaN of V reaches all of a row that sees it.

@@ -293,15 +293,19 @@ inline Kv4ManyLayout kv4_many_layout(int B, int64_t total_q, int Nk, int H, int 
     return L;
 }
 // Whether a call takes that form.  It writes the whole cache out once, which pays
-// where a sequence has 128 rows a kv head or more on average (4 x 16k keys, 8 kv
-// heads: 128 rows 127 us against 161; 64 x 4k with 64 rows 427 against 330), its
-// kernels where there is some work (4 x 256 queries on 256 keys, 16 heads, 2 GFLOP:
-// 19 us against 34), and some tens of its CTAs where each has few tiles.
+// where a sequence has 128 rows a kv head or more on average (8 kv heads: 4 x 16k keys
+// 128 us against 164, 1 x 16k and 4 x 2k the same), and from 96 on where many heads of
+// 128 fill the GPU (64 x 4k keys with 96 rows 421 us against 492, 16 x 1k 37 against
+// 51, but 1 x 16k 49 against 43 and 16 x 4k with d = 64 88 against 84; 64 x 4k with 64
+// rows 416 against 333); its kernels pay where there is some work (4 x 256 queries on
+// 256 keys, 16 heads, 2 GFLOP: 19 us against 34), and some tens of its CTAs where each
+// has few tiles.
 inline bool kv4_many(int B, int64_t total_q, int Nk, int H, int Hkv, int d)
 {
     const int64_t limit = (int64_t(1) << 31) - 512;
     const int64_t rows = total_q > limit ? 0 : total_q * (H / Hkv);   // of a kv head, all sequences
-    if (rows < int64_t(128) * B || Nk < 128 || B > kKv4MaxSeqs || double(rows) * Hkv > limit ||
+    const int least = d == 128 && int64_t(B) * Hkv >= 128 ? 96 : 128;
+    if (rows < int64_t(least) * B || Nk < 128 || B > kKv4MaxSeqs || double(rows) * Hkv > limit ||
         double(B) * Hkv * (Nk + 127.0) > limit ||
         4.0 * rows * Hkv * Nk * d < 1e9)
         return false;
