@@ -1148,8 +1148,9 @@ template <int D, int G>
 int launch_rows(const Kv4AttnArgs &a, cudaStream_t stream)
 {
     // Rows beyond 16 go on as further tiles, whose keys come from L2 the second
-    // time: 32 rows a tile spill their registers (16 sequences x 4 queries x 8
-    // heads a kv head: 102 us, against 77 with two tiles of 16).
+    // time.  Tiles of 32 rows, one cell at a time, take the same time where their rows
+    // are filled (16 sequences x 4 queries x 8 heads a kv head: 66 us) and more where
+    // not (5 queries: 109 us, so 88).
     switch (kv4_attention_rows(a.Nq, a.H, a.Hkv)) {
     case 4: return launch<D, G, 1, 1>(a, stream);
     case 8: return launch<D, G, 1, 2>(a, stream);
