@@ -233,7 +233,10 @@ struct Shared {
 
     static constexpr int crews = kv4_attention_crews(R, D);
     static constexpr int pre = 0;                                    // [B + 1] blocks before b
-    static constexpr int scan = pre + (kKv4MaxSeqs + 4) * 4;         // a uint2 of each warp
+    // [B + 1] their costs.  Not in a ring: a barrier does not order these stores before
+    // the copies, which another proxy makes
+    static constexpr int cost = pre + (kKv4MaxSeqs + 4) * 4;
+    static constexpr int scan = cost + (kKv4MaxSeqs + 4) * 4;        // a uint2 of each warp
     static constexpr int own = (scan + crews * kWarps * 8 + 127) / 128 * 128;
     static constexpr int all = own + crews * bytes;
 };
@@ -501,8 +504,7 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
     // ---- the line of blocks ------------------------------------------------
     constexpr int kAll = kThreads * Smem::crews;
     const int per = (a.B + kAll - 1) / kAll;
-    // [B + 1], in the first crew's ring until the first copy
-    uint32_t *s_cost = reinterpret_cast<uint32_t *>(smem_cta + Smem::own + Smem::ring);
+    uint32_t *s_cost = reinterpret_cast<uint32_t *>(smem_cta + Smem::cost);
     uint32_t mine = 0, mine_cost = 0;
     for (int i = 0; i < per; ++i) {
         const int b = threadIdx.x * per + i;
@@ -566,7 +568,6 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
         end = __shfl_sync(0xffffffffu, x, 1);
     }
     Desc desc{begin, 0, 0, 0, 0, {}};
-    __syncthreads();                       // s_cost gives way to the copies
     if (begin >= end) {
         if (tid == 0 && !a.whole_items)
             parts.desc[id] = desc;

@@ -794,3 +794,21 @@ def test_steps_straight_after_one_another(lens):
     for (O, lse), (O1, l1) in zip(run_all(torch.cuda.synchronize), run_all(lambda: None)):
         assert torch.equal(O, O1) and torch.equal(lse, l1)
     device_error_clear()
+
+
+@pytest.mark.parametrize("d,group,page", [(64, 64, 16), (128, 64, 32)])
+def test_many_sequences_in_ranges_time_after_time(d, group, page):
+    """The layout of 1024 sequences and the first copies of the keys are apart in shared
+    memory, whichever comes first."""
+    rng = np.random.default_rng(430)
+    lens = [int(x) for x in rng.integers(0, 60, 1024)]
+    lens[0], lens[500], lens[1023] = 1500, 1100, 2000
+    pool, q = make(lens, 1, 2, 1, d, group, page, seed=431)
+    args = (gpu_bf16(np.stack(q)), torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table),
+            gpu_i32(lens))
+    O, lse = fa.attention_kv4(*args, group=group, max_seqlen=2000)
+    check(pool, q, O.reshape(-1, 2, d), lse.transpose(0, 1).reshape(2, -1), 1 / math.sqrt(d), True)
+    for _ in range(50):
+        O1, l1 = fa.attention_kv4(*args, group=group, max_seqlen=2000)
+        assert torch.equal(O, O1) and torch.equal(lse, l1)
+    device_error_clear()
