@@ -535,7 +535,9 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  * power of two a tile of 128 tokens of a head: values below 2^-28 of the tile's
  * largest have fewer bits), and a NaN of V reaches all of a row that sees it.
  * B <= 1024.  Results do not depend on timing: the same call gives the same
- * bits.  One to three kernels on the library stream, no synchronisation.
+ * bits.  One to three kernels on the library stream, no synchronisation.  Rows
+ * whose computation a timed-out wait cut short (FA_DEVERR_WAIT_TIMEOUT) are left
+ * as they were.
  * Errors: FA_ERR_BAD_SIZE (also a workspace that is too small, Nk above the
  * table, H no multiple of Hkv), FA_ERR_UNSUPPORTED (d, group, page_size),
  * FA_ERR_NULL_POINTER, FA_ERR_MISALIGNED, FA_ERR_TOO_LARGE, FA_ERR_NO_DEVICE,
@@ -574,9 +576,10 @@ FA_API int fa_set_stream(void *stream);
 
 /*
  * Failure detection, for tests: arms a wait that cannot complete in the next
- * bf16 attention forward (fa_attention_fwd / fa_attention_fwd_varlen) or
- * one-pass backward (fa_attention_bwd_atomic / fa_attention_bwd_atomic_varlen)
- * launched from this host thread, whichever comes first.  In that launch the
+ * bf16 attention forward (fa_attention_fwd / fa_attention_fwd_varlen), one-pass
+ * backward (fa_attention_bwd_atomic / fa_attention_bwd_atomic_varlen) or
+ * attention over the 4-bit cache (fa_attention_kv4) launched from this host
+ * thread, whichever comes first.  In a forward or backward launch the
  * warp that issues the tensor-core instructions first waits, bounded by `ns`
  * nanoseconds, on a barrier that nothing arrives at.  The wait runs out, sets
  * FA_DEVERR_WAIT_TIMEOUT in the device error word and raises the CTA's abort
@@ -584,10 +587,13 @@ FA_API int fa_set_stream(void *stream);
  * other roles leave their loops, copies already issued are waited for, tensor
  * memory is freed, and O and lse (forward) or dK and dV (backward) are left
  * unwritten; the backward's dQ is converted from an accumulator that received
- * nothing, so it reads zero.  The launch returns FA_OK; the error shows in
- * fa_get_device_error.  One-shot: the setting is consumed by that launch.  The
- * kernels' own waits keep their bound (2 s), so the device stays usable and the
- * next call runs normally.  ns: 1 .. 10^9 arms, 0 disarms.
+ * nothing, so it reads zero.  In fa_attention_kv4 a single warp waits so, for bytes
+ * that no copy brings: the rows that it has a part in are left unwritten, with
+ * others of its share of the work, and the rest comes out right.  The launch
+ * returns FA_OK; the error shows in fa_get_device_error.  One-shot: the setting is
+ * consumed by that launch.  The kernels' own waits keep their bound (2 s), so the
+ * device stays usable and the next call runs normally.  ns: 1 .. 10^9 arms, 0
+ * disarms.
  * Errors: FA_ERR_BAD_SIZE (ns < 0 or > 10^9).
  */
 FA_API int fa_debug_expire_next_wait(int64_t ns);

@@ -173,7 +173,8 @@ struct Desc {          // of a range
     uint32_t begin;    // first block of its range
     uint32_t item_end; // end of the item that begins in it and goes on after it; 0: none
     int b, kvh, tile;  // that item
-    int unused[3];
+    int aborted;       // a wait ran out: parts of the range's items may be missing
+    int unused[2];
 };
 
 // Workspace: Desc[ranges], then (reference, sum) [2 ranges][R], then the
@@ -229,7 +230,8 @@ struct Shared {
     static constexpr int ref = full + kWarps * kStages * 8;          // [kWarps][R]
     static constexpr int sum = ref + kWarps * R * 4;                 // [kWarps][R]
     static constexpr int abort = sum + kWarps * R * 4;               // a wait ran out
-    static constexpr int bytes = (abort + 4 + 127) / 128 * 128;
+    static constexpr int limit = abort + 4;                          // of its waits, ns
+    static constexpr int bytes = (limit + 4 + 127) / 128 * 128;
 
     static constexpr int crews = kv4_attention_crews(R, D);
     static constexpr int pre = 0;                                    // [B + 1] blocks before b
@@ -425,6 +427,19 @@ __device__ __forceinline__ void place_queries(const Kv4AttnArgs &a, const Item &
     }
 }
 
+// A warp's wait for a pair of cells; behind the abort flag stands its limit in ns.
+__device__ __noinline__ bool wait_pair_slow(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                            int *err_word)
+{
+    return ptx::mbar_wait_limited(bar, parity, abort, err_word, uint32_t(abort[1]));
+}
+__device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                          int *err_word)
+{
+    return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity) ||
+                                       wait_pair_slow(bar, parity, abort, err_word)) != 0;
+}
+
 // One copy: `bytes` from `src`; 0: none; -n: n bytes of a page that there is not.
 struct Copy {
     const uint8_t *src;
@@ -483,6 +498,7 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
     float *s_ref = reinterpret_cast<float *>(smem + Smem::ref);
     float *s_sum = reinterpret_cast<float *>(smem + Smem::sum);
     volatile int &s_abort = *reinterpret_cast<volatile int *>(smem + Smem::abort);
+    volatile uint32_t &s_limit = *reinterpret_cast<volatile uint32_t *>(smem + Smem::limit);
     const int tid = threadIdx.x % kThreads, warp = uniform(tid >> 5), lane = tid & 31, g = lane >> 2,
               c = lane & 3;
     auto sync_crew = [&] { asm volatile("bar.sync %0, 128;" ::"r"(crew + 1) : "memory"); };
@@ -494,8 +510,10 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
             ptx::mbar_init(full + i, 2);   // a pair's two lanes
         ptx::fence_barrier_init();
     }
-    if (tid == 0)
+    if (tid == 0) {
         s_abort = 0;
+        s_limit = uint32_t(kWaitTimeoutNs);
+    }
     // the kernels before have ended; the join's launch may overlap this kernel, whose
     // end it waits for
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -567,7 +585,7 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
         begin = __shfl_sync(0xffffffffu, x, 0);
         end = __shfl_sync(0xffffffffu, x, 1);
     }
-    Desc desc{begin, 0, 0, 0, 0, {}};
+    Desc desc{begin, 0, 0, 0, 0, 0, {}};
     if (begin >= end) {
         if (tid == 0 && !a.whole_items)
             parts.desc[id] = desc;
@@ -607,6 +625,12 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
                 ptx::bulk_load(to, copy.src, uint32_t(copy.bytes), bar);
         }
     };
+    // Failure-detection test: in the range that holds the line's middle the first warp's
+    // first pair is to wait for 16 bytes that no copy brings.
+    if (a.expire_wait_ns != 0u && tid == 0 && begin <= T / 2 && T / 2 < end) {
+        s_limit = a.expire_wait_ns;
+        ptx::mbar_expect_tx(full, 16);
+    }
     for (uint32_t k = 0; k < kStages; ++k)
         fill(k);
     const uint32_t ring_at = ptx::smem_u32(ring);
@@ -859,9 +883,9 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
         const uint32_t k_stop = stop - begin;
         const int n_full = max(0, (all_end - kPair - tok + kBlock) / kBlock);
         const uint32_t k_full = min(k_stop, k + uint32_t(n_full));
-        auto landed = [&] {                // else the error is recorded, nothing written
-            stuck = stuck || !ptx::mbar_wait_warp(full + k % kStages, k / kStages & 1, &s_abort,
-                                                  a.err_word);
+        auto landed = [&] {                // else the error is recorded and the crew writes
+                                           // nothing of this item and the later ones
+            stuck = stuck || !wait_pair(full + k % kStages, k / kStages & 1, &s_abort, a.err_word);
             done = stuck ? min(done, k) : done;
             return !stuck;
         };
@@ -995,12 +1019,17 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
         it = next;
     }
     if (s_abort) {
-        // a wait ran out: the copies under way must land before the crew ends
+        // a wait ran out: the join leaves out the items that have a part here, and the
+        // copies under way must land before the crew ends
         desc.item_end = 0;
-        volatile int go_on = 0;
-        for (uint32_t k = done; k < min(done + kStages, n_blocks); ++k)
+        desc.aborted = 1;
+        if (a.expire_wait_ns != 0u && tid == 0 && begin <= T / 2 && T / 2 < end)
+            ptx::mbar_complete_tx(full, 16);
+        for (uint32_t k = done; k < min(done + kStages, n_blocks); ++k) {
+            volatile int go_on = 0;
             ptx::mbar_wait_limited(full + k % kStages, k / kStages & 1, &go_on, a.err_word,
                                    kWaitTimeoutNs);
+        }
     }
     if (tid == 0 && !a.whole_items)
         parts.desc[id] = desc;
@@ -1011,7 +1040,8 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
 // take every kPart-th part, eight loads of O under way at a time, and their sums
 // are added in the order of the warps.  Few items have many parts each and take
 // 8 warps a row (1 x 130001 keys in 76 parts: 28 us with one, 7 with eight); many
-// items have a few and take one (64 x 8 items: 6 us, with eight 10).
+// items have a few and take one (64 x 8 items: 6 us, with eight 10).  An item with a
+// part in a range where a wait ran out is not written: parts of it may be missing.
 template <int D, int R, int kPart>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_kv4_join_kernel(const Kv4AttnArgs a)
 {
@@ -1037,10 +1067,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_kv4_join_kernel(const Kv
         y[e] = 0.f;
     // the ranges from this one on that begin before the item's end
     int n_parts = 0;
+    bool aborted = false;
     for (uint32_t in = ~0u; in == ~0u; n_parts += __popc(in)) {
         const uint32_t x = blockIdx.x + n_parts + lane;
-        in = __ballot_sync(0xffffffffu, x < gridDim.x && parts.desc[x].begin < desc.item_end);
+        const bool part = x < gridDim.x && parts.desc[x].begin < desc.item_end;
+        aborted = aborted || (part && parts.desc[x].aborted);
+        in = __ballot_sync(0xffffffffu, part);
     }
+    if (__any_sync(0xffffffffu, aborted))  // in every warp of the block alike
+        return;
     if (desc.tile * R + r >= all)
         n_parts = 0;
     for (int p0 = warp % kPart; p0 < n_parts; p0 += 32 * kPart) {

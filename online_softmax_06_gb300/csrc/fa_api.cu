@@ -19,8 +19,8 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 thread_local cudaStream_t t_stream = nullptr;
-// fa_debug_expire_next_wait: armed for the next bf16 forward or one-pass
-// backward from this thread
+// fa_debug_expire_next_wait: armed for the next bf16 forward, one-pass backward
+// or 4-bit cache attention from this thread
 thread_local uint32_t t_expire_wait_ns = 0;
 
 struct DeviceInfo {
@@ -935,6 +935,8 @@ int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num
     a.workspace = workspace;
     a.whole_items = Nk <= fa::kKv4Short;
     a.err_word = dev->err_word;
+    a.expire_wait_ns = fa::t_expire_wait_ns;
+    fa::t_expire_wait_ns = 0;
     return fa::kv4_many(B, total_q, Nk, H, Hkv, d) ? fa::launch_attention_kv4_many(a, fa::t_stream)
                                                    : fa::launch_attention_kv4(a, fa::t_stream);
 }

@@ -219,6 +219,7 @@ struct Kv4AttnArgs {
     void *workspace;           // not used with whole_items
     int whole_items;           // Nk <= kKv4Short
     int *err_word;
+    uint32_t expire_wait_ns;   // failure-detection test (fa_debug_expire_next_wait), or 0
 };
 constexpr int kKv4Short = 1024;    // keys up to which a crew takes a sequence's head whole
 constexpr int kKv4MaxSeqs = 1024;  // each CTA lays the sequences' work out in shared memory

@@ -19,7 +19,9 @@ import torch
 import online_softmax_06_gb300 as fa
 import oracle
 import workloads
+from kv4_common import Pool, bf16_rows, gpu_bf16, gpu_i32, kv4
 from gpu_common import ATTN_BF16_LSE_TOL, ATTN_BF16_O_TOL, max_abs, require_gpu
+from test_kv4_attention_gpu import params
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +138,75 @@ def test_expired_wait_in_one_pass_backward(dev, packed, lens, d, causal):
     for name, g in (("dQ", dq), ("dK", dk), ("dV", dv)):
         e = _normwise(g.float().cpu().numpy(), ref[name])
         assert e <= BWD_TOL, f"{name}: {e}"
+
+
+def _kv4_expired(lens, nq, H, Hkv, d, form, max_seqlen=None):
+    """One call with a wait that runs out, then one without: (rows written right, rows
+    untouched) of the first as masks [total, H], having checked both against the oracle."""
+    rng = np.random.default_rng(sum(lens) + nq)
+    pool = Pool(lens, Hkv, d, 64, 32, seed=7)
+    pool.fill([bf16_rows(rng, n, Hkv, d) for n in lens], [bf16_rows(rng, n, Hkv, d) for n in lens])
+    q = [bf16_rows(rng, nq, H, d) for _ in lens]
+    x, cache, table = gpu_bf16(np.stack(q)), torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table)
+    o = torch.full_like(x, 3.0)
+    lse = torch.full((len(lens), H, nq), 3.0, device="cuda")
+    # the workspace holds what an earlier call may have left: parts that would count
+    ws = torch.full((fa.fa_attention_kv4_workspace_bytes(len(lens), nq, len(lens) * nq, max_seqlen, H,
+                                                         Hkv, d),), 0x3f, dtype=torch.uint8, device="cuda")
+    call = lambda: fa.attention_kv4(x, cache, table, gpu_i32(lens), max_seqlen=max_seqlen,  # noqa: E731
+                                    out=o, lse=lse, workspace=ws)
+    assert fa.fa_get_device_error() == 0
+    assert fa.fa_debug_expire_next_wait(20_000) == 0
+    t0 = time.perf_counter()
+    call()
+    torch.cuda.synchronize()
+    elapsed = time.perf_counter() - t0
+    assert fa.fa_get_device_error() == fa.FA_DEVERR_WAIT_TIMEOUT
+    assert fa.fa_get_device_error() == 0
+    assert elapsed < 1.5, elapsed
+    # the tolerances of the cache's own tests, with the largest of all sequences
+    ref = [kv4.attention(y, *pool.rows(b), 1 / math.sqrt(d), True) for b, y in enumerate(q)]
+    Or, lr = np.concatenate([r[0] for r in ref]), np.concatenate([r[1].T for r in ref])
+    par = [params(pool, b) for b in range(len(lens))]
+    s_v, v_max = max(p[1] for p in par), max(p[2] for p in par)
+    dots = lambda ks: max(float((np.abs(y[:, h]) @ np.abs(k[:, h // (H // Hkv)]).T).max())  # noqa: E731
+                          for y, k in zip(q, ks) for h in range(H)) / math.sqrt(d)
+    eS = dots([p[0] for p in par]) * 2.0 ** -19
+    if form == "many":
+        eS += dots([pool.rows(b)[0] for b in range(len(lens))]) * 2.0 ** -11
+    tol = 4 * eS * v_max + 2.0 ** -8 * np.abs(Or) + 2.0 ** -10 * (v_max if form == "many" else 15 * s_v)
+    tol_l = 2 * eS + 2.0 ** -20 + 2.0 ** -22 * np.abs(lr)
+
+    def right():
+        oo = o.double().cpu().numpy().reshape(-1, H, d)
+        ll = lse.transpose(1, 2).reshape(-1, H).double().cpu().numpy()
+        return oo, ll, (np.abs(oo - Or) <= tol).all(-1) & (np.abs(ll - lr) <= tol_l)
+
+    oo, ll, good = right()
+    stay = (oo == 3.0).all(-1) & (ll == 3.0)
+    call()
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_error() == 0
+    assert right()[2].all()
+    return good, stay
+
+
+@pytest.mark.parametrize("lens,nq,H,Hkv,d", [
+    ([30000], 1, 8, 2, 64),               # two items over all ranges, joined from many parts
+    ([9000, 40, 5000, 700], 2, 4, 2, 128),
+    ([1000, 33, 600], 1, 4, 2, 64),       # heads whole, no join
+])
+def test_expired_wait_in_cache_attention(dev, lens, nq, H, Hkv, d):
+    """Few query rows: no item with a part in the range of the warp that gave up is
+    written, whatever the parts' memory held; the rest is right."""
+    bound = max(lens)
+    good, stay = _kv4_expired(lens, nq, H, Hkv, d, "few", bound)
+    assert (good | stay).all()
+    assert stay.any()
+    # rows of a (sequence, kv head) item go together
+    for b in range(len(lens)):
+        for h in range(Hkv):
+            rows, heads = slice(b * nq, (b + 1) * nq), slice(h * H // Hkv, (h + 1) * H // Hkv)
+            assert len(set(stay[rows, heads].flatten())) == 1
+    if len(lens) > 1:
+        assert good.any()
