@@ -281,7 +281,7 @@ struct Cfg {
     static constexpr int kStages = D == 128 ? 4 : 8;                 // K/V ring depth
     static constexpr uint32_t kOffRing = 2 * kTileBytes;
     static constexpr uint32_t kOffBar = kOffRing + kStages * kTileBytes;
-    static constexpr uint32_t kBarBytes = 8 * (2 + 2 * kStages + 2 + 2 + 2 + 1);
+    static constexpr uint32_t kBarBytes = 8 * (2 + 2 * kStages + 2 + 2 + 2 + 1 + 1);
     static constexpr uint32_t kSmemBytes = kOffBar + kBarBytes + 16 + 1024;  // +1024 align slack
 };
 
@@ -350,7 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *q_full = bars, *kv_full = bars + 2, *kv_empty = kv_full + C::kStages,
              *s_full = kv_empty + C::kStages, *p_full = s_full + 2, *o_full = p_full + 2,
-             *drain = o_full + 2;
+             *drain = o_full + 2,
+             *never = drain + 1;      // nothing arrives: the failure-detection test waits here
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + (C::kBarBytes / 8));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -412,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&o_full[t], 1);
         }
         ptx::mbar_init(drain, 1);
+        ptx::mbar_init(never, 1);
         *abort_flag = 0;
         ptx::fence_barrier_init();
     }
@@ -466,15 +468,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         load_q(1);
                 }
             }
-            if (aborted || *abort_flag) {
-                // every copy already issued lands before the CTA goes away
-                for (int t = 0; t < 2; ++t)
-                    if (q_issued[t])
-                        drain_wait(&q_full[t], 0);
-                for (int s = 0; s < C::kStages; ++s)
-                    if (last_phase[s] >= 0)
-                        drain_wait(&kv_full[s], uint32_t(last_phase[s]));
-            }
+            // Every copy issued lands before the CTA goes away, also where another
+            // warp gives up after this one is through.
+            for (int t = 0; t < 2; ++t)
+                if (q_issued[t])
+                    drain_wait(&q_full[t], 0);
+            for (int s = 0; s < C::kStages; ++s)
+                if (last_phase[s] >= 0)
+                    drain_wait(&kv_full[s], uint32_t(last_phase[s]));
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -535,7 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_after_sync();
             return ok;
         };
-        if (n_max > 0) do {
+        // Failure-detection test: in the first CTA of the longest sequence's first head a
+        // wait on a barrier that nothing arrives at runs out.
+        if (a.expire_wait_ns != 0u && rest == 0 && pair == 0)
+            aborted = !__all_sync(0xffffffffu, ptx::mbar_wait_limited(never, 0, abort_flag, a.err_word,
+                                                                      a.expire_wait_ns));
+        if (n_max > 0 && !aborted) do {
             uint64_t k_desc, v_desc, unused;
             if (!next_stage(k_desc, unused))
                 break;
@@ -721,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     dst[q] = make_uint4(0, 0, 0, 0);
                 store_lse(x, -INFINITY);
             }
-        } else if (!aborted && ptx::mbar_wait(&o_full[t], 0, abort_flag, a.err_word)) {
+        } else if (!aborted && ptx::mbar_wait_warp(&o_full[t], 0, abort_flag, a.err_word)) {
             ptx::tc_fence_after_sync();
             const bool any = l > 0.f || l != l;
             const float inv = any ? 1.f / l : 0.f;
@@ -761,6 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p.w.ml[part] = make_float2(m, l);
             else if (row_ok)
                 store_lse(x, any ? (m + log2f(l)) * kLn2 : -INFINITY);
+        } else if (row_ok && parts) {
+            p.w.ml[part] = make_float2(0.f, -1.f);     // a wait ran out: no such part
         }
     }
 
@@ -773,7 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the ranges of the items that have several, in their order: block (x, y)
-// takes every eighth eight rows of item x, a warp a row.
+// takes every eighth eight rows of item x, a warp a row.  Rows that lack a part (its
+// sum is negative: a wait ran out) stay as they were.
 template <int D>
 __global__ void __launch_bounds__(kExpandThreads) kv4_many_join_kernel(const ManyParams p)
 {
@@ -796,14 +805,20 @@ __global__ void __launch_bounds__(kExpandThreads) kv4_many_join_kernel(const Man
          x += int(gridDim.y) * (kExpandThreads / 32)) {
         const int64_t row = (int64_t(h) * a.total_q + seq.q0) * grp + x, step = a.total_q * a.H;
         float m = -INFINITY, l = 0.f, y[kPer];
-        for (int s = 0; s < n; ++s)
-            m = fmaxf(m, p.w.ml[s * step + row].x);
+        bool lacks = false;
+        for (int s = 0; s < n; ++s) {
+            const float2 ml = p.w.ml[s * step + row];
+            m = fmaxf(m, ml.x);
+            lacks = lacks || ml.y < 0.f;
+        }
+        if (lacks)
+            continue;
 #pragma unroll
         for (int e = 0; e < kPer; ++e)
             y[e] = 0.f;
         for (int s = 0; s < n; ++s) {
             const float2 ml = p.w.ml[s * step + row];
-            if (ml.y == 0.f)                   // nothing seen, or nothing written
+            if (ml.y == 0.f)                   // nothing seen
                 continue;
             const float f = ptx::ex2(ml.x - m);
             l = fmaf(ml.y, f, l);

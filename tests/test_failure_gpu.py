@@ -210,3 +210,14 @@ def test_expired_wait_in_cache_attention(dev, lens, nq, H, Hkv, d):
             assert len(set(stay[rows, heads].flatten())) == 1
     if len(lens) > 1:
         assert good.any()
+
+
+@pytest.mark.parametrize("lens", [[2300, 4500], [513, 700]], ids=["ranges", "whole"])
+def test_expired_wait_in_cache_attention_many_rows(dev, lens):
+    """Many query rows: the 256 rows of the CTA whose wait ran out (those of the longest
+    sequence's first head) stay, with one range of keys or several; the rest is right."""
+    good, stay = _kv4_expired(lens, 300, 16, 16, 64, "many", max(lens))
+    want = np.zeros_like(stay)
+    want[300:556, 0] = True
+    assert np.array_equal(stay, want)
+    assert good[~want].all()
