@@ -529,7 +529,10 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  *   fa_attention_kv4_workspace_bytes(...) bytes; contents on entry are
  *   ignored.  Calls that may run at the same time need one each.
  * Few query rows a kv head (Nq * H / Hkv; decode steps, drafted tokens): the
- * codes go into the products as they are and nothing is rounded but P, to fp16.
+ * codes go into the products as they are.  Rounded to fp16 are P times a group's
+ * scale (2^-11 relative, after a power of two for each row and group, so that a
+ * group's accuracy does not depend on its neighbours) and Q (exact down to 2^-26
+ * of a row's largest value).
  * Many (about 100 and more on average, enough to fill the GPU; chunks of
  * prompts): the values are first written out as fp16 (2^-11 relative, with a
  * power of two a tile of 128 tokens of a head: values below 2^-28 of the tile's

@@ -14,7 +14,8 @@
 // matrix instructions take subnormals exactly; 2^24 and the 16 go into Q and
 // the epilogue.  Q is scaled per row by a power of two into fp16's range, so
 // its 8 bits are exact down to 2^-26 of the row's largest value.  P s is
-// rounded to fp16 (2^-11), against 2^-8 for bf16.
+// rounded to fp16 (2^-11, against 2^-8 for bf16), after a power of two for each row
+// and group.
 //
 // Layout: keys are the rows (M = 16 tokens), query rows (query, head of the
 // group) the columns (N = 8) of mma.m16n8k16, S^T = K Q^T and O^T = V^T P^T, so
@@ -57,11 +58,20 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kPair = 2 * kv4::kCellTokens;         // tokens that a warp copies and takes at once
 constexpr int kBlock = kWarps * kPair;              // tokens of a block: two cells each warp
 constexpr float kNoRef = -1e30f;   // reference of a row that has seen no key: exp2(-inf - kNoRef) = 0
-// A row's reference is max(S + log2 w), w the weight of a key's V parameters, so
-// that P s <= 1 in fp16 whatever the scales are; it may lag by a factor of 16.
-// w >= 2^-92 keeps P <= 2^96 and the sum of 2^31 of them finite.
-constexpr float kLag = 16.f;
-constexpr float kLeastWeight = 0x1p-92f;
+// A row's reference stands kRefAbove above its largest S and may lag until a P exceeds
+// kMostP, so that the fp32 sums of P and P m stay finite for values up to 2^110.  P s
+// goes to fp16 after a power of two of the row and group (`up`) that brings the largest
+// into [2^10, 2^11), up to kMostPs as it lags: a group of small scales keeps its bits
+// beside one of large scales, and a key of 2^-24 of the largest weight its share.  (With
+// one reference for all groups, P s <= 1 for a key's largest scale, a group of scales
+// 2^-20 of its neighbour's was off by three of its own steps.  Times are the same within
+// 2 %: 64 x 8k keys 102.3 us, so 101.8; 256 x 1k 79.7 and 78.2; 32 x 4k 42.3 and 44.9.)
+constexpr float kRefAbove = 10.f, kMostP = 0x1p-2f, kMostPs = 0x1p15f;
+constexpr int kMostUp = 120;       // log2 of `up` at the most, and of 1 / `up`
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
+// 1 / x of such a power of two
+__device__ __forceinline__ float inverse(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -672,7 +682,7 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
             }
 
         // ---- the keys ----------------------------------------------------------
-        float O[NT][D / 16][4], ref[NT][E], sum[NT][E], pm[NT][NG][E];
+        float O[NT][D / 16][4], ref[NT][E], sum[NT][E], pm[NT][NG][E], up[NT][NG][E];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -683,8 +693,10 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
                 ref[nt][e] = kNoRef;
                 sum[nt][e] = 0.f;
 #pragma unroll
-                for (int x = 0; x < NG; ++x)
+                for (int x = 0; x < NG; ++x) {
                     pm[nt][x][e] = 0.f;
+                    up[nt][x][e] = 1.f;
+                }
             }
         }
         // The keys of kCells cells, from token `tok` on.  kMasked: some query row of
@@ -742,21 +754,6 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
                             for (int y = 0; y < NG; ++y)
                                 pk[x][t][y] = pv[x][t][y] = 0;
             }
-            float w[NC][2];
-#pragma unroll
-            for (int x = 0; x < NC; ++x)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    float s_big = bf16_lo(pv[x][t][0]), m_big = fabsf(bf16_hi(pv[x][t][0]));
-#pragma unroll
-                    for (int y = 1; y < NG; ++y) {
-                        s_big = fmaxf(s_big, bf16_lo(pv[x][t][y]));
-                        m_big = fmaxf(m_big, fabsf(bf16_hi(pv[x][t][y])));
-                    }
-                    // |m| counts too (a constant group has s = 0), so that P m stays
-                    // finite in fp32
-                    w[x][t] = max3(s_big, m_big * 0x1p-12f, kLeastWeight);
-                }
             uint32_t pf[NC][NT][NG][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -772,7 +769,36 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
                         y = fmaf(bf16_hi(pk[x][t][gr]), qbar[nt][gr][e], y);
                     return seen[x][t][e] ? fmaf(s, mul[nt][e], y) : -INFINITY;
                 };
-                float P[NC][2][E], over = 0.f;
+                float P[NC][2][E];
+                // P s in fp16; whether one outgrew its power of two
+                auto weigh = [&] {
+                    float over = 0.f;
+#pragma unroll
+                    for (int x = 0; x < NC; ++x)
+#pragma unroll
+                        for (int y = 0; y < NG; ++y) {
+                            float ps[2][2] = {{0.f, 0.f}, {0.f, 0.f}};     // [t][e]
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                                for (int e = 0; e < E; ++e) {
+                                    // (a product with s first might be infinite where P is 0)
+                                    ps[t][e] = P[x][t][e] * up[nt][y][e] * bf16_lo(pv[x][t][y]);
+                                    // a key that the row does not see adds nothing,
+                                    // whatever its parameters are
+                                    if (kMasked && !seen[x][t][e])
+                                        ps[t][e] = 0.f;
+                                }
+                                if (E == 2)
+                                    over = max3(over, ps[t][0], ps[t][1]);
+                                pf[x][nt][y][t] = pack_f16(ps[t][0], ps[t][1]);
+                            }
+                            if (E == 1)
+                                over = max3(over, ps[0][0], ps[1][0]);
+                        }
+                    return over > kMostPs;
+                };
+                float over = 0.f;
 #pragma unroll
                 for (int x = 0; x < NC; ++x)
 #pragma unroll
@@ -783,11 +809,14 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
                                                             s_q.end[nt * 8 + 2 * c + e];
                             P[x][t][e] = ptx::ex2(score(x, t, e, ref[nt][e]));
                         }
-                        over = max3(over, P[x][t][0] * w[x][t], P[x][t][E - 1] * w[x][t]);
+                        if (E == 2)
+                            over = max3(over, P[x][t][0], P[x][t][E - 1]);
+                        else if (t == 1)
+                            over = max3(over, P[x][0][0], P[x][1][0]);
                     }
-                if (__any_sync(0xffffffffu, over > kLag)) {
-                    // a row outgrew its reference: every row's becomes the largest
-                    // S + log2 w seen
+                if (__any_sync(0xffffffffu, weigh() || over > kMostP)) {
+                    // a row outgrew its reference, or a group its power of two: all go by
+                    // the largest seen
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
                         float S[NC][2], m = ref[nt][e];
@@ -796,7 +825,7 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
 #pragma unroll
                             for (int t = 0; t < 2; ++t) {
                                 S[x][t] = score(x, t, e, 0.f);
-                                m = fmaxf(m, S[x][t] + __log2f(w[x][t]));
+                                m = fmaxf(m, S[x][t] + kRefAbove);
                             }
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
@@ -805,19 +834,34 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
                         ref[nt][e] = m;
                         sum[nt][e] *= f;
 #pragma unroll
-                        for (int y = 0; y < NG; ++y)
-                            pm[nt][y][e] *= f;
-#pragma unroll
-                        for (int y = 0; y < D / 16; ++y) {
-                            O[nt][y][e] *= f;
-                            O[nt][y][2 + e] *= f;
-                        }
-#pragma unroll
                         for (int x = 0; x < NC; ++x)
 #pragma unroll
                             for (int t = 0; t < 2; ++t)
                                 P[x][t][e] = ptx::ex2(S[x][t] - m);
+#pragma unroll
+                        for (int y = 0; y < NG; ++y) {
+                            const float old = inverse(up[nt][y][e]);
+                            float big = 0x1p10f * f * old;
+#pragma unroll
+                            for (int x = 0; x < NC; ++x)
+#pragma unroll
+                                for (int t = 0; t < 2; ++t)
+                                    big = fmaxf(big, P[x][t][e] * bf16_lo(pv[x][t][y]));
+                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 4));
+                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 8));
+                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 16));
+                            const int log = 137 - int(__float_as_uint(big) >> 23);
+                            up[nt][y][e] = pow2(max(-kMostUp, min(kMostUp, log)));
+                            const float r = f * up[nt][y][e] * old;
+                            pm[nt][y][e] *= f;
+#pragma unroll
+                            for (int q = 2 * y * (G / 32); q < 2 * (y + 1) * (G / 32); ++q) {
+                                O[nt][q][e] *= r;
+                                O[nt][q][2 + e] *= r;
+                            }
+                        }
                     }
+                    weigh();
                 }
 #pragma unroll
                 for (int x = 0; x < NC; ++x) {
@@ -828,20 +872,14 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
                     for (int y = 0; y < NG; ++y)
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
-                            float ps[2] = {0.f, 0.f};
 #pragma unroll
                             for (int e = 0; e < E; ++e) {
-                                // a key that the row does not see adds nothing,
-                                // whatever its parameters are
-                                ps[e] = P[x][t][e] * bf16_lo(pv[x][t][y]);
                                 const float z =
                                     fmaf(P[x][t][e], bf16_hi(pv[x][t][y]), pm[nt][y][e]);
-                                if (kMasked && !seen[x][t][e])
-                                    ps[e] = 0.f;
-                                else
+                                if (!kMasked || seen[x][t][e])
                                     pm[nt][y][e] = z;
                             }
-                            pf[x][nt][y][t] = transpose8x8(pack_f16(ps[0], ps[1]));
+                            pf[x][nt][y][t] = transpose8x8(pf[x][nt][y][t]);
                         }
                 }
             }
@@ -950,10 +988,12 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
 #pragma unroll
                         for (int q = 0; q < D / 32; ++q) {
                             const float p = pm[nt][32 * q / G][e];
-                            float4 y = make_float4(fmaf(O[nt][2 * q][e], 0x1p24f, p) * f,
-                                                   fmaf(O[nt][2 * q][2 + e], 0x1p20f, p) * f,
-                                                   fmaf(O[nt][2 * q + 1][e], 0x1p24f, p) * f,
-                                                   fmaf(O[nt][2 * q + 1][2 + e], 0x1p20f, p) * f);
+                            const float down = inverse(up[nt][32 * q / G][e]);
+                            float4 y =
+                                make_float4(fmaf(O[nt][2 * q][e] * 0x1p24f, down, p) * f,
+                                            fmaf(O[nt][2 * q][2 + e] * 0x1p20f, down, p) * f,
+                                            fmaf(O[nt][2 * q + 1][e] * 0x1p24f, down, p) * f,
+                                            fmaf(O[nt][2 * q + 1][2 + e] * 0x1p20f, down, p) * f);
                             float4 *at = reinterpret_cast<float4 *>(row + 32 * q);
                             if (half == 1) {
                                 const float4 z = *at;

@@ -812,3 +812,55 @@ def test_many_sequences_in_ranges_time_after_time(d, group, page):
         O1, l1 = fa.attention_kv4(*args, group=group, max_seqlen=2000)
         assert torch.equal(O, O1) and torch.equal(lse, l1)
     device_error_clear()
+
+
+def group_params(pool, b):
+    """(scale, |min|) of V, float64 [L, Hkv, d / group], from the values held (a group's
+    largest code is 15, its least 0)."""
+    V = pool.rows(b)[1]
+    g = V.reshape(*V.shape[:2], -1, pool.group)
+    return (g.max(-1) - g.min(-1)) / 15, np.abs(g.min(-1))
+
+
+@pytest.mark.parametrize("H,Nq", [(4, 1), (8, 1), (4, 4)], ids=["4 rows", "8 rows", "16 rows"])
+@pytest.mark.parametrize("d,group", [(128, 64), (128, 32), (64, 32)])
+@pytest.mark.parametrize("k", [8, 12, 16, 20, 40])
+def test_groups_of_far_apart_scales(H, Nq, d, group, k):
+    """A group of V keeps its accuracy beside groups of scales 2^k times its own, in every
+    key, or in every other one.
+
+    Few rows: P s goes to fp16 after a power of two of its (row, group), so 2^-11 of
+    each key's P 15 s, and a fixed step of 2^-25 where the largest P s of the group is
+    2^10 at least: 2^-35 of it a key, 2^-23 for 4000 keys.  Errors of S (eS) act twice,
+    on the weights and their sum, and on codes and minimum alike; the fp32 sums of at
+    most 2^8 terms a lane add 2^-16 of the sum of the magnitudes.  The bound goes by the
+    row's and the group's own P, s and m:
+        2 u16 sum_j P 15 s + (4 eS + 2^-16) sum_j P (15 s + |m|) + ub |ref|.
+    """
+    L = 4000
+    rng = np.random.default_rng(440 + k)
+    pool = Pool([L], 1, d, group, 64, seed=441)
+    v = bf16_rows(rng, L, 1, d)
+    v[:, :, :group] *= 2.0 ** -k
+    v[::2, :, -group:] *= 2.0 ** -k                # the last group's in every other key
+    pool.fill([bf16_rows(rng, L, 1, d, std=1.3)], [v])
+    q = bf16_rows(rng, Nq, H, d, std=1.3)
+    scale = 1 / math.sqrt(d)
+    O, lse = run(pool, [q], True, False, scale=scale)
+    K, V = pool.rows(0)
+    Or, lr = kv4.attention(q, K, V, scale, True)
+    s, m = (np.repeat(x[:, 0], group, -1) for x in group_params(pool, 0))
+    k_abs = params(pool, 0)[0]
+    eS = scale * float(np.max(np.abs(q).reshape(-1, d) @ k_abs[:, 0].T)) * 2.0 ** -19
+    o = O.double().cpu().numpy().reshape(Nq, H, d)
+    for i in range(Nq):
+        S = scale * q[i] @ K[:, 0].T
+        S[:, L - Nq + i + 1:] = -np.inf
+        P = np.exp(S - S.max(1, keepdims=True))
+        P /= P.sum(1, keepdims=True)
+        tol = 2.0 ** -10 * 15 * P @ s + (4 * eS + 2.0 ** -16) * (P @ (15 * s + m)) + \
+            2.0 ** -8 * np.abs(Or[i])
+        err = np.abs(o[i] - Or[i])
+        assert (err <= tol).all(), (i, (err / tol).max())
+    assert np.abs(lse.cpu().numpy() - lr).max() <= 2 * eS + 2.0 ** -20 + 2.0 ** -22 * np.abs(lr).max()
+    device_error_clear()
