@@ -522,7 +522,8 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  *   page_size).
  *   causal != 0: query i of n sees keys j <= i + seqlens[b] - n (bottom-right,
  *   as in fa_attention_fwd_splitkv); otherwise all seqlens[b] keys.  A query
- *   that sees no key gets O = 0 and lse = -inf.  What the cache holds behind a
+ *   that sees no key gets O = 0 and lse = -inf.  Scores are fp32: one of magnitude
+ *   s is off by some 2^-24 s, which P feels.  What the cache holds behind a
  *   sequence's end, or at keys that a query does not see, does not reach its
  *   result, NaN or not.
  *   workspace: DEVICE scratch owned by the caller, 256-byte aligned, at least

@@ -57,7 +57,9 @@ constexpr int kWarps = 4;            // of a crew
 constexpr int kThreads = kWarps * 32;
 constexpr int kPair = 2 * kv4::kCellTokens;         // tokens that a warp copies and takes at once
 constexpr int kBlock = kWarps * kPair;              // tokens of a block: two cells each warp
-constexpr float kNoRef = -1e30f;   // reference of a row that has seen no key: exp2(-inf - kNoRef) = 0
+// Reference of a row that has seen no key: exp2(-inf - kNoRef) = 0, and a score above it
+// by 2^7 or more makes a P that moves it.
+constexpr float kNoRef = -0x1p126f;
 // A row's reference stands kRefAbove above its largest S and may lag until a P exceeds
 // kMostP, so that the fp32 sums of P and P m stay finite for values up to 2^110.  P s
 // goes to fp16 after a power of two of the row and group (`up`) that brings the largest

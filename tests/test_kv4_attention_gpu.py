@@ -864,3 +864,36 @@ def test_groups_of_far_apart_scales(H, Nq, d, group, k):
         assert (err <= tol).all(), (i, (err / tol).max())
     assert np.abs(lse.cpu().numpy() - lr).max() <= 2 * eS + 2.0 ** -20 + 2.0 ** -22 * np.abs(lr).max()
     device_error_clear()
+
+
+@pytest.mark.parametrize("H,n", [(4, 1), (8, 800)], ids=["few", "many"])
+def test_scores_of_huge_magnitude_below_zero(H, n):
+    """Scores near -2^114 and -2^115 for every key: the first half of them counts alike."""
+    d, L = 128, 1300
+    rng = np.random.default_rng(450)
+    pool = Pool([L], 4, d, 64, 16, seed=451)
+    k, v = np.full((L, 4, d), -2.0 ** 55), bf16_rows(rng, L, 4, d)
+    k[L // 2:] *= 2
+    q = np.full((n, H, d), 2.0 ** 55)
+    pool.fill([k], [v])
+    assert takes_many(pool, [q], pool.table.shape[1] * 16) == (n > 1)
+    O, lse = run(pool, [q], False, True, scale=0.1)
+    V = pool.rows(0)[1]
+    want = np.repeat(V[:L // 2].mean(0), H // 4, 0)
+    o, l = O.double().cpu().numpy(), lse.double().cpu().numpy()
+    if n == 1:
+        # the weights are equal: the head's bounds with eS = 0
+        tol = 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * np.abs(V).max()
+        assert (np.abs(o - want) <= tol).all()
+    else:
+        # With many rows the reference is the largest S log2e + f, f the exponent of the
+        # tile's V, rounded to 2^-24 of 2^114: f is lost, and tiles of other exponents weigh
+        # powers of two more or less (eS is of that size).  But the weights are positive, sum
+        # to 1, and are 0 for the second half, 2^114 below: each value lies within the range
+        # of the first half's, up to the roundings of V, P and O.
+        lo, hi = (np.repeat(f(V[:L // 2], 0), H // 4, 0) for f in (np.min, np.max))
+        tol = 2.0 ** -8 * np.maximum(np.abs(lo), np.abs(hi)) + 2.0 ** -10 * np.abs(V).max()
+        assert (o >= lo - tol).all() and (o <= hi + tol).all()
+    # -0.1 d 2^110, which log L / 2 does not show beside; a few roundings of the factors
+    assert (np.abs(l / (-0.1 * d * 2.0 ** 110) - 1) <= 2.0 ** -20).all()
+    device_error_clear()
