@@ -517,7 +517,8 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  *          int32 [B + 1], Nq the most queries of a sequence (an upper bound is
  *          fine).  Rows behind the last sequence are left as they were.
  *   Q: rows of H * d contiguous bf16, q_stride elements apart (a multiple of
- *   8, at least H * d).  O: contiguous bf16.
+ *   8, at least H * d), of magnitudes below 2^115 (an infinity or a NaN, or with
+ *   few query rows a larger value, makes NaN of its row).  O: contiguous bf16.
  *   seqlens: each sequence's keys, 0 .. Nk (Nk: an upper bound, <= max_pages *
  *   page_size).
  *   causal != 0: query i of n sees keys j <= i + seqlens[b] - n (bottom-right,

@@ -410,8 +410,9 @@ __device__ __forceinline__ void place_queries(const Kv4AttnArgs &a, const Item &
     }
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-    // a power of two that brings the row's largest value into [2^12, 2^13)
-    const int ex = big > 0.f ? max(-100, min(100, 139 - int(__float_as_uint(big) >> 23))) : 0;
+    // a power of two that brings the row's largest value into [2^12, 2^13) (below 2^16 up
+    // to 2^116, so that the factor of the scores stays finite; none too small is left out)
+    const int ex = big > 0.f ? max(-100, min(127, 139 - int(__float_as_uint(big) >> 23))) : 0;
     const float up = __uint_as_float(uint32_t(127 + ex) << 23);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {

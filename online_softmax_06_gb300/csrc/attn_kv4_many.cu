@@ -58,11 +58,13 @@ __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x 
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
-// e with 2^-e x in [2^13, 2^14).  -84 at least: a sum of 2^31 P = P^ 2^-e <= 2^92
-// stays finite.
-__device__ __forceinline__ int exponent_of(float x)
+// e with 2^-e x in [2^13, 2^14), `least` at least.  For V -84: a sum of 2^31 P = P^ 2^-e
+// <= 2^92 stays finite.  For Q and K -110: their factors stay normal numbers, and any
+// bf16 number is 2^-16 at least.
+constexpr int kLeastOfV = -84, kLeastOfQK = -110;
+__device__ __forceinline__ int exponent_of(float x, int least)
 {
-    return x > 0.f ? max(-84, min(114, int(__float_as_uint(x) >> 23) - 140)) : -84;
+    return x > 0.f ? max(least, min(114, int(__float_as_uint(x) >> 23) - 140)) : least;
 }
 
 // Sequence b's first query row, queries and keys; false (with the error recorded
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(kExpandThreads, 4)
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-            const int e2 = big > 0.f ? exponent_of(big) : 0;
+            const int e2 = big > 0.f ? exponent_of(big, kLeastOfQK) : 0;
             const float up = a.scale < 0.f ? -pow2(-e2) : pow2(-e2);   // q_mul is positive
             const int64_t row = ((head / grp) * a.total_q + tok) * grp + head % grp;
             auto *dst = reinterpret_cast<__half2 *>(w.Q + row * D + lane * kPer);
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(kExpandThreads, 4)
 #pragma unroll
         for (int i = 1; i < kExpandThreads / 32; ++i)
             top = fmaxf(top, s_big[kv][i]);
-        const int e = exponent_of(top);
+        const int e = exponent_of(top, kv ? kLeastOfV : kLeastOfQK);
         if (tid == 0) {
             float2 &f = w.tile[bh * w.n_tiles + blockIdx.x];
             if (kv)

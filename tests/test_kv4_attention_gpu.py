@@ -897,3 +897,20 @@ def test_scores_of_huge_magnitude_below_zero(H, n):
     # -0.1 d 2^110, which log L / 2 does not show beside; a few roundings of the factors
     assert (np.abs(l / (-0.1 * d * 2.0 ** 110) - 1) <= 2.0 ** -20).all()
     device_error_clear()
+
+
+@pytest.mark.parametrize("H,n", [(4, 1), (16, 1), (8, 800)], ids=["few", "16 rows", "many"])
+@pytest.mark.parametrize("e", [-122, -105, 105])
+def test_queries_and_keys_of_opposite_magnitudes(H, n, e):
+    """Q times 2^e and K times 2^-e give the scores of Q and K: nothing of a row is lost
+    to fp16's range, however small or large its values are."""
+    d, L = 128, 1300
+    rng = np.random.default_rng(460 + e)
+    pool = Pool([L], 4, d, 64, 16, seed=461)
+    pool.fill([bf16_rows(rng, L, 4, d) * 2.0 ** -e], [bf16_rows(rng, L, 4, d)])
+    q = bf16_rows(rng, n, H, d) * 2.0 ** e
+    q = np.where(np.abs(q) < 2.0 ** -126, 0, q)            # bf16's normal numbers
+    assert takes_many(pool, [q], pool.table.shape[1] * 16) == (n > 1)
+    O, lse = run(pool, [q], True, True, scale=0.1)
+    check(pool, [q], O, lse, 0.1, True, many=n > 1)
+    device_error_clear()
