@@ -18,9 +18,10 @@
 // S log2e + f, P^ = 2^(S log2e + f - m) <= 2^8 goes into P V^ as fp16 and
 // P = P^ 2^-f into the sum.
 //
-// A P of 0 does not keep a NaN of V from the sums: where a token's V parameters are
-// not finite, its V is written as 0 and its K as NaN, which the mask takes away for
-// the rows that do not see it and which makes NaN of those that do.
+// A P of 0 does not keep a NaN of V from the sums: a group of a token whose V is not
+// finite is written as 0, and each tile says which of its tokens is the first such one
+// of each group.  A row sees a prefix of the keys, so that the epilogue knows from these
+// whether the group's columns are NaN.
 //
 // The rows of a kv head are (query, head of the group) pairs, query by query, so
 // that the heads of a group share K and V tiles; a row's mask goes by its query.
@@ -29,6 +30,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -53,6 +55,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleLog2 = 8.f;  // the reference lags by up to 2^8
 constexpr uint32_t kChunkBytes = BM * 128;
 constexpr int kExpandThreads = 256;
+constexpr int kNoNan = 255;          // of a tile's group
 
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
@@ -159,9 +162,9 @@ __global__ void __launch_bounds__(kExpandThreads, 4)
     const int n = min(BN, seq.L - tok0);
     __shared__ const uint8_t *s_cell[BN / kv4::kCellTokens];
     __shared__ float s_big[2][kExpandThreads / 32];
-    __shared__ uint8_t s_nan[BN];      // tokens whose V is not finite
-    if (tid < BN)
-        s_nan[tid] = 0;
+    __shared__ int s_nan[4];           // a group's first token whose V is not finite
+    if (tid < 4)
+        s_nan[tid] = kNoNan;
     if (tid < BN / kv4::kCellTokens) {
         const int tok = tok0 + tid * kv4::kCellTokens;
         const uint8_t *cell = nullptr;
@@ -223,10 +226,15 @@ __global__ void __launch_bounds__(kExpandThreads, 4)
             for (int i = 0; i < kPairs; ++i) {
                 const uint32_t p = pair[kv][x][i];
                 const float m = bf16_hi(p), top = fmaf(15.f, bf16_lo(p), m);
-                if (fabsf(m) < INFINITY && fabsf(top) < INFINITY)
-                    big[kv] = ptx::max3(big[kv], fabsf(m), fabsf(top));
-                else if (kv)
-                    s_nan[tid / kLanes + x * (kExpandThreads / kLanes)] = 1;
+                if (fabsf(m) < INFINITY && bf16_lo(p) < INFINITY) {
+                    // (the last of a group near the end of fp32's range may lie beyond it)
+                    big[kv] = ptx::max3(big[kv], fabsf(m), fminf(fabsf(top), 3.4e38f));
+                } else if (kv) {
+                    const int jj = tid % kLanes / 4;
+                    atomicMin(&s_nan[G == 32 ? 2 * jj + i : G == 64 ? jj : 0],
+                              tid / kLanes + x * (kExpandThreads / kLanes));
+                    pair[kv][x][i] = 0;
+                }
             }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -249,6 +257,8 @@ __global__ void __launch_bounds__(kExpandThreads, 4)
                 f.y = float(e);
             else
                 f.x = pow2(e);
+            w.first_nan[bh * w.n_tiles + blockIdx.x] =
+                uint32_t(s_nan[0] | s_nan[1] << 8 | s_nan[2] << 16) | uint32_t(s_nan[3]) << 24;
         }
         const float up = pow2(-e);
 #pragma unroll
@@ -263,10 +273,6 @@ __global__ void __launch_bounds__(kExpandThreads, 4)
                                                     : __byte_perm(other, z, 0x7632);
                 const uint32_t p = pair[kv][x][kPairs == 2 ? i : 0];
                 y[i] = values_of(u, __float2half2_rn(bf16_lo(p) * up), __float2half2_rn(bf16_hi(p) * up));
-            }
-            if (s_nan[t]) {
-                const uint32_t fill = kv ? 0u : 0x7e007e00u;
-                y[0] = y[1] = make_uint4(fill, fill, fill, fill);
             }
             __half *dst = (kv ? w.V : w.K) + (bh * w.n_tiles * BN + tok0 + t) * D +
                           (8 * (l / 4) + l % 4) * 8;
@@ -716,6 +722,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = m_new;
         }
 
+        // Each group's first key whose V is not finite, relative to the range's first key:
+        // the columns of a row that sees it are NaN.
+        int first_nan[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX};
+        for (int j = lane; j < n_t; j += 32) {
+            const uint32_t z = p.w.first_nan[tile0 + j];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if ((z >> (8 * y) & 255u) != kNoNan)
+                    first_nan[y] = min(first_nan[y], j * BN + int(z >> (8 * y) & 255u));
+        }
+        float keep[D / 32];                // of 32 columns: 1 or NaN
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            first_nan[y] = __reduce_min_sync(0xffffffffu, first_nan[y]);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            const int y = c * 32 / a.group;
+            const int at = y == 0 ? first_nan[0] : y == 1 ? first_nan[1]
+                           : y == 2 ? first_nan[2] : first_nan[3];
+            keep[c] = at <= last ? NAN : 1.f;
+        }
+
         // ---- epilogue: O = O~ / l (bf16), lse = (m + log2 l) ln 2 --------------------
         const int64_t part = int64_t(split) * a.total_q * a.H +
                              (int64_t(h) * a.total_q + seq.q0) * grp + x;
@@ -732,9 +760,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (!aborted && ptx::mbar_wait_warp(&o_full[t], 0, abort_flag, a.err_word)) {
             ptx::tc_fence_after_sync();
             const bool any = l > 0.f || l != l;
-            const float inv = any ? 1.f / l : 0.f;
+            const float all_inv = any ? 1.f / l : 0.f;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
+                const float inv = all_inv * keep[c];
                 uint32_t o[32];
                 ptx::tmem_ld32(tO + c * 32, o);
                 ptx::tmem_wait_ld();
@@ -744,10 +773,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float4 *dst = reinterpret_cast<float4 *>(p.w.O_part + part * D + c * 32);
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        dst[q] = make_float4(__uint_as_float(o[4 * q + 0]),
-                                             __uint_as_float(o[4 * q + 1]),
-                                             __uint_as_float(o[4 * q + 2]),
-                                             __uint_as_float(o[4 * q + 3]));
+                        dst[q] = make_float4(__uint_as_float(o[4 * q + 0]) * keep[c],
+                                             __uint_as_float(o[4 * q + 1]) * keep[c],
+                                             __uint_as_float(o[4 * q + 2]) * keep[c],
+                                             __uint_as_float(o[4 * q + 3]) * keep[c]);
                     continue;
                 }
                 uint4 *dst = reinterpret_cast<uint4 *>(out_row(x) + c * 32);
@@ -859,6 +888,7 @@ int launch(const Kv4AttnArgs &a, cudaStream_t stream)
     p.w.V = reinterpret_cast<__half *>(ws + at.v);
     p.w.q_mul = reinterpret_cast<float *>(ws + at.q_mul);
     p.w.tile = reinterpret_cast<float2 *>(ws + at.tile);
+    p.w.first_nan = reinterpret_cast<uint32_t *>(ws + at.first_nan);
     p.w.O_part = reinterpret_cast<float *>(ws + at.O_part);
     p.w.ml = reinterpret_cast<float2 *>(ws + at.ml);
     p.w.n_tiles = at.n_tiles;

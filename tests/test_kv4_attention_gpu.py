@@ -914,3 +914,25 @@ def test_queries_and_keys_of_opposite_magnitudes(H, n, e):
     O, lse = run(pool, [q], True, True, scale=0.1)
     check(pool, [q], O, lse, 0.1, True, many=n > 1)
     device_error_clear()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("lens,nq", [([900, 700], 3), ([900, 300], 500), ([5000], 1100)],
+                         ids=["few", "many", "many, ranges"])
+def test_nan_values_reach_their_columns(lens, nq, group):
+    """A NaN in V reaches the columns of its group in the rows that see it, and nothing
+    else, with few query rows and with many."""
+    H, Hkv, d, page = 16, 8, 128, 32
+    pool, q = make(lens, nq, H, Hkv, d, group, page, seed=470)
+    assert takes_many(pool, q, pool.table.shape[1] * page) == (nq > 3)
+    rng = np.random.default_rng(471)
+    L = lens[0]
+    for pos, h, i in ((L - nq // 2 - 1, 0, 5), (L - 2, 0, 100), (L - nq - 1, 2, 64), (L - 1, 3, 127),
+                      (100, 4, 40)):
+        k, v = bf16_rows(rng, 1, Hkv, d), bf16_rows(rng, 1, Hkv, d)
+        v[0, h, i] = np.inf if i == 40 else np.nan
+        kv4.write(pool.bytes, pool.table[0], np.array([pos]), k, v, page, group)
+    O, lse = run(pool, q, True, True)
+    assert not torch.isnan(lse).any()
+    check(pool, q, O, lse, 1 / math.sqrt(d), True, many=nq > 3)
+    device_error_clear()
