@@ -538,7 +538,8 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  * Many (about 100 and more on average, enough to fill the GPU; chunks of
  * prompts): the values are first written out as fp16 (2^-11 relative, with a
  * power of two a tile of 128 tokens of a head: values below 2^-28 of the tile's
- * largest have fewer bits).
+ * largest have fewer bits), and so have probabilities below 2^-21 of the largest
+ * that a row has, each times its tile's largest value.
  * A group of a token that holds NaN makes NaN of the rows that see it, for V in
  * the group's columns alone.
  * B <= 1024.  Results do not depend on timing: the same call gives the same

@@ -15,7 +15,7 @@
 // value of its tile (128 tokens of a head) into [2^13, 2^14).  Q is scaled per row
 // likewise (8 bits: exact down to 2^-28 of the row's largest).  The tile's factors act
 // on the scores and, for V, on P: with V = V^ 2^f and the reference m of
-// S log2e + f, P^ = 2^(S log2e + f - m) <= 2^8 goes into P V^ as fp16 and
+// S log2e + f, P^ = 2^(S log2e + f - m) <= 2^8 goes into P V^ as fp16 (times 2^7) and
 // P = P^ 2^-f into the sum.
 //
 // A P of 0 does not keep a NaN of V from the sums: a group of a token whose V is not
@@ -53,6 +53,9 @@ constexpr uint32_t kColPinS = 64;    // P_t starts 64 columns into S_t
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleLog2 = 8.f;  // the reference lags by up to 2^8
+// P^ goes to fp16 times 2^7, up to 2^15: a key keeps all bits down to 2^-21 of the row's
+// largest P 2^f, where tiles with values far larger than its own would take them.
+constexpr float kUp = 7.f, kDown = 0x1p-7f;
 constexpr uint32_t kChunkBytes = BM * 128;
 constexpr int kExpandThreads = 256;
 constexpr int kNoNan = 255;          // of a tile's group
@@ -686,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float m_use = m_new == -INFINITY ? 0.f : m_new;
             const float corr = grew ? ptx::ex2(m - m_use) : 1.f;   // 0 on the first tile
             const uint32_t tP = tS + kColPinS;
-            const float2 sl2 = make_float2(slj, slj), nm2 = make_float2(f - m_use, f - m_use);
+            const float2 sl2 = make_float2(slj, slj), nm2 = make_float2(f - m_use + kUp, f - m_use + kUp);
             float2 rowsum2 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -718,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tmem_wait_st();
             ptx::tc_fence_before_sync();
             ptx::mbar_arrive(&p_full[t]);
-            l = l * corr + (rowsum2.x + rowsum2.y) * ptx::ex2(-factor.y);
+            l = l * corr + (rowsum2.x + rowsum2.y) * ptx::ex2(-factor.y - kUp);
             m = m_new;
         }
 
@@ -760,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (!aborted && ptx::mbar_wait_warp(&o_full[t], 0, abort_flag, a.err_word)) {
             ptx::tc_fence_after_sync();
             const bool any = l > 0.f || l != l;
-            const float all_inv = any ? 1.f / l : 0.f;
+            const float all_inv = any ? kDown / l : 0.f;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 const float inv = all_inv * keep[c];
@@ -862,7 +865,7 @@ __global__ void __launch_bounds__(kExpandThreads) kv4_many_join_kernel(const Man
             }
         }
         const bool any = l > 0.f || l != l;
-        const float inv = any ? 1.f / l : 0.f;
+        const float inv = any ? kDown / l : 0.f;
         const int i = x / grp, head = h * grp + x % grp;
         auto *dst = static_cast<__nv_bfloat16 *>(a.O) + (int64_t(seq.q0 + i) * a.H + head) * D +
                     lane * kPer;

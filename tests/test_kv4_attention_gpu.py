@@ -936,3 +936,40 @@ def test_nan_values_reach_their_columns(lens, nq, group):
     assert not torch.isnan(lse).any()
     check(pool, q, O, lse, 1 / math.sqrt(d), True, many=nq > 3)
     device_error_clear()
+
+
+@pytest.mark.parametrize("k", [10, 24, 28])
+def test_many_rows_beside_one_huge_value(k):
+    """One value of V 2^k times the others, in a tile of its own: the other tiles' keys
+    still count in the other columns.
+
+    With T_j the largest value of key j's tile, P V^ takes P T relative to the row's
+    largest, as fp16: 2^-11 of each P, or a step of 2^-25 beside at least 2^7, so
+    2^-32 max_i (P_i T_i) |V_j| / T_j; T is known to a factor of 2 (a power of two).  V
+    is rounded likewise: 2^-11 of itself, or 2^-25 beside 2^13: 2^-38 T_j P_j.
+    """
+    d, L, n, H = 128, 1300, 900, 8
+    rng = np.random.default_rng(480)
+    pool = Pool([L], H, d, 64, 16, seed=481)
+    v = bf16_rows(rng, L, H, d)
+    v[700, :, 3] = 2.0 ** k
+    pool.fill([bf16_rows(rng, L, H, d)], [v])
+    q = bf16_rows(rng, n, H, d)
+    assert takes_many(pool, [q], pool.table.shape[1] * 16)
+    O, lse = run(pool, [q], False, True, scale=0.1)
+    K, V = pool.rows(0)
+    Or, lr = kv4.attention(q, K, V, 0.1, False)
+    o = O.double().cpu().numpy()
+    for h in range(H):
+        S = 0.1 * q[:, h] @ K[:, h].T
+        P = np.exp(S - S.max(1, keepdims=True))
+        P /= P.sum(1, keepdims=True)
+        eS = 0.1 * (np.abs(q[:, h]) @ np.abs(K[:, h]).T).max() * (2.0 ** -11 + 2.0 ** -15)
+        A = np.abs(V[:, h])
+        T = np.repeat([A[j:j + 128].max() for j in range(0, L, 128)], 128)[:L]
+        step = 2 * (P * T).max(1)[:, None] * 2.0 ** -32 * (A / T[:, None]).sum(0) + \
+            2.0 ** -37 * (P @ T)[:, None]
+        tol = (2.0 ** -10 + 4 * eS) * (P @ A) + step + 2.0 ** -8 * np.abs(Or[:, h])
+        err = np.abs(o[:, h] - Or[:, h])
+        assert (err <= tol).all(), (h, (err / tol).max())
+    device_error_clear()
