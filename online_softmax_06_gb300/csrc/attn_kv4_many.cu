@@ -255,13 +255,11 @@ __global__ void __launch_bounds__(kExpandThreads, 4)
             top = fmaxf(top, s_big[kv][i]);
         const int e = exponent_of(top, kv ? kLeastOfV : kLeastOfQK);
         if (tid == 0) {
-            float2 &f = w.tile[bh * w.n_tiles + blockIdx.x];
+            uint2 &f = w.tile[bh * w.n_tiles + blockIdx.x];
             if (kv)
-                f.y = float(e);
+                f.y = __float_as_uint(float(e)) | uint32_t(s_nan[2] | s_nan[3] << 8);
             else
-                f.x = pow2(e);
-            w.first_nan[bh * w.n_tiles + blockIdx.x] =
-                uint32_t(s_nan[0] | s_nan[1] << 8 | s_nan[2] << 16) | uint32_t(s_nan[3]) << 24;
+                f.x = __float_as_uint(pow2(e)) | uint32_t(s_nan[0] | s_nan[1] << 8);
         }
         const float up = pow2(-e);
 #pragma unroll
@@ -630,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         for (int j = 0; j < n_t; ++j) {
             // (a factor of 0 would make NaN of the mask's -inf, one of inf of a score of 0)
-            const float2 factor = p.w.tile[tile0 + j];
+            const uint2 both = p.w.tile[tile0 + j];
+            const float2 factor = make_float2(bf16_hi(both.x), bf16_hi(both.y));
             const float slj = fminf(fmaxf(sl * factor.x, 1.2e-38f), 3e38f);
             float f = factor.y;
             // |raw scores| are below 2^28 d: scores beyond 2^18 are possible
@@ -729,7 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the columns of a row that sees it are NaN.
         int first_nan[4] = {INT_MAX, INT_MAX, INT_MAX, INT_MAX};
         for (int j = lane; j < n_t; j += 32) {
-            const uint32_t z = p.w.first_nan[tile0 + j];
+            const uint2 both = p.w.tile[tile0 + j];
+            const uint32_t z = __byte_perm(both.x, both.y, 0x5410);
 #pragma unroll
             for (int y = 0; y < 4; ++y)
                 if ((z >> (8 * y) & 255u) != kNoNan)
@@ -890,8 +890,7 @@ int launch(const Kv4AttnArgs &a, cudaStream_t stream)
     p.w.K = reinterpret_cast<__half *>(ws + at.k);
     p.w.V = reinterpret_cast<__half *>(ws + at.v);
     p.w.q_mul = reinterpret_cast<float *>(ws + at.q_mul);
-    p.w.tile = reinterpret_cast<float2 *>(ws + at.tile);
-    p.w.first_nan = reinterpret_cast<uint32_t *>(ws + at.first_nan);
+    p.w.tile = reinterpret_cast<uint2 *>(ws + at.tile);
     p.w.O_part = reinterpret_cast<float *>(ws + at.O_part);
     p.w.ml = reinterpret_cast<float2 *>(ws + at.ml);
     p.w.n_tiles = at.n_tiles;

@@ -252,15 +252,16 @@ __host__ __device__ constexpr int kv4_attention_ranges(int rows, int d)
 struct Kv4ManyBuffers {
     __half *Q, *K, *V;
     float *q_mul;                  // a row of Q's factor
-    float2 *tile;                  // a tile's: K's, and the exponent of V's
-    uint32_t *first_nan;           // its first tokens with a V that is not finite, a byte a group
+    // a tile's: K's, and the exponent of V's, floats whose lower halves are 0 and hold each
+    // group's first token with a V that is not finite, a byte each
+    uint2 *tile;
     float *O_part;                 // with splits > 1: [splits, rows of Q, d], unnormalised
     float2 *ml;                    // and [splits, rows of Q]: (reference, sum)
     int n_tiles;                   // tiles of 128 keys of the longest sequence
     int splits, chunk;             // ranges of `chunk` tiles that its keys are cut into
 };
 struct Kv4ManyLayout {
-    int64_t q, k, v, q_mul, tile, first_nan, O_part, ml, bytes;
+    int64_t q, k, v, q_mul, tile, O_part, ml, bytes;
     int n_tiles, splits, chunk;
 };
 // CTAs of 256 rows of a kv head, as far as the host can tell.
@@ -289,8 +290,7 @@ inline Kv4ManyLayout kv4_many_layout(int B, int64_t total_q, int Nk, int H, int 
     L.v = L.k + up(tiles * 128 * d * 2);
     L.q_mul = L.v + up(tiles * 128 * d * 2);
     L.tile = L.q_mul + up(total_q * H * 4);
-    L.first_nan = L.tile + up(tiles * 8);
-    L.O_part = L.first_nan + up(tiles * 4);
+    L.O_part = L.tile + up(tiles * 8);
     L.ml = L.O_part + (L.splits > 1 ? up(L.splits * total_q * H * d * 4) : 0);
     L.bytes = L.ml + (L.splits > 1 ? up(L.splits * total_q * H * 8) : 0);
     return L;
