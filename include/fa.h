@@ -464,9 +464,11 @@ FA_API int fa_attention_fwd_splitkv_noalloc(const void *Q, const void *K, const 
  *
  * Errors raised by the device (fa_get_device_error): FA_DEVERR_BAD_SEQLENS for
  * a sequence whose counts are negative, above N or Nk, or do not fit (seqlens
- * below the new tokens, or above max_pages * page_size), FA_DEVERR_BAD_PAGE for
- * a page outside [0, num_pages).  Such a sequence, or such a page's tokens, is
- * left out: nothing is read or written out of bounds.
+ * below the new tokens, or above max_pages * page_size; rows outside the tensor),
+ * FA_DEVERR_BAD_PAGE for a page outside [0, num_pages).  Such a sequence, or such a
+ * page's tokens, is left out: nothing is read or written out of bounds.  Where
+ * cu_seqlens decreases, sequences that claim the same rows are undefined among one
+ * another.
  */
 
 /* Bytes of one head's page, or a negative FA_ERR_* code. */

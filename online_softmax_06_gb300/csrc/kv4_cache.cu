@@ -37,6 +37,27 @@ struct RowAt {
     int t;          // token within the cell
 };
 
+// Whether a sequence of n new rows from row c0 on, with L tokens in the end, is allowed.
+__device__ __forceinline__ bool counts_fit(const Kv4CacheArgs &a, int64_t c0, int64_t n, int64_t L)
+{
+    return c0 >= 0 && n >= 0 && n <= a.N && c0 + n <= a.total && L >= n &&
+           L <= int64_t(a.max_pages) * a.page_size;
+}
+
+// Records what no row shows: packed sequences without a row, or with rows that another
+// one claims.  The first block looks, its last warps first: the first ones look for their
+// rows meanwhile.
+__device__ __forceinline__ void check_counts(const Kv4CacheArgs &a)
+{
+    if (a.cu_seqlens == nullptr || blockIdx.x != 0 || blockIdx.y != 0)
+        return;
+    for (int b = kThreads - 1 - int(threadIdx.x); b < a.B; b += kThreads) {
+        const int64_t c0 = a.cu_seqlens[b];
+        if (!counts_fit(a, c0, a.cu_seqlens[b + 1] - c0, a.seqlens[b]))
+            record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
+    }
+}
+
 // The place of packed row r: its sequence, its position (the rows of sequence
 // b are its last n_b tokens), its page.
 __device__ RowAt locate(const Kv4CacheArgs &a, int64_t r, int cell)
@@ -63,13 +84,9 @@ __device__ RowAt locate(const Kv4CacheArgs &a, int64_t r, int cell)
             return at;          // behind the last sequence
         i = r - c0;
         n = c1 - c0;
-        if (n > a.N) {
-            record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
-            return at;
-        }
     }
     const int64_t L = a.seqlens[b];
-    if (L < n || L > int64_t(a.max_pages) * a.page_size) {
+    if (!counts_fit(a, r - i, n, L)) {
         record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
         return at;
     }
@@ -193,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     extern __shared__ RowAt at[];
+    check_counts(a);
     const int64_t row0 = int64_t(blockIdx.x) * rows_per_block;
     const int rows = int(min(int64_t(rows_per_block), a.total - row0));
     for (int i = threadIdx.x; i < rows; i += kThreads)
@@ -280,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     extern __shared__ RowAt at[];
+    check_counts(a);
     const int64_t row0 = int64_t(blockIdx.x) * rows_per_block;
     const int rows = int(min(int64_t(rows_per_block), a.total - row0));
     for (int i = threadIdx.x; i < rows; i += kThreads)

@@ -214,3 +214,35 @@ def test_on_a_stream_and_in_a_graph():
     assert np.array_equal(read_back(ko)[0], want)
     assert not torch.equal(ko, first)
     device_error_clear()
+
+
+@pytest.mark.parametrize("cu,lens,good", [
+    ([0, 2, 4, 9], [20, 20, 20], [0, 1]),        # the last run leaves the rows
+    ([-2, 2, 4, 6], [20, 20, 20], [1, 2]),       # the first begins before them
+    ([0, 2, 1, 1], [20, 20, 20], [0]),           # a run of fewer than no rows
+    ([0, 3, 3, 6], [20, -1, 20], [0, 2]),        # no new rows, but no length
+    ([0, 3, 3, 6], [20, 33, 20], [0, 2]),        # nor one that the table holds
+])
+def test_bad_packed_counts_are_told_and_left_out(cu, lens, good):
+    d, group, Hkv, page = 128, 64, 3, 16
+    rng = np.random.default_rng(21)
+    pool = Pool([20, 20, 20], Hkv, d, group, page, seed=22, extra_cols=0)
+    cache = torch.from_numpy(pool.bytes.copy()).cuda()
+    x = bf16_rows(rng, 6, Hkv, d)
+    table, sl, cut = gpu_i32(pool.table), gpu_i32(lens), gpu_i32(cu)
+    kt = gpu_bf16(x)
+    for b in good:
+        n = cu[b + 1] - cu[b]
+        kv4.write(pool.bytes, pool.table[b], np.arange(20 - n, 20), x[cu[b]:cu[b + 1]],
+                  x[cu[b]:cu[b + 1]], page, group)
+    fa.kv4_append(kt, kt, cache, table, sl, cu_seqlens=cut, max_new=6, group=group)
+    assert fa.fa_get_device_error() == fa.FA_DEVERR_BAD_SEQLENS
+    assert same_cache(cache.cpu().numpy(), pool.bytes, d, group)
+    out = torch.full_like(kt, 5.0)
+    fa.kv4_read(cache, table, sl, d=d, cu_seqlens=cut, max_new=6, group=group, k=out, v=out.clone())
+    assert fa.fa_get_device_error() == fa.FA_DEVERR_BAD_SEQLENS
+    rows = np.zeros(6, bool)
+    for b in good:
+        rows[cu[b]:cu[b + 1]] = True
+    want = np.where(rows[:, None, None], kv4.bf16(kv4.values(*kv4.quantise(x, group))), 5.0)
+    assert np.array_equal(read_back(out), want)
