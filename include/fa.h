@@ -467,8 +467,8 @@ FA_API int fa_attention_fwd_splitkv_noalloc(const void *Q, const void *K, const 
  * below the new tokens, or above max_pages * page_size; rows outside the tensor),
  * FA_DEVERR_BAD_PAGE for a page outside [0, num_pages).  Such a sequence, or such a
  * page's tokens, is left out: nothing is read or written out of bounds.  Where
- * cu_seqlens decreases, sequences that claim the same rows are undefined among one
- * another.
+ * cu_seqlens decreases, other sequences may be left out too, and those that claim
+ * the same rows are undefined among one another.
  */
 
 /* Bytes of one head's page, or a negative FA_ERR_* code. */
@@ -517,7 +517,8 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  *          total_q = B * Nq.
  *   packed: Q rows and O [total_q, H, d], lse [H, total_q]; cu_seqlens_q DEVICE
  *          int32 [B + 1], Nq the most queries of a sequence (an upper bound is
- *          fine).  Rows behind the last sequence are left as they were.
+ *          fine, but the work is laid out by it: a close one runs faster).  Rows
+ *          behind the last sequence are left as they were.
  *   Q: rows of H * d contiguous bf16, q_stride elements apart (a multiple of
  *   8, at least H * d), of magnitudes below 2^115 (an infinity or a NaN, or with
  *   few query rows a larger value, makes NaN of its row).  O: contiguous bf16.

@@ -537,6 +537,7 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
     const int per = (a.B + kAll - 1) / kAll;
     uint32_t *s_cost = reinterpret_cast<uint32_t *>(smem_cta + Smem::cost);
     uint32_t mine = 0, mine_cost = 0;
+    bool falls = false;                    // cu_seqlens_q does, somewhere
     for (int i = 0; i < per; ++i) {
         const int b = threadIdx.x * per + i;
         if (b >= a.B)
@@ -544,6 +545,7 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
         const int2 q = queries_of(a, b);
         const int L = a.seqlens[b];
         uint32_t items = 0;
+        falls = falls || q.y < 0;
         if (q.y < 0 || q.y > a.Nq || q.x < 0 || int64_t(q.x) + q.y > a.total_q || L < 0 ||
             L > a.Nk)
             record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
@@ -567,7 +569,9 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
     uint2 *s_w = reinterpret_cast<uint2 *>(smem_cta + Smem::scan);
     if (lane == 31)
         s_w[crew * kWarps + warp] = make_uint2(incl, incl_cost);
-    __syncthreads();
+    // Where cu_seqlens_q falls, sequences may claim more rows together than there are, and
+    // their blocks more than 32 bits: nothing is computed.
+    falls = __syncthreads_or(falls);
     uint32_t base = incl - mine, base_cost = incl_cost - mine_cost;
     for (int w = 0; w < crew * kWarps + warp; ++w) {
         base += s_w[w].x;
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
     if (threadIdx.x == 0)
         s_pre[0] = s_cost[0] = 0;
     __syncthreads();
-    const uint32_t T = uint32_t(uniform(int(s_pre[a.B])));
+    const uint32_t T = falls ? 0u : uint32_t(uniform(int(s_pre[a.B])));
     const uint32_t n_ranges = min(T, uint32_t(kv4_attention_ranges(R, D)));
     const Parts parts = parts_of<D, R>(a.workspace);
     uint32_t begin = T, end = T;

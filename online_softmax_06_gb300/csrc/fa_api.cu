@@ -898,14 +898,16 @@ int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num
         !fa::aligned(lse, 4) || !fa::aligned(page_table, 4) || !fa::aligned(seqlens, 4) ||
         !fa::aligned(cu_seqlens_q, 4) || !fa::aligned(workspace, 256) || q_stride % 8 != 0)
         return FA_ERR_MISALIGNED;
-    // the blocks of 128 keys of all (sequence, kv head, row tile) items are
-    // counted in 32 bits
-    const int rows = fa::kv4_attention_rows(Nq, H, Hkv);
-    const int64_t tiles = (int64_t(Nq) * (H / Hkv) + rows - 1) / rows;
-    const int64_t blocks = Nk / 128 + 4;   // one begun, three for the item itself
-    if (B > fa::kKv4MaxSeqs || total_q > (int64_t(1) << 31) - 512 || q_stride > (int64_t(1) << 31) ||
-        H > 65535 || int64_t(Nq) * (H / Hkv) > (int64_t(1) << 31) - 512 ||
-        double(tiles) * double(blocks) * B * Hkv > double((int64_t(1) << 31) - 512))
+    const int64_t limit = (int64_t(1) << 31) - 512, most = Nq < total_q ? Nq : total_q;
+    if (B > fa::kKv4MaxSeqs || total_q > limit || q_stride > (int64_t(1) << 31) || H > 65535 ||
+        most * (H / Hkv) > limit)
+        return FA_ERR_TOO_LARGE;
+    const bool many = fa::kv4_many(B, total_q, Nk, H, Hkv, d);
+    // With few rows the blocks of 128 keys of all (sequence, kv head, row tile) items are
+    // counted in 32 bits, as are their costs; each sequence begins a tile.
+    const double tiles = double(total_q) * (H / Hkv) / fa::kv4_attention_rows(Nq, H, Hkv) + B;
+    const double blocks = Nk / 128 + 4;    // one begun, three for the item itself
+    if (!many && tiles * blocks * Hkv > double(limit))
         return FA_ERR_TOO_LARGE;
     fa::DeviceInfo *dev = fa::current_device();
     if (dev == nullptr)
@@ -923,7 +925,7 @@ int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num
     a.O = O;
     a.lse = lse;
     a.B = B;
-    a.Nq = Nq;
+    a.Nq = int(most);
     a.Nk = Nk;
     a.total_q = total_q;
     a.H = H;
@@ -937,8 +939,8 @@ int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num
     a.err_word = dev->err_word;
     a.expire_wait_ns = fa::t_expire_wait_ns;
     fa::t_expire_wait_ns = 0;
-    return fa::kv4_many(B, total_q, Nk, H, Hkv, d) ? fa::launch_attention_kv4_many(a, fa::t_stream)
-                                                   : fa::launch_attention_kv4(a, fa::t_stream);
+    return many ? fa::launch_attention_kv4_many(a, fa::t_stream)
+                : fa::launch_attention_kv4(a, fa::t_stream);
 }
 
 int fa_attention_fwd_f32(const float *Q, const float *K, const float *V, float *O, float *lse,

@@ -973,3 +973,30 @@ def test_many_rows_beside_one_huge_value(k):
         err = np.abs(o[:, h] - Or[:, h])
         assert (err <= tol).all(), (h, (err / tol).max())
     device_error_clear()
+
+
+def test_one_query_each_with_loose_bounds():
+    """A packed decode step of 1024 sequences without max_q, on a table for 131072 keys."""
+    rng = np.random.default_rng(490)
+    B, H, Hkv, d, page = 1024, 64, 8, 64, 256
+    lens = [int(x) for x in rng.integers(0, 40, B)]
+    pool, q = make(lens, 1, H, Hkv, d, 64, page, seed=491, extra_cols=511)
+    x = gpu_bf16(np.concatenate(q))
+    args = (torch.from_numpy(pool.bytes).cuda(), gpu_i32(pool.table), gpu_i32(lens))
+    O, lse = fa.attention_kv4(x, *args, cu_seqlens=gpu_i32(np.arange(B + 1)), group=64)
+    check(pool, q, O, lse, 1 / 8, True)
+    device_error_clear()
+
+
+def test_decreasing_cu_seqlens_are_told():
+    """Runs that overlap because cu_seqlens falls in between: nothing is computed."""
+    pool, q = make([50, 60, 70], 2, 4, 2, 64, 64, 16, seed=495)
+    out = torch.full((6, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4, 6), 9.0, device="cuda")
+    for cu in ([0, 6, 0, 6], [0, 2, 1, 4], [4, 2, 2, 2]):
+        fa.attention_kv4(gpu_bf16(np.concatenate(q)), torch.from_numpy(pool.bytes).cuda(),
+                         gpu_i32(pool.table), gpu_i32([50, 60, 70]), cu_seqlens=gpu_i32(cu), max_q=6,
+                         out=out, lse=lse)
+        assert fa.fa_get_device_error() == fa.FA_DEVERR_BAD_SEQLENS
+        assert (out == 9).all() and (lse == 9).all()
+    device_error_clear()

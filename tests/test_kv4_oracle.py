@@ -219,3 +219,20 @@ def test_attention_refusals_without_gpu():
     assert go(B=0, total=0) == fa.FA_OK
     assert go(Nq=0, total=0) == fa.FA_OK
     assert go(H=0, Hkv=0) == fa.FA_OK
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are none: no device may take the call")
+def test_loose_bounds_of_packed_queries_are_no_refusal():
+    """A call's size goes by its rows: the queries of one sequence, however many may be
+    allowed, do not count for each sequence."""
+    def go(B, Nq, total, Nk, H, Hkv=8, d=128, cu=256):
+        return fa.fa_attention_kv4(256, H * d, 256, 4, 256, 256, 1 << 20, 256, cu, 256, 256, B, Nq,
+                                   total, Nk, H, Hkv, d, 64, 1.0, 1, 256, 1 << 40)
+    # one query each of 1024 sequences, most = all: 16-row tiles on up to 131072 keys
+    assert go(1024, 1024, 1024, 131072, 64) == fa.FA_ERR_NO_DEVICE
+    assert go(1024, 2 ** 31 - 1, 1024, 131072, 64) == fa.FA_ERR_NO_DEVICE
+    # 256 queries each of 256 sequences, in the form for many rows, which has no such count
+    assert go(256, 65536, 65536, 4096, 64) == fa.FA_ERR_NO_DEVICE
+    # what does not fit 32 bits is refused: (2^25 / 16 * 8 + 1024) * 2052 * 8 blocks
+    assert go(1024, 1 << 25, 1 << 25, 1 << 18, 64) == fa.FA_ERR_TOO_LARGE
+    assert go(1024, 1 << 16, 1 << 26, 1 << 18, 64, cu=None) == fa.FA_ERR_TOO_LARGE
