@@ -51,6 +51,11 @@
 namespace fa {
 namespace {
 
+using kv4::bf16_hi;
+using kv4::bf16_lo;
+using kv4::pow2;
+using ptx::max3;
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kWarps = 4;            // of a crew
@@ -70,8 +75,6 @@ constexpr float kNoRef = -0x1p126f;
 // 2 %: 64 x 8k keys 102.3 us, so 101.8; 256 x 1k 79.7 and 78.2; 32 x 4k 42.3 and 44.9.)
 constexpr float kRefAbove = 10.f, kMostP = 0x1p-2f, kMostPs = 0x1p15f;
 constexpr int kMostUp = 120;       // log2 of `up` at the most, and of 1 / `up`
-// 2^e, -126 <= e <= 127
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 // 1 / x of such a power of two
 __device__ __forceinline__ float inverse(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
 
@@ -104,13 +107,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ float max3(float x, float y, float z)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-    return r;
 }
 
 // The same value in every lane, as the compiler cannot know: what follows from it
@@ -157,9 +153,6 @@ __device__ __forceinline__ void load_values(uint32_t (&v)[NC][4][N], int i, uint
     if constexpr (NC == 2)
         load_shared<CELL + OFF>(v[1][i], at);
 }
-
-__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
 // Pairs of cells on their way or in use: each warp has a ring of its own and
 // fills a place again as soon as it has read it; no barrier between warps.  12

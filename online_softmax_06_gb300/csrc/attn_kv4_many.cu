@@ -43,6 +43,10 @@
 namespace fa {
 namespace {
 
+using kv4::bf16_hi;
+using kv4::bf16_lo;
+using kv4::pow2;
+
 constexpr int BM = 128;              // query rows of a Q tile
 constexpr int BN = 128;              // keys of a K/V tile
 constexpr int kThreads = 320;
@@ -60,10 +64,6 @@ constexpr uint32_t kChunkBytes = BM * 128;
 constexpr int kExpandThreads = 256;
 constexpr int kNoNan = 255;          // of a tile's group
 
-__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-// 2^e, -126 <= e <= 127
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 // e with 2^-e x in [2^13, 2^14), `least` at least.  For V -84: a sum of 2^31 P = P^ 2^-e
 // <= 2^92 stays finite.  For Q and K -110: their factors stay normal numbers, and any
 // bf16 number is 2^-16 at least.

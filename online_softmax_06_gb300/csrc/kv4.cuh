@@ -41,5 +41,11 @@ __device__ __forceinline__ int v_swizzle(int a)
     return (((s & ~3) | ((s + (s >> 2)) & 3)) << 5) | (a & 31);
 }
 
+// The two bf16 numbers of a word.
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
+
 }  // namespace kv4
 }  // namespace fa

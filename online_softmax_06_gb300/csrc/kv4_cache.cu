@@ -28,6 +28,9 @@
 namespace fa {
 namespace {
 
+using kv4::bf16_hi;
+using kv4::bf16_lo;
+
 constexpr int kThreads = 256;
 constexpr int kBlocksPerSm = 5;
 
@@ -108,9 +111,6 @@ __device__ __forceinline__ uint32_t min_nan2(uint32_t x, uint32_t y)
     asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
     return r;
 }
-
-__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
 __device__ __forceinline__ uint32_t max_nan2(uint32_t x, uint32_t y)
 {
