@@ -68,11 +68,12 @@ constexpr float kNoRef = -0x1p126f;
 // A row's reference stands kRefAbove above its largest S and may lag until a P exceeds
 // kMostP, so that the fp32 sums of P and P m stay finite for values up to 2^110.  P s
 // goes to fp16 after a power of two of the row and group (`up`) that brings the largest
-// into [2^10, 2^11), up to kMostPs as it lags: a group of small scales keeps its bits
-// beside one of large scales, and a key of 2^-24 of the largest weight its share.  (With
+// into [2^7, 2^8), up to kMostPs as it lags: a group of small scales keeps its bits
+// beside one of large scales, and a key of 2^-21 of the largest weight its share.  (With
 // one reference for all groups, P s <= 1 for a key's largest scale, a group of scales
-// 2^-20 of its neighbour's was off by three of its own steps.  Times are the same within
-// 2 %: 64 x 8k keys 102.3 us, so 101.8; 256 x 1k 79.7 and 78.2; 32 x 4k 42.3 and 44.9.)
+// 2^-20 of its neighbour's was off by three of its own steps.)  It costs 0 to 1 % with
+// 4 rows (64 x 8k keys 101.7 us) and one to five with 8 and 16 and groups of 32 or 64 (32
+// x 2 queries on 2k to 9k keys, groups of 64, 48.8 us, so 47.7; of 32 56.3 and 55.1).
 constexpr float kRefAbove = 10.f, kMostP = 0x1p-2f, kMostPs = 0x1p15f;
 constexpr int kMostUp = 120;       // log2 of `up` at the most, and of 1 / `up`
 // 1 / x of such a power of two
@@ -838,19 +839,27 @@ __global__ void __launch_bounds__(kThreads *kv4_attention_crews(8 * NT, D), 1)
 #pragma unroll
                             for (int t = 0; t < 2; ++t)
                                 P[x][t][e] = ptx::ex2(S[x][t] - m);
+                        // the upper halves of two groups' largest P s a word
+                        uint32_t big[(NG + 1) / 2] = {};
 #pragma unroll
                         for (int y = 0; y < NG; ++y) {
-                            const float old = inverse(up[nt][y][e]);
-                            float big = 0x1p10f * f * old;
+                            float top = 0x1p7f * f * inverse(up[nt][y][e]);
 #pragma unroll
                             for (int x = 0; x < NC; ++x)
+                                top = max3(top, P[x][0][e] * bf16_lo(pv[x][0][y]),
+                                           P[x][1][e] * bf16_lo(pv[x][1][y]));
+                            big[y / 2] = __byte_perm(big[y / 2], __float_as_uint(top),
+                                                     y % 2 ? 0x7610 : 0x3276);
+                        }
 #pragma unroll
-                                for (int t = 0; t < 2; ++t)
-                                    big = fmaxf(big, P[x][t][e] * bf16_lo(pv[x][t][y]));
-                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 4));
-                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 8));
-                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 16));
-                            const int log = 137 - int(__float_as_uint(big) >> 23);
+                        for (int y = 0; y < (NG + 1) / 2; ++y)
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1)
+                                big[y] = __vmaxu2(big[y], __shfl_xor_sync(0xffffffffu, big[y], o));
+#pragma unroll
+                        for (int y = 0; y < NG; ++y) {
+                            const int log = 134 - int(y % 2 ? big[y / 2] >> 23 : big[y / 2] >> 7 & 255);
+                            const float old = inverse(up[nt][y][e]);
                             up[nt][y][e] = pow2(max(-kMostUp, min(kMostUp, log)));
                             const float r = f * up[nt][y][e] * old;
                             pm[nt][y][e] *= f;

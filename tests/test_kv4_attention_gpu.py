@@ -831,7 +831,7 @@ def test_groups_of_far_apart_scales(H, Nq, d, group, k):
 
     Few rows: P s goes to fp16 after a power of two of its (row, group), so 2^-11 of
     each key's P 15 s, and a fixed step of 2^-25 where the largest P s of the group is
-    2^10 at least: 2^-35 of it a key, 2^-23 for 4000 keys.  Errors of S (eS) act twice,
+    2^7 at least: 2^-32 of it a key, 2^-20 for 4000 keys.  Errors of S (eS) act twice,
     on the weights and their sum, and on codes and minimum alike; the fp32 sums of at
     most 2^8 terms a lane add 2^-16 of the sum of the magnitudes.  The bound goes by the
     row's and the group's own P, s and m:
