@@ -466,7 +466,8 @@ FA_API int fa_attention_fwd_splitkv_noalloc(const void *Q, const void *K, const 
  * a sequence whose counts are negative, above N or Nk, or do not fit (seqlens
  * below the new tokens, or above max_pages * page_size; rows outside the tensor),
  * FA_DEVERR_BAD_PAGE for a page outside [0, num_pages).  Such a sequence, or such a
- * page's tokens, is left out: nothing is read or written out of bounds.  Where
+ * page's tokens, is left out (in the attention these count as zeros): nothing is
+ * read or written out of bounds.  Where
  * cu_seqlens decreases, other sequences may be left out too, and those that claim
  * the same rows are undefined among one another.
  */
@@ -523,7 +524,7 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  *   8, at least H * d), of magnitudes below 2^115 (an infinity or a NaN, or with
  *   few query rows a larger value, makes NaN of its row).  O: contiguous bf16.
  *   seqlens: each sequence's keys, 0 .. Nk (Nk: an upper bound, <= max_pages *
- *   page_size).
+ *   page_size; with many rows the work is laid out by it).
  *   causal != 0: query i of n sees keys j <= i + seqlens[b] - n (bottom-right,
  *   as in fa_attention_fwd_splitkv); otherwise all seqlens[b] keys.  A query
  *   that sees no key gets O = 0 and lse = -inf.  Scores are fp32: one of magnitude
@@ -541,8 +542,9 @@ FA_API int fa_kv4_read(void *K, void *V, int64_t k_stride, int64_t v_stride, con
  * Many (about 100 and more on average, enough to fill the GPU; chunks of
  * prompts): the values are first written out as fp16 (2^-11 relative, with a
  * power of two a tile of 128 tokens of a head: values below 2^-28 of the tile's
- * largest have fewer bits), and so have probabilities below 2^-21 of the largest
- * that a row has, each times its tile's largest value.
+ * largest, or below 2^-98, have fewer bits), and so have probabilities below 2^-21
+ * of the largest that a row has, each times its tile's largest value.  A call whose
+ * copies would take more than 8 GB goes the way of few rows, more slowly.
  * A group of a token that holds NaN makes NaN of the rows that see it, for V in
  * the group's columns alone.
  * B <= 1024.  Results do not depend on timing: the same call gives the same

@@ -25,7 +25,7 @@
 // than the products (attn_kv4_many.cu does it where there are rows enough).
 //
 // What bounds it: a cell of 16 tokens (2304 bytes with d = 128, group 64) costs a
-// warp some 240 instructions with 4 rows, 270 with 8, of which half are logical
+// warp 236 instructions with 4 rows, 274 with 8, of which half are logical
 // operations at two a cycle and SM, 88 of them the expansion; HBM leaves 100 cycles a
 // cell.  64 sequences of 300 to 16000 keys (32 heads on 8) take 102 us, 5.9 TB/s, 0.87
 // of the measured copy rate: the start (lengths, page table, first cells: three memory

@@ -6,9 +6,9 @@
 // values are written out once, as fp16, and a kernel of the shape of attn_bf16.cu
 // (two 128-row Q tiles a CTA, K and V tiles of 128 keys through a TMA ring, S, P
 // and O in tensor memory) reads them: 4 sequences x 256 to 512 queries on 2k to 16k
-// keys, 32 heads on 8, take 843 us with the one and 216 with the other, 44 of them
-// for the copy (5.2 TB/s) and 15 for the join; with 1024 queries each on 16k keys
-// the whole runs at 1.35 PFLOP/s, 0.72 of the measured cuBLAS rate.
+// keys, 32 heads on 8, take 843 us with the one and 214 with the other, 44 of them
+// for the copy (5.2 TB/s) and 15 for the join; with 1024 queries each on 16384 keys
+// the whole takes 0.80 ms, 1.33 PFLOP/s, 0.71 of the measured cuBLAS rate.
 //
 // fp16 has 11 bits where min + scale * code needs up to 16: each value is rounded
 // once, by 2^-11 of itself at most, after the power of two that brings the largest
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---- work item: (sequence, kv head, range of p.w.chunk key tiles, pair of Q
     //      tiles), the pairs side by side: they read the same K and V tiles (with the
-    //      pairs apart, 4 x 512 queries on 16k keys took 240 us, so 216) --------------
+    //      pairs apart, 4 x 512 queries on 16k keys took 240 us, so 214) --------------
     const Kv4AttnArgs &a = p.a;
     const int grp = a.H / a.Hkv;
     const int rest = int(blockIdx.x) / p.n_pairs, px = int(blockIdx.x) % p.n_pairs;
