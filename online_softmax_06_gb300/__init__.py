@@ -777,7 +777,8 @@ def kv4_read(cache, page_table, seqlens, total: int | None = None, d: int = 128,
     With ``cu_seqlens`` (int32 [B+1]) the last cu_seqlens[b+1] - cu_seqlens[b]
     tokens of sequence b, packed into [total, kv_heads, d]; otherwise the last
     ``n`` of each, [B, n, kv_heads, d].  ``k`` and ``v``: write into these (rows
-    that belong to no sequence are left as they are).
+    that belong to no sequence are left as they are).  ``d`` and ``group`` are the
+    cache's own: its bytes do not always tell them.
     """
     import torch
     if k is None or v is None:
