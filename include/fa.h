@@ -569,6 +569,63 @@ FA_API int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, 
 FA_API int64_t fa_attention_kv4_workspace_bytes(int B, int Nq, int64_t total_q, int Nk, int H,
                                                 int Hkv, int d);
 
+/* ---- Norm and rotation of queries and keys ---------------------------------------
+ *
+ * What an attention layer does to the heads of Q and K before the attention, in
+ * one pass over them (the pages begin at Q, K and V; this is the library's own).
+ * For a head's row x of d values of a token at position p:
+ *     n = x / sqrt(mean(x^2) + eps) o weight,   y = R_p n,
+ * R_p turning the pairs (a, b) of the first `rot` values by p * inv_freq[j], j =
+ * 0 .. rot / 2 - 1:  a cos - b sin,  a sin + b cos.  Pair j is values j and j +
+ * rot / 2, or with interleaved != 0 values 2 j and 2 j + 1; values from rot on
+ * are not turned.
+ *   Q, K: bf16, `total` token rows of H * d and Hkv * d contiguous values,
+ *   q_stride and k_stride elements apart (multiples of 8, at least the row: parts
+ *   of a fused projection's rows, say).  Qo, Ko: bf16 likewise; Qo may be Q, and
+ *   Ko K, at the same stride (in place); any other overlap is not allowed.
+ *   q_weight, k_weight: DEVICE fp32 [d], or NULL for ones.  inv_freq: DEVICE fp64
+ *   [rot / 2], finite.  positions: DEVICE int32 [total], any values: angles are
+ *   formed modulo a turn in 64 bits, so far positions lose nothing.  Both may be
+ *   NULL where rot is 0.
+ *   d: 64 or 128.  rot: 0 .. d, a multiple of 8.  eps >= 0.  H or Hkv may be 0
+ *   (its pointers are not read then).  All pointers to bf16 16-byte aligned.
+ * Sums in fp32, each output rounded once to bf16.  One kernel on the library
+ * stream, no synchronisation.
+ * Errors: FA_ERR_BAD_SIZE, FA_ERR_UNSUPPORTED (d, rot), FA_ERR_NULL_POINTER,
+ * FA_ERR_MISALIGNED, FA_ERR_TOO_LARGE, FA_ERR_NO_DEVICE, FA_ERR_CUDA.
+ */
+FA_API int fa_qk_norm_rope_fwd(const void *Q, int64_t q_stride, const void *K, int64_t k_stride,
+                               const float *q_weight, const float *k_weight,
+                               const double *inv_freq, const int32_t *positions, void *Qo,
+                               int64_t qo_stride, void *Ko, int64_t ko_stride, int64_t total,
+                               int H, int Hkv, int d, int rot, int interleaved, float eps);
+
+/*
+ * Its gradient: dQo and dKo are the gradients of Qo and Ko (rows like theirs,
+ * with strides of their own), Q and K the inputs of the forward.
+ *   dQ, dK: bf16 rows, written; each may be the gradient it is formed from, or
+ *   the input, at the same stride.
+ *   dq_weight, dk_weight: fp32 [d], written (summed over tokens and heads; zeros
+ *   without any), or NULL.
+ *   workspace: DEVICE scratch owned by the caller, 256-byte aligned, at least
+ *   fa_qk_norm_rope_bwd_workspace_bytes(total, H, Hkv, d) bytes; contents on
+ *   entry are ignored.  Calls that may run at the same time need one each.
+ * The same call gives the same bits.  One or two kernels on the library stream,
+ * no synchronisation.  Errors: as above; FA_ERR_BAD_SIZE also for a workspace
+ * that is too small.
+ */
+FA_API int fa_qk_norm_rope_bwd(const void *Q, int64_t q_stride, const void *K, int64_t k_stride,
+                               const void *dQo, int64_t dqo_stride, const void *dKo,
+                               int64_t dko_stride, const float *q_weight, const float *k_weight,
+                               const double *inv_freq, const int32_t *positions, void *dQ,
+                               int64_t dq_stride, void *dK, int64_t dk_stride, float *dq_weight,
+                               float *dk_weight, int64_t total, int H, int Hkv, int d, int rot,
+                               int interleaved, float eps, void *workspace,
+                               int64_t workspace_bytes);
+
+/* Workspace bytes fa_qk_norm_rope_bwd needs, or a negative FA_ERR_* code. */
+FA_API int64_t fa_qk_norm_rope_bwd_workspace_bytes(int64_t total, int H, int Hkv, int d);
+
 /*
  * Exact attention forward in fp32 throughout (fp32 Q, K, V, O, lse), on the
  * CUDA cores, for inputs that need fp32 accuracy.  Same definition, layouts,

@@ -17,11 +17,13 @@ Raw C-ABI names (same names, same argument order, ints and pointers only):
 ``fa_attention_host_workspace_bytes``,
 ``fa_kv4_page_bytes``, ``fa_kv4_append``, ``fa_kv4_read``,
 ``fa_attention_kv4``, ``fa_attention_kv4_workspace_bytes``,
+``fa_qk_norm_rope_fwd``, ``fa_qk_norm_rope_bwd``, ``fa_qk_norm_rope_bwd_workspace_bytes``,
 ``fa_set_stream``, ``fa_get_stream``, ``fa_get_device_error``, ``fa_strerror``,
 ``fa_version``, ``fa_debug_expire_next_wait``.
 Tensor-level helpers: :func:`softmax_rows`, :func:`attention_fwd`,
 :func:`attention_fwd_splitkv`, :func:`attention_bwd`, :func:`attention_fwd_fp8`,
-:func:`kv4_cache`, :func:`kv4_append`, :func:`kv4_read`, :func:`attention_kv4`.
+:func:`kv4_cache`, :func:`kv4_append`, :func:`kv4_read`, :func:`attention_kv4`,
+:func:`qk_norm_rope_fwd`, :func:`qk_norm_rope_bwd`.
 """
 from __future__ import annotations
 
@@ -116,6 +118,13 @@ def lib():
                                        i64, i32, i32, i32, i32, i32, f32, i32, vp, i64]
         L.fa_attention_kv4_workspace_bytes.argtypes = [i32, i32, i64, i32, i32, i32, i32]
         L.fa_attention_kv4_workspace_bytes.restype = i64
+        L.fa_qk_norm_rope_fwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, i64,
+                                          i32, i32, i32, i32, i32, f32]
+        L.fa_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp,
+                                          i64, vp, i64, vp, vp, i64, i32, i32, i32, i32, i32, f32,
+                                          vp, i64]
+        L.fa_qk_norm_rope_bwd_workspace_bytes.argtypes = [i64, i32, i32, i32]
+        L.fa_qk_norm_rope_bwd_workspace_bytes.restype = i64
         L.fa_set_stream.argtypes = [vp]
         L.fa_get_stream.argtypes = []
         L.fa_get_stream.restype = vp
@@ -132,7 +141,8 @@ def lib():
                      "fa_attention_fwd_splitkv_varlen",
                      "fa_attention_fwd_fp8", "fa_attention_fwd_fp8_varlen",
                      "fa_attention_fwd_host", "fa_kv4_append", "fa_kv4_read",
-                     "fa_attention_kv4", "fa_set_stream", "fa_get_device_error", "fa_version",
+                     "fa_attention_kv4", "fa_qk_norm_rope_fwd", "fa_qk_norm_rope_bwd",
+                     "fa_set_stream", "fa_get_device_error", "fa_version",
                      "fa_debug_expire_next_wait"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -282,6 +292,27 @@ def fa_attention_kv4(q, q_stride, cache, num_pages, page_size, page_table, max_p
 
 def fa_attention_kv4_workspace_bytes(B, Nq, total_q, Nk, H, Hkv, d) -> int:
     return lib().fa_attention_kv4_workspace_bytes(B, Nq, total_q, Nk, H, Hkv, d)
+
+
+def fa_qk_norm_rope_fwd(q, q_stride, k, k_stride, q_weight, k_weight, inv_freq, positions, qo,
+                        qo_stride, ko, ko_stride, total, H, Hkv, d, rot, interleaved, eps) -> int:
+    return lib().fa_qk_norm_rope_fwd(q, q_stride, k, k_stride, q_weight, k_weight, inv_freq,
+                                     positions, qo, qo_stride, ko, ko_stride, total, H, Hkv, d,
+                                     rot, interleaved, eps)
+
+
+def fa_qk_norm_rope_bwd(q, q_stride, k, k_stride, dqo, dqo_stride, dko, dko_stride, q_weight,
+                        k_weight, inv_freq, positions, dq, dq_stride, dk, dk_stride, dq_weight,
+                        dk_weight, total, H, Hkv, d, rot, interleaved, eps, workspace,
+                        workspace_bytes) -> int:
+    return lib().fa_qk_norm_rope_bwd(q, q_stride, k, k_stride, dqo, dqo_stride, dko, dko_stride,
+                                     q_weight, k_weight, inv_freq, positions, dq, dq_stride, dk,
+                                     dk_stride, dq_weight, dk_weight, total, H, Hkv, d, rot,
+                                     interleaved, eps, workspace, workspace_bytes)
+
+
+def fa_qk_norm_rope_bwd_workspace_bytes(total, H, Hkv, d) -> int:
+    return lib().fa_qk_norm_rope_bwd_workspace_bytes(total, H, Hkv, d)
 
 
 def fa_set_stream(stream_ptr) -> int:
@@ -865,7 +896,122 @@ def attention_kv4(q, cache, page_table, seqlens, max_seqlen: int | None = None, 
     return out, lse
 
 
+# ---- norm and rotation of queries and keys ----------------------------------------
+
+def _plan_norm_rope(shapes, strides, w_shapes, pos, freq):
+    """(strides of the rows, total, H, Hkv, d, rot) of q, k and tensors like them.
+
+    shapes and strides: pairs (of q, of k), the inputs first.
+    """
+    q, k = shapes[0]
+    if len(q) not in (3, 4) or len(k) != len(q) or q[:-2] != k[:-2] or q[-1] != k[-1]:
+        raise ValueError("q and k must be [total, heads, d] or [B, N, heads, d] of the same tokens")
+    total = 1
+    for s in q[:-2]:
+        total *= s
+    for pair in shapes[1:]:
+        if pair != shapes[0]:
+            raise ValueError("outputs and gradients must have the shapes of q and k")
+    if any(w is not None and tuple(w) != (q[-1],) for w in w_shapes):
+        raise ValueError(f"weights must be [{q[-1]}]")
+    rot = 0 if freq is None else 2 * freq[0]
+    if rot and (pos is None or tuple(pos) not in (tuple(q[:-2]), (total,))):
+        raise ValueError("positions must have one entry a token")
+    rows = [_row_stride(s, st, n) for pair, stp in zip(shapes, strides)
+            for s, st, n in zip(pair, stp, ("q", "k"))]
+    return rows, total, q[-2], k[-2], q[-1], rot
+
+
+def _check_norm_rope(torch, rows, weights, inv_freq, positions):
+    index = rows[0].get_device()
+    if index < 0:
+        raise ValueError("q and k must be CUDA tensors")
+    for t in rows:
+        if t.dtype is not torch.bfloat16 or t.get_device() != index:
+            raise ValueError("q, k and tensors like them must be bf16 and on one device")
+    for t, dtype, name in ((weights[0], torch.float32, "q_weight"),
+                           (weights[1], torch.float32, "k_weight"),
+                           (inv_freq, torch.float64, "inv_freq"),
+                           (positions, torch.int32, "positions")):
+        if t is not None and (t.dtype is not dtype or t.get_device() != index
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor on q's device")
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot / 2]")
+    return index
+
+
+def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None,
+                     eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None):
+    """Norm of each head of q and k, x / sqrt(mean(x^2) + eps) * weight, and the rotation of its
+    first values by position, in one pass.
+
+    q: bf16 [total, H, d] or [B, N, H, d]; k likewise with the kv heads.  A token's heads are
+    contiguous, tokens may be any multiple of 8 elements apart (slices of a fused projection).
+    ``q_weight``, ``k_weight``: fp32 [d], or None for ones.  ``inv_freq``: fp64 [rot / 2], rot a
+    multiple of 8: values j and j + rot / 2 (``interleaved``: 2 j and 2 j + 1) are turned by
+    positions * inv_freq[j]; None: no rotation.  ``positions``: int32, one a token.  ``q_out``,
+    ``k_out``: write into these (they may be q and k).  Returns (q_out, k_out).
+    """
+    import torch
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+    index = _check_norm_rope(torch, (q, k, q_out, k_out), (q_weight, k_weight), inv_freq, positions)
+    shape = lambda t: None if t is None else t.shape  # noqa: E731
+    key = (((q.shape, k.shape), (q_out.shape, k_out.shape)),
+           ((q.stride(), k.stride()), (q_out.stride(), k_out.stride())),
+           (shape(q_weight), shape(k_weight)), shape(positions), shape(inv_freq))
+    (qs, ks, qos, kos), total, H, hkv, d, rot = _kv4_plan(key, _plan_norm_rope, *key)
+    _kv4_call(torch, index, "fa_qk_norm_rope_fwd", q.data_ptr(), qs, k.data_ptr(), ks,
+              _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), q_out.data_ptr(),
+              qos, k_out.data_ptr(), kos, total, H, hkv, d, rot, 1 if interleaved else 0, eps)
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, inv_freq=None,
+                     positions=None, eps: float = 1e-6, interleaved: bool = False, dq=None,
+                     dk=None, workspace=None):
+    """Gradient of :func:`qk_norm_rope_fwd`: its inputs, and the gradients of its outputs.
+
+    ``dq`` and ``dk``: write into these (they may be dq_out and dk_out).  The workspace is
+    allocated here (torch) unless given (uint8, fa_qk_norm_rope_bwd_workspace_bytes).  Returns
+    (dq, dk, dq_weight, dk_weight); the last two are fp32 [d], None without that weight.
+    """
+    import torch
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+    index = _check_norm_rope(torch, (q, k, dq_out, dk_out, dq, dk), (q_weight, k_weight), inv_freq,
+                             positions)
+    shape = lambda t: None if t is None else t.shape  # noqa: E731
+    key = (((q.shape, k.shape), (dq_out.shape, dk_out.shape), (dq.shape, dk.shape)),
+           ((q.stride(), k.stride()), (dq_out.stride(), dk_out.stride()),
+            (dq.stride(), dk.stride())),
+           (shape(q_weight), shape(k_weight)), shape(positions), shape(inv_freq))
+    (qs, ks, gqs, gks, dqs, dks), total, H, hkv, d, rot = _kv4_plan(key, _plan_norm_rope, *key)
+    dwq, dwk = (None if w is None else torch.empty(w.shape, dtype=torch.float32, device=q.device)
+                for w in (q_weight, k_weight))
+    if workspace is None:
+        nbytes = fa_qk_norm_rope_bwd_workspace_bytes(total, H, hkv, d)
+        _check(int(min(nbytes, 0)), "fa_qk_norm_rope_bwd_workspace_bytes")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    elif not (workspace.dtype is torch.uint8 and workspace.get_device() == index
+              and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    _kv4_call(torch, index, "fa_qk_norm_rope_bwd", q.data_ptr(), qs, k.data_ptr(), ks,
+              dq_out.data_ptr(), gqs, dk_out.data_ptr(), gks, _ptr(q_weight), _ptr(k_weight),
+              _ptr(inv_freq), _ptr(positions), dq.data_ptr(), dqs, dk.data_ptr(), dks, _ptr(dwq),
+              _ptr(dwk), total, H, hkv, d, rot, 1 if interleaved else 0, eps, workspace.data_ptr(),
+              workspace.numel())
+    return dq, dk, dwq, dwk
+
+
 __all__ = [
+    "qk_norm_rope_fwd", "qk_norm_rope_bwd", "fa_qk_norm_rope_fwd", "fa_qk_norm_rope_bwd",
+    "fa_qk_norm_rope_bwd_workspace_bytes",
     "attention_kv4", "kv4_cache", "kv4_append", "kv4_read", "fa_attention_kv4",
     "fa_attention_kv4_workspace_bytes", "fa_kv4_page_bytes", "fa_kv4_append", "fa_kv4_read",
     "FA_DEVERR_BAD_PAGE",

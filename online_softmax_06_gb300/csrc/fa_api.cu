@@ -943,6 +943,133 @@ int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, int num
                 : fa::launch_attention_kv4(a, fa::t_stream);
 }
 
+}  // extern "C"
+
+namespace fa {
+namespace {
+// Shared by the norm and rotation (g empty) and its gradient; fills a.
+int check_norm_rope(bool backward, const void *const x[2], const int64_t xs[2],
+                    const void *const g[2], const int64_t gs[2], void *const y[2],
+                    const int64_t ys[2], const float *const w[2], const double *inv_freq,
+                    const int32_t *positions, int64_t tokens, const int heads[2], int d, int rot,
+                    int interleaved, float eps, NormRopeArgs *a)
+{
+    if (tokens < 0 || heads[0] < 0 || heads[1] < 0 || rot < 0 || rot > d || !(eps >= 0.f))
+        return FA_ERR_BAD_SIZE;
+    if ((d != 64 && d != 128) || rot % 8 != 0)
+        return FA_ERR_UNSUPPORTED;
+    const int64_t limit = int64_t(1) << 31;
+    if (tokens > limit - 512 || heads[0] > 65535 || heads[1] > 65535)
+        return FA_ERR_TOO_LARGE;
+    for (int i = 0; i < 2 && tokens > 0; ++i) {
+        if (heads[i] == 0)
+            continue;
+        if (!x[i] || !y[i] || (backward && !g[i]) || (rot > 0 && (!inv_freq || !positions)))
+            return FA_ERR_NULL_POINTER;
+        const int64_t row = int64_t(heads[i]) * d;
+        if (xs[i] < row || ys[i] < row || (backward && gs[i] < row))
+            return FA_ERR_BAD_SIZE;
+        if (!aligned(x[i], 16) || !aligned(y[i], 16) || xs[i] % 8 != 0 || ys[i] % 8 != 0 ||
+            (backward && (!aligned(g[i], 16) || gs[i] % 8 != 0)) || !aligned(w[i], 4) ||
+            !aligned(inv_freq, 8) || !aligned(positions, 4))
+            return FA_ERR_MISALIGNED;
+        if (xs[i] > limit || ys[i] > limit || (backward && gs[i] > limit))
+            return FA_ERR_TOO_LARGE;
+    }
+    for (int i = 0; i < 2; ++i) {
+        a->x[i] = x[i];
+        a->xs[i] = xs[i];
+        a->g[i] = g[i];
+        a->gs[i] = gs[i];
+        a->y[i] = y[i];
+        a->ys[i] = ys[i];
+        a->w[i] = w[i];
+        a->heads[i] = heads[i];
+        a->dw[i] = nullptr;
+    }
+    a->freq = inv_freq;
+    a->pos = positions;
+    a->partial = nullptr;
+    a->tokens = tokens;
+    a->d = d;
+    a->rot = rot;
+    a->interleaved = interleaved ? 1 : 0;
+    a->eps = eps;
+    return FA_OK;
+}
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+int fa_qk_norm_rope_fwd(const void *Q, int64_t q_stride, const void *K, int64_t k_stride,
+                        const float *q_weight, const float *k_weight, const double *inv_freq,
+                        const int32_t *positions, void *Qo, int64_t qo_stride, void *Ko,
+                        int64_t ko_stride, int64_t total, int H, int Hkv, int d, int rot,
+                        int interleaved, float eps)
+{
+    const void *x[2] = {Q, K}, *g[2] = {nullptr, nullptr};
+    void *y[2] = {Qo, Ko};
+    const int64_t xs[2] = {q_stride, k_stride}, gs[2] = {0, 0}, ys[2] = {qo_stride, ko_stride};
+    const float *w[2] = {q_weight, k_weight};
+    const int heads[2] = {H, Hkv};
+    fa::NormRopeArgs a;
+    const int rc = fa::check_norm_rope(false, x, xs, g, gs, y, ys, w, inv_freq, positions, total,
+                                       heads, d, rot, interleaved, eps, &a);
+    if (rc != FA_OK)
+        return rc;
+    if (total == 0 || (H == 0 && Hkv == 0))
+        return FA_OK;
+    if (fa::current_device() == nullptr)
+        return FA_ERR_NO_DEVICE;
+    return fa::launch_norm_rope_fwd(a, fa::t_stream);
+}
+
+int64_t fa_qk_norm_rope_bwd_workspace_bytes(int64_t total, int H, int Hkv, int d)
+{
+    if (total < 0 || H < 0 || Hkv < 0)
+        return FA_ERR_BAD_SIZE;
+    if (d != 64 && d != 128)
+        return FA_ERR_UNSUPPORTED;
+    return total == 0 || (H == 0 && Hkv == 0) ? 0 : int64_t(fa::kNormRopeCtas) * 2 * d * 4;
+}
+
+int fa_qk_norm_rope_bwd(const void *Q, int64_t q_stride, const void *K, int64_t k_stride,
+                        const void *dQo, int64_t dqo_stride, const void *dKo, int64_t dko_stride,
+                        const float *q_weight, const float *k_weight, const double *inv_freq,
+                        const int32_t *positions, void *dQ, int64_t dq_stride, void *dK,
+                        int64_t dk_stride, float *dq_weight, float *dk_weight, int64_t total,
+                        int H, int Hkv, int d, int rot, int interleaved, float eps,
+                        void *workspace, int64_t workspace_bytes)
+{
+    const void *x[2] = {Q, K}, *g[2] = {dQo, dKo};
+    void *y[2] = {dQ, dK};
+    const int64_t xs[2] = {q_stride, k_stride}, gs[2] = {dqo_stride, dko_stride};
+    const int64_t ys[2] = {dq_stride, dk_stride};
+    const float *w[2] = {q_weight, k_weight};
+    const int heads[2] = {H, Hkv};
+    fa::NormRopeArgs a;
+    const int rc = fa::check_norm_rope(true, x, xs, g, gs, y, ys, w, inv_freq, positions, total,
+                                       heads, d, rot, interleaved, eps, &a);
+    if (rc != FA_OK)
+        return rc;
+    const int64_t needs = fa_qk_norm_rope_bwd_workspace_bytes(total, H, Hkv, d);
+    if (workspace_bytes < needs)
+        return FA_ERR_BAD_SIZE;
+    if (needs > 0 && workspace == nullptr)
+        return FA_ERR_NULL_POINTER;
+    if (!fa::aligned(workspace, 256) || !fa::aligned(dq_weight, 4) || !fa::aligned(dk_weight, 4))
+        return FA_ERR_MISALIGNED;
+    if (needs == 0 && dq_weight == nullptr && dk_weight == nullptr)
+        return FA_OK;
+    if (fa::current_device() == nullptr)
+        return FA_ERR_NO_DEVICE;
+    a.dw[0] = dq_weight;
+    a.dw[1] = dk_weight;
+    a.partial = static_cast<float *>(workspace);
+    return fa::launch_norm_rope_bwd(a, fa::t_stream);
+}
+
 int fa_attention_fwd_f32(const float *Q, const float *K, const float *V, float *O, float *lse,
                          int B, int H, int N, int d, float scale, int causal,
                          const int32_t *cu_seqlens)

@@ -331,4 +331,23 @@ inline int64_t kv4_attention_workspace_bytes(int B, int Nq, int64_t total_q, int
 int launch_attention_kv4_many(const Kv4AttnArgs &a, cudaStream_t stream);
 int launch_attention_kv4(const Kv4AttnArgs &a, cudaStream_t stream);
 
+// Norm and rotation of the heads of Q (index 0) and K (1), and its gradient.
+struct NormRopeArgs {
+    const void *x[2], *g[2];   // inputs; backward: gradients of the outputs
+    void *y[2];                // outputs; backward: gradients of the inputs
+    int64_t xs[2], gs[2], ys[2];  // elements between tokens
+    const float *w[2];         // or nullptr: ones
+    float *dw[2];              // backward, or nullptr
+    const double *freq;        // [rot / 2]
+    const int32_t *pos;        // [tokens]
+    float *partial;            // backward: workspace
+    int64_t tokens;
+    int heads[2];
+    int d, rot, interleaved;
+    float eps;
+};
+constexpr int kNormRopeCtas = 152 * 4;     // the gradient's CTAs, each with sums of its own
+int launch_norm_rope_fwd(const NormRopeArgs &a, cudaStream_t stream);
+int launch_norm_rope_bwd(const NormRopeArgs &a, cudaStream_t stream);
+
 }  // namespace fa
