@@ -569,6 +569,48 @@ FA_API int fa_attention_kv4(const void *Q, int64_t q_stride, const void *cache, 
 FA_API int64_t fa_attention_kv4_workspace_bytes(int B, int Nq, int64_t total_q, int Nk, int H,
                                                 int Hkv, int d);
 
+/* ---- Attention with a sliding window and sinks -----------------------------------
+ *
+ * Exact attention where a query sees the last `window` keys up to its own, and the
+ * first `sinks` keys of its sequence, which stay visible (the pages know causal
+ * and padding masks, [L22] §三十四-三十五; this mask is the library's own):
+ * query i of the n of a sequence of L keys sits at position p = i + L - n (bottom-
+ * right, as in fa_attention_fwd_splitkv) and sees key j iff
+ *     j <= p  and  (j > p - window  or  j < sinks).
+ * O = softmax(scale Q K^T | seen keys) V and lse as in fa_attention_fwd; a query
+ * that sees no key (p < 0) gets O = 0 and lse = -inf.  Query head h reads kv head
+ * h / (H / Hkv).  The work grows with the window, not with the keys.
+ *   dense  (cu_seqlens_q == NULL): Q rows and O [B, Nq, H, d], lse [B, H, Nq];
+ *          total_q = B * Nq.
+ *   packed: Q rows and O [total_q, H, d], lse [H, total_q]; cu_seqlens_q DEVICE
+ *          int32 [B + 1], Nq the most queries of a sequence (an upper bound is
+ *          fine).  Rows behind the last sequence are left as they were.
+ *   Keys of sequence b: rows b * Nk on (cu_seqlens_k == NULL; total_k = B * Nk), or
+ *   cu_seqlens_k[b] .. cu_seqlens_k[b + 1] - 1 of total_k rows, Nk at least as many
+ *   as a sequence uses.  Of these rows the first seqlens_k[b] hold keys (a cache
+ *   with room for more; DEVICE int32 [B]), or all of them where seqlens_k is NULL.
+ *   Q, K, V: bf16 rows of H * d, and Hkv * d, contiguous values, q_stride, k_stride
+ *   and v_stride elements apart (multiples of 8, at least the row); 16-byte
+ *   aligned.  O: contiguous bf16, 16-byte aligned.  d: 64 or 128.  H / Hkv <= 128.
+ *   window >= 1, sinks >= 0, scale > 0 and finite.
+ * What K and V hold behind a sequence's keys does not reach a result, NaN or not,
+ * and K neither at keys that a query does not see; a V that is not finite reaches
+ * the queries that see its key and may reach others near them.
+ * A sequence whose counts do not fit (negative, decreasing, above Nq, Nk or its
+ * rows, outside the tensors) is not computed and sets FA_DEVERR_BAD_SEQLENS.
+ * The same call gives the same bits.  One kernel on the library stream, no
+ * synchronisation, no workspace.
+ * Errors: FA_ERR_BAD_SIZE, FA_ERR_UNSUPPORTED (d, H / Hkv), FA_ERR_NULL_POINTER,
+ * FA_ERR_MISALIGNED (pointers, strides), FA_ERR_TOO_LARGE, FA_ERR_NO_DEVICE,
+ * FA_ERR_CUDA.
+ */
+FA_API int fa_attention_window_fwd(const void *Q, int64_t q_stride, const void *K,
+                                   int64_t k_stride, const void *V, int64_t v_stride, void *O,
+                                   float *lse, int B, int Nq, int64_t total_q, int Nk,
+                                   int64_t total_k, int H, int Hkv, int d, float scale,
+                                   int window, int sinks, const int32_t *cu_seqlens_q,
+                                   const int32_t *cu_seqlens_k, const int32_t *seqlens_k);
+
 /* ---- Norm and rotation of queries and keys ---------------------------------------
  *
  * What an attention layer does to the heads of Q and K before the attention, in

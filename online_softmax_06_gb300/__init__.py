@@ -17,12 +17,14 @@ Raw C-ABI names (same names, same argument order, ints and pointers only):
 ``fa_attention_host_workspace_bytes``,
 ``fa_kv4_page_bytes``, ``fa_kv4_append``, ``fa_kv4_read``,
 ``fa_attention_kv4``, ``fa_attention_kv4_workspace_bytes``,
+``fa_attention_window_fwd``,
 ``fa_qk_norm_rope_fwd``, ``fa_qk_norm_rope_bwd``, ``fa_qk_norm_rope_bwd_workspace_bytes``,
 ``fa_set_stream``, ``fa_get_stream``, ``fa_get_device_error``, ``fa_strerror``,
 ``fa_version``, ``fa_debug_expire_next_wait``.
 Tensor-level helpers: :func:`softmax_rows`, :func:`attention_fwd`,
 :func:`attention_fwd_splitkv`, :func:`attention_bwd`, :func:`attention_fwd_fp8`,
 :func:`kv4_cache`, :func:`kv4_append`, :func:`kv4_read`, :func:`attention_kv4`,
+:func:`attention_window_fwd`,
 :func:`qk_norm_rope_fwd`, :func:`qk_norm_rope_bwd`.
 """
 from __future__ import annotations
@@ -118,6 +120,8 @@ def lib():
                                        i64, i32, i32, i32, i32, i32, f32, i32, vp, i64]
         L.fa_attention_kv4_workspace_bytes.argtypes = [i32, i32, i64, i32, i32, i32, i32]
         L.fa_attention_kv4_workspace_bytes.restype = i64
+        L.fa_attention_window_fwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i32, i32, i64, i32,
+                                              i64, i32, i32, i32, f32, i32, i32, vp, vp, vp]
         L.fa_qk_norm_rope_fwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, i64,
                                           i32, i32, i32, i32, i32, f32]
         L.fa_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp,
@@ -141,7 +145,7 @@ def lib():
                      "fa_attention_fwd_splitkv_varlen",
                      "fa_attention_fwd_fp8", "fa_attention_fwd_fp8_varlen",
                      "fa_attention_fwd_host", "fa_kv4_append", "fa_kv4_read",
-                     "fa_attention_kv4", "fa_qk_norm_rope_fwd", "fa_qk_norm_rope_bwd",
+                     "fa_attention_kv4", "fa_attention_window_fwd", "fa_qk_norm_rope_fwd", "fa_qk_norm_rope_bwd",
                      "fa_set_stream", "fa_get_device_error", "fa_version",
                      "fa_debug_expire_next_wait"):
             getattr(L, name).restype = ctypes.c_int
@@ -292,6 +296,14 @@ def fa_attention_kv4(q, q_stride, cache, num_pages, page_size, page_table, max_p
 
 def fa_attention_kv4_workspace_bytes(B, Nq, total_q, Nk, H, Hkv, d) -> int:
     return lib().fa_attention_kv4_workspace_bytes(B, Nq, total_q, Nk, H, Hkv, d)
+
+
+def fa_attention_window_fwd(q, q_stride, k, k_stride, v, v_stride, o, lse, B, Nq, total_q, Nk,
+                            total_k, H, Hkv, d, scale, window, sinks, cu_seqlens_q, cu_seqlens_k,
+                            seqlens_k) -> int:
+    return lib().fa_attention_window_fwd(q, q_stride, k, k_stride, v, v_stride, o, lse, B, Nq,
+                                         total_q, Nk, total_k, H, Hkv, d, scale, window, sinks,
+                                         cu_seqlens_q, cu_seqlens_k, seqlens_k)
 
 
 def fa_qk_norm_rope_fwd(q, q_stride, k, k_stride, q_weight, k_weight, inv_freq, positions, qo,
@@ -896,6 +908,87 @@ def attention_kv4(q, cache, page_table, seqlens, max_seqlen: int | None = None, 
     return out, lse
 
 
+# ---- attention with a sliding window and sinks --------------------------------------
+
+def _window_check(torch, rows, ints):
+    """Types, devices and contiguity; returns the device's index."""
+    index = rows[0].get_device()
+    if index < 0:
+        raise ValueError("q, k and v must be CUDA tensors")
+    for t in rows:
+        if t.dtype is not torch.bfloat16 or t.get_device() != index:
+            raise ValueError("q, k, v and tensors like them must be bf16 and on one device")
+    for t in ints:
+        if t is not None and (t.dtype is not torch.int32 or t.get_device() != index
+                              or not t.is_contiguous() or t.dim() != 1):
+            raise ValueError("cu_seqlens and seqlens must be contiguous int32 tensors, one "
+                             "dimension, on q's device")
+    return index
+
+
+def _plan_window(q, qs, k, ks, v, vs, cu_q, cu_k, seqlens, max_q, max_k):
+    if k != v:
+        raise ValueError("k and v must have one shape")
+    if len(q) != (4 if cu_q is None else 3):
+        raise ValueError("q must be [B, Nq, H, d], or [total, H, d] with cu_seqlens_q")
+    if len(k) != (4 if cu_k is None else 3):
+        raise ValueError("k and v must be [B, Nk, kv_heads, d], or [total, kv_heads, d] with "
+                         "cu_seqlens_k")
+    H, d = q[-2:]
+    hkv = k[-2]
+    if k[-1] != d:
+        raise ValueError("q, k and v must have one head dimension")
+    if hkv == 0 or H % hkv:
+        raise ValueError(f"{H} query heads on {hkv} kv heads")
+    B = q[0] if cu_q is None else cu_q[0] - 1
+    if B < 0 or any(n is not None and n != B + 1 for n in
+                    (cu_k and cu_k[0], seqlens and seqlens[0] + 1, None if cu_k else k[0] + 1)):
+        raise ValueError(f"k, cu_seqlens_k and seqlens_k must be of q's {B} sequences")
+    total_q, total_k = (t[0] if len(t) == 3 else t[0] * t[1] for t in (q, k))
+    Nq = q[1] if cu_q is None else total_q if max_q is None else int(max_q)
+    Nk = k[1] if cu_k is None else total_k if max_k is None else int(max_k)
+    return (_row_stride(q, qs, "q"), _row_stride(k, ks, "k"), _row_stride(v, vs, "v"), B, Nq,
+            total_q, Nk, total_k, H, hkv, d, (B, H, Nq) if cu_q is None else (H, total_q))
+
+
+def attention_window_fwd(q, k, v, window: int, sinks: int = 0, scale: float | None = None,
+                         cu_seqlens_q=None, cu_seqlens_k=None, seqlens_k=None,
+                         max_q: int | None = None, max_k: int | None = None, out=None, lse=None):
+    """Attention with a sliding window and sinks: query i of the n of a sequence of L keys, at
+    p = i + L - n, sees key j iff j <= p and (j > p - window or j < sinks).
+
+    q: bf16 [B, Nq, H, d] -> (O [B, Nq, H, d], lse [B, H, Nq] fp32), or packed [total, H, d] with
+    ``cu_seqlens_q`` (int32 [B+1]) and ``max_q`` (the most queries of a sequence; default: total)
+    -> (O [total, H, d], lse [H, total]).  k, v: [B, Nk, kv_heads, d], or packed [total, kv_heads,
+    d] with ``cu_seqlens_k`` and ``max_k``; H is a multiple of kv_heads.  ``seqlens_k`` int32 [B]:
+    how many of a sequence's rows hold keys (a cache with room for more; default: all).  A token's
+    heads are contiguous, tokens may be any multiple of 8 elements apart.
+    """
+    import torch
+    index = _window_check(torch, (q, k, v), (cu_seqlens_q, cu_seqlens_k, seqlens_k))
+    key = (q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
+           None if cu_seqlens_q is None else cu_seqlens_q.shape,
+           None if cu_seqlens_k is None else cu_seqlens_k.shape,
+           None if seqlens_k is None else seqlens_k.shape, max_q, max_k)
+    (qs, ks, vs, B, Nq, total_q, Nk, total_k, H, hkv, d,
+     lse_shape) = _kv4_plan(key, _plan_window, *key)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    elif not (out.shape == q.shape and out.dtype is torch.bfloat16 and out.get_device() == index
+              and out.is_contiguous()):
+        raise ValueError("out must be a contiguous tensor like q")
+    if lse is None:
+        lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+    elif not (tuple(lse.shape) == lse_shape and lse.dtype is torch.float32
+              and lse.get_device() == index and lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 tensor {list(lse_shape)}")
+    _kv4_call(torch, index, "fa_attention_window_fwd", q.data_ptr(), qs, k.data_ptr(), ks,
+              v.data_ptr(), vs, out.data_ptr(), lse.data_ptr(), B, Nq, total_q, Nk, total_k, H, hkv,
+              d, 1.0 / math.sqrt(d) if scale is None else scale, window, sinks, _ptr(cu_seqlens_q),
+              _ptr(cu_seqlens_k), _ptr(seqlens_k))
+    return out, lse
+
+
 # ---- norm and rotation of queries and keys ----------------------------------------
 
 def _plan_norm_rope(shapes, strides, w_shapes, pos, freq):
@@ -1010,6 +1103,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, inv_fre
 
 
 __all__ = [
+    "attention_window_fwd", "fa_attention_window_fwd",
     "qk_norm_rope_fwd", "qk_norm_rope_bwd", "fa_qk_norm_rope_fwd", "fa_qk_norm_rope_bwd",
     "fa_qk_norm_rope_bwd_workspace_bytes",
     "attention_kv4", "kv4_cache", "kv4_append", "kv4_read", "fa_attention_kv4",

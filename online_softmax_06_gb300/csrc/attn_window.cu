@@ -1,0 +1,589 @@
+// attn_window.cu -- attention with a sliding window and sinks, forward, for many
+// queries (chunks of prompts, training), on the sm_103a tensor cores.
+//
+// What it computes: O = softmax(scale Q K^T | seen keys) V and the row logsumexp,
+// with the online softmax over tiles of 128 keys, as attn_bf16.cu does.  What the
+// window changes:
+//   * a CTA's keys are the window of its queries and the sinks, laid one behind
+//     the other (window.cuh), so that few sinks share a tile with the window's
+//     first keys instead of taking a tile of their own; the window starts at any
+//     row, tiles need no alignment to multiples of 128;
+//   * the tiles are few (window 1024: nine), so rows that do not see the same keys
+//     cost: the rows of a tile are the queries of the G query heads that share a kv
+//     head, row r = query r / G, head r % G, and the two tiles of a CTA follow one
+//     another in the sequence: 256 rows span 256 / G positions and see window + 256
+//     / G keys at most;
+//   * a row's mask is two ranges of columns, formed as bits 32 columns at a time.
+// Roles, tensor memory and the order of the products are those of attn_bf16.cu: a
+// CTA per SM; warps 0-3 and 4-7 the softmax of Q0 and Q1, a thread per row; warp 8
+// TMA, warp 9 tcgen05.  S0 [0, 128), S1 [128, 256), O0 and O1 from 256; P in bf16
+// over the upper half of S: probabilities relative to a reference that at most 2^8
+// below the row's maximum, each off by 2^-9 relative, and the sum that divides O
+// is corrected by the error of the tile's largest.
+// Rows of V behind a sequence's keys (the room of a cache, the next sequence) are
+// zeroed in shared memory before the product reads them: their P is 0, but they may
+// hold NaN.  Every wait is bounded; a timed-out one leaves the CTA's rows unwritten.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/fa.h"
+#include "fa_error.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+#include "window.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int BM = 128, BN = 128;
+constexpr int kPad = 32;               // sinks fill whole pieces of a tile
+constexpr int kThreads = 320;
+constexpr int kWarpLoad = 8, kWarpMma = 9;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColPinS = 64;
+constexpr uint32_t kChunkBytes = BM * 128;   // 128 rows of 64 bf16
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kRescaleLog2 = 8.f;
+
+__device__ __forceinline__ uint32_t col_s(int t) { return uint32_t(t) * 128u; }
+template <int D>
+__device__ __forceinline__ uint32_t col_o(int t) { return 256u + uint32_t(t) * D; }
+
+template <int D>
+struct Cfg {
+    static constexpr int kChunks = D / 64;
+    static constexpr uint32_t kTileBytes = BM * D * 2;
+    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr uint32_t kOffRing = 2 * kTileBytes;       // [Q0][Q1][ring][barriers]
+    static constexpr uint32_t kOffBar = kOffRing + kStages * kTileBytes;
+    static constexpr uint32_t kBars = 2 + 2 * kStages + 2 + 2 + 2 + 1 + 1;
+    static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16 + 1024;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+struct Params {
+    CUtensorMap tm_q, tm_o;            // box {64, G, 1, P}
+    CUtensorMap tm_k, tm_v;            // box {64, 1, 1, 128}
+    CUtensorMap tm_k32, tm_v32;        // box {64, 1, 1, 32}: the tile where the sinks end
+    WindowArgs a;
+    int G, P;                          // heads of a kv head; queries of a tile
+    int n_pairs;
+    float scale_log2;
+};
+
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t it = 0; it < kWaitMaxPolls; ++it) {
+        if (ptx::mbar_try_wait(bar, parity))
+            return;
+        if ((it & 255u) == 255u && ptx::globaltimer() - t0 > kWaitTimeoutNs)
+            return;
+    }
+}
+
+// The lowest `n` bits, n clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t low_bits(int n)
+{
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_constant__ Params p)
+{
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    uint64_t *q_full = bars, *kv_full = bars + 2, *kv_empty = kv_full + C::kStages;
+    uint64_t *s_full = kv_empty + C::kStages, *p_full = s_full + 2, *o_full = s_full + 4;
+    uint64_t *drain = s_full + 6, *never = s_full + 7;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    // nothing that a kernel before may still be writing is read ahead of this
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // ---- work item: the last pairs of a sequence first (early ones see less) ------
+    const WindowArgs &a = p.a;
+    const int pair = p.n_pairs - 1 - int(blockIdx.x % unsigned(p.n_pairs));
+    const int bh = int(blockIdx.x / unsigned(p.n_pairs));
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    WindowSeq sq;
+    if (!window_seq(a, b, sq)) {
+        if (threadIdx.x == 0 && pair == 0 && hk == 0)
+            record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
+        return;
+    }
+    const int i0 = pair * 2 * p.P;             // first query of the pair
+    if (i0 >= sq.n)
+        return;
+    const int off = sq.L - sq.n;
+    const bool has_q1 = i0 + p.P < sq.n;
+    const int i1 = min(i0 + p.P, sq.n), i2 = min(i0 + 2 * p.P, sq.n);
+    const WindowKeys w = window_keys(a.window, a.sinks, i0, i2, off, kPad);
+    // tile t takes steps [first_t, last_t) of the places' tiles: Q0 those that its
+    // own last query reaches, Q1 all but leading ones that are behind its window
+    const int n_steps = (w.places + BN - 1) / BN;
+    const int reach0 = w.places - (i2 - i1);
+    const int last0 = reach0 > w.sp ? (reach0 + BN - 1) / BN : 0;
+    const int first1 = a.sinks == 0 && w.lo > 0 ? p.P / BN : 0;
+    const int last1 = has_q1 ? n_steps : 0;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(&q_full[t], 1);
+            ptx::mbar_init(&s_full[t], 1);
+            ptx::mbar_init(&p_full[t], 128);
+            ptx::mbar_init(&o_full[t], 1);
+        }
+        for (int s = 0; s < C::kStages; ++s) {
+            ptx::mbar_init(&kv_full[s], 1);
+            ptx::mbar_init(&kv_empty[s], 1);
+        }
+        ptx::mbar_init(drain, 1);
+        ptx::mbar_init(never, 1);
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        ptx::tmem_alloc(tmem_slot, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    if (warp == kWarpLoad && lane == 0) {
+        ptx::prefetch_tmap(&p.tm_q);
+        ptx::prefetch_tmap(&p.tm_k);
+        ptx::prefetch_tmap(&p.tm_v);
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    bool aborted = false;
+    uint8_t *ring = smem + C::kOffRing;
+
+    if (warp == kWarpLoad) {
+        // ======================= TMA producer ==============================
+        if (lane == 0) {
+            int last_phase[C::kStages];
+            for (int s = 0; s < C::kStages; ++s)
+                last_phase[s] = -1;
+            bool q_issued[2] = {false, false};
+            auto load_q = [&](int t) {
+                q_issued[t] = true;
+                ptx::mbar_arrive_expect_tx(&q_full[t], C::kChunks * p.P * p.G * 128);
+                for (int c = 0; c < C::kChunks; ++c)
+                    ptx::tma_load_4d(smem + t * C::kTileBytes + c * kChunkBytes, &p.tm_q,
+                                     &q_full[t], c * 64, 0, hk, int(sq.q0 + (t ? i1 : i0)));
+            };
+            if (last0 > 0)
+                load_q(0);
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int j = 0; j < n_steps && !aborted; ++j) {
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (!ptx::mbar_wait(&kv_empty[stage], phase ^ 1u, abort_flag, a.err_word)) {
+                        aborted = true;
+                        break;
+                    }
+                    ptx::mbar_arrive_expect_tx(&kv_full[stage], C::kTileBytes);
+                    uint8_t *dst = ring + stage * C::kTileBytes;
+                    const int v0 = j * BN;
+                    if (v0 < w.sp && v0 + BN > w.sp) {
+                        for (int q = 0; q < BN / kPad; ++q) {
+                            const int v = v0 + q * kPad;
+                            const int64_t row = sq.k0 + (v < w.sp ? v : w.lo + v - w.sp);
+                            for (int c = 0; c < C::kChunks; ++c)
+                                ptx::tma_load_4d(dst + c * kChunkBytes + q * kPad * 128,
+                                                 kv ? &p.tm_v32 : &p.tm_k32, &kv_full[stage],
+                                                 c * 64, 0, hk, int(row));
+                        }
+                    } else {
+                        const int64_t row = sq.k0 + (v0 < w.sp ? v0 : w.lo + v0 - w.sp);
+                        for (int c = 0; c < C::kChunks; ++c)
+                            ptx::tma_load_4d(dst + c * kChunkBytes, kv ? &p.tm_v : &p.tm_k,
+                                             &kv_full[stage], c * 64, 0, hk, int(row));
+                    }
+                    last_phase[stage] = int(phase);
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (j == 0 && kv == 0 && last1 > 0)
+                        load_q(1);
+                }
+            }
+            if (aborted || *abort_flag) {
+                // copies already issued land before the CTA goes away
+                for (int t = 0; t < 2; ++t)
+                    if (q_issued[t])
+                        drain_wait(&q_full[t], 0);
+                for (int s = 0; s < C::kStages; ++s)
+                    if (last_phase[s] >= 0)
+                        drain_wait(&kv_full[s], uint32_t(last_phase[s]));
+            }
+        }
+        __syncwarp();
+    } else if (warp == kWarpMma) {
+        // ======================= MMA issuer (whole warp) =====================
+        constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(BM, BN, false);
+        constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(BM, D, true);
+        constexpr uint64_t desc_kmajor = ptx::smem_desc_base(16, 1024);
+        constexpr uint64_t desc_mnmajor = ptx::smem_desc_base(kChunkBytes, 1024);
+        const uint32_t ring_addr = ptx::smem_u32(ring), q_addr = ptx::smem_u32(smem);
+        auto issue_qk = [&](int t, int st) {
+            const uint64_t dq = ptx::smem_desc(desc_kmajor, q_addr + t * C::kTileBytes);
+            const uint64_t dk = ptx::smem_desc(desc_kmajor, ring_addr + st * C::kTileBytes);
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t o = ((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4;
+                    ptx::mma_ss(tmem + col_s(t), dq + o, dk + o, idesc_qk, kk > 0 ? 1u : 0u);
+                }
+                ptx::mma_commit(&s_full[t]);
+            }
+            __syncwarp();
+        };
+        auto issue_pv = [&](int t, int st, bool accumulate, bool last) {
+            const uint64_t dv = ptx::smem_desc(desc_mnmajor, ring_addr + st * C::kTileBytes);
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    ptx::mma_ts(tmem + col_o<D>(t), tmem + col_s(t) + kColPinS + kk * 8,
+                                dv + uint64_t((kk * 16 * 128) >> 4), idesc_pv,
+                                (accumulate || kk > 0) ? 1u : 0u);
+                if (last)
+                    ptx::mma_commit(&o_full[t]);
+            }
+            __syncwarp();
+        };
+        auto release = [&](int st) {
+            if (ptx::elect_one())
+                ptx::mma_commit(&kv_empty[st]);
+            __syncwarp();
+        };
+        int stage = 0;
+        uint32_t phase = 0;
+        // waits for the next ring stage and returns it (-1: gave up)
+        auto next_stage = [&]() -> int {
+            if (!ptx::mbar_wait_warp(&kv_full[stage], phase, abort_flag, a.err_word))
+                return -1;
+            const int st = stage;
+            if (++stage == C::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            return st;
+        };
+        // V's rows of step j behind the sequence's keys are cleared
+        const int end_place = w.sp + (sq.L - w.lo);
+        auto clear_tail = [&](int j, int st) {
+            const int r0 = end_place - j * BN;
+            if (r0 >= BN)
+                return;
+            uint8_t *v = ring + st * C::kTileBytes;
+            for (int r = max(r0, 0) + (lane >> 3); r < BN; r += 4)
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c)
+                    *reinterpret_cast<uint4 *>(v + c * kChunkBytes + r * 128 + (lane & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+        };
+        if (a.expire_wait_ns != 0u &&
+            !__all_sync(0xffffffffu, ptx::mbar_wait_limited(never, 0, abort_flag, a.err_word,
+                                                            a.expire_wait_ns)))
+            aborted = true;
+        const int first[2] = {0, first1}, last[2] = {last0, last1};
+        auto has = [&](int t, int j) { return j >= first[t] && j < last[t]; };
+        bool q_ready[2] = {false, false};
+        auto wait_q = [&](int t) -> bool {
+            if (!q_ready[t])
+                q_ready[t] = ptx::mbar_wait_warp(&q_full[t], 0, abort_flag, a.err_word);
+            return q_ready[t];
+        };
+        do {
+            if (aborted || n_steps == 0)
+                break;
+            aborted = true;                        // until the loop is through
+            int k_st = next_stage();
+            if (k_st < 0)
+                break;
+            if ((has(0, 0) && !wait_q(0)))
+                break;
+            ptx::tc_fence_after_sync();
+            if (has(0, 0))
+                issue_qk(0, k_st);
+            if (has(1, 0)) {
+                if (!wait_q(1))
+                    break;
+                ptx::tc_fence_after_sync();
+                issue_qk(1, k_st);
+            }
+            release(k_st);
+            int j = 0;
+            for (; j < n_steps; ++j) {
+                const int v_st = next_stage();
+                if (v_st < 0)
+                    break;
+                clear_tail(j, v_st);
+                if (has(0, j)) {
+                    if (!ptx::mbar_wait_warp(&p_full[0], uint32_t(j) & 1u, abort_flag, a.err_word))
+                        break;
+                    ptx::tc_fence_after_sync();
+                    issue_pv(0, v_st, j > 0, j == last0 - 1);
+                }
+                const bool more = j + 1 < n_steps;
+                if (more) {
+                    if ((k_st = next_stage()) < 0)
+                        break;
+                    ptx::tc_fence_after_sync();
+                    if (has(0, j + 1))
+                        issue_qk(0, k_st);
+                }
+                if (has(1, j)) {
+                    if (!ptx::mbar_wait_warp(&p_full[1], uint32_t(j - first1) & 1u, abort_flag,
+                                             a.err_word))
+                        break;
+                    ptx::tc_fence_after_sync();
+                    issue_pv(1, v_st, j > first1, j == last1 - 1);
+                }
+                release(v_st);
+                if (more) {
+                    if (has(1, j + 1)) {
+                        if (!wait_q(1))
+                            break;
+                        ptx::tc_fence_after_sync();
+                        issue_qk(1, k_st);
+                    }
+                    release(k_st);
+                }
+            }
+            aborted = j < n_steps;
+        } while (false);
+        // every product issued above is through once this commit arrives
+        if (ptx::elect_one()) {
+            ptx::mma_commit(drain);
+            drain_wait(drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ======================= softmax warpgroups ========================
+        const int t = warp >> 2;
+        const int r = threadIdx.x & 127;               // row of the tile = TMEM lane
+        const int j0 = t ? first1 : 0, j1 = t ? last1 : last0;
+        const int qi = r / p.G, i = (t ? i1 : i0) + qi;   // query, head of the kv head
+        const int h = hk * p.G + r % p.G;
+        const bool row_ok = qi < p.P && i < (t ? i2 : i1);
+        const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_bits + col_s(t);
+        const uint32_t tO = tmem + lane_bits + col_o<D>(t);
+        const int vhi = row_ok ? i + off - w.lo + w.sp : -1;
+        const int64_t vl = int64_t(vhi) - a.window + 1;
+        const int vlo = vl > w.sp ? int(vl) : w.sp;
+        const float sl = p.scale_log2;
+        float m = -INFINITY;                           // reference, log2 units
+        float l = 0.f;                                 // running sum (lse)
+        float l_o = 0.f;                               // the sum that divides O (see above)
+
+        for (int j = j0; j < j1; ++j) {
+            if (!ptx::mbar_wait(&s_full[t], uint32_t(j - j0) & 1u, abort_flag, a.err_word)) {
+                aborted = true;
+                break;
+            }
+            ptx::tc_fence_after_sync();
+            uint32_t sr[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                ptx::tmem_ld32(tS + c * 32, sr[c]);
+            ptx::tmem_wait_ld();
+            const int v0 = j * BN;
+            if (__any_sync(0xffffffffu, v0 < vlo || v0 + BN - 1 > vhi)) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int vc = v0 + 32 * c;
+                    const uint32_t seen = low_bits(vhi - vc + 1) &
+                                          (~low_bits(vlo - vc) | low_bits(a.sinks - vc));
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!(seen & (1u << e)))
+                            sr[c][e] = __float_as_uint(-INFINITY);
+                }
+            }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int c = q * 8 + 2 * k;
+                    m4[k] = ptx::max3(m4[k], __uint_as_float(sr[c >> 5][c & 31]),
+                                      __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
+                }
+            const float mx = fmaxf(ptx::max3(m4[0], m4[1], m4[2]), m4[3]);
+            const float mt = mx * sl;
+            const bool grew = mt > m + kRescaleLog2;
+            const float m_new = grew ? mt : m;
+            const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+            const float corr = grew ? ptx::ex2(m - m_use) : 1.f;
+
+            const uint32_t tP = tS + kColPinS;
+            const float2 sl2 = make_float2(sl, sl);
+            const float2 nm2 = make_float2(-m_use, -m_use);
+            float2 rowsum2 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const int col = half * 64 + 2 * e;
+                    const float2 sv = make_float2(__uint_as_float(sr[col >> 5][col & 31]),
+                                                  __uint_as_float(sr[(col + 1) >> 5][(col + 1) & 31]));
+                    const float2 arg = __ffma2_rn(sv, sl2, nm2);
+                    const float p0 = ptx::ex2(arg.x), p1 = ptx::ex2(arg.y);
+                    rowsum2 = __fadd2_rn(rowsum2, make_float2(p0, p1));
+                    pk[e] = ptx::pack_bf16x2(p0, p1);
+                }
+                ptx::tmem_st32(tP + half * 32, pk);
+            }
+            // O's row moves to the new reference (never in the first step: its product
+            // overwrites O); a warp goes together
+            if (j > j0 && __any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    ptx::tmem_ld32(tO + c * 32, o);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                    ptx::tmem_st32(tO + c * 32, o);
+                }
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before_sync();
+            ptx::mbar_arrive(&p_full[t]);
+
+            const float tile_sum = rowsum2.x + rowsum2.y;
+            l = l * corr + tile_sum;
+            // the tile's largest probability as the loop formed it, and in bf16
+            const float p_top = ptx::ex2(fmaf(mx, sl, -m_use));
+            const float p_top_bf16 = __uint_as_float(ptx::pack_bf16x2(p_top, 0.f) << 16);
+            l_o = l_o * corr + (tile_sum + (p_top_bf16 - p_top));
+            m = m_new;
+        }
+
+        // ---- epilogue ------------------------------------------------------------
+        const int rows_t = t ? i2 - i1 : i1 - i0;      // queries of the tile
+        if (rows_t > 0) {
+            const bool full_tile = rows_t == p.P;
+            const bool work = j1 > j0;                 // else O was never formed: zeros
+            const bool ok = !aborted &&
+                            (!work || ptx::mbar_wait(&o_full[t], 0, abort_flag, a.err_word));
+            uint8_t *o_stage = smem + t * C::kTileBytes;
+            if (ok) {
+                ptx::tc_fence_after_sync();
+                // a row that sees no key: zeros (a NaN keeps its way)
+                const float inv = l == 0.f ? 0.f : 1.f / l_o;
+                __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(a.O) +
+                                      ((sq.q0 + i) * a.H + h) * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (work) {
+                        ptx::tmem_ld32(tO + c * 32, o);
+                        ptx::tmem_wait_ld();
+                    }
+                    uint4 v[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            u[e] = work && l != 0.f
+                                       ? ptx::pack_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv,
+                                                          __uint_as_float(o[8 * q + 2 * e + 1]) * inv)
+                                       : 0u;
+                        v[q] = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                    if (full_tile) {
+                        uint8_t *rowp = o_stage + (c >> 1) * kChunkBytes + r * 128;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int u = (c & 1) * 4 + q;
+                            *reinterpret_cast<uint4 *>(rowp + ((u ^ (r & 7)) << 4)) = v[q];
+                        }
+                    } else if (row_ok) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(orow + c * 32);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            dst[q] = v[q];
+                    }
+                }
+                if (row_ok) {
+                    const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                    a.lse[a.cu_seqlens_q != nullptr ? int64_t(h) * a.total_q + sq.q0 + i
+                                                    : (int64_t(b) * a.H + h) * a.Nq + i] = lse;
+                }
+            }
+            if (full_tile) {
+                ptx::fence_proxy_async_smem();
+                // the store goes out only if all 128 threads are through
+                if (!ptx::bar_red_or(1 + t, 128, !ok) && r == 0) {
+                    for (int c = 0; c < C::kChunks; ++c)
+                        ptx::tma_store_4d(&p.tm_o, o_stage + c * kChunkBytes, c * 64, 0, hk,
+                                          int(sq.q0 + (t ? i1 : i0)));
+                    ptx::bulk_commit_and_wait_read();
+                }
+            }
+        }
+    }
+
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    if (warp == kWarpMma)
+        ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D>
+int launch_d(const Params &p, int64_t blocks, cudaStream_t stream)
+{
+    auto kern = attn_window_kernel<D>;
+    static PerDeviceOnce once;
+    constexpr int smem = int(Cfg<D>::kSmemBytes);
+    if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(kern), smem))
+        return FA_ERR_CUDA;
+    return launch_early(kern, dim3(unsigned(blocks)), kThreads, smem, stream, p) == cudaSuccess
+               ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_attention_window(const WindowArgs &a, cudaStream_t stream)
+{
+    Params p;
+    p.a = a;
+    p.G = a.H / a.Hkv;
+    p.P = BM / p.G;
+    p.n_pairs = (a.Nq + 2 * p.P - 1) / (2 * p.P);
+    p.scale_log2 = float(double(a.scale) * 1.4426950408889634);
+    const int64_t blocks = int64_t(p.n_pairs) * a.B * a.Hkv;
+    if (blocks > 0x7fffffffLL)
+        return FA_ERR_TOO_LARGE;
+    if (!make_tmap_heads(&p.tm_q, a.Q, a.total_q, a.Hkv, p.G, a.d, a.q_stride, p.P) ||
+        !make_tmap_heads(&p.tm_o, a.O, a.total_q, a.Hkv, p.G, a.d, int64_t(a.H) * a.d, p.P) ||
+        !make_tmap_heads(&p.tm_k, a.K, a.total_k, a.Hkv, 1, a.d, a.k_stride, BN) ||
+        !make_tmap_heads(&p.tm_v, a.V, a.total_k, a.Hkv, 1, a.d, a.v_stride, BN) ||
+        !make_tmap_heads(&p.tm_k32, a.K, a.total_k, a.Hkv, 1, a.d, a.k_stride, kPad) ||
+        !make_tmap_heads(&p.tm_v32, a.V, a.total_k, a.Hkv, 1, a.d, a.v_stride, kPad))
+        return FA_ERR_CUDA;
+    return a.d == 64 ? launch_d<64>(p, blocks, stream) : launch_d<128>(p, blocks, stream);
+}
+
+}  // namespace fa

@@ -1070,6 +1070,100 @@ int fa_qk_norm_rope_bwd(const void *Q, int64_t q_stride, const void *K, int64_t 
     return fa::launch_norm_rope_bwd(a, fa::t_stream);
 }
 
+}  // extern "C"
+
+namespace fa {
+namespace {
+// What the window attention and its gradient check alike; fills a.  Sets *empty where
+// there is no query.
+int check_window(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, const void *V,
+                 int64_t v_stride, const void *O, const float *lse, int B, int Nq, int64_t total_q,
+                 int Nk, int64_t total_k, int H, int Hkv, int d, float scale, int window,
+                 int sinks, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                 const int32_t *seqlens_k, WindowArgs *a, bool *empty)
+{
+    *empty = false;
+    if (B < 0 || Nq < 0 || total_q < 0 || Nk < 0 || total_k < 0 || H < 0 || window < 1 ||
+        sinks < 0 || (H > 0 && (Hkv < 1 || H % Hkv != 0)) ||
+        !(scale > 0.f && scale <= 3.0e38f) ||
+        (cu_seqlens_q == nullptr && total_q != int64_t(B) * Nq) ||
+        (cu_seqlens_k == nullptr && total_k != int64_t(B) * Nk))
+        return FA_ERR_BAD_SIZE;
+    if (d != 64 && d != 128)
+        return FA_ERR_UNSUPPORTED;
+    if (B == 0 || Nq == 0 || total_q == 0 || H == 0) {
+        *empty = true;
+        return FA_OK;
+    }
+    if (H / Hkv > 128)
+        return FA_ERR_UNSUPPORTED;
+    if (!Q || !O || !lse || (total_k > 0 && (!K || !V)))
+        return FA_ERR_NULL_POINTER;
+    if (q_stride < int64_t(H) * d ||
+        (total_k > 0 && (k_stride < int64_t(Hkv) * d || v_stride < int64_t(Hkv) * d)))
+        return FA_ERR_BAD_SIZE;
+    if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(O, 16) ||
+        !aligned(lse, 4) || !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) ||
+        !aligned(seqlens_k, 4) || q_stride % 8 != 0 ||
+        (total_k > 0 && (k_stride % 8 != 0 || v_stride % 8 != 0)))
+        return FA_ERR_MISALIGNED;
+    const int64_t limit = (int64_t(1) << 31) - 512;
+    if (total_q > limit || total_k > limit || Nq > limit || Nk > limit || q_stride > limit ||
+        k_stride > limit || v_stride > limit || H > 65535)
+        return FA_ERR_TOO_LARGE;
+    a->Q = Q;
+    a->q_stride = q_stride;
+    // without a key nothing of K and V is read; their maps need some address
+    a->K = total_k > 0 ? K : Q;
+    a->V = total_k > 0 ? V : Q;
+    a->k_stride = total_k > 0 ? k_stride : q_stride;
+    a->v_stride = total_k > 0 ? v_stride : q_stride;
+    a->O = const_cast<void *>(O);          // written by the forward alone
+    a->lse = const_cast<float *>(lse);
+    a->B = B;
+    a->Nq = Nq < total_q ? Nq : int(total_q);
+    a->Nk = Nk;
+    a->total_q = total_q;
+    a->total_k = total_k;
+    a->H = H;
+    a->Hkv = Hkv;
+    a->d = d;
+    a->scale = scale;
+    a->window = window;
+    a->sinks = sinks;
+    a->cu_seqlens_q = cu_seqlens_q;
+    a->cu_seqlens_k = cu_seqlens_k;
+    a->seqlens_k = seqlens_k;
+    a->expire_wait_ns = 0;
+    return FA_OK;
+}
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+int fa_attention_window_fwd(const void *Q, int64_t q_stride, const void *K, int64_t k_stride,
+                            const void *V, int64_t v_stride, void *O, float *lse, int B, int Nq,
+                            int64_t total_q, int Nk, int64_t total_k, int H, int Hkv, int d,
+                            float scale, int window, int sinks, const int32_t *cu_seqlens_q,
+                            const int32_t *cu_seqlens_k, const int32_t *seqlens_k)
+{
+    fa::WindowArgs a;
+    bool empty;
+    const int rc = fa::check_window(Q, q_stride, K, k_stride, V, v_stride, O, lse, B, Nq, total_q,
+                                    Nk, total_k, H, Hkv, d, scale, window, sinks, cu_seqlens_q,
+                                    cu_seqlens_k, seqlens_k, &a, &empty);
+    if (rc != FA_OK || empty)
+        return rc;
+    fa::DeviceInfo *dev = fa::current_device();
+    if (dev == nullptr)
+        return FA_ERR_NO_DEVICE;
+    a.err_word = dev->err_word;
+    a.expire_wait_ns = fa::t_expire_wait_ns;
+    fa::t_expire_wait_ns = 0;
+    return fa::launch_attention_window(a, fa::t_stream);
+}
+
 int fa_attention_fwd_f32(const float *Q, const float *K, const float *V, float *O, float *lse,
                          int B, int H, int N, int d, float scale, int causal,
                          const int32_t *cu_seqlens)

@@ -83,6 +83,12 @@ int choose_num_splits(int B, int H, int N, int Nk);
 bool make_tmap_bf16(CUtensorMap *tm, const void *base, int64_t total, int H, int d,
                     int box_rows = 128, int H_row = 0);
 
+// 4-D TMA map over rows of heads * group * d bf16 values, `stride` elements apart:
+// box = 64 values (the 128-byte swizzle span) x the `group` heads of one of `heads`
+// groups x box_rows rows.  Rows past `rows` read as zero and are not stored.
+bool make_tmap_heads(CUtensorMap *tm, const void *base, int64_t rows, int heads, int group, int d,
+                     int64_t stride, int box_rows);
+
 // TMA maps over the FP8 forward's e4m3 tensors: rows of Q' / K' ([total, H, d]
 // bytes, box d x 1 x 128, d = 128 so a row is one 128-byte swizzle span) and
 // the transposed V' ([rows = B*H*d, n_pad] bytes, box 128 keys x d rows).
@@ -330,6 +336,25 @@ inline int64_t kv4_attention_workspace_bytes(int B, int Nq, int64_t total_q, int
 }
 int launch_attention_kv4_many(const Kv4AttnArgs &a, cudaStream_t stream);
 int launch_attention_kv4(const Kv4AttnArgs &a, cudaStream_t stream);
+
+// Attention with a sliding window and sinks (layouts as in fa.h).
+struct WindowArgs {
+    const void *Q, *K, *V;
+    int64_t q_stride, k_stride, v_stride;  // elements between rows
+    void *O;
+    float *lse;
+    int B, Nq, Nk;             // Nq, Nk: the most queries and keys of a sequence
+    int64_t total_q, total_k;
+    int H, Hkv, d;
+    float scale;
+    int window, sinks;
+    const int32_t *cu_seqlens_q;  // or nullptr: Nq queries each
+    const int32_t *cu_seqlens_k;  // or nullptr: rows b * Nk on
+    const int32_t *seqlens_k;     // or nullptr: all of a sequence's rows
+    int *err_word;
+    uint32_t expire_wait_ns;   // failure-detection test (fa_debug_expire_next_wait), or 0
+};
+int launch_attention_window(const WindowArgs &a, cudaStream_t stream);
 
 // Norm and rotation of the heads of Q (index 0) and K (1), and its gradient.
 struct NormRopeArgs {

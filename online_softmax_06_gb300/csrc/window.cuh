@@ -1,0 +1,77 @@
+// window.cuh -- what the kernels of the window attention share: a sequence's
+// rows, and the keys that a block of its queries sees.
+//
+// Query i of the n of a sequence of L keys sits at position p = i + L - n and
+// sees key j iff j <= p and (j > p - window or j < sinks).  The keys that the
+// queries i0 .. i1 - 1 see are two ranges, [0, sinks) and [lo, hi); they are
+// taken one behind the other, the sinks filled up to a multiple of `pad`, as
+// places v = 0, 1, ...: place v < sp is key v, another one key lo + v - sp.
+// Where the ranges meet (lo <= sp) they are one, [0, hi), and sp = 0.  A query
+// at p sees the places
+//     v <= vhi and (v >= vlo or v < sinks),
+//     vhi = p - lo + sp,  vlo = max(sp, vhi - window + 1).
+#pragma once
+
+#include <cstdint>
+
+#include "../../include/fa.h"
+#include "fa_error.cuh"
+#include "launch.h"
+
+namespace fa {
+
+struct WindowSeq {
+    int64_t q0, k0;            // first rows of Q and K
+    int n, L;                  // queries and keys
+};
+
+// False where the counts contradict the tensors.
+__device__ __forceinline__ bool window_seq(const WindowArgs &a, int b, WindowSeq &s)
+{
+    if (a.cu_seqlens_q != nullptr) {
+        const int64_t r0 = a.cu_seqlens_q[b], r1 = a.cu_seqlens_q[b + 1];
+        if (r0 < 0 || r1 < r0 || r1 > a.total_q || r1 - r0 > a.Nq)
+            return false;
+        s.q0 = r0;
+        s.n = int(r1 - r0);
+    } else {
+        s.q0 = int64_t(b) * a.Nq;
+        s.n = a.Nq;
+    }
+    int64_t room = a.Nk;
+    s.k0 = int64_t(b) * a.Nk;
+    if (a.cu_seqlens_k != nullptr) {
+        const int64_t r0 = a.cu_seqlens_k[b], r1 = a.cu_seqlens_k[b + 1];
+        if (r0 < 0 || r1 < r0 || r1 > a.total_k)
+            return false;
+        s.k0 = r0;
+        room = r1 - r0;
+    }
+    const int64_t L = a.seqlens_k != nullptr ? int64_t(a.seqlens_k[b]) : room;
+    if (L < 0 || L > room || L > a.Nk)
+        return false;
+    s.L = int(L);
+    return true;
+}
+
+struct WindowKeys {
+    int lo, sp, places;        // places = sp + hi - lo (0: the queries see no key)
+};
+
+// Of queries i0 .. i1 - 1 (i1 > i0).
+__device__ __forceinline__ WindowKeys window_keys(int window, int sinks, int i0, int i1, int off,
+                                                  int pad)
+{
+    WindowKeys w;
+    const int hi = i1 + off;   // <= L
+    const int64_t first = int64_t(i0) + off - window + 1;
+    w.lo = first > 0 ? int(first) : 0;
+    const int s = sinks < w.lo ? sinks : w.lo;
+    w.sp = (s + pad - 1) / pad * pad;
+    if (w.sp >= w.lo)
+        w.lo = w.sp = 0;
+    w.places = hi > 0 ? w.sp + hi - w.lo : 0;
+    return w;
+}
+
+}  // namespace fa

@@ -1,0 +1,60 @@
+"""Refusals of the window attention's C entry points: all return before any CUDA call (no GPU); and the
+oracle's gradient against differences of its forward."""
+import numpy as np
+import pytest
+
+import online_softmax_06_gb300 as fa
+from oracle import layer
+
+P = 0x1000   # an address that nothing reads
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    fa.build()
+
+
+def fwd(**kw):
+    a = dict(q=P, qs=512, k=P, ks=256, v=P, vs=256, o=P, lse=P, B=2, Nq=4, total_q=8, Nk=10, total_k=20, H=4, Hkv=2,
+             d=128, scale=0.1, window=8, sinks=2, cu_q=None, cu_k=None, sl=None)
+    a.update(kw)
+    return fa.fa_attention_window_fwd(*a.values())
+
+
+def test_forward_refusals():
+    for bad in (dict(B=-1), dict(Nq=-1), dict(total_q=9), dict(total_k=21), dict(window=0), dict(sinks=-1),
+                dict(H=5), dict(Hkv=0), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
+                dict(scale=float("inf")), dict(qs=504), dict(ks=248), dict(vs=128)):
+        assert fwd(**bad) == fa.FA_ERR_BAD_SIZE, bad
+    for bad in (dict(d=96), dict(H=258, qs=258 * 128)):
+        assert fwd(**bad) == fa.FA_ERR_UNSUPPORTED, bad
+    for bad in (dict(q=None), dict(k=None), dict(v=None), dict(o=None), dict(lse=None)):
+        assert fwd(**bad) == fa.FA_ERR_NULL_POINTER, bad
+    for bad in (dict(q=P + 8), dict(k=P + 2), dict(o=P + 4), dict(lse=P + 2), dict(cu_q=P + 1), dict(cu_k=P + 2),
+                dict(sl=P + 1), dict(qs=516), dict(ks=257)):
+        assert fwd(**bad) == fa.FA_ERR_MISALIGNED, bad
+    for bad in (dict(B=1, Nk=2 ** 31 - 1, total_k=2 ** 31 - 1, total_q=4), dict(qs=1 << 32)):
+        assert fwd(**bad) == fa.FA_ERR_TOO_LARGE, bad
+    assert fwd(B=0, total_q=0, total_k=0) == fa.FA_OK
+    assert fwd(Nq=0, total_q=0) == fa.FA_OK
+    assert fwd(H=0, Hkv=0) == fa.FA_OK
+
+
+def test_oracle_gradient():
+    rng = np.random.default_rng(0)
+    q, k, v = rng.standard_normal((5, 4, 8)), rng.standard_normal((7, 2, 8)), rng.standard_normal((7, 2, 8))
+    do = rng.standard_normal(q.shape)
+    f = lambda q, k, v: (layer.window_attention(q, k, v, 3, 1, 0.3)[0] * do).sum()  # noqa: E731
+    grads = layer.window_attention_bwd(q, k, v, do, 3, 1, 0.3)
+    for _ in range(10):
+        e = [rng.standard_normal(x.shape) for x in (q, k, v)]
+        h = 1e-5
+        d = (f(*(x + h * y for x, y in zip((q, k, v), e))) - f(*(x - h * y for x, y in zip((q, k, v), e)))) / (2 * h)
+        want = sum((g * y).sum() for g, y in zip(grads, e))
+        assert abs(d - want) <= 1e-7 * sum(np.abs(g * y).sum() for g, y in zip(grads, e))
+
+
+def test_oracle_mask():
+    seen = layer.window_seen(3, 6, 2, 1)
+    assert seen.astype(int).tolist() == [[1, 0, 1, 1, 0, 0], [1, 0, 0, 1, 1, 0], [1, 0, 0, 0, 1, 1]]
+    assert layer.window_seen(2, 1, 5, 5).astype(int).tolist() == [[0], [1]]
