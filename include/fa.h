@@ -611,6 +611,42 @@ FA_API int fa_attention_window_fwd(const void *Q, int64_t q_stride, const void *
                                    int window, int sinks, const int32_t *cu_seqlens_q,
                                    const int32_t *cu_seqlens_k, const int32_t *seqlens_k);
 
+/*
+ * Its gradient where queries and keys are the same tokens (training): the gradients
+ * of sum(dO * O) with respect to Q, K and V, from O and lse as the forward wrote
+ * them for the same Q, K, V, scale, window and sinks.  dK and dV are summed over the
+ * H / Hkv query heads of a kv head.
+ *   dense  (cu_seqlens == NULL): B sequences of N tokens, total = B * N; packed:
+ *   cu_seqlens DEVICE int32 [B + 1], N the most tokens of a sequence (an upper bound
+ *   is fine; it sizes the grid and the workspace), total rows there; those behind
+ *   the last sequence are neither read into a result nor written.
+ *   Q, K, V: rows as in the forward.  O, dO: contiguous bf16 [.., H, d]; lse as
+ *   there.  dQ, dK, dV: bf16 rows of H * d, Hkv * d and Hkv * d values, dq_stride,
+ *   dk_stride and dv_stride elements apart (multiples of 8), 16-byte aligned; written.
+ *   workspace: DEVICE scratch owned by the caller, 256-byte aligned, at least
+ *   fa_attention_window_bwd_workspace_bytes(...) bytes; contents on entry are
+ *   ignored.  Calls that may run at the same time need one each.
+ * All of a sequence's Q, K, V, O and dO should be finite: a NaN reaches the gradients
+ * that its row takes part in and may reach others near them (not other sequences').
+ * The same call gives the same bits (no atomics).  Two or three kernels on the
+ * library stream, no synchronisation.
+ * Errors: as fa_attention_window_fwd; FA_ERR_BAD_SIZE also for a workspace that is
+ * too small.
+ */
+FA_API int fa_attention_window_bwd(const void *Q, int64_t q_stride, const void *K,
+                                   int64_t k_stride, const void *V, int64_t v_stride,
+                                   const void *O, const void *dO, const float *lse, void *dQ,
+                                   int64_t dq_stride, void *dK, int64_t dk_stride, void *dV,
+                                   int64_t dv_stride, int B, int N, int64_t total, int H,
+                                   int Hkv, int d, float scale, int window, int sinks,
+                                   const int32_t *cu_seqlens, void *workspace,
+                                   int64_t workspace_bytes);
+
+/* Workspace bytes fa_attention_window_bwd needs (4 bytes a query and head, and fp32
+ * parts of the tiles of 128 keys that hold sinks), or a negative FA_ERR_* code. */
+FA_API int64_t fa_attention_window_bwd_workspace_bytes(int B, int N, int64_t total, int H,
+                                                       int Hkv, int d, int window, int sinks);
+
 /* ---- Norm and rotation of queries and keys ---------------------------------------
  *
  * What an attention layer does to the heads of Q and K before the attention, in
@@ -689,8 +725,9 @@ FA_API int fa_set_stream(void *stream);
 /*
  * Failure detection, for tests: arms a wait that cannot complete in the next
  * bf16 attention forward (fa_attention_fwd / fa_attention_fwd_varlen), one-pass
- * backward (fa_attention_bwd_atomic / fa_attention_bwd_atomic_varlen) or
- * attention over the 4-bit cache (fa_attention_kv4) launched from this host
+ * backward (fa_attention_bwd_atomic / fa_attention_bwd_atomic_varlen),
+ * attention over the 4-bit cache (fa_attention_kv4) or window attention
+ * (fa_attention_window_fwd, fa_attention_window_bwd) launched from this host
  * thread, whichever comes first.  In a forward or backward launch the
  * warp that issues the tensor-core instructions first waits, bounded by `ns`
  * nanoseconds, on a barrier that nothing arrives at.  The wait runs out, sets

@@ -17,14 +17,15 @@ Raw C-ABI names (same names, same argument order, ints and pointers only):
 ``fa_attention_host_workspace_bytes``,
 ``fa_kv4_page_bytes``, ``fa_kv4_append``, ``fa_kv4_read``,
 ``fa_attention_kv4``, ``fa_attention_kv4_workspace_bytes``,
-``fa_attention_window_fwd``,
+``fa_attention_window_fwd``, ``fa_attention_window_bwd``,
+``fa_attention_window_bwd_workspace_bytes``,
 ``fa_qk_norm_rope_fwd``, ``fa_qk_norm_rope_bwd``, ``fa_qk_norm_rope_bwd_workspace_bytes``,
 ``fa_set_stream``, ``fa_get_stream``, ``fa_get_device_error``, ``fa_strerror``,
 ``fa_version``, ``fa_debug_expire_next_wait``.
 Tensor-level helpers: :func:`softmax_rows`, :func:`attention_fwd`,
 :func:`attention_fwd_splitkv`, :func:`attention_bwd`, :func:`attention_fwd_fp8`,
 :func:`kv4_cache`, :func:`kv4_append`, :func:`kv4_read`, :func:`attention_kv4`,
-:func:`attention_window_fwd`,
+:func:`attention_window_fwd`, :func:`attention_window_bwd`,
 :func:`qk_norm_rope_fwd`, :func:`qk_norm_rope_bwd`.
 """
 from __future__ import annotations
@@ -122,6 +123,12 @@ def lib():
         L.fa_attention_kv4_workspace_bytes.restype = i64
         L.fa_attention_window_fwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i32, i32, i64, i32,
                                               i64, i32, i32, i32, f32, i32, i32, vp, vp, vp]
+        L.fa_attention_window_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp,
+                                              i64, vp, i64, i32, i32, i64, i32, i32, i32, f32, i32,
+                                              i32, vp, vp, i64]
+        L.fa_attention_window_bwd_workspace_bytes.argtypes = [i32, i32, i64, i32, i32, i32, i32,
+                                                              i32]
+        L.fa_attention_window_bwd_workspace_bytes.restype = i64
         L.fa_qk_norm_rope_fwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, i64,
                                           i32, i32, i32, i32, i32, f32]
         L.fa_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp,
@@ -145,7 +152,8 @@ def lib():
                      "fa_attention_fwd_splitkv_varlen",
                      "fa_attention_fwd_fp8", "fa_attention_fwd_fp8_varlen",
                      "fa_attention_fwd_host", "fa_kv4_append", "fa_kv4_read",
-                     "fa_attention_kv4", "fa_attention_window_fwd", "fa_qk_norm_rope_fwd", "fa_qk_norm_rope_bwd",
+                     "fa_attention_kv4", "fa_attention_window_fwd", "fa_attention_window_bwd",
+                     "fa_qk_norm_rope_fwd", "fa_qk_norm_rope_bwd",
                      "fa_set_stream", "fa_get_device_error", "fa_version",
                      "fa_debug_expire_next_wait"):
             getattr(L, name).restype = ctypes.c_int
@@ -304,6 +312,19 @@ def fa_attention_window_fwd(q, q_stride, k, k_stride, v, v_stride, o, lse, B, Nq
     return lib().fa_attention_window_fwd(q, q_stride, k, k_stride, v, v_stride, o, lse, B, Nq,
                                          total_q, Nk, total_k, H, Hkv, d, scale, window, sinks,
                                          cu_seqlens_q, cu_seqlens_k, seqlens_k)
+
+
+def fa_attention_window_bwd(q, q_stride, k, k_stride, v, v_stride, o, do, lse, dq, dq_stride, dk,
+                            dk_stride, dv, dv_stride, B, N, total, H, Hkv, d, scale, window, sinks,
+                            cu_seqlens, workspace, workspace_bytes) -> int:
+    return lib().fa_attention_window_bwd(q, q_stride, k, k_stride, v, v_stride, o, do, lse, dq,
+                                         dq_stride, dk, dk_stride, dv, dv_stride, B, N, total, H,
+                                         Hkv, d, scale, window, sinks, cu_seqlens, workspace,
+                                         workspace_bytes)
+
+
+def fa_attention_window_bwd_workspace_bytes(B, N, total, H, Hkv, d, window, sinks) -> int:
+    return lib().fa_attention_window_bwd_workspace_bytes(B, N, total, H, Hkv, d, window, sinks)
 
 
 def fa_qk_norm_rope_fwd(q, q_stride, k, k_stride, q_weight, k_weight, inv_freq, positions, qo,
@@ -989,6 +1010,62 @@ def attention_window_fwd(q, k, v, window: int, sinks: int = 0, scale: float | No
     return out, lse
 
 
+def _plan_window_bwd(q, qs, k, ks, v, vs, dq, dqs, dk, dks, dv, dvs, cu, max_seqlen, window, sinks):
+    if dq != q or dk != k or dv != v:
+        raise ValueError("dq, dk and dv must have the shapes of q, k and v")
+    if q[:-2] != k[:-2]:
+        raise ValueError("q, k and v must be of the same tokens")
+    plan = _plan_window(q, qs, k, ks, v, vs, cu, cu, None, max_seqlen, max_seqlen)
+    (s_q, s_k, s_v, B, N, total, _, _, H, hkv, d, lse_shape) = plan
+    nbytes = fa_attention_window_bwd_workspace_bytes(B, N, total, H, hkv, d, window, sinks)
+    _check(int(min(nbytes, 0)), "fa_attention_window_bwd_workspace_bytes")
+    return (s_q, s_k, s_v, _row_stride(dq, dqs, "dq"), _row_stride(dk, dks, "dk"),
+            _row_stride(dv, dvs, "dv"), B, N, total, H, hkv, d, lse_shape, nbytes)
+
+
+def attention_window_bwd(q, k, v, o, do, lse, window: int, sinks: int = 0,
+                         scale: float | None = None, cu_seqlens=None,
+                         max_seqlen: int | None = None, dq=None, dk=None, dv=None, workspace=None):
+    """Gradient of :func:`attention_window_fwd` where queries and keys are the same tokens.
+
+    q, o, do: [B, N, H, d], k, v: [B, N, kv_heads, d], lse [B, H, N]; or packed [total, .., d] with
+    ``cu_seqlens`` (int32 [B+1]) and ``max_seqlen`` (default: total), lse [H, total].  ``o`` and
+    ``lse`` are the forward's outputs for the same inputs; o and do are contiguous.  ``dq``, ``dk``,
+    ``dv``: write into these (rows any multiple of 8 elements apart: slices of a fused
+    projection's gradient).  The workspace is allocated here (torch) unless given (uint8,
+    fa_attention_window_bwd_workspace_bytes).  Returns (dq, dk, dv).
+    """
+    import torch
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+    if dv is None:
+        dv = torch.empty(v.shape, dtype=torch.bfloat16, device=q.device)
+    index = _window_check(torch, (q, k, v, o, do, dq, dk, dv), (cu_seqlens,))
+    key = (q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), dq.shape, dq.stride(),
+           dk.shape, dk.stride(), dv.shape, dv.stride(),
+           None if cu_seqlens is None else cu_seqlens.shape, max_seqlen, window, sinks)
+    (qs, ks, vs, dqs, dks, dvs, B, N, total, H, hkv, d, lse_shape,
+     nbytes) = _kv4_plan(key, _plan_window_bwd, *key)
+    if o.shape != q.shape or do.shape != q.shape or not o.is_contiguous() or not do.is_contiguous():
+        raise ValueError("o and do must be contiguous tensors like q")
+    if not (tuple(lse.shape) == lse_shape and lse.dtype is torch.float32
+            and lse.get_device() == index and lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 tensor {list(lse_shape)}")
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    elif not (workspace.dtype is torch.uint8 and workspace.get_device() == index
+              and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    _kv4_call(torch, index, "fa_attention_window_bwd", q.data_ptr(), qs, k.data_ptr(), ks,
+              v.data_ptr(), vs, o.data_ptr(), do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dqs,
+              dk.data_ptr(), dks, dv.data_ptr(), dvs, B, N, total, H, hkv, d,
+              1.0 / math.sqrt(d) if scale is None else scale, window, sinks, _ptr(cu_seqlens),
+              workspace.data_ptr(), workspace.numel())
+    return dq, dk, dv
+
+
 # ---- norm and rotation of queries and keys ----------------------------------------
 
 def _plan_norm_rope(shapes, strides, w_shapes, pos, freq):
@@ -1103,7 +1180,8 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, inv_fre
 
 
 __all__ = [
-    "attention_window_fwd", "fa_attention_window_fwd",
+    "attention_window_fwd", "attention_window_bwd", "fa_attention_window_fwd",
+    "fa_attention_window_bwd", "fa_attention_window_bwd_workspace_bytes",
     "qk_norm_rope_fwd", "qk_norm_rope_bwd", "fa_qk_norm_rope_fwd", "fa_qk_norm_rope_bwd",
     "fa_qk_norm_rope_bwd_workspace_bytes",
     "attention_kv4", "kv4_cache", "kv4_append", "kv4_read", "fa_attention_kv4",

@@ -86,12 +86,6 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
     }
 }
 
-// The lowest `n` bits, n clamped to 0 .. 32.
-__device__ __forceinline__ uint32_t low_bits(int n)
-{
-    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_constant__ Params p)
 {
@@ -407,9 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
             if (__any_sync(0xffffffffu, v0 < vlo || v0 + BN - 1 > vhi)) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const int vc = v0 + 32 * c;
-                    const uint32_t seen = low_bits(vhi - vc + 1) &
-                                          (~low_bits(vlo - vc) | low_bits(a.sinks - vc));
+                    const uint32_t seen = window_bits(v0 + 32 * c, vlo, vhi, a.sinks);
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (!(seen & (1u << e)))

@@ -1,0 +1,1072 @@
+// attn_window_bwd.cu -- gradients of the window attention (dQ, dK, dV) on the
+// sm_103a tensor cores.
+//
+// With P = exp(scale Q K^T - lse) at the seen keys, formed again tile by tile, and
+// D_i = dO_i . O_i:
+//     dV = P^T dO,  dS = P o (dO V^T - D),  dQ = scale dS K,  dK = scale dS^T Q,
+// dK and dV summed over the G query heads that share a kv head.  Two kernels as in
+// attn_bwd.cu, whose roles, tensor memory and order of products they have, and no
+// atomics; then, where sinks are seen from outside their tile's window, a third:
+//   * attn_window_dq_kernel: a CTA per (sequence, kv head, 128 rows: queries x G
+//     heads), the keys that they see in 128-key steps, the window's behind the
+//     sinks' as in the forward (window.cuh).  Also writes D.
+//   * attn_window_dkdv_kernel: a CTA per (sequence, kv head, 128 keys); 64-query
+//     steps over the queries that have these keys in their window, one head of the
+//     group after the other into the same accumulators.  Keys below `sinks` are seen
+//     by all later queries too: these steps, of which a long sequence has many more
+//     than a window, go to CTAs of their own in pieces as long as a window's, and
+//     all pieces of such a tile write fp32 parts.
+//   * attn_window_join_kernel adds a tile's parts in order.
+// P and dS are rounded to bf16 (2^-9 relative each) as operands; all sums are fp32.
+// Rows behind a sequence's end (the next sequence, room at the end of the batch) are
+// zeroed in shared memory before a product sums over them: their P is 0, but they may
+// hold NaN.  Every wait is bounded; a timed-out one leaves its CTA's rows unwritten.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/fa.h"
+#include "fa_error.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+#include "window.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int BT = 128;                     // rows of the resident tile
+constexpr int BS = 64;                      // queries of a dK/dV step
+constexpr int kPad = 32;                    // sinks fill whole pieces of a tile
+constexpr int kRowWarps = 8;                // two threads a row
+constexpr int kThreads = 32 * (kRowWarps + 2);
+constexpr int kWarpLoad = kRowWarps, kWarpMma = kRowWarps + 1;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kChunkBytes = BT * 128;     // 128 rows of 64 bf16
+constexpr uint32_t kSubChunkBytes = BS * 128;  // 64 rows
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Params {
+    CUtensorMap tm_q, tm_do;           // dQ: box {64, G, 1, P}; dK/dV: {64, 1, 1, 64}
+    CUtensorMap tm_k, tm_v;            // box {64, 1, 1, 128}
+    CUtensorMap tm_k32, tm_v32;        // dQ: box {64, 1, 1, 32}
+    WindowArgs a;                      // O read; queries and keys are the same tokens
+    float *D;                          // as lse
+    __nv_bfloat16 *dQ, *dK, *dV;
+    int64_t dq_stride, dk_stride, dv_stride;
+    float *parts;                      // [B Hkv][sink tiles][slots][dV, dK][128][d]
+    int G, P, n_tiles;                 // n_tiles: row tiles (dQ), key tiles (dK/dV) of Nq
+    int sink_tiles, slots, piece;      // piece: 64-query sub-tiles of a far piece
+    float scale_log2;
+};
+
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t it = 0; it < kWaitMaxPolls; ++it) {
+        if (ptx::mbar_try_wait(bar, parity))
+            return;
+        if ((it & 255u) == 255u && ptx::globaltimer() - t0 > kWaitTimeoutNs)
+            return;
+    }
+}
+
+// A row warp's wait: one lane polls and shares the outcome.
+__device__ __forceinline__ bool row_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                         int *err_word)
+{
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0)
+        ok = ptx::mbar_wait(bar, parity, abort, err_word) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
+    return ok != 0;
+}
+
+// Rows [r0, rows) of a tile of 64-value chunks (`stride` bytes apart) cleared by a warp.
+template <int CHUNKS>
+__device__ __forceinline__ void clear_rows(uint8_t *tile, int r0, int rows, uint32_t stride)
+{
+    const int lane = threadIdx.x & 31;
+    for (int r = (r0 > 0 ? r0 : 0) + (lane >> 3); r < rows; r += 4)
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+            *reinterpret_cast<uint4 *>(tile + c * stride + r * 128 + (lane & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+}
+
+// Shared-memory descriptor offset of K step kk (16 bf16) in a K-major tile.
+__device__ __forceinline__ uint64_t kmajor_off(int kk, uint32_t chunk_bytes)
+{
+    return uint64_t(((kk >> 2) * chunk_bytes + (kk & 3) * 32) >> 4);
+}
+
+// Columns [32 c0, 32 c1) of this thread's row of an accumulator times `mul`, as bf16.
+__device__ __forceinline__ void store_row(uint32_t t_acc, float mul, __nv_bfloat16 *dst, bool ok,
+                                          int c0, int c1)
+{
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+        uint32_t o[32];
+        ptx::tmem_ld32(t_acc + c * 32, o);
+        ptx::tmem_wait_ld();
+        if (ok) {
+            uint4 *out = reinterpret_cast<uint4 *>(dst + c * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t u[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    u[e] = ptx::pack_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * mul,
+                                            __uint_as_float(o[8 * q + 2 * e + 1]) * mul);
+                out[q] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+        }
+    }
+}
+
+// Index of the row statistic (lse, D) of a sequence's first query, head h.
+__device__ __forceinline__ int64_t stat_row(const WindowArgs &a, int b, int h, int64_t q0)
+{
+    return a.cu_seqlens_q != nullptr ? int64_t(h) * a.total_q + q0
+                                     : (int64_t(b) * a.H + h) * a.Nq;
+}
+
+// =============================================================================
+// dQ and D
+// =============================================================================
+// S in columns [0, 128), dP (then dS packed into the first half of each row thread's
+// 64 columns) in [128, 256), dQ from 256, Q and dO as bf16 A operands behind it.  The
+// MMA warp issues, per step j: S_{j+1} as soon as the rows have read S_j, dQ += dS_j
+// K_j once they have stored dS_j, then dP_{j+1}.  The ring's third stage is the region
+// that held Q and dO, free once they are in tensor memory and D is formed.
+template <int D>
+struct CfgQ {
+    static constexpr int kChunks = D / 64;
+    static constexpr uint32_t kTileBytes = BT * D * 2;
+    static constexpr uint32_t kStageBytes = 2 * kTileBytes;  // K_j, V_j
+    static constexpr int kStages = 3;
+    static constexpr uint32_t kOffRing = 2 * kTileBytes;
+    static constexpr uint32_t kOffXch = kOffRing + 2 * kStageBytes;   // 128 D_i values
+    static constexpr uint32_t kOffBar = kOffXch + BT * 4;
+    static constexpr int kBars = 1 + 2 * kStages + 9;
+    static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16 + 1024;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+    static __device__ __forceinline__ uint32_t stage_off(int s)
+    {
+        return s == 2 ? 0u : kOffRing + uint32_t(s) * kStageBytes;
+    }
+};
+constexpr uint32_t kColAcc = 256, kQColDP = 128;
+constexpr int kQCols = 64;                      // columns of a step per row thread
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __grid_constant__ Params p)
+{
+    using C = CfgQ<D>;
+    constexpr uint32_t kColQA = kColAcc + D;
+    static_assert(kColQA + D <= kTmemCols, "tensor memory");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    uint64_t *a_full = bars, *kv_full = bars + 1, *kv_empty = bars + 1 + C::kStages;
+    uint64_t *s_full = bars + 1 + 2 * C::kStages, *dp_full = s_full + 1, *s_free = s_full + 2,
+             *p_full = s_full + 3, *o_full = s_full + 4, *drain = s_full + 5, *a_tm = s_full + 6,
+             *res_free = s_full + 7, *never = s_full + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    // nothing that a kernel before may still be writing is read ahead of this
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const WindowArgs &a = p.a;
+    const int tile = p.n_tiles - 1 - int(blockIdx.x % unsigned(p.n_tiles));
+    const int bh = int(blockIdx.x / unsigned(p.n_tiles));
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    WindowSeq sq;
+    if (!window_seq(a, b, sq)) {
+        if (threadIdx.x == 0 && tile == 0 && hk == 0)
+            record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
+        return;
+    }
+    const int i0 = tile * p.P, L = sq.L;
+    if (i0 >= L)
+        return;
+    const int i1 = min(i0 + p.P, L);
+    const WindowKeys w = window_keys(a.window, a.sinks, i0, i1, 0, kPad);
+    const int n_kv = (w.places + BT - 1) / BT;      // at least one
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(a_full, 1);
+        for (int st = 0; st < C::kStages; ++st) {
+            ptx::mbar_init(&kv_full[st], 1);
+            ptx::mbar_init(&kv_empty[st], 1);
+        }
+        ptx::mbar_init(s_full, 1);
+        ptx::mbar_init(dp_full, 1);
+        ptx::mbar_init(s_free, kRowWarps);
+        ptx::mbar_init(p_full, kRowWarps);
+        ptx::mbar_init(o_full, 1);
+        ptx::mbar_init(drain, 1);
+        ptx::mbar_init(a_tm, kRowWarps);
+        ptx::mbar_init(res_free, kRowWarps);
+        ptx::mbar_init(never, 1);
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        ptx::tmem_alloc(tmem_slot, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    if (warp == kWarpLoad && lane == 0) {
+        ptx::prefetch_tmap(&p.tm_q);
+        ptx::prefetch_tmap(&p.tm_do);
+        ptx::prefetch_tmap(&p.tm_k);
+        ptx::prefetch_tmap(&p.tm_v);
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    bool aborted = false;
+    uint8_t *tile_q = smem, *tile_do = smem + C::kTileBytes;
+
+    if (warp == kWarpLoad) {
+        // ======================= TMA producer ==============================
+        if (lane == 0) {
+            int last_phase[C::kStages];
+            for (int st = 0; st < C::kStages; ++st)
+                last_phase[st] = -1;
+            ptx::mbar_arrive_expect_tx(a_full, 2 * C::kChunks * p.P * p.G * 128);
+            for (int c = 0; c < C::kChunks; ++c) {
+                ptx::tma_load_4d(tile_q + c * kChunkBytes, &p.tm_q, a_full, c * 64, 0, hk,
+                                 int(sq.q0 + i0));
+                ptx::tma_load_4d(tile_do + c * kChunkBytes, &p.tm_do, a_full, c * 64, 0, hk,
+                                 int(sq.q0 + i0));
+            }
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int j = 0; j < n_kv; ++j) {
+                if (!ptx::mbar_wait(&kv_empty[stage], phase ^ 1u, abort_flag, a.err_word))
+                    break;
+                // stage 2 is the Q / dO region: free once the rows are done with it
+                if (j == 2 && !ptx::mbar_wait(res_free, 0, abort_flag, a.err_word))
+                    break;
+                uint8_t *dst = smem + C::stage_off(stage);
+                const int v0 = j * BT;
+                ptx::mbar_arrive_expect_tx(&kv_full[stage], C::kStageBytes);
+                if (v0 < w.sp && v0 + BT > w.sp) {
+                    for (int q = 0; q < BT / kPad; ++q) {
+                        const int v = v0 + q * kPad;
+                        const int row = int(sq.k0 + (v < w.sp ? v : w.lo + v - w.sp));
+                        for (int c = 0; c < C::kChunks; ++c) {
+                            uint8_t *to = dst + c * kChunkBytes + q * kPad * 128;
+                            ptx::tma_load_4d(to, &p.tm_k32, &kv_full[stage], c * 64, 0, hk, row);
+                            ptx::tma_load_4d(to + C::kTileBytes, &p.tm_v32, &kv_full[stage],
+                                             c * 64, 0, hk, row);
+                        }
+                    }
+                } else {
+                    const int row = int(sq.k0 + (v0 < w.sp ? v0 : w.lo + v0 - w.sp));
+                    for (int c = 0; c < C::kChunks; ++c) {
+                        ptx::tma_load_4d(dst + c * kChunkBytes, &p.tm_k, &kv_full[stage], c * 64,
+                                         0, hk, row);
+                        ptx::tma_load_4d(dst + C::kTileBytes + c * kChunkBytes, &p.tm_v,
+                                         &kv_full[stage], c * 64, 0, hk, row);
+                    }
+                }
+                last_phase[stage] = int(phase);
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (*abort_flag) {
+                drain_wait(a_full, 0);
+                for (int st = 0; st < C::kStages; ++st)
+                    if (last_phase[st] >= 0)
+                        drain_wait(&kv_full[st], uint32_t(last_phase[st]));
+            }
+        }
+        __syncwarp();
+    } else if (warp == kWarpMma) {
+        // ======================= MMA issuer (whole warp) =====================
+        constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(BT, BT, false);
+        constexpr uint32_t idesc_q = ptx::idesc_bf16_f32(BT, D, true);     // B MN-major
+        constexpr uint64_t desc_kmajor = ptx::smem_desc_base(16, 1024);
+        constexpr uint64_t desc_mnmajor = ptx::smem_desc_base(kChunkBytes, 1024);
+        auto issue_s = [&](uint32_t kaddr) {
+            const uint64_t dk = ptx::smem_desc(desc_kmajor, kaddr);
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    ptx::mma_ts(tmem, tmem + kColQA + 8 * kk, dk + kmajor_off(kk, kChunkBytes),
+                                idesc_s, kk > 0 ? 1u : 0u);
+                ptx::mma_commit(s_full);
+            }
+            __syncwarp();
+        };
+        auto issue_dp = [&](uint32_t vaddr) {
+            const uint64_t dv = ptx::smem_desc(desc_kmajor, vaddr);
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    ptx::mma_ts(tmem + kQColDP, tmem + kColQA + D / 2 + 8 * kk,
+                                dv + kmajor_off(kk, kChunkBytes), idesc_s, kk > 0 ? 1u : 0u);
+                ptx::mma_commit(dp_full);
+            }
+            __syncwarp();
+        };
+        const uint32_t smem_base = ptx::smem_u32(smem);
+        // K's and V's rows of step j behind the sequence's end are cleared
+        const int end_place = w.sp + (L - w.lo);
+        auto clear_tail = [&](int j, int st) {
+            const int r0 = end_place - j * BT;
+            if (r0 >= BT)
+                return;
+            clear_rows<2 * C::kChunks>(smem + C::stage_off(st), r0, BT, kChunkBytes);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+        };
+        if (a.expire_wait_ns != 0u &&
+            !__all_sync(0xffffffffu, ptx::mbar_wait_limited(never, 0, abort_flag, a.err_word,
+                                                            a.expire_wait_ns)))
+            aborted = true;
+        do {
+            if (aborted || !ptx::mbar_wait_warp(a_tm, 0, abort_flag, a.err_word) ||
+                !ptx::mbar_wait_warp(&kv_full[0], 0, abort_flag, a.err_word)) {
+                aborted = true;
+                break;
+            }
+            clear_tail(0, 0);
+            ptx::tc_fence_after_sync();
+            issue_s(smem_base + C::stage_off(0));
+            issue_dp(smem_base + C::stage_off(0) + C::kTileBytes);
+            int cur = 0, nxt = 1;                      // ring stages of steps j, j + 1
+            uint32_t nxt_phase = 0;
+            for (int j = 0; j < n_kv; ++j) {
+                const bool more = j + 1 < n_kv;
+                if (more) {
+                    // S_{j+1} overwrites S_j once every row has read it
+                    if (!ptx::mbar_wait_warp(s_free, uint32_t(j) & 1u, abort_flag, a.err_word) ||
+                        !ptx::mbar_wait_warp(&kv_full[nxt], nxt_phase, abort_flag, a.err_word)) {
+                        aborted = true;
+                        break;
+                    }
+                    clear_tail(j + 1, nxt);
+                    ptx::tc_fence_after_sync();
+                    issue_s(smem_base + C::stage_off(nxt));
+                }
+                if (!ptx::mbar_wait_warp(p_full, uint32_t(j) & 1u, abort_flag, a.err_word)) {
+                    aborted = true;
+                    break;
+                }
+                ptx::tc_fence_after_sync();
+                const uint64_t dkn = ptx::smem_desc(desc_mnmajor, smem_base + C::stage_off(cur));
+                if (ptx::elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < BT / 16; ++kk)
+                        ptx::mma_ts(tmem + kColAcc,
+                                    tmem + kQColDP + uint32_t(kQCols * (kk >> 2) + 8 * (kk & 3)),
+                                    dkn + uint64_t((kk * 16 * 128) >> 4), idesc_q,
+                                    (j > 0 || kk > 0) ? 1u : 0u);
+                    ptx::mma_commit(&kv_empty[cur]);
+                }
+                __syncwarp();
+                // dP_{j+1} overwrites dS_j after the dQ product has read it
+                if (more)
+                    issue_dp(smem_base + C::stage_off(nxt) + C::kTileBytes);
+                cur = nxt;
+                if (++nxt == C::kStages) {
+                    nxt = 0;
+                    nxt_phase ^= 1u;
+                }
+            }
+        } while (false);
+        if (ptx::elect_one()) {
+            if (!aborted)
+                ptx::mma_commit(o_full);
+            ptx::mma_commit(drain);
+            drain_wait(drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ======================= query rows ================================
+        const int r = (warp & 3) * 32 + lane;        // row of the tile = TMEM lane
+        const int g = warp >> 2;                     // column group
+        const int qi = r / p.G, i = i0 + qi;         // query, head of the kv head
+        const int h = hk * p.G + r % p.G;
+        const bool row_ok = qi < p.P && i < i1;
+        const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
+        const int64_t stat = row_ok ? stat_row(a, b, h, sq.q0) + i : 0;
+        // D_i = dO_i . O_i: a warp takes 16 rows, D / 8 lanes each; O from global memory,
+        // dO from the resident tile (128-byte swizzle)
+        constexpr int kLanesPerRow = D / 8, kRowsPerInst = 32 / kLanesPerRow;
+        constexpr int kRowsPerWarp = BT / kRowWarps;          // 16
+        float *xch = reinterpret_cast<float *>(smem + C::kOffXch);
+        {
+            const int sub = lane / kLanesPerRow, lr = lane % kLanesPerRow;
+            uint4 ov[kRowsPerWarp / kRowsPerInst];
+#pragma unroll
+            for (int k = 0; k < kRowsPerWarp / kRowsPerInst; ++k) {
+                const int rr = warp * kRowsPerWarp + k * kRowsPerInst + sub;
+                const int qr = rr / p.G, hr = hk * p.G + rr % p.G;
+                ov[k] = qr < p.P && i0 + qr < i1
+                            ? *reinterpret_cast<const uint4 *>(
+                                  static_cast<const __nv_bfloat16 *>(a.O) +
+                                  ((sq.q0 + i0 + qr) * a.H + hr) * D + lr * 8)
+                            : make_uint4(0, 0, 0, 0);
+            }
+            const bool a_ok = row_wait(a_full, 0, abort_flag, a.err_word);
+            if (a_ok) {
+                // this thread's half of its row of Q and of dO into tensor memory
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const uint8_t *src = t == 0 ? tile_q : tile_do;
+                    uint32_t u[D / 4];
+#pragma unroll
+                    for (int ul = 0; ul < D / 16; ++ul) {
+                        const int e0 = g * (D / 2) + ul * 8;
+                        const int un = (e0 & 63) >> 3;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(
+                            src + (e0 >> 6) * kChunkBytes + r * 128 + ((un ^ (r & 7)) << 4));
+                        u[4 * ul + 0] = v.x;
+                        u[4 * ul + 1] = v.y;
+                        u[4 * ul + 2] = v.z;
+                        u[4 * ul + 3] = v.w;
+                    }
+                    const uint32_t dst =
+                        tmem + lane_bits + kColQA + uint32_t(t * (D / 2) + g * (D / 4));
+                    if constexpr (D == 128)
+                        ptx::tmem_st32(dst, u);
+                    else
+                        ptx::tmem_st16(dst, u);
+                }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(a_tm);
+            }
+#pragma unroll
+            for (int k = 0; k < kRowsPerWarp / kRowsPerInst; ++k) {
+                const int rr = warp * kRowsPerWarp + k * kRowsPerInst + sub;
+                const int u = lr & 7, chunk = lr >> 3;
+                const uint4 gv = a_ok ? *reinterpret_cast<const uint4 *>(
+                                            tile_do + chunk * kChunkBytes + rr * 128 +
+                                            ((u ^ (rr & 7)) << 4))
+                                      : make_uint4(0, 0, 0, 0);
+                const uint32_t ow[4] = {ov[k].x, ov[k].y, ov[k].z, ov[k].w};
+                const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w};
+                float part = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    part = fmaf(__uint_as_float(ow[e] << 16), __uint_as_float(gw[e] << 16), part);
+                    part = fmaf(__uint_as_float(ow[e] & 0xffff0000u),
+                                __uint_as_float(gw[e] & 0xffff0000u), part);
+                }
+#pragma unroll
+                for (int o = kLanesPerRow / 2; o > 0; o >>= 1)
+                    part += __shfl_xor_sync(0xffffffffu, part, o);
+                if (lr == 0)
+                    xch[rr] = part;
+            }
+            // this warp has finished with the Q / dO region (ring stage 2)
+            __syncwarp();
+            if (a_ok && lane == 0)
+                ptx::mbar_arrive(res_free);
+        }
+        const float lse2 = row_ok ? a.lse[stat] * kLog2e : 0.f;
+        asm volatile("bar.sync 1, 256;" ::: "memory");              // the row threads
+        const float Di = xch[r];
+        if (g == 0 && row_ok)
+            p.D[stat] = Di;
+        const float sl = p.scale_log2;
+        const int col0 = g * kQCols;
+        const uint32_t tS = tmem + lane_bits + uint32_t(col0);
+        const uint32_t tDP = tmem + lane_bits + kQColDP + uint32_t(col0);
+        const int vhi = row_ok ? i - w.lo + w.sp : -1;
+        const int64_t vl = int64_t(vhi) - a.window + 1;
+        const int vlo = vl > w.sp ? int(vl) : w.sp;
+
+        for (int j = 0; j < n_kv; ++j) {
+            const uint32_t par = uint32_t(j) & 1u;
+            if (!row_wait(s_full, par, abort_flag, a.err_word)) {
+                aborted = true;
+                break;
+            }
+            ptx::tc_fence_after_sync();
+            const int v0 = j * BT + col0;            // this thread's first place
+            const bool masked = __any_sync(0xffffffffu, v0 < vlo || v0 + kQCols - 1 > vhi);
+            uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+            if (masked)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    seen[c] = window_bits(v0 + 32 * c, vlo, vhi, a.sinks);
+            float pr[kQCols];
+            {
+                uint32_t sv0[32], sv1[32];
+                ptx::tmem_ld32(tS, sv0);
+                ptx::tmem_ld32(tS + 32, sv1);
+                ptx::tmem_wait_ld();
+                // S is read: the MMA warp may overwrite it with the next step's
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(s_free);
+                if (masked) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        if (!(seen[0] & (1u << k)))
+                            sv0[k] = __float_as_uint(-INFINITY);
+                        if (!(seen[1] & (1u << k)))
+                            sv1[k] = __float_as_uint(-INFINITY);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    pr[k] = ptx::ex2(fmaf(__uint_as_float(sv0[k]), sl, -lse2));
+                    pr[32 + k] = ptx::ex2(fmaf(__uint_as_float(sv1[k]), sl, -lse2));
+                }
+            }
+            if (!row_wait(dp_full, par, abort_flag, a.err_word)) {
+                aborted = true;
+                break;
+            }
+            ptx::tc_fence_after_sync();
+            uint32_t pk[32];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t dv[32];
+                ptx::tmem_ld32(tDP + 32 * half, dv);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float d0 = pr[32 * half + 2 * e] * (__uint_as_float(dv[2 * e]) - Di);
+                    const float d1 =
+                        pr[32 * half + 2 * e + 1] * (__uint_as_float(dv[2 * e + 1]) - Di);
+                    pk[16 * half + e] = ptx::pack_bf16x2(d0, d1);
+                }
+            }
+            ptx::tmem_st32(tDP, pk);                  // dS of this row's 64 keys, packed
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(p_full);
+        }
+        // the two threads of a row store half of its dQ each
+        if (!aborted && ptx::mbar_wait(o_full, 0, abort_flag, a.err_word)) {
+            ptx::tc_fence_after_sync();
+            store_row(tmem + lane_bits + kColAcc, a.scale,
+                      p.dQ + (sq.q0 + i) * p.dq_stride + int64_t(h) * D, row_ok, g * (D / 64),
+                      (g + 1) * (D / 64));
+        }
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    if (warp == kWarpMma)
+        ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+// =============================================================================
+// dK, dV
+// =============================================================================
+// Per step S^T = K Q_s^T and dP^T = V dO_s^T (a key per lane) in one of two buffers of
+// tensor memory, [0, 128) and [128, 256): S^T in a buffer's first 64 columns, dP^T in
+// the others, P^T and dS^T packed into them; dV from 256, dK behind it.
+template <int D>
+struct CfgK {
+    static constexpr int kChunks = D / 64;
+    static constexpr uint32_t kResBytes = BT * D * 2;
+    static constexpr uint32_t kSubBytes = BS * D * 2;
+    static constexpr int kStages = 4;
+    static constexpr uint32_t kStageBytes = 2 * kSubBytes;
+    // [K][V][ring: Q_s, dO_s][statistics: (lse log2 e, D) x 64 a stage][barriers]
+    static constexpr uint32_t kOffRing = 2 * kResBytes;
+    static constexpr uint32_t kOffStat = kOffRing + kStages * kStageBytes;
+    static constexpr uint32_t kOffBar = kOffStat + kStages * 2 * BS * 4;
+    static constexpr int kBars = 1 + 2 * kStages + 6;
+    static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16 + 1024;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+constexpr uint32_t kColBuf = 128, kColDP = 64;
+__host__ __device__ constexpr uint32_t packed_col(int kk)
+{
+    return uint32_t(32 * (kk >> 1) + 8 * (kk & 1));
+}
+
+// 64-query sub-tiles of a sequence that have a key of tile kt in their window: [2 kt,
+// near_end); those behind it see the tile's sinks alone.
+__device__ __forceinline__ int near_end(int kt, int window, int L)
+{
+    const int n_sub = (L + BS - 1) / BS;
+    const int64_t e = (int64_t(kt) * BT + BT - 1 + window + BS - 1) / BS;
+    return e < n_sub ? int(e) : n_sub;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_window_dkdv_kernel(const __grid_constant__ Params p)
+{
+    using C = CfgK<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    uint64_t *a_full = bars, *kv_full = bars + 1, *kv_empty = kv_full + C::kStages;
+    uint64_t *s_full = kv_empty + C::kStages, *p_full = s_full + 2, *o_full = s_full + 4,
+             *drain = s_full + 5;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // work item: the far pieces of the sinks' tiles first, then every key tile's window
+    const WindowArgs &a = p.a;
+    const int bh_count = a.B * a.Hkv;
+    const int far_items = (p.slots - 1) * p.sink_tiles;       // of a (sequence, kv head)
+    int bh, kt, slot;
+    {
+        const unsigned far = unsigned(far_items) * unsigned(bh_count);
+        if (blockIdx.x < far) {
+            bh = int(blockIdx.x % unsigned(bh_count));
+            const int f = int(blockIdx.x / unsigned(bh_count));
+            kt = f % p.sink_tiles;
+            slot = 1 + f / p.sink_tiles;
+        } else {
+            const unsigned rest = blockIdx.x - far;
+            bh = int(rest / unsigned(p.n_tiles));
+            kt = int(rest % unsigned(p.n_tiles));
+            slot = 0;
+        }
+    }
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    WindowSeq sq;
+    if (!window_seq(a, b, sq) || kt * BT >= sq.L)   // (a bad one is flagged by the dQ kernel)
+        return;
+    const int L = sq.L;
+    const int n_sub = (L + BS - 1) / BS;
+    const int near = near_end(kt, a.window, L);
+    const bool in_parts = kt < p.sink_tiles && near < n_sub;  // several CTAs form this tile's sums
+    int s0 = 2 * kt, s1 = near;                               // 64-query sub-tiles
+    if (slot > 0) {
+        s0 = near + (slot - 1) * p.piece;
+        s1 = min(s0 + p.piece, n_sub);
+        if (s0 >= s1)
+            return;
+    }
+    const int n_i = s1 - s0, n_q = n_i * p.G;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(a_full, 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            ptx::mbar_init(&kv_full[s], 32);         // the load warp's lanes
+            ptx::mbar_init(&kv_empty[s], 1);
+        }
+        for (int k = 0; k < 2; ++k) {
+            ptx::mbar_init(&s_full[k], 1);
+            ptx::mbar_init(&p_full[k], kRowWarps);
+        }
+        ptx::mbar_init(o_full, 1);
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        ptx::tmem_alloc(tmem_slot, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    if (warp == kWarpLoad && lane == 0) {
+        ptx::prefetch_tmap(&p.tm_q);
+        ptx::prefetch_tmap(&p.tm_do);
+        ptx::prefetch_tmap(&p.tm_k);
+        ptx::prefetch_tmap(&p.tm_v);
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    bool aborted = false;
+    uint8_t *tile_k = smem, *tile_v = smem + C::kResBytes;
+    uint8_t *ring = smem + C::kOffRing;
+    float *stats = reinterpret_cast<float *>(smem + C::kOffStat);
+
+    if (warp == kWarpLoad) {
+        // ======================= TMA producer (whole warp) ===================
+        int last_phase[C::kStages];
+        for (int s = 0; s < C::kStages; ++s)
+            last_phase[s] = -1;
+        if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(a_full, 2 * C::kResBytes);
+            for (int c = 0; c < C::kChunks; ++c) {
+                ptx::tma_load_4d(tile_k + c * kChunkBytes, &p.tm_k, a_full, c * 64, 0, hk,
+                                 int(sq.k0 + int64_t(kt) * BT));
+                ptx::tma_load_4d(tile_v + c * kChunkBytes, &p.tm_v, a_full, c * 64, 0, hk,
+                                 int(sq.k0 + int64_t(kt) * BT));
+            }
+        }
+        int stage = 0;
+        uint32_t phase = 0;
+        int h = hk * p.G, i = s0;
+        for (int s = 0; s < n_q; ++s) {
+            const int64_t stat0 = stat_row(a, b, h, sq.q0);
+            float ls[BS / 32], ds[BS / 32];
+#pragma unroll
+            for (int u = 0; u < BS / 32; ++u) {
+                const int q = i * BS + lane * (BS / 32) + u;
+                ls[u] = q < L ? a.lse[stat0 + q] : 0.f;
+                ds[u] = q < L ? p.D[stat0 + q] : 0.f;
+            }
+            int ok = 1;
+            if (lane == 0)
+                ok = ptx::mbar_wait(&kv_empty[stage], phase ^ 1u, abort_flag, a.err_word) ? 1 : 0;
+            if (!__shfl_sync(0xffffffffu, ok, 0))
+                break;
+            if (lane == 0) {
+                uint8_t *dst = ring + stage * C::kStageBytes;
+                const int row = int(sq.q0 + int64_t(i) * BS);
+                ptx::mbar_expect_tx(&kv_full[stage], C::kStageBytes);
+                for (int c = 0; c < C::kChunks; ++c) {
+                    ptx::tma_load_4d(dst + c * kSubChunkBytes, &p.tm_q, &kv_full[stage], c * 64, 0,
+                                     h, row);
+                    ptx::tma_load_4d(dst + C::kSubBytes + c * kSubChunkBytes, &p.tm_do,
+                                     &kv_full[stage], c * 64, 0, h, row);
+                }
+                last_phase[stage] = int(phase);
+            }
+            float *st = stats + stage * (2 * BS);
+#pragma unroll
+            for (int u = 0; u < BS / 32; ++u) {
+                st[lane * (BS / 32) + u] = ls[u] * kLog2e;
+                st[BS + lane * (BS / 32) + u] = ds[u];
+            }
+            ptx::mbar_arrive(&kv_full[stage]);       // all lanes, after their writes
+            if (++stage == C::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            if (++i == s1) {
+                i = s0;
+                ++h;
+            }
+        }
+        if (lane == 0 && *abort_flag) {
+            drain_wait(a_full, 0);
+            for (int s = 0; s < C::kStages; ++s)
+                if (last_phase[s] >= 0)
+                    drain_wait(&kv_full[s], uint32_t(last_phase[s]));
+        }
+        __syncwarp();
+    } else if (warp == kWarpMma) {
+        // ======================= MMA issuer (whole warp) =====================
+        // Order: S^T_0, dP^T_0; per step s: S^T_{s+1}, dP^T_{s+1} (other buffer), dV +=
+        // P^T_s dO_s, dK += dS^T_s Q_s.
+        constexpr uint32_t idesc_ss = ptx::idesc_bf16_f32(BT, BS, false);
+        constexpr uint32_t idesc_ts = ptx::idesc_bf16_f32(BT, D, true);
+        constexpr uint64_t desc_kmajor = ptx::smem_desc_base(16, 1024);
+        constexpr uint64_t desc_mnmajor = ptx::smem_desc_base(kSubChunkBytes, 1024);
+        const uint64_t dk = ptx::smem_desc(desc_kmajor, ptx::smem_u32(tile_k));
+        const uint64_t dvk = ptx::smem_desc(desc_kmajor, ptx::smem_u32(tile_v));
+        const uint32_t ring_addr = ptx::smem_u32(ring);
+        int stage = 0, i = s0;
+        uint32_t phase = 0;
+        int st0 = 0, st1 = 0;                       // ring stage of the step in each buffer
+        auto issue_s = [&](int s) -> bool {
+            if (!ptx::mbar_wait_warp(&kv_full[stage], phase, abort_flag, a.err_word))
+                return false;
+            (s & 1 ? st1 : st0) = stage;
+            if ((i + 1) * BS > L) {                 // rows behind the sequence's end
+                clear_rows<2 * C::kChunks>(ring + stage * C::kStageBytes, L - i * BS, BS,
+                                           kSubChunkBytes);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (++i == s1)
+                i = s0;
+            const uint32_t qaddr = ring_addr + stage * C::kStageBytes;
+            if (++stage == C::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            ptx::tc_fence_after_sync();
+            const uint64_t dq = ptx::smem_desc(desc_kmajor, qaddr);
+            const uint64_t ddo = ptx::smem_desc(desc_kmajor, qaddr + C::kSubBytes);
+            const uint32_t buf = tmem + uint32_t(s & 1) * kColBuf;
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    ptx::mma_ss(buf, dk + kmajor_off(kk, kChunkBytes),
+                                dq + kmajor_off(kk, kSubChunkBytes), idesc_ss, kk > 0 ? 1u : 0u);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    ptx::mma_ss(buf + kColDP, dvk + kmajor_off(kk, kChunkBytes),
+                                ddo + kmajor_off(kk, kSubChunkBytes), idesc_ss, kk > 0 ? 1u : 0u);
+                ptx::mma_commit(&s_full[s & 1]);
+            }
+            __syncwarp();
+            return true;
+        };
+        do {
+            if (!ptx::mbar_wait_warp(a_full, 0, abort_flag, a.err_word) || !issue_s(0)) {
+                aborted = true;
+                break;
+            }
+            for (int s = 0; s < n_q; ++s) {
+                if ((s + 1 < n_q && !issue_s(s + 1)) ||
+                    !ptx::mbar_wait_warp(&p_full[s & 1], uint32_t(s >> 1) & 1u, abort_flag,
+                                         a.err_word)) {
+                    aborted = true;
+                    break;
+                }
+                ptx::tc_fence_after_sync();
+                const int st = (s & 1) ? st1 : st0;
+                const uint32_t qaddr = ring_addr + st * C::kStageBytes;
+                const uint64_t dq_mn = ptx::smem_desc(desc_mnmajor, qaddr);
+                const uint64_t ddo_mn = ptx::smem_desc(desc_mnmajor, qaddr + C::kSubBytes);
+                const uint32_t a_tm = tmem + uint32_t(s & 1) * kColBuf;
+                if (ptx::elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < BS / 16; ++kk)
+                        ptx::mma_ts(tmem + kColAcc, a_tm + packed_col(kk),
+                                    ddo_mn + uint64_t((kk * 16 * 128) >> 4), idesc_ts,
+                                    (s > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+                    for (int kk = 0; kk < BS / 16; ++kk)
+                        ptx::mma_ts(tmem + kColAcc + D, a_tm + kColDP + packed_col(kk),
+                                    dq_mn + uint64_t((kk * 16 * 128) >> 4), idesc_ts,
+                                    (s > 0 || kk > 0) ? 1u : 0u);
+                    ptx::mma_commit(&kv_empty[st]);
+                }
+                __syncwarp();
+            }
+        } while (false);
+        if (ptx::elect_one()) {
+            if (!aborted)
+                ptx::mma_commit(o_full);
+            ptx::mma_commit(drain);
+            drain_wait(drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ======================= key rows ==================================
+        const int r = (warp & 3) * 32 + lane;        // key of the tile = TMEM lane
+        const int g = warp >> 2;                     // column group
+        const int k = kt * BT + r;
+        const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
+        const float sl = p.scale_log2;
+        const int col0 = g * 32;
+        // queries that see the key: k .. last
+        const int64_t end = k < a.sinks ? int64_t(L) : int64_t(k) + a.window;
+        const int last = int(end < L ? end : L) - 1;
+        int i = s0;
+        for (int s = 0; s < n_q; ++s) {
+            // the statistics arrive with the step's ring stage
+            const int st = s % C::kStages;
+            if (!row_wait(&kv_full[st], uint32_t(s / C::kStages) & 1u, abort_flag, a.err_word)) {
+                aborted = true;
+                break;
+            }
+            float lv[32], dd[32];
+            {
+                const float *lse2s = stats + st * (2 * BS) + col0;
+#pragma unroll
+                for (int e4 = 0; e4 < 8; ++e4) {
+                    const float4 l4 = *reinterpret_cast<const float4 *>(lse2s + 4 * e4);
+                    const float4 d4 = *reinterpret_cast<const float4 *>(lse2s + BS + 4 * e4);
+                    lv[4 * e4] = l4.x;
+                    lv[4 * e4 + 1] = l4.y;
+                    lv[4 * e4 + 2] = l4.z;
+                    lv[4 * e4 + 3] = l4.w;
+                    dd[4 * e4] = d4.x;
+                    dd[4 * e4 + 1] = d4.y;
+                    dd[4 * e4 + 2] = d4.z;
+                    dd[4 * e4 + 3] = d4.w;
+                }
+            }
+            if (!row_wait(&s_full[s & 1], uint32_t(s >> 1) & 1u, abort_flag, a.err_word)) {
+                aborted = true;
+                break;
+            }
+            ptx::tc_fence_after_sync();
+            const int lo = k - i * BS - col0, hi = last - i * BS - col0;   // seen columns
+            const uint32_t tS = tmem + lane_bits + uint32_t(s & 1) * kColBuf + col0;
+            uint32_t sv[32], dv[32], pk[16], dk[16];
+            ptx::tmem_ld32(tS, sv);
+            ptx::tmem_ld32(tS + kColDP, dv);
+            ptx::tmem_wait_ld();
+            if (__any_sync(0xffffffffu, lo > 0 || hi < 31)) {
+                const uint32_t seen = low_bits(hi + 1) & ~low_bits(lo);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (!(seen & (1u << e)))
+                        sv[e] = __float_as_uint(-INFINITY);
+            }
+#pragma unroll
+            for (int e2 = 0; e2 < 16; ++e2) {
+                float pv[2], ds[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int e = 2 * e2 + u;
+                    pv[u] = ptx::ex2(fmaf(__uint_as_float(sv[e]), sl, -lv[e]));
+                    ds[u] = pv[u] * (__uint_as_float(dv[e]) - dd[e]);
+                }
+                pk[e2] = ptx::pack_bf16x2(pv[0], pv[1]);
+                dk[e2] = ptx::pack_bf16x2(ds[0], ds[1]);
+            }
+            ptx::tmem_st16(tS, pk);                   // P^T of this block, packed
+            ptx::tmem_st16(tS + kColDP, dk);          // dS^T of this block, packed
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(&p_full[s & 1]);
+            if (++i == s1)
+                i = s0;
+        }
+        if (!aborted && ptx::mbar_wait(o_full, 0, abort_flag, a.err_word)) {
+            ptx::tc_fence_after_sync();
+            const bool key_ok = k < L;
+            // group 0 writes dV, group 1 dK
+            const uint32_t acc = tmem + lane_bits + kColAcc + uint32_t(g * D);
+            const float mul = g == 0 ? 1.f : a.scale;
+            if (in_parts) {
+                float *part = p.parts + (((int64_t(bh) * p.sink_tiles + kt) * p.slots + slot) * 2 + g) *
+                                            (BT * D) + r * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    ptx::tmem_ld32(acc + c * 32, o);
+                    ptx::tmem_wait_ld();
+                    if (key_ok)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            *reinterpret_cast<float4 *>(part + c * 32 + 4 * q) =
+                                make_float4(__uint_as_float(o[4 * q]) * mul,
+                                            __uint_as_float(o[4 * q + 1]) * mul,
+                                            __uint_as_float(o[4 * q + 2]) * mul,
+                                            __uint_as_float(o[4 * q + 3]) * mul);
+                }
+            } else {
+                __nv_bfloat16 *dst = g == 0 ? p.dV + (sq.k0 + k) * p.dv_stride
+                                            : p.dK + (sq.k0 + k) * p.dk_stride;
+                store_row(acc, mul, dst + int64_t(hk) * D, key_ok, 0, D / 32);
+            }
+        }
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    if (warp == kWarpMma)
+        ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+// A sink tile's parts added in order: a warp a row of dV or dK.
+template <int D>
+__global__ void __launch_bounds__(256) attn_window_join_kernel(const __grid_constant__ Params p)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const WindowArgs &a = p.a;
+    const int lane = threadIdx.x & 31;
+    const int64_t item = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int r = int(item % BT);
+    const int g = int(item / BT % 2), kt = int(item / (2 * BT) % p.sink_tiles);
+    const int bh = int(item / (2 * BT) / p.sink_tiles);
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    WindowSeq sq;
+    if (!window_seq(a, b, sq) || kt * BT + r >= sq.L)
+        return;
+    const int n_sub = (sq.L + BS - 1) / BS, near = near_end(kt, a.window, sq.L);
+    if (near >= n_sub)
+        return;
+    const int n = 1 + (n_sub - near + p.piece - 1) / p.piece;
+    const float *part = p.parts + (((int64_t(bh) * p.sink_tiles + kt) * p.slots) * 2 + g) * (BT * D) +
+                        r * D + lane * (D / 32);
+    float v[D / 32] = {};
+    for (int s = 0; s < n; ++s, part += 2 * BT * D)
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+            v[e] += part[e];
+    const int64_t row = sq.k0 + kt * BT + r;
+    __nv_bfloat16 *dst = (g == 0 ? p.dV + row * p.dv_stride : p.dK + row * p.dk_stride) +
+                         int64_t(hk) * D + lane * (D / 32);
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2)
+        *reinterpret_cast<uint32_t *>(dst + e) = ptx::pack_bf16x2(v[e], v[e + 1]);
+}
+
+template <int D>
+int launch_d(const Params &pq, const Params &pk, int64_t dq_blocks, int64_t kv_blocks,
+             int64_t join_blocks, cudaStream_t stream)
+{
+    auto kq = attn_window_dq_kernel<D>;
+    auto kk = attn_window_dkdv_kernel<D>;
+    static PerDeviceOnce once_q, once_k;
+    constexpr int smem_q = int(CfgQ<D>::kSmemBytes), smem_k = int(CfgK<D>::kSmemBytes);
+    if (!set_max_dynamic_smem(once_q, reinterpret_cast<const void *>(kq), smem_q) ||
+        !set_max_dynamic_smem(once_k, reinterpret_cast<const void *>(kk), smem_k) ||
+        launch_early(kq, dim3(unsigned(dq_blocks)), kThreads, smem_q, stream, pq) != cudaSuccess ||
+        launch_early(kk, dim3(unsigned(kv_blocks)), kThreads, smem_k, stream, pk) != cudaSuccess)
+        return FA_ERR_CUDA;
+    if (join_blocks > 0 && launch_early(attn_window_join_kernel<D>, dim3(unsigned(join_blocks)), 256, 0,
+                                        stream, pk) != cudaSuccess)
+        return FA_ERR_CUDA;
+    return FA_OK;
+}
+
+}  // namespace
+
+int launch_attention_window_bwd(const WindowBwdArgs &w, cudaStream_t stream)
+{
+    const WindowArgs &a = w.a;
+    const WindowBwdLayout lay = window_bwd_layout(a.B, a.Nq, a.total_q, a.H, a.Hkv, a.d, a.window,
+                                                  a.sinks);
+    Params pq{};
+    pq.a = a;
+    uint8_t *ws = static_cast<uint8_t *>(w.workspace);
+    pq.D = reinterpret_cast<float *>(ws + lay.D);
+    pq.parts = reinterpret_cast<float *>(ws + lay.parts);
+    pq.dQ = static_cast<__nv_bfloat16 *>(w.dQ);
+    pq.dK = static_cast<__nv_bfloat16 *>(w.dK);
+    pq.dV = static_cast<__nv_bfloat16 *>(w.dV);
+    pq.dq_stride = w.dq_stride;
+    pq.dk_stride = w.dk_stride;
+    pq.dv_stride = w.dv_stride;
+    pq.G = a.H / a.Hkv;
+    pq.P = BT / pq.G;
+    pq.n_tiles = (a.Nq + pq.P - 1) / pq.P;
+    pq.sink_tiles = lay.sink_tiles;
+    pq.slots = lay.slots;
+    pq.piece = lay.piece;
+    pq.scale_log2 = float(double(a.scale) * 1.4426950408889634);
+    Params pk = pq;
+    pk.n_tiles = (a.Nq + BT - 1) / BT;
+    const int64_t bh = int64_t(a.B) * a.Hkv;
+    const int64_t dq_blocks = pq.n_tiles * bh;
+    const int64_t kv_blocks = (pk.n_tiles + int64_t(lay.slots - 1) * lay.sink_tiles) * bh;
+    const int64_t join_blocks = lay.slots > 1 ? bh * lay.sink_tiles * (2 * BT / 8) : 0;
+    if (dq_blocks > 0x7fffffffLL || kv_blocks > 0x7fffffffLL || join_blocks > 0x7fffffffLL)
+        return FA_ERR_TOO_LARGE;
+    const int64_t row = int64_t(a.H) * a.d;
+    if (!make_tmap_heads(&pq.tm_q, a.Q, a.total_q, a.Hkv, pq.G, a.d, a.q_stride, pq.P) ||
+        !make_tmap_heads(&pq.tm_do, w.dO, a.total_q, a.Hkv, pq.G, a.d, row, pq.P) ||
+        !make_tmap_heads(&pq.tm_k, a.K, a.total_k, a.Hkv, 1, a.d, a.k_stride, BT) ||
+        !make_tmap_heads(&pq.tm_v, a.V, a.total_k, a.Hkv, 1, a.d, a.v_stride, BT) ||
+        !make_tmap_heads(&pq.tm_k32, a.K, a.total_k, a.Hkv, 1, a.d, a.k_stride, kPad) ||
+        !make_tmap_heads(&pq.tm_v32, a.V, a.total_k, a.Hkv, 1, a.d, a.v_stride, kPad) ||
+        !make_tmap_heads(&pk.tm_q, a.Q, a.total_q, a.H, 1, a.d, a.q_stride, BS) ||
+        !make_tmap_heads(&pk.tm_do, w.dO, a.total_q, a.H, 1, a.d, row, BS))
+        return FA_ERR_CUDA;
+    pk.tm_k = pq.tm_k;
+    pk.tm_v = pq.tm_v;
+    return a.d == 64 ? launch_d<64>(pq, pk, dq_blocks, kv_blocks, join_blocks, stream)
+                     : launch_d<128>(pq, pk, dq_blocks, kv_blocks, join_blocks, stream);
+}
+
+}  // namespace fa

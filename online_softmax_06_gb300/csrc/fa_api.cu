@@ -1164,6 +1164,70 @@ int fa_attention_window_fwd(const void *Q, int64_t q_stride, const void *K, int6
     return fa::launch_attention_window(a, fa::t_stream);
 }
 
+int64_t fa_attention_window_bwd_workspace_bytes(int B, int N, int64_t total, int H, int Hkv, int d,
+                                                int window, int sinks)
+{
+    if (B < 0 || N < 0 || total < 0 || H < 0 || window < 1 || sinks < 0 ||
+        (H > 0 && (Hkv < 1 || H % Hkv != 0)))
+        return FA_ERR_BAD_SIZE;
+    if (d != 64 && d != 128)
+        return FA_ERR_UNSUPPORTED;
+    if (B == 0 || N == 0 || total == 0 || H == 0)
+        return 0;
+    if (total > (int64_t(1) << 31) - 512)
+        return FA_ERR_TOO_LARGE;
+    return fa::window_bwd_layout(B, N < total ? N : int(total), total, H, Hkv, d, window, sinks)
+        .bytes;
+}
+
+int fa_attention_window_bwd(const void *Q, int64_t q_stride, const void *K, int64_t k_stride,
+                            const void *V, int64_t v_stride, const void *O, const void *dO,
+                            const float *lse, void *dQ, int64_t dq_stride, void *dK,
+                            int64_t dk_stride, void *dV, int64_t dv_stride, int B, int N,
+                            int64_t total, int H, int Hkv, int d, float scale, int window,
+                            int sinks, const int32_t *cu_seqlens, void *workspace,
+                            int64_t workspace_bytes)
+{
+    fa::WindowBwdArgs w;
+    bool empty;
+    const int rc = fa::check_window(Q, q_stride, K, k_stride, V, v_stride, O, lse, B, N, total, N,
+                                    total, H, Hkv, d, scale, window, sinks, cu_seqlens, cu_seqlens,
+                                    nullptr, &w.a, &empty);
+    if (rc != FA_OK || empty)
+        return rc;
+    if (!dO || !dQ || !dK || !dV || !workspace)
+        return FA_ERR_NULL_POINTER;
+    if (dq_stride < int64_t(H) * d || dk_stride < int64_t(Hkv) * d ||
+        dv_stride < int64_t(Hkv) * d ||
+        workspace_bytes <
+            fa_attention_window_bwd_workspace_bytes(B, N, total, H, Hkv, d, window, sinks))
+        return FA_ERR_BAD_SIZE;
+    if (!fa::aligned(dO, 16) || !fa::aligned(dQ, 16) || !fa::aligned(dK, 16) ||
+        !fa::aligned(dV, 16) || !fa::aligned(workspace, 256) || dq_stride % 8 != 0 ||
+        dk_stride % 8 != 0 || dv_stride % 8 != 0)
+        return FA_ERR_MISALIGNED;
+    const int64_t limit = (int64_t(1) << 31) - 512;
+    if (dq_stride > limit || dk_stride > limit || dv_stride > limit)
+        return FA_ERR_TOO_LARGE;
+    fa::DeviceInfo *dev = fa::current_device();
+    if (dev == nullptr)
+        return FA_ERR_NO_DEVICE;
+    w.dO = dO;
+    w.dQ = dQ;
+    w.dK = dK;
+    w.dV = dV;
+    w.dq_stride = dq_stride;
+    w.dk_stride = dk_stride;
+    w.dv_stride = dv_stride;
+    w.workspace = workspace;
+    if (sinks >= w.a.Nq)                   // every earlier key is seen
+        w.a.window = w.a.Nq;
+    w.a.err_word = dev->err_word;
+    w.a.expire_wait_ns = fa::t_expire_wait_ns;
+    fa::t_expire_wait_ns = 0;
+    return fa::launch_attention_window_bwd(w, fa::t_stream);
+}
+
 int fa_attention_fwd_f32(const float *Q, const float *K, const float *V, float *O, float *lse,
                          int B, int H, int N, int d, float scale, int causal,
                          const int32_t *cu_seqlens)

@@ -356,6 +356,43 @@ struct WindowArgs {
 };
 int launch_attention_window(const WindowArgs &a, cudaStream_t stream);
 
+// Its gradient: a's queries and keys are the same tokens, O and lse read.
+struct WindowBwdArgs {
+    WindowArgs a;
+    const void *dO;
+    void *dQ, *dK, *dV;
+    int64_t dq_stride, dk_stride, dv_stride;
+    void *workspace;
+};
+// Its workspace: D, laid out as lse, and the fp32 parts of the tiles with sinks in
+// them: their window's, and one for each `piece` sub-tiles of 64 queries behind it.  A
+// piece is as long as a window's steps (its CTA takes as long as another one's), and
+// has 16 sub-tiles at least, which pays for its part.
+struct WindowBwdLayout {
+    int64_t D, parts, bytes;
+    int sink_tiles, slots, piece;
+};
+inline WindowBwdLayout window_bwd_layout(int B, int N, int64_t total, int H, int Hkv, int d,
+                                         int window, int sinks)
+{
+    auto up = [](int64_t x) { return (x + 255) & ~int64_t(255); };
+    WindowBwdLayout L;
+    if (sinks >= N)            // every earlier key is seen
+        window = N;
+    const int64_t n_sub = (int64_t(N) + 63) / 64, near = (int64_t(window) + 127 + 63) / 64;
+    L.piece = int(near < 16 ? 16 : near > n_sub ? n_sub : near);
+    // tile 0 has the most queries behind its window
+    const int64_t far = n_sub > near ? (n_sub - near + L.piece - 1) / L.piece : 0;
+    L.slots = sinks > 0 && far > 0 ? int(far) + 1 : 1;
+    const int64_t tiles = ((sinks < N ? sinks : N) + 127) / 128;
+    L.sink_tiles = L.slots > 1 ? int(tiles) : 0;
+    L.D = 0;
+    L.parts = up(total * H * 4);
+    L.bytes = L.parts + (L.slots > 1 ? int64_t(B) * Hkv * tiles * L.slots * 2 * 128 * d * 4 : 0);
+    return L;
+}
+int launch_attention_window_bwd(const WindowBwdArgs &a, cudaStream_t stream);
+
 // Norm and rotation of the heads of Q (index 0) and K (1), and its gradient.
 struct NormRopeArgs {
     const void *x[2], *g[2];   // inputs; backward: gradients of the outputs

@@ -74,4 +74,16 @@ __device__ __forceinline__ WindowKeys window_keys(int window, int sinks, int i0,
     return w;
 }
 
+// The lowest `n` bits, n clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t low_bits(int n)
+{
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// Which of the 32 places from v on a query sees.
+__device__ __forceinline__ uint32_t window_bits(int v, int vlo, int vhi, int sinks)
+{
+    return low_bits(vhi - v + 1) & (~low_bits(vlo - v) | low_bits(sinks - v));
+}
+
 }  // namespace fa

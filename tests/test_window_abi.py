@@ -40,6 +40,39 @@ def test_forward_refusals():
     assert fwd(H=0, Hkv=0) == fa.FA_OK
 
 
+def bwd(**kw):
+    a = dict(q=P, qs=512, k=P, ks=256, v=P, vs=256, o=P, do=P, lse=P, dq=P, dqs=512, dk=P, dks=256, dv=P, dvs=256, B=2,
+             N=40, total=80, H=4, Hkv=2, d=128, scale=0.1, window=8, sinks=2, cu=None, ws=P, n=1 << 30)
+    a.update(kw)
+    return fa.fa_attention_window_bwd(*a.values())
+
+
+def test_gradient_refusals():
+    for bad in (dict(B=-1), dict(N=-1), dict(total=81), dict(window=0), dict(sinks=-1), dict(H=5), dict(Hkv=0),
+                dict(scale=0.0), dict(qs=504), dict(dqs=504), dict(dks=128), dict(dvs=248), dict(n=100)):
+        assert bwd(**bad) == fa.FA_ERR_BAD_SIZE, bad
+    for bad in (dict(d=96), dict(H=258, qs=258 * 128)):
+        assert bwd(**bad) == fa.FA_ERR_UNSUPPORTED, bad
+    for x in ("q", "k", "v", "o", "do", "lse", "dq", "dk", "dv", "ws"):
+        assert bwd(**{x: None}) == fa.FA_ERR_NULL_POINTER, x
+    for bad in (dict(do=P + 8), dict(dq=P + 2), dict(dv=P + 8), dict(ws=P + 128), dict(cu=P + 2), dict(dks=260)):
+        assert bwd(**bad) == fa.FA_ERR_MISALIGNED, bad
+    assert bwd(total=1 << 31, cu=P) == fa.FA_ERR_TOO_LARGE
+    assert bwd(total=0, cu=P) == fa.FA_OK
+
+
+def test_gradient_workspace():
+    n = fa.fa_attention_window_bwd_workspace_bytes
+    assert n(1, 100, 100, 4, 2, 96, 8, 0) == fa.FA_ERR_UNSUPPORTED
+    assert n(1, 100, 100, 4, 3, 64, 8, 0) == fa.FA_ERR_BAD_SIZE
+    assert n(0, 100, 0, 4, 2, 64, 8, 0) == 0
+    assert n(2, 1000, 2000, 4, 2, 64, 8, 0) == 2000 * 4 * 4                     # D alone
+    assert n(2, 1000, 2000, 4, 2, 64, 1000, 4) == 2000 * 4 * 4                  # no query behind the window
+    assert n(2, 1000, 2000, 4, 2, 64, 8, 1000) == 2000 * 4 * 4                  # all keys are sinks
+    # 1000 tokens: 16 sub-tiles of 64, three of them near the sinks' tile: one piece behind
+    assert n(2, 1000, 2000, 4, 2, 64, 8, 4) == 2000 * 4 * 4 + 2 * 2 * 2 * 2 * 128 * 64 * 4
+
+
 def test_oracle_gradient():
     rng = np.random.default_rng(0)
     q, k, v = rng.standard_normal((5, 4, 8)), rng.standard_normal((7, 2, 8)), rng.standard_normal((7, 2, 8))

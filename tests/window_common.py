@@ -93,4 +93,42 @@ def check_forward(batch, o, lse, window, sinks, scale=None):
         assert np.all(err <= tol), ("lse", b, (err / tol).max())
 
 
-__all__ = ["Batch", "bf16", "check_forward", "f64", "fa", "layer", "score_error"]
+def check_gradients(batch, do, grads, window, sinks, scale=None):
+    """dS is rounded to bf16 (2^-8), as is P; D = dO . O has O's rounding (2^-7 of |dO| |O| and what
+    P's does to it); the gradients are rounded at the end.  do: float64 [n, H, d] per sequence."""
+    scale = batch.d ** -0.5 if scale is None else scale
+    at = np.concatenate(([0], np.cumsum(batch.n)))
+    for b in range(len(batch.n)):
+        q, k, v, g = f64(batch.q[b]), f64(batch.k[b]), f64(batch.v[b]), do[b]
+        if len(q) == 0:
+            continue
+        n, H, d = q.shape
+        G = H // k.shape[1]
+        ref = layer.window_attention_bwd(q, k, v, g, window, sinks, scale)
+        O, lse = layer.window_attention(q, k, v, window, sinks, scale)
+        spread = layer.window_attention(q, k, np.abs(v), window, sinks, scale)[0]
+        ds_err = score_error(q, k, scale, d)                      # relative error of P
+        seen = layer.window_seen(n, len(k), window, sinks)
+        tol = [np.zeros_like(x) for x in ref]
+        for h in range(H):
+            kh, vh = k[:, h // G], v[:, h // G]
+            p = np.where(seen, np.exp(np.where(seen, q[:, h] @ kh.T * scale - lse[h][:, None], -np.inf)), 0)
+            dp = g[:, h] @ vh.T
+            mass = np.abs(g[:, h]) @ np.abs(vh).T                 # what dP sums
+            D = (g[:, h] * O[:, h]).sum(1, keepdims=True)
+            # D's error: O's in each value, times dO; sums of d products in fp32
+            eo = (2.0 ** -8 + 2 * ds_err[:, h]) * spread[:, h] + 2.0 ** -7 * np.abs(O[:, h])
+            eD = (np.abs(g[:, h]) * eo).sum(1, keepdims=True)
+            e = p * (eD + d * 2.0 ** -24 * mass) + (2.0 ** -8 + 2 * ds_err[:, h] + 2.0 ** -20) * p * np.abs(dp - D)
+            tol[0][:, h] = e @ np.abs(kh) * scale
+            tol[1][:, h // G] += e.T @ np.abs(q[:, h]) * scale
+            tol[2][:, h // G] += ((2.0 ** -8 + 2 * ds_err[:, h] + 2.0 ** -20) * p).T @ np.abs(g[:, h])
+        for name, got, r, t in zip("qkv", grads, ref, tol):
+            got = f64(got)
+            got = got[b] if batch.form == "dense" else got[at[b]:at[b + 1]]
+            t = t + 2.0 ** -8 * (np.abs(r) + t) + 1e-12
+            err = np.abs(got - r)
+            assert np.all(err <= t), ("d" + name, b, np.unravel_index(np.argmax(err / t), err.shape), (err / t).max())
+
+
+__all__ = ["Batch", "bf16", "check_forward", "check_gradients", "f64", "fa", "layer", "score_error"]
