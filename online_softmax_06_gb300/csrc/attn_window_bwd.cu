@@ -9,7 +9,12 @@
 // atomics; then, where sinks are seen from outside their tile's window, a third:
 //   * attn_window_dq_kernel: a CTA per (sequence, kv head, 128 rows: queries x G
 //     heads), the keys that they see in 128-key steps, the window's behind the
-//     sinks' as in the forward (window.cuh).  Also writes D.
+//     sinks' as in the forward (window.cuh).  Also writes D.  D comes from O rounded
+//     to bf16, an error e that all keys of a row share: dQ is off by e sum_j P_ij K_j,
+//     which grows against dQ where keys have a part in common and the window is long
+//     (2^-9 of dQ becomes 2^-7.5 with a window of 2048).  But sum_j dS_ij is 0, so its
+//     computed value r_i is the error's, and r_i times a mean of the keys is taken off
+//     (the common part; of 16 rows a step, which the row warps read beside their work).
 //   * attn_window_dkdv_kernel: a CTA per (sequence, kv head, 128 keys); 64-query
 //     steps over the queries that have these keys in their window, one head of the
 //     group after the other into the same accumulators.  Keys below `sinks` are seen
@@ -103,15 +108,21 @@ __device__ __forceinline__ uint64_t kmajor_off(int kk, uint32_t chunk_bytes)
     return uint64_t(((kk >> 2) * chunk_bytes + (kk & 3) * 32) >> 4);
 }
 
-// Columns [32 c0, 32 c1) of this thread's row of an accumulator times `mul`, as bf16.
+// Columns [32 c0, 32 c1) of this thread's row of an accumulator, plus `more` times the
+// values at `add` where given, times `mul`, as bf16.
 __device__ __forceinline__ void store_row(uint32_t t_acc, float mul, __nv_bfloat16 *dst, bool ok,
-                                          int c0, int c1)
+                                          int c0, int c1, float more = 0.f,
+                                          const float *add = nullptr)
 {
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
         uint32_t o[32];
         ptx::tmem_ld32(t_acc + c * 32, o);
         ptx::tmem_wait_ld();
+        if (add != nullptr)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                o[e] = __float_as_uint(fmaf(more, add[c * 32 + e], __uint_as_float(o[e])));
         if (ok) {
             uint4 *out = reinterpret_cast<uint4 *>(dst + c * 32);
 #pragma unroll
@@ -149,8 +160,11 @@ struct CfgQ {
     static constexpr uint32_t kStageBytes = 2 * kTileBytes;  // K_j, V_j
     static constexpr int kStages = 3;
     static constexpr uint32_t kOffRing = 2 * kTileBytes;
-    static constexpr uint32_t kOffXch = kOffRing + 2 * kStageBytes;   // 128 D_i values
-    static constexpr uint32_t kOffBar = kOffXch + BT * 4;
+    // 128 D_i values, later the rows' sums of dS, [2][128]; the warps' sums of keys
+    // [8][D] and how many
+    static constexpr uint32_t kOffXch = kOffRing + 2 * kStageBytes;
+    static constexpr uint32_t kOffMean = kOffXch + 2 * BT * 4;
+    static constexpr uint32_t kOffBar = kOffMean + kRowWarps * D * 4 + 32;
     static constexpr int kBars = 1 + 2 * kStages + 9;
     static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16 + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -493,13 +507,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         const int64_t vl = int64_t(vhi) - a.window + 1;
         const int vlo = vl > w.sp ? int(vl) : w.sp;
 
+        // two rows of each step's keys a warp, half a warp (d = 64: a quarter) each: 8
+        // values a lane
+        constexpr int kKeyLanes = D / 8;
+        float key_sum[8] = {}, ds_sum = 0.f;
+        int key_n = 0;
+
         for (int j = 0; j < n_kv; ++j) {
             const uint32_t par = uint32_t(j) & 1u;
-            if (!row_wait(s_full, par, abort_flag, a.err_word)) {
+            if (!row_wait(s_full, par, abort_flag, a.err_word) ||
+                !row_wait(&kv_full[j % C::kStages], uint32_t(j / C::kStages) & 1u, abort_flag,
+                          a.err_word)) {
                 aborted = true;
                 break;
             }
             ptx::tc_fence_after_sync();
+            {
+                const int kr = warp * 16 + (lane / kKeyLanes) * 8, u = lane % kKeyLanes;
+                if (lane < 2 * kKeyLanes && j * BT + kr < w.places) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(
+                        smem + C::stage_off(j % C::kStages) + (u >> 3) * kChunkBytes + kr * 128 +
+                        (((u & 7) ^ (kr & 7)) << 4));
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        key_sum[2 * e] += __uint_as_float(x[e] << 16);
+                        key_sum[2 * e + 1] += __uint_as_float(x[e] & 0xffff0000u);
+                    }
+                    ++key_n;
+                }
+            }
             const int v0 = j * BT + col0;            // this thread's first place
             const bool masked = __any_sync(0xffffffffu, v0 < vlo || v0 + kQCols - 1 > vhi);
             uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
@@ -549,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                     const float d0 = pr[32 * half + 2 * e] * (__uint_as_float(dv[2 * e]) - Di);
                     const float d1 =
                         pr[32 * half + 2 * e + 1] * (__uint_as_float(dv[2 * e + 1]) - Di);
+                    ds_sum += d0 + d1;
                     pk[16 * half + e] = ptx::pack_bf16x2(d0, d1);
                 }
             }
@@ -559,12 +597,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             if (lane == 0)
                 ptx::mbar_arrive(p_full);
         }
+        // the keys' mean, and the sum of the row's dS over both its threads
+        float *mean = reinterpret_cast<float *>(smem + C::kOffMean);
+        int *mean_n = reinterpret_cast<int *>(mean + kRowWarps * D);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            key_sum[e] += __shfl_down_sync(0xffffffffu, key_sum[e], kKeyLanes);
+        key_n += __shfl_down_sync(0xffffffffu, key_n, kKeyLanes);
+        if (lane < kKeyLanes)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                mean[warp * D + lane * 8 + e] = key_sum[e];
+        if (lane == 0)
+            mean_n[warp] = key_n;
+        asm volatile("bar.sync 1, 256;" ::: "memory");   // (all have read D from xch)
+        xch[g * BT + r] = ds_sum;
+        float km = 0.f;
+        if (threadIdx.x < D) {
+            int n = 0;
+#pragma unroll
+            for (int k = 0; k < kRowWarps; ++k) {
+                km += mean[k * D + threadIdx.x];
+                n += mean_n[k];
+            }
+            km = n > 0 ? km / float(n) : 0.f;
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (threadIdx.x < D)
+            mean[threadIdx.x] = km;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float ri = xch[r] + xch[BT + r];
         // the two threads of a row store half of its dQ each
         if (!aborted && ptx::mbar_wait(o_full, 0, abort_flag, a.err_word)) {
             ptx::tc_fence_after_sync();
             store_row(tmem + lane_bits + kColAcc, a.scale,
                       p.dQ + (sq.q0 + i) * p.dq_stride + int64_t(h) * D, row_ok, g * (D / 64),
-                      (g + 1) * (D / 64));
+                      (g + 1) * (D / 64), -ri, mean);
         }
     }
     ptx::tc_fence_before_sync();

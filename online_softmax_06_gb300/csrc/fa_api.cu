@@ -1159,6 +1159,8 @@ int fa_attention_window_fwd(const void *Q, int64_t q_stride, const void *K, int6
     if (dev == nullptr)
         return FA_ERR_NO_DEVICE;
     a.err_word = dev->err_word;
+    if (fa::window_few(a.Nq, H, Hkv))
+        return fa::launch_attention_window_few(a, fa::t_stream);
     a.expire_wait_ns = fa::t_expire_wait_ns;
     fa::t_expire_wait_ns = 0;
     return fa::launch_attention_window(a, fa::t_stream);

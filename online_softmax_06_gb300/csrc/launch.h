@@ -355,6 +355,9 @@ struct WindowArgs {
     uint32_t expire_wait_ns;   // failure-detection test (fa_debug_expire_next_wait), or 0
 };
 int launch_attention_window(const WindowArgs &a, cudaStream_t stream);
+// The form for few query rows (attn_window_few.cu).
+int launch_attention_window_few(const WindowArgs &a, cudaStream_t stream);
+inline bool window_few(int Nq, int H, int Hkv) { return int64_t(Nq) * (H / Hkv) <= 64; }
 
 // Its gradient: a's queries and keys are the same tokens, O and lse read.
 struct WindowBwdArgs {

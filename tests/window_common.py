@@ -119,8 +119,12 @@ def check_gradients(batch, do, grads, window, sinks, scale=None):
             # D's error: O's in each value, times dO; sums of d products in fp32
             eo = (2.0 ** -8 + 2 * ds_err[:, h]) * spread[:, h] + 2.0 ** -7 * np.abs(O[:, h])
             eD = (np.abs(g[:, h]) * eo).sum(1, keepdims=True)
-            e = p * (eD + d * 2.0 ** -24 * mass) + (2.0 ** -8 + 2 * ds_err[:, h] + 2.0 ** -20) * p * np.abs(dp - D)
-            tol[0][:, h] = e @ np.abs(kh) * scale
+            e = p * (eD + d * 2.0 ** -24 * mass) + (2 * ds_err[:, h] + 2.0 ** -20) * p * np.abs(dp - D)
+            # dQ has the sum of these errors times a mean of the keys taken off, at most the largest key:
+            # sum_j e_j (K_j - mean) in place of sum_j e_j K_j
+            tol[0][:, h] = e.sum(1, keepdims=True) * np.abs(kh).max(0) * scale
+            e = e + 2.0 ** -8 * p * np.abs(dp - D)
+            tol[0][:, h] += e @ np.abs(kh) * scale
             tol[1][:, h // G] += e.T @ np.abs(q[:, h]) * scale
             tol[2][:, h // G] += ((2.0 ** -8 + 2 * ds_err[:, h] + 2.0 ** -20) * p).T @ np.abs(g[:, h])
         for name, got, r, t in zip("qkv", grads, ref, tol):
