@@ -698,7 +698,7 @@ def _kv4_call(torch, index, where, *args):
     """Calls an entry point on the current stream of device `index`, made current."""
     L = _lib or lib()
     L.fa_set_stream(torch._C._cuda_getCurrentRawStream(index))
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         rc = getattr(L, where)(*args)
     else:
         with torch.cuda.device(index):
@@ -931,45 +931,102 @@ def attention_kv4(q, cache, page_table, seqlens, max_seqlen: int | None = None, 
 
 # ---- attention with a sliding window and sinks --------------------------------------
 
-def _window_check(torch, rows, ints):
-    """Types, devices and contiguity; returns the device's index."""
-    index = rows[0].get_device()
+# As with the 4-bit cache, what shapes, strides, types and devices say is checked once for
+# each set of them (a decode step is short enough for the checks to show); new tensors are
+# made with the strides at hand, which takes torch half the time.
+
+def _like(t):
+    """What a plan's checks look at of a tensor, or None."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _dense(shape):
+    """The strides of a contiguous tensor."""
+    stride, n = [], 1
+    for s in reversed(shape):
+        stride.append(n)
+        n *= max(s, 1)
+    return tuple(reversed(stride))
+
+
+def _contiguous(t):
+    shape, stride = t[:2]
+    return 0 in shape or all(a == b or n == 1 for n, a, b in zip(shape, stride, _dense(shape)))
+
+
+def _check_rows(what, rows):
+    """bf16 CUDA tensors on one device, whose index is returned."""
+    import torch
+    index = rows[0][3]
     if index < 0:
-        raise ValueError("q, k and v must be CUDA tensors")
-    for t in rows:
-        if t.dtype is not torch.bfloat16 or t.get_device() != index:
-            raise ValueError("q, k, v and tensors like them must be bf16 and on one device")
-    for t in ints:
-        if t is not None and (t.dtype is not torch.int32 or t.get_device() != index
-                              or not t.is_contiguous() or t.dim() != 1):
-            raise ValueError("cu_seqlens and seqlens must be contiguous int32 tensors, one "
-                             "dimension, on q's device")
+        raise ValueError(f"{what} must be CUDA tensors")
+    if any(t[2] is not torch.bfloat16 or t[3] != index for t in rows):
+        raise ValueError(f"{what} and tensors like them must be bf16 and on one device")
     return index
 
 
-def _plan_window(q, qs, k, ks, v, vs, cu_q, cu_k, seqlens, max_q, max_k):
-    if k != v:
+def _check_vector(t, dtype, index, name):
+    if t is not None and (t[2] is not dtype or t[3] != index or not _contiguous(t)
+                          or len(t[0]) != 1):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor, one dimension, on q's "
+                         "device")
+
+
+def _check_given(t, like, name):
+    """A tensor to write into that the caller passed: shape, dtype and device of `like`."""
+    if not (t.shape == like[0] and t.dtype is like[2] and t.get_device() == like[3]
+            and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {like[2]} tensor {list(like[0])} on q's "
+                         "device")
+
+
+def _check_workspace(torch, workspace, index):
+    if not (workspace.dtype is torch.uint8 and workspace.get_device() == index
+            and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+
+
+def _window_shapes(q, k, v, cu_q, cu_k, seqlens, max_q, max_k):
+    """(row strides of q, k, v, B, Nq, total_q, Nk, total_k, H, Hkv, d), index, lse."""
+    import torch
+    index = _check_rows("q, k, v", (q, k, v))
+    for t, name in ((cu_q, "cu_seqlens_q"), (cu_k, "cu_seqlens_k"), (seqlens, "seqlens_k")):
+        _check_vector(t, torch.int32, index, name)
+    qs, ks = q[0], k[0]
+    if ks != v[0]:
         raise ValueError("k and v must have one shape")
-    if len(q) != (4 if cu_q is None else 3):
+    if len(qs) != (4 if cu_q is None else 3):
         raise ValueError("q must be [B, Nq, H, d], or [total, H, d] with cu_seqlens_q")
-    if len(k) != (4 if cu_k is None else 3):
+    if len(ks) != (4 if cu_k is None else 3):
         raise ValueError("k and v must be [B, Nk, kv_heads, d], or [total, kv_heads, d] with "
                          "cu_seqlens_k")
-    H, d = q[-2:]
-    hkv = k[-2]
-    if k[-1] != d:
+    H, d = qs[-2:]
+    hkv = ks[-2]
+    if ks[-1] != d:
         raise ValueError("q, k and v must have one head dimension")
     if hkv == 0 or H % hkv:
         raise ValueError(f"{H} query heads on {hkv} kv heads")
-    B = q[0] if cu_q is None else cu_q[0] - 1
-    if B < 0 or any(n is not None and n != B + 1 for n in
-                    (cu_k and cu_k[0], seqlens and seqlens[0] + 1, None if cu_k else k[0] + 1)):
+    B = qs[0] if cu_q is None else cu_q[0][0] - 1
+    of = [qs[0] if cu_q is None else cu_q[0][0] - 1, ks[0] if cu_k is None else cu_k[0][0] - 1]
+    if seqlens is not None:
+        of.append(seqlens[0][0])
+    if B < 0 or any(n != B for n in of):
         raise ValueError(f"k, cu_seqlens_k and seqlens_k must be of q's {B} sequences")
-    total_q, total_k = (t[0] if len(t) == 3 else t[0] * t[1] for t in (q, k))
-    Nq = q[1] if cu_q is None else total_q if max_q is None else int(max_q)
-    Nk = k[1] if cu_k is None else total_k if max_k is None else int(max_k)
-    return (_row_stride(q, qs, "q"), _row_stride(k, ks, "k"), _row_stride(v, vs, "v"), B, Nq,
-            total_q, Nk, total_k, H, hkv, d, (B, H, Nq) if cu_q is None else (H, total_q))
+    total_q, total_k = (t[0] if len(t) == 3 else t[0] * t[1] for t in (qs, ks))
+    Nq = qs[1] if cu_q is None else total_q if max_q is None else int(max_q)
+    Nk = ks[1] if cu_k is None else total_k if max_k is None else int(max_k)
+    sizes = (_row_stride(qs, q[1], "q"), _row_stride(ks, k[1], "k"), _row_stride(v[0], v[1], "v"),
+             B, Nq, total_q, Nk, total_k, H, hkv, d)
+    return sizes, index, (B, H, Nq) if cu_q is None else (H, total_q)
+
+
+def _plan_window(q, k, v, cu_q, cu_k, seqlens, max_q, max_k):
+    import torch
+    sizes, index, lse = _window_shapes(q, k, v, cu_q, cu_k, seqlens, max_q, max_k)
+    (qs, ks, vs, B, Nq, total_q, Nk, total_k, H, hkv, d) = sizes
+    return (qs, ks, vs, (B, Nq, total_q, Nk, total_k, H, hkv, d), index,
+            (q[0], _dense(q[0]), torch.bfloat16, index),
+            (torch.Size(lse), _dense(lse), torch.float32, index), 1.0 / math.sqrt(max(d, 1)))
 
 
 def attention_window_fwd(q, k, v, window: int, sinks: int = 0, scale: float | None = None,
@@ -986,41 +1043,45 @@ def attention_window_fwd(q, k, v, window: int, sinks: int = 0, scale: float | No
     heads are contiguous, tokens may be any multiple of 8 elements apart.
     """
     import torch
-    index = _window_check(torch, (q, k, v), (cu_seqlens_q, cu_seqlens_k, seqlens_k))
-    key = (q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
-           None if cu_seqlens_q is None else cu_seqlens_q.shape,
-           None if cu_seqlens_k is None else cu_seqlens_k.shape,
-           None if seqlens_k is None else seqlens_k.shape, max_q, max_k)
-    (qs, ks, vs, B, Nq, total_q, Nk, total_k, H, hkv, d,
-     lse_shape) = _kv4_plan(key, _plan_window, *key)
+    key = (_like(q), _like(k), _like(v), _like(cu_seqlens_q), _like(cu_seqlens_k),
+           _like(seqlens_k), max_q, max_k)
+    qs, ks, vs, sizes, index, o_like, lse_like, usual = _kv4_plan(key, _plan_window, *key)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    elif not (out.shape == q.shape and out.dtype is torch.bfloat16 and out.get_device() == index
-              and out.is_contiguous()):
-        raise ValueError("out must be a contiguous tensor like q")
+        out = torch.empty_strided(o_like[0], o_like[1], dtype=o_like[2], device=q.device)
+    else:
+        _check_given(out, o_like, "out")
     if lse is None:
-        lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
-    elif not (tuple(lse.shape) == lse_shape and lse.dtype is torch.float32
-              and lse.get_device() == index and lse.is_contiguous()):
-        raise ValueError(f"lse must be a contiguous float32 tensor {list(lse_shape)}")
+        lse = torch.empty_strided(lse_like[0], lse_like[1], dtype=lse_like[2], device=q.device)
+    else:
+        _check_given(lse, lse_like, "lse")
     _kv4_call(torch, index, "fa_attention_window_fwd", q.data_ptr(), qs, k.data_ptr(), ks,
-              v.data_ptr(), vs, out.data_ptr(), lse.data_ptr(), B, Nq, total_q, Nk, total_k, H, hkv,
-              d, 1.0 / math.sqrt(d) if scale is None else scale, window, sinks, _ptr(cu_seqlens_q),
+              v.data_ptr(), vs, out.data_ptr(), lse.data_ptr(), *sizes,
+              usual if scale is None else scale, window, sinks, _ptr(cu_seqlens_q),
               _ptr(cu_seqlens_k), _ptr(seqlens_k))
     return out, lse
 
 
-def _plan_window_bwd(q, qs, k, ks, v, vs, dq, dqs, dk, dks, dv, dvs, cu, max_seqlen, window, sinks):
-    if dq != q or dk != k or dv != v:
-        raise ValueError("dq, dk and dv must have the shapes of q, k and v")
-    if q[:-2] != k[:-2]:
+def _plan_window_bwd(q, k, v, o, do, dq, dk, dv, cu, max_seqlen, window, sinks):
+    import torch
+    sizes, index, lse = _window_shapes(q, k, v, cu, cu, None, max_seqlen, max_seqlen)
+    if q[0][:-2] != k[0][:-2]:
         raise ValueError("q, k and v must be of the same tokens")
-    plan = _plan_window(q, qs, k, ks, v, vs, cu, cu, None, max_seqlen, max_seqlen)
-    (s_q, s_k, s_v, B, N, total, _, _, H, hkv, d, lse_shape) = plan
+    given = [t for t in (o, do, dq, dk, dv) if t is not None]
+    _check_rows("q, k, v", [q] + given)
+    for t, like, name in ((o, q, "o"), (do, q, "do"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        if t is not None and t[0] != like[0]:
+            raise ValueError(f"{name} must have the shape {list(like[0])}")
+    if not _contiguous(o) or not _contiguous(do):
+        raise ValueError("o and do must be contiguous")
+    qs, ks, vs, B, N, total, _, _, H, hkv, d = sizes
     nbytes = fa_attention_window_bwd_workspace_bytes(B, N, total, H, hkv, d, window, sinks)
     _check(int(min(nbytes, 0)), "fa_attention_window_bwd_workspace_bytes")
-    return (s_q, s_k, s_v, _row_stride(dq, dqs, "dq"), _row_stride(dk, dks, "dk"),
-            _row_stride(dv, dvs, "dv"), B, N, total, H, hkv, d, lse_shape, nbytes)
+    new = [(like[0], _dense(like[0])) for like in (q, k, v)]
+    rows = [_row_stride(like[0], n[1] if t is None else t[1], name)
+            for t, like, n, name in ((dq, q, new[0], "dq"), (dk, k, new[1], "dk"),
+                                     (dv, v, new[2], "dv"))]
+    return (qs, ks, vs, rows, (B, N, total, H, hkv, d), index, new,
+            (torch.Size(lse), None, torch.float32, index), nbytes, 1.0 / math.sqrt(max(d, 1)))
 
 
 def attention_window_bwd(q, k, v, o, do, lse, window: int, sinks: int = 0,
@@ -1036,79 +1097,55 @@ def attention_window_bwd(q, k, v, o, do, lse, window: int, sinks: int = 0,
     fa_attention_window_bwd_workspace_bytes).  Returns (dq, dk, dv).
     """
     import torch
-    if dq is None:
-        dq = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    if dk is None:
-        dk = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
-    if dv is None:
-        dv = torch.empty(v.shape, dtype=torch.bfloat16, device=q.device)
-    index = _window_check(torch, (q, k, v, o, do, dq, dk, dv), (cu_seqlens,))
-    key = (q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), dq.shape, dq.stride(),
-           dk.shape, dk.stride(), dv.shape, dv.stride(),
-           None if cu_seqlens is None else cu_seqlens.shape, max_seqlen, window, sinks)
-    (qs, ks, vs, dqs, dks, dvs, B, N, total, H, hkv, d, lse_shape,
-     nbytes) = _kv4_plan(key, _plan_window_bwd, *key)
-    if o.shape != q.shape or do.shape != q.shape or not o.is_contiguous() or not do.is_contiguous():
-        raise ValueError("o and do must be contiguous tensors like q")
-    if not (tuple(lse.shape) == lse_shape and lse.dtype is torch.float32
-            and lse.get_device() == index and lse.is_contiguous()):
-        raise ValueError(f"lse must be a contiguous float32 tensor {list(lse_shape)}")
+    key = (_like(q), _like(k), _like(v), _like(o), _like(do), _like(dq), _like(dk), _like(dv),
+           _like(cu_seqlens), max_seqlen, window, sinks)
+    (qs, ks, vs, (dqs, dks, dvs), sizes, index, new, lse_like, nbytes,
+     usual) = _kv4_plan(key, _plan_window_bwd, *key)
+    _check_given(lse, lse_like, "lse")
+    dq, dk, dv = (torch.empty_strided(*n, dtype=torch.bfloat16, device=q.device) if t is None
+                  else t for t, n in zip((dq, dk, dv), new))
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    elif not (workspace.dtype is torch.uint8 and workspace.get_device() == index
-              and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    else:
+        _check_workspace(torch, workspace, index)
     _kv4_call(torch, index, "fa_attention_window_bwd", q.data_ptr(), qs, k.data_ptr(), ks,
               v.data_ptr(), vs, o.data_ptr(), do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dqs,
-              dk.data_ptr(), dks, dv.data_ptr(), dvs, B, N, total, H, hkv, d,
-              1.0 / math.sqrt(d) if scale is None else scale, window, sinks, _ptr(cu_seqlens),
-              workspace.data_ptr(), workspace.numel())
+              dk.data_ptr(), dks, dv.data_ptr(), dvs, *sizes, usual if scale is None else scale,
+              window, sinks, _ptr(cu_seqlens), workspace.data_ptr(), workspace.numel())
     return dq, dk, dv
 
 
 # ---- norm and rotation of queries and keys ----------------------------------------
 
-def _plan_norm_rope(shapes, strides, w_shapes, pos, freq):
-    """(strides of the rows, total, H, Hkv, d, rot) of q, k and tensors like them.
-
-    shapes and strides: pairs (of q, of k), the inputs first.
-    """
-    q, k = shapes[0]
+def _plan_norm_rope(pairs, weights, freq, pos):
+    """pairs: (q, k), then (of tensors like them, or None for new ones) their outputs and gradients."""
+    import torch
+    given = [t for pair in pairs for t in pair if t is not None]
+    index = _check_rows("q, k", given)
+    _check_vector(freq, torch.float64, index, "inv_freq")
+    for w, name in zip(weights, ("q_weight", "k_weight")):
+        _check_vector(w, torch.float32, index, name)
+    if pos is not None and (pos[2] is not torch.int32 or pos[3] != index or not _contiguous(pos)):
+        raise ValueError("positions must be a contiguous int32 tensor on q's device")
+    q, k = pairs[0][0][0], pairs[0][1][0]
     if len(q) not in (3, 4) or len(k) != len(q) or q[:-2] != k[:-2] or q[-1] != k[-1]:
         raise ValueError("q and k must be [total, heads, d] or [B, N, heads, d] of the same tokens")
     total = 1
     for s in q[:-2]:
         total *= s
-    for pair in shapes[1:]:
-        if pair != shapes[0]:
-            raise ValueError("outputs and gradients must have the shapes of q and k")
-    if any(w is not None and tuple(w) != (q[-1],) for w in w_shapes):
+    if any(t is not None and t[0] != like for pair in pairs for t, like in zip(pair, (q, k))):
+        raise ValueError("outputs and gradients must have the shapes of q and k")
+    if any(w is not None and tuple(w[0]) != (q[-1],) for w in weights):
         raise ValueError(f"weights must be [{q[-1]}]")
-    rot = 0 if freq is None else 2 * freq[0]
-    if rot and (pos is None or tuple(pos) not in (tuple(q[:-2]), (total,))):
+    rot = 0 if freq is None else 2 * freq[0][0]
+    if rot and (pos is None or tuple(pos[0]) not in (tuple(q[:-2]), (total,))):
         raise ValueError("positions must have one entry a token")
-    rows = [_row_stride(s, st, n) for pair, stp in zip(shapes, strides)
-            for s, st, n in zip(pair, stp, ("q", "k"))]
-    return rows, total, q[-2], k[-2], q[-1], rot
-
-
-def _check_norm_rope(torch, rows, weights, inv_freq, positions):
-    index = rows[0].get_device()
-    if index < 0:
-        raise ValueError("q and k must be CUDA tensors")
-    for t in rows:
-        if t.dtype is not torch.bfloat16 or t.get_device() != index:
-            raise ValueError("q, k and tensors like them must be bf16 and on one device")
-    for t, dtype, name in ((weights[0], torch.float32, "q_weight"),
-                           (weights[1], torch.float32, "k_weight"),
-                           (inv_freq, torch.float64, "inv_freq"),
-                           (positions, torch.int32, "positions")):
-        if t is not None and (t.dtype is not dtype or t.get_device() != index
-                              or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor on q's device")
-    if inv_freq is not None and inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rot / 2]")
-    return index
+    new = [(q, _dense(q)), (k, _dense(k))]
+    rows = [_row_stride(like, n[1] if t is None else t[1], name) for pair in pairs
+            for t, like, n, name in zip(pair, (q, k), new, ("q", "k"))]
+    nbytes = fa_qk_norm_rope_bwd_workspace_bytes(total, q[-2], k[-2], q[-1])
+    _check(int(min(nbytes, 0)), "fa_qk_norm_rope: d")
+    return rows, (total, q[-2], k[-2], q[-1], rot), index, new, nbytes
 
 
 def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None,
@@ -1124,19 +1161,16 @@ def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, inv_freq=None, position
     ``k_out``: write into these (they may be q and k).  Returns (q_out, k_out).
     """
     import torch
+    key = (((_like(q), _like(k)), (_like(q_out), _like(k_out))),
+           (_like(q_weight), _like(k_weight)), _like(inv_freq), _like(positions))
+    (qs, ks, qos, kos), sizes, index, new, _ = _kv4_plan(key, _plan_norm_rope, *key)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty_strided(*new[0], dtype=torch.bfloat16, device=q.device)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
-    index = _check_norm_rope(torch, (q, k, q_out, k_out), (q_weight, k_weight), inv_freq, positions)
-    shape = lambda t: None if t is None else t.shape  # noqa: E731
-    key = (((q.shape, k.shape), (q_out.shape, k_out.shape)),
-           ((q.stride(), k.stride()), (q_out.stride(), k_out.stride())),
-           (shape(q_weight), shape(k_weight)), shape(positions), shape(inv_freq))
-    (qs, ks, qos, kos), total, H, hkv, d, rot = _kv4_plan(key, _plan_norm_rope, *key)
+        k_out = torch.empty_strided(*new[1], dtype=torch.bfloat16, device=q.device)
     _kv4_call(torch, index, "fa_qk_norm_rope_fwd", q.data_ptr(), qs, k.data_ptr(), ks,
               _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), q_out.data_ptr(),
-              qos, k_out.data_ptr(), kos, total, H, hkv, d, rot, 1 if interleaved else 0, eps)
+              qos, k_out.data_ptr(), kos, *sizes, 1 if interleaved else 0, eps)
     return q_out, k_out
 
 
@@ -1150,31 +1184,25 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, inv_fre
     (dq, dk, dq_weight, dk_weight); the last two are fp32 [d], None without that weight.
     """
     import torch
+    key = (((_like(q), _like(k)), (_like(dq_out), _like(dk_out)), (_like(dq), _like(dk))),
+           (_like(q_weight), _like(k_weight)), _like(inv_freq), _like(positions))
+    (qs, ks, gqs, gks, dqs, dks), sizes, index, new, nbytes = _kv4_plan(key, _plan_norm_rope, *key)
     if dq is None:
-        dq = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        dq = torch.empty_strided(*new[0], dtype=torch.bfloat16, device=q.device)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
-    index = _check_norm_rope(torch, (q, k, dq_out, dk_out, dq, dk), (q_weight, k_weight), inv_freq,
-                             positions)
-    shape = lambda t: None if t is None else t.shape  # noqa: E731
-    key = (((q.shape, k.shape), (dq_out.shape, dk_out.shape), (dq.shape, dk.shape)),
-           ((q.stride(), k.stride()), (dq_out.stride(), dk_out.stride()),
-            (dq.stride(), dk.stride())),
-           (shape(q_weight), shape(k_weight)), shape(positions), shape(inv_freq))
-    (qs, ks, gqs, gks, dqs, dks), total, H, hkv, d, rot = _kv4_plan(key, _plan_norm_rope, *key)
-    dwq, dwk = (None if w is None else torch.empty(w.shape, dtype=torch.float32, device=q.device)
+        dk = torch.empty_strided(*new[1], dtype=torch.bfloat16, device=q.device)
+    d = sizes[3]
+    dwq, dwk = (None if w is None else torch.empty_strided((d,), (1,), dtype=torch.float32,
+                                                           device=q.device)
                 for w in (q_weight, k_weight))
     if workspace is None:
-        nbytes = fa_qk_norm_rope_bwd_workspace_bytes(total, H, hkv, d)
-        _check(int(min(nbytes, 0)), "fa_qk_norm_rope_bwd_workspace_bytes")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    elif not (workspace.dtype is torch.uint8 and workspace.get_device() == index
-              and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+        workspace = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=q.device)
+    else:
+        _check_workspace(torch, workspace, index)
     _kv4_call(torch, index, "fa_qk_norm_rope_bwd", q.data_ptr(), qs, k.data_ptr(), ks,
               dq_out.data_ptr(), gqs, dk_out.data_ptr(), gks, _ptr(q_weight), _ptr(k_weight),
               _ptr(inv_freq), _ptr(positions), dq.data_ptr(), dqs, dk.data_ptr(), dks, _ptr(dwq),
-              _ptr(dwk), total, H, hkv, d, rot, 1 if interleaved else 0, eps, workspace.data_ptr(),
+              _ptr(dwk), *sizes, 1 if interleaved else 0, eps, workspace.data_ptr(),
               workspace.numel())
     return dq, dk, dwq, dwk
 

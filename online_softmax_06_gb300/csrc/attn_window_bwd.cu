@@ -15,7 +15,7 @@
 //     (2^-9 of dQ becomes 2^-7.5 with a window of 2048).  But sum_j dS_ij is 0, so its
 //     computed value r_i is the error's, and r_i times a mean of the keys is taken off
 //     (the common part; of 16 rows a step, which the row warps read beside their work).
-//   * attn_window_dkdv_kernel: a CTA per (sequence, kv head, 128 keys); 64-query
+//   * attn_window_dkdv_kernel: a CTA per (sequence, kv head, 128 keys); 128-query
 //     steps over the queries that have these keys in their window, one head of the
 //     group after the other into the same accumulators.  Keys below `sinks` are seen
 //     by all later queries too: these steps, of which a long sequence has many more
@@ -42,15 +42,13 @@
 namespace fa {
 namespace {
 
-constexpr int BT = 128;                     // rows of the resident tile
-constexpr int BS = 64;                      // queries of a dK/dV step
+constexpr int BT = 128;                     // rows of a tile, resident or streamed
 constexpr int kPad = 32;                    // sinks fill whole pieces of a tile
-constexpr int kRowWarps = 8;                // two threads a row
+constexpr int kRowWarps = 16;               // four threads a row: see the kernels
 constexpr int kThreads = 32 * (kRowWarps + 2);
 constexpr int kWarpLoad = kRowWarps, kWarpMma = kRowWarps + 1;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kChunkBytes = BT * 128;     // 128 rows of 64 bf16
-constexpr uint32_t kSubChunkBytes = BS * 128;  // 64 rows
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
@@ -63,7 +61,7 @@ struct Params {
     int64_t dq_stride, dk_stride, dv_stride;
     float *parts;                      // [B Hkv][sink tiles][slots][dV, dK][128][d]
     int G, P, n_tiles;                 // n_tiles: row tiles (dQ), key tiles (dK/dV) of Nq
-    int sink_tiles, slots, piece;      // piece: 64-query sub-tiles of a far piece
+    int sink_tiles, slots, piece;      // piece: 128-query tiles of a far piece
     float scale_log2;
 };
 
@@ -148,11 +146,13 @@ __device__ __forceinline__ int64_t stat_row(const WindowArgs &a, int b, int h, i
 // =============================================================================
 // dQ and D
 // =============================================================================
-// S in columns [0, 128), dP (then dS packed into the first half of each row thread's
-// 64 columns) in [128, 256), dQ from 256, Q and dO as bf16 A operands behind it.  The
-// MMA warp issues, per step j: S_{j+1} as soon as the rows have read S_j, dQ += dS_j
-// K_j once they have stored dS_j, then dP_{j+1}.  The ring's third stage is the region
-// that held Q and dO, free once they are in tensor memory and D is formed.
+// S_j in columns [0, 128), dP_j (dS_j packed into it) in [128, 256), dQ from 256, Q and
+// dO as bf16 A operands behind it.  The MMA warp issues, per 128-key step j: S_{j+1} as
+// soon as the rows have read S_j, dQ += dS_j K_j once they have stored dS_j, then dP_{j+1};
+// sixteen row warps (four threads a row, 32 columns each) form P while dQ and dP run and
+// dS while S does.  (Steps of 64 keys in two buffers took 246 us where these take NNN: a
+// product 64 wide takes the tensor cores as long as one of 128.)  The ring's third stage
+// is the region that held Q and dO, free once they are in tensor memory and D is formed.
 template <int D>
 struct CfgQ {
     static constexpr int kChunks = D / 64;
@@ -160,11 +160,10 @@ struct CfgQ {
     static constexpr uint32_t kStageBytes = 2 * kTileBytes;  // K_j, V_j
     static constexpr int kStages = 3;
     static constexpr uint32_t kOffRing = 2 * kTileBytes;
-    // 128 D_i values, later the rows' sums of dS, [2][128]; the warps' sums of keys
-    // [8][D] and how many
+    // 128 D_i values, later the sums of dS of the rows' four threads; the keys' mean
     static constexpr uint32_t kOffXch = kOffRing + 2 * kStageBytes;
-    static constexpr uint32_t kOffMean = kOffXch + 2 * BT * 4;
-    static constexpr uint32_t kOffBar = kOffMean + kRowWarps * D * 4 + 32;
+    static constexpr uint32_t kOffMean = kOffXch + 4 * BT * 4;
+    static constexpr uint32_t kOffBar = kOffMean + D * 4;
     static constexpr int kBars = 1 + 2 * kStages + 9;
     static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16 + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -173,8 +172,14 @@ struct CfgQ {
         return s == 2 ? 0u : kOffRing + uint32_t(s) * kStageBytes;
     }
 };
-constexpr uint32_t kColAcc = 256, kQColDP = 128;
-constexpr int kQCols = 64;                      // columns of a step per row thread
+constexpr uint32_t kColAcc = 256, kColDP = 128;
+// Column of the packed bf16 operand for the product's K step kk: the 32 values of each
+// 32-column block go to the block's first 16 columns, so a thread only overwrites
+// columns that it has read.
+__host__ __device__ constexpr uint32_t packed_col(int kk)
+{
+    return uint32_t(32 * (kk >> 1) + 8 * (kk & 1));
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __grid_constant__ Params p)
@@ -250,11 +255,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     uint8_t *tile_q = smem, *tile_do = smem + C::kTileBytes;
 
     if (warp == kWarpLoad) {
-        // ======================= TMA producer ==============================
+        // ======================= TMA producer, keys' mean =====================
+        // Lane 0 issues the copies.  Behind the copies of step j the warp sums 16 rows
+        // of K_{j-2}, whose stage is this warp's to fill again.
+        constexpr int kKeyLanes = D / 8, kKeyRows = 32 / kKeyLanes;
+        float key_sum[8] = {};
+        int key_n = 0;
+        auto sum_keys = [&](int j) {
+            const int st = j % C::kStages, un = lane % kKeyLanes;
+            if (!ptx::mbar_wait_warp(&kv_full[st], uint32_t(j / C::kStages) & 1u, abort_flag,
+                                     a.err_word))
+                return;
+            const uint8_t *tile_k = smem + C::stage_off(st) + (un >> 3) * kChunkBytes;
+#pragma unroll
+            for (int q = 0; q < 16 / kKeyRows; ++q) {
+                const int kr = (q * kKeyRows + lane / kKeyLanes) * 8;
+                if (j * BT + kr >= w.places)
+                    break;
+                const uint4 v =
+                    *reinterpret_cast<const uint4 *>(tile_k + kr * 128 + ((un & 7) << 4));
+                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    key_sum[2 * e] += __uint_as_float(x[e] << 16);
+                    key_sum[2 * e + 1] += __uint_as_float(x[e] & 0xffff0000u);
+                }
+                ++key_n;
+            }
+            __syncwarp();
+        };
         if (lane == 0) {
-            int last_phase[C::kStages];
-            for (int st = 0; st < C::kStages; ++st)
-                last_phase[st] = -1;
             ptx::mbar_arrive_expect_tx(a_full, 2 * C::kChunks * p.P * p.G * 128);
             for (int c = 0; c < C::kChunks; ++c) {
                 ptx::tma_load_4d(tile_q + c * kChunkBytes, &p.tm_q, a_full, c * 64, 0, hk,
@@ -262,14 +292,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 ptx::tma_load_4d(tile_do + c * kChunkBytes, &p.tm_do, a_full, c * 64, 0, hk,
                                  int(sq.q0 + i0));
             }
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int j = 0; j < n_kv; ++j) {
-                if (!ptx::mbar_wait(&kv_empty[stage], phase ^ 1u, abort_flag, a.err_word))
-                    break;
-                // stage 2 is the Q / dO region: free once the rows are done with it
-                if (j == 2 && !ptx::mbar_wait(res_free, 0, abort_flag, a.err_word))
-                    break;
+        }
+        int issued = 0;
+        for (int j = 0; j < n_kv; ++j) {
+            const int stage = j % C::kStages;
+            // stage 2 is the Q / dO region: free once the rows are done with it
+            if (!ptx::mbar_wait_warp(&kv_empty[stage], (uint32_t(j / C::kStages) & 1u) ^ 1u,
+                                     abort_flag, a.err_word) ||
+                (j == 2 && !ptx::mbar_wait_warp(res_free, 0, abort_flag, a.err_word)))
+                break;
+            if (lane == 0) {
                 uint8_t *dst = smem + C::stage_off(stage);
                 const int v0 = j * BT;
                 ptx::mbar_arrive_expect_tx(&kv_full[stage], C::kStageBytes);
@@ -293,18 +325,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                                          &kv_full[stage], c * 64, 0, hk, row);
                     }
                 }
-                last_phase[stage] = int(phase);
-                if (++stage == C::kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
             }
-            if (*abort_flag) {
-                drain_wait(a_full, 0);
-                for (int st = 0; st < C::kStages; ++st)
-                    if (last_phase[st] >= 0)
-                        drain_wait(&kv_full[st], uint32_t(last_phase[st]));
-            }
+            __syncwarp();
+            issued = j + 1;
+            if (j >= 2)
+                sum_keys(j - 2);
+        }
+        for (int j = issued >= 2 ? issued - 2 : 0; j < issued; ++j)
+            sum_keys(j);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int o = 16; o >= kKeyLanes; o >>= 1)
+                key_sum[e] += __shfl_xor_sync(0xffffffffu, key_sum[e], o);
+#pragma unroll
+        for (int o = 16; o >= kKeyLanes; o >>= 1)
+            key_n += __shfl_xor_sync(0xffffffffu, key_n, o);
+        if (lane < kKeyLanes)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                reinterpret_cast<float *>(smem + C::kOffMean)[lane * 8 + e] =
+                    key_n > 0 ? key_sum[e] / float(key_n) : 0.f;
+        __syncwarp();
+        asm volatile("bar.sync 2, %0;" ::"n"(32 * kRowWarps + 32) : "memory");
+        if (*abort_flag && lane == 0) {
+            drain_wait(a_full, 0);
+            for (int j = issued > C::kStages ? issued - C::kStages : 0; j < issued; ++j)
+                drain_wait(&kv_full[j % C::kStages], uint32_t(j / C::kStages) & 1u);
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -313,28 +360,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         constexpr uint32_t idesc_q = ptx::idesc_bf16_f32(BT, D, true);     // B MN-major
         constexpr uint64_t desc_kmajor = ptx::smem_desc_base(16, 1024);
         constexpr uint64_t desc_mnmajor = ptx::smem_desc_base(kChunkBytes, 1024);
-        auto issue_s = [&](uint32_t kaddr) {
-            const uint64_t dk = ptx::smem_desc(desc_kmajor, kaddr);
-            if (ptx::elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    ptx::mma_ts(tmem, tmem + kColQA + 8 * kk, dk + kmajor_off(kk, kChunkBytes),
-                                idesc_s, kk > 0 ? 1u : 0u);
-                ptx::mma_commit(s_full);
-            }
-            __syncwarp();
-        };
-        auto issue_dp = [&](uint32_t vaddr) {
-            const uint64_t dv = ptx::smem_desc(desc_kmajor, vaddr);
-            if (ptx::elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    ptx::mma_ts(tmem + kQColDP, tmem + kColQA + D / 2 + 8 * kk,
-                                dv + kmajor_off(kk, kChunkBytes), idesc_s, kk > 0 ? 1u : 0u);
-                ptx::mma_commit(dp_full);
-            }
-            __syncwarp();
-        };
         const uint32_t smem_base = ptx::smem_u32(smem);
         // K's and V's rows of step j behind the sequence's end are cleared
         const int end_place = w.sp + (L - w.lo);
@@ -350,6 +375,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             !__all_sync(0xffffffffu, ptx::mbar_wait_limited(never, 0, abort_flag, a.err_word,
                                                             a.expire_wait_ns)))
             aborted = true;
+        // S = Q K^T and dP = dO V^T, A from tensor memory
+        auto issue = [&](uint32_t to, uint32_t from, uint32_t addr, uint64_t *bar) {
+            const uint64_t db = ptx::smem_desc(desc_kmajor, addr);
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    ptx::mma_ts(tmem + to, tmem + from + 8 * kk, db + kmajor_off(kk, kChunkBytes),
+                                idesc_s, kk > 0 ? 1u : 0u);
+                ptx::mma_commit(bar);
+            }
+            __syncwarp();
+        };
+        auto issue_s = [&](int st) { issue(0, kColQA, smem_base + C::stage_off(st), s_full); };
+        auto issue_dp = [&](int st) {
+            issue(kColDP, kColQA + D / 2, smem_base + C::stage_off(st) + C::kTileBytes, dp_full);
+        };
         do {
             if (aborted || !ptx::mbar_wait_warp(a_tm, 0, abort_flag, a.err_word) ||
                 !ptx::mbar_wait_warp(&kv_full[0], 0, abort_flag, a.err_word)) {
@@ -358,22 +399,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             }
             clear_tail(0, 0);
             ptx::tc_fence_after_sync();
-            issue_s(smem_base + C::stage_off(0));
-            issue_dp(smem_base + C::stage_off(0) + C::kTileBytes);
+            issue_s(0);
+            issue_dp(0);
             int cur = 0, nxt = 1;                      // ring stages of steps j, j + 1
             uint32_t nxt_phase = 0;
             for (int j = 0; j < n_kv; ++j) {
                 const bool more = j + 1 < n_kv;
                 if (more) {
                     // S_{j+1} overwrites S_j once every row has read it
-                    if (!ptx::mbar_wait_warp(s_free, uint32_t(j) & 1u, abort_flag, a.err_word) ||
-                        !ptx::mbar_wait_warp(&kv_full[nxt], nxt_phase, abort_flag, a.err_word)) {
+                    if (!ptx::mbar_wait_warp(&kv_full[nxt], nxt_phase, abort_flag, a.err_word) ||
+                        !ptx::mbar_wait_warp(s_free, uint32_t(j) & 1u, abort_flag, a.err_word)) {
                         aborted = true;
                         break;
                     }
                     clear_tail(j + 1, nxt);
                     ptx::tc_fence_after_sync();
-                    issue_s(smem_base + C::stage_off(nxt));
+                    issue_s(nxt);
                 }
                 if (!ptx::mbar_wait_warp(p_full, uint32_t(j) & 1u, abort_flag, a.err_word)) {
                     aborted = true;
@@ -384,8 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 if (ptx::elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk)
-                        ptx::mma_ts(tmem + kColAcc,
-                                    tmem + kQColDP + uint32_t(kQCols * (kk >> 2) + 8 * (kk & 3)),
+                        ptx::mma_ts(tmem + kColAcc, tmem + kColDP + packed_col(kk),
                                     dkn + uint64_t((kk * 16 * 128) >> 4), idesc_q,
                                     (j > 0 || kk > 0) ? 1u : 0u);
                     ptx::mma_commit(&kv_empty[cur]);
@@ -393,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 __syncwarp();
                 // dP_{j+1} overwrites dS_j after the dQ product has read it
                 if (more)
-                    issue_dp(smem_base + C::stage_off(nxt) + C::kTileBytes);
+                    issue_dp(nxt);
                 cur = nxt;
                 if (++nxt == C::kStages) {
                     nxt = 0;
@@ -411,16 +451,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     } else {
         // ======================= query rows ================================
         const int r = (warp & 3) * 32 + lane;        // row of the tile = TMEM lane
-        const int g = warp >> 2;                     // column group
+        const int g = warp >> 2, col0 = 32 * g;      // of the row's four threads; its columns
         const int qi = r / p.G, i = i0 + qi;         // query, head of the kv head
         const int h = hk * p.G + r % p.G;
         const bool row_ok = qi < p.P && i < i1;
         const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
         const int64_t stat = row_ok ? stat_row(a, b, h, sq.q0) + i : 0;
-        // D_i = dO_i . O_i: a warp takes 16 rows, D / 8 lanes each; O from global memory,
+        // D_i = dO_i . O_i: a warp takes 8 rows, D / 8 lanes each; O from global memory,
         // dO from the resident tile (128-byte swizzle)
         constexpr int kLanesPerRow = D / 8, kRowsPerInst = 32 / kLanesPerRow;
-        constexpr int kRowsPerWarp = BT / kRowWarps;          // 16
+        constexpr int kRowsPerWarp = BT / kRowWarps;
         float *xch = reinterpret_cast<float *>(smem + C::kOffXch);
         {
             const int sub = lane / kLanesPerRow, lr = lane % kLanesPerRow;
@@ -437,14 +477,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             }
             const bool a_ok = row_wait(a_full, 0, abort_flag, a.err_word);
             if (a_ok) {
-                // this thread's half of its row of Q and of dO into tensor memory
+                // this thread's quarter of its row of Q and of dO into tensor memory
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const uint8_t *src = t == 0 ? tile_q : tile_do;
-                    uint32_t u[D / 4];
+                    uint32_t u[D / 8];
 #pragma unroll
-                    for (int ul = 0; ul < D / 16; ++ul) {
-                        const int e0 = g * (D / 2) + ul * 8;
+                    for (int ul = 0; ul < D / 32; ++ul) {
+                        const int e0 = g * (D / 4) + ul * 8;
                         const int un = (e0 & 63) >> 3;
                         const uint4 v = *reinterpret_cast<const uint4 *>(
                             src + (e0 >> 6) * kChunkBytes + r * 128 + ((un ^ (r & 7)) << 4));
@@ -454,11 +494,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                         u[4 * ul + 3] = v.w;
                     }
                     const uint32_t dst =
-                        tmem + lane_bits + kColQA + uint32_t(t * (D / 2) + g * (D / 4));
+                        tmem + lane_bits + kColQA + uint32_t(t * (D / 2) + g * (D / 8));
                     if constexpr (D == 128)
-                        ptx::tmem_st32(dst, u);
-                    else
                         ptx::tmem_st16(dst, u);
+                    else
+                        ptx::tmem_st8(dst, u);
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before_sync();
@@ -495,144 +535,86 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 ptx::mbar_arrive(res_free);
         }
         const float lse2 = row_ok ? a.lse[stat] * kLog2e : 0.f;
-        asm volatile("bar.sync 1, 256;" ::: "memory");              // the row threads
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");   // the row threads
         const float Di = xch[r];
         if (g == 0 && row_ok)
             p.D[stat] = Di;
         const float sl = p.scale_log2;
-        const int col0 = g * kQCols;
-        const uint32_t tS = tmem + lane_bits + uint32_t(col0);
-        const uint32_t tDP = tmem + lane_bits + kQColDP + uint32_t(col0);
         const int vhi = row_ok ? i - w.lo + w.sp : -1;
         const int64_t vl = int64_t(vhi) - a.window + 1;
         const int vlo = vl > w.sp ? int(vl) : w.sp;
 
-        // two rows of each step's keys a warp, half a warp (d = 64: a quarter) each: 8
-        // values a lane
-        constexpr int kKeyLanes = D / 8;
-        float key_sum[8] = {}, ds_sum = 0.f;
-        int key_n = 0;
+        float2 ds_sum2 = make_float2(0.f, 0.f);
+        const uint32_t tS = tmem + lane_bits + uint32_t(col0);
 
         for (int j = 0; j < n_kv; ++j) {
             const uint32_t par = uint32_t(j) & 1u;
-            if (!row_wait(s_full, par, abort_flag, a.err_word) ||
-                !row_wait(&kv_full[j % C::kStages], uint32_t(j / C::kStages) & 1u, abort_flag,
-                          a.err_word)) {
+            if (!row_wait(s_full, par, abort_flag, a.err_word)) {
                 aborted = true;
                 break;
             }
             ptx::tc_fence_after_sync();
-            {
-                const int kr = warp * 16 + (lane / kKeyLanes) * 8, u = lane % kKeyLanes;
-                if (lane < 2 * kKeyLanes && j * BT + kr < w.places) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(
-                        smem + C::stage_off(j % C::kStages) + (u >> 3) * kChunkBytes + kr * 128 +
-                        (((u & 7) ^ (kr & 7)) << 4));
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        key_sum[2 * e] += __uint_as_float(x[e] << 16);
-                        key_sum[2 * e + 1] += __uint_as_float(x[e] & 0xffff0000u);
-                    }
-                    ++key_n;
-                }
-            }
+            uint32_t sv[32];
+            ptx::tmem_ld32(tS, sv);
+            ptx::tmem_wait_ld();
+            // S is read: the MMA warp may overwrite it with the next step's
+            ptx::tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(s_free);
             const int v0 = j * BT + col0;            // this thread's first place
-            const bool masked = __any_sync(0xffffffffu, v0 < vlo || v0 + kQCols - 1 > vhi);
-            uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
-            if (masked)
+            if (__any_sync(0xffffffffu, v0 < vlo || v0 + 31 > vhi)) {
+                const uint32_t seen = window_bits(v0, vlo, vhi, a.sinks);
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    seen[c] = window_bits(v0 + 32 * c, vlo, vhi, a.sinks);
-            float pr[kQCols];
-            {
-                uint32_t sv0[32], sv1[32];
-                ptx::tmem_ld32(tS, sv0);
-                ptx::tmem_ld32(tS + 32, sv1);
-                ptx::tmem_wait_ld();
-                // S is read: the MMA warp may overwrite it with the next step's
-                ptx::tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    ptx::mbar_arrive(s_free);
-                if (masked) {
+                for (int e = 0; e < 32; ++e)
+                    if (!(seen & (1u << e)))
+                        sv[e] = __float_as_uint(-INFINITY);
+            }
+            float2 pr[16];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        if (!(seen[0] & (1u << k)))
-                            sv0[k] = __float_as_uint(-INFINITY);
-                        if (!(seen[1] & (1u << k)))
-                            sv1[k] = __float_as_uint(-INFINITY);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    pr[k] = ptx::ex2(fmaf(__uint_as_float(sv0[k]), sl, -lse2));
-                    pr[32 + k] = ptx::ex2(fmaf(__uint_as_float(sv1[k]), sl, -lse2));
-                }
+            for (int e = 0; e < 16; ++e) {
+                const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[2 * e]),
+                                                        __uint_as_float(sv[2 * e + 1])),
+                                            make_float2(sl, sl), make_float2(-lse2, -lse2));
+                pr[e] = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
             }
             if (!row_wait(dp_full, par, abort_flag, a.err_word)) {
                 aborted = true;
                 break;
             }
             ptx::tc_fence_after_sync();
-            uint32_t pk[32];
+            uint32_t dv[32], pk[16];
+            ptx::tmem_ld32(tS + kColDP, dv);
+            ptx::tmem_wait_ld();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t dv[32];
-                ptx::tmem_ld32(tDP + 32 * half, dv);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float d0 = pr[32 * half + 2 * e] * (__uint_as_float(dv[2 * e]) - Di);
-                    const float d1 =
-                        pr[32 * half + 2 * e + 1] * (__uint_as_float(dv[2 * e + 1]) - Di);
-                    ds_sum += d0 + d1;
-                    pk[16 * half + e] = ptx::pack_bf16x2(d0, d1);
-                }
+            for (int e = 0; e < 16; ++e) {
+                const float2 y = __fmul2_rn(
+                    pr[e], __fadd2_rn(make_float2(__uint_as_float(dv[2 * e]),
+                                                  __uint_as_float(dv[2 * e + 1])),
+                                      make_float2(-Di, -Di)));
+                ds_sum2 = __fadd2_rn(ds_sum2, y);
+                pk[e] = ptx::pack_bf16x2(y.x, y.y);
             }
-            ptx::tmem_st32(tDP, pk);                  // dS of this row's 64 keys, packed
+            ptx::tmem_st16(tS + kColDP, pk);         // dS of this row's 32 keys, packed
             ptx::tmem_wait_st();
             ptx::tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
                 ptx::mbar_arrive(p_full);
         }
-        // the keys' mean, and the sum of the row's dS over both its threads
-        float *mean = reinterpret_cast<float *>(smem + C::kOffMean);
-        int *mean_n = reinterpret_cast<int *>(mean + kRowWarps * D);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            key_sum[e] += __shfl_down_sync(0xffffffffu, key_sum[e], kKeyLanes);
-        key_n += __shfl_down_sync(0xffffffffu, key_n, kKeyLanes);
-        if (lane < kKeyLanes)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                mean[warp * D + lane * 8 + e] = key_sum[e];
-        if (lane == 0)
-            mean_n[warp] = key_n;
-        asm volatile("bar.sync 1, 256;" ::: "memory");   // (all have read D from xch)
+        const float ds_sum = ds_sum2.x + ds_sum2.y;
+        // the sum of the row's dS over its threads, and (from the load warp) the keys' mean
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");   // all have read D
         xch[g * BT + r] = ds_sum;
-        float km = 0.f;
-        if (threadIdx.x < D) {
-            int n = 0;
-#pragma unroll
-            for (int k = 0; k < kRowWarps; ++k) {
-                km += mean[k * D + threadIdx.x];
-                n += mean_n[k];
-            }
-            km = n > 0 ? km / float(n) : 0.f;
-        }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (threadIdx.x < D)
-            mean[threadIdx.x] = km;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        const float ri = xch[r] + xch[BT + r];
-        // the two threads of a row store half of its dQ each
-        if (!aborted && ptx::mbar_wait(o_full, 0, abort_flag, a.err_word)) {
+        asm volatile("bar.sync 2, %0;" ::"n"(32 * kRowWarps + 32) : "memory");
+        const float ri = (xch[r] + xch[BT + r]) + (xch[2 * BT + r] + xch[3 * BT + r]);
+        const float *mean = reinterpret_cast<const float *>(smem + C::kOffMean);
+        // 32 columns of each row's dQ a thread
+        if (g < D / 32 && !aborted && ptx::mbar_wait(o_full, 0, abort_flag, a.err_word)) {
             ptx::tc_fence_after_sync();
             store_row(tmem + lane_bits + kColAcc, a.scale,
-                      p.dQ + (sq.q0 + i) * p.dq_stride + int64_t(h) * D, row_ok, g * (D / 64),
-                      (g + 1) * (D / 64), -ri, mean);
+                      p.dQ + (sq.q0 + i) * p.dq_stride + int64_t(h) * D, row_ok, g, g + 1, -ri,
+                      mean);
         }
     }
     ptx::tc_fence_before_sync();
@@ -645,37 +627,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
 // =============================================================================
 // dK, dV
 // =============================================================================
-// Per step S^T = K Q_s^T and dP^T = V dO_s^T (a key per lane) in one of two buffers of
-// tensor memory, [0, 128) and [128, 256): S^T in a buffer's first 64 columns, dP^T in
-// the others, P^T and dS^T packed into them; dV from 256, dK behind it.
+// Per 128-query step S^T = K Q_j^T in columns [0, 128) and dP^T = V dO_j^T in [128, 256)
+// (a key per lane), P^T and dS^T packed into them; dV from 256, dK behind it.  The MMA
+// warp issues dV += P^T_j dO_j, S^T_{j+1}, dK += dS^T_j Q_j, dP^T_{j+1}: sixteen row warps
+// (four threads a row, 32 columns each) form P^T while dK and dP^T run, and dS^T while dV
+// and S^T do.  (Steps of 64 queries in two buffers took 304 us where these take NNN.)
 template <int D>
 struct CfgK {
     static constexpr int kChunks = D / 64;
-    static constexpr uint32_t kResBytes = BT * D * 2;
-    static constexpr uint32_t kSubBytes = BS * D * 2;
-    static constexpr int kStages = 4;
-    static constexpr uint32_t kStageBytes = 2 * kSubBytes;
-    // [K][V][ring: Q_s, dO_s][statistics: (lse log2 e, D) x 64 a stage][barriers]
-    static constexpr uint32_t kOffRing = 2 * kResBytes;
+    static constexpr uint32_t kTileBytes = BT * D * 2;
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr uint32_t kStageBytes = 2 * kTileBytes;
+    // [K][V][ring: Q_j, dO_j][statistics: (-lse log2 e, -D) x 128 a stage][barriers]
+    static constexpr uint32_t kOffRing = 2 * kTileBytes;
     static constexpr uint32_t kOffStat = kOffRing + kStages * kStageBytes;
-    static constexpr uint32_t kOffBar = kOffStat + kStages * 2 * BS * 4;
+    static constexpr uint32_t kOffBar = kOffStat + kStages * 2 * BT * 4;
     static constexpr int kBars = 1 + 2 * kStages + 6;
     static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16 + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
-constexpr uint32_t kColBuf = 128, kColDP = 64;
-__host__ __device__ constexpr uint32_t packed_col(int kk)
-{
-    return uint32_t(32 * (kk >> 1) + 8 * (kk & 1));
-}
-
-// 64-query sub-tiles of a sequence that have a key of tile kt in their window: [2 kt,
+// 128-query tiles of a sequence that have a key of tile kt in their window: [kt,
 // near_end); those behind it see the tile's sinks alone.
 __device__ __forceinline__ int near_end(int kt, int window, int L)
 {
-    const int n_sub = (L + BS - 1) / BS;
-    const int64_t e = (int64_t(kt) * BT + BT - 1 + window + BS - 1) / BS;
-    return e < n_sub ? int(e) : n_sub;
+    const int n = (L + BT - 1) / BT;
+    const int64_t e = (int64_t(kt) * BT + BT - 1 + window + BT - 1) / BT;
+    return e < n ? int(e) : n;
 }
 
 template <int D>
@@ -688,8 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *a_full = bars, *kv_full = bars + 1, *kv_empty = kv_full + C::kStages;
-    uint64_t *s_full = kv_empty + C::kStages, *p_full = s_full + 2, *o_full = s_full + 4,
-             *drain = s_full + 5;
+    uint64_t *s_full = kv_empty + C::kStages, *dp_full = s_full + 1, *p_full = s_full + 2,
+             *ds_full = s_full + 3, *o_full = s_full + 4, *drain = s_full + 5;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -719,13 +696,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!window_seq(a, b, sq) || kt * BT >= sq.L)   // (a bad one is flagged by the dQ kernel)
         return;
     const int L = sq.L;
-    const int n_sub = (L + BS - 1) / BS;
+    const int n_qt = (L + BT - 1) / BT;
     const int near = near_end(kt, a.window, L);
-    const bool in_parts = kt < p.sink_tiles && near < n_sub;  // several CTAs form this tile's sums
-    int s0 = 2 * kt, s1 = near;                               // 64-query sub-tiles
+    const bool in_parts = kt < p.sink_tiles && near < n_qt;   // several CTAs form this tile's sums
+    int s0 = kt, s1 = near;                                   // 128-query tiles
     if (slot > 0) {
         s0 = near + (slot - 1) * p.piece;
-        s1 = min(s0 + p.piece, n_sub);
+        s1 = min(s0 + p.piece, n_qt);
         if (s0 >= s1)
             return;
     }
@@ -738,10 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&kv_full[s], 32);         // the load warp's lanes
             ptx::mbar_init(&kv_empty[s], 1);
         }
-        for (int k = 0; k < 2; ++k) {
-            ptx::mbar_init(&s_full[k], 1);
-            ptx::mbar_init(&p_full[k], kRowWarps);
-        }
+        ptx::mbar_init(s_full, 1);
+        ptx::mbar_init(dp_full, 1);
+        ptx::mbar_init(p_full, kRowWarps);
+        ptx::mbar_init(ds_full, kRowWarps);
         ptx::mbar_init(o_full, 1);
         ptx::mbar_init(drain, 1);
         *abort_flag = 0;
@@ -762,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     bool aborted = false;
-    uint8_t *tile_k = smem, *tile_v = smem + C::kResBytes;
+    uint8_t *tile_k = smem, *tile_v = smem + C::kTileBytes;
     uint8_t *ring = smem + C::kOffRing;
     float *stats = reinterpret_cast<float *>(smem + C::kOffStat);
 
@@ -772,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < C::kStages; ++s)
             last_phase[s] = -1;
         if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(a_full, 2 * C::kResBytes);
+            ptx::mbar_arrive_expect_tx(a_full, 2 * C::kTileBytes);
             for (int c = 0; c < C::kChunks; ++c) {
                 ptx::tma_load_4d(tile_k + c * kChunkBytes, &p.tm_k, a_full, c * 64, 0, hk,
                                  int(sq.k0 + int64_t(kt) * BT));
@@ -785,10 +762,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int h = hk * p.G, i = s0;
         for (int s = 0; s < n_q; ++s) {
             const int64_t stat0 = stat_row(a, b, h, sq.q0);
-            float ls[BS / 32], ds[BS / 32];
+            float ls[BT / 32], ds[BT / 32];
 #pragma unroll
-            for (int u = 0; u < BS / 32; ++u) {
-                const int q = i * BS + lane * (BS / 32) + u;
+            for (int u = 0; u < BT / 32; ++u) {
+                const int q = i * BT + u * 32 + lane;
                 ls[u] = q < L ? a.lse[stat0 + q] : 0.f;
                 ds[u] = q < L ? p.D[stat0 + q] : 0.f;
             }
@@ -799,21 +776,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             if (lane == 0) {
                 uint8_t *dst = ring + stage * C::kStageBytes;
-                const int row = int(sq.q0 + int64_t(i) * BS);
+                const int row = int(sq.q0 + int64_t(i) * BT);
                 ptx::mbar_expect_tx(&kv_full[stage], C::kStageBytes);
                 for (int c = 0; c < C::kChunks; ++c) {
-                    ptx::tma_load_4d(dst + c * kSubChunkBytes, &p.tm_q, &kv_full[stage], c * 64, 0,
-                                     h, row);
-                    ptx::tma_load_4d(dst + C::kSubBytes + c * kSubChunkBytes, &p.tm_do,
+                    ptx::tma_load_4d(dst + c * kChunkBytes, &p.tm_q, &kv_full[stage], c * 64, 0, h,
+                                     row);
+                    ptx::tma_load_4d(dst + C::kTileBytes + c * kChunkBytes, &p.tm_do,
                                      &kv_full[stage], c * 64, 0, h, row);
                 }
                 last_phase[stage] = int(phase);
             }
-            float *st = stats + stage * (2 * BS);
+            float *st = stats + stage * (2 * BT);
 #pragma unroll
-            for (int u = 0; u < BS / 32; ++u) {
-                st[lane * (BS / 32) + u] = ls[u] * kLog2e;
-                st[BS + lane * (BS / 32) + u] = ds[u];
+            for (int u = 0; u < BT / 32; ++u) {
+                st[u * 32 + lane] = -ls[u] * kLog2e;
+                st[BT + u * 32 + lane] = -ds[u];
             }
             ptx::mbar_arrive(&kv_full[stage]);       // all lanes, after their writes
             if (++stage == C::kStages) {
@@ -834,85 +811,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kWarpMma) {
         // ======================= MMA issuer (whole warp) =====================
-        // Order: S^T_0, dP^T_0; per step s: S^T_{s+1}, dP^T_{s+1} (other buffer), dV +=
-        // P^T_s dO_s, dK += dS^T_s Q_s.
-        constexpr uint32_t idesc_ss = ptx::idesc_bf16_f32(BT, BS, false);
+        constexpr uint32_t idesc_ss = ptx::idesc_bf16_f32(BT, BT, false);
         constexpr uint32_t idesc_ts = ptx::idesc_bf16_f32(BT, D, true);
         constexpr uint64_t desc_kmajor = ptx::smem_desc_base(16, 1024);
-        constexpr uint64_t desc_mnmajor = ptx::smem_desc_base(kSubChunkBytes, 1024);
+        constexpr uint64_t desc_mnmajor = ptx::smem_desc_base(kChunkBytes, 1024);
         const uint64_t dk = ptx::smem_desc(desc_kmajor, ptx::smem_u32(tile_k));
         const uint64_t dvk = ptx::smem_desc(desc_kmajor, ptx::smem_u32(tile_v));
         const uint32_t ring_addr = ptx::smem_u32(ring);
-        int stage = 0, i = s0;
-        uint32_t phase = 0;
-        int st0 = 0, st1 = 0;                       // ring stage of the step in each buffer
-        auto issue_s = [&](int s) -> bool {
-            if (!ptx::mbar_wait_warp(&kv_full[stage], phase, abort_flag, a.err_word))
+        int i = s0;
+        // waits for step j's Q and dO
+        auto ready = [&](int j) -> bool {
+            const int st = j % C::kStages;
+            if (!ptx::mbar_wait_warp(&kv_full[st], uint32_t(j / C::kStages) & 1u, abort_flag,
+                                     a.err_word))
                 return false;
-            (s & 1 ? st1 : st0) = stage;
-            if ((i + 1) * BS > L) {                 // rows behind the sequence's end
-                clear_rows<2 * C::kChunks>(ring + stage * C::kStageBytes, L - i * BS, BS,
-                                           kSubChunkBytes);
+            if ((i + 1) * BT > L) {                 // rows behind the sequence's end
+                clear_rows<2 * C::kChunks>(ring + st * C::kStageBytes, L - i * BT, BT, kChunkBytes);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
             }
             if (++i == s1)
                 i = s0;
-            const uint32_t qaddr = ring_addr + stage * C::kStageBytes;
-            if (++stage == C::kStages) {
-                stage = 0;
-                phase ^= 1u;
-            }
             ptx::tc_fence_after_sync();
-            const uint64_t dq = ptx::smem_desc(desc_kmajor, qaddr);
-            const uint64_t ddo = ptx::smem_desc(desc_kmajor, qaddr + C::kSubBytes);
-            const uint32_t buf = tmem + uint32_t(s & 1) * kColBuf;
+            return true;
+        };
+        auto stage = [&](int j) { return ring_addr + uint32_t(j % C::kStages) * C::kStageBytes; };
+        // S^T = K Q^T, dP^T = V dO^T
+        auto issue = [&](uint32_t to, uint64_t da, uint32_t addr, uint64_t *bar) {
+            const uint64_t db = ptx::smem_desc(desc_kmajor, addr);
             if (ptx::elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    ptx::mma_ss(buf, dk + kmajor_off(kk, kChunkBytes),
-                                dq + kmajor_off(kk, kSubChunkBytes), idesc_ss, kk > 0 ? 1u : 0u);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    ptx::mma_ss(buf + kColDP, dvk + kmajor_off(kk, kChunkBytes),
-                                ddo + kmajor_off(kk, kSubChunkBytes), idesc_ss, kk > 0 ? 1u : 0u);
-                ptx::mma_commit(&s_full[s & 1]);
+                    ptx::mma_ss(tmem + to, da + kmajor_off(kk, kChunkBytes),
+                                db + kmajor_off(kk, kChunkBytes), idesc_ss, kk > 0 ? 1u : 0u);
+                ptx::mma_commit(bar);
             }
             __syncwarp();
-            return true;
+        };
+        // dV += P^T dO, dK += dS^T Q
+        auto add = [&](uint32_t to, uint32_t from, uint32_t addr, bool first, uint64_t *bar) {
+            const uint64_t db = ptx::smem_desc(desc_mnmajor, addr);
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < BT / 16; ++kk)
+                    ptx::mma_ts(tmem + to, tmem + from + packed_col(kk),
+                                db + uint64_t((kk * 16 * 128) >> 4), idesc_ts,
+                                (!first || kk > 0) ? 1u : 0u);
+                if (bar != nullptr)
+                    ptx::mma_commit(bar);
+            }
+            __syncwarp();
         };
         do {
-            if (!ptx::mbar_wait_warp(a_full, 0, abort_flag, a.err_word) || !issue_s(0)) {
+            if (!ptx::mbar_wait_warp(a_full, 0, abort_flag, a.err_word) || !ready(0)) {
                 aborted = true;
                 break;
             }
-            for (int s = 0; s < n_q; ++s) {
-                if ((s + 1 < n_q && !issue_s(s + 1)) ||
-                    !ptx::mbar_wait_warp(&p_full[s & 1], uint32_t(s >> 1) & 1u, abort_flag,
-                                         a.err_word)) {
+            issue(0, dk, stage(0), s_full);
+            issue(kColDP, dvk, stage(0) + C::kTileBytes, dp_full);
+            for (int j = 0; j < n_q; ++j) {
+                const bool more = j + 1 < n_q;
+                if (!ptx::mbar_wait_warp(p_full, uint32_t(j) & 1u, abort_flag, a.err_word)) {
                     aborted = true;
                     break;
                 }
                 ptx::tc_fence_after_sync();
-                const int st = (s & 1) ? st1 : st0;
-                const uint32_t qaddr = ring_addr + st * C::kStageBytes;
-                const uint64_t dq_mn = ptx::smem_desc(desc_mnmajor, qaddr);
-                const uint64_t ddo_mn = ptx::smem_desc(desc_mnmajor, qaddr + C::kSubBytes);
-                const uint32_t a_tm = tmem + uint32_t(s & 1) * kColBuf;
-                if (ptx::elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < BS / 16; ++kk)
-                        ptx::mma_ts(tmem + kColAcc, a_tm + packed_col(kk),
-                                    ddo_mn + uint64_t((kk * 16 * 128) >> 4), idesc_ts,
-                                    (s > 0 || kk > 0) ? 1u : 0u);
-#pragma unroll
-                    for (int kk = 0; kk < BS / 16; ++kk)
-                        ptx::mma_ts(tmem + kColAcc + D, a_tm + kColDP + packed_col(kk),
-                                    dq_mn + uint64_t((kk * 16 * 128) >> 4), idesc_ts,
-                                    (s > 0 || kk > 0) ? 1u : 0u);
-                    ptx::mma_commit(&kv_empty[st]);
+                add(kColAcc, 0, stage(j) + C::kTileBytes, j == 0, nullptr);
+                if (more) {                         // S^T_{j+1} overwrites P^T_j, which dV has read
+                    if (!ready(j + 1)) {
+                        aborted = true;
+                        break;
+                    }
+                    issue(0, dk, stage(j + 1), s_full);
                 }
-                __syncwarp();
+                if (!ptx::mbar_wait_warp(ds_full, uint32_t(j) & 1u, abort_flag, a.err_word)) {
+                    aborted = true;
+                    break;
+                }
+                ptx::tc_fence_after_sync();
+                add(kColAcc + D, kColDP, stage(j), j == 0, &kv_empty[j % C::kStages]);
+                if (more)
+                    issue(kColDP, dvk, stage(j + 1) + C::kTileBytes, dp_full);
             }
         } while (false);
         if (ptx::elect_one()) {
@@ -925,50 +904,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ======================= key rows ==================================
         const int r = (warp & 3) * 32 + lane;        // key of the tile = TMEM lane
-        const int g = warp >> 2;                     // column group
+        const int g = warp >> 2, col0 = 32 * g;      // of the row's four threads; its columns
         const int k = kt * BT + r;
         const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
         const float sl = p.scale_log2;
-        const int col0 = g * 32;
         // queries that see the key: k .. last
         const int64_t end = k < a.sinks ? int64_t(L) : int64_t(k) + a.window;
         const int last = int(end < L ? end : L) - 1;
+        const uint32_t tS = tmem + lane_bits + uint32_t(col0);
         int i = s0;
-        for (int s = 0; s < n_q; ++s) {
+        for (int j = 0; j < n_q; ++j) {
+            const uint32_t par = uint32_t(j) & 1u;
+            const int q0 = i * BT + col0;            // this thread's first query
+            if (++i == s1)
+                i = s0;
             // the statistics arrive with the step's ring stage
-            const int st = s % C::kStages;
-            if (!row_wait(&kv_full[st], uint32_t(s / C::kStages) & 1u, abort_flag, a.err_word)) {
-                aborted = true;
-                break;
-            }
-            float lv[32], dd[32];
-            {
-                const float *lse2s = stats + st * (2 * BS) + col0;
-#pragma unroll
-                for (int e4 = 0; e4 < 8; ++e4) {
-                    const float4 l4 = *reinterpret_cast<const float4 *>(lse2s + 4 * e4);
-                    const float4 d4 = *reinterpret_cast<const float4 *>(lse2s + BS + 4 * e4);
-                    lv[4 * e4] = l4.x;
-                    lv[4 * e4 + 1] = l4.y;
-                    lv[4 * e4 + 2] = l4.z;
-                    lv[4 * e4 + 3] = l4.w;
-                    dd[4 * e4] = d4.x;
-                    dd[4 * e4 + 1] = d4.y;
-                    dd[4 * e4 + 2] = d4.z;
-                    dd[4 * e4 + 3] = d4.w;
-                }
-            }
-            if (!row_wait(&s_full[s & 1], uint32_t(s >> 1) & 1u, abort_flag, a.err_word)) {
+            const int st = j % C::kStages;
+            if (!row_wait(&kv_full[st], uint32_t(j / C::kStages) & 1u, abort_flag, a.err_word) ||
+                !row_wait(s_full, par, abort_flag, a.err_word)) {
                 aborted = true;
                 break;
             }
             ptx::tc_fence_after_sync();
-            const int lo = k - i * BS - col0, hi = last - i * BS - col0;   // seen columns
-            const uint32_t tS = tmem + lane_bits + uint32_t(s & 1) * kColBuf + col0;
-            uint32_t sv[32], dv[32], pk[16], dk[16];
+            const float *stat = stats + st * (2 * BT) + col0;
+            uint32_t sv[32], pk[16];
             ptx::tmem_ld32(tS, sv);
-            ptx::tmem_ld32(tS + kColDP, dv);
             ptx::tmem_wait_ld();
+            const int lo = k - q0, hi = last - q0;   // seen columns
             if (__any_sync(0xffffffffu, lo > 0 || hi < 31)) {
                 const uint32_t seen = low_bits(hi + 1) & ~low_bits(lo);
 #pragma unroll
@@ -976,39 +938,67 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(seen & (1u << e)))
                         sv[e] = __float_as_uint(-INFINITY);
             }
+            float2 pr[16];
 #pragma unroll
-            for (int e2 = 0; e2 < 16; ++e2) {
-                float pv[2], ds[2];
+            for (int e4 = 0; e4 < 8; ++e4) {
+                const float4 l4 = *reinterpret_cast<const float4 *>(stat + 4 * e4);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int e = 2 * e2 + u;
-                    pv[u] = ptx::ex2(fmaf(__uint_as_float(sv[e]), sl, -lv[e]));
-                    ds[u] = pv[u] * (__uint_as_float(dv[e]) - dd[e]);
+                for (int half = 0; half < 2; ++half) {
+                    const int e = 4 * e4 + 2 * half;
+                    const float2 x = __ffma2_rn(
+                        make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
+                        make_float2(sl, sl),
+                        half ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
+                    pr[e / 2] = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+                    pk[e / 2] = ptx::pack_bf16x2(pr[e / 2].x, pr[e / 2].y);
                 }
-                pk[e2] = ptx::pack_bf16x2(pv[0], pv[1]);
-                dk[e2] = ptx::pack_bf16x2(ds[0], ds[1]);
             }
-            ptx::tmem_st16(tS, pk);                   // P^T of this block, packed
-            ptx::tmem_st16(tS + kColDP, dk);          // dS^T of this block, packed
+            ptx::tmem_st16(tS, pk);                  // P^T of this block, packed
             ptx::tmem_wait_st();
             ptx::tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
-                ptx::mbar_arrive(&p_full[s & 1]);
-            if (++i == s1)
-                i = s0;
+                ptx::mbar_arrive(p_full);
+            if (!row_wait(dp_full, par, abort_flag, a.err_word)) {
+                aborted = true;
+                break;
+            }
+            ptx::tc_fence_after_sync();
+            uint32_t dv[32];
+            ptx::tmem_ld32(tS + kColDP, dv);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e4 = 0; e4 < 8; ++e4) {
+                const float4 d4 = *reinterpret_cast<const float4 *>(stat + BT + 4 * e4);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int e = 4 * e4 + 2 * half;
+                    const float2 y = __fmul2_rn(
+                        pr[e / 2],
+                        __fadd2_rn(make_float2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])),
+                                   half ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y)));
+                    pk[e / 2] = ptx::pack_bf16x2(y.x, y.y);
+                }
+            }
+            ptx::tmem_st16(tS + kColDP, pk);         // dS^T of this block, packed
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(ds_full);
         }
         if (!aborted && ptx::mbar_wait(o_full, 0, abort_flag, a.err_word)) {
             ptx::tc_fence_after_sync();
             const bool key_ok = k < L;
-            // group 0 writes dV, group 1 dK
-            const uint32_t acc = tmem + lane_bits + kColAcc + uint32_t(g * D);
-            const float mul = g == 0 ? 1.f : a.scale;
+            // groups 0 and 1 write dV, 2 and 3 dK, half of the columns each
+            const int of = g >> 1, c0 = (g & 1) * (D / 64), c1 = c0 + D / 64;
+            const uint32_t acc = tmem + lane_bits + kColAcc + uint32_t(of * D);
+            const float mul = of == 0 ? 1.f : a.scale;
             if (in_parts) {
-                float *part = p.parts + (((int64_t(bh) * p.sink_tiles + kt) * p.slots + slot) * 2 + g) *
+                float *part = p.parts + (((int64_t(bh) * p.sink_tiles + kt) * p.slots + slot) * 2 + of) *
                                             (BT * D) + r * D;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = c0; c < c1; ++c) {
                     uint32_t o[32];
                     ptx::tmem_ld32(acc + c * 32, o);
                     ptx::tmem_wait_ld();
@@ -1022,9 +1012,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             __uint_as_float(o[4 * q + 3]) * mul);
                 }
             } else {
-                __nv_bfloat16 *dst = g == 0 ? p.dV + (sq.k0 + k) * p.dv_stride
-                                            : p.dK + (sq.k0 + k) * p.dk_stride;
-                store_row(acc, mul, dst + int64_t(hk) * D, key_ok, 0, D / 32);
+                __nv_bfloat16 *dst = of == 0 ? p.dV + (sq.k0 + k) * p.dv_stride
+                                             : p.dK + (sq.k0 + k) * p.dk_stride;
+                store_row(acc, mul, dst + int64_t(hk) * D, key_ok, c0, c1);
             }
         }
     }
@@ -1050,10 +1040,10 @@ __global__ void __launch_bounds__(256) attn_window_join_kernel(const __grid_cons
     WindowSeq sq;
     if (!window_seq(a, b, sq) || kt * BT + r >= sq.L)
         return;
-    const int n_sub = (sq.L + BS - 1) / BS, near = near_end(kt, a.window, sq.L);
-    if (near >= n_sub)
+    const int n_qt = (sq.L + BT - 1) / BT, near = near_end(kt, a.window, sq.L);
+    if (near >= n_qt)
         return;
-    const int n = 1 + (n_sub - near + p.piece - 1) / p.piece;
+    const int n = 1 + (n_qt - near + p.piece - 1) / p.piece;
     const float *part = p.parts + (((int64_t(bh) * p.sink_tiles + kt) * p.slots) * 2 + g) * (BT * D) +
                         r * D + lane * (D / 32);
     float v[D / 32] = {};
@@ -1128,8 +1118,8 @@ int launch_attention_window_bwd(const WindowBwdArgs &w, cudaStream_t stream)
         !make_tmap_heads(&pq.tm_v, a.V, a.total_k, a.Hkv, 1, a.d, a.v_stride, BT) ||
         !make_tmap_heads(&pq.tm_k32, a.K, a.total_k, a.Hkv, 1, a.d, a.k_stride, kPad) ||
         !make_tmap_heads(&pq.tm_v32, a.V, a.total_k, a.Hkv, 1, a.d, a.v_stride, kPad) ||
-        !make_tmap_heads(&pk.tm_q, a.Q, a.total_q, a.H, 1, a.d, a.q_stride, BS) ||
-        !make_tmap_heads(&pk.tm_do, w.dO, a.total_q, a.H, 1, a.d, row, BS))
+        !make_tmap_heads(&pk.tm_q, a.Q, a.total_q, a.H, 1, a.d, a.q_stride, BT) ||
+        !make_tmap_heads(&pk.tm_do, w.dO, a.total_q, a.H, 1, a.d, row, BT))
         return FA_ERR_CUDA;
     pk.tm_k = pq.tm_k;
     pk.tm_v = pq.tm_v;

@@ -382,10 +382,10 @@ inline WindowBwdLayout window_bwd_layout(int B, int N, int64_t total, int H, int
     WindowBwdLayout L;
     if (sinks >= N)            // every earlier key is seen
         window = N;
-    const int64_t n_sub = (int64_t(N) + 63) / 64, near = (int64_t(window) + 127 + 63) / 64;
-    L.piece = int(near < 16 ? 16 : near > n_sub ? n_sub : near);
+    const int64_t n_qt = (int64_t(N) + 127) / 128, near = (int64_t(window) + 127 + 127) / 128;
+    L.piece = int(near < 8 ? 8 : near > n_qt ? n_qt : near);
     // tile 0 has the most queries behind its window
-    const int64_t far = n_sub > near ? (n_sub - near + L.piece - 1) / L.piece : 0;
+    const int64_t far = n_qt > near ? (n_qt - near + L.piece - 1) / L.piece : 0;
     L.slots = sinks > 0 && far > 0 ? int(far) + 1 : 1;
     const int64_t tiles = ((sinks < N ? sinks : N) + 127) / 128;
     L.sink_tiles = L.slots > 1 ? int(tiles) : 0;
