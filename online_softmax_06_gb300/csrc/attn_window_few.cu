@@ -14,8 +14,8 @@
 //     exact running maximum, not at all);
 //   * an item (sequence, kv head, 16 or 32 query rows) is taken by a cluster of 1 to
 //     16 CTAs, a range of the places (window.cuh) each; the warps' parts meet in
-//     shared memory, the CTAs' in distributed shared memory, where each CTA joins a
-//     share of the values: one launch, no workspace.
+//     shared memory, and each CTA sends its sums to the one that joins that share of
+//     the values, through distributed shared memory: one launch, no workspace.
 // Keys that no query of an item sees (behind the sequence, between sinks and window)
 // are not read; their rows are zeros.
 #include <cuda_bf16.h>
@@ -44,11 +44,14 @@ struct Cfg {
     static constexpr int kRowBytes = D * 2;
     static constexpr int kHalf = kKeys * kRowBytes;              // K or V of a block
     static constexpr int kRing = kWarps * kStages * 2 * kHalf;
-    // the warps' parts of O and the CTA's reuse the ring; behind it the rows' (m, l)
+    // behind the keys, the ring holds the warps' parts of O, then the CTAs' parts of
+    // this CTA's share
     static constexpr int kPart = kRows * D * 4;
-    static constexpr int kOffO = kWarps * kPart;
-    static constexpr int kOffMl = kRing > kOffO + kPart ? kRing : kOffO + kPart;
-    static constexpr int kSmem = kOffMl + (kWarps + 1) * kRows * 8;
+    static_assert((kWarps + 1) * kPart <= kRing, "shared memory");
+    static constexpr int kOffQ = kRing;
+    static constexpr int kOffMl = kOffQ + kRows * kRowBytes;     // the warps' rows' (m, l), weights
+    static constexpr int kOffCl = kOffMl + kWarps * kRows * 8;   // the CTAs' (m, l)
+    static constexpr int kSmem = kOffCl + 16 * kRows * 8;
 };
 
 struct Params {
@@ -92,12 +95,16 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float2 ld_cluster2(uint32_t addr)
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v)
 {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr)
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x),
+                 "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
-    return v;
+}
+__device__ __forceinline__ void st_cluster2(uint32_t addr, float2 v)
+{
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y)
+                 : "memory");
 }
 __device__ __forceinline__ void cluster_sync()
 {
@@ -136,25 +143,53 @@ __global__ void __launch_bounds__(kThreads) attn_window_few_kernel(const __grid_
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = ptx::smem_u32(smem) + uint32_t(warp) * kStages * 2 * C::kHalf;
 
-    // ---- copies: a lane takes one 16-byte unit of every kLanesPerRow-th row -------------
+    // ---- copies: a lane takes one 16-byte unit of every kRowsPerCopy-th row -------------
     constexpr int kUnits = D / 8, kRowsPerCopy = 32 / kUnits, kCopies = kKeys / kRowsPerCopy;
     const int cu = lane % kUnits, cr = lane / kUnits;
     const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(a.K) + sq.k0 * a.k_stride +
                               int64_t(hk) * D + cu * 8;
     const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.V) + sq.k0 * a.v_stride +
                               int64_t(hk) * D + cu * 8;
+    const int64_t k_step = int64_t(kRowsPerCopy) * a.k_stride;
+    const int64_t v_step = int64_t(kRowsPerCopy) * a.v_stride;
     auto copy = [&](int blk, int stage) {
-        const uint32_t dst = ring + uint32_t(stage) * 2 * C::kHalf;
+        const uint32_t dst = ring + uint32_t(stage) * 2 * C::kHalf + cr * C::kRowBytes;
+        const int v0 = blk * kKeys;
+        if (v0 >= w.sp && v0 + kKeys <= w.places) {
+            // a block of the window: consecutive rows, all there
+            const int64_t key = w.lo + v0 - w.sp + cr;
+            const __nv_bfloat16 *ks = kp + key * a.k_stride, *vs = vp + key * a.v_stride;
 #pragma unroll
+            for (int c = 0; c < kCopies; ++c) {
+                const int row = cr + c * kRowsPerCopy;
+                const uint32_t to = dst + c * kRowsPerCopy * C::kRowBytes + ((cu ^ (row & 7)) << 4);
+                cp16(to, ks, true);
+                cp16(to + C::kHalf, vs, true);
+                ks += k_step;
+                vs += v_step;
+            }
+            return;
+        }
+#pragma unroll 1
         for (int c = 0; c < kCopies; ++c) {
-            const int row = cr + c * kRowsPerCopy, v = blk * kKeys + row;
+            const int row = cr + c * kRowsPerCopy, v = v0 + row;
             const bool ok = v < w.places && (v >= w.sp || v < a.sinks);
             const int64_t key = !ok ? 0 : v < w.sp ? v : w.lo + v - w.sp;
-            const uint32_t to = dst + row * C::kRowBytes + ((cu ^ (row & 7)) << 4);
+            const uint32_t to = dst + c * kRowsPerCopy * C::kRowBytes + ((cu ^ (row & 7)) << 4);
             cp16(to, kp + key * a.k_stride, ok);
             cp16(to + C::kHalf, vp + key * a.v_stride, ok);
         }
     };
+    // the queries' rows, with the first block (rows behind the last: zeros)
+    const uint32_t qs = ptx::smem_u32(smem) + C::kOffQ;
+    for (int e = threadIdx.x; e < C::kRows * kUnits; e += kThreads) {
+        const int r = e / kUnits, u = e % kUnits, i = (r0 + r) / p.G, g = (r0 + r) % p.G;
+        const bool ok = r0 + r < rows;
+        cp16(qs + r * C::kRowBytes + ((u ^ (r & 7)) << 4),
+             static_cast<const __nv_bfloat16 *>(a.Q) + (ok ? (sq.q0 + i) * a.q_stride : 0) +
+                 int64_t(hk * p.G + g) * D + u * 8,
+             ok);
+    }
     int next = first + warp;                       // this warp's blocks: every kWarps-th
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s, next += kWarps) {
@@ -163,27 +198,27 @@ __global__ void __launch_bounds__(kThreads) attn_window_few_kernel(const __grid_
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
 
-    // ---- queries as fragments -----------------------------------------------------------
-    uint32_t qa[MT][D / 16][4];
+    // ---- queries as fragments (of 32 rows they are read again for each block) ----------------
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncthreads();
+    uint32_t qa[D / 16][4];
+    auto load_q = [&](int t, int k, uint32_t (&f)[4]) {
+        const int r = 16 * t + (lane & 15), u = 2 * k + (lane >> 4);
+        ldsm(f, qs + r * C::kRowBytes + ((u ^ (r & 7)) << 4));
+    };
+    if constexpr (MT == 1)
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+            load_q(0, k, qa[k]);
     int vhi[MT][2], vlo[MT][2];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int r = r0 + 16 * t + 8 * half + (lane >> 2);
-            const bool ok = r < rows;
-            const int i = ok ? r / p.G : 0, g = ok ? r % p.G : 0;
-            vhi[t][half] = ok ? i + off - w.lo + w.sp : -1;
+            vhi[t][half] = r < rows ? r / p.G + off - w.lo + w.sp : -1;
             const int64_t vl = int64_t(vhi[t][half]) - a.window + 1;
             vlo[t][half] = vl > w.sp ? int(vl) : w.sp;
-            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.Q) +
-                                     (sq.q0 + i) * a.q_stride + int64_t(hk * p.G + g) * D +
-                                     2 * (lane & 3);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                qa[t][k][half] = ok ? *reinterpret_cast<const uint32_t *>(q + 16 * k) : 0u;
-                qa[t][k][2 + half] = ok ? *reinterpret_cast<const uint32_t *>(q + 16 * k + 8) : 0u;
-            }
         }
     // places that all queries of the item see: [all0, all1]
     const int64_t al = int64_t(i1 - 1 + off - w.lo + w.sp) - a.window + 1;
@@ -222,8 +257,10 @@ __global__ void __launch_bounds__(kThreads) attn_window_few_kernel(const __grid_
             ldsm(f, ks + mr * C::kRowBytes + (((2 * k + mu) ^ (mr & 7)) << 4));
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                mma16(s[t][0], qa[t][k], f[0], f[1]);
-                mma16(s[t][1], qa[t][k], f[2], f[3]);
+                if constexpr (MT > 1)
+                    load_q(t, k, qa[k]);
+                mma16(s[t][0], qa[k], f[0], f[1]);
+                mma16(s[t][1], qa[k], f[2], f[3]);
             }
         }
         // ---- mask, running maximum, P -------------------------------------------------
@@ -301,8 +338,7 @@ __global__ void __launch_bounds__(kThreads) attn_window_few_kernel(const __grid_
     // ---- the warps' parts, through shared memory ----------------------------------------
     __syncthreads();                               // all are done with the ring
     float *parts = reinterpret_cast<float *>(smem);
-    float *cta_o = reinterpret_cast<float *>(smem + C::kOffO);
-    float2 *ml = reinterpret_cast<float2 *>(smem + C::kOffMl);   // [warp][row], then the CTA's
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::kOffMl);   // [warp][row]
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -319,74 +355,88 @@ __global__ void __launch_bounds__(kThreads) attn_window_few_kernel(const __grid_
                 *reinterpret_cast<float2 *>(dst + 8 * n) =
                     make_float2(o[t][n][2 * half], o[t][n][2 * half + 1]);
         }
-    __syncthreads();
-    // the factor of a part with maximum m beside the largest, M (one without keys: 0)
+    // all CTAs of the cluster are done with their rings
+    if (p.split > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+
+    // (m, l) of several parts joined: the largest m, the sum of l at it; a part's factor
     auto weight = [](float mv, float M) { return mv == -INFINITY ? 0.f : ptx::ex2(mv - M); };
-    constexpr int kPairs = C::kRows * D / 2;
-    for (int e = threadIdx.x; e < kPairs; e += kThreads) {
-        const int r = e / (D / 2), c = e % (D / 2) * 2;
-        float M = -INFINITY;
+    const uint32_t share = ptx::smem_u32(smem) + kWarps * C::kPart;
+    const uint32_t cl = ptx::smem_u32(smem) + C::kOffCl;
+    constexpr int kQuads = C::kRows * D / 4;       // four values of a row each
+    const int per = kQuads / p.split;              // of a CTA's share
+    // a thread's quads are of the same columns of rows kThreads / (D / 4) apart
+    for (int e = threadIdx.x; e < kQuads; e += kThreads) {
+        const int r = e / (D / 4), c = e % (D / 4) * 4;
+        float2 s[kWarps];
+        float4 x[kWarps];
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k)
-            M = fmaxf(M, ml[k * C::kRows + r].x);
-        float2 v = make_float2(0.f, 0.f);
+        for (int k = 0; k < kWarps; ++k) {
+            s[k] = ml[k * C::kRows + r];
+            x[k] = *reinterpret_cast<const float4 *>(parts + (k * C::kRows + r) * D + c);
+        }
+        const float M = fmaxf(fmaxf(s[0].x, s[1].x), fmaxf(s[2].x, s[3].x));
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
-            const float2 s = ml[k * C::kRows + r];
-            const float f = weight(s.x, M);
-            const float2 x = *reinterpret_cast<const float2 *>(parts + (k * C::kRows + r) * D + c);
-            v.x = fmaf(f, x.x, v.x);
-            v.y = fmaf(f, x.y, v.y);
-            sum = fmaf(f, s.y, sum);
+            const float f = weight(s[k].x, M);
+            v.x = fmaf(f, x[k].x, v.x);
+            v.y = fmaf(f, x[k].y, v.y);
+            v.z = fmaf(f, x[k].z, v.z);
+            v.w = fmaf(f, x[k].w, v.w);
+            sum = fmaf(f, s[k].y, sum);
         }
-        *reinterpret_cast<float2 *>(cta_o + r * D + c) = v;
-        if (c == 0)
-            ml[kWarps * C::kRows + r] = make_float2(M, sum);
+        const int owner = e / per;
+        st_cluster4(cluster_addr(share + uint32_t(part * per + e % per) * 16, uint32_t(owner)), v);
+        // the row's (m, l) to every CTA: one column's thread each
+        const int to = c / 4;
+        if (to < p.split)
+            st_cluster2(cluster_addr(cl + uint32_t(part * C::kRows + r) * 8, uint32_t(to)),
+                        make_float2(M, sum));
     }
     if (p.split > 1)
         cluster_sync();
     else
         __syncthreads();
 
-    // ---- the CTAs' parts: each joins a share of the values ---------------------------------
-    const uint32_t o_addr = ptx::smem_u32(cta_o), ml_addr = ptx::smem_u32(ml + kWarps * C::kRows);
-    for (int e = part * kThreads + threadIdx.x; e < kPairs; e += p.split * kThreads) {
-        const int r = e / (D / 2), c = e % (D / 2) * 2;
+    // ---- the CTAs' parts of this one's share ------------------------------------------------
+    const float4 *mine = reinterpret_cast<const float4 *>(smem + kWarps * C::kPart);
+    const float2 *cml = reinterpret_cast<const float2 *>(smem + C::kOffCl);
+    for (int q = threadIdx.x; q < per; q += kThreads) {
+        const int e = part * per + q, r = e / (D / 4), c = e % (D / 4) * 4;
         if (r0 + r >= rows)
             break;
-        float M = -INFINITY, sum = 0.f;
-        float2 v = make_float2(0.f, 0.f);
-        if (p.split == 1) {
-            const float2 s = ml[kWarps * C::kRows + r];
-            M = s.x;
-            sum = s.y;
-            v = *reinterpret_cast<const float2 *>(cta_o + r * D + c);
-        } else {
-            for (int k = 0; k < p.split; ++k)
-                M = fmaxf(M, ld_cluster2(cluster_addr(ml_addr + r * 8, uint32_t(k))).x);
-            for (int k = 0; k < p.split; ++k) {
-                const float2 s = ld_cluster2(cluster_addr(ml_addr + r * 8, uint32_t(k)));
-                const float2 x =
-                    ld_cluster2(cluster_addr(o_addr + uint32_t(r * D + c) * 4, uint32_t(k)));
-                const float f = weight(s.x, M);
-                v.x = fmaf(f, x.x, v.x);
-                v.y = fmaf(f, x.y, v.y);
-                sum = fmaf(f, s.y, sum);
-            }
+        float M = -INFINITY;
+#pragma unroll 4
+        for (int k = 0; k < p.split; ++k)
+            M = fmaxf(M, cml[k * C::kRows + r].x);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < p.split; ++k) {
+            const float2 s = cml[k * C::kRows + r];
+            const float4 x = mine[k * per + q];
+            const float f = weight(s.x, M);
+            v.x = fmaf(f, x.x, v.x);
+            v.y = fmaf(f, x.y, v.y);
+            v.z = fmaf(f, x.z, v.z);
+            v.w = fmaf(f, x.w, v.w);
+            sum = fmaf(f, s.y, sum);
         }
         const int i = (r0 + r) / p.G, h = hk * p.G + (r0 + r) % p.G;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.O) +
-                                      ((sq.q0 + i) * a.H + h) * D + c) =
-            ptx::pack_bf16x2(v.x * inv, v.y * inv);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.O) +
+                                   ((sq.q0 + i) * a.H + h) * D + c) =
+            make_uint2(ptx::pack_bf16x2(v.x * inv, v.y * inv),
+                       ptx::pack_bf16x2(v.z * inv, v.w * inv));
         if (c == 0)
             a.lse[a.cu_seqlens_q != nullptr ? int64_t(h) * a.total_q + sq.q0 + i
                                             : (int64_t(b) * a.H + h) * a.Nq + i] =
                 sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
     }
-    if (p.split > 1)
-        cluster_sync();                            // its shared memory was being read
 }
 
 template <int D, int MT>
@@ -435,12 +485,16 @@ int launch_attention_window_few(const WindowArgs &a, cudaStream_t stream)
     const int mt = rows <= 16 ? 1 : 2;
     p.row_blocks = int((rows + 16 * mt - 1) / (16 * mt));
     const int64_t items = int64_t(a.B) * a.Hkv * p.row_blocks;
-    // CTAs of an item: a power of two, as many as make some 6 for each of the 304
-    // places there are, as long as each has 128 keys at least
+    // CTAs of an item: a power of two.  Up to one for each of the 304 places there are,
+    // as long as each has 128 keys at least (4 x 16 sequences of 1043 keys: 15.7 us with
+    // four CTAs, 16.8 with two, 24.7 with eight, which are more than the places); one step
+    // more where each then has 1024 (8 items of 8196 keys: 12.1 us with 16, 14.1 with 8;
+    // 512 items of 4100: 137 with one, 143 with two, 177 with eight).
     int64_t keys = int64_t(a.window) + a.Nq - 1 + a.sinks;
     keys = keys < a.Nk ? keys : a.Nk;
     p.split = 1;
-    while (p.split < 16 && items * p.split < 6 * 304 && keys >= int64_t(p.split) * 2 * 128)
+    while (p.split < 16 && ((items * p.split * 2 <= 304 && keys >= int64_t(p.split) * 2 * 128) ||
+                            (items * p.split < 304 && keys >= int64_t(p.split) * 2 * 1024)))
         p.split *= 2;
     const int64_t blocks = items * p.split;
     if (blocks > 0x7fffffffLL)
