@@ -932,8 +932,15 @@ def attention_kv4(q, cache, page_table, seqlens, max_seqlen: int | None = None, 
 # ---- attention with a sliding window and sinks --------------------------------------
 
 # As with the 4-bit cache, what shapes, strides, types and devices say is checked once for
-# each set of them (a decode step is short enough for the checks to show); new tensors are
-# made with the strides at hand, which takes torch half the time.
+# each set of them (a decode step is short enough for the checks to show).  New tensors are
+# made with the strides at hand, which takes torch half the time, and the sizes are kept as
+# the C types that the call takes.
+
+def _c_sizes(strides, *sizes):
+    """64-bit strides, and sizes: those given as a pair (n,) in 64 bits, the others as int."""
+    return ([ctypes.c_int64(s) for s in strides],
+            tuple(ctypes.c_int64(s[0]) if isinstance(s, tuple) else ctypes.c_int(s) for s in sizes))
+
 
 def _like(t):
     """What a plan's checks look at of a tensor, or None."""
@@ -1024,7 +1031,8 @@ def _plan_window(q, k, v, cu_q, cu_k, seqlens, max_q, max_k):
     import torch
     sizes, index, lse = _window_shapes(q, k, v, cu_q, cu_k, seqlens, max_q, max_k)
     (qs, ks, vs, B, Nq, total_q, Nk, total_k, H, hkv, d) = sizes
-    return (qs, ks, vs, (B, Nq, total_q, Nk, total_k, H, hkv, d), index,
+    (qs, ks, vs), sizes = _c_sizes((qs, ks, vs), B, Nq, (total_q,), Nk, (total_k,), H, hkv, d)
+    return (qs, ks, vs, sizes, index,
             (q[0], _dense(q[0]), torch.bfloat16, index),
             (torch.Size(lse), _dense(lse), torch.float32, index), 1.0 / math.sqrt(max(d, 1)))
 
@@ -1080,7 +1088,8 @@ def _plan_window_bwd(q, k, v, o, do, dq, dk, dv, cu, max_seqlen, window, sinks):
     rows = [_row_stride(like[0], n[1] if t is None else t[1], name)
             for t, like, n, name in ((dq, q, new[0], "dq"), (dk, k, new[1], "dk"),
                                      (dv, v, new[2], "dv"))]
-    return (qs, ks, vs, rows, (B, N, total, H, hkv, d), index, new,
+    (qs, ks, vs, *rows), sizes = _c_sizes((qs, ks, vs, *rows), B, N, (total,), H, hkv, d)
+    return (qs, ks, vs, rows, sizes, index, new,
             (torch.Size(lse), None, torch.float32, index), nbytes, 1.0 / math.sqrt(max(d, 1)))
 
 
@@ -1145,7 +1154,8 @@ def _plan_norm_rope(pairs, weights, freq, pos):
             for t, like, n, name in zip(pair, (q, k), new, ("q", "k"))]
     nbytes = fa_qk_norm_rope_bwd_workspace_bytes(total, q[-2], k[-2], q[-1])
     _check(int(min(nbytes, 0)), "fa_qk_norm_rope: d")
-    return rows, (total, q[-2], k[-2], q[-1], rot), index, new, nbytes
+    rows, sizes = _c_sizes(rows, (total,), q[-2], k[-2], q[-1], rot)
+    return rows, sizes, index, new, nbytes
 
 
 def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None,
@@ -1191,8 +1201,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, inv_fre
         dq = torch.empty_strided(*new[0], dtype=torch.bfloat16, device=q.device)
     if dk is None:
         dk = torch.empty_strided(*new[1], dtype=torch.bfloat16, device=q.device)
-    d = sizes[3]
-    dwq, dwk = (None if w is None else torch.empty_strided((d,), (1,), dtype=torch.float32,
+    dwq, dwk = (None if w is None else torch.empty_strided(w.shape, (1,), dtype=torch.float32,
                                                            device=q.device)
                 for w in (q_weight, k_weight))
     if workspace is None:

@@ -411,7 +411,7 @@ struct NormRopeArgs {
     int d, rot, interleaved;
     float eps;
 };
-constexpr int kNormRopeCtas = 152 * 4;     // the gradient's CTAs, each with sums of its own
+constexpr int kNormRopeCtas = 152 * 2;     // the gradient's CTAs, each with sums of its own
 int launch_norm_rope_fwd(const NormRopeArgs &a, cudaStream_t stream);
 int launch_norm_rope_bwd(const NormRopeArgs &a, cudaStream_t stream);
 

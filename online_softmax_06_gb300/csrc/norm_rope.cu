@@ -47,6 +47,27 @@ struct Params {
     float eps;
 };
 
+// f / (2 pi) modulo 1 as a 64-bit fraction, in whole numbers: f = m 2^e, times 2^66 /
+// (2 pi), shifted.  (Products in fp64, of which an SM has two lanes, took half of the
+// kernel's time where a warp has one token.)
+__device__ __forceinline__ uint64_t turns(double f)
+{
+    const uint64_t bits = uint64_t(__double_as_longlong(f));
+    const int ex = int(bits >> 52) & 0x7ff;
+    const uint64_t m = (bits & 0xfffffffffffffull) | (ex != 0 ? 1ull << 52 : 0);
+    constexpr uint64_t c = 0xa2f9836e4e44152aull;    // round(2^66 / (2 pi))
+    const uint64_t lo = m * c, hi = __umul64hi(m, c);
+    const int s = 2 + 1075 - (ex != 0 ? ex : 1);     // result = (hi : lo) >> s, modulo 2^64
+    uint64_t r = 0;
+    if (s <= 0)
+        r = s > -64 ? lo << -s : 0;
+    else if (s < 64)
+        r = (hi << (64 - s)) | (lo >> s);
+    else if (s < 128)
+        r = hi >> (s - 64);
+    return (bits >> 63) != 0 ? 0 - r : r;
+}
+
 // What a lane does in its row, the same for all rows of a token.
 template <int D, bool PAIRS>
 struct Lane {
@@ -64,14 +85,8 @@ struct Lane {
         oa = PAIRS || !turned ? 8 * l : 4 * l;
         ob = PAIRS || !turned ? oa + 4 : p.rot / 2 + oa;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            turn[i] = 0;
-            if (turned) {
-                double f = p.freq[4 * l + i] * 0.15915494309189533577;   // 1 / (2 pi)
-                f -= floor(f);
-                turn[i] = uint64_t(f * 18446744073709551616.0);          // saturates
-            }
-        }
+        for (int i = 0; i < 4; ++i)
+            turn[i] = turned ? turns(p.freq[4 * l + i]) : 0;
     }
     __device__ __forceinline__ void at(int32_t pos)
     {
@@ -147,7 +162,8 @@ __device__ __forceinline__ void unpack(const uint2 (&v)[2], float (&f)[8])
 }
 
 template <int D, bool PAIRS>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_fwd_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(32 * kWarps, 4)
+    norm_rope_fwd_kernel(const __grid_constant__ Params p)
 {
     using L = Lane<D, PAIRS>;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -200,79 +216,167 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_fwd_kernel(const __grid
     }
 }
 
+// Rows, positions and weights of the gradient come through shared memory: a thread's own
+// copies (nobody else reads them), kStages - 1 passes ahead, so that an SM's loads in
+// flight do not depend on its registers.
+constexpr int kStages = 4;
+template <int D>
+struct BwdSmem {
+    static constexpr int kSlot = 16 * 32 * kWarps;              // 16 bytes a thread
+    static constexpr int kSlots = 2 * kBwdRows;                 // x and g of each row
+    static constexpr int kOffPos = kStages * kSlots * kSlot;
+    static constexpr int kOffW = kOffPos + kStages * 4 * 32 * kWarps;
+    static constexpr int kBytes = kOffW + 2 * D * 4;
+    static_assert(kWarps * 2 * D * 4 <= kOffPos, "the warps' sums use the rows' place");
+};
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+
+// Where a warp is in its units: pass `step` of token `t`.
+struct Place {
+    int64_t unit, t;
+    int step, last;
+    __device__ __forceinline__ void enter(const Params &p, int64_t u)
+    {
+        unit = u;
+        t = p.token_units == 1 ? u : u / p.token_units;
+        step = p.token_units == 1 ? 0 : int(u - t * p.token_units) * p.unit_steps;
+        last = min(step + p.unit_steps, p.steps[0] + p.steps[1]);
+    }
+    __device__ __forceinline__ void next(const Params &p, int64_t stride)
+    {
+        if (++step == last)
+            enter(p, unit + stride);
+    }
+};
+
 template <int D, bool PAIRS>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_bwd_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(32 * kWarps, 2)
+    norm_rope_bwd_kernel(const __grid_constant__ Params p)
 {
     using L = Lane<D, PAIRS>;
-    __shared__ float part[kWarps][2][D];
+    using S = BwdSmem<D>;
+    extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     L lane(p);
-    float dw[2][8] = {};
-    const int64_t units = p.tokens * p.token_units;
-    for (int64_t unit = int64_t(blockIdx.x) * kWarps + warp; unit < units;
-         unit += int64_t(gridDim.x) * kWarps) {
-        const int64_t t = unit / p.token_units;
-        const int first = int(unit - t * p.token_units) * p.unit_steps;
-        const int last = min(first + p.unit_steps, p.steps[0] + p.steps[1]);
-        if (p.rot > 0)
-            lane.at(p.pos[t]);
-        else
-            lane.at(0);
-        auto pass = [&](int of, int step, const float (&w)[8], float (&acc)[8]) {
-            const int h0 = step * kBwdRows * L::kPerWarp + lane.sub;
-            const __nv_bfloat16 *x = p.x[of] + t * p.xs[of], *g = p.g[of] + t * p.gs[of];
-            __nv_bfloat16 *y = p.y[of] + t * p.ys[of];
-            uint2 xv[kBwdRows][2], gv[kBwdRows][2];
+    const uint32_t base = ptx::smem_u32(smem);
+    const int64_t units = p.tokens * p.token_units, stride = int64_t(gridDim.x) * kWarps;
+    float *ws = reinterpret_cast<float *>(smem + S::kOffW);
+    for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarps)
+        ws[i] = p.w[i / D] != nullptr ? p.w[i / D][i % D] : 1.f;
+
+    auto slot = [&](int stage, int n) { return uint32_t((stage * S::kSlots + n) * S::kSlot); };
+    auto fetch = [&](const Place &at, int stage) {
+        const int of = at.step >= p.steps[0];                  // 0: Q, 1: K
+        const int h0 = (at.step - (of ? p.steps[0] : 0)) * kBwdRows * L::kPerWarp + lane.sub;
+        const __nv_bfloat16 *x = p.x[of] + at.t * p.xs[of], *g = p.g[of] + at.t * p.gs[of];
 #pragma unroll
-            for (int u = 0; u < kBwdRows; ++u) {
-                const int h = h0 + u * L::kPerWarp;
-                xv[u][0] = xv[u][1] = gv[u][0] = gv[u][1] = make_uint2(0, 0);
-                if (h < p.heads[of]) {
-                    lane.load(x + h * D, xv[u]);
-                    lane.load(g + h * D, gv[u]);
+        for (int n = 0; n < S::kSlots; ++n) {
+            const int h = h0 + (n >> 1) * L::kPerWarp;
+            if (h < p.heads[of]) {
+                const __nv_bfloat16 *row = (n & 1 ? g : x) + h * D;
+                const uint32_t to = base + slot(stage, n);
+                if constexpr (PAIRS) {
+                    copy_async<16>(to + threadIdx.x * 16, row + lane.oa);
+                } else {
+                    copy_async<8>(to + threadIdx.x * 8, row + lane.oa);
+                    copy_async<8>(to + S::kSlot / 2 + threadIdx.x * 8, row + lane.ob);
                 }
             }
+        }
+        if (p.rot > 0)
+            copy_async<4>(base + S::kOffPos + uint32_t(stage * 32 * kWarps + threadIdx.x) * 4,
+                          p.pos + at.t);
+    };
+    auto row = [&](int stage, int n, float (&f)[8]) {
+        const uint8_t *from = smem + slot(stage, n);
+        uint2 v[2];
+        if constexpr (PAIRS) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(from + threadIdx.x * 16);
+            v[0] = make_uint2(q.x, q.y);
+            v[1] = make_uint2(q.z, q.w);
+        } else {
+            v[0] = *reinterpret_cast<const uint2 *>(from + threadIdx.x * 8);
+            v[1] = *reinterpret_cast<const uint2 *>(from + S::kSlot / 2 + threadIdx.x * 8);
+        }
+        unpack(v, f);
+    };
+
+    Place ahead, at;
+    ahead.enter(p, int64_t(blockIdx.x) * kWarps + warp);
+    at = ahead;
 #pragma unroll
-            for (int u = 0; u < kBwdRows; ++u) {
-                const int h = h0 + u * L::kPerWarp;
-                float f[8], q[8], ss = 0.f, hx = 0.f;
-                unpack(xv[u], f);
-                unpack(gv[u], q);
-                if (lane.turned)
-                    lane.template rotate<true>(q);
+    for (int s = 0; s < kStages - 1; ++s) {
+        if (ahead.unit < units) {
+            fetch(ahead, s);
+            ahead.next(p, stride);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __syncthreads();                                           // the weights
+    float dw[2][8] = {};
+    int stage = 0;
+    int64_t angles = -1;                                       // the token whose angles these are
+    while (at.unit < units) {
+        if (ahead.unit < units) {
+            fetch(ahead, stage == 0 ? kStages - 1 : stage - 1);
+            ahead.next(p, stride);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        if (at.t != angles) {
+            angles = at.t;
+            lane.at(p.rot > 0 ? *reinterpret_cast<const int32_t *>(
+                                    smem + S::kOffPos + (stage * 32 * kWarps + threadIdx.x) * 4)
+                              : 0);
+        }
+        const int of = at.step >= p.steps[0];
+        const int h0 = (at.step - (of ? p.steps[0] : 0)) * kBwdRows * L::kPerWarp + lane.sub;
+        __nv_bfloat16 *y = p.y[of] + at.t * p.ys[of];
+        const float4 wa = *reinterpret_cast<const float4 *>(ws + of * D + lane.oa);
+        const float4 wb = *reinterpret_cast<const float4 *>(ws + of * D + lane.ob);
+        const float w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+        for (int u = 0; u < kBwdRows; ++u) {
+            const int h = h0 + u * L::kPerWarp;
+            float f[8], q[8], ss = 0.f, hx = 0.f;
+            row(stage, 2 * u, f);
+            row(stage, 2 * u + 1, q);
+            if (lane.turned)
+                lane.template rotate<true>(q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                ss = fmaf(f[i], f[i], ss);
+                hx = fmaf(q[i] * w[i], f[i], hx);
+            }
+            const float r = rsqrtf(L::sum(ss) * (1.f / D) + p.eps);
+            const float m = L::sum(hx) * r * (1.f / D);        // mean(h o x^)
+            if (h < p.heads[of]) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    ss = fmaf(f[i], f[i], ss);
-                    hx = fmaf(q[i] * w[i], f[i], hx);
+                    const float hat = f[i] * r;
+                    if (of == 0)
+                        dw[0][i] = fmaf(q[i], hat, dw[0][i]);
+                    else
+                        dw[1][i] = fmaf(q[i], hat, dw[1][i]);
+                    f[i] = r * fmaf(-hat, m, q[i] * w[i]);
                 }
-                const float r = rsqrtf(L::sum(ss) * (1.f / D) + p.eps);
-                const float m = L::sum(hx) * r * (1.f / D);     // mean(h o x^)
-                if (h < p.heads[of]) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float hat = f[i] * r;
-                        acc[i] = fmaf(q[i], hat, acc[i]);
-                        f[i] = r * fmaf(-hat, m, q[i] * w[i]);
-                    }
-                    lane.store(y + h * D, f);
-                }
+                lane.store(y + h * D, f);
             }
-        };
-        if (first < p.steps[0]) {
-            float w[8];
-            lane.weights(p.w[0], w);
-            for (int step = first; step < min(last, p.steps[0]); ++step)
-                pass(0, step, w, dw[0]);
         }
-        if (last > p.steps[0]) {
-            float w[8];
-            lane.weights(p.w[1], w);
-            for (int step = max(first, p.steps[0]); step < last; ++step)
-                pass(1, step - p.steps[0], w, dw[1]);
-        }
+        at.next(p, stride);
+        stage = stage == kStages - 1 ? 0 : stage + 1;
     }
     // the CTA's sums: rows of a warp, then warps, in a fixed order
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float *part = reinterpret_cast<float *>(smem);             // [warp][2][D]
 #pragma unroll
     for (int of = 0; of < 2; ++of)
 #pragma unroll
@@ -282,14 +386,14 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_bwd_kernel(const __grid
             for (int o = 16; o >= L::kLanes; o >>= 1)
                 v += __shfl_xor_sync(0xffffffffu, v, o);
             if (lane.sub == 0)
-                part[warp][of][i < 4 ? lane.oa + i : lane.ob + i - 4] = v;
+                part[(warp * 2 + of) * D + (i < 4 ? lane.oa + i : lane.ob + i - 4)] = v;
         }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarps) {
         float v = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k)
-            v += part[k][i / D][i % D];
+            v += part[k * 2 * D + i];
         p.partial[int64_t(blockIdx.x) * 2 * D + i] = v;
     }
 }
@@ -350,6 +454,18 @@ Params make_params(const NormRopeArgs &a, int rows, int64_t *units)
     return p;
 }
 
+template <int D, bool PAIRS>
+int launch_bwd(const Params &p, int64_t blocks, cudaStream_t stream)
+{
+    auto kern = norm_rope_bwd_kernel<D, PAIRS>;
+    static PerDeviceOnce once;
+    constexpr int smem = BwdSmem<D>::kBytes;
+    if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(kern), smem))
+        return FA_ERR_CUDA;
+    return launch_early(kern, dim3(unsigned(blocks)), 32 * kWarps, smem, stream, p) == cudaSuccess
+               ? FA_OK : FA_ERR_CUDA;
+}
+
 }  // namespace
 
 int launch_norm_rope_fwd(const NormRopeArgs &a, cudaStream_t stream)
@@ -378,15 +494,12 @@ int launch_norm_rope_bwd(const NormRopeArgs &a, cudaStream_t stream)
     blocks = blocks > kNormRopeCtas ? kNormRopeCtas : blocks;
     cudaError_t e = cudaSuccess;
     if (blocks > 0) {
-        const dim3 grid{unsigned(blocks)};
-        if (a.d == 64)
-            e = a.interleaved ? launch_early(norm_rope_bwd_kernel<64, true>, grid, 32 * kWarps, 0, stream, p)
-                              : launch_early(norm_rope_bwd_kernel<64, false>, grid, 32 * kWarps, 0, stream, p);
-        else
-            e = a.interleaved ? launch_early(norm_rope_bwd_kernel<128, true>, grid, 32 * kWarps, 0, stream, p)
-                              : launch_early(norm_rope_bwd_kernel<128, false>, grid, 32 * kWarps, 0, stream, p);
-        if (e != cudaSuccess)
-            return FA_ERR_CUDA;
+        const int rc = a.d == 64 ? a.interleaved ? launch_bwd<64, true>(p, blocks, stream)
+                                                 : launch_bwd<64, false>(p, blocks, stream)
+                       : a.interleaved ? launch_bwd<128, true>(p, blocks, stream)
+                                       : launch_bwd<128, false>(p, blocks, stream);
+        if (rc != FA_OK)
+            return rc;
     }
     if (a.dw[0] != nullptr || a.dw[1] != nullptr)
         e = launch_early(norm_rope_dw_kernel, dim3(unsigned(2 * a.d / 32)), 1024, 0, stream,
