@@ -82,7 +82,7 @@ __device__ __forceinline__ bool row_wait(uint64_t *bar, uint32_t parity, volatil
 {
     int ok = 1;
     if ((threadIdx.x & 31) == 0)
-        ok = ptx::mbar_wait(bar, parity, abort, err_word) ? 1 : 0;
+        ok = ptx::mbar_poll(bar, parity, abort, err_word) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
     __syncwarp();
     return ok != 0;
@@ -636,16 +636,18 @@ template <int D>
 struct CfgK {
     static constexpr int kChunks = D / 64;
     static constexpr uint32_t kTileBytes = BT * D * 2;
-    static constexpr int kStages = D == 128 ? 2 : 4;
-    static constexpr uint32_t kStageBytes = 2 * kTileBytes;
-    // [K][V][ring: Q_j, dO_j][statistics: (-lse log2 e, -D) x 128 a stage][barriers]
-    static constexpr uint32_t kOffRing = 2 * kTileBytes;
-    static constexpr uint32_t kOffStat = kOffRing + kStages * kStageBytes;
-    static constexpr uint32_t kOffBar = kOffStat + kStages * 2 * BT * 4;
-    static constexpr int kBars = 1 + 2 * kStages + 6;
-    static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16 + 1024;
+    // [K][V][three Q][two dO][statistics: two of (-lse log2 e, -D) x 128][barriers]: Q_j is
+    // read by S^T_j and, a step later, dK; dO_j by dP^T_j and dV soon after it
+    static constexpr int kQ = 3, kDO = 2;
+    static constexpr uint32_t kOffQ = 2 * kTileBytes;
+    static constexpr uint32_t kOffDO = kOffQ + kQ * kTileBytes;
+    static constexpr uint32_t kOffStat = kOffDO + kDO * kTileBytes;
+    static constexpr uint32_t kOffBar = kOffStat + 2 * 2 * BT * 4;
+    static constexpr int kBars = 1 + 2 * kQ + 2 * kDO + 2 + 6;
+    static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
+
 // 128-query tiles of a sequence that have a key of tile kt in their window: [kt,
 // near_end); those behind it see the tile's sinks alone.
 __device__ __forceinline__ int near_end(int kt, int window, int L)
@@ -660,12 +662,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_window_dkdv_kernel(const __grid_constant__ Params p)
 {
     using C = CfgK<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // aligned as the tiles need it, with no room to align it here
+    extern __shared__ __align__(1024) uint8_t smem_aligned[];
+    uint8_t *smem = smem_aligned;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
-    uint64_t *a_full = bars, *kv_full = bars + 1, *kv_empty = kv_full + C::kStages;
-    uint64_t *s_full = kv_empty + C::kStages, *dp_full = s_full + 1, *p_full = s_full + 2,
+    uint64_t *a_full = bars, *q_full = bars + 1, *q_empty = q_full + C::kQ;
+    uint64_t *do_full = q_empty + C::kQ, *do_empty = do_full + C::kDO, *st_full = do_empty + C::kDO;
+    uint64_t *s_full = st_full + 2, *dp_full = s_full + 1, *p_full = s_full + 2,
              *ds_full = s_full + 3, *o_full = s_full + 4, *drain = s_full + 5;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -711,9 +714,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         ptx::mbar_init(a_full, 1);
-        for (int s = 0; s < C::kStages; ++s) {
-            ptx::mbar_init(&kv_full[s], 32);         // the load warp's lanes
-            ptx::mbar_init(&kv_empty[s], 1);
+        for (int s = 0; s < C::kQ; ++s) {
+            ptx::mbar_init(&q_full[s], 1);
+            ptx::mbar_init(&q_empty[s], 1);
+        }
+        for (int s = 0; s < C::kDO; ++s) {
+            ptx::mbar_init(&do_full[s], 1);
+            ptx::mbar_init(&do_empty[s], 1);
+            ptx::mbar_init(&st_full[s], 32);         // the load warp's lanes
         }
         ptx::mbar_init(s_full, 1);
         ptx::mbar_init(dp_full, 1);
@@ -740,14 +748,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     bool aborted = false;
     uint8_t *tile_k = smem, *tile_v = smem + C::kTileBytes;
-    uint8_t *ring = smem + C::kOffRing;
     float *stats = reinterpret_cast<float *>(smem + C::kOffStat);
 
     if (warp == kWarpLoad) {
         // ======================= TMA producer (whole warp) ===================
-        int last_phase[C::kStages];
-        for (int s = 0; s < C::kStages; ++s)
-            last_phase[s] = -1;
+        // Per step j: Q_j (its place is free once dK_{j-3} is through), dO_j (dV_{j-2}),
+        // and the queries' statistics (dK_{j-2}: the rows are done with step j - 2).
         if (lane == 0) {
             ptx::mbar_arrive_expect_tx(a_full, 2 * C::kTileBytes);
             for (int c = 0; c < C::kChunks; ++c) {
@@ -757,11 +763,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  int(sq.k0 + int64_t(kt) * BT));
             }
         }
-        int stage = 0;
-        uint32_t phase = 0;
+        int q_issued = 0, do_issued = 0;
         int h = hk * p.G, i = s0;
-        for (int s = 0; s < n_q; ++s) {
+        for (int j = 0; j < n_q; ++j) {
             const int64_t stat0 = stat_row(a, b, h, sq.q0);
+            const int row = int(sq.q0 + int64_t(i) * BT);
+            auto load = [&](uint8_t *dst, const CUtensorMap *tm, uint64_t *full) {
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(full, C::kTileBytes);
+                    for (int c = 0; c < C::kChunks; ++c)
+                        ptx::tma_load_4d(dst + c * kChunkBytes, tm, full, c * 64, 0, h, row);
+                }
+                __syncwarp();
+            };
             float ls[BT / 32], ds[BT / 32];
 #pragma unroll
             for (int u = 0; u < BT / 32; ++u) {
@@ -769,34 +783,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ls[u] = q < L ? a.lse[stat0 + q] : 0.f;
                 ds[u] = q < L ? p.D[stat0 + q] : 0.f;
             }
-            int ok = 1;
-            if (lane == 0)
-                ok = ptx::mbar_wait(&kv_empty[stage], phase ^ 1u, abort_flag, a.err_word) ? 1 : 0;
-            if (!__shfl_sync(0xffffffffu, ok, 0))
+            const int qs = j % C::kQ, os = j % C::kDO;
+            if (!ptx::mbar_wait_warp(&q_empty[qs], (uint32_t(j / C::kQ) & 1u) ^ 1u, abort_flag,
+                                     a.err_word))
                 break;
-            if (lane == 0) {
-                uint8_t *dst = ring + stage * C::kStageBytes;
-                const int row = int(sq.q0 + int64_t(i) * BT);
-                ptx::mbar_expect_tx(&kv_full[stage], C::kStageBytes);
-                for (int c = 0; c < C::kChunks; ++c) {
-                    ptx::tma_load_4d(dst + c * kChunkBytes, &p.tm_q, &kv_full[stage], c * 64, 0, h,
-                                     row);
-                    ptx::tma_load_4d(dst + C::kTileBytes + c * kChunkBytes, &p.tm_do,
-                                     &kv_full[stage], c * 64, 0, h, row);
-                }
-                last_phase[stage] = int(phase);
-            }
-            float *st = stats + stage * (2 * BT);
+            load(smem + C::kOffQ + qs * C::kTileBytes, &p.tm_q, &q_full[qs]);
+            q_issued = j + 1;
+            if (!ptx::mbar_wait_warp(&do_empty[os], (uint32_t(j / C::kDO) & 1u) ^ 1u, abort_flag,
+                                     a.err_word))
+                break;
+            load(smem + C::kOffDO + os * C::kTileBytes, &p.tm_do, &do_full[os]);
+            do_issued = j + 1;
+            if (j >= 2 && !ptx::mbar_wait_warp(&q_empty[(j - 2) % C::kQ],
+                                               uint32_t((j - 2) / C::kQ) & 1u, abort_flag,
+                                               a.err_word))
+                break;
+            float *st = stats + os * (2 * BT);
 #pragma unroll
             for (int u = 0; u < BT / 32; ++u) {
                 st[u * 32 + lane] = -ls[u] * kLog2e;
                 st[BT + u * 32 + lane] = -ds[u];
             }
-            ptx::mbar_arrive(&kv_full[stage]);       // all lanes, after their writes
-            if (++stage == C::kStages) {
-                stage = 0;
-                phase ^= 1u;
-            }
+            ptx::mbar_arrive(&st_full[os]);          // all lanes, after their writes
             if (++i == s1) {
                 i = s0;
                 ++h;
@@ -804,9 +812,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0 && *abort_flag) {
             drain_wait(a_full, 0);
-            for (int s = 0; s < C::kStages; ++s)
-                if (last_phase[s] >= 0)
-                    drain_wait(&kv_full[s], uint32_t(last_phase[s]));
+            for (int j = q_issued > C::kQ ? q_issued - C::kQ : 0; j < q_issued; ++j)
+                drain_wait(&q_full[j % C::kQ], uint32_t(j / C::kQ) & 1u);
+            for (int j = do_issued > C::kDO ? do_issued - C::kDO : 0; j < do_issued; ++j)
+                drain_wait(&do_full[j % C::kDO], uint32_t(j / C::kDO) & 1u);
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -817,25 +826,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint64_t desc_mnmajor = ptx::smem_desc_base(kChunkBytes, 1024);
         const uint64_t dk = ptx::smem_desc(desc_kmajor, ptx::smem_u32(tile_k));
         const uint64_t dvk = ptx::smem_desc(desc_kmajor, ptx::smem_u32(tile_v));
-        const uint32_t ring_addr = ptx::smem_u32(ring);
+        const uint32_t q_addr = ptx::smem_u32(smem + C::kOffQ);
+        const uint32_t do_addr = ptx::smem_u32(smem + C::kOffDO);
         int i = s0;
-        // waits for step j's Q and dO
-        auto ready = [&](int j) -> bool {
-            const int st = j % C::kStages;
-            if (!ptx::mbar_wait_warp(&kv_full[st], uint32_t(j / C::kStages) & 1u, abort_flag,
-                                     a.err_word))
-                return false;
-            if ((i + 1) * BT > L) {                 // rows behind the sequence's end
-                clear_rows<2 * C::kChunks>(ring + st * C::kStageBytes, L - i * BT, BT, kChunkBytes);
+        auto q_tile = [&](int j) { return uint32_t(j % C::kQ) * C::kTileBytes; };
+        auto do_tile = [&](int j) { return uint32_t(j % C::kDO) * C::kTileBytes; };
+        // waits for step j's Q, for its dO; rows behind the sequence's end are cleared
+        auto tail = [&](uint8_t *tile, int i) {
+            if ((i + 1) * BT > L) {
+                clear_rows<C::kChunks>(tile, L - i * BT, BT, kChunkBytes);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
             }
-            if (++i == s1)
-                i = s0;
             ptx::tc_fence_after_sync();
+        };
+        auto q_ready = [&](int j) -> bool {
+            if (!ptx::mbar_wait_warp(&q_full[j % C::kQ], uint32_t(j / C::kQ) & 1u, abort_flag,
+                                     a.err_word))
+                return false;
+            tail(smem + C::kOffQ + q_tile(j), i);
             return true;
         };
-        auto stage = [&](int j) { return ring_addr + uint32_t(j % C::kStages) * C::kStageBytes; };
+        auto do_ready = [&](int j) -> bool {
+            if (!ptx::mbar_wait_warp(&do_full[j % C::kDO], uint32_t(j / C::kDO) & 1u, abort_flag,
+                                     a.err_word))
+                return false;
+            tail(smem + C::kOffDO + do_tile(j), i);
+            if (++i == s1)
+                i = s0;
+            return true;
+        };
         // S^T = K Q^T, dP^T = V dO^T
         auto issue = [&](uint32_t to, uint64_t da, uint32_t addr, uint64_t *bar) {
             const uint64_t db = ptx::smem_desc(desc_kmajor, addr);
@@ -857,42 +877,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::mma_ts(tmem + to, tmem + from + packed_col(kk),
                                 db + uint64_t((kk * 16 * 128) >> 4), idesc_ts,
                                 (!first || kk > 0) ? 1u : 0u);
-                if (bar != nullptr)
-                    ptx::mma_commit(bar);
+                ptx::mma_commit(bar);
             }
             __syncwarp();
         };
         do {
-            if (!ptx::mbar_wait_warp(a_full, 0, abort_flag, a.err_word) || !ready(0)) {
+            if (!ptx::mbar_wait_warp(a_full, 0, abort_flag, a.err_word) || !q_ready(0)) {
                 aborted = true;
                 break;
             }
-            issue(0, dk, stage(0), s_full);
-            issue(kColDP, dvk, stage(0) + C::kTileBytes, dp_full);
-            for (int j = 0; j < n_q; ++j) {
-                const bool more = j + 1 < n_q;
-                if (!ptx::mbar_wait_warp(p_full, uint32_t(j) & 1u, abort_flag, a.err_word)) {
-                    aborted = true;
-                    break;
-                }
-                ptx::tc_fence_after_sync();
-                add(kColAcc, 0, stage(j) + C::kTileBytes, j == 0, nullptr);
-                if (more) {                         // S^T_{j+1} overwrites P^T_j, which dV has read
-                    if (!ready(j + 1)) {
-                        aborted = true;
-                        break;
-                    }
-                    issue(0, dk, stage(j + 1), s_full);
-                }
-                if (!ptx::mbar_wait_warp(ds_full, uint32_t(j) & 1u, abort_flag, a.err_word)) {
-                    aborted = true;
-                    break;
-                }
-                ptx::tc_fence_after_sync();
-                add(kColAcc + D, kColDP, stage(j), j == 0, &kv_empty[j % C::kStages]);
-                if (more)
-                    issue(kColDP, dvk, stage(j + 1) + C::kTileBytes, dp_full);
+            issue(0, dk, q_addr, s_full);
+            if (!do_ready(0)) {
+                aborted = true;
+                break;
             }
+            issue(kColDP, dvk, do_addr, dp_full);
+            int j = 0;
+            for (; j < n_q; ++j) {
+                const bool more = j + 1 < n_q;
+                if (!ptx::mbar_wait_warp(p_full, uint32_t(j) & 1u, abort_flag, a.err_word))
+                    break;
+                ptx::tc_fence_after_sync();
+                add(kColAcc, 0, do_addr + do_tile(j), j == 0, &do_empty[j % C::kDO]);
+                if (more) {                         // S^T_{j+1} overwrites P^T_j, which dV has read
+                    if (!q_ready(j + 1))
+                        break;
+                    issue(0, dk, q_addr + q_tile(j + 1), s_full);
+                }
+                if (!ptx::mbar_wait_warp(ds_full, uint32_t(j) & 1u, abort_flag, a.err_word))
+                    break;
+                ptx::tc_fence_after_sync();
+                add(kColAcc + D, kColDP, q_addr + q_tile(j), j == 0, &q_empty[j % C::kQ]);
+                if (more) {
+                    if (!do_ready(j + 1))
+                        break;
+                    issue(kColDP, dvk, do_addr + do_tile(j + 1), dp_full);
+                }
+            }
+            aborted = j < n_q;
         } while (false);
         if (ptx::elect_one()) {
             if (!aborted)
@@ -918,15 +940,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int q0 = i * BT + col0;            // this thread's first query
             if (++i == s1)
                 i = s0;
-            // the statistics arrive with the step's ring stage
-            const int st = j % C::kStages;
-            if (!row_wait(&kv_full[st], uint32_t(j / C::kStages) & 1u, abort_flag, a.err_word) ||
+            if (!row_wait(&st_full[j & 1], uint32_t(j >> 1) & 1u, abort_flag, a.err_word) ||
                 !row_wait(s_full, par, abort_flag, a.err_word)) {
                 aborted = true;
                 break;
             }
             ptx::tc_fence_after_sync();
-            const float *stat = stats + st * (2 * BT) + col0;
+            const float *stat = stats + (j & 1) * (2 * BT) + col0;
             uint32_t sv[32], pk[16];
             ptx::tmem_ld32(tS, sv);
             ptx::tmem_wait_ld();

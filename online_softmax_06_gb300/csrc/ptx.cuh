@@ -144,6 +144,32 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity,
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err_word)) != 0;
 }
 
+// Polls without suspending the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// mbar_wait for one thread of many that wait for the same barrier: it polls, where a
+// suspended thread (mbarrier.try_wait) among sixteen waiting warps was seen to go on up to
+// 1000 cycles after the phase had completed.  The same bounds and error reporting.
+static __device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity,
+                                                 volatile int *abort, int *err_word)
+{
+    for (int k = 0; k < 256; ++k)
+        if (mbar_test_wait(bar, parity))
+            return true;
+    return mbar_wait_slow(bar, parity, abort, err_word);
+}
+
 // One lane of a converged warp (elect.sync over the full mask): the lane that
 // issues a warp's tcgen05.mma / commit instructions.  Running the issuing loop
 // on the whole warp keeps its operands warp-uniform.
