@@ -20,6 +20,9 @@
 // over the upper half of S: probabilities relative to a reference that at most 2^8
 // below the row's maximum, each off by 2^-9 relative, and the sum that divides O
 // is corrected by the error of the tile's largest.
+// Where the items (two tiles of a kv head) are few, a cluster of 2 to 8 CTAs takes one, a
+// range of its steps each; the rows' unnormalised O, maxima and sums meet through
+// distributed shared memory, where each CTA joins a share of the rows.
 // Rows of V behind a sequence's keys (the room of a cache, the next sequence) are
 // zeroed in shared memory before the product reads them: their P is 0, but they may
 // hold NaN.  Every wait is bounded; a timed-out one leaves the CTA's rows unwritten.
@@ -71,9 +74,26 @@ struct Params {
     CUtensorMap tm_k32, tm_v32;        // box {64, 1, 1, 32}: the tile where the sinks end
     WindowArgs a;
     int G, P;                          // heads of a kv head; queries of a tile
-    int n_pairs;
+    int n_pairs, split;
     float scale_log2;
 };
+
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x),
+                 "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
 
 __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
 {
@@ -86,7 +106,7 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
     }
 }
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_constant__ Params p)
 {
     using C = Cfg<D>;
@@ -105,12 +125,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
 
     // ---- work item: the last pairs of a sequence first (early ones see less) ------
     const WindowArgs &a = p.a;
-    const int pair = p.n_pairs - 1 - int(blockIdx.x % unsigned(p.n_pairs));
-    const int bh = int(blockIdx.x / unsigned(p.n_pairs));
+    const int n_split = SPLIT ? p.split : 1;
+    const int part = SPLIT ? int(blockIdx.x % unsigned(n_split)) : 0;
+    const int item = SPLIT ? int(blockIdx.x / unsigned(n_split)) : int(blockIdx.x);
+    const int pair = p.n_pairs - 1 - int(item % unsigned(p.n_pairs));
+    const int bh = int(item / unsigned(p.n_pairs));
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     WindowSeq sq;
     if (!window_seq(a, b, sq)) {
-        if (threadIdx.x == 0 && pair == 0 && hk == 0)
+        if (threadIdx.x == 0 && pair == 0 && hk == 0 && part == 0)
             record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
         return;
     }
@@ -123,11 +146,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
     const WindowKeys w = window_keys(a.window, a.sinks, i0, i2, off, kPad);
     // tile t takes steps [first_t, last_t) of the places' tiles: Q0 those that its
     // own last query reaches, Q1 all but leading ones that are behind its window
-    const int n_steps = (w.places + BN - 1) / BN;
+    const int all_steps = (w.places + BN - 1) / BN;
     const int reach0 = w.places - (i2 - i1);
-    const int last0 = reach0 > w.sp ? (reach0 + BN - 1) / BN : 0;
-    const int first1 = a.sinks == 0 && w.lo > 0 ? p.P / BN : 0;
-    const int last1 = has_q1 ? n_steps : 0;
+    // this CTA's steps are [step0, step1)
+    const int step0 = SPLIT ? int(int64_t(all_steps) * part / n_split) : 0;
+    const int step1 = SPLIT ? int(int64_t(all_steps) * (part + 1) / n_split) : all_steps;
+    const int first0 = step0;
+    const int last0 = min(reach0 > w.sp ? (reach0 + BN - 1) / BN : 0, step1);
+    const int first1 = max(a.sinks == 0 && w.lo > 0 ? p.P / BN : 0, step0);
+    const int last1 = has_q1 ? step1 : 0;
+    const int n_steps = step1 - step0;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -176,11 +204,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
                     ptx::tma_load_4d(smem + t * C::kTileBytes + c * kChunkBytes, &p.tm_q,
                                      &q_full[t], c * 64, 0, hk, int(sq.q0 + (t ? i1 : i0)));
             };
-            if (last0 > 0)
+            if (last0 > first0)
                 load_q(0);
             int stage = 0;
             uint32_t phase = 0;
-            for (int j = 0; j < n_steps && !aborted; ++j) {
+            for (int j = step0; j < step1 && !aborted; ++j) {
                 for (int kv = 0; kv < 2; ++kv) {
                     if (!ptx::mbar_wait(&kv_empty[stage], phase ^ 1u, abort_flag, a.err_word)) {
                         aborted = true;
@@ -209,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (j == 0 && kv == 0 && last1 > 0)
+                    if (j == step0 && kv == 0 && last1 > first1)
                         load_q(1);
                 }
             }
@@ -294,8 +322,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
             !__all_sync(0xffffffffu, ptx::mbar_wait_limited(never, 0, abort_flag, a.err_word,
                                                             a.expire_wait_ns)))
             aborted = true;
-        const int first[2] = {0, first1}, last[2] = {last0, last1};
-        auto has = [&](int t, int j) { return j >= first[t] && j < last[t]; };
+        auto has = [&](int t, int j) {
+            return t ? j >= first1 && j < last1 : j >= first0 && j < last0;
+        };
         bool q_ready[2] = {false, false};
         auto wait_q = [&](int t) -> bool {
             if (!q_ready[t])
@@ -309,31 +338,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
             int k_st = next_stage();
             if (k_st < 0)
                 break;
-            if ((has(0, 0) && !wait_q(0)))
+            if (has(0, step0) && !wait_q(0))
                 break;
             ptx::tc_fence_after_sync();
-            if (has(0, 0))
+            if (has(0, step0))
                 issue_qk(0, k_st);
-            if (has(1, 0)) {
+            if (has(1, step0)) {
                 if (!wait_q(1))
                     break;
                 ptx::tc_fence_after_sync();
                 issue_qk(1, k_st);
             }
             release(k_st);
-            int j = 0;
-            for (; j < n_steps; ++j) {
+            int j = step0;
+            for (; j < step1; ++j) {
                 const int v_st = next_stage();
                 if (v_st < 0)
                     break;
                 clear_tail(j, v_st);
                 if (has(0, j)) {
-                    if (!ptx::mbar_wait_warp(&p_full[0], uint32_t(j) & 1u, abort_flag, a.err_word))
+                    if (!ptx::mbar_wait_warp(&p_full[0], uint32_t(j - first0) & 1u, abort_flag,
+                                             a.err_word))
                         break;
                     ptx::tc_fence_after_sync();
-                    issue_pv(0, v_st, j > 0, j == last0 - 1);
+                    issue_pv(0, v_st, j > first0, j == last0 - 1);
                 }
-                const bool more = j + 1 < n_steps;
+                const bool more = j + 1 < step1;
                 if (more) {
                     if ((k_st = next_stage()) < 0)
                         break;
@@ -359,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
                     release(k_st);
                 }
             }
-            aborted = j < n_steps;
+            aborted = j < step1;
         } while (false);
         // every product issued above is through once this commit arrives
         if (ptx::elect_one()) {
@@ -371,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
         // ======================= softmax warpgroups ========================
         const int t = warp >> 2;
         const int r = threadIdx.x & 127;               // row of the tile = TMEM lane
-        const int j0 = t ? first1 : 0, j1 = t ? last1 : last0;
+        const int j0 = t ? first1 : first0, j1 = t ? last1 : last0;
         const int qi = r / p.G, i = (t ? i1 : i0) + qi;   // query, head of the kv head
         const int h = hk * p.G + r % p.G;
         const bool row_ok = qi < p.P && i < (t ? i2 : i1);
@@ -471,8 +501,105 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
         }
 
         // ---- epilogue ------------------------------------------------------------
+        if constexpr (SPLIT) {
+            // this CTA's part of its row; every CTA of the cluster is through with its ring
+            bool ok = !aborted && (j1 <= j0 || ptx::mbar_wait(&o_full[t], 0, abort_flag, a.err_word));
+            ptx::tc_fence_after_sync();
+            cluster_sync();
+            // Rows [owner * per, + per) are joined by CTA `owner`: it gets (m, l, l_o) and O
+            // of each from every CTA.  A part's O lies by units of four values, the rows of
+            // a unit one behind the other, so that a warp's stores fill whole lines (rows
+            // one behind the other took twice as long).
+            const int per = 2 * BM / n_split;
+            constexpr uint32_t kOffParts = 2 * BM * 16;
+            static_assert(kOffParts + 2 * BM * D * 4 <= C::kOffBar, "shared memory");
+            {
+                const int row = t * BM + r;
+                const uint32_t to = cluster_addr(ptx::smem_u32(smem), uint32_t(row / per));
+                const uint32_t at = to + kOffParts +
+                                    uint32_t(part * per * (D / 4) + row % per) * 16;
+                st_cluster4(to + uint32_t(part * per + row % per) * 16,
+                            make_float4(m, l, l_o, ok ? 0.f : 1.f));
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (j1 > j0) {
+                        ptx::tmem_ld32(tO + c * 32, o);
+                        ptx::tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            o[q] = 0u;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        st_cluster4(at + uint32_t((c * 8 + q) * per) * 16,
+                                    make_float4(__uint_as_float(o[4 * q]),
+                                                __uint_as_float(o[4 * q + 1]),
+                                                __uint_as_float(o[4 * q + 2]),
+                                                __uint_as_float(o[4 * q + 3])));
+                }
+            }
+            cluster_sync();
+            // eight rows and four units a warp at once: whole 32-byte sectors of O
+            const float4 *st = reinterpret_cast<const float4 *>(smem);
+            const int groups = per / 8;                    // of rows: 16, 8 or 4
+            const int share = groups < 8 ? 8 / groups : 1; // warps of a group
+            for (int rg = warp % (8 / share); rg < groups; rg += 8) {
+                const int jr = rg * 8 + (lane & 7);
+                const int gt = (part * per + jr) / BM, gr = (part * per + jr) % BM;
+                const int gq = gr / p.G, gi = (gt ? i1 : i0) + gq, gh = hk * p.G + gr % p.G;
+                float M = -INFINITY, bad = 0.f, sum = 0.f, sum_o = 0.f;
+                float f[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < n_split) {
+                        const float4 x = st[k * per + jr];
+                        M = fmaxf(M, x.x);
+                        bad += x.w;
+                    }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    f[k] = 0.f;
+                    if (k < n_split) {
+                        const float4 x = st[k * per + jr];
+                        f[k] = x.x == -INFINITY ? 1.f : ptx::ex2(x.x - M);   // (zeros, or NaN)
+                        sum = fmaf(f[k], x.y, sum);
+                        sum_o = fmaf(f[k], x.z, sum_o);
+                    }
+                }
+                // (bad: a CTA's wait ran out)
+                if (gq >= p.P || gi >= (gt ? i2 : i1) || bad != 0.f)
+                    continue;
+                const float inv = 1.f / sum_o;
+                __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(a.O) +
+                                      ((sq.q0 + gi) * a.H + gh) * D;
+                const float4 *parts = reinterpret_cast<const float4 *>(smem + kOffParts) + jr;
+                for (int u = warp / (8 / share) * 4 + (lane >> 3); u < D / 4; u += 4 * share) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < n_split) {
+                            const float4 y = parts[(k * (D / 4) + u) * per];
+                            v.x = fmaf(f[k], y.x, v.x);
+                            v.y = fmaf(f[k], y.y, v.y);
+                            v.z = fmaf(f[k], y.z, v.z);
+                            v.w = fmaf(f[k], y.w, v.w);
+                        }
+                    *reinterpret_cast<uint2 *>(orow + u * 4) =
+                        sum == 0.f ? make_uint2(0, 0)
+                                   : make_uint2(ptx::pack_bf16x2(v.x * inv, v.y * inv),
+                                                ptx::pack_bf16x2(v.z * inv, v.w * inv));
+                    if (u == 0)
+                        a.lse[a.cu_seqlens_q != nullptr
+                                  ? int64_t(gh) * a.total_q + sq.q0 + gi
+                                  : (int64_t(b) * a.H + gh) * a.Nq + gi] =
+                            sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+                }
+            }
+        }
         const int rows_t = t ? i2 - i1 : i1 - i0;      // queries of the tile
-        if (rows_t > 0) {
+        if (!SPLIT && rows_t > 0) {
             const bool full_tile = rows_t == p.P;
             const bool work = j1 > j0;                 // else O was never formed: zeros
             const bool ok = !aborted &&
@@ -536,6 +663,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
         }
     }
 
+    if (SPLIT && warp >= kWarpLoad) {              // the rows' warps wait twice above
+        cluster_sync();
+        cluster_sync();
+    }
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
@@ -543,16 +674,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
         ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D>
+template <int D, bool SPLIT>
 int launch_d(const Params &p, int64_t blocks, cudaStream_t stream)
 {
-    auto kern = attn_window_kernel<D>;
+    auto kern = attn_window_kernel<D, SPLIT>;
     static PerDeviceOnce once;
     constexpr int smem = int(Cfg<D>::kSmemBytes);
     if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(kern), smem))
         return FA_ERR_CUDA;
-    return launch_early(kern, dim3(unsigned(blocks)), kThreads, smem, stream, p) == cudaSuccess
-               ? FA_OK : FA_ERR_CUDA;
+    const cudaError_t e =
+        SPLIT ? launch_early_clusters(kern, dim3(unsigned(blocks)), kThreads, smem, p.split, stream, p)
+              : launch_early(kern, dim3(unsigned(blocks)), kThreads, smem, stream, p);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// CTAs of an item.  They run one an SM, so what counts is waves of the SMs that clusters
+// find (of 152; eight neighbours are not free everywhere), a step of an item taking some
+// 1.5 us, its start and end 3.5, a join 8.5 more.  1 x 512 queries on a window of 4096, 64
+// items: 56 us with one, 38 with two, 51 with four; 1 x 64, 8 items: 56, 37, 25, 19 with eight.
+int choose_split(const WindowArgs &a, int P)
+{
+    const int64_t pairs = (a.total_q + 2 * P - 1) / (2 * P), most = (a.Nq + 2 * P - 1) / (2 * P);
+    // packed sequences may all be short: at least the pairs that the rows need
+    const int64_t items = (a.cu_seqlens_q != nullptr ? pairs : most * a.B) * a.Hkv;
+    int64_t keys = int64_t(a.window) + a.sinks + 2 * P;
+    keys = keys < a.Nk ? keys : a.Nk;
+    const int64_t steps = (keys + BN - 1) / BN;
+    int best = 1;
+    double least = 0;
+    for (int s = 1; s <= 8; s *= 2) {
+        const int64_t sms = s <= 2 ? 152 : s == 4 ? 144 : 112;
+        const double t = double((items * s + sms - 1) / sms) *
+                         (1.5 * double((steps + s - 1) / s) + 3.5 + (s > 1 ? 8.5 : 0.));
+        if (s == 1 || t < least) {
+            best = s;
+            least = t;
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -564,8 +723,9 @@ int launch_attention_window(const WindowArgs &a, cudaStream_t stream)
     p.G = a.H / a.Hkv;
     p.P = BM / p.G;
     p.n_pairs = (a.Nq + 2 * p.P - 1) / (2 * p.P);
+    p.split = choose_split(a, p.P);
     p.scale_log2 = float(double(a.scale) * 1.4426950408889634);
-    const int64_t blocks = int64_t(p.n_pairs) * a.B * a.Hkv;
+    const int64_t blocks = int64_t(p.n_pairs) * a.B * a.Hkv * p.split;
     if (blocks > 0x7fffffffLL)
         return FA_ERR_TOO_LARGE;
     if (!make_tmap_heads(&p.tm_q, a.Q, a.total_q, a.Hkv, p.G, a.d, a.q_stride, p.P) ||
@@ -575,7 +735,11 @@ int launch_attention_window(const WindowArgs &a, cudaStream_t stream)
         !make_tmap_heads(&p.tm_k32, a.K, a.total_k, a.Hkv, 1, a.d, a.k_stride, kPad) ||
         !make_tmap_heads(&p.tm_v32, a.V, a.total_k, a.Hkv, 1, a.d, a.v_stride, kPad))
         return FA_ERR_CUDA;
-    return a.d == 64 ? launch_d<64>(p, blocks, stream) : launch_d<128>(p, blocks, stream);
+    if (p.split > 1)
+        return a.d == 64 ? launch_d<64, true>(p, blocks, stream)
+                         : launch_d<128, true>(p, blocks, stream);
+    return a.d == 64 ? launch_d<64, false>(p, blocks, stream)
+                     : launch_d<128, false>(p, blocks, stream);
 }
 
 }  // namespace fa

@@ -456,21 +456,11 @@ int launch_d(const Params &p, int64_t blocks, cudaStream_t stream)
     });
     if (once_c.err[dev] != cudaSuccess)
         return FA_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(blocks));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(p.split);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.split > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p), after = cudaGetLastError();
-    return e == cudaSuccess && after == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    const cudaError_t e =
+        p.split > 1
+            ? launch_early_clusters(kern, dim3(unsigned(blocks)), kThreads, smem, p.split, stream, p)
+            : launch_early(kern, dim3(unsigned(blocks)), kThreads, smem, stream, p);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace

@@ -187,6 +187,28 @@ cudaError_t launch_early(K kernel, dim3 grid, int threads, int smem, cudaStream_
     return e == cudaSuccess ? last : e;
 }
 
+// The same in clusters of `size` CTAs.
+template <typename K, typename... Args>
+cudaError_t launch_early_clusters(K kernel, dim3 grid, int threads, int smem, int size,
+                                  cudaStream_t stream, const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(size);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...), last = cudaGetLastError();
+    return e == cudaSuccess ? last : e;
+}
+
 // Writing to and reading from the 4-bit paged cache (layouts as in fa.h).
 struct Kv4CacheArgs {
     void *K, *V;               // read by the appending kernel, written by the reading one
