@@ -16,8 +16,9 @@
 //   * a row's mask is two ranges of columns, formed as bits 32 columns at a time.
 // Roles, tensor memory and the order of the products are those of attn_bf16.cu: a
 // CTA per SM; warps 0-3 and 4-7 the softmax of Q0 and Q1, a thread per row; warp 8
-// TMA, warp 9 tcgen05.  S0 [0, 128), S1 [128, 256), O0 and O1 from 256; P in bf16
-// over the upper half of S: probabilities relative to a reference that at most 2^8
+// TMA, warp 9 tcgen05.  S0 [0, 128), S1 [128, 256), O0 and O1 from 256 (with a narrow
+// window one tile a CTA, two CTAs an SM: S0, then O0 from 128); P in bf16 over the upper
+// half of S: probabilities relative to a reference that at most 2^8
 // below the row's maximum, each off by 2^-9 relative, and the sum that divides O
 // is corrected by the error of the tile's largest.
 // Where the items (two tiles of a kv head) are few, a cluster of 2 to 8 CTAs takes one, a
@@ -44,28 +45,27 @@ namespace {
 
 constexpr int BM = 128, BN = 128;
 constexpr int kPad = 32;               // sinks fill whole pieces of a tile
-constexpr int kThreads = 320;
-constexpr int kWarpLoad = 8, kWarpMma = 9;
-constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColPinS = 64;
 constexpr uint32_t kChunkBytes = BM * 128;   // 128 rows of 64 bf16
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleLog2 = 8.f;
 
 __device__ __forceinline__ uint32_t col_s(int t) { return uint32_t(t) * 128u; }
-template <int D>
-__device__ __forceinline__ uint32_t col_o(int t) { return 256u + uint32_t(t) * D; }
 
-template <int D>
+// TILES query tiles a CTA: two, one CTA an SM; or one, two CTAs an SM.
+template <int D, int TILES>
 struct Cfg {
+    static constexpr int kThreads = 128 * TILES + 64;
+    static constexpr int kWarpLoad = 4 * TILES, kWarpMma = kWarpLoad + 1;
+    static constexpr uint32_t kTmemCols = 256 * TILES, kColO = 128 * TILES;
     static constexpr int kChunks = D / 64;
     static constexpr uint32_t kTileBytes = BM * D * 2;
-    static constexpr int kStages = D == 128 ? 4 : 8;
-    static constexpr uint32_t kOffRing = 2 * kTileBytes;       // [Q0][Q1][ring][barriers]
+    static constexpr int kStages = (D == 128 ? 2 : 4) * TILES;
+    static constexpr uint32_t kOffRing = TILES * kTileBytes;   // [Q0][Q1][ring][barriers]
     static constexpr uint32_t kOffBar = kOffRing + kStages * kTileBytes;
     static constexpr uint32_t kBars = 2 + 2 * kStages + 2 + 2 + 2 + 1 + 1;
     static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16 + 1024;
-    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+    static_assert(kSmemBytes <= (TILES == 2 ? 227 : 113) * 1024, "shared memory");
 };
 
 struct Params {
@@ -106,10 +106,12 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
     }
 }
 
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_constant__ Params p)
+template <int D, bool SPLIT, int TILES>
+__global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
+    attn_window_kernel(const __grid_constant__ Params p)
 {
-    using C = Cfg<D>;
+    using C = Cfg<D, TILES>;
+    static_assert(!SPLIT || TILES == 2, "a join has two tiles' threads");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -120,6 +122,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
+    if (threadIdx.x == 0) {
+        ptx::prefetch_tmap(&p.tm_q);
+        ptx::prefetch_tmap(&p.tm_k);
+        ptx::prefetch_tmap(&p.tm_v);
+        ptx::prefetch_tmap(&p.tm_k32);
+        ptx::prefetch_tmap(&p.tm_v32);
+        ptx::prefetch_tmap(&p.tm_o);
+    }
     // nothing that a kernel before may still be writing is read ahead of this
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -137,12 +147,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
             record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
         return;
     }
-    const int i0 = pair * 2 * p.P;             // first query of the pair
+    const int i0 = pair * TILES * p.P;         // first query of the pair
     if (i0 >= sq.n)
         return;
     const int off = sq.L - sq.n;
-    const bool has_q1 = i0 + p.P < sq.n;
-    const int i1 = min(i0 + p.P, sq.n), i2 = min(i0 + 2 * p.P, sq.n);
+    const bool has_q1 = TILES == 2 && i0 + p.P < sq.n;
+    const int i1 = min(i0 + p.P, sq.n), i2 = min(i0 + TILES * p.P, sq.n);
     const WindowKeys w = window_keys(a.window, a.sinks, i0, i2, off, kPad);
     // tile t takes steps [first_t, last_t) of the places' tiles: Q0 those that its
     // own last query reaches, Q1 all but leading ones that are behind its window
@@ -159,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < TILES; ++t) {
             ptx::mbar_init(&q_full[t], 1);
             ptx::mbar_init(&s_full[t], 1);
             ptx::mbar_init(&p_full[t], 128);
@@ -174,14 +184,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
         *abort_flag = 0;
         ptx::fence_barrier_init();
     }
-    if (warp == kWarpMma) {
-        ptx::tmem_alloc(tmem_slot, kTmemCols);
+    if (warp == C::kWarpMma) {
+        ptx::tmem_alloc(tmem_slot, C::kTmemCols);
         ptx::tmem_relinquish();
-    }
-    if (warp == kWarpLoad && lane == 0) {
-        ptx::prefetch_tmap(&p.tm_q);
-        ptx::prefetch_tmap(&p.tm_k);
-        ptx::prefetch_tmap(&p.tm_v);
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
@@ -190,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
     bool aborted = false;
     uint8_t *ring = smem + C::kOffRing;
 
-    if (warp == kWarpLoad) {
+    if (warp == C::kWarpLoad) {
         // ======================= TMA producer ==============================
         if (lane == 0) {
             int last_phase[C::kStages];
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
             }
         }
         __syncwarp();
-    } else if (warp == kWarpMma) {
+    } else if (warp == C::kWarpMma) {
         // ======================= MMA issuer (whole warp) =====================
         constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(BM, BN, false);
         constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(BM, D, true);
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
             if (ptx::elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
-                    ptx::mma_ts(tmem + col_o<D>(t), tmem + col_s(t) + kColPinS + kk * 8,
+                    ptx::mma_ts(tmem + C::kColO + uint32_t(t) * D, tmem + col_s(t) + kColPinS + kk * 8,
                                 dv + uint64_t((kk * 16 * 128) >> 4), idesc_pv,
                                 (accumulate || kk > 0) ? 1u : 0u);
                 if (last)
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
                                                             a.expire_wait_ns)))
             aborted = true;
         auto has = [&](int t, int j) {
-            return t ? j >= first1 && j < last1 : j >= first0 && j < last0;
+            return t ? TILES == 2 && j >= first1 && j < last1 : j >= first0 && j < last0;
         };
         bool q_ready[2] = {false, false};
         auto wait_q = [&](int t) -> bool {
@@ -399,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
         __syncwarp();
     } else {
         // ======================= softmax warpgroups ========================
-        const int t = warp >> 2;
+        const int t = TILES == 1 ? 0 : warp >> 2;
         const int r = threadIdx.x & 127;               // row of the tile = TMEM lane
         const int j0 = t ? first1 : first0, j1 = t ? last1 : last0;
         const int qi = r / p.G, i = (t ? i1 : i0) + qi;   // query, head of the kv head
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
         const bool row_ok = qi < p.P && i < (t ? i2 : i1);
         const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_bits + col_s(t);
-        const uint32_t tO = tmem + lane_bits + col_o<D>(t);
+        const uint32_t tO = tmem + lane_bits + C::kColO + uint32_t(t) * D;
         const int vhi = row_ok ? i + off - w.lo + w.sp : -1;
         const int64_t vl = int64_t(vhi) - a.window + 1;
         const int vlo = vl > w.sp ? int(vl) : w.sp;
@@ -663,23 +668,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const __grid_c
         }
     }
 
-    if (SPLIT && warp >= kWarpLoad) {              // the rows' warps wait twice above
+    if (SPLIT && warp >= C::kWarpLoad) {              // the rows' warps wait twice above
         cluster_sync();
         cluster_sync();
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
-    if (warp == kWarpMma)
-        ptx::tmem_dealloc(tmem, kTmemCols);
+    if (warp == C::kWarpMma)
+        ptx::tmem_dealloc(tmem, C::kTmemCols);
 }
 
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, int TILES>
 int launch_d(const Params &p, int64_t blocks, cudaStream_t stream)
 {
-    auto kern = attn_window_kernel<D, SPLIT>;
+    auto kern = attn_window_kernel<D, SPLIT, TILES>;
     static PerDeviceOnce once;
-    constexpr int smem = int(Cfg<D>::kSmemBytes);
+    constexpr int smem = int(Cfg<D, TILES>::kSmemBytes), kThreads = Cfg<D, TILES>::kThreads;
     if (!set_max_dynamic_smem(once, reinterpret_cast<const void *>(kern), smem))
         return FA_ERR_CUDA;
     const cudaError_t e =
@@ -714,6 +719,16 @@ int choose_split(const WindowArgs &a, int P)
     return best;
 }
 
+// Tiles of a CTA.  With a narrow window a CTA has few steps, and its start and end (loads
+// without a product, the way of O) weigh more than that two tiles share K and V: one tile
+// then, two CTAs an SM (2 x 4096 tokens, d = 64, 16 heads: window 64 26 us against 34, 256
+// 39 against 46, 512 49 against 54, 1024 65 and 66, 4096 113 against 109; d = 128, 32 heads
+// on 8: 64 51 against 64, 256 75 and 76, 512 95 and 95, 1024 133 against 128).
+int choose_tiles(const WindowArgs &a)
+{
+    return a.window <= (a.d == 64 ? 512 : 256) ? 1 : 2;
+}
+
 }  // namespace
 
 int launch_attention_window(const WindowArgs &a, cudaStream_t stream)
@@ -722,8 +737,9 @@ int launch_attention_window(const WindowArgs &a, cudaStream_t stream)
     p.a = a;
     p.G = a.H / a.Hkv;
     p.P = BM / p.G;
-    p.n_pairs = (a.Nq + 2 * p.P - 1) / (2 * p.P);
     p.split = choose_split(a, p.P);
+    const int tiles = p.split > 1 ? 2 : choose_tiles(a);
+    p.n_pairs = (a.Nq + tiles * p.P - 1) / (tiles * p.P);
     p.scale_log2 = float(double(a.scale) * 1.4426950408889634);
     const int64_t blocks = int64_t(p.n_pairs) * a.B * a.Hkv * p.split;
     if (blocks > 0x7fffffffLL)
@@ -736,10 +752,13 @@ int launch_attention_window(const WindowArgs &a, cudaStream_t stream)
         !make_tmap_heads(&p.tm_v32, a.V, a.total_k, a.Hkv, 1, a.d, a.v_stride, kPad))
         return FA_ERR_CUDA;
     if (p.split > 1)
-        return a.d == 64 ? launch_d<64, true>(p, blocks, stream)
-                         : launch_d<128, true>(p, blocks, stream);
-    return a.d == 64 ? launch_d<64, false>(p, blocks, stream)
-                     : launch_d<128, false>(p, blocks, stream);
+        return a.d == 64 ? launch_d<64, true, 2>(p, blocks, stream)
+                         : launch_d<128, true, 2>(p, blocks, stream);
+    if (tiles == 1)
+        return a.d == 64 ? launch_d<64, false, 1>(p, blocks, stream)
+                         : launch_d<128, false, 1>(p, blocks, stream);
+    return a.d == 64 ? launch_d<64, false, 2>(p, blocks, stream)
+                     : launch_d<128, false, 2>(p, blocks, stream);
 }
 
 }  // namespace fa

@@ -198,6 +198,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
+    if (threadIdx.x == 0) {
+        ptx::prefetch_tmap(&p.tm_q);
+        ptx::prefetch_tmap(&p.tm_do);
+        ptx::prefetch_tmap(&p.tm_k);
+        ptx::prefetch_tmap(&p.tm_v);
+        ptx::prefetch_tmap(&p.tm_k32);
+        ptx::prefetch_tmap(&p.tm_v32);
+    }
     // nothing that a kernel before may still be writing is read ahead of this
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -240,12 +248,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     if (warp == kWarpMma) {
         ptx::tmem_alloc(tmem_slot, kTmemCols);
         ptx::tmem_relinquish();
-    }
-    if (warp == kWarpLoad && lane == 0) {
-        ptx::prefetch_tmap(&p.tm_q);
-        ptx::prefetch_tmap(&p.tm_do);
-        ptx::prefetch_tmap(&p.tm_k);
-        ptx::prefetch_tmap(&p.tm_v);
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
@@ -673,6 +675,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
+    if (threadIdx.x == 0) {
+        ptx::prefetch_tmap(&p.tm_k);
+        ptx::prefetch_tmap(&p.tm_v);
+        ptx::prefetch_tmap(&p.tm_q);
+        ptx::prefetch_tmap(&p.tm_do);
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // work item: the far pieces of the sinks' tiles first, then every key tile's window
@@ -735,12 +743,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpMma) {
         ptx::tmem_alloc(tmem_slot, kTmemCols);
         ptx::tmem_relinquish();
-    }
-    if (warp == kWarpLoad && lane == 0) {
-        ptx::prefetch_tmap(&p.tm_q);
-        ptx::prefetch_tmap(&p.tm_do);
-        ptx::prefetch_tmap(&p.tm_k);
-        ptx::prefetch_tmap(&p.tm_v);
     }
     ptx::tc_fence_before_sync();
     __syncthreads();

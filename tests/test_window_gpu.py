@@ -70,6 +70,14 @@ def test_cache_long(nq, sinks, window):
     run([nq] * 3, [3000, 2999, 2901], 8, 2, 128, "cache", window, sinks)
 
 
+@pytest.mark.parametrize("H,Hkv,d", [(2, 2, 64), (6, 2, 128), (7, 1, 64), (16, 2, 128)])
+@pytest.mark.parametrize("window,sinks", [(3000, 4), (2 ** 30, 0), (2500, 200)])
+def test_few_items_long_windows(H, Hkv, d, window, sinks):
+    """Items so few that clusters share their steps: whole and cut tiles, queries without a key."""
+    run([200, 200, 200], [4000, 100, 0], H, Hkv, d, "cache", window, sinks)
+    run([90, 1, 0, 257], [3900, 3001, 50, 257], H, Hkv, d, "packed", window, sinks)
+
+
 @pytest.mark.parametrize("nq", [1, 200])
 def test_large_scores_and_scales(nq):
     """A scale that makes single keys dominate; one that makes all keys alike."""
@@ -170,18 +178,20 @@ def test_replayed_graph_and_other_stream(nq):
     device_error_clear()
 
 
-def test_timed_out_wait():
-    """A wait that runs out leaves the rows unwritten, flags it, and the next call is right."""
-    batch = Batch([300], [300], 4, 2, 128, "dense")
+@pytest.mark.parametrize("n,L,window", [(300, 300, 100), (300, 300, 280), (200, 4000, 3900)])
+def test_timed_out_wait(n, L, window):
+    """A wait that runs out (one tile a CTA, two, a cluster's) leaves the rows unwritten, flags it, and
+    the next call is right."""
+    batch = Batch([n], [L], 4, 2, 128, "dense")
     o = torch.full(batch.gq.shape, 7.0, dtype=torch.bfloat16, device="cuda")
-    lse = torch.full((1, 4, 300), 7.0, device="cuda")
+    lse = torch.full((1, 4, n), 7.0, device="cuda")
     fa.fa_debug_expire_next_wait(1_000_000)
-    fa.attention_window_fwd(batch.gq, batch.gk, batch.gv, 100, 4, out=o, lse=lse)
+    fa.attention_window_fwd(batch.gq, batch.gk, batch.gv, window, 4, out=o, lse=lse)
     assert fa.fa_get_device_error() == fa.FA_DEVERR_WAIT_TIMEOUT
     assert (o == 7).all() and (lse == 7).all()
-    o, lse = fa.attention_window_fwd(batch.gq, batch.gk, batch.gv, 100, 4)
+    o, lse = fa.attention_window_fwd(batch.gq, batch.gk, batch.gv, window, 4)
     device_error_clear()
-    check_forward(batch, o, lse, 100, 4)
+    check_forward(batch, o, lse, window, 4)
 
 
 def test_tensor_refusals():
