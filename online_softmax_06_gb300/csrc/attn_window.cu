@@ -69,11 +69,12 @@ struct Cfg {
 };
 
 struct Params {
-    CUtensorMap tm_q, tm_o;            // box {64, G, 1, P}
-    CUtensorMap tm_k, tm_v;            // box {64, 1, 1, 128}
-    CUtensorMap tm_k32, tm_v32;        // box {64, 1, 1, 32}: the tile where the sinks end
+    CUtensorMap tm_q, tm_o;            // P rows of G heads, q_chunks chunks a copy
+    CUtensorMap tm_k, tm_v;            // 128 rows of a head
+    CUtensorMap tm_k32, tm_v32;        // 32 rows, a chunk a copy: the tile where the sinks end
     WindowArgs a;
-    int G, P;                          // heads of a kv head; queries of a tile
+    int G, P, q_chunks;                // heads of a kv head; queries of a tile
+    uint32_t div_g;                    // r / G = r * div_g >> 16 for r < 128
     int n_pairs, split;
     float scale_log2;
 };
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 32) {
         ptx::prefetch_tmap(&p.tm_q);
         ptx::prefetch_tmap(&p.tm_k);
         ptx::prefetch_tmap(&p.tm_v);
@@ -196,65 +197,79 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
     uint8_t *ring = smem + C::kOffRing;
 
     if (warp == C::kWarpLoad) {
-        // ======================= TMA producer ==============================
-        if (lane == 0) {
-            int last_phase[C::kStages];
-            for (int s = 0; s < C::kStages; ++s)
-                last_phase[s] = -1;
-            bool q_issued[2] = {false, false};
-            auto load_q = [&](int t) {
-                q_issued[t] = true;
+        // ======================= TMA producer (whole warp) ===================
+        int last_phase[C::kStages];
+        for (int s = 0; s < C::kStages; ++s)
+            last_phase[s] = -1;
+        bool q_issued[2] = {false, false};
+        auto load_q = [&](int t) {
+            q_issued[t] = true;
+            if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(&q_full[t], C::kChunks * p.P * p.G * 128);
-                for (int c = 0; c < C::kChunks; ++c)
-                    ptx::tma_load_4d(smem + t * C::kTileBytes + c * kChunkBytes, &p.tm_q,
-                                     &q_full[t], c * 64, 0, hk, int(sq.q0 + (t ? i1 : i0)));
-            };
-            if (last0 > first0)
-                load_q(0);
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int j = step0; j < step1 && !aborted; ++j) {
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (!ptx::mbar_wait(&kv_empty[stage], phase ^ 1u, abort_flag, a.err_word)) {
-                        aborted = true;
-                        break;
-                    }
-                    ptx::mbar_arrive_expect_tx(&kv_full[stage], C::kTileBytes);
-                    uint8_t *dst = ring + stage * C::kTileBytes;
-                    const int v0 = j * BN;
-                    if (v0 < w.sp && v0 + BN > w.sp) {
-                        for (int q = 0; q < BN / kPad; ++q) {
-                            const int v = v0 + q * kPad;
-                            const int64_t row = sq.k0 + (v < w.sp ? v : w.lo + v - w.sp);
-                            for (int c = 0; c < C::kChunks; ++c)
-                                ptx::tma_load_4d(dst + c * kChunkBytes + q * kPad * 128,
-                                                 kv ? &p.tm_v32 : &p.tm_k32, &kv_full[stage],
-                                                 c * 64, 0, hk, int(row));
-                        }
-                    } else {
-                        const int64_t row = sq.k0 + (v0 < w.sp ? v0 : w.lo + v0 - w.sp);
-                        for (int c = 0; c < C::kChunks; ++c)
-                            ptx::tma_load_4d(dst + c * kChunkBytes, kv ? &p.tm_v : &p.tm_k,
-                                             &kv_full[stage], c * 64, 0, hk, int(row));
-                    }
-                    last_phase[stage] = int(phase);
-                    if (++stage == C::kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                    if (j == step0 && kv == 0 && last1 > first1)
-                        load_q(1);
+                for (int c = 0; c < C::kChunks; c += p.q_chunks)
+                    ptx::tma_load_5d(smem + t * C::kTileBytes + c * kChunkBytes, &p.tm_q,
+                                     &q_full[t], 0, 0, int(sq.q0 + (t ? i1 : i0)), c, hk);
+            }
+            __syncwarp();
+        };
+        // the next CTA's queries into L2
+        auto prefetch_next = [&]() {
+            const int64_t ni = int64_t(item) + kWindowSms * (TILES == 2 ? 1 : 2);
+            const int nbh = int(ni / p.n_pairs);
+            WindowSeq ns;
+            if (SPLIT || lane >= TILES || nbh >= a.B * a.Hkv || !window_seq(a, nbh / a.Hkv, ns))
+                return;
+            const int ni0 = ((p.n_pairs - 1 - int(ni % p.n_pairs)) * TILES + lane) * p.P;
+            if (ni0 < ns.n)
+                for (int c = 0; c < C::kChunks; c += p.q_chunks)
+                    ptx::tma_prefetch_5d(&p.tm_q, 0, 0, int(ns.q0 + ni0), c, nbh % a.Hkv);
+        };
+        if (last0 > first0)
+            load_q(0);
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int j = step0; j < step1 && !aborted; ++j) {
+            for (int kv = 0; kv < 2; ++kv) {
+                if (!ptx::mbar_wait_warp(&kv_empty[stage], phase ^ 1u, abort_flag, a.err_word)) {
+                    aborted = true;
+                    break;
                 }
+                if (lane == 0)
+                    ptx::mbar_arrive_expect_tx(&kv_full[stage], C::kTileBytes);
+                __syncwarp();
+                uint8_t *dst = ring + stage * C::kTileBytes;
+                const int v0 = j * BN;
+                if (v0 < w.sp && v0 + BN > w.sp) {
+                    // pieces of 32 rows, a lane each
+                    const int c = lane / (BN / kPad), q = lane % (BN / kPad), v = v0 + q * kPad;
+                    if (c < C::kChunks)
+                        ptx::tma_load_5d(dst + c * kChunkBytes + q * kPad * 128,
+                                         kv ? &p.tm_v32 : &p.tm_k32, &kv_full[stage], 0, 0,
+                                         int(sq.k0 + (v < w.sp ? v : w.lo + v - w.sp)), c, hk);
+                } else if (lane == 0) {
+                    ptx::tma_load_5d(dst, kv ? &p.tm_v : &p.tm_k, &kv_full[stage], 0, 0,
+                                     int(sq.k0 + (v0 < w.sp ? v0 : w.lo + v0 - w.sp)), 0, hk);
+                }
+                __syncwarp();
+                last_phase[stage] = int(phase);
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                if (j == step0 && kv == 0 && last1 > first1)
+                    load_q(1);
+                if (j == step0 && kv == 1)
+                    prefetch_next();
             }
-            if (aborted || *abort_flag) {
-                // copies already issued land before the CTA goes away
-                for (int t = 0; t < 2; ++t)
-                    if (q_issued[t])
-                        drain_wait(&q_full[t], 0);
-                for (int s = 0; s < C::kStages; ++s)
-                    if (last_phase[s] >= 0)
-                        drain_wait(&kv_full[s], uint32_t(last_phase[s]));
-            }
+        }
+        if (lane == 0 && (aborted || *abort_flag)) {
+            // copies already issued land before the CTA goes away
+            for (int t = 0; t < TILES; ++t)
+                if (q_issued[t])
+                    drain_wait(&q_full[t], 0);
+            for (int s = 0; s < C::kStages; ++s)
+                if (last_phase[s] >= 0)
+                    drain_wait(&kv_full[s], uint32_t(last_phase[s]));
         }
         __syncwarp();
     } else if (warp == C::kWarpMma) {
@@ -407,8 +422,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
         const int t = TILES == 1 ? 0 : warp >> 2;
         const int r = threadIdx.x & 127;               // row of the tile = TMEM lane
         const int j0 = t ? first1 : first0, j1 = t ? last1 : last0;
-        const int qi = r / p.G, i = (t ? i1 : i0) + qi;   // query, head of the kv head
-        const int h = hk * p.G + r % p.G;
+        const int qi = int(r * p.div_g >> 16), i = (t ? i1 : i0) + qi;
+        const int h = hk * p.G + r - qi * p.G;            // query, head
         const bool row_ok = qi < p.P && i < (t ? i2 : i1);
         const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_bits + col_s(t);
@@ -553,7 +568,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
             for (int rg = warp % (8 / share); rg < groups; rg += 8) {
                 const int jr = rg * 8 + (lane & 7);
                 const int gt = (part * per + jr) / BM, gr = (part * per + jr) % BM;
-                const int gq = gr / p.G, gi = (gt ? i1 : i0) + gq, gh = hk * p.G + gr % p.G;
+                const int gq = int(gr * p.div_g >> 16), gi = (gt ? i1 : i0) + gq;
+                const int gh = hk * p.G + gr - gq * p.G;
                 float M = -INFINITY, bad = 0.f, sum = 0.f, sum_o = 0.f;
                 float f[8];
 #pragma unroll
@@ -659,9 +675,9 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
                 ptx::fence_proxy_async_smem();
                 // the store goes out only if all 128 threads are through
                 if (!ptx::bar_red_or(1 + t, 128, !ok) && r == 0) {
-                    for (int c = 0; c < C::kChunks; ++c)
-                        ptx::tma_store_4d(&p.tm_o, o_stage + c * kChunkBytes, c * 64, 0, hk,
-                                          int(sq.q0 + (t ? i1 : i0)));
+                    for (int c = 0; c < C::kChunks; c += p.q_chunks)
+                        ptx::tma_store_5d(&p.tm_o, o_stage + c * kChunkBytes, 0, 0,
+                                          int(sq.q0 + (t ? i1 : i0)), c, hk);
                     ptx::bulk_commit_and_wait_read();
                 }
             }
@@ -737,6 +753,8 @@ int launch_attention_window(const WindowArgs &a, cudaStream_t stream)
     p.a = a;
     p.G = a.H / a.Hkv;
     p.P = BM / p.G;
+    p.q_chunks = tmap_heads_chunks(p.G, a.d, p.P);
+    p.div_g = uint32_t(65536 / p.G + 1);
     p.split = choose_split(a, p.P);
     const int tiles = p.split > 1 ? 2 : choose_tiles(a);
     p.n_pairs = (a.Nq + tiles * p.P - 1) / (tiles * p.P);

@@ -52,14 +52,18 @@ constexpr uint32_t kChunkBytes = BT * 128;     // 128 rows of 64 bf16
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
-    CUtensorMap tm_q, tm_do;           // dQ: box {64, G, 1, P}; dK/dV: {64, 1, 1, 64}
-    CUtensorMap tm_k, tm_v;            // box {64, 1, 1, 128}
-    CUtensorMap tm_k32, tm_v32;        // dQ: box {64, 1, 1, 32}
+    CUtensorMap tm_o;                  // dQ: as tm_q
+    CUtensorMap tm_q, tm_do;           // dQ: P rows of G heads, q_chunks chunks a copy; dK/dV:
+                                       // 128 rows of a head
+    CUtensorMap tm_k, tm_v;            // 128 rows of a head
+    CUtensorMap tm_k32, tm_v32;        // dQ: 32 rows, a chunk a copy
     WindowArgs a;                      // O read; queries and keys are the same tokens
     float *D;                          // as lse
     __nv_bfloat16 *dQ, *dK, *dV;
     int64_t dq_stride, dk_stride, dv_stride;
     float *parts;                      // [B Hkv][sink tiles][slots][dV, dK][128][d]
+    int q_chunks;
+    uint32_t div_g;                    // r / G = r * div_g >> 16 for r < 128
     int G, P, n_tiles;                 // n_tiles: row tiles (dQ), key tiles (dK/dV) of Nq
     int sink_tiles, slots, piece;      // piece: 128-query tiles of a far piece
     float scale_log2;
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 32) {
         ptx::prefetch_tmap(&p.tm_q);
         ptx::prefetch_tmap(&p.tm_do);
         ptx::prefetch_tmap(&p.tm_k);
@@ -226,6 +230,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     const WindowKeys w = window_keys(a.window, a.sinks, i0, i1, 0, kPad);
     const int n_kv = (w.places + BT - 1) / BT;      // at least one
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // O for D: a row warp takes 8 rows, D / 8 lanes each; on its way during the set-up
+    constexpr int kLanesPerRow = D / 8, kRowsPerInst = 32 / kLanesPerRow;
+    constexpr int kRowsPerWarp = BT / kRowWarps;
+    const int sub = lane / kLanesPerRow, lr = lane % kLanesPerRow;
+    uint4 ov[kRowsPerWarp / kRowsPerInst];
+    if (warp < kRowWarps)
+#pragma unroll
+        for (int k = 0; k < kRowsPerWarp / kRowsPerInst; ++k) {
+            const int rr = warp * kRowsPerWarp + k * kRowsPerInst + sub;
+            const int qr = int(rr * p.div_g >> 16), hr = hk * p.G + rr - qr * p.G;
+            ov[k] = make_uint4(0, 0, 0, 0);
+            if (qr < p.P && i0 + qr < i1)
+                ov[k] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.O) +
+                                                         ((sq.q0 + i0 + qr) * a.H + hr) * D + lr * 8);
+        }
 
     if (threadIdx.x == 0) {
         ptx::mbar_init(a_full, 1);
@@ -288,13 +308,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         };
         if (lane == 0) {
             ptx::mbar_arrive_expect_tx(a_full, 2 * C::kChunks * p.P * p.G * 128);
-            for (int c = 0; c < C::kChunks; ++c) {
-                ptx::tma_load_4d(tile_q + c * kChunkBytes, &p.tm_q, a_full, c * 64, 0, hk,
-                                 int(sq.q0 + i0));
-                ptx::tma_load_4d(tile_do + c * kChunkBytes, &p.tm_do, a_full, c * 64, 0, hk,
-                                 int(sq.q0 + i0));
+            for (int c = 0; c < C::kChunks; c += p.q_chunks) {
+                ptx::tma_load_5d(tile_q + c * kChunkBytes, &p.tm_q, a_full, 0, 0, int(sq.q0 + i0),
+                                 c, hk);
+                ptx::tma_load_5d(tile_do + c * kChunkBytes, &p.tm_do, a_full, 0, 0,
+                                 int(sq.q0 + i0), c, hk);
             }
         }
+        // the next CTA's rows into L2: a map a lane
+        auto prefetch_next = [&]() {
+            const int64_t ni = int64_t(blockIdx.x) + kWindowSms;
+            const int nbh = int(ni / p.n_tiles);
+            WindowSeq ns;
+            if (nbh >= a.B * a.Hkv || !window_seq(a, nbh / a.Hkv, ns))
+                return;
+            const int ni0 = (p.n_tiles - 1 - int(ni % p.n_tiles)) * p.P;
+            if (ni0 < ns.L && lane < 3)
+                for (int c = 0; c < C::kChunks; c += p.q_chunks)
+                    ptx::tma_prefetch_5d(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_do : &p.tm_o, 0, 0,
+                                         int(ns.q0 + ni0), c, nbh % a.Hkv);
+        };
         int issued = 0;
         for (int j = 0; j < n_kv; ++j) {
             const int stage = j % C::kStages;
@@ -303,33 +336,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                                      abort_flag, a.err_word) ||
                 (j == 2 && !ptx::mbar_wait_warp(res_free, 0, abort_flag, a.err_word)))
                 break;
-            if (lane == 0) {
-                uint8_t *dst = smem + C::stage_off(stage);
-                const int v0 = j * BT;
+            if (lane == 0)
                 ptx::mbar_arrive_expect_tx(&kv_full[stage], C::kStageBytes);
-                if (v0 < w.sp && v0 + BT > w.sp) {
-                    for (int q = 0; q < BT / kPad; ++q) {
-                        const int v = v0 + q * kPad;
-                        const int row = int(sq.k0 + (v < w.sp ? v : w.lo + v - w.sp));
-                        for (int c = 0; c < C::kChunks; ++c) {
-                            uint8_t *to = dst + c * kChunkBytes + q * kPad * 128;
-                            ptx::tma_load_4d(to, &p.tm_k32, &kv_full[stage], c * 64, 0, hk, row);
-                            ptx::tma_load_4d(to + C::kTileBytes, &p.tm_v32, &kv_full[stage],
-                                             c * 64, 0, hk, row);
-                        }
-                    }
-                } else {
-                    const int row = int(sq.k0 + (v0 < w.sp ? v0 : w.lo + v0 - w.sp));
-                    for (int c = 0; c < C::kChunks; ++c) {
-                        ptx::tma_load_4d(dst + c * kChunkBytes, &p.tm_k, &kv_full[stage], c * 64,
-                                         0, hk, row);
-                        ptx::tma_load_4d(dst + C::kTileBytes + c * kChunkBytes, &p.tm_v,
-                                         &kv_full[stage], c * 64, 0, hk, row);
-                    }
-                }
+            __syncwarp();
+            uint8_t *dst = smem + C::stage_off(stage);
+            const int v0 = j * BT;
+            if (v0 < w.sp && v0 + BT > w.sp) {
+                // pieces of 32 rows, a lane each
+                const int of = lane >> 4, c = lane / (BT / kPad) & 3, q = lane % (BT / kPad);
+                const int v = v0 + q * kPad;
+                if (c < C::kChunks)
+                    ptx::tma_load_5d(dst + of * C::kTileBytes + c * kChunkBytes + q * kPad * 128,
+                                     of ? &p.tm_v32 : &p.tm_k32, &kv_full[stage], 0, 0,
+                                     int(sq.k0 + (v < w.sp ? v : w.lo + v - w.sp)), c, hk);
+            } else if (lane < 2) {
+                ptx::tma_load_5d(dst + lane * C::kTileBytes, lane ? &p.tm_v : &p.tm_k,
+                                 &kv_full[stage], 0, 0,
+                                 int(sq.k0 + (v0 < w.sp ? v0 : w.lo + v0 - w.sp)), 0, hk);
             }
             __syncwarp();
             issued = j + 1;
+            if (j == 1 || n_kv == 1)
+                prefetch_next();
             if (j >= 2)
                 sum_keys(j - 2);
         }
@@ -454,29 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         // ======================= query rows ================================
         const int r = (warp & 3) * 32 + lane;        // row of the tile = TMEM lane
         const int g = warp >> 2, col0 = 32 * g;      // of the row's four threads; its columns
-        const int qi = r / p.G, i = i0 + qi;         // query, head of the kv head
-        const int h = hk * p.G + r % p.G;
+        const int qi = int(r * p.div_g >> 16), i = i0 + qi;   // query, head
+        const int h = hk * p.G + r - qi * p.G;
         const bool row_ok = qi < p.P && i < i1;
         const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
         const int64_t stat = row_ok ? stat_row(a, b, h, sq.q0) + i : 0;
-        // D_i = dO_i . O_i: a warp takes 8 rows, D / 8 lanes each; O from global memory,
-        // dO from the resident tile (128-byte swizzle)
-        constexpr int kLanesPerRow = D / 8, kRowsPerInst = 32 / kLanesPerRow;
-        constexpr int kRowsPerWarp = BT / kRowWarps;
+        // D_i = dO_i . O_i, dO from the resident tile (128-byte swizzle)
         float *xch = reinterpret_cast<float *>(smem + C::kOffXch);
         {
-            const int sub = lane / kLanesPerRow, lr = lane % kLanesPerRow;
-            uint4 ov[kRowsPerWarp / kRowsPerInst];
-#pragma unroll
-            for (int k = 0; k < kRowsPerWarp / kRowsPerInst; ++k) {
-                const int rr = warp * kRowsPerWarp + k * kRowsPerInst + sub;
-                const int qr = rr / p.G, hr = hk * p.G + rr % p.G;
-                ov[k] = qr < p.P && i0 + qr < i1
-                            ? *reinterpret_cast<const uint4 *>(
-                                  static_cast<const __nv_bfloat16 *>(a.O) +
-                                  ((sq.q0 + i0 + qr) * a.H + hr) * D + lr * 8)
-                            : make_uint4(0, 0, 0, 0);
-            }
             const bool a_ok = row_wait(a_full, 0, abort_flag, a.err_word);
             if (a_ok) {
                 // this thread's quarter of its row of Q and of dO into tensor memory
@@ -675,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 32) {
         ptx::prefetch_tmap(&p.tm_k);
         ptx::prefetch_tmap(&p.tm_v);
         ptx::prefetch_tmap(&p.tm_q);
@@ -758,13 +771,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         // and the queries' statistics (dK_{j-2}: the rows are done with step j - 2).
         if (lane == 0) {
             ptx::mbar_arrive_expect_tx(a_full, 2 * C::kTileBytes);
-            for (int c = 0; c < C::kChunks; ++c) {
-                ptx::tma_load_4d(tile_k + c * kChunkBytes, &p.tm_k, a_full, c * 64, 0, hk,
-                                 int(sq.k0 + int64_t(kt) * BT));
-                ptx::tma_load_4d(tile_v + c * kChunkBytes, &p.tm_v, a_full, c * 64, 0, hk,
-                                 int(sq.k0 + int64_t(kt) * BT));
-            }
+            ptx::tma_load_5d(tile_k, &p.tm_k, a_full, 0, 0, int(sq.k0 + int64_t(kt) * BT), 0, hk);
+            ptx::tma_load_5d(tile_v, &p.tm_v, a_full, 0, 0, int(sq.k0 + int64_t(kt) * BT), 0, hk);
         }
+        // the next CTA's first tiles into L2: a map a lane
+        auto prefetch_next = [&]() {
+            const int64_t ni = int64_t(blockIdx.x) + kWindowSms - int64_t(far_items) * bh_count;
+            const int nbh = int(ni / p.n_tiles), nkt = int(ni % p.n_tiles);
+            WindowSeq ns;
+            if (ni < 0 || nbh >= bh_count || !window_seq(a, nbh / a.Hkv, ns))
+                return;
+            const int nh = nbh % a.Hkv;
+            if (nkt * BT < ns.L && lane < 4)
+                ptx::tma_prefetch_5d(lane == 0   ? &p.tm_k
+                                     : lane == 1 ? &p.tm_v
+                                     : lane == 2 ? &p.tm_q
+                                                 : &p.tm_do,
+                                     0, 0, int(ns.k0 + nkt * BT), 0, lane < 2 ? nh : nh * p.G);
+        };
         int q_issued = 0, do_issued = 0;
         int h = hk * p.G, i = s0;
         for (int j = 0; j < n_q; ++j) {
@@ -773,8 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto load = [&](uint8_t *dst, const CUtensorMap *tm, uint64_t *full) {
                 if (lane == 0) {
                     ptx::mbar_arrive_expect_tx(full, C::kTileBytes);
-                    for (int c = 0; c < C::kChunks; ++c)
-                        ptx::tma_load_4d(dst + c * kChunkBytes, tm, full, c * 64, 0, h, row);
+                    ptx::tma_load_5d(dst, tm, full, 0, 0, row, 0, h);
                 }
                 __syncwarp();
             };
@@ -807,6 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st[BT + u * 32 + lane] = -ds[u];
             }
             ptx::mbar_arrive(&st_full[os]);          // all lanes, after their writes
+            if (j == 1 || n_q == 1)
+                prefetch_next();
             if (++i == s1) {
                 i = s0;
                 ++h;
@@ -1120,6 +1145,8 @@ int launch_attention_window_bwd(const WindowBwdArgs &w, cudaStream_t stream)
     pq.dv_stride = w.dv_stride;
     pq.G = a.H / a.Hkv;
     pq.P = BT / pq.G;
+    pq.q_chunks = tmap_heads_chunks(pq.G, a.d, pq.P);
+    pq.div_g = uint32_t(65536 / pq.G + 1);
     pq.n_tiles = (a.Nq + pq.P - 1) / pq.P;
     pq.sink_tiles = lay.sink_tiles;
     pq.slots = lay.slots;
@@ -1136,6 +1163,7 @@ int launch_attention_window_bwd(const WindowBwdArgs &w, cudaStream_t stream)
     const int64_t row = int64_t(a.H) * a.d;
     if (!make_tmap_heads(&pq.tm_q, a.Q, a.total_q, a.Hkv, pq.G, a.d, a.q_stride, pq.P) ||
         !make_tmap_heads(&pq.tm_do, w.dO, a.total_q, a.Hkv, pq.G, a.d, row, pq.P) ||
+        !make_tmap_heads(&pq.tm_o, a.O, a.total_q, a.Hkv, pq.G, a.d, row, pq.P) ||
         !make_tmap_heads(&pq.tm_k, a.K, a.total_k, a.Hkv, 1, a.d, a.k_stride, BT) ||
         !make_tmap_heads(&pq.tm_v, a.V, a.total_k, a.Hkv, 1, a.d, a.v_stride, BT) ||
         !make_tmap_heads(&pq.tm_k32, a.K, a.total_k, a.Hkv, 1, a.d, a.k_stride, kPad) ||

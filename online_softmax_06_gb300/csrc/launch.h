@@ -83,9 +83,15 @@ int choose_num_splits(int B, int H, int N, int Nk);
 bool make_tmap_bf16(CUtensorMap *tm, const void *base, int64_t total, int H, int d,
                     int box_rows = 128, int H_row = 0);
 
-// 4-D TMA map over rows of heads * group * d bf16 values, `stride` elements apart:
-// box = 64 values (the 128-byte swizzle span) x the `group` heads of one of `heads`
-// groups x box_rows rows.  Rows past `rows` read as zero and are not stored.
+// 5-D TMA map (64 values, group, rows, 64-value chunks, heads) over rows of heads * group
+// * d bf16 values, `stride` elements apart: box = 64 values (the 128-byte swizzle span) x
+// the `group` heads of one of `heads` groups x box_rows rows x all chunks where these fill
+// 128 rows each (one copy a tile then, its chunks 16 KB apart), else one chunk.  Rows past
+// `rows` read as zero and are not stored.
+inline int tmap_heads_chunks(int group, int d, int box_rows)
+{
+    return group * box_rows == 128 ? d / 64 : 1;
+}
 bool make_tmap_heads(CUtensorMap *tm, const void *base, int64_t rows, int heads, int group, int d,
                      int64_t stride, int box_rows);
 

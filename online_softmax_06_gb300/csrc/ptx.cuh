@@ -230,12 +230,31 @@ __device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *t
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_5d(void *smem_dst, const CUtensorMap *tmap,
+                                            uint64_t *bar, int x, int y, int z, int w, int v)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
 // Brings a tensor-map box into L2 ahead of its TMA load (no completion).
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *tmap, int x, int y, int z)
 {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
                      reinterpret_cast<uint64_t>(tmap)),
                  "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_5d(const CUtensorMap *tmap, int x, int y, int z,
+                                                int w, int v)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
                  : "memory");
 }
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *tmap)
@@ -291,6 +310,15 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap *tmap, const void
         "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::
             "l"(reinterpret_cast<uint64_t>(tmap)),
         "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_5d(const CUtensorMap *tmap, const void *smem_src, int x,
+                                             int y, int z, int w, int v)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5, %6}], [%1];" ::"l"(
+            reinterpret_cast<uint64_t>(tmap)),
+        "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
         : "memory");
 }
 __device__ __forceinline__ void bulk_commit_and_wait_read()

@@ -60,13 +60,14 @@ bool make_tmap_heads(CUtensorMap *tm, const void *base, int64_t rows, int heads,
     EncodeTiledFn fn = encode_fn();
     if (fn == nullptr)
         return false;
-    const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(group), cuuint64_t(heads),
-                                cuuint64_t(rows)};
-    const cuuint64_t strides[3] = {cuuint64_t(d) * 2, cuuint64_t(group) * d * 2,
-                                   cuuint64_t(stride) * 2};
-    const cuuint32_t box[4] = {64, cuuint32_t(group), 1, cuuint32_t(box_rows)};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides,
+    const cuuint64_t dims[5] = {64, cuuint64_t(group), cuuint64_t(rows), cuuint64_t(d / 64),
+                                cuuint64_t(heads)};
+    const cuuint64_t strides[4] = {cuuint64_t(d) * 2, cuuint64_t(stride) * 2, 128,
+                                   cuuint64_t(group) * d * 2};
+    const cuuint32_t box[5] = {64, cuuint32_t(group), cuuint32_t(box_rows),
+                               cuuint32_t(tmap_heads_chunks(group, d, box_rows)), 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides,
               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

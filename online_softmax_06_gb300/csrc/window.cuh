@@ -74,6 +74,11 @@ __device__ __forceinline__ WindowKeys window_keys(int window, int sinks, int i0,
     return w;
 }
 
+// CTAs that run at once, one an SM: the CTA this far behind in the grid is about the next
+// on this one's SM, and its first tiles, which nobody reads before it, are brought into L2
+// meanwhile (from DRAM its first product waited some 3 us for them).
+constexpr int kWindowSms = 152;
+
 // The lowest `n` bits, n clamped to 0 .. 32.
 __device__ __forceinline__ uint32_t low_bits(int n)
 {
