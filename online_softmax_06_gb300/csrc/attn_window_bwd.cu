@@ -53,6 +53,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
     CUtensorMap tm_o;                  // dQ: as tm_q
+    CUtensorMap tm_d0, tm_d1;          // outputs: dQ as tm_q; or dV and dK as tm_k
     CUtensorMap tm_q, tm_do;           // dQ: P rows of G heads, q_chunks chunks a copy; dK/dV:
                                        // 128 rows of a head
     CUtensorMap tm_k, tm_v;            // 128 rows of a head
@@ -110,10 +111,11 @@ __device__ __forceinline__ uint64_t kmajor_off(int kk, uint32_t chunk_bytes)
     return uint64_t(((kk >> 2) * chunk_bytes + (kk & 3) * 32) >> 4);
 }
 
-// Columns [32 c0, 32 c1) of this thread's row of an accumulator, plus `more` times the
-// values at `add` where given, times `mul`, as bf16.
-__device__ __forceinline__ void store_row(uint32_t t_acc, float mul, __nv_bfloat16 *dst, bool ok,
-                                          int c0, int c1, float more = 0.f,
+// Columns [32 c0, 32 c1) of this thread's row r of an accumulator, plus `more` times the
+// values at `add` where given, times `mul`, as bf16: to `dst` (the row's first value; null:
+// nowhere), or into a tile in shared memory laid out as a copy's (128-byte swizzle).
+__device__ __forceinline__ void store_row(uint32_t t_acc, float mul, __nv_bfloat16 *dst,
+                                          uint8_t *tile, int r, int c0, int c1, float more = 0.f,
                                           const float *add = nullptr)
 {
 #pragma unroll 1
@@ -125,16 +127,20 @@ __device__ __forceinline__ void store_row(uint32_t t_acc, float mul, __nv_bfloat
 #pragma unroll
             for (int e = 0; e < 32; ++e)
                 o[e] = __float_as_uint(fmaf(more, add[c * 32 + e], __uint_as_float(o[e])));
-        if (ok) {
-            uint4 *out = reinterpret_cast<uint4 *>(dst + c * 32);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t u[4];
+        for (int q = 0; q < 4; ++q) {
+            uint32_t u[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    u[e] = ptx::pack_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * mul,
-                                            __uint_as_float(o[8 * q + 2 * e + 1]) * mul);
-                out[q] = make_uint4(u[0], u[1], u[2], u[3]);
+            for (int e = 0; e < 4; ++e)
+                u[e] = ptx::pack_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * mul,
+                                        __uint_as_float(o[8 * q + 2 * e + 1]) * mul);
+            const uint4 v = make_uint4(u[0], u[1], u[2], u[3]);
+            if (tile != nullptr) {
+                const int un = (c & 1) * 4 + q;
+                *reinterpret_cast<uint4 *>(tile + (c >> 1) * kChunkBytes + r * 128 +
+                                           ((un ^ (r & 7)) << 4)) = v;
+            } else if (dst != nullptr) {
+                *reinterpret_cast<uint4 *>(dst + c * 32 + q * 8) = v;
             }
         }
     }
@@ -247,23 +253,64 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                                                          ((sq.q0 + i0 + qr) * a.H + hr) * D + lr * 8);
         }
 
-    if (threadIdx.x == 0) {
-        ptx::mbar_init(a_full, 1);
-        for (int st = 0; st < C::kStages; ++st) {
-            ptx::mbar_init(&kv_full[st], 1);
-            ptx::mbar_init(&kv_empty[st], 1);
+    const int row_r = (warp & 3) * 32 + lane, row_q = int(row_r * p.div_g >> 16);
+    const bool row_ok = warp < kRowWarps && row_q < p.P && i0 + row_q < i1;
+    const int row_h = hk * p.G + row_r - row_q * p.G;         // the row's head
+    const int64_t stat = row_ok ? stat_row(a, b, row_h, sq.q0) + i0 + row_q : 0;
+    const float lse2 = row_ok ? a.lse[stat] * kLog2e : 0.f;
+
+    uint8_t *tile_q = smem, *tile_do = smem + C::kTileBytes;
+    // the copies of step j into its ring stage, by the load warp
+    auto issue_step = [&](int j) {
+        const int stage = j % C::kStages;
+        if (lane == 0)
+            ptx::mbar_arrive_expect_tx(&kv_full[stage], C::kStageBytes);
+        __syncwarp();
+        uint8_t *dst = smem + C::stage_off(stage);
+        const int v0 = j * BT;
+        if (v0 < w.sp && v0 + BT > w.sp) {
+            // pieces of 32 rows, a lane each
+            const int of = lane >> 4, c = lane / (BT / kPad) & 3, q = lane % (BT / kPad);
+            const int v = v0 + q * kPad;
+            if (c < C::kChunks)
+                ptx::tma_load_5d(dst + of * C::kTileBytes + c * kChunkBytes + q * kPad * 128,
+                                 of ? &p.tm_v32 : &p.tm_k32, &kv_full[stage], 0, 0,
+                                 int(sq.k0 + (v < w.sp ? v : w.lo + v - w.sp)), c, hk);
+        } else if (lane < 2) {
+            ptx::tma_load_5d(dst + lane * C::kTileBytes, lane ? &p.tm_v : &p.tm_k, &kv_full[stage],
+                             0, 0, int(sq.k0 + (v0 < w.sp ? v0 : w.lo + v0 - w.sp)), 0, hk);
         }
-        ptx::mbar_init(s_full, 1);
-        ptx::mbar_init(dp_full, 1);
-        ptx::mbar_init(s_free, kRowWarps);
-        ptx::mbar_init(p_full, kRowWarps);
-        ptx::mbar_init(o_full, 1);
-        ptx::mbar_init(drain, 1);
-        ptx::mbar_init(a_tm, kRowWarps);
-        ptx::mbar_init(res_free, kRowWarps);
-        ptx::mbar_init(never, 1);
-        *abort_flag = 0;
-        ptx::fence_barrier_init();
+        __syncwarp();
+    };
+    if (warp == kWarpLoad) {
+        // the barriers, and the first copies while the others set up
+        if (lane == 0) {
+            ptx::mbar_init(a_full, 1);
+            for (int st = 0; st < C::kStages; ++st) {
+                ptx::mbar_init(&kv_full[st], 1);
+                ptx::mbar_init(&kv_empty[st], 1);
+            }
+            ptx::mbar_init(s_full, 1);
+            ptx::mbar_init(dp_full, 1);
+            ptx::mbar_init(s_free, kRowWarps);
+            ptx::mbar_init(p_full, kRowWarps);
+            ptx::mbar_init(o_full, 1);
+            ptx::mbar_init(drain, 1);
+            ptx::mbar_init(a_tm, kRowWarps);
+            ptx::mbar_init(res_free, kRowWarps);
+            ptx::mbar_init(never, 1);
+            *abort_flag = 0;
+            ptx::fence_barrier_init();
+            ptx::mbar_arrive_expect_tx(a_full, 2 * C::kChunks * p.P * p.G * 128);
+            for (int c = 0; c < C::kChunks; c += p.q_chunks) {
+                ptx::tma_load_5d(tile_q + c * kChunkBytes, &p.tm_q, a_full, 0, 0, int(sq.q0 + i0),
+                                 c, hk);
+                ptx::tma_load_5d(tile_do + c * kChunkBytes, &p.tm_do, a_full, 0, 0,
+                                 int(sq.q0 + i0), c, hk);
+            }
+        }
+        __syncwarp();
+        issue_step(0);
     }
     if (warp == kWarpMma) {
         ptx::tmem_alloc(tmem_slot, kTmemCols);
@@ -274,7 +321,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     ptx::tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     bool aborted = false;
-    uint8_t *tile_q = smem, *tile_do = smem + C::kTileBytes;
 
     if (warp == kWarpLoad) {
         // ======================= TMA producer, keys' mean =====================
@@ -306,15 +352,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             }
             __syncwarp();
         };
-        if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(a_full, 2 * C::kChunks * p.P * p.G * 128);
-            for (int c = 0; c < C::kChunks; c += p.q_chunks) {
-                ptx::tma_load_5d(tile_q + c * kChunkBytes, &p.tm_q, a_full, 0, 0, int(sq.q0 + i0),
-                                 c, hk);
-                ptx::tma_load_5d(tile_do + c * kChunkBytes, &p.tm_do, a_full, 0, 0,
-                                 int(sq.q0 + i0), c, hk);
-            }
-        }
         // the next CTA's rows into L2: a map a lane
         auto prefetch_next = [&]() {
             const int64_t ni = int64_t(blockIdx.x) + kWindowSms;
@@ -328,34 +365,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                     ptx::tma_prefetch_5d(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_do : &p.tm_o, 0, 0,
                                          int(ns.q0 + ni0), c, nbh % a.Hkv);
         };
-        int issued = 0;
+        int issued = 1;
         for (int j = 0; j < n_kv; ++j) {
-            const int stage = j % C::kStages;
-            // stage 2 is the Q / dO region: free once the rows are done with it
-            if (!ptx::mbar_wait_warp(&kv_empty[stage], (uint32_t(j / C::kStages) & 1u) ^ 1u,
-                                     abort_flag, a.err_word) ||
-                (j == 2 && !ptx::mbar_wait_warp(res_free, 0, abort_flag, a.err_word)))
-                break;
-            if (lane == 0)
-                ptx::mbar_arrive_expect_tx(&kv_full[stage], C::kStageBytes);
-            __syncwarp();
-            uint8_t *dst = smem + C::stage_off(stage);
-            const int v0 = j * BT;
-            if (v0 < w.sp && v0 + BT > w.sp) {
-                // pieces of 32 rows, a lane each
-                const int of = lane >> 4, c = lane / (BT / kPad) & 3, q = lane % (BT / kPad);
-                const int v = v0 + q * kPad;
-                if (c < C::kChunks)
-                    ptx::tma_load_5d(dst + of * C::kTileBytes + c * kChunkBytes + q * kPad * 128,
-                                     of ? &p.tm_v32 : &p.tm_k32, &kv_full[stage], 0, 0,
-                                     int(sq.k0 + (v < w.sp ? v : w.lo + v - w.sp)), c, hk);
-            } else if (lane < 2) {
-                ptx::tma_load_5d(dst + lane * C::kTileBytes, lane ? &p.tm_v : &p.tm_k,
-                                 &kv_full[stage], 0, 0,
-                                 int(sq.k0 + (v0 < w.sp ? v0 : w.lo + v0 - w.sp)), 0, hk);
+            if (j > 0) {
+                const int stage = j % C::kStages;
+                // stage 2 is the Q / dO region: free once the rows are done with it
+                if (!ptx::mbar_wait_warp(&kv_empty[stage], (uint32_t(j / C::kStages) & 1u) ^ 1u,
+                                         abort_flag, a.err_word) ||
+                    (j == 2 && !ptx::mbar_wait_warp(res_free, 0, abort_flag, a.err_word)))
+                    break;
+                issue_step(j);
+                issued = j + 1;
             }
-            __syncwarp();
-            issued = j + 1;
             if (j == 1 || n_kv == 1)
                 prefetch_next();
             if (j >= 2)
@@ -480,13 +501,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         __syncwarp();
     } else {
         // ======================= query rows ================================
-        const int r = (warp & 3) * 32 + lane;        // row of the tile = TMEM lane
+        const int r = row_r;                         // row of the tile = TMEM lane
         const int g = warp >> 2, col0 = 32 * g;      // of the row's four threads; its columns
-        const int qi = int(r * p.div_g >> 16), i = i0 + qi;   // query, head
-        const int h = hk * p.G + r - qi * p.G;
-        const bool row_ok = qi < p.P && i < i1;
+        const int i = i0 + row_q;
         const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
-        const int64_t stat = row_ok ? stat_row(a, b, h, sq.q0) + i : 0;
         // D_i = dO_i . O_i, dO from the resident tile (128-byte swizzle)
         float *xch = reinterpret_cast<float *>(smem + C::kOffXch);
         {
@@ -549,7 +567,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             if (a_ok && lane == 0)
                 ptx::mbar_arrive(res_free);
         }
-        const float lse2 = row_ok ? a.lse[stat] * kLog2e : 0.f;
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");   // the row threads
         const float Di = xch[r];
         if (g == 0 && row_ok)
@@ -624,12 +641,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         asm volatile("bar.sync 2, %0;" ::"n"(32 * kRowWarps + 32) : "memory");
         const float ri = (xch[r] + xch[BT + r]) + (xch[2 * BT + r] + xch[3 * BT + r]);
         const float *mean = reinterpret_cast<const float *>(smem + C::kOffMean);
-        // 32 columns of each row's dQ a thread
-        if (g < D / 32 && !aborted && ptx::mbar_wait(o_full, 0, abort_flag, a.err_word)) {
+        // 32 columns of each row's dQ a thread: a whole tile by way of the ring (all products
+        // are through) and one copy, a cut one row by row
+        const bool whole = i1 - i0 == p.P;
+        uint8_t *stage = smem + C::kOffRing;
+        const bool ok = !aborted && ptx::mbar_wait(o_full, 0, abort_flag, a.err_word);
+        if (ok && g < D / 32) {
             ptx::tc_fence_after_sync();
             store_row(tmem + lane_bits + kColAcc, a.scale,
-                      p.dQ + (sq.q0 + i) * p.dq_stride + int64_t(h) * D, row_ok, g, g + 1, -ri,
-                      mean);
+                      row_ok ? p.dQ + (sq.q0 + i) * p.dq_stride + int64_t(row_h) * D : nullptr,
+                      whole ? stage : nullptr, r, g, g + 1, -ri, mean);
+        }
+        if (whole) {
+            ptx::fence_proxy_async_smem();
+            if (!ptx::bar_red_or(1, 32 * kRowWarps, !ok) && threadIdx.x == 0) {
+                for (int c = 0; c < C::kChunks; c += p.q_chunks)
+                    ptx::tma_store_5d(&p.tm_d0, stage + c * kChunkBytes, 0, 0, int(sq.q0 + i0), c,
+                                      hk);
+                ptx::bulk_commit_and_wait_read();
+            }
         }
     }
     ptx::tc_fence_before_sync();
@@ -733,25 +763,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_i = s1 - s0, n_q = n_i * p.G;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-        ptx::mbar_init(a_full, 1);
-        for (int s = 0; s < C::kQ; ++s) {
-            ptx::mbar_init(&q_full[s], 1);
-            ptx::mbar_init(&q_empty[s], 1);
+    uint8_t *tile_k = smem, *tile_v = smem + C::kTileBytes;
+    float *stats = reinterpret_cast<float *>(smem + C::kOffStat);
+    if (warp == kWarpLoad) {
+        // the barriers, and the first copies while the others set up
+        if (lane == 0) {
+            ptx::mbar_init(a_full, 1);
+            for (int s = 0; s < C::kQ; ++s) {
+                ptx::mbar_init(&q_full[s], 1);
+                ptx::mbar_init(&q_empty[s], 1);
+            }
+            for (int s = 0; s < C::kDO; ++s) {
+                ptx::mbar_init(&do_full[s], 1);
+                ptx::mbar_init(&do_empty[s], 1);
+                ptx::mbar_init(&st_full[s], 32);     // the load warp's lanes
+            }
+            ptx::mbar_init(s_full, 1);
+            ptx::mbar_init(dp_full, 1);
+            ptx::mbar_init(p_full, kRowWarps);
+            ptx::mbar_init(ds_full, kRowWarps);
+            ptx::mbar_init(o_full, 1);
+            ptx::mbar_init(drain, 1);
+            *abort_flag = 0;
+            ptx::fence_barrier_init();
+            const int k_row = int(sq.k0 + int64_t(kt) * BT), q_row = int(sq.q0 + int64_t(s0) * BT);
+            ptx::mbar_arrive_expect_tx(a_full, 2 * C::kTileBytes);
+            ptx::mbar_arrive_expect_tx(&q_full[0], C::kTileBytes);
+            ptx::mbar_arrive_expect_tx(&do_full[0], C::kTileBytes);
+            ptx::tma_load_5d(tile_k, &p.tm_k, a_full, 0, 0, k_row, 0, hk);
+            ptx::tma_load_5d(smem + C::kOffQ, &p.tm_q, &q_full[0], 0, 0, q_row, 0, hk * p.G);
+            ptx::tma_load_5d(tile_v, &p.tm_v, a_full, 0, 0, k_row, 0, hk);
+            ptx::tma_load_5d(smem + C::kOffDO, &p.tm_do, &do_full[0], 0, 0, q_row, 0, hk * p.G);
         }
-        for (int s = 0; s < C::kDO; ++s) {
-            ptx::mbar_init(&do_full[s], 1);
-            ptx::mbar_init(&do_empty[s], 1);
-            ptx::mbar_init(&st_full[s], 32);         // the load warp's lanes
-        }
-        ptx::mbar_init(s_full, 1);
-        ptx::mbar_init(dp_full, 1);
-        ptx::mbar_init(p_full, kRowWarps);
-        ptx::mbar_init(ds_full, kRowWarps);
-        ptx::mbar_init(o_full, 1);
-        ptx::mbar_init(drain, 1);
-        *abort_flag = 0;
-        ptx::fence_barrier_init();
+        __syncwarp();
     }
     if (warp == kWarpMma) {
         ptx::tmem_alloc(tmem_slot, kTmemCols);
@@ -762,18 +806,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     bool aborted = false;
-    uint8_t *tile_k = smem, *tile_v = smem + C::kTileBytes;
-    float *stats = reinterpret_cast<float *>(smem + C::kOffStat);
-
     if (warp == kWarpLoad) {
         // ======================= TMA producer (whole warp) ===================
         // Per step j: Q_j (its place is free once dK_{j-3} is through), dO_j (dV_{j-2}),
         // and the queries' statistics (dK_{j-2}: the rows are done with step j - 2).
-        if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(a_full, 2 * C::kTileBytes);
-            ptx::tma_load_5d(tile_k, &p.tm_k, a_full, 0, 0, int(sq.k0 + int64_t(kt) * BT), 0, hk);
-            ptx::tma_load_5d(tile_v, &p.tm_v, a_full, 0, 0, int(sq.k0 + int64_t(kt) * BT), 0, hk);
-        }
         // the next CTA's first tiles into L2: a map a lane
         auto prefetch_next = [&]() {
             const int64_t ni = int64_t(blockIdx.x) + kWindowSms - int64_t(far_items) * bh_count;
@@ -789,10 +825,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                  : &p.tm_do,
                                      0, 0, int(ns.k0 + nkt * BT), 0, lane < 2 ? nh : nh * p.G);
         };
-        int q_issued = 0, do_issued = 0;
+        int q_issued = 1, do_issued = 1;
         int h = hk * p.G, i = s0;
-        for (int j = 0; j < n_q; ++j) {
+        // a step's statistics, on their way a step ahead
+        float ls[BT / 32], ds[BT / 32];
+        auto load_stats = [&](int h, int i) {
             const int64_t stat0 = stat_row(a, b, h, sq.q0);
+#pragma unroll
+            for (int u = 0; u < BT / 32; ++u) {
+                const int q = i * BT + u * 32 + lane;
+                ls[u] = q < L ? a.lse[stat0 + q] : 0.f;
+                ds[u] = q < L ? p.D[stat0 + q] : 0.f;
+            }
+        };
+        load_stats(h, i);
+        for (int j = 0; j < n_q; ++j) {
             const int row = int(sq.q0 + int64_t(i) * BT);
             auto load = [&](uint8_t *dst, const CUtensorMap *tm, uint64_t *full) {
                 if (lane == 0) {
@@ -801,24 +848,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             };
-            float ls[BT / 32], ds[BT / 32];
-#pragma unroll
-            for (int u = 0; u < BT / 32; ++u) {
-                const int q = i * BT + u * 32 + lane;
-                ls[u] = q < L ? a.lse[stat0 + q] : 0.f;
-                ds[u] = q < L ? p.D[stat0 + q] : 0.f;
-            }
             const int qs = j % C::kQ, os = j % C::kDO;
-            if (!ptx::mbar_wait_warp(&q_empty[qs], (uint32_t(j / C::kQ) & 1u) ^ 1u, abort_flag,
-                                     a.err_word))
-                break;
-            load(smem + C::kOffQ + qs * C::kTileBytes, &p.tm_q, &q_full[qs]);
-            q_issued = j + 1;
-            if (!ptx::mbar_wait_warp(&do_empty[os], (uint32_t(j / C::kDO) & 1u) ^ 1u, abort_flag,
-                                     a.err_word))
-                break;
-            load(smem + C::kOffDO + os * C::kTileBytes, &p.tm_do, &do_full[os]);
-            do_issued = j + 1;
+            if (j > 0) {
+                if (!ptx::mbar_wait_warp(&q_empty[qs], (uint32_t(j / C::kQ) & 1u) ^ 1u, abort_flag,
+                                         a.err_word))
+                    break;
+                load(smem + C::kOffQ + qs * C::kTileBytes, &p.tm_q, &q_full[qs]);
+                q_issued = j + 1;
+                if (!ptx::mbar_wait_warp(&do_empty[os], (uint32_t(j / C::kDO) & 1u) ^ 1u, abort_flag,
+                                         a.err_word))
+                    break;
+                load(smem + C::kOffDO + os * C::kTileBytes, &p.tm_do, &do_full[os]);
+                do_issued = j + 1;
+            }
             if (j >= 2 && !ptx::mbar_wait_warp(&q_empty[(j - 2) % C::kQ],
                                                uint32_t((j - 2) / C::kQ) & 1u, abort_flag,
                                                a.err_word))
@@ -836,6 +878,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 i = s0;
                 ++h;
             }
+            if (j + 1 < n_q)
+                load_stats(h, i);
         }
         if (lane == 0 && *abort_flag) {
             drain_wait(a_full, 0);
@@ -1034,16 +1078,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0)
                 ptx::mbar_arrive(ds_full);
         }
-        if (!aborted && ptx::mbar_wait(o_full, 0, abort_flag, a.err_word)) {
+        // groups 0 and 1 have dV, 2 and 3 dK, half of the columns each: a whole tile by way of
+        // V's and K's places (all products are through) and a copy each, a cut one row by row
+        const int of = g >> 1, c0 = (g & 1) * (D / 64), c1 = c0 + D / 64;
+        const uint32_t acc = tmem + lane_bits + kColAcc + uint32_t(of * D);
+        const float mul = of == 0 ? 1.f : a.scale;
+        const bool key_ok = k < L, whole = !in_parts && kt * BT + BT <= L;
+        const bool ok = !aborted && ptx::mbar_wait(o_full, 0, abort_flag, a.err_word);
+        if (ok) {
             ptx::tc_fence_after_sync();
-            const bool key_ok = k < L;
-            // groups 0 and 1 write dV, 2 and 3 dK, half of the columns each
-            const int of = g >> 1, c0 = (g & 1) * (D / 64), c1 = c0 + D / 64;
-            const uint32_t acc = tmem + lane_bits + kColAcc + uint32_t(of * D);
-            const float mul = of == 0 ? 1.f : a.scale;
             if (in_parts) {
-                float *part = p.parts + (((int64_t(bh) * p.sink_tiles + kt) * p.slots + slot) * 2 + of) *
-                                            (BT * D) + r * D;
+                float *part = p.parts +
+                              (((int64_t(bh) * p.sink_tiles + kt) * p.slots + slot) * 2 + of) *
+                                  (BT * D) + r * D;
 #pragma unroll 1
                 for (int c = c0; c < c1; ++c) {
                     uint32_t o[32];
@@ -1061,7 +1108,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 __nv_bfloat16 *dst = of == 0 ? p.dV + (sq.k0 + k) * p.dv_stride
                                              : p.dK + (sq.k0 + k) * p.dk_stride;
-                store_row(acc, mul, dst + int64_t(hk) * D, key_ok, c0, c1);
+                store_row(acc, mul, key_ok ? dst + int64_t(hk) * D : nullptr,
+                          whole ? (of == 0 ? tile_v : tile_k) : nullptr, r, c0, c1);
+            }
+        }
+        if (whole) {
+            ptx::fence_proxy_async_smem();
+            if (!ptx::bar_red_or(1, 32 * kRowWarps, !ok) && threadIdx.x == 0) {
+                const int k_row = int(sq.k0 + int64_t(kt) * BT);
+                ptx::tma_store_5d(&p.tm_d0, tile_v, 0, 0, k_row, 0, hk);
+                ptx::tma_store_5d(&p.tm_d1, tile_k, 0, 0, k_row, 0, hk);
+                ptx::bulk_commit_and_wait_read();
             }
         }
     }
@@ -1170,6 +1227,10 @@ int launch_attention_window_bwd(const WindowBwdArgs &w, cudaStream_t stream)
         !make_tmap_heads(&pq.tm_v32, a.V, a.total_k, a.Hkv, 1, a.d, a.v_stride, kPad) ||
         !make_tmap_heads(&pk.tm_q, a.Q, a.total_q, a.H, 1, a.d, a.q_stride, BT) ||
         !make_tmap_heads(&pk.tm_do, w.dO, a.total_q, a.H, 1, a.d, row, BT))
+        return FA_ERR_CUDA;
+    if (!make_tmap_heads(&pq.tm_d0, w.dQ, a.total_q, a.Hkv, pq.G, a.d, w.dq_stride, pq.P) ||
+        !make_tmap_heads(&pk.tm_d0, w.dV, a.total_k, a.Hkv, 1, a.d, w.dv_stride, BT) ||
+        !make_tmap_heads(&pk.tm_d1, w.dK, a.total_k, a.Hkv, 1, a.d, w.dk_stride, BT))
         return FA_ERR_CUDA;
     pk.tm_k = pq.tm_k;
     pk.tm_v = pq.tm_v;
