@@ -597,7 +597,8 @@ FA_API int64_t fa_attention_kv4_workspace_bytes(int B, int Nq, int64_t total_q, 
  * and K neither at keys that a query does not see; a V that is not finite reaches
  * the queries that see its key and may reach others near them.
  * A sequence whose counts do not fit (negative, decreasing, above Nq, Nk or its
- * rows, outside the tensors) is not computed and sets FA_DEVERR_BAD_SEQLENS.
+ * rows, outside the tensors) is not computed and sets FA_DEVERR_BAD_SEQLENS; where
+ * cu_seqlens_q decreases, others may be left out too.
  * The same call gives the same bits.  One kernel on the library stream, no
  * synchronisation, no workspace.
  * Errors: FA_ERR_BAD_SIZE, FA_ERR_UNSUPPORTED (d, H / Hkv), FA_ERR_NULL_POINTER,

@@ -75,7 +75,8 @@ struct Params {
     WindowArgs a;
     int G, P, q_chunks;                // heads of a kv head; queries of a tile
     uint32_t div_g;                    // r / G = r * div_g >> 16 for r < 128
-    int n_pairs, split;
+    WindowGrid grid;                   // of TILES * P queries
+    int split;
     float scale_log2;
 };
 
@@ -139,9 +140,9 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
     const int n_split = SPLIT ? p.split : 1;
     const int part = SPLIT ? int(blockIdx.x % unsigned(n_split)) : 0;
     const int item = SPLIT ? int(blockIdx.x / unsigned(n_split)) : int(blockIdx.x);
-    const int pair = p.n_pairs - 1 - int(item % unsigned(p.n_pairs));
-    const int bh = int(item / unsigned(p.n_pairs));
-    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    int b, hk, pair;
+    if (!window_item(a, p.grid, TILES * p.P, item, b, hk, pair))
+        return;
     WindowSeq sq;
     if (!window_seq(a, b, sq)) {
         if (threadIdx.x == 0 && pair == 0 && hk == 0 && part == 0)
@@ -214,15 +215,17 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
         };
         // the next CTA's queries into L2
         auto prefetch_next = [&]() {
-            const int64_t ni = int64_t(item) + kWindowSms * (TILES == 2 ? 1 : 2);
-            const int nbh = int(ni / p.n_pairs);
+            int nb, nh, nt;
             WindowSeq ns;
-            if (SPLIT || lane >= TILES || nbh >= a.B * a.Hkv || !window_seq(a, nbh / a.Hkv, ns))
+            if (SPLIT ||
+                !window_item(a, p.grid, TILES * p.P,
+                             unsigned(item) + kWindowSms * (TILES == 2 ? 1 : 2), nb, nh, nt) ||
+                lane >= TILES || !window_seq(a, nb, ns))
                 return;
-            const int ni0 = ((p.n_pairs - 1 - int(ni % p.n_pairs)) * TILES + lane) * p.P;
+            const int ni0 = (nt * TILES + lane) * p.P;
             if (ni0 < ns.n)
                 for (int c = 0; c < C::kChunks; c += p.q_chunks)
-                    ptx::tma_prefetch_5d(&p.tm_q, 0, 0, int(ns.q0 + ni0), c, nbh % a.Hkv);
+                    ptx::tma_prefetch_5d(&p.tm_q, 0, 0, int(ns.q0 + ni0), c, nh);
         };
         if (last0 > first0)
             load_q(0);
@@ -757,9 +760,9 @@ int launch_attention_window(const WindowArgs &a, cudaStream_t stream)
     p.div_g = uint32_t(65536 / p.G + 1);
     p.split = choose_split(a, p.P);
     const int tiles = p.split > 1 ? 2 : choose_tiles(a);
-    p.n_pairs = (a.Nq + tiles * p.P - 1) / (tiles * p.P);
+    p.grid = window_grid(a, tiles * p.P);
     p.scale_log2 = float(double(a.scale) * 1.4426950408889634);
-    const int64_t blocks = int64_t(p.n_pairs) * a.B * a.Hkv * p.split;
+    const int64_t blocks = window_items(a, p.grid) * p.split;
     if (blocks > 0x7fffffffLL)
         return FA_ERR_TOO_LARGE;
     if (!make_tmap_heads(&p.tm_q, a.Q, a.total_q, a.Hkv, p.G, a.d, a.q_stride, p.P) ||

@@ -65,7 +65,8 @@ struct Params {
     float *parts;                      // [B Hkv][sink tiles][slots][dV, dK][128][d]
     int q_chunks;
     uint32_t div_g;                    // r / G = r * div_g >> 16 for r < 128
-    int G, P, n_tiles;                 // n_tiles: row tiles (dQ), key tiles (dK/dV) of Nq
+    int G, P;
+    WindowGrid grid;                   // of P queries (dQ), of 128 keys (dK/dV)
     int sink_tiles, slots, piece;      // piece: 128-query tiles of a far piece
     float scale_log2;
 };
@@ -125,8 +126,13 @@ __device__ __forceinline__ void store_row(uint32_t t_acc, float mul, __nv_bfloat
         ptx::tmem_wait_ld();
         if (add != nullptr)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-                o[e] = __float_as_uint(fmaf(more, add[c * 32 + e], __uint_as_float(o[e])));
+            for (int e = 0; e < 8; ++e) {
+                const float4 x = *reinterpret_cast<const float4 *>(add + c * 32 + 4 * e);
+                o[4 * e] = __float_as_uint(fmaf(more, x.x, __uint_as_float(o[4 * e])));
+                o[4 * e + 1] = __float_as_uint(fmaf(more, x.y, __uint_as_float(o[4 * e + 1])));
+                o[4 * e + 2] = __float_as_uint(fmaf(more, x.z, __uint_as_float(o[4 * e + 2])));
+                o[4 * e + 3] = __float_as_uint(fmaf(more, x.w, __uint_as_float(o[4 * e + 3])));
+            }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             uint32_t u[4];
@@ -170,12 +176,14 @@ struct CfgQ {
     static constexpr uint32_t kStageBytes = 2 * kTileBytes;  // K_j, V_j
     static constexpr int kStages = 3;
     static constexpr uint32_t kOffRing = 2 * kTileBytes;
-    // 128 D_i values, later the sums of dS of the rows' four threads; the keys' mean
-    static constexpr uint32_t kOffXch = kOffRing + 2 * kStageBytes;
+    // O's rows, later dQ's
+    static constexpr uint32_t kOffO = kOffRing + 2 * kStageBytes;
+    // parts of D_i, later the sums of dS, of the rows' four threads; the keys' mean
+    static constexpr uint32_t kOffXch = kOffO + kTileBytes;
     static constexpr uint32_t kOffMean = kOffXch + 4 * BT * 4;
     static constexpr uint32_t kOffBar = kOffMean + D * 4;
-    static constexpr int kBars = 1 + 2 * kStages + 9;
-    static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16 + 1024;
+    static constexpr int kBars = 1 + 2 * kStages + 8;
+    static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
     static __device__ __forceinline__ uint32_t stage_off(int s)
     {
@@ -197,14 +205,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     using C = CfgQ<D>;
     constexpr uint32_t kColQA = kColAcc + D;
     static_assert(kColQA + D <= kTmemCols, "tensor memory");
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // aligned as the tiles need it, with no room to align it here
+    extern __shared__ __align__(1024) uint8_t smem_aligned[];
+    uint8_t *smem = smem_aligned;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *a_full = bars, *kv_full = bars + 1, *kv_empty = bars + 1 + C::kStages;
     uint64_t *s_full = bars + 1 + 2 * C::kStages, *dp_full = s_full + 1, *s_free = s_full + 2,
              *p_full = s_full + 3, *o_full = s_full + 4, *drain = s_full + 5, *a_tm = s_full + 6,
-             *res_free = s_full + 7, *never = s_full + 8;
+             *never = s_full + 7;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -220,9 +228,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     const WindowArgs &a = p.a;
-    const int tile = p.n_tiles - 1 - int(blockIdx.x % unsigned(p.n_tiles));
-    const int bh = int(blockIdx.x / unsigned(p.n_tiles));
-    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    int b, hk, tile;
+    if (!window_item(a, p.grid, p.P, blockIdx.x, b, hk, tile))
+        return;
     WindowSeq sq;
     if (!window_seq(a, b, sq)) {
         if (threadIdx.x == 0 && tile == 0 && hk == 0)
@@ -237,29 +245,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     const int n_kv = (w.places + BT - 1) / BT;      // at least one
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // O for D: a row warp takes 8 rows, D / 8 lanes each; on its way during the set-up
-    constexpr int kLanesPerRow = D / 8, kRowsPerInst = 32 / kLanesPerRow;
-    constexpr int kRowsPerWarp = BT / kRowWarps;
-    const int sub = lane / kLanesPerRow, lr = lane % kLanesPerRow;
-    uint4 ov[kRowsPerWarp / kRowsPerInst];
-    if (warp < kRowWarps)
-#pragma unroll
-        for (int k = 0; k < kRowsPerWarp / kRowsPerInst; ++k) {
-            const int rr = warp * kRowsPerWarp + k * kRowsPerInst + sub;
-            const int qr = int(rr * p.div_g >> 16), hr = hk * p.G + rr - qr * p.G;
-            ov[k] = make_uint4(0, 0, 0, 0);
-            if (qr < p.P && i0 + qr < i1)
-                ov[k] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.O) +
-                                                         ((sq.q0 + i0 + qr) * a.H + hr) * D + lr * 8);
-        }
-
+    // a row thread's row of the tile, its query and head
     const int row_r = (warp & 3) * 32 + lane, row_q = int(row_r * p.div_g >> 16);
     const bool row_ok = warp < kRowWarps && row_q < p.P && i0 + row_q < i1;
-    const int row_h = hk * p.G + row_r - row_q * p.G;         // the row's head
+    const int row_h = hk * p.G + row_r - row_q * p.G;
     const int64_t stat = row_ok ? stat_row(a, b, row_h, sq.q0) + i0 + row_q : 0;
-    const float lse2 = row_ok ? a.lse[stat] * kLog2e : 0.f;
+    const float lse = row_ok ? a.lse[stat] : 0.f;     // (on its way during the set-up)
 
-    uint8_t *tile_q = smem, *tile_do = smem + C::kTileBytes;
+    uint8_t *tile_q = smem, *tile_do = smem + C::kTileBytes, *tile_o = smem + C::kOffO;
     // the copies of step j into its ring stage, by the load warp
     auto issue_step = [&](int j) {
         const int stage = j % C::kStages;
@@ -297,16 +290,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             ptx::mbar_init(o_full, 1);
             ptx::mbar_init(drain, 1);
             ptx::mbar_init(a_tm, kRowWarps);
-            ptx::mbar_init(res_free, kRowWarps);
             ptx::mbar_init(never, 1);
             *abort_flag = 0;
             ptx::fence_barrier_init();
-            ptx::mbar_arrive_expect_tx(a_full, 2 * C::kChunks * p.P * p.G * 128);
+            ptx::mbar_arrive_expect_tx(a_full, 3 * C::kChunks * p.P * p.G * 128);
             for (int c = 0; c < C::kChunks; c += p.q_chunks) {
                 ptx::tma_load_5d(tile_q + c * kChunkBytes, &p.tm_q, a_full, 0, 0, int(sq.q0 + i0),
                                  c, hk);
                 ptx::tma_load_5d(tile_do + c * kChunkBytes, &p.tm_do, a_full, 0, 0,
                                  int(sq.q0 + i0), c, hk);
+                ptx::tma_load_5d(tile_o + c * kChunkBytes, &p.tm_o, a_full, 0, 0, int(sq.q0 + i0),
+                                 c, hk);
             }
         }
         __syncwarp();
@@ -354,25 +348,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         };
         // the next CTA's rows into L2: a map a lane
         auto prefetch_next = [&]() {
-            const int64_t ni = int64_t(blockIdx.x) + kWindowSms;
-            const int nbh = int(ni / p.n_tiles);
+            int nb, nh, nt;
             WindowSeq ns;
-            if (nbh >= a.B * a.Hkv || !window_seq(a, nbh / a.Hkv, ns))
+            if (!window_item(a, p.grid, p.P, blockIdx.x + kWindowSms, nb, nh, nt) ||
+                !window_seq(a, nb, ns))
                 return;
-            const int ni0 = (p.n_tiles - 1 - int(ni % p.n_tiles)) * p.P;
+            const int ni0 = nt * p.P;
             if (ni0 < ns.L && lane < 3)
                 for (int c = 0; c < C::kChunks; c += p.q_chunks)
                     ptx::tma_prefetch_5d(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_do : &p.tm_o, 0, 0,
-                                         int(ns.q0 + ni0), c, nbh % a.Hkv);
+                                         int(ns.q0 + ni0), c, nh);
         };
         int issued = 1;
         for (int j = 0; j < n_kv; ++j) {
             if (j > 0) {
                 const int stage = j % C::kStages;
-                // stage 2 is the Q / dO region: free once the rows are done with it
+                // stage 2 is the Q / dO region: free once these are in tensor memory
                 if (!ptx::mbar_wait_warp(&kv_empty[stage], (uint32_t(j / C::kStages) & 1u) ^ 1u,
                                          abort_flag, a.err_word) ||
-                    (j == 2 && !ptx::mbar_wait_warp(res_free, 0, abort_flag, a.err_word)))
+                    (j == 2 && !ptx::mbar_wait_warp(a_tm, 0, abort_flag, a.err_word)))
                     break;
                 issue_step(j);
                 issued = j + 1;
@@ -505,22 +499,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         const int g = warp >> 2, col0 = 32 * g;      // of the row's four threads; its columns
         const int i = i0 + row_q;
         const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
-        // D_i = dO_i . O_i, dO from the resident tile (128-byte swizzle)
         float *xch = reinterpret_cast<float *>(smem + C::kOffXch);
         {
             const bool a_ok = row_wait(a_full, 0, abort_flag, a.err_word);
+            float part = 0.f;                        // of D_i = dO_i . O_i
             if (a_ok) {
-                // this thread's quarter of its row of Q and of dO into tensor memory
+                // this thread's quarter of its row of Q and of dO (128-byte swizzle) into
+                // tensor memory, and of O beside dO
+                auto unit = [&](const uint8_t *tile, int ul) {
+                    const int e0 = g * (D / 4) + ul * 8, un = (e0 & 63) >> 3;
+                    return *reinterpret_cast<const uint4 *>(tile + (e0 >> 6) * kChunkBytes + r * 128 +
+                                                            ((un ^ (r & 7)) << 4));
+                };
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const uint8_t *src = t == 0 ? tile_q : tile_do;
                     uint32_t u[D / 8];
 #pragma unroll
                     for (int ul = 0; ul < D / 32; ++ul) {
-                        const int e0 = g * (D / 4) + ul * 8;
-                        const int un = (e0 & 63) >> 3;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(
-                            src + (e0 >> 6) * kChunkBytes + r * 128 + ((un ^ (r & 7)) << 4));
+                        const uint4 v = unit(t == 0 ? tile_q : tile_do, ul);
                         u[4 * ul + 0] = v.x;
                         u[4 * ul + 1] = v.y;
                         u[4 * ul + 2] = v.z;
@@ -532,43 +528,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                         ptx::tmem_st16(dst, u);
                     else
                         ptx::tmem_st8(dst, u);
+                    if (t == 1)
+#pragma unroll
+                        for (int ul = 0; ul < D / 32; ++ul) {
+                            const uint4 o = unit(tile_o, ul);
+                            const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t gw = u[4 * ul + e];
+                                part = fmaf(__uint_as_float(ow[e] << 16), __uint_as_float(gw << 16),
+                                            part);
+                                part = fmaf(__uint_as_float(ow[e] & 0xffff0000u),
+                                            __uint_as_float(gw & 0xffff0000u), part);
+                            }
+                        }
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before_sync();
                 __syncwarp();
+                // (the Q / dO region is free for the ring's third stage, too)
                 if (lane == 0)
                     ptx::mbar_arrive(a_tm);
             }
-#pragma unroll
-            for (int k = 0; k < kRowsPerWarp / kRowsPerInst; ++k) {
-                const int rr = warp * kRowsPerWarp + k * kRowsPerInst + sub;
-                const int u = lr & 7, chunk = lr >> 3;
-                const uint4 gv = a_ok ? *reinterpret_cast<const uint4 *>(
-                                            tile_do + chunk * kChunkBytes + rr * 128 +
-                                            ((u ^ (rr & 7)) << 4))
-                                      : make_uint4(0, 0, 0, 0);
-                const uint32_t ow[4] = {ov[k].x, ov[k].y, ov[k].z, ov[k].w};
-                const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w};
-                float part = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    part = fmaf(__uint_as_float(ow[e] << 16), __uint_as_float(gw[e] << 16), part);
-                    part = fmaf(__uint_as_float(ow[e] & 0xffff0000u),
-                                __uint_as_float(gw[e] & 0xffff0000u), part);
-                }
-#pragma unroll
-                for (int o = kLanesPerRow / 2; o > 0; o >>= 1)
-                    part += __shfl_xor_sync(0xffffffffu, part, o);
-                if (lr == 0)
-                    xch[rr] = part;
-            }
-            // this warp has finished with the Q / dO region (ring stage 2)
-            __syncwarp();
-            if (a_ok && lane == 0)
-                ptx::mbar_arrive(res_free);
+            xch[g * BT + r] = part;
         }
+        const float lse2 = lse * kLog2e;
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");   // the row threads
-        const float Di = xch[r];
+        const float Di = (xch[r] + xch[BT + r]) + (xch[2 * BT + r] + xch[3 * BT + r]);
         if (g == 0 && row_ok)
             p.D[stat] = Di;
         const float sl = p.scale_log2;
@@ -636,15 +622,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         }
         const float ds_sum = ds_sum2.x + ds_sum2.y;
         // the sum of the row's dS over its threads, and (from the load warp) the keys' mean
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");   // all have read D
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");   // xch has been read
         xch[g * BT + r] = ds_sum;
         asm volatile("bar.sync 2, %0;" ::"n"(32 * kRowWarps + 32) : "memory");
         const float ri = (xch[r] + xch[BT + r]) + (xch[2 * BT + r] + xch[3 * BT + r]);
         const float *mean = reinterpret_cast<const float *>(smem + C::kOffMean);
-        // 32 columns of each row's dQ a thread: a whole tile by way of the ring (all products
-        // are through) and one copy, a cut one row by row
+        // 32 columns of each row's dQ a thread: a whole tile by way of O's place and one copy,
+        // a cut one row by row
         const bool whole = i1 - i0 == p.P;
-        uint8_t *stage = smem + C::kOffRing;
+        uint8_t *stage = tile_o;
         const bool ok = !aborted && ptx::mbar_wait(o_full, 0, abort_flag, a.err_word);
         if (ok && g < D / 32) {
             ptx::tc_fence_after_sync();
@@ -730,22 +716,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const WindowArgs &a = p.a;
     const int bh_count = a.B * a.Hkv;
     const int far_items = (p.slots - 1) * p.sink_tiles;       // of a (sequence, kv head)
-    int bh, kt, slot;
-    {
-        const unsigned far = unsigned(far_items) * unsigned(bh_count);
-        if (blockIdx.x < far) {
-            bh = int(blockIdx.x % unsigned(bh_count));
-            const int f = int(blockIdx.x / unsigned(bh_count));
-            kt = f % p.sink_tiles;
-            slot = 1 + f / p.sink_tiles;
-        } else {
-            const unsigned rest = blockIdx.x - far;
-            bh = int(rest / unsigned(p.n_tiles));
-            kt = int(rest % unsigned(p.n_tiles));
-            slot = 0;
-        }
+    int b, hk, kt, slot = 0;
+    const unsigned far = unsigned(far_items) * unsigned(bh_count);
+    if (blockIdx.x < far) {
+        const int bh = int(blockIdx.x % unsigned(bh_count));
+        const int f = int(blockIdx.x / unsigned(bh_count));
+        b = bh / a.Hkv;
+        hk = bh % a.Hkv;
+        kt = f % p.sink_tiles;
+        slot = 1 + f / p.sink_tiles;
+    } else if (!window_item(a, p.grid, BT, blockIdx.x - far, b, hk, kt)) {
+        return;
     }
-    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int bh = b * a.Hkv + hk;
     WindowSeq sq;
     if (!window_seq(a, b, sq) || kt * BT >= sq.L)   // (a bad one is flagged by the dQ kernel)
         return;
@@ -812,12 +795,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // and the queries' statistics (dK_{j-2}: the rows are done with step j - 2).
         // the next CTA's first tiles into L2: a map a lane
         auto prefetch_next = [&]() {
-            const int64_t ni = int64_t(blockIdx.x) + kWindowSms - int64_t(far_items) * bh_count;
-            const int nbh = int(ni / p.n_tiles), nkt = int(ni % p.n_tiles);
+            const unsigned ni = blockIdx.x + kWindowSms;
+            int nb, nh, nkt;
             WindowSeq ns;
-            if (ni < 0 || nbh >= bh_count || !window_seq(a, nbh / a.Hkv, ns))
+            if (ni < far || !window_item(a, p.grid, BT, ni - far, nb, nh, nkt) || !window_seq(a, nb, ns))
                 return;
-            const int nh = nbh % a.Hkv;
             if (nkt * BT < ns.L && lane < 4)
                 ptx::tma_prefetch_5d(lane == 0   ? &p.tm_k
                                      : lane == 1 ? &p.tm_v
@@ -1204,16 +1186,16 @@ int launch_attention_window_bwd(const WindowBwdArgs &w, cudaStream_t stream)
     pq.P = BT / pq.G;
     pq.q_chunks = tmap_heads_chunks(pq.G, a.d, pq.P);
     pq.div_g = uint32_t(65536 / pq.G + 1);
-    pq.n_tiles = (a.Nq + pq.P - 1) / pq.P;
+    pq.grid = window_grid(a, pq.P);
     pq.sink_tiles = lay.sink_tiles;
     pq.slots = lay.slots;
     pq.piece = lay.piece;
     pq.scale_log2 = float(double(a.scale) * 1.4426950408889634);
     Params pk = pq;
-    pk.n_tiles = (a.Nq + BT - 1) / BT;
+    pk.grid = window_grid(a, BT);
     const int64_t bh = int64_t(a.B) * a.Hkv;
-    const int64_t dq_blocks = pq.n_tiles * bh;
-    const int64_t kv_blocks = (pk.n_tiles + int64_t(lay.slots - 1) * lay.sink_tiles) * bh;
+    const int64_t dq_blocks = window_items(a, pq.grid);
+    const int64_t kv_blocks = window_items(a, pk.grid) + int64_t(lay.slots - 1) * lay.sink_tiles * bh;
     const int64_t join_blocks = lay.slots > 1 ? bh * lay.sink_tiles * (2 * BT / 8) : 0;
     if (dq_blocks > 0x7fffffffLL || kv_blocks > 0x7fffffffLL || join_blocks > 0x7fffffffLL)
         return FA_ERR_TOO_LARGE;

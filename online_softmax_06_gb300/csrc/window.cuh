@@ -74,6 +74,74 @@ __device__ __forceinline__ WindowKeys window_keys(int window, int sinks, int i0,
     return w;
 }
 
+// Tile `idx` of all tiles of `rows` queries of packed sequences, as (sequence, tile from the
+// sequence's end); false behind the last.  A sequence whose counts do not fit has one (whose
+// CTA flags it).  All lanes of a warp together.
+__device__ __forceinline__ bool window_tile(const WindowArgs &a, int rows, int idx, int &b,
+                                            int &tile)
+{
+    const int lane = threadIdx.x & 31;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        int n = 0;
+        if (b0 + lane < a.B) {
+            const int64_t len = int64_t(a.cu_seqlens_q[b0 + lane + 1]) - a.cu_seqlens_q[b0 + lane];
+            n = len < 0 || len > a.Nq ? 1 : int((len + rows - 1) / rows);
+        }
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int x = __shfl_up_sync(0xffffffffu, sum, o);
+            sum += lane >= o ? x : 0;
+        }
+        const int all = __shfl_sync(0xffffffffu, sum, 31);
+        if (idx < all) {
+            const unsigned behind = __ballot_sync(0xffffffffu, idx < sum);
+            const int k = __ffs(int(behind)) - 1;
+            b = b0 + k;
+            tile = __shfl_sync(0xffffffffu, sum, k) - 1 - idx;
+            return true;
+        }
+        idx -= all;
+    }
+    return false;
+}
+
+// How the grid's items (tiles of `rows` queries of a kv head) are laid out: B times the
+// longest sequence's, or where packed sequences are unlike, as many as their rows have (an
+// empty CTA of these kernels holds its SM for a microsecond or more).
+struct WindowGrid {
+    int per_head;              // items of a kv head, or (not packed) of a sequence's kv head
+    int packed;
+};
+inline WindowGrid window_grid(const WindowArgs &a, int rows)
+{
+    const int64_t each = (int64_t(a.Nq) + rows - 1) / rows;
+    const int64_t all = a.total_q / rows + a.B;
+    if (a.cu_seqlens_q != nullptr && all < each * a.B && all < (int64_t(1) << 31))
+        return {int(all), 1};
+    return {int(each), 0};
+}
+inline int64_t window_items(const WindowArgs &a, const WindowGrid &g)
+{
+    return int64_t(g.per_head) * a.Hkv * (g.packed ? 1 : a.B);
+}
+// Item `idx` as (sequence, kv head, tile): the last tiles of a sequence first (early ones
+// see less), tiles of a head one behind the other.
+__device__ __forceinline__ bool window_item(const WindowArgs &a, const WindowGrid &g, int rows,
+                                            unsigned idx, int &b, int &hk, int &tile)
+{
+    const unsigned bh = idx / unsigned(g.per_head);
+    const int t = int(idx - bh * unsigned(g.per_head));
+    if (g.packed) {
+        hk = int(bh);
+        return hk < a.Hkv && window_tile(a, rows, t, b, tile);
+    }
+    b = int(bh / unsigned(a.Hkv));
+    hk = int(bh - unsigned(b) * unsigned(a.Hkv));
+    tile = g.per_head - 1 - t;
+    return b < a.B;
+}
+
 // CTAs that run at once, one an SM: the CTA this far behind in the grid is about the next
 // on this one's SM, and its first tiles, which nobody reads before it, are brought into L2
 // meanwhile (from DRAM its first product waited some 3 us for them).
