@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
     const int part = SPLIT ? int(blockIdx.x % unsigned(n_split)) : 0;
     const int item = SPLIT ? int(blockIdx.x / unsigned(n_split)) : int(blockIdx.x);
     int b, hk, pair;
-    if (!window_item(a, p.grid, TILES * p.P, item, b, hk, pair))
+    window_check(a, p.grid, blockIdx.x);
+    if (!window_item(a, p.grid, unsigned(item), b, hk, pair))
         return;
     WindowSeq sq;
     if (!window_seq(a, b, sq)) {
@@ -218,8 +219,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
             int nb, nh, nt;
             WindowSeq ns;
             if (SPLIT ||
-                !window_item(a, p.grid, TILES * p.P,
-                             unsigned(item) + kWindowSms * (TILES == 2 ? 1 : 2), nb, nh, nt) ||
+                !window_item(a, p.grid, unsigned(item) + kWindowSms * (TILES == 2 ? 1 : 2), nb, nh,
+                             nt) ||
                 lane >= TILES || !window_seq(a, nb, ns))
                 return;
             const int ni0 = (nt * TILES + lane) * p.P;

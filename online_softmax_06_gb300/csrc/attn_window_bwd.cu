@@ -62,7 +62,9 @@ struct Params {
     float *D;                          // as lse
     __nv_bfloat16 *dQ, *dK, *dV;
     int64_t dq_stride, dk_stride, dv_stride;
-    float *parts;                      // [B Hkv][sink tiles][slots][dV, dK][128][d]
+    float *parts;                      // [places][Hkv][sink tiles][dV, dK][128][d]
+    WindowCut part_cut;                // places of packed sequences (div 0: b * slots)
+    int far_items;                     // CTAs for them
     int q_chunks;
     uint32_t div_g;                    // r / G = r * div_g >> 16 for r < 128
     int G, P;
@@ -229,7 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
 
     const WindowArgs &a = p.a;
     int b, hk, tile;
-    if (!window_item(a, p.grid, p.P, blockIdx.x, b, hk, tile))
+    window_check(a, p.grid, blockIdx.x);
+    if (!window_item(a, p.grid, blockIdx.x, b, hk, tile))
         return;
     WindowSeq sq;
     if (!window_seq(a, b, sq)) {
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         auto prefetch_next = [&]() {
             int nb, nh, nt;
             WindowSeq ns;
-            if (!window_item(a, p.grid, p.P, blockIdx.x + kWindowSms, nb, nh, nt) ||
+            if (!window_item(a, p.grid, blockIdx.x + kWindowSms, nb, nh, nt) ||
                 !window_seq(a, nb, ns))
                 return;
             const int ni0 = nt * p.P;
@@ -688,6 +691,15 @@ __device__ __forceinline__ int near_end(int kt, int window, int L)
     return e < n ? int(e) : n;
 }
 
+// A sink tile's parts: [place][kv head][sink tile], a place being a slot of a sequence, slot
+// 0 its window's.
+__device__ __forceinline__ int64_t part_offset(const Params &p, int b, int hk, int kt, int slot,
+                                               int64_t q0)
+{
+    const int64_t place = (p.part_cut.div > 0 ? p.part_cut.at(q0, b) : int64_t(b) * p.slots) + slot;
+    return (place * p.a.Hkv + hk) * p.sink_tiles + kt;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_window_dkdv_kernel(const __grid_constant__ Params p)
@@ -714,21 +726,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // work item: the far pieces of the sinks' tiles first, then every key tile's window
     const WindowArgs &a = p.a;
-    const int bh_count = a.B * a.Hkv;
-    const int far_items = (p.slots - 1) * p.sink_tiles;       // of a (sequence, kv head)
     int b, hk, kt, slot = 0;
-    const unsigned far = unsigned(far_items) * unsigned(bh_count);
+    const unsigned far = unsigned(p.far_items);
     if (blockIdx.x < far) {
-        const int bh = int(blockIdx.x % unsigned(bh_count));
-        const int f = int(blockIdx.x / unsigned(bh_count));
-        b = bh / a.Hkv;
-        hk = bh % a.Hkv;
-        kt = f % p.sink_tiles;
-        slot = 1 + f / p.sink_tiles;
-    } else if (!window_item(a, p.grid, BT, blockIdx.x - far, b, hk, kt)) {
+        // (kt, place, kv head): a place is a (sequence, slot)
+        const unsigned q = blockIdx.x / unsigned(p.sink_tiles);
+        kt = int(blockIdx.x - q * unsigned(p.sink_tiles));
+        hk = int(q % unsigned(a.Hkv));
+        const int place = int(q / unsigned(a.Hkv));
+        if (p.part_cut.div > 0) {
+            int64_t number;
+            b = window_find(a.cu_seqlens_q, a.B, p.part_cut, place, number);
+            slot = int(number);
+        } else {
+            b = place / p.slots;
+            slot = place - b * p.slots;
+        }
+        if (slot <= 0)
+            return;                            // (the window's own part has its place, too)
+    } else if (!window_item(a, p.grid, blockIdx.x - far, b, hk, kt)) {
         return;
     }
-    const int bh = b * a.Hkv + hk;
     WindowSeq sq;
     if (!window_seq(a, b, sq) || kt * BT >= sq.L)   // (a bad one is flagged by the dQ kernel)
         return;
@@ -798,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const unsigned ni = blockIdx.x + kWindowSms;
             int nb, nh, nkt;
             WindowSeq ns;
-            if (ni < far || !window_item(a, p.grid, BT, ni - far, nb, nh, nkt) || !window_seq(a, nb, ns))
+            if (ni < far || !window_item(a, p.grid, ni - far, nb, nh, nkt) || !window_seq(a, nb, ns))
                 return;
             if (nkt * BT < ns.L && lane < 4)
                 ptx::tma_prefetch_5d(lane == 0   ? &p.tm_k
@@ -1070,9 +1088,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
             ptx::tc_fence_after_sync();
             if (in_parts) {
-                float *part = p.parts +
-                              (((int64_t(bh) * p.sink_tiles + kt) * p.slots + slot) * 2 + of) *
-                                  (BT * D) + r * D;
+                float *part = p.parts + part_offset(p, b, hk, kt, slot, sq.q0) * (2 * BT * D) +
+                              of * (BT * D) + r * D;
 #pragma unroll 1
                 for (int c = c0; c < c1; ++c) {
                     uint32_t o[32];
@@ -1130,10 +1147,11 @@ __global__ void __launch_bounds__(256) attn_window_join_kernel(const __grid_cons
     if (near >= n_qt)
         return;
     const int n = 1 + (n_qt - near + p.piece - 1) / p.piece;
-    const float *part = p.parts + (((int64_t(bh) * p.sink_tiles + kt) * p.slots) * 2 + g) * (BT * D) +
+    const float *part = p.parts + part_offset(p, b, hk, kt, 0, sq.q0) * (2 * BT * D) + g * (BT * D) +
                         r * D + lane * (D / 32);
+    const int64_t next = int64_t(a.Hkv) * p.sink_tiles * (2 * BT * D);
     float v[D / 32] = {};
-    for (int s = 0; s < n; ++s, part += 2 * BT * D)
+    for (int s = 0; s < n; ++s, part += next)
 #pragma unroll
         for (int e = 0; e < D / 32; ++e)
             v[e] += part[e];
@@ -1189,16 +1207,19 @@ int launch_attention_window_bwd(const WindowBwdArgs &w, cudaStream_t stream)
     pq.grid = window_grid(a, pq.P);
     pq.sink_tiles = lay.sink_tiles;
     pq.slots = lay.slots;
+    pq.part_cut = lay.cut_div > 0 ? WindowCut{3, lay.cut_div, 0} : WindowCut{0, 0, 0};
     pq.piece = lay.piece;
     pq.scale_log2 = float(double(a.scale) * 1.4426950408889634);
     Params pk = pq;
     pk.grid = window_grid(a, BT);
     const int64_t bh = int64_t(a.B) * a.Hkv;
     const int64_t dq_blocks = window_items(a, pq.grid);
-    const int64_t kv_blocks = window_items(a, pk.grid) + int64_t(lay.slots - 1) * lay.sink_tiles * bh;
+    const int64_t far_blocks = lay.places * lay.sink_tiles * a.Hkv;
+    const int64_t kv_blocks = window_items(a, pk.grid) + far_blocks;
     const int64_t join_blocks = lay.slots > 1 ? bh * lay.sink_tiles * (2 * BT / 8) : 0;
     if (dq_blocks > 0x7fffffffLL || kv_blocks > 0x7fffffffLL || join_blocks > 0x7fffffffLL)
         return FA_ERR_TOO_LARGE;
+    pk.far_items = int(far_blocks);
     const int64_t row = int64_t(a.H) * a.d;
     if (!make_tmap_heads(&pq.tm_q, a.Q, a.total_q, a.Hkv, pq.G, a.d, a.q_stride, pq.P) ||
         !make_tmap_heads(&pq.tm_do, w.dO, a.total_q, a.Hkv, pq.G, a.d, row, pq.P) ||

@@ -396,12 +396,17 @@ struct WindowBwdArgs {
     void *workspace;
 };
 // Its workspace: D, laid out as lse, and the fp32 parts of the tiles with sinks in
-// them: their window's, and one for each `piece` sub-tiles of 64 queries behind it.  A
-// piece is as long as a window's steps (its CTA takes as long as another one's), and
-// has 16 sub-tiles at least, which pays for its part.
+// them: their window's, and one for each `piece` tiles of 128 queries behind it.  A piece is
+// as long as a window's steps (its CTA takes as long as another one's), and has 8 tiles
+// at least, which pays for its part.
+// A sequence has 1 + ceil((tiles - near) / piece) parts where its tiles are more than the
+// window's `near`, so that it is y > 1 times 128 near long, and at most 2 + floor(y) parts.
+// Packed sequences have floor(3 x / (128 near)) places up to row x, so such a one has 3
+// floor(y) at least; or each the longest one's parts, whichever is less (with sequences of
+// one length the latter).
 struct WindowBwdLayout {
-    int64_t D, parts, bytes;
-    int sink_tiles, slots, piece;
+    int64_t D, parts, places, bytes;
+    int sink_tiles, slots, piece, cut_div;     // cut_div: 128 near, or 0
 };
 inline WindowBwdLayout window_bwd_layout(int B, int N, int64_t total, int H, int Hkv, int d,
                                          int window, int sinks)
@@ -415,11 +420,16 @@ inline WindowBwdLayout window_bwd_layout(int B, int N, int64_t total, int H, int
     // tile 0 has the most queries behind its window
     const int64_t far = n_qt > near ? (n_qt - near + L.piece - 1) / L.piece : 0;
     L.slots = sinks > 0 && far > 0 ? int(far) + 1 : 1;
-    const int64_t tiles = ((sinks < N ? sinks : N) + 127) / 128;
-    L.sink_tiles = L.slots > 1 ? int(tiles) : 0;
+    L.sink_tiles = L.slots > 1 ? int(((sinks < N ? sinks : N) + 127) / 128) : 0;
+    L.cut_div = 0;
+    L.places = L.slots > 1 ? int64_t(B) * L.slots : 0;
+    if (L.slots > 1 && 3 * total / (128 * near) < L.places) {
+        L.cut_div = int(128 * near);
+        L.places = 3 * total / (128 * near);
+    }
     L.D = 0;
     L.parts = up(total * H * 4);
-    L.bytes = L.parts + (L.slots > 1 ? int64_t(B) * Hkv * tiles * L.slots * 2 * 128 * d * 4 : 0);
+    L.bytes = L.parts + L.places * Hkv * L.sink_tiles * 2 * 128 * d * 4;
     return L;
 }
 int launch_attention_window_bwd(const WindowBwdArgs &a, cudaStream_t stream);

@@ -74,36 +74,34 @@ __device__ __forceinline__ WindowKeys window_keys(int window, int sinks, int i0,
     return w;
 }
 
-// Tile `idx` of all tiles of `rows` queries of packed sequences, as (sequence, tile from the
-// sequence's end); false behind the last.  A sequence whose counts do not fit has one (whose
-// CTA flags it).  All lanes of a warp together.
-__device__ __forceinline__ bool window_tile(const WindowArgs &a, int rows, int idx, int &b,
-                                            int &tile)
+// How the rows of packed sequences are cut into numbered places without asking how many
+// each sequence needs: sequence b has the places from F(cu[b], b) to F(cu[b + 1], b + 1),
+// F(x, b) = floor(x mul / div) + add b.  With div = rows, mul = add = 1 that is enough for
+// its tiles of `rows` rows; with add = 0 for what only long sequences have.
+struct WindowCut {
+    int mul, div, add;
+    __host__ __device__ int64_t at(int64_t x, int64_t b) const
+    {
+        return (mul == 1 ? int64_t(uint32_t(x) / uint32_t(div)) : x * mul / div) + add * b;
+    }
+};
+// The sequence whose places hold `idx` and idx's number among them; all lanes of a warp
+// together (32 probes a round).  idx is below at(total, B).
+__device__ __forceinline__ int window_find(const int32_t *cu, int B, const WindowCut &cut,
+                                           int64_t idx, int64_t &number)
 {
     const int lane = threadIdx.x & 31;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        int n = 0;
-        if (b0 + lane < a.B) {
-            const int64_t len = int64_t(a.cu_seqlens_q[b0 + lane + 1]) - a.cu_seqlens_q[b0 + lane];
-            n = len < 0 || len > a.Nq ? 1 : int((len + rows - 1) / rows);
-        }
-        int sum = n;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int x = __shfl_up_sync(0xffffffffu, sum, o);
-            sum += lane >= o ? x : 0;
-        }
-        const int all = __shfl_sync(0xffffffffu, sum, 31);
-        if (idx < all) {
-            const unsigned behind = __ballot_sync(0xffffffffu, idx < sum);
-            const int k = __ffs(int(behind)) - 1;
-            b = b0 + k;
-            tile = __shfl_sync(0xffffffffu, sum, k) - 1 - idx;
-            return true;
-        }
-        idx -= all;
+    int lo = 0, hi = B;                        // at(cu[lo], lo) <= idx < at(cu[hi], hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, probe = lo + lane * step;
+        const bool below = probe < hi && cut.at(cu[probe], probe) <= idx;
+        const unsigned ok = __ballot_sync(0xffffffffu, below);
+        const int last = 31 - __clz(int(ok | 1u));
+        lo += last * step;
+        hi = hi < lo + step ? hi : lo + step;
     }
-    return false;
+    number = idx - cut.at(cu[lo], lo);
+    return lo;
 }
 
 // How the grid's items (tiles of `rows` queries of a kv head) are laid out: B times the
@@ -112,34 +110,52 @@ __device__ __forceinline__ bool window_tile(const WindowArgs &a, int rows, int i
 struct WindowGrid {
     int per_head;              // items of a kv head, or (not packed) of a sequence's kv head
     int packed;
+    WindowCut cut;
 };
 inline WindowGrid window_grid(const WindowArgs &a, int rows)
 {
-    const int64_t each = (int64_t(a.Nq) + rows - 1) / rows;
-    const int64_t all = a.total_q / rows + a.B;
-    if (a.cu_seqlens_q != nullptr && all < each * a.B && all < (int64_t(1) << 31))
-        return {int(all), 1};
-    return {int(each), 0};
+    const WindowCut cut{1, rows, 1};
+    const int64_t each = (int64_t(a.Nq) + rows - 1) / rows, all = cut.at(a.total_q, a.B);
+    const bool packed = a.cu_seqlens_q != nullptr && all < each * a.B && all < (int64_t(1) << 31);
+    return {int(packed ? all : each), packed, cut};
 }
 inline int64_t window_items(const WindowArgs &a, const WindowGrid &g)
 {
     return int64_t(g.per_head) * a.Hkv * (g.packed ? 1 : a.B);
 }
-// Item `idx` as (sequence, kv head, tile): the last tiles of a sequence first (early ones
-// see less), tiles of a head one behind the other.
-__device__ __forceinline__ bool window_item(const WindowArgs &a, const WindowGrid &g, int rows,
-                                            unsigned idx, int &b, int &hk, int &tile)
+// Item `idx` as (sequence, kv head, tile): tiles of a head one behind the other, the last
+// of a sequence first where these are known (early ones see less).  The tile may lie behind
+// the sequence's end.
+__device__ __forceinline__ bool window_item(const WindowArgs &a, const WindowGrid &g, unsigned idx,
+                                            int &b, int &hk, int &tile)
 {
     const unsigned bh = idx / unsigned(g.per_head);
     const int t = int(idx - bh * unsigned(g.per_head));
     if (g.packed) {
         hk = int(bh);
-        return hk < a.Hkv && window_tile(a, rows, t, b, tile);
+        if (hk >= a.Hkv)
+            return false;
+        int64_t number;
+        b = window_find(a.cu_seqlens_q, a.B, g.cut, t, number);
+        tile = number < 0 || number > a.Nq ? 0 : int(number);
+        return true;
     }
     b = int(bh / unsigned(a.Hkv));
     hk = int(bh - unsigned(b) * unsigned(a.Hkv));
     tile = g.per_head - 1 - t;
     return b < a.B;
+}
+// The grid's first CTA flags sequences whose counts do not fit: others might find no CTA.
+__device__ __forceinline__ void window_check(const WindowArgs &a, const WindowGrid &g, unsigned idx)
+{
+    if (!g.packed || idx != 0)
+        return;
+    bool bad = false;
+    WindowSeq s;
+    for (int b = int(threadIdx.x); b < a.B; b += int(blockDim.x))
+        bad |= !window_seq(a, b, s);
+    if (bad)
+        record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
 }
 
 // CTAs that run at once, one an SM: the CTA this far behind in the grid is about the next

@@ -69,8 +69,30 @@ def test_gradient_workspace():
     assert n(2, 1000, 2000, 4, 2, 64, 8, 0) == 2000 * 4 * 4                     # D alone
     assert n(2, 1000, 2000, 4, 2, 64, 1000, 4) == 2000 * 4 * 4                  # no query behind the window
     assert n(2, 1000, 2000, 4, 2, 64, 8, 1000) == 2000 * 4 * 4                  # all keys are sinks
-    # 1000 tokens: 16 sub-tiles of 64, three of them near the sinks' tile: one piece behind
+    # 1000 tokens: eight tiles, two of them near the sinks' tile: one piece behind
     assert n(2, 1000, 2000, 4, 2, 64, 8, 4) == 2000 * 4 * 4 + 2 * 2 * 2 * 2 * 128 * 64 * 4
+
+
+def test_gradient_workspace_of_unlike_sequences():
+    """One long sequence among many: room for its parts, not for as many of each."""
+    n = fa.fa_attention_window_bwd_workspace_bytes
+    part = 2 * 128 * 64 * 4
+    places = (n(1000, 32768, 100000, 2, 1, 64, 1024, 4) - 100000 * 2 * 4) // part
+    assert places == 3 * 100000 // (128 * 9)
+    # every sequence's parts fit its places
+    rng = np.random.default_rng(0)
+    for _ in range(2000):
+        window = int(rng.integers(1, 3000))
+        near = (window + 254) // 128
+        lens = rng.integers(0, 20000, 20) * (rng.random(20) < 0.4)
+        cu = np.concatenate(([0], np.cumsum(lens)))
+        piece = max(8, near)
+        for b, x in enumerate(lens):
+            tiles = -(-int(x) // 128)
+            if tiles > near:
+                parts = 1 + -(-(tiles - near) // piece)
+                at = [3 * int(c) // (128 * near) for c in cu[b:b + 2]]
+                assert at[1] - at[0] >= parts
 
 
 def test_oracle_gradient():

@@ -69,6 +69,12 @@ def test_packed_ragged(form, H, Hkv, d, sinks):
     run([130, 0, 1, 129, 2400, 128, 3, 0], H, Hkv, d, form, 150, sinks)
 
 
+@pytest.mark.parametrize("window,sinks", [(64, 4), (300, 200), (1000, 1)])
+def test_unlike_sequences(window, sinks):
+    """Many short sequences and a few long ones: the places of the sinks' parts go by the rows."""
+    run([3000, 1, 0, 40] + [17] * 60 + [900, 129] + [128] * 5 + [2300, 3], 2, 1, 64, "packed", window, sinks)
+
+
 def test_rows_behind_the_last_sequence_stay():
     batch, o, lse, do, how, want = run([200, 61], 4, 2, 128, "packed", 64, 4, spare=90)
     out = [torch.full(x.shape, 7.0, dtype=torch.bfloat16, device="cuda") for x in want]

@@ -46,6 +46,15 @@ def test_packed_ragged(form, H, Hkv, d):
                         form, 150, 4)
 
 
+@pytest.mark.parametrize("window", [60, 700])
+def test_many_sequences(window):
+    """More sequences than a warp looks up at once, most of them short or empty."""
+    rng = np.random.default_rng(9)
+    n = [int(x) for x in rng.integers(0, 90, 1200)]
+    n[700], n[1199] = 1500, 800
+    run(n, n, 2, 1, 64, "packed", window, 3)
+
+
 def test_rows_behind_the_last_sequence_stay():
     batch = Batch([200, 60], [300, 60], 4, 2, 128, "packed", spare=90)
     o = torch.full(batch.gq.shape, 7.0, dtype=torch.bfloat16, device="cuda")
