@@ -214,20 +214,6 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
             }
             __syncwarp();
         };
-        // the next CTA's queries into L2
-        auto prefetch_next = [&]() {
-            int nb, nh, nt;
-            WindowSeq ns;
-            if (SPLIT ||
-                !window_item(a, p.grid, unsigned(item) + kWindowSms * (TILES == 2 ? 1 : 2), nb, nh,
-                             nt) ||
-                lane >= TILES || !window_seq(a, nb, ns))
-                return;
-            const int ni0 = (nt * TILES + lane) * p.P;
-            if (ni0 < ns.n)
-                for (int c = 0; c < C::kChunks; c += p.q_chunks)
-                    ptx::tma_prefetch_5d(&p.tm_q, 0, 0, int(ns.q0 + ni0), c, nh);
-        };
         if (last0 > first0)
             load_q(0);
         int stage = 0;
@@ -262,8 +248,6 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
                 }
                 if (j == step0 && kv == 0 && last1 > first1)
                     load_q(1);
-                if (j == step0 && kv == 1)
-                    prefetch_next();
             }
         }
         if (lane == 0 && (aborted || *abort_flag)) {

@@ -811,20 +811,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ======================= TMA producer (whole warp) ===================
         // Per step j: Q_j (its place is free once dK_{j-3} is through), dO_j (dV_{j-2}),
         // and the queries' statistics (dK_{j-2}: the rows are done with step j - 2).
-        // the next CTA's first tiles into L2: a map a lane
-        auto prefetch_next = [&]() {
-            const unsigned ni = blockIdx.x + kWindowSms;
-            int nb, nh, nkt;
-            WindowSeq ns;
-            if (ni < far || !window_item(a, p.grid, ni - far, nb, nh, nkt) || !window_seq(a, nb, ns))
-                return;
-            if (nkt * BT < ns.L && lane < 4)
-                ptx::tma_prefetch_5d(lane == 0   ? &p.tm_k
-                                     : lane == 1 ? &p.tm_v
-                                     : lane == 2 ? &p.tm_q
-                                                 : &p.tm_do,
-                                     0, 0, int(ns.k0 + nkt * BT), 0, lane < 2 ? nh : nh * p.G);
-        };
         int q_issued = 1, do_issued = 1;
         int h = hk * p.G, i = s0;
         // a step's statistics, on their way a step ahead
@@ -872,8 +858,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st[BT + u * 32 + lane] = -ds[u];
             }
             ptx::mbar_arrive(&st_full[os]);          // all lanes, after their writes
-            if (j == 1 || n_q == 1)
-                prefetch_next();
             if (++i == s1) {
                 i = s0;
                 ++h;

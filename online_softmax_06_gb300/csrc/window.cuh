@@ -159,8 +159,7 @@ __device__ __forceinline__ void window_check(const WindowArgs &a, const WindowGr
 }
 
 // CTAs that run at once, one an SM: the CTA this far behind in the grid is about the next
-// on this one's SM, and its first tiles, which nobody reads before it, are brought into L2
-// meanwhile (from DRAM its first product waited some 3 us for them).
+// on this one's SM.
 constexpr int kWindowSms = 152;
 
 // The lowest `n` bits, n clamped to 0 .. 32.
