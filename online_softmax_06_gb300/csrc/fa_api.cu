@@ -36,6 +36,15 @@ DeviceInfo *current_device()
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
         return nullptr;
+    // A host thread's first call may be this one (a training framework's gradients run on
+    // threads of their own): the tensor maps' encoding needs the device's context current
+    // there, which cudaGetDevice does not see to.
+    thread_local int bound = -1;
+    if (bound != dev) {
+        if (cudaSetDevice(dev) != cudaSuccess)
+            return nullptr;
+        bound = dev;
+    }
     DeviceInfo *info = &g_dev[dev];
     std::call_once(info->once, [info, dev] {
         int major = 0, minor = 0;
