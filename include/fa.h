@@ -592,14 +592,17 @@ FA_API int64_t fa_attention_kv4_workspace_bytes(int B, int Nq, int64_t total_q, 
  *   Q, K, V: bf16 rows of H * d, and Hkv * d, contiguous values, q_stride, k_stride
  *   and v_stride elements apart (multiples of 8, at least the row); 16-byte
  *   aligned.  O: contiguous bf16, 16-byte aligned.  d: 64 or 128.  H / Hkv <= 128.
- *   window >= 1, sinks >= 0, scale > 0 and finite.
+ *   window >= 1, sinks >= 0, scale > 0 (and below 2^126).
  * What K and V hold behind a sequence's keys does not reach a result, NaN or not,
  * and K neither at keys that a query does not see; a V that is not finite reaches
  * the queries that see its key and may reach others near them.
  * A sequence whose counts do not fit (negative, decreasing, above Nq, Nk or its
  * rows, outside the tensors) is not computed and sets FA_DEVERR_BAD_SEQLENS; where
  * cu_seqlens_q decreases, others may be left out too.
- * The same call gives the same bits.  One kernel on the library stream, no
+ * Probabilities are rounded to bf16 for the product with V, scores and sums are fp32.
+ * Up to 64 query rows a kv head (Nq * H / Hkv; decode steps, drafted tokens) have a
+ * kernel of their own, so Nq should not be far above the most queries there are.  The
+ * same call gives the same bits.  One kernel on the library stream, no
  * synchronisation, no workspace.
  * Errors: FA_ERR_BAD_SIZE, FA_ERR_UNSUPPORTED (d, H / Hkv), FA_ERR_NULL_POINTER,
  * FA_ERR_MISALIGNED (pointers, strides), FA_ERR_TOO_LARGE, FA_ERR_NO_DEVICE,
@@ -728,7 +731,8 @@ FA_API int fa_set_stream(void *stream);
  * bf16 attention forward (fa_attention_fwd / fa_attention_fwd_varlen), one-pass
  * backward (fa_attention_bwd_atomic / fa_attention_bwd_atomic_varlen),
  * attention over the 4-bit cache (fa_attention_kv4) or window attention
- * (fa_attention_window_fwd, fa_attention_window_bwd) launched from this host
+ * (fa_attention_window_bwd, and fa_attention_window_fwd with more than 64 query rows
+ * a kv head, whose other form waits for nothing) launched from this host
  * thread, whichever comes first.  In a forward or backward launch the
  * warp that issues the tensor-core instructions first waits, bounded by `ns`
  * nanoseconds, on a barrier that nothing arrives at.  The wait runs out, sets

@@ -748,14 +748,15 @@ int launch_attention_window(const WindowArgs &a, cudaStream_t stream)
     p.grid = window_grid(a, tiles * p.P);
     p.scale_log2 = float(double(a.scale) * 1.4426950408889634);
     const int64_t blocks = window_items(a, p.grid) * p.split;
+    const int64_t k_rows = a.total_k > 0 ? a.total_k : 1;      // (a map has a row at least)
     if (blocks > 0x7fffffffLL)
         return FA_ERR_TOO_LARGE;
     if (!make_tmap_heads(&p.tm_q, a.Q, a.total_q, a.Hkv, p.G, a.d, a.q_stride, p.P) ||
         !make_tmap_heads(&p.tm_o, a.O, a.total_q, a.Hkv, p.G, a.d, int64_t(a.H) * a.d, p.P) ||
-        !make_tmap_heads(&p.tm_k, a.K, a.total_k, a.Hkv, 1, a.d, a.k_stride, BN) ||
-        !make_tmap_heads(&p.tm_v, a.V, a.total_k, a.Hkv, 1, a.d, a.v_stride, BN) ||
-        !make_tmap_heads(&p.tm_k32, a.K, a.total_k, a.Hkv, 1, a.d, a.k_stride, kPad) ||
-        !make_tmap_heads(&p.tm_v32, a.V, a.total_k, a.Hkv, 1, a.d, a.v_stride, kPad))
+        !make_tmap_heads(&p.tm_k, a.K, k_rows, a.Hkv, 1, a.d, a.k_stride, BN) ||
+        !make_tmap_heads(&p.tm_v, a.V, k_rows, a.Hkv, 1, a.d, a.v_stride, BN) ||
+        !make_tmap_heads(&p.tm_k32, a.K, k_rows, a.Hkv, 1, a.d, a.k_stride, kPad) ||
+        !make_tmap_heads(&p.tm_v32, a.V, k_rows, a.Hkv, 1, a.d, a.v_stride, kPad))
         return FA_ERR_CUDA;
     if (p.split > 1)
         return a.d == 64 ? launch_d<64, true, 2>(p, blocks, stream)

@@ -1094,7 +1094,7 @@ int check_window(const void *Q, int64_t q_stride, const void *K, int64_t k_strid
     *empty = false;
     if (B < 0 || Nq < 0 || total_q < 0 || Nk < 0 || total_k < 0 || H < 0 || window < 1 ||
         sinks < 0 || (H > 0 && (Hkv < 1 || H % Hkv != 0)) ||
-        !(scale > 0.f && scale <= 3.0e38f) ||
+        !(scale > 0.f && scale < 8.5e37f) ||
         (cu_seqlens_q == nullptr && total_q != int64_t(B) * Nq) ||
         (cu_seqlens_k == nullptr && total_k != int64_t(B) * Nk))
         return FA_ERR_BAD_SIZE;

@@ -55,14 +55,59 @@ def test_many_sequences(window):
     run(n, n, 2, 1, 64, "packed", window, 3)
 
 
-def test_rows_behind_the_last_sequence_stay():
-    batch = Batch([200, 60], [300, 60], 4, 2, 128, "packed", spare=90)
+@pytest.mark.parametrize("n,L,window", [([200, 60], [300, 60], 64), ([200, 60], [300, 60], 290), ([3, 1, 0, 5], [300, 60, 9, 5], 64),
+                                        ([100, 90], [4000, 3900], 3800)])
+def test_rows_behind_the_last_sequence_stay(n, L, window):
+    """One tile a CTA, two, few queries, clusters."""
+    batch = Batch(n, L, 4, 2, 128, "packed", spare=90)
     o = torch.full(batch.gq.shape, 7.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((4, len(batch.gq)), 7.0, device="cuda")
-    fa.attention_window_fwd(batch.gq, batch.gk, batch.gv, 64, 4, out=o, lse=lse, **batch.kw)
+    fa.attention_window_fwd(batch.gq, batch.gk, batch.gv, window, 4, out=o, lse=lse, **batch.kw)
     device_error_clear()
-    assert (o[260:] == 7).all() and (lse[:, 260:] == 7).all()
-    check_forward(batch, o, lse, 64, 4)
+    assert (o[sum(n):] == 7).all() and (lse[:, sum(n):] == 7).all()
+    check_forward(batch, o, lse, window, 4)
+
+
+@pytest.mark.parametrize("nq", [1, 300])
+def test_no_keys_at_all(nq):
+    q = torch.randn(2, nq, 4, 64, device="cuda").bfloat16()
+    k = torch.empty(2, 0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = fa.attention_window_fwd(q, k, k, 10, 2)
+    device_error_clear()
+    assert (o == 0).all() and (lse == float("-inf")).all()
+
+
+def test_no_queries():
+    q = torch.empty(2, 0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(2, 9, 2, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = fa.attention_window_fwd(q, k, k, 10, 2)
+    assert o.shape == q.shape and lse.shape == (2, 4, 0)
+    e = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    o, lse = fa.attention_window_fwd(e, e, e, 10, 2, cu_seqlens_q=cu, cu_seqlens_k=cu)
+    assert o.shape == e.shape and lse.shape == (4, 0)
+    assert [g.shape for g in fa.attention_window_bwd(e, e, e, e, e, lse, 10, 2, cu_seqlens=cu)] == [e.shape] * 3
+
+
+@pytest.mark.parametrize("nq", [1, 300])
+def test_rows_far_into_a_long_cache(nq):
+    """K and V rows behind 2^31 elements, and rows of K and V unlike distances apart."""
+    H, Hkv, d, room, L = 4, 2, 128, 4_300_000, 4_299_990
+    rng = np.random.default_rng(8)
+    k = torch.empty(2, room, 2 * Hkv, d, dtype=torch.bfloat16, device="cuda")[:, :, :Hkv]     # 2.2e9 elements a sequence
+    v = torch.empty(2, room, Hkv, d, dtype=torch.bfloat16, device="cuda")
+    q = torch.from_numpy(rng.standard_normal((2, nq, H, d))).bfloat16().cuda()
+    seen = slice(L - nq - 200, L)
+    for x in (k, v):
+        x[1, seen] = torch.from_numpy(rng.standard_normal((nq + 200, Hkv, d))).bfloat16().cuda()
+        x[1, :4] = torch.from_numpy(rng.standard_normal((4, Hkv, d))).bfloat16().cuda()
+    o, lse = fa.attention_window_fwd(q, k, v, 200, 4, seqlens_k=torch.tensor([0, L], dtype=torch.int32, device="cuda"))
+    device_error_clear()
+    assert (o[0] == 0).all()
+    part = Batch([nq], [nq + 204], H, Hkv, d, "dense")
+    part.q = [q[1].cpu()]
+    part.k, part.v = ([torch.cat((x[1, :4], x[1, seen])).cpu()] for x in (k, v))
+    check_forward(part, o[1:], lse[1:], 200, 4)
 
 
 @pytest.mark.parametrize("nq", [1, 2, 5, 40, 300])
