@@ -17,6 +17,9 @@
 // an fp32 product would be off by p f_j 2^-24 (0.06 at a position of 10^6) --
 // and its upper 32 bits to sincospif.
 // Sums are fp32; each output is rounded once.
+// 32768 tokens, 32 + 8 heads of 128: forward 109 us, 6.2 TB/s (0.91 of a copy's rate), gradient
+// 173 us, 5.8 TB/s (issue slots two thirds used: the arithmetic of a value is what is left beside
+// memory); the weights' sums joined in 5 us.  64 tokens: 3.2 us, a launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
