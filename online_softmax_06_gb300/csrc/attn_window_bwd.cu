@@ -7,14 +7,15 @@
 // dK and dV summed over the G query heads that share a kv head.  Two kernels as in
 // attn_bwd.cu, whose roles, tensor memory and order of products they have, and no
 // atomics; then, where sinks are seen from outside their tile's window, a third:
-//   * attn_window_dq_kernel: a CTA per (sequence, kv head, 128 rows: queries x G
+//   * attn_window_dq_kernel: an item per (sequence, kv head, 128 rows: queries x G
 //     heads), the keys that they see in 128-key steps, the window's behind the
 //     sinks' as in the forward (window.cuh).  Also writes D.  D comes from O rounded
 //     to bf16, an error e that all keys of a row share: dQ is off by e sum_j P_ij K_j,
 //     which grows against dQ where keys have a part in common and the window is long
 //     (2^-9 of dQ becomes 2^-7.5 with a window of 2048).  But sum_j dS_ij is 0, so its
-//     computed value r_i is the error's, and r_i times a mean of the keys is taken off
-//     (the common part; of 16 rows a step, which the load warp reads beside its work).
+//     computed value r_i, of dS as rounded, is the errors', and r_i times a mean of the
+//     keys is taken off (the common part; of 16 rows of each step but the last, which the
+//     load warp reads beside its work); D_i + r_i is what dK takes.
 //   * attn_window_dkdv_kernel: a CTA per (sequence, kv head, 128 keys); 128-query
 //     steps over the queries that have these keys in their window, one head of the
 //     group after the other into the same accumulators.  Keys below `sinks` are seen
@@ -168,30 +169,45 @@ __device__ __forceinline__ int64_t stat_row(const WindowArgs &a, int b, int h, i
 // dO as bf16 A operands behind it.  The MMA warp issues, per 128-key step j: S_{j+1} as
 // soon as the rows have read S_j, dQ += dS_j K_j once they have stored dS_j, then dP_{j+1};
 // sixteen row warps (four threads a row, 32 columns each) form P while dQ and dP run and
-// dS while S does.  (2 x 4096 queries, 32 heads on 8, d = 128, window 1024: 190 us, tensor
-// cores 46 % busy; steps of 64 keys in two buffers took 246 us where these took 211: a
-// product 64 wide takes the tensor cores as long as one of 128.)  The ring's third stage
-// is the region that held Q and dO, free once they are in tensor memory and D is formed.
+// dS while S does.  A step takes 2300 cycles, its products 1640 (d = 128): dS_j -> dQ_j ->
+// dP_{j+1} -> dS_{j+1} is a chain.  With d = 64 there are columns for a second dP behind the
+// operands (384), and dP_{j+1} goes ahead of dQ_j (2 x 4096, 16 heads, window 4096, all three
+// kernels: 343 us, 351 without).  Steps of 64 keys in two buffers took 246 us where these
+// took 211 (2 x 4096, 32 heads on 8, d = 128, window 1024): a product 64 wide takes the
+// tensor cores as long as one of 128.
+// A CTA, one an SM, does items one after the other, its own and then such as have not begun
+// (it asks for their CTAs): Q and dO of the next pass through the ring behind this one's last
+// keys and are copied to tensor memory by the tensor cores' own path, and the next item's
+// first products run while the rows store this one's dQ.  2 x 4096, 32 heads on 8, d = 128,
+// window 1024: 188 us, a CTA an item 190; 8 packed sequences of 3001 tokens at most, 16
+// heads, d = 64, window 256: 84 us and 104.  r_i of dS as rounded, not before: dQ is off by
+// 0.0026 of its norm instead of 0.0030, dK by 0.0024 instead of 0.0026, for 1 % of the time.
 template <int D>
 struct CfgQ {
     static constexpr int kChunks = D / 64;
     static constexpr uint32_t kTileBytes = BT * D * 2;
-    static constexpr uint32_t kStageBytes = 2 * kTileBytes;  // K_j, V_j
+    static constexpr uint32_t kStageBytes = 2 * kTileBytes;  // Q and dO, or K_j and V_j
     static constexpr int kStages = 3;
-    static constexpr uint32_t kOffRing = 2 * kTileBytes;
-    // O's rows, later dQ's
-    static constexpr uint32_t kOffO = kOffRing + 2 * kStageBytes;
-    // parts of D_i, later the sums of dS, of the rows' four threads; the keys' mean
-    static constexpr uint32_t kOffXch = kOffO + kTileBytes;
-    static constexpr uint32_t kOffMean = kOffXch + 4 * BT * 4;
-    static constexpr uint32_t kOffBar = kOffMean + D * 4;
-    static constexpr int kBars = 1 + 2 * kStages + 8;
+    // O's rows, where there is room two items', and dQ's on their way out
+    static constexpr int kOBufs = D == 64 ? 2 : 1;
+    static constexpr uint32_t kOffO = kStages * kStageBytes;
+    static constexpr uint32_t kOffOut = kOffO + (kOBufs == 2 ? 2 : 0) * kTileBytes;
+    // parts of D_i, and of the sums of dS, of the rows' four threads; the keys' mean; items
+    static constexpr uint32_t kOffXch = kOffOut + kTileBytes;
+    static constexpr uint32_t kOffSum = kOffXch + (kOBufs == 2 ? 4 * BT * 4 : 0);
+    static constexpr uint32_t kOffMean = kOffSum + 4 * BT * 4;
+    static constexpr uint32_t kOffItem = kOffMean + D * 4;
+    static constexpr uint32_t kOffNext = kOffItem + 2 * 40;
+    static constexpr uint32_t kOffBar = kOffNext + 16;
+    // of dP and dS: where there are columns for two, dP_{j+1} need not wait for dQ_j
+    static constexpr int kDPs = D == 64 ? 2 : 1;
+    static __device__ __forceinline__ uint32_t col_dp(uint32_t step)
+    {
+        return kDPs == 2 && (step & 1u) ? 256 + 2 * D : 128;
+    }
+    static constexpr int kBars = 2 * kStages + kOBufs + kDPs + 10;
     static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-    static __device__ __forceinline__ uint32_t stage_off(int s)
-    {
-        return s == 2 ? 0u : kOffRing + uint32_t(s) * kStageBytes;
-    }
 };
 constexpr uint32_t kColAcc = 256, kColDP = 128;
 // Column of the packed bf16 operand for the product's K step kk: the 32 values of each
@@ -201,6 +217,13 @@ __host__ __device__ constexpr uint32_t packed_col(int kk)
 {
     return uint32_t(32 * (kk >> 1) + 8 * (kk & 1));
 }
+
+// An item of dQ, as the load warp found it.
+struct DqItem {
+    int done, b, hk, i0, i1, L;
+    int64_t q0, k0;
+};
+static_assert(sizeof(DqItem) == 40, "CfgQ");
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __grid_constant__ Params p)
@@ -212,12 +235,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     extern __shared__ __align__(1024) uint8_t smem_aligned[];
     uint8_t *smem = smem_aligned;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
-    uint64_t *a_full = bars, *kv_full = bars + 1, *kv_empty = bars + 1 + C::kStages;
-    uint64_t *s_full = bars + 1 + 2 * C::kStages, *dp_full = s_full + 1, *s_free = s_full + 2,
-             *p_full = s_full + 3, *o_full = s_full + 4, *drain = s_full + 5, *a_tm = s_full + 6,
-             *never = s_full + 7;
+    uint64_t *full = bars, *empty = bars + C::kStages, *o_in = bars + 2 * C::kStages;
+    uint64_t *s_full = o_in + C::kOBufs, *s_free = s_full + 1, *p_full = s_full + 2,
+             *acc_full = s_full + 3, *drain = s_full + 4, *out_full = s_full + 5,
+             *next_in = s_full + 6, *never = s_full + 7, *known = s_full + 8, *dp_full = s_full + 10;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    DqItem *items = reinterpret_cast<DqItem *>(smem + C::kOffItem);
 
     if (threadIdx.x == 32) {
         ptx::prefetch_tmap(&p.tm_q);
@@ -231,39 +255,104 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     const WindowArgs &a = p.a;
-    int b, hk, tile;
     window_check(a, p.grid, blockIdx.x);
-    if (!window_item(a, p.grid, blockIdx.x, b, hk, tile))
-        return;
-    WindowSeq sq;
-    if (!window_seq(a, b, sq)) {
-        if (threadIdx.x == 0 && tile == 0 && hk == 0)
-            record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
-        return;
-    }
-    const int i0 = tile * p.P, L = sq.L;
-    if (i0 >= L)
-        return;
-    const int i1 = min(i0 + p.P, L);
-    const WindowKeys w = window_keys(a.window, a.sinks, i0, i1, 0, kPad);
-    const int n_kv = (w.places + BT - 1) / BT;      // at least one
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto keys_of = [&](const DqItem &it) {
+        return window_keys(a.window, a.sinks, it.i0, it.i1, 0, kPad);
+    };
+    auto steps_of = [](const WindowKeys &w) { return (w.places + BT - 1) / BT; };   // at least one
+    auto stage_ptr = [&](int n) { return smem + uint32_t(n % C::kStages) * C::kStageBytes; };
 
-    // a row thread's row of the tile, its query and head
-    const int row_r = (warp & 3) * 32 + lane, row_q = int(row_r * p.div_g >> 16);
-    const bool row_ok = warp < kRowWarps && row_q < p.P && i0 + row_q < i1;
-    const int row_h = hk * p.G + row_r - row_q * p.G;
-    const int64_t stat = row_ok ? stat_row(a, b, row_h, sq.q0) + i0 + row_q : 0;
-    const float lse = row_ok ? a.lse[stat] : 0.f;     // (on its way during the set-up)
-
-    uint8_t *tile_q = smem, *tile_do = smem + C::kTileBytes, *tile_o = smem + C::kOffO;
-    // the copies of step j into its ring stage, by the load warp
-    auto issue_step = [&](int j) {
-        const int stage = j % C::kStages;
-        if (lane == 0)
-            ptx::mbar_arrive_expect_tx(&kv_full[stage], C::kStageBytes);
+    // ---- the load warp's: slots of the ring are numbered; Q and dO of an item take one,
+    // each step's keys one
+    int slots = 0, o_tiles = 0;
+    DqItem item{};
+    int asked = 0;                                   // for other CTAs' items
+    bool pending = false;
+    auto ask = [&]() {
+        if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(next_in, 16);
+            ptx::cta_cancel(smem + C::kOffNext, next_in);
+        }
+        ++asked;
+        pending = true;
         __syncwarp();
-        uint8_t *dst = smem + C::stage_off(stage);
+    };
+    auto find = [&](bool first, DqItem &item) {      // the next item
+        for (;; first = false) {
+            int64_t idx = blockIdx.x;
+            if (!first) {
+                if (!pending)
+                    ask();
+                if (!ptx::mbar_wait_warp(next_in, uint32_t(asked + 1) & 1u, abort_flag, a.err_word))
+                    return false;
+                idx = ptx::cta_cancelled(smem + C::kOffNext);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                pending = false;
+                if (idx < 0)
+                    return false;                    // (nor may any be asked for again)
+            }
+            int tile;
+            WindowSeq sq;
+            if (!window_item(a, p.grid, unsigned(idx), item.b, item.hk, tile))
+                continue;
+            if (!window_seq(a, item.b, sq)) {
+                if (lane == 0 && tile == 0 && item.hk == 0)
+                    record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
+                continue;
+            }
+            item.i0 = tile * p.P;
+            if (item.i0 >= sq.L)
+                continue;
+            item.i1 = min(item.i0 + p.P, sq.L);
+            item.L = sq.L;
+            item.q0 = sq.q0;
+            item.k0 = sq.k0;
+            return true;
+        }
+    };
+    // (a slot's copies are issued when the slot is free)
+    auto issue_o = [&](int k) {
+        if (lane == 0) {
+            uint64_t *bar = &o_in[k % C::kOBufs];
+            uint8_t *dst = smem + C::kOffO + uint32_t(k % C::kOBufs) * C::kTileBytes;
+            ptx::mbar_arrive_expect_tx(bar, C::kChunks * p.P * p.G * 128);
+            for (int c = 0; c < C::kChunks; c += p.q_chunks)
+                ptx::tma_load_5d(dst + c * kChunkBytes, &p.tm_o, bar, 0, 0, int(item.q0 + item.i0), c,
+                                 item.hk);
+        }
+        o_tiles = k + 1;
+        __syncwarp();
+    };
+    auto tell = [&](int k, const DqItem &it) {
+        if (lane == 0) {
+            items[k & 1] = it;
+            ptx::mbar_arrive(&known[k & 1]);
+        }
+        __syncwarp();
+    };
+    auto issue_q = [&](int k) {
+        if (lane == 0) {
+            uint64_t *bar = &full[slots % C::kStages];
+            ptx::mbar_arrive_expect_tx(bar, 2 * C::kChunks * p.P * p.G * 128);
+            for (int c = 0; c < C::kChunks; c += p.q_chunks) {
+                uint8_t *dst = stage_ptr(slots) + c * kChunkBytes;
+                const int row = int(item.q0 + item.i0);
+                ptx::tma_load_5d(dst, &p.tm_q, bar, 0, 0, row, c, item.hk);
+                ptx::tma_load_5d(dst + C::kTileBytes, &p.tm_do, bar, 0, 0, row, c, item.hk);
+            }
+        }
+        __syncwarp();
+        if (C::kOBufs == 2 || k == 0)
+            issue_o(k);
+    };
+    auto issue_keys = [&](const WindowKeys &w, int j) {
+        uint64_t *bar = &full[slots % C::kStages];
+        if (lane == 0)
+            ptx::mbar_arrive_expect_tx(bar, C::kStageBytes);
+        __syncwarp();
+        uint8_t *dst = stage_ptr(slots);
         const int v0 = j * BT;
         if (v0 < w.sp && v0 + BT > w.sp) {
             // pieces of 32 rows, a lane each
@@ -271,44 +360,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             const int v = v0 + q * kPad;
             if (c < C::kChunks)
                 ptx::tma_load_5d(dst + of * C::kTileBytes + c * kChunkBytes + q * kPad * 128,
-                                 of ? &p.tm_v32 : &p.tm_k32, &kv_full[stage], 0, 0,
-                                 int(sq.k0 + (v < w.sp ? v : w.lo + v - w.sp)), c, hk);
+                                 of ? &p.tm_v32 : &p.tm_k32, bar, 0, 0,
+                                 int(item.k0 + (v < w.sp ? v : w.lo + v - w.sp)), c, item.hk);
         } else if (lane < 2) {
-            ptx::tma_load_5d(dst + lane * C::kTileBytes, lane ? &p.tm_v : &p.tm_k, &kv_full[stage],
-                             0, 0, int(sq.k0 + (v0 < w.sp ? v0 : w.lo + v0 - w.sp)), 0, hk);
+            ptx::tma_load_5d(dst + lane * C::kTileBytes, lane ? &p.tm_v : &p.tm_k, bar, 0, 0,
+                             int(item.k0 + (v0 < w.sp ? v0 : w.lo + v0 - w.sp)), 0, item.hk);
         }
         __syncwarp();
     };
+    bool more = false;
+    WindowKeys w{};
     if (warp == kWarpLoad) {
         // the barriers, and the first copies while the others set up
         if (lane == 0) {
-            ptx::mbar_init(a_full, 1);
             for (int st = 0; st < C::kStages; ++st) {
-                ptx::mbar_init(&kv_full[st], 1);
-                ptx::mbar_init(&kv_empty[st], 1);
+                ptx::mbar_init(&full[st], 1);
+                ptx::mbar_init(&empty[st], 1);
             }
+            for (int st = 0; st < C::kOBufs; ++st)
+                ptx::mbar_init(&o_in[st], 1);
             ptx::mbar_init(s_full, 1);
-            ptx::mbar_init(dp_full, 1);
+            for (int st = 0; st < C::kDPs; ++st)
+                ptx::mbar_init(&dp_full[st], 1);
             ptx::mbar_init(s_free, kRowWarps);
             ptx::mbar_init(p_full, kRowWarps);
-            ptx::mbar_init(o_full, 1);
+            ptx::mbar_init(acc_full, 1);
             ptx::mbar_init(drain, 1);
-            ptx::mbar_init(a_tm, kRowWarps);
+            ptx::mbar_init(&known[0], 1);
+            ptx::mbar_init(&known[1], 1);
+            ptx::mbar_init(out_full, kRowWarps);
+            ptx::mbar_init(next_in, 1);
             ptx::mbar_init(never, 1);
             *abort_flag = 0;
             ptx::fence_barrier_init();
-            ptx::mbar_arrive_expect_tx(a_full, 3 * C::kChunks * p.P * p.G * 128);
-            for (int c = 0; c < C::kChunks; c += p.q_chunks) {
-                ptx::tma_load_5d(tile_q + c * kChunkBytes, &p.tm_q, a_full, 0, 0, int(sq.q0 + i0),
-                                 c, hk);
-                ptx::tma_load_5d(tile_do + c * kChunkBytes, &p.tm_do, a_full, 0, 0,
-                                 int(sq.q0 + i0), c, hk);
-                ptx::tma_load_5d(tile_o + c * kChunkBytes, &p.tm_o, a_full, 0, 0, int(sq.q0 + i0),
-                                 c, hk);
-            }
         }
         __syncwarp();
-        issue_step(0);
+        more = find(true, item);
+        item.done = more ? 0 : 1;
+        tell(0, item);
+        if (more) {
+            w = keys_of(item);
+            issue_q(0);
+            ++slots;
+            issue_keys(w, 0);
+            ++slots;
+        } else if (lane == 0) {
+            ptx::mbar_arrive(&full[0]);
+        }
+        __syncwarp();
     }
     if (warp == kWarpMma) {
         ptx::tmem_alloc(tmem_slot, kTmemCols);
@@ -320,23 +419,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     const uint32_t tmem = *tmem_slot;
     bool aborted = false;
 
+    // Named barrier 1: the row threads.  2: these and the load warp, when an item's last step is
+    // done; whoever gave up says so there, and all leave together.
+    constexpr int kAll = 32 * kRowWarps + 32;
     if (warp == kWarpLoad) {
         // ======================= TMA producer, keys' mean =====================
-        // Lane 0 issues the copies.  Behind the copies of step j the warp sums 16 rows
-        // of K_{j-2}, whose stage is this warp's to fill again.
+        // Lane 0 issues the copies.  Behind those of slot n the warp sums 16 rows of the
+        // keys in slot n - 2, whose stage is this warp's to fill again.
         constexpr int kKeyLanes = D / 8, kKeyRows = 32 / kKeyLanes;
         float key_sum[8] = {};
         int key_n = 0;
-        auto sum_keys = [&](int j) {
-            const int st = j % C::kStages, un = lane % kKeyLanes;
-            if (!ptx::mbar_wait_warp(&kv_full[st], uint32_t(j / C::kStages) & 1u, abort_flag,
-                                     a.err_word))
+        // of the last two slots: places to sum (0: Q and dO; nor the last step's, so that the
+        // mean is there in time), and the steps behind it (-1: Q and dO)
+        int rows1 = 0, rows2 = 0, left1 = -1, left2 = -1;
+        bool stop = false;
+        int started = 1, finished = 0;               // items
+        constexpr int kShort = 4;                    // steps: the answer takes longer than these
+        auto free_slot = [&]() {
+            const int st = slots % C::kStages, use = slots / C::kStages;
+            if (use > 0 && !ptx::mbar_wait_warp(&empty[st], uint32_t(use + 1) & 1u, abort_flag,
+                                                a.err_word))
+                aborted = true;
+            return !aborted;
+        };
+        auto sum_keys = [&](int n, int rows) {
+            const int un = lane % kKeyLanes;
+            if (!ptx::mbar_wait_warp(&full[n % C::kStages], uint32_t(n / C::kStages) & 1u,
+                                     abort_flag, a.err_word)) {
+                aborted = true;
                 return;
-            const uint8_t *tile_k = smem + C::stage_off(st) + (un >> 3) * kChunkBytes;
+            }
+            const uint8_t *tile_k = stage_ptr(n) + (un >> 3) * kChunkBytes;
 #pragma unroll
             for (int q = 0; q < 16 / kKeyRows; ++q) {
                 const int kr = (q * kKeyRows + lane / kKeyLanes) * 8;
-                if (j * BT + kr >= w.places)
+                if (kr >= rows)
                     break;
                 const uint4 v =
                     *reinterpret_cast<const uint4 *>(tile_k + kr * 128 + ((un & 7) << 4));
@@ -350,57 +467,138 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             }
             __syncwarp();
         };
-        // the next CTA's rows into L2: a map a lane
-        auto prefetch_next = [&]() {
-            int nb, nh, nt;
-            WindowSeq ns;
-            if (!window_item(a, p.grid, blockIdx.x + kWindowSms, nb, nh, nt) ||
-                !window_seq(a, nb, ns))
-                return;
-            const int ni0 = nt * p.P;
-            if (ni0 < ns.L && lane < 3)
-                for (int c = 0; c < C::kChunks; c += p.q_chunks)
-                    ptx::tma_prefetch_5d(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_do : &p.tm_o, 0, 0,
-                                         int(ns.q0 + ni0), c, nh);
-        };
-        int issued = 1;
-        for (int j = 0; j < n_kv; ++j) {
-            if (j > 0) {
-                const int stage = j % C::kStages;
-                // stage 2 is the Q / dO region: free once these are in tensor memory
-                if (!ptx::mbar_wait_warp(&kv_empty[stage], (uint32_t(j / C::kStages) & 1u) ^ 1u,
-                                         abort_flag, a.err_word) ||
-                    (j == 2 && !ptx::mbar_wait_warp(a_tm, 0, abort_flag, a.err_word)))
-                    break;
-                issue_step(j);
-                issued = j + 1;
-            }
-            if (j == 1 || n_kv == 1)
-                prefetch_next();
-            if (j >= 2)
-                sum_keys(j - 2);
-        }
-        for (int j = issued >= 2 ? issued - 2 : 0; j < issued; ++j)
-            sum_keys(j);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-#pragma unroll
-            for (int o = 16; o >= kKeyLanes; o >>= 1)
-                key_sum[e] += __shfl_xor_sync(0xffffffffu, key_sum[e], o);
-#pragma unroll
-        for (int o = 16; o >= kKeyLanes; o >>= 1)
-            key_n += __shfl_xor_sync(0xffffffffu, key_n, o);
-        if (lane < kKeyLanes)
+        auto close = [&]() {                         // the mean of an item's keys
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                reinterpret_cast<float *>(smem + C::kOffMean)[lane * 8 + e] =
-                    key_n > 0 ? key_sum[e] / float(key_n) : 0.f;
-        __syncwarp();
-        asm volatile("bar.sync 2, %0;" ::"n"(32 * kRowWarps + 32) : "memory");
+#pragma unroll
+                for (int o = 16; o >= kKeyLanes; o >>= 1)
+                    key_sum[e] += __shfl_xor_sync(0xffffffffu, key_sum[e], o);
+#pragma unroll
+            for (int o = 16; o >= kKeyLanes; o >>= 1)
+                key_n += __shfl_xor_sync(0xffffffffu, key_n, o);
+            const float inv = key_n > 0 ? 1.f / float(key_n) : 0.f;
+            if (lane < kKeyLanes)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    reinterpret_cast<float *>(smem + C::kOffMean)[lane * 8 + e] = key_sum[e] * inv;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                key_sum[e] = 0.f;
+            key_n = 0;
+            __syncwarp();
+        };
+        // slot `slots` has been issued (or, at the end, there is none)
+        auto issued = [&](int rows, int left) {
+            if (rows2 > 0) {
+                sum_keys(slots - 2, rows2);
+                if (left2 <= 1)
+                    close();
+            }
+            if (left2 == 0 && !aborted) {
+                stop = ptx::bar_red_or(2, kAll, false);
+                ++finished;
+            }
+            rows2 = rows1;
+            left2 = left1;
+            rows1 = rows;
+            left1 = left;
+            ++slots;
+            return !aborted && !stop;
+        };
+        // dQ of item k leaves; where O's place held it, O of the next one comes
+        auto hand_over = [&](int k, bool next) {
+            if (!ptx::mbar_wait_warp(out_full, uint32_t(k) & 1u, abort_flag, a.err_word)) {
+                aborted = true;
+                return false;
+            }
+            const DqItem &it = items[k & 1];
+            if (lane == 0 && it.i1 - it.i0 == p.P) {
+                for (int c = 0; c < C::kChunks; c += p.q_chunks)
+                    ptx::tma_store_5d(&p.tm_d0, smem + C::kOffOut + c * kChunkBytes, 0, 0,
+                                      int(it.q0 + it.i0), c, it.hk);
+                ptx::bulk_commit_and_wait_read();
+            }
+            __syncwarp();
+            if (C::kOBufs == 1 && next)
+                issue_o(k + 1);
+            return true;
+        };
+        int k = 0;
+        if (more) {
+            // the two slots issued above
+            rows1 = min(w.places, BT);
+            left1 = steps_of(w) - 1;
+        }
+        while (more) {
+            const int n_kv = steps_of(w);
+            int j = 1;
+            auto keys = [&]() {
+                if (!free_slot())
+                    return false;
+                issue_keys(w, j);
+                const bool ok = issued(j + 1 < n_kv ? BT : 0, n_kv - 1 - j);
+                ++j;
+                return ok;
+            };
+            if ((n_kv > 1 && !keys()) || (n_kv > 2 && !keys()) || (k > 0 && !hand_over(k - 1, true)))
+                break;
+            // The next item is asked for late in a long one, so that no CTA holds items that
+            // others could have begun (2 x 4096 queries, 32 heads on 8, d = 128, window 4096, all
+            // three kernels: 797 us with each asked for an item ahead, 773 so, 776 four steps
+            // before the end); its rows go to L2, a map a lane.
+            DqItem next{};
+            for (bool found = false;;) {
+                if (!found && !pending && j >= n_kv - 8)
+                    ask();
+                if (!found && j >= n_kv - 5) {
+                    more = find(false, next);
+                    next.done = more ? 0 : 1;
+                    tell(k + 1, next);
+                    if (more && steps_of(keys_of(next)) <= kShort)
+                        ask();
+                    if (more && lane < 3)
+                        for (int c = 0; c < C::kChunks; c += p.q_chunks)
+                            ptx::tma_prefetch_5d(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_do : &p.tm_o,
+                                                 0, 0, int(next.q0 + next.i0), c, next.hk);
+                    found = true;
+                }
+                if (j >= n_kv || !keys())
+                    break;
+            }
+            if (j < n_kv || aborted || stop || !free_slot())
+                break;
+            if (!more) {
+                if (lane == 0)
+                    ptx::mbar_arrive(&full[slots % C::kStages]);
+                __syncwarp();
+                if (issued(0, -1)) {
+                    if (issued(0, -1))
+                        hand_over(k, false);
+                    --slots;
+                }
+                break;
+            }
+            item = next;
+            issue_q(k + 1);
+            ++started;
+            if (!issued(0, -1))
+                break;
+            w = keys_of(item);
+            ++k;
+            if (!free_slot())
+                break;
+            issue_keys(w, 0);
+            if (!issued(min(w.places, BT), steps_of(w) - 1))
+                break;
+        }
+        if (aborted && !stop && finished < started)
+            ptx::bar_red_or(2, kAll, true);
         if (*abort_flag && lane == 0) {
-            drain_wait(a_full, 0);
-            for (int j = issued > C::kStages ? issued - C::kStages : 0; j < issued; ++j)
-                drain_wait(&kv_full[j % C::kStages], uint32_t(j / C::kStages) & 1u);
+            drain_wait(next_in, uint32_t(asked + 1) & 1u);
+            for (int n = slots > C::kStages ? slots - C::kStages : 0; n < slots; ++n)
+                drain_wait(&full[n % C::kStages], uint32_t(n / C::kStages) & 1u);
+            for (int n = o_tiles > C::kOBufs ? o_tiles - C::kOBufs : 0; n < o_tiles; ++n)
+                drain_wait(&o_in[n % C::kOBufs], uint32_t(n / C::kOBufs) & 1u);
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -409,17 +607,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         constexpr uint32_t idesc_q = ptx::idesc_bf16_f32(BT, D, true);     // B MN-major
         constexpr uint64_t desc_kmajor = ptx::smem_desc_base(16, 1024);
         constexpr uint64_t desc_mnmajor = ptx::smem_desc_base(kChunkBytes, 1024);
-        const uint32_t smem_base = ptx::smem_u32(smem);
-        // K's and V's rows of step j behind the sequence's end are cleared
-        const int end_place = w.sp + (L - w.lo);
-        auto clear_tail = [&](int j, int st) {
-            const int r0 = end_place - j * BT;
-            if (r0 >= BT)
-                return;
-            clear_rows<2 * C::kChunks>(smem + C::stage_off(st), r0, BT, kChunkBytes);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-        };
         if (a.expire_wait_ns != 0u &&
             !__all_sync(0xffffffffu, ptx::mbar_wait_limited(never, 0, abort_flag, a.err_word,
                                                             a.expire_wait_ns)))
@@ -436,103 +623,199 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             }
             __syncwarp();
         };
-        auto issue_s = [&](int st) { issue(0, kColQA, smem_base + C::stage_off(st), s_full); };
-        auto issue_dp = [&](int st) {
-            issue(kColDP, kColQA + D / 2, smem_base + C::stage_off(st) + C::kTileBytes, dp_full);
-        };
-        do {
-            if (aborted || !ptx::mbar_wait_warp(a_tm, 0, abort_flag, a.err_word) ||
-                !ptx::mbar_wait_warp(&kv_full[0], 0, abort_flag, a.err_word)) {
+        int st = 0;                                  // the next slot's stage, and its phase
+        uint32_t phase = 0, g = 0;                   // steps done
+        auto wait_slot = [&]() {
+            if (!aborted && !ptx::mbar_wait_warp(&full[st], phase, abort_flag, a.err_word))
                 aborted = true;
-                break;
+            return !aborted;
+        };
+        auto next_slot = [&]() {
+            if (++st == C::kStages) {
+                st = 0;
+                phase ^= 1u;
             }
-            clear_tail(0, 0);
+        };
+        for (int k = 0; wait_slot(); ++k) {
+            if (items[k & 1].done)
+                break;
+            const int L = items[k & 1].L;
+            const WindowKeys wk = keys_of(items[k & 1]);
+            const int n_kv = steps_of(wk), end_place = wk.sp + (L - wk.lo);
+            // K's and V's rows of step j behind the sequence's end are cleared
+            auto clear_tail = [&](int j) {
+                const int r0 = end_place - j * BT;
+                if (r0 >= BT)
+                    return;
+                clear_rows<2 * C::kChunks>(stage_ptr(st), r0, BT, kChunkBytes);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            };
+            // Q and dO go to tensor memory.  (The rows have stored the last dS, so they have
+            // read S and dP, and these products are done.)
             ptx::tc_fence_after_sync();
-            issue_s(0);
-            issue_dp(0);
-            int cur = 0, nxt = 1;                      // ring stages of steps j, j + 1
-            uint32_t nxt_phase = 0;
-            for (int j = 0; j < n_kv; ++j) {
-                const bool more = j + 1 < n_kv;
-                if (more) {
+            if (ptx::elect_one()) {
+                const uint64_t from = ptx::smem_desc(desc_kmajor, ptx::smem_u32(stage_ptr(st)));
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        ptx::tmem_cp(tmem + kColQA + t * (D / 2) + 8 * kk,
+                                     from + uint64_t(t * (C::kTileBytes >> 4)) +
+                                         kmajor_off(kk, kChunkBytes));
+                ptx::mma_commit(&empty[st]);
+            }
+            __syncwarp();
+            next_slot();
+            if (!wait_slot())
+                break;
+            clear_tail(0);
+            ptx::tc_fence_after_sync();
+            auto issue_s = [&]() { issue(0, kColQA, ptx::smem_u32(stage_ptr(st)), s_full); };
+            auto issue_dp = [&](uint32_t of) {
+                issue(C::col_dp(of), kColQA + D / 2, ptx::smem_u32(stage_ptr(st)) + C::kTileBytes,
+                      &dp_full[of % C::kDPs]);
+            };
+            issue_s();
+            issue_dp(g);
+            for (int j = 0; j < n_kv; ++j, ++g) {
+                const bool more_keys = j + 1 < n_kv;
+                const int cur = st;
+                next_slot();
+                if (more_keys) {
                     // S_{j+1} overwrites S_j once every row has read it
-                    if (!ptx::mbar_wait_warp(&kv_full[nxt], nxt_phase, abort_flag, a.err_word) ||
-                        !ptx::mbar_wait_warp(s_free, uint32_t(j) & 1u, abort_flag, a.err_word)) {
+                    if (!wait_slot() ||
+                        !ptx::mbar_wait_warp(s_free, g & 1u, abort_flag, a.err_word)) {
                         aborted = true;
                         break;
                     }
-                    clear_tail(j + 1, nxt);
+                    clear_tail(j + 1);
                     ptx::tc_fence_after_sync();
-                    issue_s(nxt);
+                    issue_s();
+                    if (C::kDPs == 2)
+                        issue_dp(g + 1);
                 }
-                if (!ptx::mbar_wait_warp(p_full, uint32_t(j) & 1u, abort_flag, a.err_word)) {
+                // (the rows have read the accumulators of the item before this one, too)
+                if (!ptx::mbar_wait_warp(p_full, g & 1u, abort_flag, a.err_word)) {
                     aborted = true;
                     break;
                 }
                 ptx::tc_fence_after_sync();
-                const uint64_t dkn = ptx::smem_desc(desc_mnmajor, smem_base + C::stage_off(cur));
+                const uint64_t dkn = ptx::smem_desc(desc_mnmajor, ptx::smem_u32(stage_ptr(cur)));
                 if (ptx::elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk)
-                        ptx::mma_ts(tmem + kColAcc, tmem + kColDP + packed_col(kk),
+                        ptx::mma_ts(tmem + kColAcc, tmem + C::col_dp(g) + packed_col(kk),
                                     dkn + uint64_t((kk * 16 * 128) >> 4), idesc_q,
                                     (j > 0 || kk > 0) ? 1u : 0u);
-                    ptx::mma_commit(&kv_empty[cur]);
+                    ptx::mma_commit(&empty[cur]);
+                    if (!more_keys)
+                        ptx::mma_commit(acc_full);
                 }
                 __syncwarp();
                 // dP_{j+1} overwrites dS_j after the dQ product has read it
-                if (more)
-                    issue_dp(nxt);
-                cur = nxt;
-                if (++nxt == C::kStages) {
-                    nxt = 0;
-                    nxt_phase ^= 1u;
-                }
+                if (more_keys && C::kDPs == 1)
+                    issue_dp(g + 1);
             }
-        } while (false);
+            if (aborted)
+                break;
+        }
         if (ptx::elect_one()) {
-            if (!aborted)
-                ptx::mma_commit(o_full);
             ptx::mma_commit(drain);
             drain_wait(drain, 0);
         }
         __syncwarp();
     } else {
         // ======================= query rows ================================
-        const int r = row_r;                         // row of the tile = TMEM lane
+        const int r = (warp & 3) * 32 + lane, row_q = int(r * p.div_g >> 16);   // row = TMEM lane
         const int g = warp >> 2, col0 = 32 * g;      // of the row's four threads; its columns
-        const int i = i0 + row_q;
         const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
         float *xch = reinterpret_cast<float *>(smem + C::kOffXch);
-        {
-            const bool a_ok = row_wait(a_full, 0, abort_flag, a.err_word);
-            float part = 0.f;                        // of D_i = dO_i . O_i
-            if (a_ok) {
-                // this thread's quarter of its row of Q and of dO (128-byte swizzle) into
-                // tensor memory, and of O beside dO
-                auto unit = [&](const uint8_t *tile, int ul) {
-                    const int e0 = g * (D / 4) + ul * 8, un = (e0 & 63) >> 3;
-                    return *reinterpret_cast<const uint4 *>(tile + (e0 >> 6) * kChunkBytes + r * 128 +
-                                                            ((un ^ (r & 7)) << 4));
-                };
+        float *xsum = reinterpret_cast<float *>(smem + C::kOffSum);
+        const float *mean = reinterpret_cast<const float *>(smem + C::kOffMean);
+        const float sl = p.scale_log2;
+        const uint32_t tS = tmem + lane_bits + uint32_t(col0);
+        const uint32_t tOA = tmem + lane_bits + kColQA + uint32_t(D / 2 + g * (D / 8));
+
+        uint32_t step = 0;
+        bool ready = !items[0].done;                 // there is an item k
+        float lse = 0.f;
+        // this thread's quarter of a row, from a tile (128-byte swizzle)
+        auto unit = [&](const uint8_t *tile, int ul) {
+            const int e0 = g * (D / 4) + ul * 8, un = (e0 & 63) >> 3;
+            return *reinterpret_cast<const uint4 *>(tile + (e0 >> 6) * kChunkBytes + r * 128 +
+                                                    ((un ^ (r & 7)) << 4));
+        };
+        auto stat_of = [&](const DqItem &it) {
+            return stat_row(a, it.b, it.hk * p.G + r - row_q * p.G, it.q0) + it.i0 + row_q;
+        };
+        auto row_in = [&](const DqItem &it) { return row_q < p.P && it.i0 + row_q < it.i1; };
+        // whether there is an item k; its statistic of this row
+        auto prepare = [&](int k) {
+            if (aborted || !row_wait(&known[k & 1], uint32_t(k >> 1) & 1u, abort_flag, a.err_word)) {
+                aborted = true;
+                return;
+            }
+            ready = !items[k & 1].done;
+            if (ready && row_in(items[k & 1]))
+                lse = a.lse[stat_of(items[k & 1])];
+        };
+        if (ready)
+            prepare(0);
+        for (int k = 0; ready; ++k) {
+            const DqItem &it = items[k & 1];         // (stays until out_full)
+            const WindowKeys wk = keys_of(it);
+            const int n_kv = steps_of(wk), i = it.i0 + row_q;
+            const bool row_ok = row_in(it);
+            const int vhi = row_ok ? i - wk.lo + wk.sp : -1;
+            const int64_t vl = int64_t(vhi) - a.window + 1;
+            const int vlo = vl > wk.sp ? int(vl) : wk.sp;
+            const float lse2 = lse * kLog2e;
+            float Di = 0.f;
+            float2 ds_sum2 = make_float2(0.f, 0.f);
+            for (int j = 0; j < n_kv; ++j, ++step) {
+                const uint32_t par = step & 1u;
+                float2 pr[16];
+                bool ok = !aborted && row_wait(s_full, par, abort_flag, a.err_word);
+                if (ok) {
+                    ptx::tc_fence_after_sync();
+                    uint32_t sv[32];
+                    ptx::tmem_ld32(tS, sv);
+                    ptx::tmem_wait_ld();
+                    // S is read: the MMA warp may overwrite it with the next step's
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive(s_free);
+                    const int v0 = j * BT + col0;    // this thread's first place
+                    if (__any_sync(0xffffffffu, v0 < vlo || v0 + 31 > vhi)) {
+                        const uint32_t seen = window_bits(v0, vlo, vhi, a.sinks);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    uint32_t u[D / 8];
-#pragma unroll
-                    for (int ul = 0; ul < D / 32; ++ul) {
-                        const uint4 v = unit(t == 0 ? tile_q : tile_do, ul);
-                        u[4 * ul + 0] = v.x;
-                        u[4 * ul + 1] = v.y;
-                        u[4 * ul + 2] = v.z;
-                        u[4 * ul + 3] = v.w;
+                        for (int e = 0; e < 32; ++e)
+                            if (!(seen & (1u << e)))
+                                sv[e] = __float_as_uint(-INFINITY);
                     }
-                    const uint32_t dst =
-                        tmem + lane_bits + kColQA + uint32_t(t * (D / 2) + g * (D / 8));
-                    if constexpr (D == 128)
-                        ptx::tmem_st16(dst, u);
-                    else
-                        ptx::tmem_st8(dst, u);
-                    if (t == 1)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[2 * e]),
+                                                                __uint_as_float(sv[2 * e + 1])),
+                                                    make_float2(sl, sl), make_float2(-lse2, -lse2));
+                        pr[e] = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+                    }
+                }
+                if (j == 0) {
+                    // D_i = dO_i . O_i, of the row's four threads
+                    ok = ok && row_wait(&o_in[k % C::kOBufs], uint32_t(k / C::kOBufs) & 1u,
+                                        abort_flag, a.err_word);
+                    float part = 0.f;
+                    if (ok) {
+                        const uint8_t *tile_o = smem + C::kOffO + uint32_t(k % C::kOBufs) * C::kTileBytes;
+                        uint32_t u[D / 8];
+                        if constexpr (D == 128)
+                            ptx::tmem_ld16(tOA, u);
+                        else
+                            ptx::tmem_ld8(tOA, u);
+                        ptx::tmem_wait_ld();
 #pragma unroll
                         for (int ul = 0; ul < D / 32; ++ul) {
                             const uint4 o = unit(tile_o, ul);
@@ -546,110 +829,70 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                                             __uint_as_float(gw & 0xffff0000u), part);
                             }
                         }
+                    }
+                    xch[g * BT + r] = part;
+                    asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");
+                    Di = (xch[r] + xch[BT + r]) + (xch[2 * BT + r] + xch[3 * BT + r]);
                 }
+                if (!ok || !row_wait(&dp_full[step % C::kDPs], (step / C::kDPs) & 1u, abort_flag,
+                                     a.err_word)) {
+                    aborted = true;
+                    break;
+                }
+                ptx::tc_fence_after_sync();
+                uint32_t dv[32], pk[16];
+                ptx::tmem_ld32(tS + C::col_dp(step), dv);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 y = __fmul2_rn(
+                        pr[e], __fadd2_rn(make_float2(__uint_as_float(dv[2 * e]),
+                                                      __uint_as_float(dv[2 * e + 1])),
+                                          make_float2(-Di, -Di)));
+                    pk[e] = ptx::pack_bf16x2(y.x, y.y);
+                }
+                ptx::tmem_st16(tS + C::col_dp(step), pk);     // dS of this row's 32 keys, packed
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before_sync();
                 __syncwarp();
-                // (the Q / dO region is free for the ring's third stage, too)
                 if (lane == 0)
-                    ptx::mbar_arrive(a_tm);
+                    ptx::mbar_arrive(p_full);
+                // (dS as the product has it)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    ds_sum2 = __fadd2_rn(ds_sum2, make_float2(__uint_as_float(pk[e] << 16),
+                                                              __uint_as_float(pk[e] & 0xffff0000u)));
             }
-            xch[g * BT + r] = part;
-        }
-        const float lse2 = lse * kLog2e;
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");   // the row threads
-        const float Di = (xch[r] + xch[BT + r]) + (xch[2 * BT + r] + xch[3 * BT + r]);
-        if (g == 0 && row_ok)
-            p.D[stat] = Di;
-        const float sl = p.scale_log2;
-        const int vhi = row_ok ? i - w.lo + w.sp : -1;
-        const int64_t vl = int64_t(vhi) - a.window + 1;
-        const int vlo = vl > w.sp ? int(vl) : w.sp;
-
-        float2 ds_sum2 = make_float2(0.f, 0.f);
-        const uint32_t tS = tmem + lane_bits + uint32_t(col0);
-
-        for (int j = 0; j < n_kv; ++j) {
-            const uint32_t par = uint32_t(j) & 1u;
-            if (!row_wait(s_full, par, abort_flag, a.err_word)) {
-                aborted = true;
+            prepare(k + 1);
+            // the sum of the row's dS over its threads, and (from the load warp) the keys'
+            // mean.  (Where D and the sums share a place: with two steps or more, dP_1 came
+            // behind every row's dS_0 and so behind its reading D.)
+            if (C::kOffSum == C::kOffXch && n_kv == 1)
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");
+            xsum[g * BT + r] = ds_sum2.x + ds_sum2.y;
+            if (ptx::bar_red_or(2, kAll, aborted))
                 break;
+            const float ri = (xsum[r] + xsum[BT + r]) + (xsum[2 * BT + r] + xsum[3 * BT + r]);
+            if (g == 0 && row_ok)
+                p.D[stat_of(it)] = Di + ri;
+            // 32 columns of each row's dQ a thread: a whole tile by one copy, a cut one row by
+            // row
+            const bool whole = it.i1 - it.i0 == p.P;
+            if (!row_wait(acc_full, uint32_t(k) & 1u, abort_flag, a.err_word)) {
+                aborted = true;
+                continue;
             }
             ptx::tc_fence_after_sync();
-            uint32_t sv[32];
-            ptx::tmem_ld32(tS, sv);
-            ptx::tmem_wait_ld();
-            // S is read: the MMA warp may overwrite it with the next step's
-            ptx::tc_fence_before_sync();
+            if (g < D / 32) {
+                const int64_t row_h = it.hk * p.G + r - row_q * p.G;
+                store_row(tmem + lane_bits + kColAcc, a.scale,
+                          row_ok ? p.dQ + (it.q0 + i) * p.dq_stride + row_h * D : nullptr,
+                          whole ? smem + C::kOffOut : nullptr, r, g, g + 1, -ri, mean);
+                ptx::fence_proxy_async_smem();
+            }
             __syncwarp();
             if (lane == 0)
-                ptx::mbar_arrive(s_free);
-            const int v0 = j * BT + col0;            // this thread's first place
-            if (__any_sync(0xffffffffu, v0 < vlo || v0 + 31 > vhi)) {
-                const uint32_t seen = window_bits(v0, vlo, vhi, a.sinks);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (!(seen & (1u << e)))
-                        sv[e] = __float_as_uint(-INFINITY);
-            }
-            float2 pr[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[2 * e]),
-                                                        __uint_as_float(sv[2 * e + 1])),
-                                            make_float2(sl, sl), make_float2(-lse2, -lse2));
-                pr[e] = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-            }
-            if (!row_wait(dp_full, par, abort_flag, a.err_word)) {
-                aborted = true;
-                break;
-            }
-            ptx::tc_fence_after_sync();
-            uint32_t dv[32], pk[16];
-            ptx::tmem_ld32(tS + kColDP, dv);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float2 y = __fmul2_rn(
-                    pr[e], __fadd2_rn(make_float2(__uint_as_float(dv[2 * e]),
-                                                  __uint_as_float(dv[2 * e + 1])),
-                                      make_float2(-Di, -Di)));
-                ds_sum2 = __fadd2_rn(ds_sum2, y);
-                pk[e] = ptx::pack_bf16x2(y.x, y.y);
-            }
-            ptx::tmem_st16(tS + kColDP, pk);         // dS of this row's 32 keys, packed
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                ptx::mbar_arrive(p_full);
-        }
-        const float ds_sum = ds_sum2.x + ds_sum2.y;
-        // the sum of the row's dS over its threads, and (from the load warp) the keys' mean
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");   // xch has been read
-        xch[g * BT + r] = ds_sum;
-        asm volatile("bar.sync 2, %0;" ::"n"(32 * kRowWarps + 32) : "memory");
-        const float ri = (xch[r] + xch[BT + r]) + (xch[2 * BT + r] + xch[3 * BT + r]);
-        const float *mean = reinterpret_cast<const float *>(smem + C::kOffMean);
-        // 32 columns of each row's dQ a thread: a whole tile by way of O's place and one copy,
-        // a cut one row by row
-        const bool whole = i1 - i0 == p.P;
-        uint8_t *stage = tile_o;
-        const bool ok = !aborted && ptx::mbar_wait(o_full, 0, abort_flag, a.err_word);
-        if (ok && g < D / 32) {
-            ptx::tc_fence_after_sync();
-            store_row(tmem + lane_bits + kColAcc, a.scale,
-                      row_ok ? p.dQ + (sq.q0 + i) * p.dq_stride + int64_t(row_h) * D : nullptr,
-                      whole ? stage : nullptr, r, g, g + 1, -ri, mean);
-        }
-        if (whole) {
-            ptx::fence_proxy_async_smem();
-            if (!ptx::bar_red_or(1, 32 * kRowWarps, !ok) && threadIdx.x == 0) {
-                for (int c = 0; c < C::kChunks; c += p.q_chunks)
-                    ptx::tma_store_5d(&p.tm_d0, stage + c * kChunkBytes, 0, 0, int(sq.q0 + i0), c,
-                                      hk);
-                ptx::bulk_commit_and_wait_read();
-            }
+                ptx::mbar_arrive(out_full);
         }
     }
     ptx::tc_fence_before_sync();

@@ -158,10 +158,6 @@ __device__ __forceinline__ void window_check(const WindowArgs &a, const WindowGr
         record_device_error(a.err_word, FA_DEVERR_BAD_SEQLENS);
 }
 
-// CTAs that run at once, one an SM: the CTA this far behind in the grid is about the next
-// on this one's SM.
-constexpr int kWindowSms = 152;
-
 // The lowest `n` bits, n clamped to 0 .. 32.
 __device__ __forceinline__ uint32_t low_bits(int n)
 {
