@@ -626,7 +626,8 @@ FA_API int fa_attention_window_fwd(const void *Q, int64_t q_stride, const void *
  *   the last sequence are neither read into a result nor written.
  *   Q, K, V: rows as in the forward.  O, dO: contiguous bf16 [.., H, d]; lse as
  *   there.  dQ, dK, dV: bf16 rows of H * d, Hkv * d and Hkv * d values, dq_stride,
- *   dk_stride and dv_stride elements apart (multiples of 8), 16-byte aligned; written.
+ *   dk_stride and dv_stride elements apart (multiples of 8), 16-byte aligned; written;
+ *   no overlap with an input or one another (rows of one fused gradient are fine).
  *   workspace: DEVICE scratch owned by the caller, 256-byte aligned, at least
  *   fa_attention_window_bwd_workspace_bytes(...) bytes; contents on entry are
  *   ignored.  Calls that may run at the same time need one each.
