@@ -75,6 +75,51 @@ def test_unlike_sequences(window, sinks):
     run([3000, 1, 0, 40] + [17] * 60 + [900, 129] + [128] * 5 + [2300, 3], 2, 1, 64, "packed", window, sinks)
 
 
+@pytest.mark.parametrize("n,H,Hkv,d,form,window,sinks", [
+    ([900] * 3, 14, 14, 64, "dense", 200, 4),                   # three steps each, both d's operands
+    ([1500] * 2, 16, 8, 128, "dense", 700, 0),                  # half a dozen
+    ([1700] * 2, 12, 6, 64, "dense", 1600, 3),                  # one step to fourteen
+    ([int(x) for x in np.random.default_rng(1).integers(0, 70, 220)], 4, 2, 64, "packed", 20, 3),       # one step
+    ([int(x) for x in np.random.default_rng(2).integers(0, 300, 90)], 6, 3, 128, "packed", 150, 3)])    # one to three
+def test_items_one_behind_the_other(n, H, Hkv, d, form, window, sinks):
+    """More tiles of rows than SMs, which take them as they come: the same bits again."""
+    batch, o, lse, do, how, grads = run(n, H, Hkv, d, form, window, sinks)
+    for _ in range(3):
+        again = fa.attention_window_bwd(batch.gq, batch.gk, batch.gv, o, do, lse, window, sinks, **how)
+        assert all(torch.equal(x[:sum(n)], y[:sum(n)]) for x, y in zip(grads, again))
+    device_error_clear()
+
+
+def test_bad_counts_among_many():
+    n = [40] * 300
+    batch, o, lse, do, how, grads = run(n, 4, 2, 64, "packed", 20, 3)
+    n[100], n[101], n[250] = 70, 10, 43                          # above the bound; the others' rows stay theirs
+    n[251] = 37
+    cu = torch.tensor(np.concatenate(([0], np.cumsum(n))), dtype=torch.int32, device="cuda")
+    out = [torch.full(x.shape, 7.0, dtype=torch.bfloat16, device="cuda") for x in grads]
+    fa.attention_window_bwd(batch.gq, batch.gk, batch.gv, o, do, lse, 20, 3, cu_seqlens=cu, max_seqlen=40,
+                            dq=out[0], dk=out[1], dv=out[2])
+    assert fa.fa_get_device_error() == fa.FA_DEVERR_BAD_SEQLENS
+    for x, y in zip(out, grads):
+        assert (x[4000:4070] == 7).all() and (x[10000:10043] == 7).all()
+        for i, j in ((0, 4000), (4080, 10000), (10080, 12000)):
+            assert torch.equal(x[i:j], y[i:j])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_timed_out_wait_with_more_tiles_than_sms(d):
+    """Each CTA gives up, whatever it has taken on; the next call is not concerned."""
+    batch, o, lse, do, how, grads = run([1000] * 2, 20, 20, d, "dense", 130, 4)
+    dq = torch.full_like(grads[0], 7.0)
+    fa.fa_debug_expire_next_wait(100_000)
+    fa.attention_window_bwd(batch.gq, batch.gk, batch.gv, o, do, lse, 130, 4, dq=dq)
+    assert fa.fa_get_device_error() == fa.FA_DEVERR_WAIT_TIMEOUT
+    assert (dq == 7).all()
+    again = fa.attention_window_bwd(batch.gq, batch.gk, batch.gv, o, do, lse, 130, 4)
+    device_error_clear()
+    assert all(torch.equal(x, y) for x, y in zip(grads, again))
+
+
 def test_rows_behind_the_last_sequence_stay():
     batch, o, lse, do, how, want = run([200, 61], 4, 2, 128, "packed", 64, 4, spare=90)
     out = [torch.full(x.shape, 7.0, dtype=torch.bfloat16, device="cuda") for x in want]
