@@ -369,7 +369,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         __syncwarp();
     };
     bool more = false;
-    WindowKeys w{};
     if (warp == kWarpLoad) {
         // the barriers, and the first copies while the others set up
         if (lane == 0) {
@@ -398,25 +397,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         more = find(true, item);
         item.done = more ? 0 : 1;
         tell(0, item);
-        if (more) {
-            w = keys_of(item);
-            issue_q(0);
-            ++slots;
-            issue_keys(w, 0);
-            ++slots;
-        } else if (lane == 0) {
-            ptx::mbar_arrive(&full[0]);
-        }
-        __syncwarp();
     }
     if (warp == kWarpMma) {
         ptx::tmem_alloc(tmem_slot, kTmemCols);
         ptx::tmem_relinquish();
     }
-    ptx::tc_fence_before_sync();
-    __syncthreads();
-    ptx::tc_fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    // (the load warp goes on)
+    if (warp == kWarpLoad) {
+        __threadfence_block();
+        asm volatile("bar.arrive 3, %0;" ::"n"(kThreads) : "memory");
+    } else {
+        ptx::tc_fence_before_sync();
+        asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory");
+        ptx::tc_fence_after_sync();
+    }
+    const uint32_t tmem = warp == kWarpLoad ? 0u : *tmem_slot;
     bool aborted = false;
 
     // Named barrier 1: the row threads.  2: these and the load warp, when an item's last step is
@@ -424,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     constexpr int kAll = 32 * kRowWarps + 32;
     if (warp == kWarpLoad) {
         // ======================= TMA producer, keys' mean =====================
+        WindowKeys w{};
         // Lane 0 issues the copies.  Behind those of slot n the warp sums 16 rows of the
         // keys in slot n - 2, whose stage is this warp's to fill again.
         constexpr int kKeyLanes = D / 8, kKeyRows = 32 / kKeyLanes;
@@ -433,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         // mean is there in time), and the steps behind it (-1: Q and dO)
         int rows1 = 0, rows2 = 0, left1 = -1, left2 = -1;
         bool stop = false;
-        int started = 1, finished = 0;               // items
+        int started = 0, finished = 0;               // items
         constexpr int kShort = 4;                    // steps: the answer takes longer than these
         auto free_slot = [&]() {
             const int st = slots % C::kStages, use = slots / C::kStages;
@@ -523,74 +519,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 issue_o(k + 1);
             return true;
         };
-        int k = 0;
-        if (more) {
-            // the two slots issued above
-            rows1 = min(w.places, BT);
-            left1 = steps_of(w) - 1;
-        }
-        while (more) {
-            const int n_kv = steps_of(w);
-            int j = 1;
-            auto keys = [&]() {
-                if (!free_slot())
-                    return false;
-                issue_keys(w, j);
-                const bool ok = issued(j + 1 < n_kv ? BT : 0, n_kv - 1 - j);
-                ++j;
-                return ok;
-            };
-            if ((n_kv > 1 && !keys()) || (n_kv > 2 && !keys()) || (k > 0 && !hand_over(k - 1, true)))
+        // A slot a round: steps of item k's keys, then Q and dO of the next item (n_kv steps: the
+        // first round's), or at the end an empty slot and, for its sums, none.
+        int k = -1, j = 0, n_kv = 0, given = 0, ending = 0;
+        bool found = true;
+        DqItem next = item;
+        for (;;) {
+            // behind three steps (the third's keys come into Q's and dO's stage)
+            if (given < k && j >= min(3, n_kv)) {
+                if (!hand_over(given, ending == 0))
+                    break;
+                ++given;
+            }
+            if (ending == 2)
                 break;
             // The next item is asked for late in a long one, so that no CTA holds items that
             // others could have begun (2 x 4096 queries, 32 heads on 8, d = 128, window 4096, all
             // three kernels: 797 us with each asked for an item ahead, 773 so, 776 four steps
             // before the end); its rows go to L2, a map a lane.
-            DqItem next{};
-            for (bool found = false;;) {
-                if (!found && !pending && j >= n_kv - 8)
+            if (!found && !pending && j >= n_kv - 8 && j >= min(3, n_kv))
+                ask();
+            if (!found && j >= n_kv - 5 && j >= min(3, n_kv)) {
+                more = find(false, next);
+                next.done = more ? 0 : 1;
+                tell(k + 1, next);
+                if (more && steps_of(keys_of(next)) <= kShort)
                     ask();
-                if (!found && j >= n_kv - 5) {
-                    more = find(false, next);
-                    next.done = more ? 0 : 1;
-                    tell(k + 1, next);
-                    if (more && steps_of(keys_of(next)) <= kShort)
-                        ask();
-                    if (more && lane < 3)
-                        for (int c = 0; c < C::kChunks; c += p.q_chunks)
-                            ptx::tma_prefetch_5d(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_do : &p.tm_o,
-                                                 0, 0, int(next.q0 + next.i0), c, next.hk);
-                    found = true;
-                }
-                if (j >= n_kv || !keys())
-                    break;
+                if (more && lane < 3)
+                    for (int c = 0; c < C::kChunks; c += p.q_chunks)
+                        ptx::tma_prefetch_5d(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_do : &p.tm_o, 0, 0,
+                                             int(next.q0 + next.i0), c, next.hk);
+                found = true;
             }
-            if (j < n_kv || aborted || stop || !free_slot())
+            if (ending == 0 && !free_slot())
                 break;
-            if (!more) {
-                if (lane == 0)
+            int rows = 0, left = -1;
+            if (j < n_kv) {
+                issue_keys(w, j);
+                left = n_kv - 1 - j;
+                rows = left > 0 ? BT : j == 0 ? w.places : 0;
+                ++j;
+            } else if (more) {
+                item = next;
+                w = keys_of(item);
+                n_kv = steps_of(w);
+                j = 0;
+                ++k;
+                ++started;
+                found = false;
+                issue_q(k);
+            } else {
+                if (ending++ == 0 && lane == 0)
                     ptx::mbar_arrive(&full[slots % C::kStages]);
                 __syncwarp();
-                if (issued(0, -1)) {
-                    if (issued(0, -1))
-                        hand_over(k, false);
-                    --slots;
-                }
-                break;
+                k += ending == 2;                    // (the last item's dQ is handed over, too)
             }
-            item = next;
-            issue_q(k + 1);
-            ++started;
-            if (!issued(0, -1))
-                break;
-            w = keys_of(item);
-            ++k;
-            if (!free_slot())
-                break;
-            issue_keys(w, 0);
-            if (!issued(min(w.places, BT), steps_of(w) - 1))
+            if (!issued(rows, left))
                 break;
         }
+        slots -= ending == 2;
         if (aborted && !stop && finished < started)
             ptx::bar_red_or(2, kAll, true);
         if (*abort_flag && lane == 0) {
@@ -666,56 +653,51 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 ptx::mma_commit(&empty[st]);
             }
             __syncwarp();
-            next_slot();
-            if (!wait_slot())
-                break;
-            clear_tail(0);
-            ptx::tc_fence_after_sync();
-            auto issue_s = [&]() { issue(0, kColQA, ptx::smem_u32(stage_ptr(st)), s_full); };
-            auto issue_dp = [&](uint32_t of) {
-                issue(C::col_dp(of), kColQA + D / 2, ptx::smem_u32(stage_ptr(st)) + C::kTileBytes,
-                      &dp_full[of % C::kDPs]);
-            };
-            issue_s();
-            issue_dp(g);
-            for (int j = 0; j < n_kv; ++j, ++g) {
+            for (int j = -1; j < n_kv; ++j) {
                 const bool more_keys = j + 1 < n_kv;
                 const int cur = st;
                 next_slot();
+                const uint32_t dst = ptx::smem_u32(stage_ptr(st));
+                auto issue_dp = [&](uint32_t of) {
+                    issue(C::col_dp(of), kColQA + D / 2, dst + C::kTileBytes, &dp_full[of % C::kDPs]);
+                };
                 if (more_keys) {
                     // S_{j+1} overwrites S_j once every row has read it
                     if (!wait_slot() ||
-                        !ptx::mbar_wait_warp(s_free, g & 1u, abort_flag, a.err_word)) {
+                        (j >= 0 && !ptx::mbar_wait_warp(s_free, g & 1u, abort_flag, a.err_word))) {
                         aborted = true;
                         break;
                     }
                     clear_tail(j + 1);
                     ptx::tc_fence_after_sync();
-                    issue_s();
+                    issue(0, kColQA, dst, s_full);
                     if (C::kDPs == 2)
-                        issue_dp(g + 1);
+                        issue_dp(g + (j >= 0));
                 }
-                // (the rows have read the accumulators of the item before this one, too)
-                if (!ptx::mbar_wait_warp(p_full, g & 1u, abort_flag, a.err_word)) {
-                    aborted = true;
-                    break;
-                }
-                ptx::tc_fence_after_sync();
-                const uint64_t dkn = ptx::smem_desc(desc_mnmajor, ptx::smem_u32(stage_ptr(cur)));
-                if (ptx::elect_one()) {
+                if (j >= 0) {
+                    // (the rows have read the accumulators of the item before this one, too)
+                    if (!ptx::mbar_wait_warp(p_full, g & 1u, abort_flag, a.err_word)) {
+                        aborted = true;
+                        break;
+                    }
+                    ptx::tc_fence_after_sync();
+                    const uint64_t dkn = ptx::smem_desc(desc_mnmajor, ptx::smem_u32(stage_ptr(cur)));
+                    if (ptx::elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < BT / 16; ++kk)
-                        ptx::mma_ts(tmem + kColAcc, tmem + C::col_dp(g) + packed_col(kk),
-                                    dkn + uint64_t((kk * 16 * 128) >> 4), idesc_q,
-                                    (j > 0 || kk > 0) ? 1u : 0u);
-                    ptx::mma_commit(&empty[cur]);
-                    if (!more_keys)
-                        ptx::mma_commit(acc_full);
+                        for (int kk = 0; kk < BT / 16; ++kk)
+                            ptx::mma_ts(tmem + kColAcc, tmem + C::col_dp(g) + packed_col(kk),
+                                        dkn + uint64_t((kk * 16 * 128) >> 4), idesc_q,
+                                        (j > 0 || kk > 0) ? 1u : 0u);
+                        ptx::mma_commit(&empty[cur]);
+                        if (!more_keys)
+                            ptx::mma_commit(acc_full);
+                    }
+                    __syncwarp();
+                    ++g;
                 }
-                __syncwarp();
                 // dP_{j+1} overwrites dS_j after the dQ product has read it
                 if (more_keys && C::kDPs == 1)
-                    issue_dp(g + 1);
+                    issue_dp(g);
             }
             if (aborted)
                 break;
