@@ -14,8 +14,9 @@
 //     which grows against dQ where keys have a part in common and the window is long
 //     (2^-9 of dQ becomes 2^-7.5 with a window of 2048).  But sum_j dS_ij is 0, so its
 //     computed value r_i, of dS as rounded, is the errors', and r_i times a mean of the
-//     keys is taken off (the common part; of 16 rows of each step but the last, which the
-//     load warp reads beside its work); D_i + r_i is what dK takes.
+//     keys is taken off (the common part; of four rows of each step but the last, which
+//     the load warp reads beside its work); D_i + r_i is what dK takes.  Where all keys are
+//     in one step D_i is the sum of P dP and nothing is taken off.
 //   * attn_window_dkdv_kernel: a CTA per (sequence, kv head, 128 keys); 128-query
 //     steps over the queries that have these keys in their window, one head of the
 //     group after the other into the same accumulators.  Keys below `sinks` are seen
@@ -420,14 +421,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     if (warp == kWarpLoad) {
         // ======================= TMA producer, keys' mean =====================
         WindowKeys w{};
-        // Lane 0 issues the copies.  Behind those of slot n the warp sums 16 rows of the
-        // keys in slot n - 2, whose stage is this warp's to fill again.
+        // Lane 0 issues the copies.  Behind those of slot n the warp sums four rows of the
+        // keys in slot n - 2, whose stage is this warp's to fill again.  (Sixteen rows: 425 us
+        // where these take 417, 2 x 4096, 32 heads on 8, d = 128, window 1024, all kernels: the
+        // ring is not so deep that its copies can wait.)
         constexpr int kKeyLanes = D / 8, kKeyRows = 32 / kKeyLanes;
         float key_sum[8] = {};
         int key_n = 0;
-        // of the last two slots: places to sum (0: Q and dO; nor the last step's, so that the
-        // mean is there in time), and the steps behind it (-1: Q and dO)
-        int rows1 = 0, rows2 = 0, left1 = -1, left2 = -1;
+        // the steps behind the last two slots' (-1: Q and dO; the last step's keys are not summed,
+        // so that the mean is there in time)
+        int left1 = -1, left2 = -1;
         bool stop = false;
         int started = 0, finished = 0;               // items
         constexpr int kShort = 4;                    // steps: the answer takes longer than these
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 aborted = true;
             return !aborted;
         };
-        auto sum_keys = [&](int n, int rows) {
+        auto sum_keys = [&](int n) {
             const int un = lane % kKeyLanes;
             if (!ptx::mbar_wait_warp(&full[n % C::kStages], uint32_t(n / C::kStages) & 1u,
                                      abort_flag, a.err_word)) {
@@ -447,12 +450,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             }
             const uint8_t *tile_k = stage_ptr(n) + (un >> 3) * kChunkBytes;
 #pragma unroll
-            for (int q = 0; q < 16 / kKeyRows; ++q) {
-                const int kr = (q * kKeyRows + lane / kKeyLanes) * 8;
-                if (kr >= rows)
-                    break;
-                const uint4 v =
-                    *reinterpret_cast<const uint4 *>(tile_k + kr * 128 + ((un & 7) << 4));
+            for (int q = 0; q < 4 / kKeyRows; ++q) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(
+                    tile_k + (q * kKeyRows + lane / kKeyLanes) * 32 * 128 + ((un & 7) << 4));
                 const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -484,19 +484,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             __syncwarp();
         };
         // slot `slots` has been issued (or, at the end, there is none)
-        auto issued = [&](int rows, int left) {
-            if (rows2 > 0) {
-                sum_keys(slots - 2, rows2);
-                if (left2 <= 1)
+        auto issued = [&](int left) {
+            if (left2 > 0) {
+                sum_keys(slots - 2);
+                if (left2 == 1)
                     close();
             }
             if (left2 == 0 && !aborted) {
                 stop = ptx::bar_red_or(2, kAll, false);
                 ++finished;
             }
-            rows2 = rows1;
             left2 = left1;
-            rows1 = rows;
             left1 = left;
             ++slots;
             return !aborted && !stop;
@@ -553,11 +551,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             }
             if (ending == 0 && !free_slot())
                 break;
-            int rows = 0, left = -1;
+            int left = -1;
             if (j < n_kv) {
                 issue_keys(w, j);
                 left = n_kv - 1 - j;
-                rows = left > 0 ? BT : j == 0 ? w.places : 0;
                 ++j;
             } else if (more) {
                 item = next;
@@ -574,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 __syncwarp();
                 k += ending == 2;                    // (the last item's dQ is handed over, too)
             }
-            if (!issued(rows, left))
+            if (!issued(left))
                 break;
         }
         slots -= ending == 2;
@@ -742,6 +739,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             if (ready && row_in(items[k & 1]))
                 lse = a.lse[stat_of(items[k & 1])];
         };
+        auto exchange = [&](float part) {            // the sum over a row's four threads
+            xch[g * BT + r] = part;
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");
+            return (xch[r] + xch[BT + r]) + (xch[2 * BT + r] + xch[3 * BT + r]);
+        };
         if (ready)
             prepare(0);
         for (int k = 0; ready; ++k) {
@@ -786,11 +788,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                     }
                 }
                 if (j == 0) {
-                    // D_i = dO_i . O_i, of the row's four threads
                     ok = ok && row_wait(&o_in[k % C::kOBufs], uint32_t(k / C::kOBufs) & 1u,
                                         abort_flag, a.err_word);
-                    float part = 0.f;
-                    if (ok) {
+                    float part = 0.f;                // of D_i = dO_i . O_i
+                    if (ok && n_kv > 1) {
                         const uint8_t *tile_o = smem + C::kOffO + uint32_t(k % C::kOBufs) * C::kTileBytes;
                         uint32_t u[D / 8];
                         if constexpr (D == 128)
@@ -812,19 +813,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                             }
                         }
                     }
-                    xch[g * BT + r] = part;
-                    asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");
-                    Di = (xch[r] + xch[BT + r]) + (xch[2 * BT + r] + xch[3 * BT + r]);
+                    if (n_kv > 1)
+                        Di = exchange(part);
                 }
                 if (!ok || !row_wait(&dp_full[step % C::kDPs], (step / C::kDPs) & 1u, abort_flag,
                                      a.err_word)) {
                     aborted = true;
+                    if (n_kv == 1)
+                        exchange(0.f);
                     break;
                 }
                 ptx::tc_fence_after_sync();
                 uint32_t dv[32], pk[16];
                 ptx::tmem_ld32(tS + C::col_dp(step), dv);
                 ptx::tmem_wait_ld();
+                // With all keys in this step D is the sum of P dP, no rounding of O's in it (few
+                // keys have little in common for r_i to act on).
+                if (n_kv == 1) {
+                    float part = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        part = fmaf(pr[e].x, __uint_as_float(dv[2 * e]),
+                                    fmaf(pr[e].y, __uint_as_float(dv[2 * e + 1]), part));
+                    Di = exchange(part);
+                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const float2 y = __fmul2_rn(
@@ -854,7 +866,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             xsum[g * BT + r] = ds_sum2.x + ds_sum2.y;
             if (ptx::bar_red_or(2, kAll, aborted))
                 break;
-            const float ri = (xsum[r] + xsum[BT + r]) + (xsum[2 * BT + r] + xsum[3 * BT + r]);
+            const float ri = n_kv == 1 ? 0.f : (xsum[r] + xsum[BT + r]) +
+                                               (xsum[2 * BT + r] + xsum[3 * BT + r]);
             if (g == 0 && row_ok)
                 p.D[stat_of(it)] = Di + ri;
             // 32 columns of each row's dQ a thread: a whole tile by one copy, a cut one row by
@@ -869,7 +882,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 const int64_t row_h = it.hk * p.G + r - row_q * p.G;
                 store_row(tmem + lane_bits + kColAcc, a.scale,
                           row_ok ? p.dQ + (it.q0 + i) * p.dq_stride + row_h * D : nullptr,
-                          whole ? smem + C::kOffOut : nullptr, r, g, g + 1, -ri, mean);
+                          whole ? smem + C::kOffOut : nullptr, r, g, g + 1, -ri,
+                          n_kv == 1 ? nullptr : mean);
                 ptx::fence_proxy_async_smem();
             }
             __syncwarp();

@@ -5,7 +5,7 @@ import torch
 
 import online_softmax_06_gb300 as fa
 from gpu_common import device_error_clear, require_gpu
-from window_common import Batch, bf16, check_gradients, f64
+from window_common import Batch, bf16, check_gradients, f64, layer, score_error
 
 pytestmark = pytest.mark.gpu
 
@@ -53,6 +53,29 @@ def test_heads_that_share(G, d):
 @pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 127, 129])
 def test_short(n):
     run([n] * 3, 4, 2, 64, "dense", 40, 2)
+
+
+@pytest.mark.parametrize("n", [1, 2, 4, 7, 16, 17, 90])
+@pytest.mark.parametrize("H,Hkv,d", [(4, 4, 64), (6, 2, 128)])
+def test_few_keys_without_the_rounding_of_o(n, H, Hkv, d):
+    """Queries whose keys fit one step: dQ is off by dS's rounding to bf16 (2^-9 of each), the correction by
+    the sum of those roundings times a mean of keys, and its own rounding; D has no part of O's rounding."""
+    batch, o, lse, do, how, grads = run([n] * 3, H, Hkv, d, "dense", 40, 3)
+    scale, parts = d ** -0.5, [f64(x) for x in do]
+    for b in range(3):
+        q, k, v, g, got = f64(batch.q[b]), f64(batch.k[b]), f64(batch.v[b]), parts[b], f64(grads[0][b])
+        want = layer.window_attention_bwd(q, k, v, g, 40, 3, scale)[0]
+        O, stat = layer.window_attention(q, k, v, 40, 3, scale)
+        slop = 4 * score_error(q, k, scale, d).max() + 2.0 ** -18
+        for h in range(H):
+            kh, vh = k[:, h // (H // Hkv)], v[:, h // (H // Hkv)]
+            s = np.where(layer.window_seen(n, n, 40, 3), q[:, h] @ kh.T * scale - stat[h][:, None], -np.inf)
+            P, dP, D = np.exp(s), g[:, h] @ vh.T, (g[:, h] * O[:, h]).sum(1, keepdims=True)
+            dS = np.abs(P * (dP - D))
+            top = np.abs(kh).max(0)
+            tol = scale * 2.0 ** -9 * (dS @ (np.abs(kh) + top)) + 2.0 ** -8 * np.abs(want[:, h])
+            tol += scale * slop * ((P * (np.abs(dP) + np.abs(dP).max(1, keepdims=True) + np.abs(D))) @ (np.abs(kh) + top))
+            assert np.all(np.abs(got[:, h] - want[:, h]) <= tol), (np.abs(got[:, h] - want[:, h]) / tol).max()
 
 
 @pytest.mark.parametrize("H,Hkv,d", [(1, 1, 64), (4, 2, 128)])
