@@ -180,9 +180,9 @@ __device__ __forceinline__ int64_t stat_row(const WindowArgs &a, int b, int h, i
 // (it asks for their CTAs): Q and dO of the next pass through the ring behind this one's last
 // keys and are copied to tensor memory by the tensor cores' own path, and the next item's
 // first products run while the rows store this one's dQ.  2 x 4096, 32 heads on 8, d = 128,
-// window 1024: 188 us, a CTA an item 190; 8 packed sequences of 3001 tokens at most, 16
-// heads, d = 64, window 256: 84 us and 104.  r_i of dS as rounded, not before: dQ is off by
-// 0.0026 of its norm instead of 0.0030, dK by 0.0024 instead of 0.0026, for 1 % of the time.
+// window 1024: 180 us, a CTA an item 190; 8 packed sequences of 3001 tokens at most, 16
+// heads, d = 64, window 256: 87 us and 104.  r_i of dS as rounded, not before: dQ is off by
+// 0.0027 of its norm instead of 0.0030, dK by 0.0024 instead of 0.0026, for 1 % of the time.
 template <int D>
 struct CfgQ {
     static constexpr int kChunks = D / 64;
