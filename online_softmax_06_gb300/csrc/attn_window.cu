@@ -732,11 +732,12 @@ int choose_split(const WindowArgs &a, int P)
 // Tiles of a CTA.  With a narrow window a CTA has few steps, and its start and end (loads
 // without a product, the way of O) weigh more than that two tiles share K and V: one tile
 // then, two CTAs an SM (2 x 4096 tokens, d = 64, 16 heads: window 64 26 us against 34, 256
-// 39 against 46, 512 49 against 54, 1024 65 and 66, 4096 113 against 109; d = 128, 32 heads
-// on 8: 64 51 against 64, 256 75 and 76, 512 95 and 95, 1024 133 against 128).
+// 39 against 46, 512 49 against 54, 1024 65 and 66, 4096 113 against 109; 4 x 4096: 1024 117
+// against 126, 4096 202 against 195; d = 128, 32 heads on 8: 64 51 against 64, 256 75 and 76,
+// 512 95 and 95, 1024 133 against 128).
 int choose_tiles(const WindowArgs &a)
 {
-    return a.window <= (a.d == 64 ? 512 : 256) ? 1 : 2;
+    return a.window <= (a.d == 64 ? 1024 : 256) ? 1 : 2;
 }
 
 }  // namespace
