@@ -11,12 +11,12 @@
 //     heads), the keys that they see in 128-key steps, the window's behind the
 //     sinks' as in the forward (window.cuh).  Also writes D.  D comes from O rounded
 //     to bf16, an error e that all keys of a row share: dQ is off by e sum_j P_ij K_j,
-//     which grows against dQ where keys have a part in common and the window is long
-//     (2^-9 of dQ becomes 2^-7.5 with a window of 2048).  But sum_j dS_ij is 0, so its
-//     computed value r_i, of dS as rounded, is the errors', and r_i times a mean of the
-//     keys is taken off (the common part; of four rows of each step but the last, which
-//     the load warp reads beside its work); D_i + r_i is what dK takes.  Where all keys are
-//     in one step D_i is the sum of P dP and nothing is taken off.
+//     which grows against dQ where a row's keys have a part in common (2^-9 of dQ
+//     becomes 2^-7.5 with a window of 2048, 2^-3.4 with keys and values whose common
+//     parts are twice the rest).  But sum_j dS_ij is 0, so its computed value r_i, of dS as
+//     rounded, is the errors' sum, and r_i sum_j P_ij K_j, a fourth product, is taken off:
+//     each key by its own weight, so that dQ depends on no key that the row does not see.
+//     D_i + r_i is what dK takes.
 //   * attn_window_dkdv_kernel: a CTA per (sequence, kv head, 128 keys); 128-query
 //     steps over the queries that have these keys in their window, one head of the
 //     group after the other into the same accumulators.  Keys below `sinks` are seen
@@ -116,27 +116,28 @@ __device__ __forceinline__ uint64_t kmajor_off(int kk, uint32_t chunk_bytes)
     return uint64_t(((kk >> 2) * chunk_bytes + (kk & 3) * 32) >> 4);
 }
 
-// Columns [32 c0, 32 c1) of this thread's row r of an accumulator, plus `more` times the
-// values at `add` where given, times `mul`, as bf16: to `dst` (the row's first value; null:
+// Columns [32 c0, 32 c1) of this thread's row r of an accumulator (TWO: plus `more` times
+// those of the one at t_more), times `mul`, as bf16: to `dst` (the row's first value; null:
 // nowhere), or into a tile in shared memory laid out as a copy's (128-byte swizzle).
+template <bool TWO = false>
 __device__ __forceinline__ void store_row(uint32_t t_acc, float mul, __nv_bfloat16 *dst,
                                           uint8_t *tile, int r, int c0, int c1, float more = 0.f,
-                                          const float *add = nullptr)
+                                          uint32_t t_more = 0)
 {
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
         uint32_t o[32];
         ptx::tmem_ld32(t_acc + c * 32, o);
-        ptx::tmem_wait_ld();
-        if (add != nullptr)
+        if constexpr (TWO) {
+            uint32_t x[32];
+            ptx::tmem_ld32(t_more + c * 32, x);
+            ptx::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float4 x = *reinterpret_cast<const float4 *>(add + c * 32 + 4 * e);
-                o[4 * e] = __float_as_uint(fmaf(more, x.x, __uint_as_float(o[4 * e])));
-                o[4 * e + 1] = __float_as_uint(fmaf(more, x.y, __uint_as_float(o[4 * e + 1])));
-                o[4 * e + 2] = __float_as_uint(fmaf(more, x.z, __uint_as_float(o[4 * e + 2])));
-                o[4 * e + 3] = __float_as_uint(fmaf(more, x.w, __uint_as_float(o[4 * e + 3])));
-            }
+            for (int e = 0; e < 32; ++e)
+                o[e] = __float_as_uint(fmaf(more, __uint_as_float(x[e]), __uint_as_float(o[e])));
+        } else {
+            ptx::tmem_wait_ld();
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             uint32_t u[4];
@@ -166,23 +167,21 @@ __device__ __forceinline__ int64_t stat_row(const WindowArgs &a, int b, int h, i
 // =============================================================================
 // dQ and D
 // =============================================================================
-// S_j in columns [0, 128), dP_j (dS_j packed into it) in [128, 256), dQ from 256, Q and
-// dO as bf16 A operands behind it.  The MMA warp issues, per 128-key step j: S_{j+1} as
-// soon as the rows have read S_j, dQ += dS_j K_j once they have stored dS_j, then dP_{j+1};
-// sixteen row warps (four threads a row, 32 columns each) form P while dQ and dP run and
-// dS while S does.  A step takes 2300 cycles, its products 1640 (d = 128): dS_j -> dQ_j ->
-// dP_{j+1} -> dS_{j+1} is a chain.  With d = 64 there are columns for a second dP behind the
-// operands (384), and dP_{j+1} goes ahead of dQ_j (2 x 4096, 16 heads, window 4096, all three
-// kernels: 343 us, 351 without).  Steps of 64 keys in two buffers took 246 us where these
-// took 211 (2 x 4096, 32 heads on 8, d = 128, window 1024): a product 64 wide takes the
-// tensor cores as long as one of 128.
+// S_j (P_j packed into it) in columns [0, 128), dP_j (dS_j packed into it) in [128, 256),
+// dS K from 256, P K behind it.  The MMA warp issues, per 128-key step j: P_j K_j once the
+// rows have stored P_j, S_{j+1}, dS_j K_j once they have stored dS_j, then dP_{j+1}; sixteen
+// row warps (four threads a row, 32 columns each) form P while dS K and dP run and dS while
+// P K and S do.  A step takes 1.6 us (d = 128), its products 1.1: dS_j -> dQ_j -> dP_{j+1}
+// -> dS_{j+1} is a chain.  With d = 64 there are columns for a second dP behind the
+// accumulators (384), and dP_{j+1} goes ahead of dQ_j.
 // A CTA, one an SM, does items one after the other, its own and then such as have not begun
-// (it asks for their CTAs): Q and dO of the next pass through the ring behind this one's last
-// keys and are copied to tensor memory by the tensor cores' own path, and the next item's
-// first products run while the rows store this one's dQ.  2 x 4096, 32 heads on 8, d = 128,
-// window 1024: 180 us, a CTA an item 190; 8 packed sequences of 3001 tokens at most, 16
-// heads, d = 64, window 256: 87 us and 104.  r_i of dS as rounded, not before: dQ is off by
-// 0.0027 of its norm instead of 0.0030, dK by 0.0024 instead of 0.0026, for 1 % of the time.
+// (it asks for their CTAs): Q and dO of the next come while this one's last step runs, and
+// its first products run while the rows store this one's dQ.  2 x 4096, 32 heads on 8,
+// d = 128, window 1024: 232 us; 1 x 32768, 16 heads on 4, window 2048: 800 us; 8 packed
+// sequences of 3001 tokens at most, 16 heads, d = 64, window 256: 95 us.  (Without P K 180,
+// 611 and 87 us, but dQ off by 0.0043 and 0.0050 of its norm for the first two's windows,
+// keys with a common part as large as the rest and values with a tenth, where it is off by
+// 0.0024 so; D from a pass over the keys before would be two products more, not one.)
 template <int D>
 struct CfgQ {
     static constexpr int kChunks = D / 64;
@@ -193,11 +192,10 @@ struct CfgQ {
     static constexpr int kOBufs = D == 64 ? 2 : 1;
     static constexpr uint32_t kOffO = kStages * kStageBytes;
     static constexpr uint32_t kOffOut = kOffO + (kOBufs == 2 ? 2 : 0) * kTileBytes;
-    // parts of D_i, and of the sums of dS, of the rows' four threads; the keys' mean; items
+    // parts of D_i, and of the sums of dS, of the rows' four threads; items
     static constexpr uint32_t kOffXch = kOffOut + kTileBytes;
     static constexpr uint32_t kOffSum = kOffXch + (kOBufs == 2 ? 4 * BT * 4 : 0);
-    static constexpr uint32_t kOffMean = kOffSum + 4 * BT * 4;
-    static constexpr uint32_t kOffItem = kOffMean + D * 4;
+    static constexpr uint32_t kOffItem = kOffSum + 4 * BT * 4;
     static constexpr uint32_t kOffNext = kOffItem + 2 * 40;
     static constexpr uint32_t kOffBar = kOffNext + 16;
     // of dP and dS: where there are columns for two, dP_{j+1} need not wait for dQ_j
@@ -209,6 +207,20 @@ struct CfgQ {
     static constexpr int kBars = 2 * kStages + kOBufs + kDPs + 10;
     static constexpr uint32_t kSmemBytes = kOffBar + 8 * kBars + 16;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+// The stages of the ring, as all warps of a CTA number them: an item's Q and dO hold one,
+// its steps' keys take the other two in turn.  The next item's Q and dO come where the
+// step before the last was, which is free first.
+struct DqRing {
+    int hold = 0, a = 1, b = 2;
+    __device__ __forceinline__ int of(int step) const { return step & 1 ? b : a; }
+    __device__ __forceinline__ void next(int steps)
+    {
+        const int last = of(steps - 1), other = a + b - last;
+        a = hold;
+        hold = other;
+        b = last;
+    }
 };
 constexpr uint32_t kColAcc = 256, kColDP = 128;
 // Column of the packed bf16 operand for the product's K step kk: the 32 values of each
@@ -230,14 +242,14 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __grid_constant__ Params p)
 {
     using C = CfgQ<D>;
-    constexpr uint32_t kColQA = kColAcc + D;
-    static_assert(kColQA + D <= kTmemCols, "tensor memory");
+    constexpr uint32_t kColPK = kColAcc + D;         // P K beside dS K
+    static_assert(kColPK + D <= kTmemCols, "tensor memory");
     // aligned as the tiles need it, with no room to align it here
     extern __shared__ __align__(1024) uint8_t smem_aligned[];
     uint8_t *smem = smem_aligned;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *full = bars, *empty = bars + C::kStages, *o_in = bars + 2 * C::kStages;
-    uint64_t *s_full = o_in + C::kOBufs, *s_free = s_full + 1, *p_full = s_full + 2,
+    uint64_t *s_full = o_in + C::kOBufs, *ds_full = s_full + 1, *p_full = s_full + 2,
              *acc_full = s_full + 3, *drain = s_full + 4, *out_full = s_full + 5,
              *next_in = s_full + 6, *never = s_full + 7, *known = s_full + 8, *dp_full = s_full + 10;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
@@ -262,11 +274,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         return window_keys(a.window, a.sinks, it.i0, it.i1, 0, kPad);
     };
     auto steps_of = [](const WindowKeys &w) { return (w.places + BT - 1) / BT; };   // at least one
-    auto stage_ptr = [&](int n) { return smem + uint32_t(n % C::kStages) * C::kStageBytes; };
+    auto stage_ptr = [&](int st) { return smem + uint32_t(st) * C::kStageBytes; };
+    DqRing ring;
 
-    // ---- the load warp's: slots of the ring are numbered; Q and dO of an item take one,
-    // each step's keys one
-    int slots = 0, o_tiles = 0;
+    // ---- the load warp's ------------------------------------------------------------
+    int o_tiles = 0;
     DqItem item{};
     int asked = 0;                                   // for other CTAs' items
     bool pending = false;
@@ -335,10 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     };
     auto issue_q = [&](int k) {
         if (lane == 0) {
-            uint64_t *bar = &full[slots % C::kStages];
+            uint64_t *bar = &full[ring.hold];
             ptx::mbar_arrive_expect_tx(bar, 2 * C::kChunks * p.P * p.G * 128);
             for (int c = 0; c < C::kChunks; c += p.q_chunks) {
-                uint8_t *dst = stage_ptr(slots) + c * kChunkBytes;
+                uint8_t *dst = stage_ptr(ring.hold) + c * kChunkBytes;
                 const int row = int(item.q0 + item.i0);
                 ptx::tma_load_5d(dst, &p.tm_q, bar, 0, 0, row, c, item.hk);
                 ptx::tma_load_5d(dst + C::kTileBytes, &p.tm_do, bar, 0, 0, row, c, item.hk);
@@ -349,11 +361,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             issue_o(k);
     };
     auto issue_keys = [&](const WindowKeys &w, int j) {
-        uint64_t *bar = &full[slots % C::kStages];
+        uint64_t *bar = &full[ring.of(j)];
         if (lane == 0)
             ptx::mbar_arrive_expect_tx(bar, C::kStageBytes);
         __syncwarp();
-        uint8_t *dst = stage_ptr(slots);
+        uint8_t *dst = stage_ptr(ring.of(j));
         const int v0 = j * BT;
         if (v0 < w.sp && v0 + BT > w.sp) {
             // pieces of 32 rows, a lane each
@@ -382,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             ptx::mbar_init(s_full, 1);
             for (int st = 0; st < C::kDPs; ++st)
                 ptx::mbar_init(&dp_full[st], 1);
-            ptx::mbar_init(s_free, kRowWarps);
+            ptx::mbar_init(ds_full, kRowWarps);
             ptx::mbar_init(p_full, kRowWarps);
             ptx::mbar_init(acc_full, 1);
             ptx::mbar_init(drain, 1);
@@ -415,95 +427,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
     const uint32_t tmem = warp == kWarpLoad ? 0u : *tmem_slot;
     bool aborted = false;
 
-    // Named barrier 1: the row threads.  2: these and the load warp, when an item's last step is
-    // done; whoever gave up says so there, and all leave together.
-    constexpr int kAll = 32 * kRowWarps + 32;
+    // Named barriers 1 and 2: the row threads.  At 2, when an item's last step is done, whoever
+    // gave up says so, and all leave together.
+    constexpr int kRows = 32 * kRowWarps;
     if (warp == kWarpLoad) {
-        // ======================= TMA producer, keys' mean =====================
-        WindowKeys w{};
-        // Lane 0 issues the copies.  Behind those of slot n the warp sums four rows of the
-        // keys in slot n - 2, whose stage is this warp's to fill again.  (Sixteen rows: 425 us
-        // where these take 417, 2 x 4096, 32 heads on 8, d = 128, window 1024, all kernels: the
-        // ring is not so deep that its copies can wait.)
-        constexpr int kKeyLanes = D / 8, kKeyRows = 32 / kKeyLanes;
-        float key_sum[8] = {};
-        int key_n = 0;
-        // the steps behind the last two slots' (-1: Q and dO; the last step's keys are not summed,
-        // so that the mean is there in time)
-        int left1 = -1, left2 = -1;
-        bool stop = false;
-        int started = 0, finished = 0;               // items
+        // ======================= TMA producer =================================
         constexpr int kShort = 4;                    // steps: the answer takes longer than these
-        auto free_slot = [&]() {
-            const int st = slots % C::kStages, use = slots / C::kStages;
-            if (use > 0 && !ptx::mbar_wait_warp(&empty[st], uint32_t(use + 1) & 1u, abort_flag,
-                                                a.err_word))
+        uint32_t used = 0, fills = 0;                // a bit a stage: filled once; fills so far, odd
+        auto free_stage = [&](int st) {
+            // (the fill before this one is through when its phase of `empty` is)
+            if ((used >> st & 1u) && !ptx::mbar_wait_warp(&empty[st], (fills >> st & 1u) ^ 1u,
+                                                          abort_flag, a.err_word))
                 aborted = true;
+            if (!aborted) {
+                used |= 1u << st;
+                fills ^= 1u << st;
+            }
             return !aborted;
-        };
-        auto sum_keys = [&](int n) {
-            const int un = lane % kKeyLanes;
-            if (!ptx::mbar_wait_warp(&full[n % C::kStages], uint32_t(n / C::kStages) & 1u,
-                                     abort_flag, a.err_word)) {
-                aborted = true;
-                return;
-            }
-            const uint8_t *tile_k = stage_ptr(n) + (un >> 3) * kChunkBytes;
-#pragma unroll
-            for (int q = 0; q < 4 / kKeyRows; ++q) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(
-                    tile_k + (q * kKeyRows + lane / kKeyLanes) * 32 * 128 + ((un & 7) << 4));
-                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    key_sum[2 * e] += __uint_as_float(x[e] << 16);
-                    key_sum[2 * e + 1] += __uint_as_float(x[e] & 0xffff0000u);
-                }
-                ++key_n;
-            }
-            __syncwarp();
-        };
-        auto close = [&]() {                         // the mean of an item's keys
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-#pragma unroll
-                for (int o = 16; o >= kKeyLanes; o >>= 1)
-                    key_sum[e] += __shfl_xor_sync(0xffffffffu, key_sum[e], o);
-#pragma unroll
-            for (int o = 16; o >= kKeyLanes; o >>= 1)
-                key_n += __shfl_xor_sync(0xffffffffu, key_n, o);
-            const float inv = key_n > 0 ? 1.f / float(key_n) : 0.f;
-            if (lane < kKeyLanes)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    reinterpret_cast<float *>(smem + C::kOffMean)[lane * 8 + e] = key_sum[e] * inv;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                key_sum[e] = 0.f;
-            key_n = 0;
-            __syncwarp();
-        };
-        // slot `slots` has been issued (or, at the end, there is none)
-        auto issued = [&](int left) {
-            if (left2 > 0) {
-                sum_keys(slots - 2);
-                if (left2 == 1)
-                    close();
-            }
-            if (left2 == 0 && !aborted) {
-                stop = ptx::bar_red_or(2, kAll, false);
-                ++finished;
-            }
-            left2 = left1;
-            left1 = left;
-            ++slots;
-            return !aborted && !stop;
         };
         // dQ of item k leaves; where O's place held it, O of the next one comes
         auto hand_over = [&](int k, bool next) {
             if (!ptx::mbar_wait_warp(out_full, uint32_t(k) & 1u, abort_flag, a.err_word)) {
                 aborted = true;
-                return false;
+                return;
             }
             const DqItem &it = items[k & 1];
             if (lane == 0 && it.i1 - it.i0 == p.P) {
@@ -515,72 +461,55 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             __syncwarp();
             if (C::kOBufs == 1 && next)
                 issue_o(k + 1);
-            return true;
         };
-        // A slot a round: steps of item k's keys, then Q and dO of the next item (n_kv steps: the
-        // first round's), or at the end an empty slot and, for its sums, none.
-        int k = -1, j = 0, n_kv = 0, given = 0, ending = 0;
-        bool found = true;
         DqItem next = item;
-        for (;;) {
-            // behind three steps (the third's keys come into Q's and dO's stage)
-            if (given < k && j >= min(3, n_kv)) {
-                if (!hand_over(given, ending == 0))
+        int k = 0;                                   // items begun; all before k - 1 are handed over
+        for (; more && !aborted; ++k) {
+            const WindowKeys w = keys_of(item);
+            const int n_kv = steps_of(w);
+            bool found = false;
+            if (!free_stage(ring.hold))
+                break;
+            issue_q(k);
+            for (int j = 0;; ++j) {
+                const bool begun = j >= min(2, n_kv);
+                // (the item before this one ends without these steps' keys)
+                if (k > 0 && j == min(2, n_kv))
+                    hand_over(k - 1, true);
+                if (aborted)
                     break;
-                ++given;
-            }
-            if (ending == 2)
-                break;
-            // The next item is asked for late in a long one, so that no CTA holds items that
-            // others could have begun (2 x 4096 queries, 32 heads on 8, d = 128, window 4096, all
-            // three kernels: 797 us with each asked for an item ahead, 773 so, 776 four steps
-            // before the end); its rows go to L2, a map a lane.
-            if (!found && !pending && j >= n_kv - 8 && j >= min(3, n_kv))
-                ask();
-            if (!found && j >= n_kv - 5 && j >= min(3, n_kv)) {
-                more = find(false, next);
-                next.done = more ? 0 : 1;
-                tell(k + 1, next);
-                if (more && steps_of(keys_of(next)) <= kShort)
+                // The next item is asked for late in a long one, so that no CTA holds items that
+                // others could have begun (2 x 4096 queries, 32 heads on 8, d = 128, window 4096, all
+                // three kernels, when a step had three products: 797 us with each asked for an item
+                // ahead, 773 so, 776 four steps before the end); its rows go to L2, a map a lane.
+                if (!found && !pending && begun && j >= n_kv - 8)
                     ask();
-                if (more && lane < 3)
-                    for (int c = 0; c < C::kChunks; c += p.q_chunks)
-                        ptx::tma_prefetch_5d(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_do : &p.tm_o, 0, 0,
-                                             int(next.q0 + next.i0), c, next.hk);
-                found = true;
-            }
-            if (ending == 0 && !free_slot())
-                break;
-            int left = -1;
-            if (j < n_kv) {
+                if (!found && begun && j >= n_kv - 5) {
+                    more = find(false, next);
+                    next.done = more ? 0 : 1;
+                    tell(k + 1, next);
+                    if (more && steps_of(keys_of(next)) <= kShort)
+                        ask();
+                    if (more && lane < 3)
+                        for (int c = 0; c < C::kChunks; c += p.q_chunks)
+                            ptx::tma_prefetch_5d(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_do : &p.tm_o,
+                                                 0, 0, int(next.q0 + next.i0), c, next.hk);
+                    found = true;
+                }
+                if (j == n_kv || !free_stage(ring.of(j)))
+                    break;
                 issue_keys(w, j);
-                left = n_kv - 1 - j;
-                ++j;
-            } else if (more) {
-                item = next;
-                w = keys_of(item);
-                n_kv = steps_of(w);
-                j = 0;
-                ++k;
-                ++started;
-                found = false;
-                issue_q(k);
-            } else {
-                if (ending++ == 0 && lane == 0)
-                    ptx::mbar_arrive(&full[slots % C::kStages]);
-                __syncwarp();
-                k += ending == 2;                    // (the last item's dQ is handed over, too)
             }
-            if (!issued(left))
-                break;
+            ring.next(n_kv);
+            item = next;
         }
-        slots -= ending == 2;
-        if (aborted && !stop && finished < started)
-            ptx::bar_red_or(2, kAll, true);
+        if (k > 0 && !aborted)
+            hand_over(k - 1, false);
         if (*abort_flag && lane == 0) {
             drain_wait(next_in, uint32_t(asked + 1) & 1u);
-            for (int n = slots > C::kStages ? slots - C::kStages : 0; n < slots; ++n)
-                drain_wait(&full[n % C::kStages], uint32_t(n / C::kStages) & 1u);
+            for (int st = 0; st < C::kStages; ++st)
+                if (used >> st & 1u)
+                    drain_wait(&full[st], (fills >> st & 1u) ^ 1u);
             for (int n = o_tiles > C::kOBufs ? o_tiles - C::kOBufs : 0; n < o_tiles; ++n)
                 drain_wait(&o_in[n % C::kOBufs], uint32_t(n / C::kOBufs) & 1u);
         }
@@ -595,32 +524,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             !__all_sync(0xffffffffu, ptx::mbar_wait_limited(never, 0, abort_flag, a.err_word,
                                                             a.expire_wait_ns)))
             aborted = true;
-        // S = Q K^T and dP = dO V^T, A from tensor memory
-        auto issue = [&](uint32_t to, uint32_t from, uint32_t addr, uint64_t *bar) {
-            const uint64_t db = ptx::smem_desc(desc_kmajor, addr);
-            if (ptx::elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    ptx::mma_ts(tmem + to, tmem + from + 8 * kk, db + kmajor_off(kk, kChunkBytes),
-                                idesc_s, kk > 0 ? 1u : 0u);
-                ptx::mma_commit(bar);
-            }
-            __syncwarp();
-        };
-        int st = 0;                                  // the next slot's stage, and its phase
-        uint32_t phase = 0, g = 0;                   // steps done
-        auto wait_slot = [&]() {
-            if (!aborted && !ptx::mbar_wait_warp(&full[st], phase, abort_flag, a.err_word))
+        uint32_t phases = 0, g = 0;                  // of the stages, a bit each; steps done
+        auto wait_stage = [&](int st) {
+            if (!aborted &&
+                !ptx::mbar_wait_warp(&full[st], phases >> st & 1u, abort_flag, a.err_word))
                 aborted = true;
+            phases ^= 1u << st;
             return !aborted;
         };
-        auto next_slot = [&]() {
-            if (++st == C::kStages) {
-                st = 0;
-                phase ^= 1u;
+        for (int k = 0; !aborted; ++k) {
+            if (!ptx::mbar_wait_warp(&known[k & 1], uint32_t(k >> 1) & 1u, abort_flag, a.err_word)) {
+                aborted = true;
+                break;
             }
-        };
-        for (int k = 0; wait_slot(); ++k) {
             if (items[k & 1].done)
                 break;
             const int L = items[k & 1].L;
@@ -631,46 +547,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 const int r0 = end_place - j * BT;
                 if (r0 >= BT)
                     return;
-                clear_rows<2 * C::kChunks>(stage_ptr(st), r0, BT, kChunkBytes);
+                clear_rows<2 * C::kChunks>(stage_ptr(ring.of(j)), r0, BT, kChunkBytes);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
             };
-            // Q and dO go to tensor memory.  (The rows have stored the last dS, so they have
-            // read S and dP, and these products are done.)
-            ptx::tc_fence_after_sync();
-            if (ptx::elect_one()) {
-                const uint64_t from = ptx::smem_desc(desc_kmajor, ptx::smem_u32(stage_ptr(st)));
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
+            const uint32_t q_at = ptx::smem_u32(stage_ptr(ring.hold));
+            // S = Q K^T (of = 0) and dP = dO V^T (of = 1)
+            auto issue = [&](int of, int j, uint32_t to, uint64_t *bar) {
+                const uint32_t at = uint32_t(of) * C::kTileBytes;
+                const uint64_t da = ptx::smem_desc(desc_kmajor, q_at + at);
+                const uint64_t db = ptx::smem_desc(desc_kmajor, ptx::smem_u32(stage_ptr(ring.of(j))) + at);
+                if (ptx::elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        ptx::tmem_cp(tmem + kColQA + t * (D / 2) + 8 * kk,
-                                     from + uint64_t(t * (C::kTileBytes >> 4)) +
-                                         kmajor_off(kk, kChunkBytes));
-                ptx::mma_commit(&empty[st]);
-            }
-            __syncwarp();
+                        ptx::mma_ss(tmem + to, da + kmajor_off(kk, kChunkBytes),
+                                    db + kmajor_off(kk, kChunkBytes), idesc_s, kk > 0 ? 1u : 0u);
+                    ptx::mma_commit(bar);
+                }
+                __syncwarp();
+            };
+            auto issue_dp = [&](int j, uint32_t step) {
+                issue(1, j, C::col_dp(step), &dp_full[step % C::kDPs]);
+            };
+            // P_j K_j and dS_j K_j into `to`
+            auto add = [&](int j, uint32_t to, uint32_t from) {
+                const uint64_t db = ptx::smem_desc(desc_mnmajor, ptx::smem_u32(stage_ptr(ring.of(j))));
+#pragma unroll
+                for (int kk = 0; kk < BT / 16; ++kk)
+                    ptx::mma_ts(tmem + to, tmem + from + packed_col(kk),
+                                db + uint64_t((kk * 16 * 128) >> 4), idesc_q,
+                                (j > 0 || kk > 0) ? 1u : 0u);
+            };
+            if (!wait_stage(ring.hold))
+                break;
             for (int j = -1; j < n_kv; ++j) {
                 const bool more_keys = j + 1 < n_kv;
-                const int cur = st;
-                next_slot();
-                const uint32_t dst = ptx::smem_u32(stage_ptr(st));
-                auto issue_dp = [&](uint32_t of) {
-                    issue(C::col_dp(of), kColQA + D / 2, dst + C::kTileBytes, &dp_full[of % C::kDPs]);
-                };
-                if (more_keys) {
-                    // S_{j+1} overwrites S_j once every row has read it
-                    if (!wait_slot() ||
-                        (j >= 0 && !ptx::mbar_wait_warp(s_free, g & 1u, abort_flag, a.err_word))) {
-                        aborted = true;
-                        break;
-                    }
-                    clear_tail(j + 1);
-                    ptx::tc_fence_after_sync();
-                    issue(0, kColQA, dst, s_full);
-                    if (C::kDPs == 2)
-                        issue_dp(g + (j >= 0));
-                }
                 if (j >= 0) {
                     // (the rows have read the accumulators of the item before this one, too)
                     if (!ptx::mbar_wait_warp(p_full, g & 1u, abort_flag, a.err_word)) {
@@ -678,14 +589,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                         break;
                     }
                     ptx::tc_fence_after_sync();
-                    const uint64_t dkn = ptx::smem_desc(desc_mnmajor, ptx::smem_u32(stage_ptr(cur)));
+                    if (ptx::elect_one())
+                        add(j, kColPK, 0);
+                    __syncwarp();
+                }
+                if (more_keys) {
+                    // S_{j+1} overwrites P_j, which its product has read
+                    if (!wait_stage(ring.of(j + 1)))
+                        break;
+                    clear_tail(j + 1);
+                    ptx::tc_fence_after_sync();
+                    issue(0, j + 1, 0, s_full);
+                    if (C::kDPs == 2)
+                        issue_dp(j + 1, g + (j >= 0));
+                }
+                if (j >= 0) {
+                    if (!ptx::mbar_wait_warp(ds_full, g & 1u, abort_flag, a.err_word)) {
+                        aborted = true;
+                        break;
+                    }
+                    ptx::tc_fence_after_sync();
                     if (ptx::elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < BT / 16; ++kk)
-                            ptx::mma_ts(tmem + kColAcc, tmem + C::col_dp(g) + packed_col(kk),
-                                        dkn + uint64_t((kk * 16 * 128) >> 4), idesc_q,
-                                        (j > 0 || kk > 0) ? 1u : 0u);
-                        ptx::mma_commit(&empty[cur]);
+                        add(j, kColAcc, C::col_dp(g));
+                        ptx::mma_commit(&empty[ring.of(j)]);
                         if (!more_keys)
                             ptx::mma_commit(acc_full);
                     }
@@ -694,10 +620,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 }
                 // dP_{j+1} overwrites dS_j after the dQ product has read it
                 if (more_keys && C::kDPs == 1)
-                    issue_dp(g);
+                    issue_dp(j + 1, g);
+                // Q and dO have no product ahead, and the rows have read dO
+                if (j == max(n_kv - 2, 0)) {
+                    if (ptx::elect_one())
+                        ptx::mma_commit(&empty[ring.hold]);
+                    __syncwarp();
+                }
             }
-            if (aborted)
-                break;
+            ring.next(n_kv);
         }
         if (ptx::elect_one()) {
             ptx::mma_commit(drain);
@@ -711,12 +642,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         const uint32_t lane_bits = uint32_t((warp & 3) * 32) << 16;
         float *xch = reinterpret_cast<float *>(smem + C::kOffXch);
         float *xsum = reinterpret_cast<float *>(smem + C::kOffSum);
-        const float *mean = reinterpret_cast<const float *>(smem + C::kOffMean);
         const float sl = p.scale_log2;
         const uint32_t tS = tmem + lane_bits + uint32_t(col0);
-        const uint32_t tOA = tmem + lane_bits + kColQA + uint32_t(D / 2 + g * (D / 8));
 
-        uint32_t step = 0;
+        uint32_t step = 0, phases = 0;               // phases: of the stages, a bit each
         bool ready = !items[0].done;                 // there is an item k
         float lse = 0.f;
         // this thread's quarter of a row, from a tile (128-byte swizzle)
@@ -741,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         };
         auto exchange = [&](float part) {            // the sum over a row's four threads
             xch[g * BT + r] = part;
-            asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");
+            asm volatile("bar.sync 1, %0;" ::"n"(kRows) : "memory");
             return (xch[r] + xch[BT + r]) + (xch[2 * BT + r] + xch[3 * BT + r]);
         };
         if (ready)
@@ -763,14 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 bool ok = !aborted && row_wait(s_full, par, abort_flag, a.err_word);
                 if (ok) {
                     ptx::tc_fence_after_sync();
-                    uint32_t sv[32];
+                    uint32_t sv[32], pk[16];
                     ptx::tmem_ld32(tS, sv);
                     ptx::tmem_wait_ld();
-                    // S is read: the MMA warp may overwrite it with the next step's
-                    ptx::tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0)
-                        ptx::mbar_arrive(s_free);
                     const int v0 = j * BT + col0;    // this thread's first place
                     if (__any_sync(0xffffffffu, v0 < vlo || v0 + 31 > vhi)) {
                         const uint32_t seen = window_bits(v0, vlo, vhi, a.sinks);
@@ -785,58 +709,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                                                                 __uint_as_float(sv[2 * e + 1])),
                                                     make_float2(sl, sl), make_float2(-lse2, -lse2));
                         pr[e] = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+                        pk[e] = ptx::pack_bf16x2(pr[e].x, pr[e].y);
                     }
+                    ptx::tmem_st16(tS, pk);          // P of this row's 32 keys, packed
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive(p_full);
                 }
                 if (j == 0) {
-                    ok = ok && row_wait(&o_in[k % C::kOBufs], uint32_t(k / C::kOBufs) & 1u,
-                                        abort_flag, a.err_word);
+                    ok = ok &&
+                         row_wait(&full[ring.hold], phases >> ring.hold & 1u, abort_flag, a.err_word) &&
+                         row_wait(&o_in[k % C::kOBufs], uint32_t(k / C::kOBufs) & 1u, abort_flag,
+                                  a.err_word);
                     float part = 0.f;                // of D_i = dO_i . O_i
-                    if (ok && n_kv > 1) {
+                    if (ok) {
+                        const uint8_t *tile_do = stage_ptr(ring.hold) + C::kTileBytes;
                         const uint8_t *tile_o = smem + C::kOffO + uint32_t(k % C::kOBufs) * C::kTileBytes;
-                        uint32_t u[D / 8];
-                        if constexpr (D == 128)
-                            ptx::tmem_ld16(tOA, u);
-                        else
-                            ptx::tmem_ld8(tOA, u);
-                        ptx::tmem_wait_ld();
 #pragma unroll
                         for (int ul = 0; ul < D / 32; ++ul) {
-                            const uint4 o = unit(tile_o, ul);
+                            const uint4 o = unit(tile_o, ul), gr = unit(tile_do, ul);
                             const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+                            const uint32_t gw[4] = {gr.x, gr.y, gr.z, gr.w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const uint32_t gw = u[4 * ul + e];
-                                part = fmaf(__uint_as_float(ow[e] << 16), __uint_as_float(gw << 16),
-                                            part);
+                                part = fmaf(__uint_as_float(ow[e] << 16),
+                                            __uint_as_float(gw[e] << 16), part);
                                 part = fmaf(__uint_as_float(ow[e] & 0xffff0000u),
-                                            __uint_as_float(gw & 0xffff0000u), part);
+                                            __uint_as_float(gw[e] & 0xffff0000u), part);
                             }
                         }
                     }
-                    if (n_kv > 1)
-                        Di = exchange(part);
+                    Di = exchange(part);
                 }
                 if (!ok || !row_wait(&dp_full[step % C::kDPs], (step / C::kDPs) & 1u, abort_flag,
                                      a.err_word)) {
                     aborted = true;
-                    if (n_kv == 1)
-                        exchange(0.f);
                     break;
                 }
                 ptx::tc_fence_after_sync();
                 uint32_t dv[32], pk[16];
                 ptx::tmem_ld32(tS + C::col_dp(step), dv);
                 ptx::tmem_wait_ld();
-                // With all keys in this step D is the sum of P dP, no rounding of O's in it (few
-                // keys have little in common for r_i to act on).
-                if (n_kv == 1) {
-                    float part = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        part = fmaf(pr[e].x, __uint_as_float(dv[2 * e]),
-                                    fmaf(pr[e].y, __uint_as_float(dv[2 * e + 1]), part));
-                    Di = exchange(part);
-                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const float2 y = __fmul2_rn(
@@ -850,24 +765,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
                 ptx::tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
-                    ptx::mbar_arrive(p_full);
+                    ptx::mbar_arrive(ds_full);
                 // (dS as the product has it)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     ds_sum2 = __fadd2_rn(ds_sum2, make_float2(__uint_as_float(pk[e] << 16),
                                                               __uint_as_float(pk[e] & 0xffff0000u)));
             }
+            // (each stage's fills in this item: one of Q and dO, then steps in turn)
+            phases ^= 1u << ring.hold | uint32_t((n_kv + 1) >> 1 & 1) << ring.a |
+                      uint32_t(n_kv >> 1 & 1) << ring.b;
+            ring.next(n_kv);
             prepare(k + 1);
-            // the sum of the row's dS over its threads, and (from the load warp) the keys'
-            // mean.  (Where D and the sums share a place: with two steps or more, dP_1 came
-            // behind every row's dS_0 and so behind its reading D.)
+            // the sum of the row's dS over its threads.  (Where D and the sums share a place:
+            // with two steps or more, dP_1 came behind every row's dS_0 and so behind its
+            // reading D.)
             if (C::kOffSum == C::kOffXch && n_kv == 1)
-                asm volatile("bar.sync 1, %0;" ::"n"(32 * kRowWarps) : "memory");
+                asm volatile("bar.sync 1, %0;" ::"n"(kRows) : "memory");
             xsum[g * BT + r] = ds_sum2.x + ds_sum2.y;
-            if (ptx::bar_red_or(2, kAll, aborted))
+            if (ptx::bar_red_or(2, kRows, aborted))
                 break;
-            const float ri = n_kv == 1 ? 0.f : (xsum[r] + xsum[BT + r]) +
-                                               (xsum[2 * BT + r] + xsum[3 * BT + r]);
+            const float ri = (xsum[r] + xsum[BT + r]) + (xsum[2 * BT + r] + xsum[3 * BT + r]);
             if (g == 0 && row_ok)
                 p.D[stat_of(it)] = Di + ri;
             // 32 columns of each row's dQ a thread: a whole tile by one copy, a cut one row by
@@ -880,10 +798,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
             ptx::tc_fence_after_sync();
             if (g < D / 32) {
                 const int64_t row_h = it.hk * p.G + r - row_q * p.G;
-                store_row(tmem + lane_bits + kColAcc, a.scale,
-                          row_ok ? p.dQ + (it.q0 + i) * p.dq_stride + row_h * D : nullptr,
-                          whole ? smem + C::kOffOut : nullptr, r, g, g + 1, -ri,
-                          n_kv == 1 ? nullptr : mean);
+                store_row<true>(tmem + lane_bits + kColAcc, a.scale,
+                                row_ok ? p.dQ + (it.q0 + i) * p.dq_stride + row_h * D : nullptr,
+                                whole ? smem + C::kOffOut : nullptr, r, g, g + 1, -ri,
+                                tmem + lane_bits + kColPK);
                 ptx::fence_proxy_async_smem();
             }
             __syncwarp();
