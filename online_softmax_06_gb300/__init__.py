@@ -306,12 +306,18 @@ def fa_attention_kv4_workspace_bytes(B, Nq, total_q, Nk, H, Hkv, d) -> int:
     return lib().fa_attention_kv4_workspace_bytes(B, Nq, total_q, Nk, H, Hkv, d)
 
 
+def _keys32(n):
+    """``window`` or ``sinks`` as the C entry points take it: more than 32 bits hold is all keys (and
+    would be taken modulo 2^32)."""
+    return max(min(n, 0x7fffffff), -1)
+
+
 def fa_attention_window_fwd(q, q_stride, k, k_stride, v, v_stride, o, lse, B, Nq, total_q, Nk,
                             total_k, H, Hkv, d, scale, window, sinks, cu_seqlens_q, cu_seqlens_k,
                             seqlens_k) -> int:
     return lib().fa_attention_window_fwd(q, q_stride, k, k_stride, v, v_stride, o, lse, B, Nq,
-                                         total_q, Nk, total_k, H, Hkv, d, scale, window, sinks,
-                                         cu_seqlens_q, cu_seqlens_k, seqlens_k)
+                                         total_q, Nk, total_k, H, Hkv, d, scale, _keys32(window),
+                                         _keys32(sinks), cu_seqlens_q, cu_seqlens_k, seqlens_k)
 
 
 def fa_attention_window_bwd(q, q_stride, k, k_stride, v, v_stride, o, do, lse, dq, dq_stride, dk,
@@ -319,12 +325,13 @@ def fa_attention_window_bwd(q, q_stride, k, k_stride, v, v_stride, o, do, lse, d
                             cu_seqlens, workspace, workspace_bytes) -> int:
     return lib().fa_attention_window_bwd(q, q_stride, k, k_stride, v, v_stride, o, do, lse, dq,
                                          dq_stride, dk, dk_stride, dv, dv_stride, B, N, total, H,
-                                         Hkv, d, scale, window, sinks, cu_seqlens, workspace,
-                                         workspace_bytes)
+                                         Hkv, d, scale, _keys32(window), _keys32(sinks),
+                                         cu_seqlens, workspace, workspace_bytes)
 
 
 def fa_attention_window_bwd_workspace_bytes(B, N, total, H, Hkv, d, window, sinks) -> int:
-    return lib().fa_attention_window_bwd_workspace_bytes(B, N, total, H, Hkv, d, window, sinks)
+    return lib().fa_attention_window_bwd_workspace_bytes(B, N, total, H, Hkv, d, _keys32(window),
+                                                         _keys32(sinks))
 
 
 def fa_qk_norm_rope_fwd(q, q_stride, k, k_stride, q_weight, k_weight, inv_freq, positions, qo,
@@ -1022,6 +1029,8 @@ def _window_shapes(q, k, v, cu_q, cu_k, seqlens, max_q, max_k):
     total_q, total_k = (t[0] if len(t) == 3 else t[0] * t[1] for t in (qs, ks))
     Nq = qs[1] if cu_q is None else total_q if max_q is None else int(max_q)
     Nk = ks[1] if cu_k is None else total_k if max_k is None else int(max_k)
+    if not all(0 <= n < 2 ** 31 for n in (Nq, Nk)):
+        raise ValueError(f"a sequence of at most {Nq} queries and {Nk} keys: not in 0 .. 2^31 - 1")
     sizes = (_row_stride(qs, q[1], "q"), _row_stride(ks, k[1], "k"), _row_stride(v[0], v[1], "v"),
              B, Nq, total_q, Nk, total_k, H, hkv, d)
     return sizes, index, (B, H, Nq) if cu_q is None else (H, total_q)
@@ -1048,9 +1057,11 @@ def attention_window_fwd(q, k, v, window: int, sinks: int = 0, scale: float | No
     -> (O [total, H, d], lse [H, total]).  k, v: [B, Nk, kv_heads, d], or packed [total, kv_heads,
     d] with ``cu_seqlens_k`` and ``max_k``; H is a multiple of kv_heads.  ``seqlens_k`` int32 [B]:
     how many of a sequence's rows hold keys (a cache with room for more; default: all).  A token's
-    heads are contiguous, tokens may be any multiple of 8 elements apart.
+    heads are contiguous, tokens may be any multiple of 8 elements apart.  ``window`` and ``sinks``
+    may be larger than any sequence: all keys.
     """
     import torch
+    window, sinks = _keys32(window), _keys32(sinks)
     key = (_like(q), _like(k), _like(v), _like(cu_seqlens_q), _like(cu_seqlens_k),
            _like(seqlens_k), max_q, max_k)
     qs, ks, vs, sizes, index, o_like, lse_like, usual = _kv4_plan(key, _plan_window, *key)
@@ -1106,6 +1117,7 @@ def attention_window_bwd(q, k, v, o, do, lse, window: int, sinks: int = 0,
     fa_attention_window_bwd_workspace_bytes).  Returns (dq, dk, dv).
     """
     import torch
+    window, sinks = _keys32(window), _keys32(sinks)
     key = (_like(q), _like(k), _like(v), _like(o), _like(do), _like(dq), _like(dk), _like(dv),
            _like(cu_seqlens), max_seqlen, window, sinks)
     (qs, ks, vs, (dqs, dks, dvs), sizes, index, new, lse_like, nbytes,
