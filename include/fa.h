@@ -636,7 +636,7 @@ FA_API int fa_attention_window_fwd(const void *Q, int64_t q_stride, const void *
  * The same call gives the same bits (no atomics).  Two or three kernels on the
  * library stream, no synchronisation.
  * Errors: as fa_attention_window_fwd; FA_ERR_BAD_SIZE also for a workspace that is
- * too small.
+ * too small, and for kv heads without query heads (H = 0, Hkv > 0).
  */
 FA_API int fa_attention_window_bwd(const void *Q, int64_t q_stride, const void *K,
                                    int64_t k_stride, const void *V, int64_t v_stride,

@@ -1204,8 +1204,13 @@ int fa_attention_window_bwd(const void *Q, int64_t q_stride, const void *K, int6
     const int rc = fa::check_window(Q, q_stride, K, k_stride, V, v_stride, O, lse, B, N, total, N,
                                     total, H, Hkv, d, scale, window, sinks, cu_seqlens, cu_seqlens,
                                     nullptr, &w.a, &empty);
-    if (rc != FA_OK || empty)
+    if (rc != FA_OK)
         return rc;
+    // (kv heads without a query head have gradients to write, and no kernel does that)
+    if (H == 0 && Hkv > 0 && B > 0 && N > 0 && total > 0)
+        return FA_ERR_BAD_SIZE;
+    if (empty)
+        return FA_OK;
     if (!dO || !dQ || !dK || !dV || !workspace)
         return FA_ERR_NULL_POINTER;
     if (dq_stride < int64_t(H) * d || dk_stride < int64_t(Hkv) * d ||
