@@ -438,7 +438,7 @@ Params make_params(const NormRopeArgs &a, int rows, int64_t *units)
         p.xs[i] = a.xs[i];
         p.gs[i] = a.gs[i];
         p.ys[i] = a.ys[i];
-        p.w[i] = a.w[i];
+        p.w[i] = a.heads[i] > 0 ? a.w[i] : nullptr;   // (not read without heads)
         p.heads[i] = a.heads[i];
         p.steps[i] = (a.heads[i] + per_step - 1) / per_step;
     }
