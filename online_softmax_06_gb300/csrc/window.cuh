@@ -137,7 +137,10 @@ __device__ __forceinline__ bool window_item(const WindowArgs &a, const WindowGri
             return false;
         int64_t number;
         b = window_find(a.cu_seqlens_q, a.B, g.cut, t, number);
-        tile = number < 0 || number > a.Nq ? 0 : int(number);
+        // (rows behind the last sequence have places, too; nobody's where counts do not fit)
+        if (number < 0 || number * g.cut.div >= a.Nq)
+            return false;
+        tile = int(number);
         return true;
     }
     b = int(bh / unsigned(a.Hkv));
