@@ -124,18 +124,6 @@ struct Barriers {
     uint64_t *never;                 // nothing arrives: the failure-detection test waits here
 };
 
-// Bounded wait used only while draining after an abort: ignores the abort flag.
-__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
-{
-    const uint64_t t0 = ptx::globaltimer();
-    for (uint32_t it = 0; it < kWaitMaxPolls; ++it) {
-        if (ptx::mbar_try_wait(bar, parity))
-            return;
-        if ((it & 255u) == 255u && ptx::globaltimer() - t0 > kWaitTimeoutNs)
-            return;
-    }
-}
-
 // SPLIT: compiled for split-KV calls (key ranges, query/key lengths that
 // differ, partial outputs); the plain instantiation has one range per pair and
 // kv_off = 0, so that logic folds away.
@@ -368,10 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // let every copy already issued land before the CTA goes away
                 for (int t = 0; t < 2; ++t)
                     if (q_issued[t])
-                        drain_wait(&bar.q_full[t], 0);
+                        ptx::drain_wait(&bar.q_full[t], 0);
                 for (int s = 0; s < C::kStages; ++s)
                     if (last_phase[s] >= 0)
-                        drain_wait(&bar.kv_full[s], uint32_t(last_phase[s]));
+                        ptx::drain_wait(&bar.kv_full[s], uint32_t(last_phase[s]));
             }
         }
         __syncwarp();
@@ -543,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // once this last commit arrives.
             if (ptx::elect_one()) {
                 ptx::mma_commit(bar.drain);
-                drain_wait(bar.drain, 0);
+                ptx::drain_wait(bar.drain, 0);
             }
         }
         __syncwarp();

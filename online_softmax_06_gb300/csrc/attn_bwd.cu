@@ -185,17 +185,6 @@ __device__ __forceinline__ Bars carve(uint8_t *smem)
     return r;
 }
 
-__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
-{
-    const uint64_t t0 = ptx::globaltimer();
-    for (uint32_t it = 0; it < kWaitMaxPolls; ++it) {
-        if (ptx::mbar_try_wait(bar, parity))
-            return;
-        if ((it & 255u) == 255u && ptx::globaltimer() - t0 > kWaitTimeoutNs)
-            return;
-    }
-}
-
 // A row warp's wait: lane 0 polls the barrier and shares the outcome; the
 // warp-synchronous exchange orders the other lanes' later accesses after the
 // completed phase (the row warps arrive once per warp for the same reason:
@@ -457,10 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (*abort_flag) {
-                drain_wait(a_full, 0);
+                ptx::drain_wait(a_full, 0);
                 for (int st = 0; st < C::kStages; ++st)
                     if (last_phase[st] >= 0)
-                        drain_wait(&kv_full[st], uint32_t(last_phase[st]));
+                        ptx::drain_wait(&kv_full[st], uint32_t(last_phase[st]));
             }
         }
         __syncwarp();
@@ -551,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!aborted)
                 ptx::mma_commit(o_full);
             ptx::mma_commit(drain);
-            drain_wait(drain, 0);
+            ptx::drain_wait(drain, 0);
         }
         __syncwarp();
     } else {
@@ -847,10 +836,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (lane == 0 && *abort_flag) {
-            drain_wait(bar.a_full, 0);
+            ptx::drain_wait(bar.a_full, 0);
             for (int s = 0; s < C::kStages; ++s)
                 if (last_phase[s] >= 0)
-                    drain_wait(&bar.kv_full[s], uint32_t(last_phase[s]));
+                    ptx::drain_wait(&bar.kv_full[s], uint32_t(last_phase[s]));
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -938,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!aborted)
                 ptx::mma_commit(bar.o_full);
             ptx::mma_commit(bar.drain);
-            drain_wait(bar.drain, 0);
+            ptx::drain_wait(bar.drain, 0);
         }
         __syncwarp();
     } else {
@@ -1218,9 +1207,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // last step issued into each stage.  Done whether or not the flag
             // is up yet: a short test timeout can raise it after this point,
             // and without an abort these phases have completed or are about to.
-            drain_wait(a_full, 0);
+            ptx::drain_wait(a_full, 0);
             for (int s = issued - C::kStages > 0 ? issued - C::kStages : 0; s < issued; ++s)
-                drain_wait(&kv_full[s % C::kStages], uint32_t(s / C::kStages) & 1u);
+                ptx::drain_wait(&kv_full[s % C::kStages], uint32_t(s / C::kStages) & 1u);
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -1341,7 +1330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!aborted)
                 ptx::mma_commit(o_full);
             ptx::mma_commit(drain);
-            drain_wait(drain, 0);
+            ptx::drain_wait(drain, 0);
         }
         __syncwarp();
     } else {

@@ -317,18 +317,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Bounded wait while draining after an abort: ignores the abort flag.
-__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
-{
-    const uint64_t t0 = ptx::globaltimer();
-    for (uint32_t it = 0; it < kWaitMaxPolls; ++it) {
-        if (ptx::mbar_try_wait(bar, parity))
-            return;
-        if ((it & 255u) == 255u && ptx::globaltimer() - t0 > kWaitTimeoutNs)
-            return;
-    }
-}
-
 // The x-th longest sequence of up to 32 (of more, the x-th): the CTAs with the most
 // work come first (32 x 256 queries on 300 to 8000 keys 456 us, in the order of the
 // batch 490; equal lengths lose half a per cent).
@@ -481,10 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // warp gives up after this one is through.
             for (int t = 0; t < 2; ++t)
                 if (q_issued[t])
-                    drain_wait(&q_full[t], 0);
+                    ptx::drain_wait(&q_full[t], 0);
             for (int s = 0; s < C::kStages; ++s)
                 if (last_phase[s] >= 0)
-                    drain_wait(&kv_full[s], uint32_t(last_phase[s]));
+                    ptx::drain_wait(&kv_full[s], uint32_t(last_phase[s]));
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -609,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every MMA issued has completed once this last commit arrives
         if (ptx::elect_one()) {
             ptx::mma_commit(drain);
-            drain_wait(drain, 0);
+            ptx::drain_wait(drain, 0);
         }
         __syncwarp();
     } else {

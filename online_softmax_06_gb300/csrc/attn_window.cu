@@ -86,34 +86,6 @@ struct Params {
     float scale_log2;
 };
 
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
-{
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v)
-{
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x),
-                 "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
-}
-
-__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
-{
-    const uint64_t t0 = ptx::globaltimer();
-    for (uint32_t it = 0; it < kWaitMaxPolls; ++it) {
-        if (ptx::mbar_try_wait(bar, parity))
-            return;
-        if ((it & 255u) == 255u && ptx::globaltimer() - t0 > kWaitTimeoutNs)
-            return;
-    }
-}
-
 template <int D, bool SPLIT, int TILES>
 __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
     attn_window_kernel(const __grid_constant__ Params p)
@@ -260,10 +232,10 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
             // copies already issued land before the CTA goes away
             for (int t = 0; t < TILES; ++t)
                 if (q_issued[t])
-                    drain_wait(&q_full[t], 0);
+                    ptx::drain_wait(&q_full[t], 0);
             for (int s = 0; s < C::kStages; ++s)
                 if (last_phase[s] >= 0)
-                    drain_wait(&kv_full[s], uint32_t(last_phase[s]));
+                    ptx::drain_wait(&kv_full[s], uint32_t(last_phase[s]));
         }
         __syncwarp();
     } else if (warp == C::kWarpMma) {
@@ -408,7 +380,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
         // every product issued above is through once this commit arrives
         if (ptx::elect_one()) {
             ptx::mma_commit(drain);
-            drain_wait(drain, 0);
+            ptx::drain_wait(drain, 0);
         }
         __syncwarp();
     } else {
@@ -519,7 +491,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
             // this CTA's part of its row; every CTA of the cluster is through with its ring
             bool ok = !aborted && (j1 <= j0 || ptx::mbar_wait(&o_full[t], 0, abort_flag, a.err_word));
             ptx::tc_fence_after_sync();
-            cluster_sync();
+            ptx::cluster_sync();
             // Rows [owner * per, + per) are joined by CTA `owner`: it gets (m, l, l_o) and O
             // of each from every CTA.  A part's O lies by units of four values, the rows of
             // a unit one behind the other, so that a warp's stores fill whole lines (rows
@@ -529,10 +501,10 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
             static_assert(kOffParts + 2 * BM * D * 4 <= C::kOffBar, "shared memory");
             {
                 const int row = t * BM + r;
-                const uint32_t to = cluster_addr(ptx::smem_u32(smem), uint32_t(row / per));
+                const uint32_t to = ptx::cluster_addr(ptx::smem_u32(smem), uint32_t(row / per));
                 const uint32_t at = to + kOffParts +
                                     uint32_t(part * per * (D / 4) + row % per) * 16;
-                st_cluster4(to + uint32_t(part * per + row % per) * 16,
+                ptx::st_cluster4(to + uint32_t(part * per + row % per) * 16,
                             make_float4(m, l, l_o, ok ? 0.f : 1.f));
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -547,14 +519,14 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
                     }
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        st_cluster4(at + uint32_t((c * 8 + q) * per) * 16,
+                        ptx::st_cluster4(at + uint32_t((c * 8 + q) * per) * 16,
                                     make_float4(__uint_as_float(o[4 * q]),
                                                 __uint_as_float(o[4 * q + 1]),
                                                 __uint_as_float(o[4 * q + 2]),
                                                 __uint_as_float(o[4 * q + 3])));
                 }
             }
-            cluster_sync();
+            ptx::cluster_sync();
             // eight rows and four units a warp at once: whole 32-byte sectors of O
             const float4 *st = reinterpret_cast<const float4 *>(smem);
             const int groups = per / 8;                    // of rows: 16, 8 or 4
@@ -679,8 +651,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
     }
 
     if (SPLIT && warp >= C::kWarpLoad) {              // the rows' warps wait twice above
-        cluster_sync();
-        cluster_sync();
+        ptx::cluster_sync();
+        ptx::cluster_sync();
     }
     ptx::tc_fence_before_sync();
     __syncthreads();

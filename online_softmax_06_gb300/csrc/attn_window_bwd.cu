@@ -75,17 +75,6 @@ struct Params {
     float scale_log2;
 };
 
-__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
-{
-    const uint64_t t0 = ptx::globaltimer();
-    for (uint32_t it = 0; it < kWaitMaxPolls; ++it) {
-        if (ptx::mbar_try_wait(bar, parity))
-            return;
-        if ((it & 255u) == 255u && ptx::globaltimer() - t0 > kWaitTimeoutNs)
-            return;
-    }
-}
-
 // A row warp's wait: one lane polls and shares the outcome.
 __device__ __forceinline__ bool row_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
                                          int *err_word)
@@ -506,12 +495,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         if (k > 0 && !aborted)
             hand_over(k - 1, false);
         if (*abort_flag && lane == 0) {
-            drain_wait(next_in, uint32_t(asked + 1) & 1u);
+            ptx::drain_wait(next_in, uint32_t(asked + 1) & 1u);
             for (int st = 0; st < C::kStages; ++st)
                 if (used >> st & 1u)
-                    drain_wait(&full[st], (fills >> st & 1u) ^ 1u);
+                    ptx::drain_wait(&full[st], (fills >> st & 1u) ^ 1u);
             for (int n = o_tiles > C::kOBufs ? o_tiles - C::kOBufs : 0; n < o_tiles; ++n)
-                drain_wait(&o_in[n % C::kOBufs], uint32_t(n / C::kOBufs) & 1u);
+                ptx::drain_wait(&o_in[n % C::kOBufs], uint32_t(n / C::kOBufs) & 1u);
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -632,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_dq_kernel(const __gri
         }
         if (ptx::elect_one()) {
             ptx::mma_commit(drain);
-            drain_wait(drain, 0);
+            ptx::drain_wait(drain, 0);
         }
         __syncwarp();
     } else {
@@ -1025,11 +1014,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_stats(h, i);
         }
         if (lane == 0 && *abort_flag) {
-            drain_wait(a_full, 0);
+            ptx::drain_wait(a_full, 0);
             for (int j = q_issued > C::kQ ? q_issued - C::kQ : 0; j < q_issued; ++j)
-                drain_wait(&q_full[j % C::kQ], uint32_t(j / C::kQ) & 1u);
+                ptx::drain_wait(&q_full[j % C::kQ], uint32_t(j / C::kQ) & 1u);
             for (int j = do_issued > C::kDO ? do_issued - C::kDO : 0; j < do_issued; ++j)
-                drain_wait(&do_full[j % C::kDO], uint32_t(j / C::kDO) & 1u);
+                ptx::drain_wait(&do_full[j % C::kDO], uint32_t(j / C::kDO) & 1u);
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
@@ -1134,7 +1123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!aborted)
                 ptx::mma_commit(o_full);
             ptx::mma_commit(drain);
-            drain_wait(drain, 0);
+            ptx::drain_wait(drain, 0);
         }
         __syncwarp();
     } else {

@@ -93,28 +93,6 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
-{
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v)
-{
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x),
-                 "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
-}
-__device__ __forceinline__ void st_cluster2(uint32_t addr, float2 v)
-{
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y)
-                 : "memory");
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
-}
-
 template <int D, int MT>
 __global__ void __launch_bounds__(kThreads) attn_window_few_kernel(const __grid_constant__ Params p)
 {
@@ -361,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) attn_window_few_kernel(const __grid_
         }
     // all CTAs of the cluster are done with their rings
     if (p.split > 1)
-        cluster_sync();
+        ptx::cluster_sync();
     else
         __syncthreads();
 
@@ -394,15 +372,15 @@ __global__ void __launch_bounds__(kThreads) attn_window_few_kernel(const __grid_
             sum = fmaf(f, s[k].y, sum);
         }
         const int owner = e / per;
-        st_cluster4(cluster_addr(share + uint32_t(part * per + e % per) * 16, uint32_t(owner)), v);
+        ptx::st_cluster4(ptx::cluster_addr(share + uint32_t(part * per + e % per) * 16, uint32_t(owner)), v);
         // the row's (m, l) to every CTA: one column's thread each
         const int to = c / 4;
         if (to < p.split)
-            st_cluster2(cluster_addr(cl + uint32_t(part * C::kRows + r) * 8, uint32_t(to)),
+            ptx::st_cluster2(ptx::cluster_addr(cl + uint32_t(part * C::kRows + r) * 8, uint32_t(to)),
                         make_float2(M, sum));
     }
     if (p.split > 1)
-        cluster_sync();
+        ptx::cluster_sync();
     else
         __syncthreads();
 

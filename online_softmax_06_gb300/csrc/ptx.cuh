@@ -136,6 +136,18 @@ static __device__ __noinline__ bool mbar_wait_limited(uint64_t *bar, uint32_t pa
     return false;
 }
 
+// Bounded wait while draining after an abort: ignores the abort flag.
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = globaltimer();
+    for (uint32_t it = 0; it < kWaitMaxPolls; ++it) {
+        if (mbar_try_wait(bar, parity))
+            return;
+        if ((it & 255u) == 255u && globaltimer() - t0 > kWaitTimeoutNs)
+            return;
+    }
+}
+
 // mbar_wait by all 32 lanes of a warp; the lanes agree on the result (a wait
 // that gives up in one lane gives up in all), so the warp stays converged.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity,
@@ -168,6 +180,29 @@ static __device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity,
         if (mbar_test_wait(bar, parity))
             return true;
     return mbar_wait_slow(bar, parity, abort, err_word);
+}
+
+// Shared memory of the cluster's CTAs; a barrier of all their threads.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x),
+                 "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void st_cluster2(uint32_t addr, float2 v)
+{
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
 // One lane of a converged warp (elect.sync over the full mask): the lane that
