@@ -633,6 +633,10 @@ FA_API int fa_attention_window_fwd(const void *Q, int64_t q_stride, const void *
  *   ignored.  Calls that may run at the same time need one each.
  * All of a sequence's Q, K, V, O and dO should be finite: a NaN reaches the gradients
  * that its row takes part in and may reach others near them (not other sequences').
+ * Finite keys that a query does not see have no part in its dQ.
+ * Probabilities and dS are rounded to bf16 as operands of the products, sums are fp32.
+ * dO . O is formed from O as the forward rounded it; what that rounding adds to a row's
+ * dS is known by their sum, which is 0 without it, and taken off dQ and dK again.
  * The same call gives the same bits (no atomics).  Two or three kernels on the
  * library stream, no synchronisation.
  * Errors: as fa_attention_window_fwd; FA_ERR_BAD_SIZE also for a workspace that is

@@ -32,7 +32,8 @@
 // queries, 32 heads on 8, d = 128, window 1024, 128 us (121 GFLOP at the keys seen, 940
 // TFLOP/s; tensor cores 48 % busy, where the start and end of a CTA, 3.5 us of its 18, leave
 // them idle).  1 x 32768, 16 heads on 4, window 2048: 427 us, 1250 TFLOP/s.  4 chunks of 512
-// queries at most, 32 heads on 8, window 4096: 84 us, 910 TFLOP/s, in two waves of CTAs.
+// queries at most, 32 heads on 8, window 4096: 84 to 86 us, 890 to 912 TFLOP/s, in two waves of
+// CTAs.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
